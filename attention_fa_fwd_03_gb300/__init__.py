@@ -10,6 +10,15 @@ library has not been built, every call raises.
     fa.fa_fwd(q, k, v, o, lse, scale, causal=True)
     ws = torch.empty(fa.fa_bwd_workspace_size(B, Hq, Tq), dtype=torch.uint8, device="cuda")
     fa.fa_bwd(q, k, v, o, do, lse, dq, dk, dv, scale, causal=True, workspace=ws)
+
+Serving from a paged key/value cache (a pool of pages and a page table):
+
+    kv = fa.PagedKV(k_pool, v_pool, page_table, kv_lens, k_bounds=bounds)   # kept from step to step
+    kv_lens += 1                                                            # the new token counts
+    fa.fa_kv_append(kv, k, v, cos=cos, sin=sin, q=q, q_out=qr)              # rotate, append
+    fa.fa_paged_fwd(kv, qr, o, lse, scale, causal=True, workspace=ws)       # attention over the cache
+    fa.fa_page_select(kv, qr, sel, sel_lens, keep_last=2, workspace=ws2)    # or over chosen pages:
+    fa.fa_paged_fwd(kv, qr, o, lse, scale, causal=True, sel=sel, sel_lens=sel_lens, workspace=ws)
 """
 from __future__ import annotations
 
@@ -19,6 +28,8 @@ import threading
 
 __all__ = ["FA_FP16", "FA_BF16", "FaError", "fa_fwd", "fa_bwd", "fa_bwd_preprocess", "fa_bwd_dkv",
            "fa_bwd_dq", "fa_bwd_workspace_size",
+           "PagedKV", "fa_kv_append", "fa_paged_fwd", "fa_paged_workspace_size", "fa_page_select",
+           "fa_page_select_workspace_size",
            "fa_status_string", "fa_device_status", "fa_abi_version", "fa_selftest_wait_timeout",
            "fa_set_wait_limit_cycles", "library", "library_path"]
 
@@ -26,11 +37,20 @@ FA_FP16 = 0
 FA_BF16 = 1
 STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED_HEAD_DIM",
                 3: "FA_ERR_UNSUPPORTED_DTYPE", 4: "FA_ERR_MISALIGNED", 5: "FA_ERR_LAUNCH",
-                6: "FA_ERR_TIMEOUT"}
+                6: "FA_ERR_TIMEOUT", 7: "FA_ERR_BAD_INDEX"}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
 _lib = None
+
+
+class _PagedKVStruct(ctypes.Structure):
+    """fa_paged_kv of include/fa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_bounds", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("dt", ctypes.c_int)]
 
 
 class FaError(RuntimeError):
@@ -69,6 +89,18 @@ def library():
         lib.fa_bwd_dq.restype = i
         lib.fa_bwd_workspace_size.argtypes = [i, i, i]
         lib.fa_bwd_workspace_size.restype = sz
+        kvp, i64p = ctypes.POINTER(_PagedKVStruct), ctypes.c_void_p
+        lib.fa_kv_append.argtypes = [kvp, vp, i64p, vp, i64p, vp, i64p, vp, i, i, vp, vp, vp, i, i,
+                                     i, vp]
+        lib.fa_kv_append.restype = i
+        lib.fa_paged_fwd.argtypes = [kvp, vp, vp, vp, i, i, f, i, i, vp, vp, vp, i, vp, sz, vp]
+        lib.fa_paged_fwd.restype = i
+        lib.fa_paged_workspace_size.argtypes = [i, i, i, i]
+        lib.fa_paged_workspace_size.restype = sz
+        lib.fa_page_select.argtypes = [kvp, vp, i, i, i, i, vp, vp, vp, sz, vp]
+        lib.fa_page_select.restype = i
+        lib.fa_page_select_workspace_size.argtypes = [i, i, i]
+        lib.fa_page_select_workspace_size.restype = sz
         lib.fa_status_string.argtypes = [i]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i, vp]
@@ -195,6 +227,193 @@ def fa_bwd_dq(q, k, v, do, lse, workspace, dq, scale: float, causal: bool = Fals
                              _ptr(dq), B, Hq, Hkv, Tq, Tkv, D, float(scale), int(bool(causal)),
                              int(window), _dtype_code(q), _stream(stream))
     _check(st, "fa_bwd_dq")
+
+
+# ------------------------------------------------------------- paged cache
+class PagedKV:
+    """A paged key/value cache as the paged calls take it: the pools and the
+    tables that say which pages each sequence has (see include/fa.h).
+
+    ``k`` and ``v`` [num_pages, Hkv, page_size, D] fp16 or bf16, page_size 16 to
+    256; ``page_table`` [B, max_pages] and ``kv_lens`` [B] int32; ``k_bounds``
+    [num_pages, Hkv, 2, D] or None. All contiguous on one CUDA device. The
+    object keeps the tensors alive and is made once: page_table and kv_lens are
+    read by every call and updated in place by the caller.
+    """
+
+    __slots__ = ("k", "v", "page_table", "kv_lens", "k_bounds", "device", "dtype", "B", "Hkv", "D",
+                 "num_pages", "page_size", "max_pages", "_struct", "_ref")
+
+    def __init__(self, k, v, page_table, kv_lens, k_bounds=None):
+        import torch
+        if k.dim() != 4 or page_table.dim() != 2:
+            raise ValueError("k and v are [num_pages, Hkv, page_size, D], page_table is [B, max_pages]")
+        self.num_pages, self.Hkv, self.page_size, self.D = k.shape
+        self.B, self.max_pages = page_table.shape
+        self.device, self.dtype = k.device, k.dtype
+        code = _dtype_code(k)
+        _expect("v", v, tuple(k.shape), k.dtype, k.device)
+        _expect("page_table", page_table, None, torch.int32, k.device)
+        _expect("kv_lens", kv_lens, (self.B,), torch.int32, k.device)
+        if k_bounds is not None:
+            _expect("k_bounds", k_bounds, (self.num_pages, self.Hkv, 2, self.D), k.dtype, k.device)
+        self.k, self.v, self.k_bounds = k, v, k_bounds
+        self.page_table, self.kv_lens = page_table, kv_lens
+        self._struct = _PagedKVStruct(_ptr(k), _ptr(v), None if k_bounds is None else _ptr(k_bounds),
+                                      _ptr(page_table), _ptr(kv_lens), self.B, self.Hkv, self.D,
+                                      self.num_pages, self.page_size, self.max_pages, code)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _expect(name: str, t, shape, dtype, device) -> int:
+    """Address of a contiguous tensor of this shape (None: any), dtype and device."""
+    if t.dtype != dtype or (shape is not None and t.shape != shape):
+        want = dtype if shape is None else f"{dtype} of shape {list(shape)}"
+        raise ValueError(f"{name}: expected {want}, got {t.dtype} of shape {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected on {device}, got {t.device}")
+    return _ptr(t)
+
+
+def _token_view(name: str, t, shape, kv):
+    """Address and strides of a [B, H, T, D] view whose innermost index is contiguous."""
+    if t.dtype != kv.dtype or t.device != kv.device or t.shape != shape:
+        raise ValueError(f"{name}: expected {kv.dtype} of shape {list(shape)} on {kv.device}, got "
+                         f"{t.dtype} of shape {list(t.shape)} on {t.device}")
+    sb, sh, st, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
+        raise ValueError(f"{name}: the innermost index must be contiguous")
+    # the stride of an index of size 1 is never used and can be anything
+    B, H, T, _ = shape
+    strides = (ctypes.c_int64 * 3)(sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0)
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    return t.data_ptr(), strides
+
+
+def _launch(kv, fn, what: str, args, stream) -> None:
+    """Call ``fn`` on ``stream`` (default: the current stream of the cache's
+    device) with that device current."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(kv.device).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == kv.device.index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(kv.device):
+            st = fn(*args, stream)
+    if st != 0:
+        raise FaError(st, what)
+
+
+def fa_kv_append(kv: PagedKV, k, v, cos=None, sin=None, interleaved: bool = False, q=None,
+                 q_out=None, new_lens=None, stream=None) -> None:
+    """Append T new tokens per sequence to the cache: keys rotated by their
+    position, values copied, page bounds updated where the cache keeps them.
+
+    ``k`` and ``v`` [B, Hkv, T, D] and ``q`` [B, Hq, T, D] may be any views
+    with a contiguous innermost index and other strides in multiples of 8, such
+    as transposed slices of a fused projection. The rotated queries go to
+    ``q_out`` (contiguous). ``cos`` and ``sin`` [positions, rot_dim / 2] fp32, or
+    None for no rotation. ``kv.kv_lens`` counts the new tokens already;
+    ``new_lens`` [B] int32 says how many of the T rows of each sequence are
+    tokens (None: all)."""
+    import torch
+    T = k.shape[2] if k.dim() == 4 else 0
+    kp, ks = _token_view("k", k, (kv.B, kv.Hkv, T, kv.D), kv)
+    vp, vs = _token_view("v", v, (kv.B, kv.Hkv, T, kv.D), kv)
+    qp = qs = qo = None
+    Hq = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 4 else 0
+        qp, qs = _token_view("q", q, (kv.B, Hq, T, kv.D), kv)
+        qo = _expect("q_out", q_out, (kv.B, Hq, T, kv.D), kv.dtype, kv.device)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    cp = sp = None
+    rope_len = rot_dim = 0
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError("cos and sin are [positions, rot_dim / 2]")
+        rope_len, half = cos.shape
+        rot_dim = 2 * half
+        cp = _expect("cos", cos, None, torch.float32, kv.device)
+        sp = _expect("sin", sin, cos.shape, torch.float32, kv.device)
+    nl = None if new_lens is None else _expect("new_lens", new_lens, (kv.B,), torch.int32, kv.device)
+    _launch(kv, library().fa_kv_append, "fa_kv_append",
+            (kv._ref, kp, ks, vp, vs, qp, qs, qo, Hq, T, nl, cp, sp, rope_len, rot_dim,
+             int(bool(interleaved))), stream)
+
+
+def fa_paged_workspace_size(Hq: int, Hkv: int, Tq: int, D: int) -> int:
+    return int(library().fa_paged_workspace_size(Hq, Hkv, Tq, D))
+
+
+def fa_paged_fwd(kv: PagedKV, q, o, lse, scale: float, causal: bool = False, window: int = 0,
+                 new_lens=None, sel=None, sel_lens=None, workspace=None, stream=None) -> None:
+    """O and LSE of Tq <= 8 new tokens per sequence over the paged cache.
+
+    ``q`` and ``o`` [B, Hq, Tq, D], ``lse`` [B, Hq, Tq] fp32, contiguous. The new
+    tokens are the last keys of the cache (``kv.kv_lens`` counts them); causal
+    and window masks go by position in the sequence. ``sel`` [B, Hkv, n_sel]
+    and ``sel_lens`` [B, Hkv] int32 restrict each KV head to these pages.
+    ``workspace`` has fa_paged_workspace_size(Hq, Hkv, Tq, D) bytes."""
+    import torch
+    if workspace is None:
+        raise ValueError("fa_paged_fwd needs a workspace tensor (the library never allocates)")
+    if q.dim() != 4 or q.shape[0] != kv.B or q.shape[3] != kv.D:
+        raise ValueError(f"q: expected [{kv.B}, Hq, Tq, {kv.D}], got {list(q.shape)}")
+    _, Hq, Tq, _ = shape = q.shape
+    dev = kv.device
+    if (sel is None) != (sel_lens is None):
+        raise ValueError("sel and sel_lens go together")
+    sp = slp = nl = None
+    n_sel = 0
+    if sel is not None:
+        n_sel = sel.shape[-1]
+        sp = _expect("sel", sel, (kv.B, kv.Hkv, n_sel), torch.int32, dev)
+        slp = _expect("sel_lens", sel_lens, (kv.B, kv.Hkv), torch.int32, dev)
+    if new_lens is not None:
+        nl = _expect("new_lens", new_lens, (kv.B,), torch.int32, dev)
+    if workspace.device != dev:
+        raise ValueError(f"workspace: expected on {dev}, got {workspace.device}")
+    _launch(kv, library().fa_paged_fwd, "fa_paged_fwd",
+            (kv._ref, _expect("q", q, shape, kv.dtype, dev), _expect("o", o, shape, kv.dtype, dev),
+             _expect("lse", lse, shape[:3], torch.float32, dev), Hq, Tq, float(scale),
+             int(bool(causal)), int(window), nl, sp, slp, n_sel, _ptr(workspace),
+             workspace.numel() * workspace.element_size()), stream)
+
+
+def fa_page_select_workspace_size(B: int, Hkv: int, max_pages: int) -> int:
+    return int(library().fa_page_select_workspace_size(B, Hkv, max_pages))
+
+
+def fa_page_select(kv: PagedKV, q, sel, sel_lens, keep_first: int = 0, keep_last: int = 1,
+                   workspace=None, stream=None) -> None:
+    """The pages that attention of one new token reads, chosen per sequence and
+    KV head by the bounds of their keys (``kv.k_bounds``): ``sel`` [B, Hkv,
+    n_sel] int32 gets the page numbers in ascending order, then -1, and
+    ``sel_lens`` [B, Hkv] int32 how many. ``q`` [B, Hq, 1, D]. The first
+    ``keep_first`` and last ``keep_last`` pages are always chosen.
+    ``workspace`` has fa_page_select_workspace_size(B, Hkv, max_pages) bytes."""
+    import torch
+    if workspace is None:
+        raise ValueError("fa_page_select needs a workspace tensor (the library never allocates)")
+    if q.dim() != 4 or q.shape[0] != kv.B or q.shape[2] != 1 or q.shape[3] != kv.D:
+        raise ValueError(f"q: expected [{kv.B}, Hq, 1, {kv.D}], got {list(q.shape)}")
+    dev = kv.device
+    n_sel = sel.shape[-1]
+    if workspace.device != dev:
+        raise ValueError(f"workspace: expected on {dev}, got {workspace.device}")
+    _launch(kv, library().fa_page_select, "fa_page_select",
+            (kv._ref, _expect("q", q, q.shape, kv.dtype, dev), q.shape[1], n_sel, int(keep_first),
+             int(keep_last), _expect("sel", sel, (kv.B, kv.Hkv, n_sel), torch.int32, dev),
+             _expect("sel_lens", sel_lens, (kv.B, kv.Hkv), torch.int32, dev), _ptr(workspace),
+             workspace.numel() * workspace.element_size()), stream)
 
 
 def fa_selftest_wait_timeout(timeout_ms: int, stream=None) -> None:

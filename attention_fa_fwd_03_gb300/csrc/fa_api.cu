@@ -18,6 +18,7 @@
 
 #include "../../include/fa.h"
 #include "fa_launch.h"
+#include "fa_paged.cuh"
 
 namespace fa {
 
@@ -73,14 +74,6 @@ bool status_ptr(uint32_t** p) {
   return true;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// [lo, hi) byte ranges of two buffers intersect.
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
 constexpr int kMaxSeq = 1 << 22;        // keeps every grid dimension within limits
 constexpr int64_t kMaxHeads = 1 << 24;  // B * Hq
 
@@ -126,6 +119,12 @@ AttnShape make_shape(int B, int Hq, int Hkv, int Tq, int Tkv, int causal, int wi
 }
 
 }  // namespace
+
+bool launch_waits(WaitCfg* wc) {
+  if (!status_ptr(&wc->status)) return false;
+  set_waits(wc);
+  return true;
+}
 
 bool encode_tile_map(CUtensorMap* map, const void* base, bool bf16, int D, int T, int BH,
                      int box_rows) {
@@ -213,6 +212,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_MISALIGNED: return "buffer not 16-byte aligned";
     case FA_ERR_LAUNCH: return "CUDA launch or driver call failed";
     case FA_ERR_TIMEOUT: return "a bounded device wait gave up";
+    case FA_ERR_BAD_INDEX: return "a page, length or position out of range";
   }
   return "unknown status";
 }
@@ -373,7 +373,8 @@ fa_status fa_device_status(unsigned int* bits, int clear, cudaStream_t stream) {
       return FA_ERR_LAUNCH;
   }
   *bits = v;
-  return v == 0 ? FA_OK : FA_ERR_TIMEOUT;
+  if (v == 0) return FA_OK;
+  return v == kStatusBadIndex ? FA_ERR_BAD_INDEX : FA_ERR_TIMEOUT;
 }
 
 }  // extern "C"

@@ -39,6 +39,18 @@ struct BwdLaunch {
 bool encode_tile_map(CUtensorMap* map, const void* base, bool bf16, int D, int T, int BH,
                      int box_rows);
 
+// Status word and wait bounds of a launch on the current device. Returns false
+// when the status word's address cannot be had.
+bool launch_waits(WaitCfg* wc);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// [lo, hi) byte ranges of two buffers intersect.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 

@@ -1,0 +1,61 @@
+// Shared definitions of the paged-cache kernels (fa_kv_append, fa_paged_fwd,
+// fa_page_select): the device view of the cache and the checks of everything
+// that only the device can see. The pages of the sources describe training
+// only; these kernels serve, with the forward's mathematics.
+#pragma once
+
+#include <cstdint>
+
+#include "fa_common.cuh"
+
+namespace fa {
+
+// Bit of the device status word beside those of sm103_ptx.cuh: a page, length,
+// position or selected page out of range. The access is skipped.
+constexpr uint32_t kStatusBadIndex = 4u;
+
+struct PagedView {
+  uint16_t* k;       // [num_pages, Hkv, page, D], 16-bit values
+  uint16_t* v;
+  uint16_t* bounds;  // [num_pages, Hkv, 2, D] or null
+  const int* table;  // [B, max_pages]
+  const int* lens;   // [B]
+  int B, Hkv, D, num_pages, page_shift, max_pages;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ void flag_bad_index(const PagedView& c) {
+  atomicOr(c.status, kStatusBadIndex);
+}
+
+// Keys of sequence b, new ones included, clamped to what its table can hold.
+__device__ __forceinline__ int cache_len(const PagedView& c, int b) {
+  const int n = __ldg(c.lens + b), most = c.max_pages << c.page_shift;
+  if (n >= 0 && n <= most) return n;
+  flag_bad_index(c);
+  return n < 0 ? 0 : most;
+}
+
+// New tokens of sequence b among the call's T rows.
+__device__ __forceinline__ int new_len(const PagedView& c, const int* new_lens, int b, int T) {
+  if (new_lens == nullptr) return T;
+  const int n = __ldg(new_lens + b);
+  if (n >= 0 && n <= T) return n;
+  flag_bad_index(c);
+  return n < 0 ? 0 : T;
+}
+
+// Pool page of page `p` of sequence b (0 <= p < max_pages), or -1.
+__device__ __forceinline__ int pool_page(const PagedView& c, int b, int p) {
+  const int id = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + p);
+  if (static_cast<unsigned>(id) < static_cast<unsigned>(c.num_pages)) return id;
+  flag_bad_index(c);
+  return -1;
+}
+
+// First element of row `slot` of KV head g in pool page `id`.
+__device__ __forceinline__ int64_t pool_row(const PagedView& c, int id, int g, int slot) {
+  return ((((static_cast<int64_t>(id) * c.Hkv + g) << c.page_shift) + slot)) * c.D;
+}
+
+}  // namespace fa

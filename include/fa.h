@@ -53,6 +53,7 @@
 #define FA_GB300_H_
 
 #include <stddef.h>
+#include <stdint.h>
 #include <cuda_runtime_api.h>
 
 #ifdef __cplusplus
@@ -66,7 +67,8 @@ typedef enum {
   FA_ERR_UNSUPPORTED_DTYPE = 3,    /* dtype not FA_FP16 / FA_BF16 */
   FA_ERR_MISALIGNED = 4,           /* a buffer is not 16-byte aligned */
   FA_ERR_LAUNCH = 5,               /* a CUDA launch or driver call failed */
-  FA_ERR_TIMEOUT = 6               /* a bounded device wait gave up */
+  FA_ERR_TIMEOUT = 6,              /* a bounded device wait gave up */
+  FA_ERR_BAD_INDEX = 7             /* a kernel met a page, length or position out of range */
 } fa_status;
 
 typedef enum { FA_FP16 = 0, FA_BF16 = 1 } fa_dtype;
@@ -173,14 +175,133 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
 /* Largest B * Hq * Tq that fa_bwd_noalloc accepts. */
 size_t fa_bwd_noalloc_max_rows(void);
 
+/* ------------------------------------------------------------------------
+ * Serving from a paged key/value cache. The pages of the sources describe
+ * training only and have no counterpart of these calls; the operation inside
+ * fa_paged_fwd is the forward above.
+ *
+ * The cache is a pool of pages: k and v are [num_pages, Hkv, page_size, D], so
+ * one KV head's keys of a page are page_size consecutive rows. Sequence b
+ * keeps key j in slot j % page_size of pool page page_table[b, j / page_size].
+ * kv_lens[b] counts the keys of sequence b, the tokens of the current call
+ * among them: with n_b new tokens (new_lens[b], or all T rows where new_lens
+ * is null) token t < n_b has position kv_lens[b] - n_b + t. Rows t >= n_b of a
+ * call are padding. One kv_lens array thus serves fa_kv_append and the
+ * fa_paged_fwd that follows; the caller advances it between steps.
+ *
+ * k_bounds (may be null: then fa_kv_append keeps none and fa_page_select
+ * refuses) is [num_pages, Hkv, 2, D]: the element-wise minimum and maximum of
+ * the keys written to the page since its slot 0 was last written.
+ *
+ * page_table and kv_lens live on the device and are read by the kernels, so
+ * calls can be captured into a graph and replayed with other lengths and
+ * pages. Entries of page_table past a sequence's last page are not read. What
+ * the host cannot check the kernels do: a page outside [0, num_pages), a length
+ * outside [0, max_pages * page_size], a position outside the angle tables or a
+ * new_lens[b] outside [0, T] raises a bit that fa_device_status() reports as
+ * FA_ERR_BAD_INDEX. Lengths are clamped to their range; keys of a bad page are
+ * neither written nor read (hidden from every query).
+ *
+ * Limits: B * Hkv <= 2^24, num_pages * Hkv <= 2^30, max_pages * page_size <= 2^30;
+ * page_size is 16, 32, 64, 128 or 256. Pool offsets are 64-bit. */
+typedef struct {
+  void* k;               /* [num_pages, Hkv, page_size, D] */
+  void* v;               /* [num_pages, Hkv, page_size, D] */
+  void* k_bounds;        /* [num_pages, Hkv, 2, D] or null */
+  const int* page_table; /* [B, max_pages] */
+  const int* kv_lens;    /* [B] */
+  int B, Hkv, D, num_pages, page_size, max_pages;
+  fa_dtype dt;
+} fa_paged_kv;
+
+/* Append the keys and values of new tokens to the cache, rotating the keys by
+ * their position on the way, and rotate the queries of the same tokens.
+ *   k_new, v_new  [B, Hkv, T, D]; q [B, Hq, T, D] or null (then q_out is null
+ *                 and Hq is not used). Each is read through its strides
+ *                 (elements) of the batch, head and token index; the innermost
+ *                 index is contiguous. Bases are 16-byte aligned and strides
+ *                 multiples of 8, so slices of a fused projection
+ *                 [B, T, (Hq + 2 Hkv) * D] are read in place.
+ *   q_out         [B, Hq, T, D] dense; padding rows are set to zero.
+ *   cos_table, sin_table  fp32 [rope_len, rot_dim / 2], row p for position p;
+ *                 both null for no rotation (rot_dim = 0).
+ * Dimensions i < rot_dim are rotated in pairs (i, i + rot_dim / 2), or, with
+ * interleaved = 1, (2i, 2i + 1): (a, b) -> (a cos - b sin, b cos + a sin) in
+ * fp32, rounded once; the rest is copied. rot_dim is a multiple of 16, at most
+ * D. Token t of sequence b is written to its slot; nothing else of the pools is
+ * touched. With k_bounds the bounds of every page that receives a token are
+ * updated: started afresh where the page's slot 0 is among the new tokens, else
+ * widened (so after tokens were taken back they may be wider than needed).
+ * 1 <= T <= 2^22. Two sequences of one call must not append to the same page.
+ * One kernel launch. Returns FA_OK or an error code (nothing launched on error). */
+fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* k_strides,
+                       const void* v_new, const int64_t* v_strides, const void* q,
+                       const int64_t* q_strides, void* q_out, int Hq, int T, const int* new_lens,
+                       const float* cos_table, const float* sin_table, int rope_len, int rot_dim,
+                       int interleaved, cudaStream_t stream);
+
+/* Bytes of device workspace fa_paged_fwd needs for Hq query heads over Hkv KV
+ * heads, Tq tokens per sequence and head dim D; independent of batch, lengths
+ * and device. Returns 0 for sizes fa_paged_fwd refuses. */
+size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D);
+
+/* Attention of Tq <= 8 new tokens per sequence over the paged cache (the forward
+ * of fa_fwd with keys and values read through the page table).
+ *   q [B, Hq, Tq, D], o likewise, lse [B, Hq, Tq] fp32; dense.
+ *   A key j < kv_lens[b] is hidden from the query at position p when
+ *     (causal && j > p)  or  (window > 0 && p >= j && p - j >= window)
+ *   so with causal = 1 the new tokens see the cache and each other causally
+ *   (the mask is aligned at the end of the cache, not at the top left).
+ *   sel, sel_lens  both null, or int32 [B, Hkv, n_sel] and [B, Hkv]: query heads
+ *     of KV head g then see only the keys of the sequence's pages sel[b, g, 0 ..
+ *     sel_lens[b, g] - 1] (page numbers within the sequence, distinct, any
+ *     order). An entry outside the sequence's pages, or sel_lens outside
+ *     [0, n_sel], is a bad index.
+ * A row that sees no key, and every padding row, gets O = 0 and LSE = -inf.
+ * Values of keys that no row sees never reach a result, whatever they hold. A
+ * key that is visible to one row and hidden from another adds exactly nothing to
+ * the latter as well.
+ *   workspace  fa_paged_workspace_size bytes, 16-byte aligned; contents
+ *     undefined before and after. Calls that may overlap need one each.
+ * The result does not depend on what else runs and is the same on every run.
+ * Returns FA_OK or an error code (nothing launched on error). */
+fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse, int Hq, int Tq,
+                       float scale, int causal, int window, const int* new_lens, const int* sel,
+                       const int* sel_lens, int n_sel, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+
+/* Bytes of device workspace fa_page_select needs. Returns 0 for non-positive
+ * sizes. */
+size_t fa_page_select_workspace_size(int B, int Hkv, int max_pages);
+
+/* Choose, for one new token per sequence, the pages its attention reads: per
+ * sequence and KV head the n_sel pages with the highest score
+ *   score(page) = max over the group's query heads h of
+ *                 sum_d max(q[h,d] min[page,d], q[h,d] max[page,d]),
+ * an upper bound of q . k over the page's keys, from k_bounds alone.
+ *   q [B, Hq, 1, D]; n_sel >= 1; the first keep_first and the last keep_last
+ *   pages of the sequence are always chosen (keep_first + keep_last <= n_sel).
+ *   sel [B, Hkv, n_sel] int32: the chosen page numbers within the sequence,
+ *   ascending, then -1; sel_lens [B, Hkv] int32: how many. A sequence of at most
+ *   n_sel pages gets all of them.
+ * The choice is the one that scores computed in 64 bits give, ties going to the
+ * lower page; a NaN score counts as the highest. A bad page (see above) scores
+ * lowest. 1 <= n_sel <= 2^20. Workspace: fa_page_select_workspace_size(B,
+ * Hkv, max_pages) bytes, 16-byte aligned; as for fa_paged_fwd.
+ * Returns FA_OK or an error code (nothing launched on error). */
+fa_status fa_page_select(const fa_paged_kv* kv, const void* q, int Hq, int n_sel, int keep_first,
+                         int keep_last, int* sel, int* sel_lens, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* fa_status_string(fa_status s);
 
 /* Read the device status word on the current device after synchronising
- * `stream`. *bits receives the raw word (bit 0: a bounded wait gave up); when
- * `clear` is non-zero the word is reset to 0 afterwards. Returns FA_OK when
- * the word is 0, FA_ERR_TIMEOUT when a wait gave up, FA_ERR_LAUNCH when the
- * read itself failed. */
+ * `stream`. *bits receives the raw word (bit 0: a bounded wait gave up; bit 2: a
+ * kernel of the paged cache met an index out of range); when `clear` is
+ * non-zero the word is reset to 0 afterwards. Returns FA_OK when the word is 0,
+ * FA_ERR_BAD_INDEX when only bit 2 is set, FA_ERR_TIMEOUT for any other bit,
+ * FA_ERR_LAUNCH when the read itself failed. */
 fa_status fa_device_status(unsigned int* bits, int clear, cudaStream_t stream);
 
 /* Self-test of the bounded waits (a library check; the pages have no

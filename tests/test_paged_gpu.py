@@ -1,0 +1,666 @@
+"""The paged-cache operators on the GPU against their plain definitions in 64 bits (paged_ref.py, where the error bounds
+are derived), at the sizes and masks where they can go wrong, and run together as a serving loop does."""
+import math
+
+import pytest
+import torch
+
+import attention_fa_fwd_03_gb300 as fa
+import paged_ref
+
+pytestmark = pytest.mark.gpu
+DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
+NAN = float("nan")
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(g, *shape, dtype):
+    return torch.randn(shape, generator=g).to(dtype)
+
+
+def make_table(g, B, max_pages, spare=3):
+    """Shuffled pool pages for every sequence, and the pool's size."""
+    n = B * max_pages + spare
+    return torch.randperm(n, generator=g)[: B * max_pages].view(B, max_pages).to(torch.int32), n
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def status_clear():
+    torch.cuda.synchronize()
+    return fa.fa_device_status() == 0
+
+
+def handle(k, v, table, lens, bounds=None):
+    d = [t.cuda() if t is not None else None for t in (k, v, table, lens, bounds)]
+    return fa.PagedKV(d[0], d[1], d[2], d[3], k_bounds=d[4])
+
+
+def attend(kv, q, scale, causal=True, window=0, new_lens=None, sel=None, sel_lens=None, stream=None):
+    q = q.cuda()
+    o, lse = torch.full_like(q, NAN), torch.full(q.shape[:3], NAN, device="cuda")
+    ws = torch.full((fa.fa_paged_workspace_size(q.shape[1], kv.Hkv, q.shape[2], kv.D),), 255, dtype=torch.uint8,
+                    device="cuda")  # as garbage as a workspace can be: every float a NaN
+    fa.fa_paged_fwd(kv, q, o, lse, scale, causal=causal, window=window,
+                    new_lens=None if new_lens is None else new_lens.cuda(), sel=None if sel is None else sel.cuda(),
+                    sel_lens=None if sel_lens is None else sel_lens.cuda(), workspace=ws, stream=stream)
+    return o, lse
+
+
+def check_attend(o, lse, ref, what=""):
+    ro, rl, bo, bl = ref
+    o, lse = o.double().cpu(), lse.double().cpu()
+    assert torch.equal(lse == -math.inf, rl == -math.inf), f"{what}: rows without keys"
+    bad = ~((o - ro).abs() <= bo)
+    assert not bad.any(), f"{what}: O off by {((o - ro).abs() / bo.clamp(min=1e-30))[bad].max():.3g} bounds at {bad.nonzero()[0].tolist()}"
+    fin = rl > -math.inf
+    bad = ~((lse - rl).abs()[fin] <= bl[fin])
+    assert not bad.any(), f"{what}: LSE off by {(lse - rl).abs()[fin].max():.3g}"
+
+
+# ------------------------------------------------------------------ append
+APPEND = [  # B, Hq, Hkv, D, page, T, start lengths, new lengths (None: T), rot, interleaved, dtype, bounds, with q
+    (1, 4, 2, 64, 16, 1, [0], None, 64, False, "fp16", True, True),
+    (2, 4, 1, 128, 64, 1, [63, 64], None, 128, False, "bf16", True, True),
+    (3, 6, 2, 96, 16, 5, [0, 14, 31], [5, 0, 3], 96, False, "fp16", True, True),
+    (3, 3, 3, 96, 32, 70, [0, 5, 31], [70, 1, 69], 48, True, "bf16", True, True),
+    (2, 16, 2, 256, 128, 200, [100, 0], [200, 131], 256, True, "fp16", True, True),
+    (2, 1, 1, 256, 256, 33, [250, 223], None, 128, False, "bf16", False, True),
+    (2, 8, 8, 128, 16, 64, [1, 16], None, 0, False, "bf16", True, False),
+    (5, 5, 5, 64, 32, 129, [0, 1, 31, 32, 33], [129, 128, 0, 1, 97], 32, True, "fp16", False, True),
+    (1, 40, 8, 128, 64, 700, [37], None, 128, False, "bf16", True, True),
+]
+
+
+@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"B{c[0]}h{c[1]}x{c[2]}d{c[3]}p{c[4]}T{c[5]}{c[10]}")
+@pytest.mark.parametrize("fused", [False, True])
+def test_append_matches_the_definition(case, fused):
+    B, Hq, Hkv, D, page, T, start, new, rot, inter, dt, with_bounds, with_q = case
+    dtype = DT[dt]
+    g = gen(B * 1000 + T)
+    n = new or [T] * B
+    lens = [s + m for s, m in zip(start, n)]
+    mp = -(-max(max(lens), 1) // page)
+    table, P = make_table(g, B, mp)
+    k_pool, v_pool = randn(g, P, Hkv, page, D, dtype=dtype), randn(g, P, Hkv, page, D, dtype=dtype)
+    bounds = torch.stack([-randn(g, P, Hkv, D, dtype=dtype).abs(), randn(g, P, Hkv, D, dtype=dtype).abs()], 2).contiguous()
+    if fused:  # one row per token with all heads side by side
+        qkv = randn(g, B, T, Hq + 2 * Hkv, D, dtype=dtype).cuda()
+        q, k, v = (t.transpose(1, 2) for t in qkv.split([Hq, Hkv, Hkv], 2))
+    else:
+        q, k, v = (randn(g, B, h, T, D, dtype=dtype).cuda() for h in (Hq, Hkv, Hkv))
+    rope_len = max(max(lens), 1)
+    ang = torch.arange(rope_len)[:, None] * 100.0 ** (-torch.arange(rot // 2) / max(rot // 2, 1))
+    cos, sin = ang.cos().float(), ang.sin().float()
+    kv = handle(k_pool, v_pool, table, i32(lens), bounds if with_bounds else None)
+    q_out = torch.full((B, Hq, T, D), NAN, dtype=dtype, device="cuda")
+    fa.fa_kv_append(kv, k, v, cos=cos.cuda() if rot else None, sin=sin.cuda() if rot else None, interleaved=inter,
+                    q=q if with_q else None, q_out=q_out if with_q else None, new_lens=None if new is None else i32(new).cuda())
+    assert status_clear()
+    got_k, got_v, got_q = kv.k.cpu(), kv.v.cpu(), q_out.cpu()
+    q, k, v = q.cpu(), k.cpu(), v.cpu()
+    h, tiny = paged_ref.half_step(dtype), paged_ref.smallest(dtype)
+    want_v, touched = v_pool.clone(), torch.zeros(P, page, dtype=torch.bool)
+    want_b = bounds.clone()
+    for b, (first, m) in enumerate(paged_ref.positions(lens, new, T)):
+        for t in range(m):
+            p = first + t
+            i, s = int(table[b, p // page]), p % page
+            touched[i, s] = True
+            want_v[i, :, s] = v[b, :, t]
+            x, err = paged_ref.rotate(k[b, :, t].double(), cos[p].double(), sin[p].double(), rot, inter)
+            assert ((got_k[i, :, s].double() - x).abs() <= h * x.abs() + err + tiny).all(), (b, t)
+            fresh = s == 0
+            want_b[i, :, 0] = got_k[i, :, s] if fresh else torch.minimum(want_b[i, :, 0], got_k[i, :, s])
+            want_b[i, :, 1] = got_k[i, :, s] if fresh else torch.maximum(want_b[i, :, 1], got_k[i, :, s])
+            if with_q:
+                x, err = paged_ref.rotate(q[b, :, t].double(), cos[p].double(), sin[p].double(), rot, inter)
+                assert ((got_q[b, :, t].double() - x).abs() <= h * x.abs() + err + tiny).all(), (b, t)
+        if with_q:
+            assert (got_q[b, :, m:] == 0).all()
+    assert torch.equal(got_v, want_v)
+    assert torch.equal(got_k.transpose(1, 2)[~touched], k_pool.transpose(1, 2)[~touched])  # nothing else was written
+    if with_bounds:
+        assert torch.equal(kv.k_bounds.cpu(), want_b)
+
+
+def test_append_is_bitwise_the_same_in_pieces():
+    """A prompt in one call, in several, and token by token gives the same cache and bounds."""
+    g = gen(5)
+    B, Hkv, D, page, n = 2, 2, 128, 16, 45
+    table, P = make_table(g, B, 3)
+    k, v = (randn(g, B, Hkv, n, D, dtype=torch.bfloat16).cuda() for _ in range(2))
+    ang = torch.arange(n)[:, None] * 100.0 ** (-torch.arange(64) / 64)
+    cos, sin = ang.cos().float().cuda(), ang.sin().float().cuda()
+    results = []
+    for sizes in ([45], [17, 28], [1] * 45, [16, 16, 13]):
+        kv = handle(torch.zeros(P, Hkv, page, D, dtype=torch.bfloat16), torch.zeros(P, Hkv, page, D, dtype=torch.bfloat16),
+                    table, i32([0, 0]), torch.zeros(P, Hkv, 2, D, dtype=torch.bfloat16))
+        at = 0
+        for m in sizes:
+            kv.kv_lens += m
+            fa.fa_kv_append(kv, k[:, :, at:at + m], v[:, :, at:at + m], cos=cos, sin=sin)
+            at += m
+        assert status_clear()
+        results.append([t.clone() for t in (kv.k, kv.v, kv.k_bounds)])
+    for r in results[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(r, results[0]))
+
+
+# ------------------------------------------------------------------ attention
+ATTEND = [  # B, Hq, Hkv, D, page, Tq, lengths, new lengths, causal, window, dtype
+    (1, 1, 1, 64, 16, 1, [1], None, True, 0, "fp16"),
+    (2, 8, 2, 128, 16, 1, [1024, 1000], None, True, 0, "fp16"),
+    (5, 4, 2, 128, 64, 1, [0, 1, 63, 64, 65], None, True, 0, "bf16"),
+    (5, 6, 2, 96, 32, 1, [31, 32, 33, 127, 129], None, False, 0, "fp16"),
+    (3, 8, 1, 256, 128, 1, [300, 7, 1029], None, True, 0, "bf16"),
+    (2, 5, 1, 256, 16, 8, [8, 517], None, True, 0, "fp16"),
+    (4, 7, 1, 64, 256, 3, [2, 3, 600, 255], None, True, 0, "bf16"),        # fewer keys than new tokens
+    (4, 21, 3, 64, 32, 5, [4000, 9, 65, 5], [5, 2, 0, 1], True, 0, "fp16"),  # padding rows
+    (3, 8, 2, 128, 64, 4, [700, 64, 66], None, False, 0, "bf16"),
+    (3, 8, 2, 128, 64, 4, [700, 64, 66], None, True, 1, "bf16"),           # each row sees itself only
+    (3, 8, 2, 96, 16, 6, [700, 64, 6], None, True, 50, "fp16"),
+    (3, 4, 4, 128, 32, 8, [1000, 3, 64], None, False, 20, "bf16"),
+    (2, 64, 1, 128, 64, 1, [333, 90], None, True, 0, "bf16"),              # 64 rows share the keys
+    (1, 64, 1, 128, 16, 8, [1000], None, True, 0, "fp16"),                 # 512 rows
+    (2, 17, 1, 64, 128, 2, [150, 129], None, True, 100, "bf16"),
+    (1, 32, 8, 128, 64, 1, [30001], None, True, 0, "bf16"),                # many parts per sequence
+    (40, 2, 1, 64, 16, 1, [(37 * i) % 211 for i in range(40)], None, True, 0, "fp16"),
+    (300, 1, 1, 64, 16, 2, [(i * i) % 97 for i in range(300)], None, True, 0, "bf16"),  # more sequences than threads
+]
+
+
+def paged_inputs(B, Hq, Hkv, D, page, Tq, lens, dtype, seed, fill=NAN, mult=1.0):
+    """Pools whose slots hold `fill` wherever no key was written, and the queries."""
+    g = gen(seed)
+    mp = max(-(-max(lens) // page), 1)
+    table, P = make_table(g, B, mp)
+    k, v = (torch.full((P, Hkv, page, D), fill, dtype=dtype) for _ in range(2))
+    for b, n in enumerate(lens):
+        for p in range(-(-n // page)):
+            m = min(page, n - p * page)
+            k[int(table[b, p]), :, :m] = randn(g, Hkv, m, D, dtype=dtype) * mult
+            v[int(table[b, p]), :, :m] = randn(g, Hkv, m, D, dtype=dtype)
+    return k, v, table, randn(g, B, Hq, Tq, D, dtype=dtype)
+
+
+@pytest.mark.parametrize("case", ATTEND, ids=lambda c: f"B{c[0]}h{c[1]}x{c[2]}d{c[3]}p{c[4]}T{c[5]}c{int(c[8])}w{c[9]}{c[10]}")
+def test_attend_matches_the_definition(case):
+    B, Hq, Hkv, D, page, Tq, lens, new, causal, window, dt = case
+    k, v, table, q = paged_inputs(B, Hq, Hkv, D, page, Tq, lens, DT[dt], seed=Hq * 100 + D)
+    scale = 1.0 / math.sqrt(D)
+    kv = handle(k, v, table, i32(lens))
+    o, lse = attend(kv, q, scale, causal, window, None if new is None else i32(new))
+    assert status_clear()
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, scale, causal, window, new))
+    again = attend(kv, q, scale, causal, window, None if new is None else i32(new))
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("fill", [math.inf, -math.inf, 65504.0])
+def test_attend_ignores_what_unwritten_slots_hold(fill):
+    lens = [5, 77, 130]
+    k, v, table, q = paged_inputs(3, 4, 2, 128, 64, 2, lens, torch.float16, seed=3, fill=fill)
+    o, lse = attend(handle(k, v, table, i32(lens)), q, 0.1)
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, 0.1, True, 0))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_sharp_softmax(D):
+    """Scores spread over hundreds: the running maximum moves often and most weights vanish."""
+    lens = [1200, 333]
+    k, v, table, q = paged_inputs(2, 8, 2, D, 32, 3, lens, torch.bfloat16, seed=8, mult=6.0)
+    scale = 4.0 / math.sqrt(D)
+    o, lse = attend(handle(k, v, table, i32(lens)), q, scale)
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, scale, True, 0))
+
+
+def test_attend_equal_scores_average_the_values():
+    lens = [100]
+    k, v, table, q = paged_inputs(1, 2, 1, 64, 16, 1, lens, torch.float16, seed=4)
+    o, lse = attend(handle(k, v, table, i32(lens)), torch.zeros_like(q), 1.0)
+    check_attend(o, lse, paged_ref.attend(torch.zeros_like(q), k, v, table, lens, 1.0, True, 0))
+    assert abs(float(lse[0, 0, 0]) - math.log(100)) < 1e-5
+
+
+@pytest.mark.parametrize("what", [NAN, math.inf])
+def test_attend_hidden_keys_add_nothing(what):
+    """Keys that a mask hides from a row, with NaN or infinite K and V: rows that do not see them stay as if they held
+    zeros, at the causal end (drafted tokens) and at the start of the window."""
+    lens, Tq, window = [200], 4, 64
+    k, v, table, q = paged_inputs(1, 4, 2, 128, 16, Tq, lens, torch.bfloat16, seed=6)
+    clean = attend(handle(k, v, table, i32(lens)), q, 0.1, True, window)
+    # rows 0..3 have positions 196..199 and see keys from 133, 134, 135 and 136
+    for bad, ok_rows in (((199, 198, 20), [0, 1]), ((133, 134, 20), [2, 3])):
+        k, v, table, q = paged_inputs(1, 4, 2, 128, 16, Tq, lens, torch.bfloat16, seed=6)
+        for j in bad:
+            for pool in (k, v):
+                pool[int(table[0, j // 16]), :, j % 16] = what
+        o, lse = attend(handle(k, v, table, i32(lens)), q, 0.1, True, window)
+        for r in ok_rows:
+            assert torch.isfinite(o[0, :, r]).all() and torch.isfinite(lse[0, :, r]).all(), (bad, r)
+            assert torch.equal(o[0, :, r], clean[0][0, :, r]), (bad, r)
+
+
+SELECTED = [  # B, Hq, Hkv, D, page, Tq, lengths, n_sel, dtype
+    (2, 8, 2, 128, 16, 1, [1000, 333], 7, "bf16"),
+    (3, 6, 3, 96, 64, 1, [640, 64, 1], 4, "fp16"),
+    (2, 4, 1, 256, 128, 1, [1025, 500], 3, "bf16"),
+    (2, 10, 2, 64, 32, 4, [400, 100], 5, "fp16"),
+    (9, 2, 2, 64, 16, 1, [0, 5, 16, 17, 100, 200, 300, 400, 512], 32, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", SELECTED, ids=lambda c: f"B{c[0]}h{c[1]}x{c[2]}d{c[3]}p{c[4]}T{c[5]}n{c[7]}")
+@pytest.mark.parametrize("window", [0, 40])
+def test_attend_over_given_pages(case, window):
+    B, Hq, Hkv, D, page, Tq, lens, n_sel, dt = case
+    k, v, table, q = paged_inputs(B, Hq, Hkv, D, page, Tq, lens, DT[dt], seed=D + n_sel)
+    g = gen(9)
+    sel = torch.full((B, Hkv, n_sel), 10 ** 6, dtype=torch.int32)  # behind the list: never read
+    count = torch.zeros(B, Hkv, dtype=torch.int32)
+    for b in range(B):
+        pages = -(-lens[b] // page)
+        for h in range(Hkv):
+            m = min(pages, int(torch.randint(0, n_sel + 1, (1,), generator=g)))
+            sel[b, h, :m] = torch.randperm(pages, generator=g)[:m].to(torch.int32)  # any order
+            count[b, h] = m
+    scale = 1.0 / math.sqrt(D)
+    o, lse = attend(handle(k, v, table, i32(lens)), q, scale, True, window, sel=sel, sel_lens=count)
+    assert status_clear()
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, scale, True, window, sel=sel, sel_lens=count))
+
+
+def test_attend_over_all_pages_by_list_equals_the_definition():
+    lens = [500, 16]
+    k, v, table, q = paged_inputs(2, 4, 2, 128, 16, 2, lens, torch.bfloat16, seed=12)
+    sel = torch.arange(32, dtype=torch.int32).expand(2, 2, 32).contiguous()
+    count = i32([[32, 32], [1, 1]])
+    o, lse = attend(handle(k, v, table, i32(lens)), q, 0.1, sel=sel, sel_lens=count)
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, 0.1, True, 0))
+
+
+# ------------------------------------------------------------------ selection
+SELECT = [  # B, Hq, Hkv, D, page, lengths, n_sel, keep_first, keep_last, dtype
+    (1, 4, 2, 128, 16, [1000], 8, 1, 2, "bf16"),
+    (3, 6, 2, 96, 32, [3200, 31, 0], 10, 0, 1, "fp16"),
+    (2, 16, 1, 256, 64, [3000, 2900], 5, 0, 0, "bf16"),
+    (2, 3, 3, 64, 16, [9000, 5000], 64, 1, 4, "fp16"),
+    (2, 8, 8, 128, 16, [700, 701], 43, 1, 1, "bf16"),     # one page left out
+    (2, 8, 8, 128, 16, [700, 16], 44, 1, 1, "bf16"),      # none left out
+    (4, 2, 1, 64, 128, [1, 128, 129, 4000], 1, 0, 1, "fp16"),
+    (2, 2, 1, 64, 16, [4000, 600], 7, 3, 4, "fp16"),      # only what is always kept
+    (1, 2, 1, 64, 16, [60000], 200, 2, 2, "bf16"),        # more pages than threads
+]
+
+
+def select(kv, q, n_sel, keep_first, keep_last):
+    sel = torch.full((kv.B, kv.Hkv, n_sel), -7, dtype=torch.int32, device="cuda")
+    count = torch.full((kv.B, kv.Hkv), -7, dtype=torch.int32, device="cuda")
+    ws = torch.full((fa.fa_page_select_workspace_size(kv.B, kv.Hkv, kv.max_pages),), 255, dtype=torch.uint8, device="cuda")
+    fa.fa_page_select(kv, q.cuda(), sel, count, keep_first=keep_first, keep_last=keep_last, workspace=ws)
+    return sel, count
+
+
+def bounds_for(g, P, Hkv, D, dtype):
+    a, b = randn(g, P, Hkv, D, dtype=dtype), randn(g, P, Hkv, D, dtype=dtype)
+    return torch.stack([torch.minimum(a, b), torch.maximum(a, b)], 2).contiguous()
+
+
+def check_select(q, bounds, table, lens, page, n_sel, kf, kl):
+    P, Hkv, _, D = bounds.shape
+    pool = torch.zeros(P, Hkv, page, D, dtype=q.dtype)
+    kv = handle(pool, pool.clone(), table, i32(lens), bounds)
+    sel, count = select(kv, q, n_sel, kf, kl)
+    want, want_count = paged_ref.select(q, bounds, table, lens, page, n_sel, kf, kl)
+    assert torch.equal(count.cpu(), want_count)
+    assert torch.equal(sel.cpu(), want)
+
+
+@pytest.mark.parametrize("case", SELECT, ids=lambda c: f"B{c[0]}h{c[1]}x{c[2]}d{c[3]}p{c[4]}n{c[6]}k{c[7]}{c[8]}")
+def test_select_matches_the_definition(case):
+    B, Hq, Hkv, D, page, lens, n_sel, kf, kl, dt = case
+    g = gen(D + n_sel)
+    table, P = make_table(g, B, max(-(-max(lens) // page), 1))
+    check_select(randn(g, B, Hq, 1, D, dtype=DT[dt]), bounds_for(g, P, Hkv, D, DT[dt]), table, lens, page, n_sel, kf, kl)
+    assert status_clear()
+
+
+@pytest.mark.parametrize("kind", ["equal", "pairs", "zero_query", "two_values"])
+def test_select_ties_go_to_the_lower_page(kind):
+    g = gen(31)
+    B, Hq, Hkv, D, page, lens = 2, 4, 2, 128, 16, [4800, 1605]
+    table, P = make_table(g, B, 300)
+    bounds, q = bounds_for(g, P, Hkv, D, torch.bfloat16), randn(g, B, Hq, 1, D, dtype=torch.bfloat16)
+    if kind == "equal":
+        bounds[:] = bounds[:1]
+    elif kind == "pairs":  # every page twice, far apart
+        for b in range(B):
+            for p in range(150):
+                bounds[int(table[b, p + 150])] = bounds[int(table[b, p])]
+    elif kind == "zero_query":
+        q.zero_()
+    else:
+        bounds[:] = bounds[torch.randint(0, 2, (P,), generator=g)]
+    for n_sel in (20, 33, 100):
+        check_select(q, bounds, table, lens, page, n_sel, 1, 1)
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_select_near_ties_as_in_64_bits(dt):
+    """Scores whose large parts cancel and whose small rest decides: sums in 32 bits would rank them by their rounding."""
+    g = gen(77)
+    B, Hq, Hkv, D, page, lens = 1, 1, 1, 256, 16, [6400]
+    dtype = DT[dt]
+    table, P = make_table(g, B, 400)
+    q = torch.ones(B, Hq, 1, D).to(dtype)
+    big = randn(g, D // 2, dtype=dtype) * 512
+    row = torch.cat([big, -big])
+    bounds = torch.empty(P, 1, 2, D, dtype=dtype)
+    for p in range(P):
+        perm = torch.randperm(D, generator=g)
+        x = row[perm].clone()
+        small = x.abs().argsort()[:8]
+        x[small] = (randn(g, 8, dtype=dtype) * 2.0 ** -12).to(dtype)
+        bounds[p, 0, 0] = bounds[p, 0, 1] = x
+    # the eight entries of least magnitude are four pairs x, -x: what is left of the large ones cancels exactly
+    for n_sel in (3, 50, 200):
+        check_select(q, bounds, table, lens, page, n_sel, 0, 1)
+
+
+def test_select_nan_and_infinite_bounds():
+    g = gen(13)
+    lens, page = [3200], 16
+    table, P = make_table(g, 1, 200)
+    bounds, q = bounds_for(g, P, 2, 64, torch.float16), randn(g, 1, 4, 1, 64, dtype=torch.float16)
+    bounds[int(table[0, 150]), :, :, 5] = NAN
+    bounds[int(table[0, 77]), :, 1, 6] = math.inf
+    bounds[int(table[0, 30]), :, 0, 7] = -math.inf
+    bounds[int(table[0, 31]), :, :, 7] = -math.inf
+    for n_sel in (2, 3, 4, 10, 150):
+        check_select(q, bounds, table, lens, page, n_sel, 0, 1)
+
+
+# ------------------------------------------------------------------ what only the device can see
+def test_bad_pages_and_lengths_are_reported_and_skipped():
+    g = gen(21)
+    B, Hq, Hkv, D, page = 3, 4, 2, 64, 16
+    lens = [100, 64, 40]
+    k, v, table, q = paged_inputs(B, Hq, Hkv, D, page, 1, lens, torch.float16, seed=21)
+    P = k.shape[0]
+    for bad in (-1, P, 2 ** 31 - 1, -2 ** 31):
+        t = table.clone()
+        t[0, 2], t[1, 0] = bad, bad
+        o, lse = attend(handle(k, v, t, i32(lens)), q, 0.1)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status() == 4
+        check_attend(o, lse, paged_ref.attend(q, k, v, t, lens, 0.1, True, 0), f"page {bad}")
+    assert status_clear()
+    # entries behind a sequence's last page are not looked at
+    t = table.clone()
+    t[1, 4:], t[2, 3:] = -5, 10 ** 9
+    o, lse = attend(handle(k, v, t, i32(lens)), q, 0.1)
+    assert status_clear()
+    # lengths: clamped to what the table holds, or to none
+    full = [table.shape[1] * page, 64, 0]
+    k2, v2 = torch.nan_to_num(k, nan=0.25), torch.nan_to_num(v, nan=0.5)
+    o, lse = attend(handle(k2, v2, table, i32([10 ** 6, 64, -3])), q, 0.1)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 4
+    check_attend(o, lse, paged_ref.attend(q, k2, v2, table, full, 0.1, False, 0))
+    # selected pages and their number
+    sel, count = i32([[[0, 7, -2, 1]] * 2] * 3), i32([[4, 4], [4, 2], [4, 4]])
+    o, lse = attend(handle(k, v, table, i32(lens)), q, 0.1, sel=sel, sel_lens=count)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 4
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, 0.1, True, 0, sel=sel, sel_lens=count))
+    sel = i32([[[0, 2, 1, 1000]] * 2] * 3)
+    o, lse = attend(handle(k, v, table, i32(lens)), q, 0.1, sel=sel[..., :3].contiguous(), sel_lens=i32([[9, 3], [-1, 3], [3, 3]]))
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 4
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, 0.1, True, 0, sel=sel[..., :3],
+                                          sel_lens=i32([[3, 3], [0, 3], [3, 3]])))
+    # selection: a bad page scores lowest
+    bounds = bounds_for(g, P, Hkv, D, torch.float16)
+    t = table.clone()
+    t[0, 3] = P
+    kv = handle(k, v, t, i32(lens), bounds)
+    for n_sel in (3, 6):
+        got = select(kv, q, n_sel, 0, 1)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status() == 4
+        want = paged_ref.select(q, bounds, t, lens, page, n_sel, 0, 1)
+        assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[1].cpu(), want[1])
+
+
+def test_append_skips_what_has_no_place():
+    g = gen(22)
+    B, Hkv, D, page, T = 4, 2, 64, 16, 4
+    table, P = make_table(g, B, 2)
+    table[1, 0] = P + 7                       # a page that is not there
+    lens = [2, 6, 34, 20]                     # starts before the sequence; bad page; beyond the table (clamped); fine
+    k, v = randn(g, B, Hkv, T, D, dtype=torch.bfloat16), randn(g, B, Hkv, T, D, dtype=torch.bfloat16)
+    pools = [randn(g, P, Hkv, page, D, dtype=torch.bfloat16) for _ in range(2)]
+    cos = torch.ones(19, 32)                  # positions 0..18: sequence 3 has angles for its first three tokens
+    kv = handle(*pools, table, i32(lens), torch.zeros(P, Hkv, 2, D, dtype=torch.bfloat16))
+    fa.fa_kv_append(kv, k.cuda(), v.cuda(), cos=cos.cuda(), sin=torch.zeros(19, 32).cuda())
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 4
+    for got, pool, x in ((kv.k, pools[0], k), (kv.v, pools[1], v)):
+        want = pool.clone()
+        for b, t, p in [(0, 2, 0), (0, 3, 1), (3, 0, 16), (3, 1, 17), (3, 2, 18)]:
+            want[int(table[b, p // page]), :, p % page] = x[b, :, t]
+        assert torch.equal(got.cpu(), want)
+    # new_lens out of range: clamped
+    kv = handle(*pools, table, i32([4, 0, 0, 0]))
+    fa.fa_kv_append(kv, k.cuda(), v.cuda(), new_lens=i32([9, -1, 0, 0]).cuda())
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 4
+    want = pools[0].clone()
+    want[int(table[0, 0]), :, :4] = k[0]
+    assert torch.equal(kv.k.cpu(), want)
+
+
+def test_pool_offsets_beyond_32_bits():
+    """Pools of more than 2^32 bytes, pages at both ends."""
+    Hkv, page, D, Hq = 8, 64, 128, 16
+    P = 2 ** 32 // (Hkv * page * D) + 5       # elements beyond 2^32
+    g = gen(2)
+    k, v = (torch.zeros(P, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ids = [P - 1, 0, P - 3, 1]
+    lens = [250]
+    small = [randn(g, 4, Hkv, page, D, dtype=torch.bfloat16) for _ in range(2)]
+    for i, p in enumerate(ids):
+        k[p], v[p] = small[0][i].cuda(), small[1][i].cuda()
+    q = randn(g, 1, Hq, 1, D, dtype=torch.bfloat16)
+    kv = fa.PagedKV(k, v, i32([ids]).cuda(), i32(lens).cuda())
+    o, lse = attend(kv, q, 0.1)
+    ref = paged_ref.attend(q, small[0], small[1], i32([[0, 1, 2, 3]]), lens, 0.1, True, 0)
+    check_attend(o, lse, ref)
+    new = randn(g, 1, Hkv, 1, D, dtype=torch.bfloat16)
+    kv.kv_lens.fill_(64)                      # the last slot of page P - 1
+    fa.fa_kv_append(kv, new.cuda(), new.cuda())
+    assert status_clear()
+    assert torch.equal(k[P - 1, :, 63].cpu(), new[0, :, 0]) and torch.equal(v[P - 1, :, 63].cpu(), new[0, :, 0])
+    assert torch.equal(k[P - 1, :, :63].cpu(), small[0][0][:, :63])
+
+
+# ------------------------------------------------------------------ together
+def rope_tables(n, half):
+    ang = torch.arange(n, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(half, dtype=torch.float64) / half)
+    return ang.cos().float().cuda(), ang.sin().float().cuda()
+
+
+def test_serving_loop_equals_dense_attention():
+    """Prompt, then tokens one by one and drafts of four through append and attention, against the dense forward on the
+    concatenated keys: the last rows of fa_fwd with all rows as queries."""
+    g = gen(40)
+    B, Hq, Hkv, D, page, total = 2, 8, 2, 128, 32, 301
+    dt, scale = torch.bfloat16, 1 / math.sqrt(128)
+    table, P = make_table(g, B, 10)
+    cos, sin = rope_tables(total, D // 2)
+    kv = handle(torch.full((P, Hkv, page, D), NAN, dtype=dt), torch.full((P, Hkv, page, D), NAN, dtype=dt), table, i32([0, 0]),
+                torch.full((P, Hkv, 2, D), NAN, dtype=dt))
+    q, k, v = (randn(g, B, h, total, D, dtype=dt).cuda() for h in (Hq, Hkv, Hkv))
+    qr = torch.empty_like(q)
+    at = 0
+    outs = []
+    for m in [290, 1, 1, 4, 1, 4]:
+        kv.kv_lens += m
+        part = torch.empty(B, Hq, m, D, dtype=dt, device="cuda")
+        fa.fa_kv_append(kv, k[:, :, at:at + m], v[:, :, at:at + m], cos=cos, sin=sin, q=q[:, :, at:at + m], q_out=part)
+        qr[:, :, at:at + m] = part
+        if m <= 8:
+            outs.append((at, m, *attend(kv, part, scale)))
+        at += m
+    assert status_clear()
+    # dense keys as the cache holds them
+    pages = kv.page_table.long()
+    kd = kv.k[pages].transpose(1, 2).reshape(B, Hkv, -1, D)[:, :, :total].contiguous()
+    vd = kv.v[pages].transpose(1, 2).reshape(B, Hkv, -1, D)[:, :, :total].contiguous()
+    assert torch.equal(vd, v)
+    o, lse = torch.empty_like(q), torch.empty(B, Hq, total, device="cuda")
+    fa.fa_fwd(qr, kd, vd, o, lse, scale, causal=True)
+    torch.cuda.synchronize()
+    for at, m, po, pl in outs:
+        _, _, bo, bl = paged_ref.attend(qr[:, :, at:at + m].cpu(), kv.k.cpu(), kv.v.cpu(), kv.page_table.cpu(), [at + m] * B,
+                                        scale, True, 0)
+        # both sides are within the bound of the definition (the dense forward rounds the same quantities)
+        assert ((po.double() - o[:, :, at:at + m].double()).abs().cpu() <= 2 * bo).all(), at
+        assert ((pl.double() - lse[:, :, at:at + m].double()).abs().cpu() <= 2 * bl + 1e-5).all(), at
+
+
+def test_selected_pages_in_a_loop():
+    """Append keeps the bounds, selection reads them, attention reads the selected pages; with room for every page the
+    result is the full attention's."""
+    g = gen(41)
+    B, Hq, Hkv, D, page = 2, 8, 2, 64, 16
+    dt = torch.float16
+    table, P = make_table(g, B, 20)
+    cos, sin = rope_tables(320, D // 2)
+    kv = handle(*(torch.full(s, NAN, dtype=dt) for s in ((P, Hkv, page, D),) * 2), table, i32([0, 0]),
+                torch.full((P, Hkv, 2, D), NAN, dtype=dt))
+    for m in (300, 1, 1, 5, 1):
+        kv.kv_lens += m
+        q, k, v = (randn(g, B, h, m, D, dtype=dt).cuda() for h in (Hq, Hkv, Hkv))
+        qr = torch.empty_like(q)
+        fa.fa_kv_append(kv, k, v, cos=cos, sin=sin, q=q, q_out=qr)
+        if m > 1:
+            continue
+        n = int(kv.kv_lens[0])
+        pages = -(-n // page)
+        used = kv.k[table[0, :pages].long().cuda()].float()  # [pages, Hkv, page, D]
+        lo = torch.nan_to_num(used, nan=math.inf).amin(2)
+        assert torch.equal(kv.k_bounds[table[0, :pages].long().cuda()][:, :, 0].float(), lo)
+        full = attend(kv, qr, 0.125)
+        for n_sel in (6, 20):
+            sel, count = select(kv, qr, n_sel, 1, 1)
+            o, lse = attend(kv, qr, 0.125, sel=sel, sel_lens=count)
+            assert status_clear()
+            ref = paged_ref.attend(qr.cpu(), kv.k.cpu(), kv.v.cpu(), table, [n] * B, 0.125, True, 0, sel=sel.cpu(), sel_lens=count.cpu())
+            check_attend(o, lse, ref)
+            if n_sel == 20:
+                ref_full = paged_ref.attend(qr.cpu(), kv.k.cpu(), kv.v.cpu(), table, [n] * B, 0.125, True, 0)
+                check_attend(*full, ref_full)
+                check_attend(o, lse, ref_full)
+
+
+def test_decoding_step_in_a_graph_replayed_at_other_lengths():
+    """The whole step (advance, append, select, attend) captured once and replayed; the same steps eagerly give the same
+    bits. The graph was captured at a short length and runs on past it."""
+    def setup():
+        g = gen(50)
+        B, Hq, Hkv, D, page = 3, 4, 2, 128, 16
+        dt = torch.bfloat16
+        table, P = make_table(g, B, 12)
+        pools = [torch.zeros(P, Hkv, page, D, dtype=dt) for _ in range(2)]
+        kv = handle(*pools, table, i32([3, 40, 77]), torch.zeros(P, Hkv, 2, D, dtype=dt))
+        pre = [randn(g, P, Hkv, page, D, dtype=dt).cuda() for _ in range(2)]
+        kv.k.copy_(pre[0]), kv.v.copy_(pre[1])
+        kv.k_bounds[:, :, 0], kv.k_bounds[:, :, 1] = kv.k.amin(2), kv.k.amax(2)
+        cos, sin = rope_tables(192, 64)
+        s = dict(kv=kv, cos=cos, sin=sin, q=torch.empty(B, Hq, 1, D, dtype=dt, device="cuda"),
+                 k=torch.empty(B, Hkv, 1, D, dtype=dt, device="cuda"), v=torch.empty(B, Hkv, 1, D, dtype=dt, device="cuda"))
+        s.update(qr=torch.empty_like(s["q"]), o=torch.empty_like(s["q"]), lse=torch.empty(B, Hq, 1, device="cuda"),
+                 sel=torch.empty(B, Hkv, 4, dtype=torch.int32, device="cuda"),
+                 n=torch.empty(B, Hkv, dtype=torch.int32, device="cuda"),
+                 ws=torch.empty(fa.fa_paged_workspace_size(Hq, Hkv, 1, D), dtype=torch.uint8, device="cuda"),
+                 ws2=torch.empty(fa.fa_page_select_workspace_size(B, Hkv, 12), dtype=torch.uint8, device="cuda"))
+        return s
+
+    def step(s):
+        kv = s["kv"]
+        kv.kv_lens.add_(1)
+        fa.fa_kv_append(kv, s["k"], s["v"], cos=s["cos"], sin=s["sin"], q=s["q"], q_out=s["qr"])
+        fa.fa_page_select(kv, s["qr"], s["sel"], s["n"], keep_first=1, keep_last=1, workspace=s["ws2"])
+        fa.fa_paged_fwd(kv, s["qr"], s["o"], s["lse"], 0.09, causal=True, sel=s["sel"], sel_lens=s["n"], workspace=s["ws"])
+
+    def feed(s, i):
+        g = gen(1000 + i)
+        for n in ("q", "k", "v"):
+            s[n].copy_(torch.randn(s[n].shape, generator=g))
+
+    eager, outs = setup(), []
+    for i in range(40):
+        feed(eager, i)
+        step(eager)
+        outs.append((eager["o"].clone(), eager["lse"].clone(), eager["sel"].clone()))
+    s = setup()
+    feed(s, 0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(s)
+    torch.cuda.current_stream().wait_stream(side)
+    s = setup()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(s)
+    for i in range(40):
+        feed(s, i)
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip((s["o"], s["lse"], s["sel"]), outs[i])), i
+    assert status_clear()
+    assert torch.equal(s["kv"].k, eager["kv"].k) and torch.equal(s["kv"].k_bounds, eager["kv"].k_bounds)
+
+
+def test_two_streams_with_a_workspace_each():
+    lens = [3000, 2000]
+    a = paged_inputs(2, 8, 2, 128, 64, 1, lens, torch.bfloat16, seed=60)
+    b = paged_inputs(2, 8, 2, 64, 16, 2, lens, torch.float16, seed=61)
+    ka, kb = handle(a[0], a[1], a[2], i32(lens)), handle(b[0], b[1], b[2], i32(lens))
+    want = attend(ka, a[3], 0.09), attend(kb, b[3], 0.125)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (kv, x, sc) in enumerate(((ka, a[3], 0.09), (kb, b[3], 0.125))):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(attend(kv, x, sc))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_an_explicit_stream_is_used():
+    lens = [500]
+    k, v, table, q = paged_inputs(1, 4, 2, 64, 16, 1, lens, torch.float16, seed=62)
+    kv = handle(k, v, table, i32(lens))
+    want = attend(kv, q, 0.1)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    q, (o, lse) = q.cuda(), (torch.empty_like(t) for t in want)
+    ws = torch.empty(fa.fa_paged_workspace_size(4, 2, 1, 64), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for handle_ in (st, st.cuda_stream):
+        o.fill_(NAN)
+        torch.cuda.synchronize()
+        fa.fa_paged_fwd(kv, q, o, lse, 0.1, causal=True, workspace=ws, stream=handle_)
+        st.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
