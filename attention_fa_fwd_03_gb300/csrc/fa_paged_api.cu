@@ -163,7 +163,7 @@ fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* 
 size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Tq < 1 || Tq > kDecodeMaxTq) return 0;
   if (!(D == 64 || D == 96 || D == 128 || D == 256)) return 0;
-  return 256;
+  return paged_fwd_workspace(Hq / Hkv * Tq, D);
 }
 
 fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse, int Hq, int Tq,
@@ -212,7 +212,14 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
   a.ws = static_cast<float*>(workspace);
   a.bf16 = kv->dt == FA_BF16;
   a.stream = stream;
-  return launch_paged_fwd(a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  cudaError_t e;
+  switch (kv->D) {
+    case 64: e = launch_paged_fwd_d64(a); break;
+    case 96: e = launch_paged_fwd_d96(a); break;
+    case 128: e = launch_paged_fwd_d128(a); break;
+    default: e = launch_paged_fwd_d256(a); break;
+  }
+  return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 size_t fa_page_select_workspace_size(int B, int Hkv, int max_pages) {

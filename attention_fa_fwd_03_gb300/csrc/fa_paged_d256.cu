@@ -1,0 +1,4 @@
+// Paged-cache attention kernels for head dim 256.
+#include "fa_paged_fwd.cuh"
+
+FA_DEFINE_PAGED_HEAD_DIM(256)

@@ -1,0 +1,767 @@
+// Attention of up to 8 new tokens per sequence over the paged cache: the
+// forward's online softmax, split over the cache's length and joined.
+//
+//   S = scale q K^T over visible keys, m = max S, l = sum 2^(S - m) (exp2
+//   domain), O = sum 2^(S - m) V / l, LSE = (m + log2 l) ln 2
+//
+// What bounds it: every visible key's K and V row is read once and used by the
+// (Hq / Hkv) * Tq query rows of its KV head, 4 D flops per row for 4 D bytes:
+// at most a few tens of flops per byte, far below the tensor cores' ridge. So
+// the kernel is built around keeping HBM busy.
+//
+// Split. A unit is a (sequence, KV head, block of up to 16 RW rows); its keys
+// are cut into tiles of 64. Only the device knows the lengths, so every CTA of a
+// grid that fills the GPU once sums the tiles of all units and takes an equal
+// share of the whole list, whatever the lengths of the sequences: CTA c the
+// tiles [T c / G, T (c + 1) / G). A share is a run of segments; the segments
+// that cover a whole unit write O and LSE themselves, the others (at most the
+// first and the last of a CTA) leave (m, l, unnormalised O) in the workspace and
+// a second kernel joins them. Nothing depends on which CTA finishes first, so
+// results are the same on every run.
+//
+// Inside a CTA one warp looks up pages and loads tiles by TMA (one box per page
+// piece and 64 columns, 128-byte swizzle) into a ring of stages; KW warps per
+// row block each take 16 keys of a tile and keep a running maximum and sum of
+// their own, so tiles need no barrier between warps. Scores and outputs are
+// m16n8k16 tensor-core products fed by ldmatrix: a 128-row tcgen05 tile would be
+// at least half padding here (at most 64 rows, usually 4 to 8), and at these few
+// rows the warp-level products take under a third of the time the tile's bytes
+// need.
+#pragma once
+
+#include "fa_inst.cuh"
+#include "fa_paged_launch.h"
+
+namespace fa {
+
+constexpr int kPagedTile = 64;       // keys of a tile
+constexpr int kPagedKeyWarps = 4;    // warps that share a tile's keys, 16 each
+
+struct PagedFwdArgs {
+  PagedView c;
+  const uint16_t* q;
+  uint16_t* o;
+  float* lse;
+  int Hq, Tq, causal, window;
+  float scale_log2;
+  const int* new_lens;
+  const int *sel, *sel_lens;
+  int n_sel;
+  int rows, row_blocks;  // query rows of a KV head and their blocks
+  // workspace: parts of units, two slots per CTA (0: the unit began in an
+  // earlier CTA, 1: it goes on in the next one)
+  float* part_o;   // [2 parts][block rows][D]
+  float2* part_ml; // [2 parts][block rows] (max, sum)
+  int4* joins;     // [parts]: unit, first part, last part, or unit = -1
+  WaitCfg wc;
+};
+
+template <int D_, int RW_, bool BF16_>
+struct PagedCfg {
+  static constexpr int D = D_, RW = RW_;
+  static constexpr bool BF16 = BF16_;
+  static constexpr int KW = kPagedKeyWarps;
+  static constexpr int ROWS = 16 * RW;               // rows of a block
+  static constexpr int WARPS = KW * RW;              // consumer warps; one producer warp beside them
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int KREG = (D + 63) / 64;         // 64-column regions of a row
+  static constexpr int REGION = kPagedTile * 128;
+  static constexpr int TILE = KREG * REGION;         // K (or V) rows of a stage
+  // RW = 1: two CTAs per SM (three at D = 64) with about 100 KB in flight each;
+  // more rows: one CTA per SM
+  static constexpr int STAGES = D == 256 ? (RW == 1 ? 3 : 2) : D == 64 ? (RW == 1 ? 4 : 6) : (RW == 1 ? 3 : 5);
+  static constexpr int CTAS = RW == 1 && D < 256 ? (D == 64 ? 3 : 2) : 1;
+  static constexpr int QREGION = ROWS * 128;
+  static constexpr int OP = D + 8;                   // row pitch of the merge buffer (floats)
+  static constexpr int OFF_KV = 0;
+  static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
+  static constexpr int OFF_O = OFF_Q + KREG * QREGION;
+  static constexpr int OFF_ML = OFF_O + ROWS * OP * 4;
+  static constexpr int SMEM_BYTES = OFF_ML + KW * ROWS * 8 + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory");
+};
+
+// ------------------------------------------------------------- tensor cores
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+// c += A (16 x 16, row-major fragments) * B (16 x 8)
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ----------------------------------------------------------------- the list
+// An item is a sequence (every KV head and row block of it has the same tiles)
+// or, with selected pages, a (sequence, KV head); `mult` units each.
+__device__ __forceinline__ int item_count(const PagedFwdArgs& p) { return p.sel ? p.c.B * p.c.Hkv : p.c.B; }
+__device__ __forceinline__ int item_mult(const PagedFwdArgs& p) {
+  return (p.sel ? 1 : p.c.Hkv) * p.row_blocks;
+}
+
+struct Item {
+  int b;       // sequence
+  int len, n;  // keys and new tokens
+  int first;   // first tile of the list that holds a visible key
+  int tiles;   // tiles of each unit
+};
+__device__ __forceinline__ Item load_item(const PagedFwdArgs& p, int i) {
+  Item it;
+  it.b = p.sel ? i / p.c.Hkv : i;
+  it.len = cache_len(p.c, it.b);
+  it.n = new_len(p.c, p.new_lens, it.b, p.Tq);
+  it.first = 0;
+  int keys = it.len;
+  if (p.sel) {
+    int m = __ldg(p.sel_lens + i);
+    if (m < 0 || m > p.n_sel) {
+      flag_bad_index(p.c);
+      m = m < 0 ? 0 : p.n_sel;
+    }
+    keys = m << p.c.page_shift;  // at most 2^20 entries of 2^8 keys
+  } else if (p.window > 0) {
+    it.first = max(0, it.len - it.n - p.window + 1) / kPagedTile;
+  }
+  it.tiles = it.n > 0 ? (keys + kPagedTile - 1) / kPagedTile - it.first : 0;
+  return it;
+}
+
+// One CTA's share of the list, found by all its threads.
+struct Share {
+  long long total, lo, hi;
+  int parts;       // CTAs with a share: every one of them has a tile
+  int item;        // where lo falls
+  long long rest;  // tiles of that item before lo
+};
+template <int THREADS>
+__device__ __forceinline__ Share find_share(const PagedFwdArgs& p, int part, int parts) {
+  __shared__ long long sums[THREADS / 32];
+  __shared__ long long found_rest;
+  __shared__ int found_item;
+  const int items = item_count(p), mult = item_mult(p);
+  const int per = (items + THREADS - 1) / THREADS;
+  const int i0 = threadIdx.x * per, i1 = min(items, i0 + per);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) mine += static_cast<long long>(load_item(p, i).tiles) * mult;
+  long long incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  Share s;
+  s.total = total;
+  s.parts = static_cast<int>(min(total, static_cast<long long>(parts)));
+  s.lo = part < s.parts ? total * part / s.parts : total;
+  s.hi = part < s.parts ? total * (part + 1) / s.parts : total;
+  if (s.lo >= before && s.lo < before + mine) {
+    long long rest = s.lo - before;
+    int i = i0;
+    for (; i < i1 - 1; ++i) {
+      const long long n = static_cast<long long>(load_item(p, i).tiles) * mult;
+      if (rest < n) break;
+      rest -= n;
+    }
+    found_item = i;
+    found_rest = rest;
+  }
+  __syncthreads();
+  s.item = found_item;
+  s.rest = found_rest;
+  return s;
+}
+
+// Walks the segments of a share: unit (item, sub), its tiles [t0, t1).
+struct Walk {
+  Item it;
+  int item, sub, mult, items;
+  int t0, t1;
+  long long left;
+  __device__ __forceinline__ bool start(const PagedFwdArgs& p, const Share& s) {
+    left = s.hi - s.lo;
+    if (left <= 0) return false;
+    mult = item_mult(p);
+    items = item_count(p);
+    item = s.item;
+    it = load_item(p, item);
+    // tiles and sub are in range unless the lengths change under the call,
+    // which must not lead out of the buffers either
+    const int tiles = max(it.tiles, 1);
+    sub = static_cast<int>(min(s.rest / tiles, static_cast<long long>(mult - 1)));
+    t0 = static_cast<int>(min(s.rest - static_cast<long long>(sub) * tiles, static_cast<long long>(tiles - 1)));
+    t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + left));
+    return true;
+  }
+  __device__ __forceinline__ bool next(const PagedFwdArgs& p) {
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    if (++sub == mult) {
+      sub = 0;
+      do {
+        if (++item >= items) return false;  // the lengths changed under the call: stay inside the list
+        it = load_item(p, item);
+      } while (it.tiles == 0);
+    }
+    t0 = 0;
+    t1 = static_cast<int>(min(static_cast<long long>(it.tiles), left));
+    return true;
+  }
+  __device__ __forceinline__ int kv_head(const PagedFwdArgs& p) const {
+    return p.sel ? item % p.c.Hkv : sub / p.row_blocks;
+  }
+  __device__ __forceinline__ int row_block(const PagedFwdArgs& p) const { return sub % p.row_blocks; }
+};
+
+// Row 0 of block `rb` of (b, g) among the rows of q, o and lse.
+__device__ __forceinline__ int64_t block_row0(const PagedFwdArgs& p, int b, int g, int rb, int block_rows) {
+  return (static_cast<int64_t>(b) * p.c.Hkv + g) * p.rows + rb * block_rows;
+}
+
+// O = sum / l and LSE of one row chunk of 8 values.
+template <bool BF16>
+__device__ __forceinline__ void store_out8(uint16_t* dst, const float (&x)[8], float inv) {
+  uint4 w;
+  w.x = pack2<BF16>(x[0] * inv, x[1] * inv);
+  w.y = pack2<BF16>(x[2] * inv, x[3] * inv);
+  w.z = pack2<BF16>(x[4] * inv, x[5] * inv);
+  w.w = pack2<BF16>(x[6] * inv, x[7] * inv);
+  *reinterpret_cast<uint4*>(dst) = w;
+}
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.f || l != l ? (m + __log2f(l)) * kLn2 : -INFINITY;
+}
+
+// A position no query reaches: the key's slot was not loaded.
+constexpr int kNoPosition = 0x7fffff00;
+
+// ------------------------------------------------------------------- kernel
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::CTAS)
+fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                    const PagedFwdArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES];
+  __shared__ int key_pos[C::STAGES][C::KW];  // position of the first of each warp's 16 keys
+  __shared__ int abort_flag;
+  constexpr int D = C::D;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PagedView& c = p.c;
+  const int part = blockIdx.x, parts = gridDim.x;
+  const uint64_t tmo = p.wc.timeout_cycles;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), C::WARPS);
+    }
+    fence_mbar_init();
+  }
+  grid_wait_prior();
+  grid_release_next();
+  const Share share = find_share<C::THREADS>(p, part, parts);  // barriers inside
+  Walk w;
+
+  if (warp == C::WARPS) {
+    // ---------------------------------------------------------- producer warp
+    const int piece = min(1 << c.page_shift, kPagedTile);  // keys of a page in one tile
+    const int pieces = kPagedTile / piece;
+    const uint32_t box = static_cast<uint32_t>(piece) * 128u;
+    int issued = 0;
+    bool ok = w.start(p, share);
+    while (ok) {
+      const int g = w.kv_head(p);
+      const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
+      const int64_t u = static_cast<int64_t>(w.it.b) * c.Hkv + g;
+      const int list = p.sel ? (w.it.tiles * kPagedTile) >> c.page_shift : pages;  // entries that tiles reach
+      const int count = p.sel ? min(list, max(0, min(p.n_sel, __ldg(p.sel_lens + u)))) : pages;
+      // pages of list entries [e0, e0 + 32) and the next 32, one per lane
+      auto look_up = [&](int e, int* page, int* id) {
+        *page = -1;
+        *id = -1;
+        if (e >= count) return;
+        int pg = e;
+        if (p.sel) {
+          pg = __ldg(p.sel + u * p.n_sel + e);
+          if (pg < 0 || pg >= pages) {
+            flag_bad_index(c);
+            return;
+          }
+        }
+        *page = pg;
+        *id = pool_page(c, w.it.b, pg);
+      };
+      int e0 = ((w.it.first + w.t0) * kPagedTile) >> c.page_shift;
+      int page0, id0, page1, id1;
+      look_up(e0 + lane, &page0, &id0);
+      look_up(e0 + 32 + lane, &page1, &id1);
+      for (int t = w.t0; t < w.t1 && ok; ++t, ++issued) {
+        const int x = (w.it.first + t) * kPagedTile;  // first key of the tile in the list
+        int e = (x >> c.page_shift) - e0;
+        if (e >= 32) {
+          e0 += 32;
+          e -= 32;
+          page0 = page1;
+          id0 = id1;
+          look_up(e0 + 32 + lane, &page1, &id1);
+        }
+        const int slot = issued % C::STAGES;
+        if (issued >= C::STAGES)
+          ok = mbar_wait(smem_u32(&empty[slot]), ((issued / C::STAGES) - 1) & 1, tmo, &abort_flag, p.wc.status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        // lane i looks at piece i of the tile
+        const int my = e + ((lane * piece) >> c.page_shift);  // below 32: pages of 16 start tiles at multiples of 4
+        const int pg = __shfl_sync(0xffffffffu, page0, my & 31), id = __shfl_sync(0xffffffffu, id0, my & 31);
+        const int off = (x + lane * piece) & ((1 << c.page_shift) - 1);
+        const bool load = lane < pieces && id >= 0;
+        if (lane < C::KW) {
+          const int pl = (lane * 16) / piece;  // piece that holds this warp's keys
+          const int kpage = __shfl_sync(0xfu, pg, pl), kid = __shfl_sync(0xfu, id, pl), koff = __shfl_sync(0xfu, off, pl);
+          key_pos[slot][lane] = kid >= 0 ? (kpage << c.page_shift) + koff + lane * 16 - pl * piece : kNoPosition;
+        }
+        const unsigned loads = __ballot_sync(0xffffffffu, load);
+        const uint32_t bar = smem_u32(&full[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
+        __syncwarp();
+        if (load) {
+          const uint32_t dst = sbase + C::OFF_KV + slot * 2 * C::TILE + lane * box;
+          const int z = id * c.Hkv + g;
+#pragma unroll
+          for (int r = 0; r < C::KREG; ++r) {
+            tma_load_3d(dst + r * C::REGION, &map_k, bar, r * 64, off, z);
+            tma_load_3d(dst + C::TILE + r * C::REGION, &map_v, bar, r * 64, off, z);
+          }
+        }
+        __syncwarp();
+      }
+      ok = ok && w.next(p);
+    }
+    // after a wait gave up: let the loads still in flight land before the CTA exits
+    if (lane == 0 && abort_flag) drain_ring(smem_u32(&full[0]), C::STAGES, issued, p.wc.drain_cycles, p.wc.status);
+    return;
+  }
+
+  // ------------------------------------------------------------ consumer warps
+  const int kw = warp % C::KW, rw = warp / C::KW;
+  const int tid = threadIdx.x;
+  float* om = reinterpret_cast<float*>(smem + C::OFF_O);
+  float2* mls = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [KW][ROWS]
+  auto sync_rows = [&] { named_bar_sync(1, 32 * C::WARPS); };
+
+  // units without tiles: nothing is visible to any of their rows
+  {
+    const int mult = item_mult(p);
+    const int64_t units = static_cast<int64_t>(item_count(p)) * mult;
+    for (int64_t u = part; u < units; u += parts) {
+      const int item = static_cast<int>(u / mult), sub = static_cast<int>(u - static_cast<int64_t>(item) * mult);
+      const Item it = load_item(p, item);
+      if (it.tiles > 0) continue;
+      const int g = p.sel ? item % c.Hkv : sub / p.row_blocks, rb = sub % p.row_blocks;
+      const int64_t row0 = block_row0(p, it.b, g, rb, C::ROWS);
+      const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
+      for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS)
+        reinterpret_cast<uint4*>(p.o + row0 * D)[i] = make_uint4(0, 0, 0, 0);
+      for (int i = tid; i < rows; i += 32 * C::WARPS) p.lse[row0 + i] = -INFINITY;
+    }
+  }
+  if (tid == 0) p.joins[part] = make_int4(-1, 0, 0, 0);
+
+  int consumed = 0;
+  bool ok = true;
+  for (bool more = w.start(p, share); more; more = w.next(p)) {
+    const int g = w.kv_head(p), rb = w.row_block(p);
+    const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
+    const int64_t row0 = block_row0(p, w.it.b, g, rb, C::ROWS);
+    const int len = w.it.len, n = w.it.n;
+    const int p_lo = len - n, p_hi = len - 1;  // positions of the new tokens
+    // the block's query rows to shared memory, rows behind the last one zero
+    for (int i = tid; i < C::ROWS * (D / 8); i += 32 * C::WARPS) {
+      const int r = i / (D / 8), ch = i - r * (D / 8);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D) + ch);
+      *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(r, ch & 7)) = x;
+    }
+    sync_rows();
+    // this thread's two rows and their tokens
+    const int r0 = rw * 16 + (lane >> 2);
+    const int tok0 = (rb * C::ROWS + r0) % p.Tq, tok1 = (rb * C::ROWS + r0 + 8) % p.Tq;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+
+    for (int t = w.t0; t < w.t1; ++t, ++consumed) {
+      const int slot = consumed % C::STAGES;
+      ok = ok && mbar_wait(smem_u32(&full[slot]), (consumed / C::STAGES) & 1, tmo, &abort_flag, p.wc.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) continue;
+      const int j0 = key_pos[slot][kw];
+      const uint32_t ks = sbase + C::OFF_KV + slot * 2 * C::TILE, vs = ks + C::TILE;
+      // does any row see any of the 16 keys; do all rows see all of them
+      const bool some = j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window);
+      if (some) {
+        const bool all = j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) && !(p.window > 0 && j0 <= p_hi - p.window);
+        // S = q K^T: B fragments of keys 0-7 and 8-15
+        float s[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        const int qr = rw * 16 + (lane & 15), kr = kw * 16 + ((lane >> 4) << 3) + (lane & 7);
+        const int qc = lane >> 4, kc = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t a[4], b[4];
+          ldsm4(a, sbase + C::OFF_Q + (k >> 2) * C::QREGION + sw128_offset(qr, (2 * k + qc) & 7));
+          ldsm4(b, ks + (k >> 2) * C::REGION + sw128_offset(kr, (2 * k + kc) & 7));
+          mma16816<C::BF16>(s[0], a, b[0], b[1]);
+          mma16816<C::BF16>(s[1], a, b[2], b[3]);
+        }
+        // element e of tile i: row r0 + 8 (e / 2), key j0 + 8 i + 2 (lane % 4) + e % 2
+        uint32_t keep0 = ~0u, keep1 = ~0u;  // keys of this thread's V fragments that some row sees
+        const int jt = j0 + 2 * (lane & 3);
+        if (all) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[i][e] *= p.scale_log2;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = jt + 8 * i + (e & 1), pos = p_lo + (e < 2 ? tok0 : tok1);
+              const bool see = j < len && !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
+              s[i][e] = see ? s[i][e] * p.scale_log2 : -INFINITY;
+            }
+          auto seen = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window); };
+          keep0 = (seen(jt) ? 0xffffu : 0u) | (seen(jt + 1) ? 0xffff0000u : 0u);
+          keep1 = (seen(jt + 8) ? 0xffffu : 0u) | (seen(jt + 9) ? 0xffff0000u : 0u);
+        }
+        // running maximum and sum of this warp's keys
+        uint32_t pa[4];
+        {
+          float mn[2], alpha[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            mn[h] = fmaxf(m[h], x);
+            alpha[h] = exp2_rel(m[h], mn[h]);
+          }
+          if (__any_sync(0xffffffffu, mn[0] != m[0] || mn[1] != m[1])) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              acc[i][0] *= alpha[0];
+              acc[i][1] *= alpha[0];
+              acc[i][2] *= alpha[1];
+              acc[i][3] *= alpha[1];
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            m[h] = mn[h];
+            const float ref = mn[h] == -INFINITY ? 0.f : mn[h];
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                s[i][2 * h + e] = ex2(s[i][2 * h + e] - ref);
+                sum += s[i][2 * h + e];
+              }
+            l[h] = l[h] * alpha[h] + sum;
+          }
+          // weights rounded to the cache's type for the product with V (the
+          // sum above keeps them in fp32)
+          pa[0] = pack2<C::BF16>(s[0][0], s[0][1]);
+          pa[1] = pack2<C::BF16>(s[0][2], s[0][3]);
+          pa[2] = pack2<C::BF16>(s[1][0], s[1][1]);
+          pa[3] = pack2<C::BF16>(s[1][2], s[1][3]);
+        }
+        // O += P V. A key hidden from every row gets V = 0 (its slot may hold
+        // anything; 0 * NaN would not be 0). Where rows differ in what they
+        // see, each token's product is taken with the keys it sees and only
+        // its rows are kept.
+        const int vr = kw * 16 + (lane & 15), vc = lane >> 4;
+        const bool differ = !all && n > 1 &&
+                            ((p.causal && j0 + 15 > p_lo && j0 <= p_hi) ||
+                             (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
+        if (!differ) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t b[4];
+            ldsm4_trans(b, vs + (i >> 2) * C::REGION + sw128_offset(vr, (2 * i + vc) & 7));
+            mma16816<C::BF16>(acc[2 * i], pa, b[0] & keep0, b[1] & keep1);
+            mma16816<C::BF16>(acc[2 * i + 1], pa, b[2] & keep0, b[3] & keep1);
+          }
+        } else {
+          for (int tok = 0; tok < n; ++tok) {
+            const int pos = p_lo + tok;
+            auto seen = [&](int j) {
+              return j < len && !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
+            };
+            const uint32_t k0 = (seen(jt) ? 0xffffu : 0u) | (seen(jt + 1) ? 0xffff0000u : 0u);
+            const uint32_t k1 = (seen(jt + 8) ? 0xffffu : 0u) | (seen(jt + 9) ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t b[4];
+              ldsm4_trans(b, vs + (i >> 2) * C::REGION + sw128_offset(vr, (2 * i + vc) & 7));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float x[4] = {acc[2 * i + h][0], acc[2 * i + h][1], acc[2 * i + h][2], acc[2 * i + h][3]};
+                mma16816<C::BF16>(x, pa, b[2 * h] & k0, b[2 * h + 1] & k1);
+                if (tok0 == tok) acc[2 * i + h][0] = x[0], acc[2 * i + h][1] = x[1];
+                if (tok1 == tok) acc[2 * i + h][2] = x[2], acc[2 * i + h][3] = x[3];
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+    }
+
+    // merge the key warps: common maximum, then each quarter of the columns is
+    // summed by the warps in turn (warp q, q - 1, q - 2, q - 3 for quarter q)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      // padding rows (tokens the sequence does not have) see nothing
+      if ((h ? tok1 : tok0) >= n) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+      }
+      if ((lane & 3) == 0) mls[kw * C::ROWS + r0 + 8 * h] = make_float2(m[h], l[h]);
+    }
+    sync_rows();
+    float f[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mt = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < C::KW; ++k) mt = fmaxf(mt, mls[k * C::ROWS + r0 + 8 * h].x);
+      f[h] = exp2_rel(m[h], mt);
+    }
+#pragma unroll
+    for (int round = 0; round < C::KW; ++round) {
+      const int quarter = (kw + round) % C::KW;
+#pragma unroll
+      for (int qq = 0; qq < C::KW; ++qq) {
+        if (qq != quarter) continue;
+#pragma unroll
+        for (int i = qq * (D / 32); i < (qq + 1) * (D / 32); ++i) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float2* at = reinterpret_cast<float2*>(om + (r0 + 8 * h) * C::OP + 8 * i + 2 * (lane & 3));
+            float2 x = make_float2(acc[i][2 * h] * f[h], acc[i][2 * h + 1] * f[h]);
+            if (m[h] == -INFINITY) x = make_float2(0.f, 0.f);  // nothing seen: not even 0 * inf
+            if (round > 0) {
+              const float2 y = *at;
+              x.x += y.x;
+              x.y += y.y;
+            }
+            *at = x;
+          }
+        }
+      }
+      sync_rows();
+    }
+    // whole unit: O and LSE; else the part
+    const bool begins = w.t0 == 0, ends = w.t1 == w.it.tiles;
+    const int part_slot = 2 * part + (begins ? 1 : 0);
+    for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS) {
+      const int r = i / (D / 8), ch = i - r * (D / 8);
+      float x[8];
+      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch);
+      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch + 4);
+      float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int k = 0; k < C::KW; ++k) mt = fmaxf(mt, mls[k * C::ROWS + r].x);
+#pragma unroll
+      for (int k = 0; k < C::KW; ++k) lt += mls[k * C::ROWS + r].y * exp2_rel(mls[k * C::ROWS + r].x, mt);
+      if (begins && ends) {
+        store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, x, lt == 0.f ? 0.f : 1.f / lt);
+        if (ch == 0) p.lse[row0 + r] = row_lse(mt, lt);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(part_slot) * C::ROWS + r) * D + 8 * ch);
+        dst[0] = *reinterpret_cast<const float4*>(x);
+        dst[1] = *reinterpret_cast<const float4*>(x + 4);
+        if (ch == 0) p.part_ml[part_slot * C::ROWS + r] = make_float2(mt, lt);
+      }
+    }
+    if (tid == 0 && begins && !ends) {
+      // the unit ends at tile `end` of the list: its last part is the CTA whose share holds end - 1
+      const long long end = share.hi - w.t1 + w.it.tiles;
+      long long last = (end * share.parts - 1) / share.total;
+      while (share.total * last / share.parts >= end) --last;
+      while (last < share.parts - 1 && share.total * (last + 1) / share.parts < end) ++last;
+      p.joins[part] = make_int4(static_cast<int>(row0 >> 31), static_cast<int>(row0 & 0x7fffffff),
+                                static_cast<int>(last), rows);
+    }
+    sync_rows();
+  }
+}
+
+// Joins the parts of the units that CTA blockIdx.x of the split kernel began
+// and did not finish: its slot 1 and slot 0 of the CTAs after it. A warp takes
+// every 8th part, a lane 4 columns (D = 256: 8); blockIdx.y strides over rows.
+constexpr int kJoinWarps = 8;
+template <int D, int ROWS, bool BF16>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+fa_paged_join_kernel(const PagedFwdArgs p) {
+  constexpr int NV = (D / 4 + 31) / 32;
+  __shared__ float4 sm_o[kJoinWarps][D / 4];
+  __shared__ float sm_l[kJoinWarps];
+  grid_wait_prior();
+  grid_release_next();
+  const int4 join = p.joins[blockIdx.x];
+  if (join.x < 0) return;
+  const int64_t row0 = (static_cast<int64_t>(join.x) << 31) + join.y;
+  const int first = blockIdx.x, nparts = join.z - first + 1, rows = join.w;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto slot = [&](int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); };
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float m = -INFINITY;
+    for (int i = lane; i < nparts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * ROWS + r].x);
+    m = warp_max(m);
+    float4 acc[NV];
+    float l = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = warp; i < nparts; i += kJoinWarps) {
+      const float2 ml = p.part_ml[slot(i) * ROWS + r];
+      const float f = exp2_rel(ml.x, m);
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(slot(i)) * ROWS + r) * D);
+      l += ml.y * f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (lane + 32 * v < D / 4) {
+          const float4 x = src[lane + 32 * v];
+          acc[v].x = fmaf(x.x, f, acc[v].x);
+          acc[v].y = fmaf(x.y, f, acc[v].y);
+          acc[v].z = fmaf(x.z, f, acc[v].z);
+          acc[v].w = fmaf(x.w, f, acc[v].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (lane + 32 * v < D / 4) sm_o[warp][lane + 32 * v] = acc[v];
+    if (lane == 0) sm_l[warp] = l;
+    __syncthreads();
+    float lt = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) lt += sm_l[k];
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+    for (int d = threadIdx.x; d < D / 4; d += 32 * kJoinWarps) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kJoinWarps; ++k) {
+        const float4 y = sm_o[k][d];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+      uint2 out;
+      out.x = pack2<BF16>(x.x * inv, x.y * inv);
+      out.y = pack2<BF16>(x.z * inv, x.w * inv);
+      *reinterpret_cast<uint2*>(p.o + (row0 + r) * D + 4 * d) = out;
+    }
+    if (threadIdx.x == 0) p.lse[row0 + r] = row_lse(m, lt);
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------- launch
+template <class C>
+cudaError_t run_paged(const PagedFwdLaunch& a) {
+  CUtensorMap mk, mv;
+  const int page = 1 << a.c.page_shift, piece = page < kPagedTile ? page : kPagedTile;
+  if (!encode_tile_map(&mk, a.c.k, C::BF16, C::D, page, a.c.num_pages * a.c.Hkv, piece) ||
+      !encode_tile_map(&mv, a.c.v, C::BF16, C::D, page, a.c.num_pages * a.c.Hkv, piece))
+    return cudaErrorInvalidValue;
+  PagedFwdArgs p;
+  p.c = a.c;
+  p.q = a.q; p.o = a.o; p.lse = a.lse;
+  p.Hq = a.Hq; p.Tq = a.Tq; p.causal = a.causal;
+  p.window = std::min(a.window, 1 << 30);  // positions end below 2^30: a longer window hides nothing either
+  p.scale_log2 = a.scale_log2;
+  p.new_lens = a.new_lens;
+  p.sel = a.sel; p.sel_lens = a.sel_lens; p.n_sel = a.n_sel;
+  p.rows = a.Hq / a.c.Hkv * a.Tq;
+  p.row_blocks = (p.rows + C::ROWS - 1) / C::ROWS;
+  p.part_o = a.ws;
+  p.part_ml = reinterpret_cast<float2*>(a.ws + static_cast<size_t>(2 * kPagedMaxParts) * C::ROWS * C::D);
+  p.joins = reinterpret_cast<int4*>(p.part_ml + 2 * kPagedMaxParts * C::ROWS);
+  p.wc = a.wc;
+  auto kern = fa_paged_fwd_kernel<C>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than the longest possible list has tiles
+  const int64_t keys = (a.sel ? static_cast<int64_t>(a.n_sel) : a.c.max_pages) << a.c.page_shift;
+  const int64_t most = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks * ((keys + kPagedTile - 1) / kPagedTile);
+  int64_t parts = static_cast<int64_t>(device_sm_count()) * C::CTAS;
+  if (parts > kPagedMaxParts) parts = kPagedMaxParts;
+  if (parts > most) parts = most;
+  e = launch_kernel(kern, parts, C::THREADS, C::SMEM_BYTES, a.stream, 1, mk, mv, p);
+  if (e != cudaSuccess) return e;
+  const int rows = p.rows < C::ROWS ? p.rows : C::ROWS;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attrs[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(parts), static_cast<unsigned>((rows + 3) / 4), 1);
+  cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
+  cfg.stream = a.stream;
+  allow_early_launch(&cfg, attrs);
+  return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<C::D, C::ROWS, C::BF16>, p);
+}
+
+template <int D, bool BF16>
+cudaError_t run_paged_rows(const PagedFwdLaunch& a) {
+  switch (paged_block_rows(a.Hq / a.c.Hkv * a.Tq, D)) {
+    case 16: return run_paged<PagedCfg<D, 1, BF16>>(a);
+    case 32: return run_paged<PagedCfg<D, 2, BF16>>(a);
+  }
+  if constexpr (D < 256) return run_paged<PagedCfg<D, 4, BF16>>(a);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fa
+
+#define FA_DEFINE_PAGED_HEAD_DIM(DIM)                                      \
+  namespace fa {                                                           \
+  cudaError_t launch_paged_fwd_d##DIM(const PagedFwdLaunch& a) {           \
+    return a.bf16 ? run_paged_rows<DIM, true>(a) : run_paged_rows<DIM, false>(a); \
+  }                                                                        \
+  }

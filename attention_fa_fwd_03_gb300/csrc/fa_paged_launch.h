@@ -53,7 +53,26 @@ struct SelectLaunch {
 };
 
 cudaError_t launch_kv_append(const AppendLaunch& a);
-cudaError_t launch_paged_fwd(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_d64(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_d96(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_d128(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_d256(const PagedFwdLaunch& a);
+
+// CTAs of the attention kernel that can leave parts of units to be joined.
+constexpr int kPagedMaxParts = 608;
+
+// Query rows of a block: 16 (usual decoding), 32 or 64 where a KV head has more,
+// so that its keys are loaded once for all of them (D = 256: at most 32, what
+// shared memory holds).
+inline int paged_block_rows(int rows, int D) { return rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64; }
+
+// Device workspace of launch_paged_fwd_d* in bytes: per CTA two parts of a
+// block (fp32 rows, maximum and sum) and a record of what is to be joined.
+inline size_t paged_fwd_workspace(int rows, int D) {
+  const size_t bytes = static_cast<size_t>(2 * kPagedMaxParts) * paged_block_rows(rows, D) * (D * 4 + 8) +
+                       kPagedMaxParts * 16;
+  return (bytes + 255) / 256 * 256;
+}
 cudaError_t launch_page_select(const SelectLaunch& a);
 
 }  // namespace fa
