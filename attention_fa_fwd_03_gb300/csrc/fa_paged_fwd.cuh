@@ -36,6 +36,8 @@ namespace fa {
 
 constexpr int kPagedTile = 64;       // keys of a tile
 constexpr int kPagedKeyWarps = 4;    // warps that share a tile's keys, 16 each
+constexpr int kPagedMaxRanks = 8;    // CTAs of a cluster
+constexpr int kPagedClusterTiles = 8;  // tiles per CTA up to which clusters are used
 
 struct PagedFwdArgs {
   PagedView c;
@@ -56,10 +58,11 @@ struct PagedFwdArgs {
   WaitCfg wc;
 };
 
-template <int D_, int RW_, bool BF16_>
+template <int D_, int RW_, bool BF16_, bool CLUSTER_>
 struct PagedCfg {
   static constexpr int D = D_, RW = RW_;
   static constexpr bool BF16 = BF16_;
+  static constexpr bool CLUSTER = CLUSTER_;          // a cluster per unit instead of equal shares
   static constexpr int KW = kPagedKeyWarps;
   static constexpr int ROWS = 16 * RW;               // rows of a block
   static constexpr int WARPS = KW * RW;              // consumer warps; one producer warp beside them
@@ -77,7 +80,8 @@ struct PagedCfg {
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
   static constexpr int OFF_O = OFF_Q + KREG * QREGION;
   static constexpr int OFF_ML = OFF_O + ROWS * OP * 4;
-  static constexpr int SMEM_BYTES = OFF_ML + KW * ROWS * 8 + 1024;
+  static constexpr int OFF_ROW = OFF_ML + KW * ROWS * 8;  // (max, sum) of the CTA's rows
+  static constexpr int SMEM_BYTES = OFF_ROW + ROWS * 8 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -217,6 +221,19 @@ struct Walk {
     t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + left));
     return true;
   }
+  // The slice of rank `rank` of the `ranks` CTAs that share unit `unit`; false
+  // when it is empty (it and sub are set all the same).
+  __device__ __forceinline__ bool start_slice(const PagedFwdArgs& p, int unit, int rank, int ranks) {
+    mult = item_mult(p);
+    items = item_count(p);
+    item = unit / mult;
+    sub = unit - item * mult;
+    it = load_item(p, item);
+    t0 = static_cast<int>(static_cast<long long>(it.tiles) * rank / ranks);
+    t1 = static_cast<int>(static_cast<long long>(it.tiles) * (rank + 1) / ranks);
+    left = t1 - t0;
+    return left > 0;
+  }
   __device__ __forceinline__ bool next(const PagedFwdArgs& p) {
     left -= t1 - t0;
     if (left <= 0) return false;
@@ -256,6 +273,31 @@ __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.f || l != l ? (m + __log2f(l)) * kLn2 : -INFINITY;
 }
 
+// Maximum and sum of row r over the key warps' own.
+template <class C>
+__device__ __forceinline__ float2 warps_max_sum(const float2* mls, int r) {
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int k = 0; k < C::KW; ++k) m = fmaxf(m, mls[k * C::ROWS + r].x);
+#pragma unroll
+  for (int k = 0; k < C::KW; ++k) l += mls[k * C::ROWS + r].y * exp2_rel(mls[k * C::ROWS + r].x, m);
+  return make_float2(m, l);
+}
+
+// Loads from CTA `rank`'s shared memory, at the place `at` has in this CTA's.
+__device__ __forceinline__ float2 ld_peer_f2(const void* at, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_addr(smem_u32(at), rank)));
+  return v;
+}
+__device__ __forceinline__ float4 ld_peer_f4(const void* at, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer_addr(smem_u32(at), rank)));
+  return v;
+}
+
 // A position no query reaches: the key's slot was not loaded.
 constexpr int kNoPosition = 0x7fffff00;
 
@@ -263,7 +305,7 @@ constexpr int kNoPosition = 0x7fffff00;
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                    const PagedFwdArgs p) {
+                    const PagedFwdArgs p, int ranks) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES];
   __shared__ int key_pos[C::STAGES][C::KW];  // position of the first of each warp's 16 keys
@@ -283,9 +325,18 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
     fence_mbar_init();
   }
+  if (threadIdx.x == 32 * C::WARPS) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
   grid_wait_prior();
   grid_release_next();
-  const Share share = find_share<C::THREADS>(p, part, parts);  // barriers inside
+  const int rank = C::CLUSTER ? part % ranks : 0, unit = C::CLUSTER ? part / ranks : 0;
+  Share share;
+  if constexpr (C::CLUSTER)
+    __syncthreads();
+  else
+    share = find_share<C::THREADS>(p, part, parts);  // barriers inside
   Walk w;
 
   if (warp == C::WARPS) {
@@ -294,7 +345,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int pieces = kPagedTile / piece;
     const uint32_t box = static_cast<uint32_t>(piece) * 128u;
     int issued = 0;
-    bool ok = w.start(p, share);
+    bool ok = C::CLUSTER ? w.start_slice(p, unit, rank, ranks) : w.start(p, share);
     while (ok) {
       const int g = w.kv_head(p);
       const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
@@ -367,6 +418,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
     // after a wait gave up: let the loads still in flight land before the CTA exits
     if (lane == 0 && abort_flag) drain_ring(smem_u32(&full[0]), C::STAGES, issued, p.wc.drain_cycles, p.wc.status);
+    if constexpr (C::CLUSTER) {  // the consumers' two cluster barriers
+      __syncwarp();
+      cluster_barrier();
+      cluster_barrier();
+    }
     return;
   }
 
@@ -377,27 +433,31 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   float2* mls = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [KW][ROWS]
   auto sync_rows = [&] { named_bar_sync(1, 32 * C::WARPS); };
 
-  // units without tiles: nothing is visible to any of their rows
-  {
-    const int mult = item_mult(p);
-    const int64_t units = static_cast<int64_t>(item_count(p)) * mult;
-    for (int64_t u = part; u < units; u += parts) {
-      const int item = static_cast<int>(u / mult), sub = static_cast<int>(u - static_cast<int64_t>(item) * mult);
-      const Item it = load_item(p, item);
-      if (it.tiles > 0) continue;
-      const int g = p.sel ? item % c.Hkv : sub / p.row_blocks, rb = sub % p.row_blocks;
-      const int64_t row0 = block_row0(p, it.b, g, rb, C::ROWS);
-      const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
-      for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS)
-        reinterpret_cast<uint4*>(p.o + row0 * D)[i] = make_uint4(0, 0, 0, 0);
-      for (int i = tid; i < rows; i += 32 * C::WARPS) p.lse[row0 + i] = -INFINITY;
+  if constexpr (!C::CLUSTER) {
+    // units without tiles: nothing is visible to any of their rows
+    {
+      const int mult = item_mult(p);
+      const int64_t units = static_cast<int64_t>(item_count(p)) * mult;
+      for (int64_t u = part; u < units; u += parts) {
+        const int item = static_cast<int>(u / mult), sub = static_cast<int>(u - static_cast<int64_t>(item) * mult);
+        const Item it = load_item(p, item);
+        if (it.tiles > 0) continue;
+        const int g = p.sel ? item % c.Hkv : sub / p.row_blocks, rb = sub % p.row_blocks;
+        const int64_t row0 = block_row0(p, it.b, g, rb, C::ROWS);
+        const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
+        for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS)
+          reinterpret_cast<uint4*>(p.o + row0 * D)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < rows; i += 32 * C::WARPS) p.lse[row0 + i] = -INFINITY;
+      }
     }
+    if (tid == 0) p.joins[part] = make_int4(-1, 0, 0, 0);
   }
-  if (tid == 0) p.joins[part] = make_int4(-1, 0, 0, 0);
 
   int consumed = 0;
   bool ok = true;
-  for (bool more = w.start(p, share); more; more = w.next(p)) {
+  // (with clusters: one segment, which may be empty)
+  for (bool more = C::CLUSTER ? w.start_slice(p, unit, rank, ranks) || true : w.start(p, share); more;
+       more = !C::CLUSTER && w.next(p)) {
     const int g = w.kv_head(p), rb = w.row_block(p);
     const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
     const int64_t row0 = block_row0(p, w.it.b, g, rb, C::ROWS);
@@ -596,6 +656,51 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       sync_rows();
     }
+    if constexpr (C::CLUSTER) {
+      // join through distributed shared memory: every CTA takes a share of the
+      // unit's 8-column pieces and adds up its peers' rows
+      float2* row_ml = reinterpret_cast<float2*>(smem + C::OFF_ROW);
+      for (int r = tid; r < rows; r += 32 * C::WARPS) row_ml[r] = warps_max_sum<C>(mls, r);
+      sync_rows();
+      __syncwarp();
+      cluster_barrier();
+      for (int i = rank * 32 * C::WARPS + tid; i < rows * (D / 8); i += ranks * 32 * C::WARPS) {
+        const int r = i / (D / 8), ch = i - r * (D / 8);
+        float2 ml[kPagedMaxRanks];
+        float4 x[kPagedMaxRanks], y[kPagedMaxRanks];
+#pragma unroll
+        for (int k = 0; k < kPagedMaxRanks; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.f);
+          if (k < ranks) {
+            ml[k] = ld_peer_f2(row_ml + r, k);
+            x[k] = ld_peer_f4(om + r * C::OP + 8 * ch, k);
+            y[k] = ld_peer_f4(om + r * C::OP + 8 * ch + 4, k);
+          }
+        }
+        float mt = -INFINITY, lt = 0.f, sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kPagedMaxRanks; ++k) mt = fmaxf(mt, ml[k].x);
+#pragma unroll
+        for (int k = 0; k < kPagedMaxRanks; ++k) {
+          if (k >= ranks) continue;
+          const float f = exp2_rel(ml[k].x, mt);
+          lt += ml[k].y * f;
+          sum[0] = fmaf(x[k].x, f, sum[0]);
+          sum[1] = fmaf(x[k].y, f, sum[1]);
+          sum[2] = fmaf(x[k].z, f, sum[2]);
+          sum[3] = fmaf(x[k].w, f, sum[3]);
+          sum[4] = fmaf(y[k].x, f, sum[4]);
+          sum[5] = fmaf(y[k].y, f, sum[5]);
+          sum[6] = fmaf(y[k].z, f, sum[6]);
+          sum[7] = fmaf(y[k].w, f, sum[7]);
+        }
+        store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, sum, lt == 0.f ? 0.f : 1.f / lt);
+        if (ch == 0) p.lse[row0 + r] = row_lse(mt, lt);
+      }
+      __syncwarp();
+      cluster_barrier();  // no CTA leaves while a peer reads its rows
+      return;
+    }
     // whole unit: O and LSE; else the part
     const bool begins = w.t0 == 0, ends = w.t1 == w.it.tiles;
     const int part_slot = 2 * part + (begins ? 1 : 0);
@@ -604,11 +709,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       float x[8];
       *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch);
       *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch + 4);
-      float mt = -INFINITY, lt = 0.f;
-#pragma unroll
-      for (int k = 0; k < C::KW; ++k) mt = fmaxf(mt, mls[k * C::ROWS + r].x);
-#pragma unroll
-      for (int k = 0; k < C::KW; ++k) lt += mls[k * C::ROWS + r].y * exp2_rel(mls[k * C::ROWS + r].x, mt);
+      const float2 ml = warps_max_sum<C>(mls, r);
+      const float mt = ml.x, lt = ml.y;
       if (begins && ends) {
         store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, x, lt == 0.f ? 0.f : 1.f / lt);
         if (ch == 0) p.lse[row0 + r] = row_lse(mt, lt);
@@ -634,14 +736,16 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 
 // Joins the parts of the units that CTA blockIdx.x of the split kernel began
 // and did not finish: its slot 1 and slot 0 of the CTAs after it. A warp takes
-// every 8th part, a lane 4 columns (D = 256: 8); blockIdx.y strides over rows.
+// every 8th part, four at a time with all their loads in flight, a lane 4
+// columns (D = 256: 8); blockIdx.y strides over rows.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 16;  // grid.y at most
 template <int D, int ROWS, bool BF16>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 fa_paged_join_kernel(const PagedFwdArgs p) {
-  constexpr int NV = (D / 4 + 31) / 32;
+  constexpr int NV = (D / 4 + 31) / 32, UN = 4;
   __shared__ float4 sm_o[kJoinWarps][D / 4];
-  __shared__ float sm_l[kJoinWarps];
+  __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
   grid_wait_prior();
   grid_release_next();
   const int4 join = p.joins[blockIdx.x];
@@ -649,69 +753,109 @@ fa_paged_join_kernel(const PagedFwdArgs p) {
   const int64_t row0 = (static_cast<int64_t>(join.x) << 31) + join.y;
   const int first = blockIdx.x, nparts = join.z - first + 1, rows = join.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto slot = [&](int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); };
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    float m = -INFINITY;
-    for (int i = lane; i < nparts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * ROWS + r].x);
-    m = warp_max(m);
+    float m = -INFINITY, l = 0.f;
     float4 acc[NV];
-    float l = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = warp; i < nparts; i += kJoinWarps) {
-      const float2 ml = p.part_ml[slot(i) * ROWS + r];
-      const float f = exp2_rel(ml.x, m);
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(slot(i)) * ROWS + r) * D);
-      l += ml.y * f;
+    for (int i0 = warp; i0 < nparts; i0 += kJoinWarps * UN) {
+      float2 ml[UN];
+      float4 x[UN][NV];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int i = i0 + u * kJoinWarps;
+        ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) x[u][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i >= nparts) continue;
+        const int slot = i == 0 ? 2 * first + 1 : 2 * (first + i);
+        ml[u] = p.part_ml[slot * ROWS + r];
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(slot) * ROWS + r) * D);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (lane + 32 * v < D / 4) x[u][v] = src[lane + 32 * v];
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < UN; ++u) mn = fmaxf(mn, ml[u].x);
+      const float alpha = exp2_rel(m, mn);
+      m = mn;
+      l *= alpha;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        if (lane + 32 * v < D / 4) {
-          const float4 x = src[lane + 32 * v];
-          acc[v].x = fmaf(x.x, f, acc[v].x);
-          acc[v].y = fmaf(x.y, f, acc[v].y);
-          acc[v].z = fmaf(x.z, f, acc[v].z);
-          acc[v].w = fmaf(x.w, f, acc[v].w);
+        acc[v].x *= alpha;
+        acc[v].y *= alpha;
+        acc[v].z *= alpha;
+        acc[v].w *= alpha;
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const float f = exp2_rel(ml[u].x, mn);
+        l += ml[u].y * f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          acc[v].x = fmaf(x[u][v].x, f, acc[v].x);
+          acc[v].y = fmaf(x[u][v].y, f, acc[v].y);
+          acc[v].z = fmaf(x[u][v].z, f, acc[v].z);
+          acc[v].w = fmaf(x[u][v].w, f, acc[v].w);
         }
       }
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (lane + 32 * v < D / 4) sm_o[warp][lane + 32 * v] = acc[v];
-    if (lane == 0) sm_l[warp] = l;
+    if (lane == 0) {
+      sm_m[warp] = m;
+      sm_l[warp] = l;
+    }
     __syncthreads();
-    float lt = 0.f;
+    float mt = -INFINITY, lt = 0.f;
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) lt += sm_l[k];
+    for (int k = 0; k < kJoinWarps; ++k) mt = fmaxf(mt, sm_m[k]);
+    float f[kJoinWarps];
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) {
+      f[k] = exp2_rel(sm_m[k], mt);
+      lt += sm_l[k] * f[k];
+    }
     const float inv = lt == 0.f ? 0.f : 1.f / lt;
     for (int d = threadIdx.x; d < D / 4; d += 32 * kJoinWarps) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kJoinWarps; ++k) {
         const float4 y = sm_o[k][d];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
+        x.x = fmaf(y.x, f[k], x.x);
+        x.y = fmaf(y.y, f[k], x.y);
+        x.z = fmaf(y.z, f[k], x.z);
+        x.w = fmaf(y.w, f[k], x.w);
       }
       uint2 out;
       out.x = pack2<BF16>(x.x * inv, x.y * inv);
       out.y = pack2<BF16>(x.z * inv, x.w * inv);
       *reinterpret_cast<uint2*>(p.o + (row0 + r) * D + 4 * d) = out;
     }
-    if (threadIdx.x == 0) p.lse[row0 + r] = row_lse(m, lt);
+    if (threadIdx.x == 0) p.lse[row0 + r] = row_lse(mt, lt);
     __syncthreads();
   }
 }
 
 // ------------------------------------------------------------------- launch
 template <class C>
-cudaError_t run_paged(const PagedFwdLaunch& a) {
+cudaError_t launch_paged(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t grid, int ranks) {
   CUtensorMap mk, mv;
   const int page = 1 << a.c.page_shift, piece = page < kPagedTile ? page : kPagedTile;
   if (!encode_tile_map(&mk, a.c.k, C::BF16, C::D, page, a.c.num_pages * a.c.Hkv, piece) ||
       !encode_tile_map(&mv, a.c.v, C::BF16, C::D, page, a.c.num_pages * a.c.Hkv, piece))
     return cudaErrorInvalidValue;
+  auto kern = fa_paged_fwd_kernel<C>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, grid, C::THREADS, C::SMEM_BYTES, a.stream, static_cast<unsigned>(ranks), mk, mv, p, ranks);
+}
+
+template <int D, int RW, bool BF16>
+cudaError_t run_paged(const PagedFwdLaunch& a) {
+  using C = PagedCfg<D, RW, BF16, false>;
   PagedFwdArgs p;
   p.c = a.c;
   p.q = a.q; p.o = a.o; p.lse = a.lse;
@@ -726,21 +870,23 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   p.part_ml = reinterpret_cast<float2*>(a.ws + static_cast<size_t>(2 * kPagedMaxParts) * C::ROWS * C::D);
   p.joins = reinterpret_cast<int4*>(p.part_ml + 2 * kPagedMaxParts * C::ROWS);
   p.wc = a.wc;
-  auto kern = fa_paged_fwd_kernel<C>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-  if (e != cudaSuccess) return e;
-  // no more CTAs than the longest possible list has tiles
+  // tiles of the longest list a unit can have
   const int64_t keys = (a.sel ? static_cast<int64_t>(a.n_sel) : a.c.max_pages) << a.c.page_shift;
-  const int64_t most = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks * ((keys + kPagedTile - 1) / kPagedTile);
-  int64_t parts = static_cast<int64_t>(device_sm_count()) * C::CTAS;
-  if (parts > kPagedMaxParts) parts = kPagedMaxParts;
-  if (parts > most) parts = most;
-  e = launch_kernel(kern, parts, C::THREADS, C::SMEM_BYTES, a.stream, 1, mk, mv, p);
+  const int64_t tiles = (keys + kPagedTile - 1) / kPagedTile;
+  const int64_t units = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks;
+  const int64_t wave = std::min<int64_t>(static_cast<int64_t>(device_sm_count()) * C::CTAS, kPagedMaxParts);
+  // Few short units: a cluster each, joined in the same launch.
+  int ranks = 1;
+  while (ranks < kPagedMaxRanks && ranks < tiles) ranks *= 2;
+  if (tiles <= kPagedClusterTiles * ranks && units * ranks <= wave)
+    return launch_paged<PagedCfg<D, RW, BF16, true>>(a, p, units * ranks, ranks);
+  // no more CTAs than the longest possible list has tiles
+  const int64_t parts = std::min(wave, units * tiles);
+  const cudaError_t e = launch_paged<C>(a, p, parts, 1);
   if (e != cudaSuccess) return e;
-  const int rows = p.rows < C::ROWS ? p.rows : C::ROWS;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(parts), static_cast<unsigned>((rows + 3) / 4), 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(parts), static_cast<unsigned>(std::min(std::min(p.rows, C::ROWS), kJoinRows)), 1);
   cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
   cfg.stream = a.stream;
   allow_early_launch(&cfg, attrs);
@@ -750,10 +896,10 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
 template <int D, bool BF16>
 cudaError_t run_paged_rows(const PagedFwdLaunch& a) {
   switch (paged_block_rows(a.Hq / a.c.Hkv * a.Tq, D)) {
-    case 16: return run_paged<PagedCfg<D, 1, BF16>>(a);
-    case 32: return run_paged<PagedCfg<D, 2, BF16>>(a);
+    case 16: return run_paged<D, 1, BF16>(a);
+    case 32: return run_paged<D, 2, BF16>(a);
   }
-  if constexpr (D < 256) return run_paged<PagedCfg<D, 4, BF16>>(a);
+  if constexpr (D < 256) return run_paged<D, 4, BF16>(a);
   return cudaErrorInvalidValue;
 }
 
