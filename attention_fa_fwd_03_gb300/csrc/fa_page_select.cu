@@ -4,22 +4,28 @@
 //   score(page) = max_h sum_d max(q_hd min_d, q_hd max_d)
 //               = max_h sum_d (q_hd > 0 ? q_hd max_d : q_hd min_d)
 //
-// Two kernels: scores of every page in fp32 (bound by reading 4 D bytes of bounds
-// per page and KV head), then one block per (sequence, KV head) that finds the
-// n_sel best.
+// One launch: a cluster of CTAs per (sequence, KV head) scores its pages in fp32
+// (bound by reading 4 D bytes of bounds per page and KV head) and leaves the
+// scores in the shared memory of its first CTA, which finds the n_sel best.
+//
+// A score is the sum of q+ max_d + q- min_d with q+ = max(q, 0), q- = min(q, 0),
+// both exact in 16 bits: a product of 16 pages' bounds with up to 8 query heads on
+// the tensor cores. Which dimension meets which index of the product is free as
+// long as both operands agree, so a thread's fragment is whole 16-byte chunks
+// loaded straight from global memory.
 //
 // The choice is the one that scores in 64 bits give although nearly all the work
-// is done in 32: beside each score the first kernel leaves A = sum_d max_h |q_hd|
-// max(|min_d|, |max_d|), and its score is off by at most E = 40 * 2^-24 A (at most
-// 24 fused additions in a lane, one more for its two halves, four joining up to
-// 16 lanes; the rest covers the rounding of A). With tau the wanted
-// place's value among the fp32 scores and E the largest such bound, the true
-// place's value is within E of tau: pages above tau + 2 E are chosen, pages under
-// tau - 2 E are not, and only the few in between are computed again in 64 bits
-// and ranked by (score, lower page). Without near ties there are no more of them
-// than places, and nothing is computed again.
+// is done in 32: with A the largest of sum_d max_h |q_hd| max(|min_d|, |max_d|)
+// over the pages, a score is off by at most E = D 2^-23 A (the products are exact,
+// the D additions at least single precision in an order and with a rounding that
+// are left open). With tau the last place's value among the fp32 scores, its true
+// value is within E of tau: pages above tau + 2 E are chosen, pages under tau - 2 E
+// are not, and only the few in between are computed again in 64 bits and ranked by
+// (score, lower page). Where there are no more of them than places, nothing is
+// computed again.
 #include "fa_inst.cuh"
 #include "fa_paged_launch.h"
+#include "fa_paged_mma.cuh"
 
 namespace fa {
 namespace {
@@ -29,9 +35,9 @@ struct SelectArgs {
   const uint16_t* q;
   int Hq, n_sel, keep_first, keep_last;
   int *sel, *sel_lens;
-  float2* scores;                 // [B * Hkv, max_pages] (score, A); a bad page has (-inf, 0)
-  unsigned long long* keys;       // [B * Hkv, max_pages] 64-bit scores where they are needed
-  int group, head_chunk, chunk;   // KV heads of a block, query heads held at a time, pages of a block
+  uint32_t* scores;          // [B * Hkv, max_pages] keys of scores beyond kHeld pages
+  unsigned long long* keys;  // [B * Hkv, max_pages] 64-bit scores where they are needed
+  int head_chunk;            // query heads held at a time
 };
 
 __device__ __forceinline__ int page_count(const PagedView& c, int b) {
@@ -41,148 +47,19 @@ __device__ __forceinline__ int page_count(const PagedView& c, int b) {
 // Larger of two with NaN the largest.
 __device__ __forceinline__ float max_or_nan(float x, float y) { return y > x || y != y ? y : x; }
 
-// ------------------------------------------------------------------- scores
-// A few lanes share a (page, KV head), 16 (D = 96: 24) dimensions each in
-// 16-byte chunks; a thread takes two pages at a time so that a query value read
-// from shared memory is used twice. Query heads are held as fp32 rows, then the
-// row of their largest magnitudes.
-constexpr int kScoreThreads = 256;
-template <int D>
-constexpr int kScoreLanes = D == 96 ? 4 : D / 16;
-template <int D>
-constexpr int kScoreSlots = kScoreThreads / kScoreLanes<D>;
-constexpr int kScorePages = 2;            // pages per thread at a time
-constexpr int kScoreSmem = 48 * 1024;
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectRanks = 8;       // CTAs of a cluster at most
+constexpr int kHeld = 12 * 1024;      // pages whose scores are held in shared memory
+constexpr int kFewTies = 256;         // pages in between that are ranked directly
+constexpr int kQuerySmem = 36 * 1024;
 
-inline int score_pitch(int heads, int D) { return (heads + 1) * D + 4; }  // floats per KV head; + 4: other banks
+constexpr int kScorePages = 16 * kSelectWarps;  // pages of a pass
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kScoreThreads)
-fa_page_score_kernel(const SelectArgs p) {
-  extern __shared__ __align__(16) float qs[];
-  grid_wait_prior();
-  grid_release_next();
-  const PagedView& c = p.c;
-  const int b = blockIdx.x, g0 = blockIdx.z * p.group;
-  const int pages = page_count(c, b);
-  const int end = min(pages - p.keep_last, static_cast<int>(blockIdx.y + 1) * p.chunk);
-  int begin = blockIdx.y * p.chunk;
-  if (pages <= p.n_sel || begin >= end) return;
-  const int groups = min(p.group, c.Hkv - g0);
-  const int reps = p.Hq / c.Hkv;
-  const int pitch = (p.head_chunk + 1) * D + 4;
-  constexpr int L = kScoreLanes<D>, CH = D / 8 / L;  // lanes of a page, chunks of a lane
-  const int slot = threadIdx.x / L, lane = threadIdx.x % L;
-  // the lanes of a slot run together, the slots of a warp need not
-  const unsigned mates = ((1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
-  const int per_pass = kScoreSlots<D> / groups;  // pages side by side
-  const int gi = slot % groups, ps = slot / groups;
-  const int g = g0 + gi;
-  float2* out = p.scores + (static_cast<int64_t>(b) * c.Hkv + g) * c.max_pages;
-  for (int h0 = 0; h0 < reps; h0 += p.head_chunk) {
-    const int heads = min(p.head_chunk, reps - h0);
-    if (h0 > 0) __syncthreads();
-    for (int i = threadIdx.x; i < groups * heads * (D / 8); i += kScoreThreads) {
-      const int ch = i % (D / 8), r = i / (D / 8), hi = r % heads, gg = r / heads;
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(
-                                p.q + (static_cast<int64_t>(b) * p.Hq + (g0 + gg) * reps + h0 + hi) * D) + ch);
-      float4* dst = reinterpret_cast<float4*>(qs + gg * pitch + hi * D + 8 * ch);
-      const float2 a = unpack2<BF16>(x.x), e = unpack2<BF16>(x.y), f = unpack2<BF16>(x.z), k = unpack2<BF16>(x.w);
-      dst[0] = make_float4(a.x, a.y, e.x, e.y);
-      dst[1] = make_float4(f.x, f.y, k.x, k.y);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < groups * D; i += kScoreThreads) {
-      const int gg = i / D, d = i - gg * D;
-      float m = 0.f;
-      for (int r = 0; r < heads; ++r) m = fmaxf(m, fabsf(qs[gg * pitch + r * D + d]));
-      qs[gg * pitch + p.head_chunk * D + d] = m;
-    }
-    __syncthreads();
-    if (ps >= per_pass) continue;
-    const float* qg = qs + gi * pitch;
-    for (int base = begin + ps; base < end; base += per_pass * kScorePages) {
-      const uint4* src[kScorePages];
-      bool there[kScorePages];
-#pragma unroll
-      for (int k = 0; k < kScorePages; ++k) {
-        const int pg = base + k * per_pass;
-        const int id = pg < end ? pool_page(c, b, pg) : -1;
-        there[k] = id >= 0;
-        src[k] = reinterpret_cast<const uint4*>(c.bounds + (static_cast<int64_t>(max(id, 0)) * c.Hkv + g) * 2 * D);
-      }
-      // the bounds' chunks of this lane: lane, lane + L, ...
-      uint4 lo[kScorePages][CH], hi[kScorePages][CH];
-#pragma unroll
-      for (int k = 0; k < kScorePages; ++k)
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          lo[k][i] = there[k] ? __ldg(src[k] + lane + L * i) : make_uint4(0, 0, 0, 0);
-          hi[k][i] = there[k] ? __ldg(src[k] + D / 8 + lane + L * i) : make_uint4(0, 0, 0, 0);
-        }
-      float best[kScorePages], most[kScorePages];
-#pragma unroll
-      for (int k = 0; k < kScorePages; ++k) {
-        best[k] = -INFINITY;
-        most[k] = 0.f;
-      }
-      for (int r = 0; r <= heads; ++r) {
-        const bool mags = r == heads;
-        const float4* qr = reinterpret_cast<const float4*>(qg + (mags ? p.head_chunk : r) * D);
-        uint64_t s2[kScorePages];
-#pragma unroll
-        for (int k = 0; k < kScorePages; ++k) s2[k] = f2_pack(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const float4 qa = qr[2 * (lane + L * i)], qb = qr[2 * (lane + L * i) + 1];
-          const float qv[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = qv[2 * e], y = qv[2 * e + 1];
-            const uint64_t up = f2_pack(fmaxf(x, 0.f), fmaxf(y, 0.f)), down = f2_pack(fminf(x, 0.f), fminf(y, 0.f));
-#pragma unroll
-            for (int k = 0; k < kScorePages; ++k) {
-              const float2 l = unpack2<BF16>(reinterpret_cast<const uint32_t*>(&lo[k][i])[e]);
-              const float2 h = unpack2<BF16>(reinterpret_cast<const uint32_t*>(&hi[k][i])[e]);
-              if (mags) {
-                s2[k] = ffma2(f2_pack(x, y), f2_pack(fmaxf(fabsf(l.x), fabsf(h.x)), fmaxf(fabsf(l.y), fabsf(h.y))), s2[k]);
-              } else {
-                s2[k] = ffma2(up, f2_pack(h.x, h.y), s2[k]);
-                s2[k] = ffma2(down, f2_pack(l.x, l.y), s2[k]);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kScorePages; ++k) {
-          const float2 v = f2_unpack(s2[k]);
-          float s = v.x + v.y;
-#pragma unroll
-          for (int off = 1; off < L; off <<= 1) s += __shfl_xor_sync(mates, s, off);
-          if (mags)
-            most[k] = s;
-          else
-            best[k] = max_or_nan(best[k], s);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kScorePages; ++k) {
-        const int pg = base + k * per_pass;
-        if (lane != 0 || pg >= end) continue;
-        float2 r = there[k] ? make_float2(best[k], most[k]) : make_float2(-INFINITY, 0.f);
-        if (h0 > 0) {
-          const float2 before = out[pg];
-          r = make_float2(max_or_nan(before.x, r.x), max_or_nan(before.y, r.y));
-        }
-        out[pg] = r;
-      }
-    }
-  }
-}
-
-// ------------------------------------------------------------------- choice
-constexpr int kPickThreads = 512;
-constexpr int kPickSmem = 12 * 1024;  // pages whose scores are held in shared memory
+// Query heads in shared memory: rows of q+, rows of q-, then the row of largest
+// magnitudes, 16-bit, padded by 16 bytes so that 8 rows' chunks have other banks.
+__host__ __device__ constexpr int query_pitch(int D) { return 2 * D + 16; }
+inline int query_bytes(int heads, int D) { return (2 * heads + 1) * query_pitch(D); }
 
 // Order-preserving maps (NaN highest, -0 as +0).
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -199,6 +76,141 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   return i >> 63 ? ~i : i | (1ull << 63);
 }
 
+// What a CTA found beside the scores.
+struct ScoreStats {
+  float a;            // largest A
+  int odd;            // a score or bound that is no number
+  uint32_t lo, hi;    // smallest and largest key
+};
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t abs_max2(uint32_t x, uint32_t y) {
+  using T2 = std::conditional_t<BF16, __nv_bfloat162, __half2>;
+  const T2 r = __hmax2(__habs2(*reinterpret_cast<T2*>(&x)), __habs2(*reinterpret_cast<T2*>(&y)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Scores of pages keep_first + [begin, end) of (b, g): put(i, key) for each, by
+// one lane; get(i) gives back what was put (heads beyond head_chunk).
+template <int D, bool BF16, class Put, class Get>
+__device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* qs, int b, int g, int begin, int end,
+                                                  const Put& put, const Get& get) {
+  constexpr int CH = D / 32, BATCH = CH < 4 ? CH : 4;  // a thread's chunks of a row, and how many at a time
+  constexpr int PITCH = query_pitch(D);
+  const PagedView& c = p.c;
+  const int reps = p.Hq / c.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = lane >> 2, col = lane & 3;
+  uint8_t* qmag = qs + 2 * p.head_chunk * PITCH;
+  ScoreStats st = {0.f, 0, ~0u, 0u};
+  for (int h0 = 0; h0 < reps; h0 += p.head_chunk) {
+    const int heads = min(p.head_chunk, reps - h0), tiles = (heads + 7) / 8;
+    const bool last = h0 + heads == reps;
+    if (h0 > 0) __syncthreads();
+    // behind the last head it again, which changes no maximum
+    for (int i = threadIdx.x; i < tiles * 8 * (D / 2); i += kSelectThreads) {
+      const int r = i / (D / 2), d2 = i - r * (D / 2);
+      const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(
+                                   p.q + (static_cast<int64_t>(b) * p.Hq + g * reps + h0 + min(r, heads - 1)) * D) + d2);
+      const float2 f = unpack2<BF16>(x);
+      *reinterpret_cast<uint32_t*>(qs + r * PITCH + 4 * d2) = pack2<BF16>(f.x < 0.f ? 0.f : f.x, f.y < 0.f ? 0.f : f.y);
+      *reinterpret_cast<uint32_t*>(qs + (p.head_chunk + r) * PITCH + 4 * d2) =
+          pack2<BF16>(f.x > 0.f ? 0.f : f.x, f.y > 0.f ? 0.f : f.y);
+    }
+    __syncthreads();
+    for (int d2 = threadIdx.x; d2 < D / 2; d2 += kSelectThreads) {
+      uint32_t m = 0;
+      for (int r = 0; r < heads; ++r) {
+        m = abs_max2<BF16>(m, *reinterpret_cast<const uint32_t*>(qs + r * PITCH + 4 * d2));
+        m = abs_max2<BF16>(m, *reinterpret_cast<const uint32_t*>(qs + (p.head_chunk + r) * PITCH + 4 * d2));
+      }
+      *reinterpret_cast<uint32_t*>(qmag + 4 * d2) = m;
+    }
+    __syncthreads();
+    for (int base = begin + 16 * warp; base < end; base += kScorePages) {
+      // this thread's rows: pages base + row and base + row + 8
+      const uint4* src[2];
+      bool there[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = base + row + 8 * k;
+        const int id = i < end ? pool_page(c, b, p.keep_first + i) : -1;
+        there[k] = id >= 0;
+        src[k] = reinterpret_cast<const uint4*>(c.bounds + (static_cast<int64_t>(max(id, 0)) * c.Hkv + g) * 2 * D) + col;
+      }
+      float best[2] = {-INFINITY, -INFINITY}, most[2] = {0.f, 0.f};
+      for (int t = 0; t < tiles; ++t) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i0 = 0; i0 < CH; i0 += BATCH) {
+          uint4 lo[2][BATCH], hi[2][BATCH];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+              lo[k][i] = there[k] ? __ldg(src[k] + 4 * (i0 + i)) : make_uint4(0, 0, 0, 0);
+              hi[k][i] = there[k] ? __ldg(src[k] + D / 8 + 4 * (i0 + i)) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int at = 16 * (col + 4 * (i0 + i));
+            const uint4 up = *reinterpret_cast<const uint4*>(qs + (8 * t + row) * PITCH + at);
+            const uint4 down = *reinterpret_cast<const uint4*>(qs + (p.head_chunk + 8 * t + row) * PITCH + at);
+            const uint32_t h0f[4] = {hi[0][i].x, hi[1][i].x, hi[0][i].y, hi[1][i].y};
+            const uint32_t h1f[4] = {hi[0][i].z, hi[1][i].z, hi[0][i].w, hi[1][i].w};
+            const uint32_t l0f[4] = {lo[0][i].x, lo[1][i].x, lo[0][i].y, lo[1][i].y};
+            const uint32_t l1f[4] = {lo[0][i].z, lo[1][i].z, lo[0][i].w, lo[1][i].w};
+            mma16816<BF16>(s, h0f, up.x, up.y);
+            mma16816<BF16>(s, h1f, up.z, up.w);
+            mma16816<BF16>(s, l0f, down.x, down.y);
+            mma16816<BF16>(s, l1f, down.z, down.w);
+            if (t == 0) {
+              const uint4 mag = *reinterpret_cast<const uint4*>(qmag + at);
+              uint32_t m0[4], m1[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                m0[e] = abs_max2<BF16>(h0f[e], l0f[e]);
+                m1[e] = abs_max2<BF16>(h1f[e], l1f[e]);
+              }
+              mma16816<BF16>(a, m0, mag.x, mag.y);
+              mma16816<BF16>(a, m1, mag.z, mag.w);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          best[k] = max_or_nan(best[k], max_or_nan(s[2 * k], s[2 * k + 1]));
+          if (t == 0) most[k] = a[2 * k];  // every column has it
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        best[k] = max_or_nan(best[k], __shfl_xor_sync(0xffffffffu, best[k], 1));
+        best[k] = max_or_nan(best[k], __shfl_xor_sync(0xffffffffu, best[k], 2));
+        const int i = base + row + 8 * k;
+        if (col != 0 || i >= end) continue;
+        float x = best[k];
+        if (there[k]) {
+          st.odd |= x != x || isinf(x) || !(most[k] < INFINITY);
+          st.a = fmaxf(st.a, most[k]);
+        } else {
+          x = -INFINITY;  // a bad page
+        }
+        uint32_t key = order_key(x);
+        if (h0 > 0) key = max(key, get(i));
+        put(i, key);
+        if (last) {
+          st.lo = min(st.lo, key);
+          st.hi = max(st.hi, key);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  return st;
+}
+
+// ------------------------------------------------------------------- choice
 // Sums over the block of three counts of every thread.
 struct BlockCounts {
   int (*c)[3];  // three sets in shared memory, all zero at first
@@ -224,16 +236,20 @@ struct BlockCounts {
   }
 };
 
-// The need-th largest of the keys that get(i, &key) gives for i in [0, n):
-// largest T with at least `need` keys >= T, two bits at a time.
+// The need-th largest of the keys that get(i, &key) gives for i in [0, n), all of
+// them in [lo, hi]: the largest T with at least `need` keys >= T, two bits at a
+// time from the first bit in which lo and hi differ.
 template <class K, class Get>
-__device__ __forceinline__ K kth_largest(BlockCounts& counts, int n, int need, const Get& get) {
-  K t = 0;
+__device__ __forceinline__ K kth_largest(BlockCounts& counts, int n, int need, K lo, K hi, const Get& get) {
+  if (lo == hi) return lo;
+  int bit = 63 - __clzll(static_cast<long long>(lo ^ hi));
+  bit -= bit & 1;
+  K t = hi >> bit >> 2 << bit << 2;  // shifts of 2 apart: bit + 2 may be the type's width
 #pragma unroll 1
-  for (int bit = static_cast<int>(sizeof(K)) * 8 - 2; bit >= 0; bit -= 2) {
+  for (; bit >= 0; bit -= 2) {
     const K t1 = t | (static_cast<K>(1) << bit), t2 = t | (static_cast<K>(2) << bit), t3 = t | (static_cast<K>(3) << bit);
     int a = 0, b = 0, e = 0;
-    for (int i = threadIdx.x; i < n; i += kPickThreads) {
+    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
       K k;
       if (!get(i, &k)) continue;
       a += k >= t1;
@@ -264,59 +280,139 @@ __device__ __forceinline__ int block_before(int x, int* warp_sums) {
   return before;
 }
 
+// Store to the first CTA of the cluster, at the place `at` has in this one's
+// shared memory.
+__device__ __forceinline__ void st_first(const uint32_t* at, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(smem_u32(at), 0)), "r"(v) : "memory");
+}
+
+// The 64-bit key of page i of the competing ones, by a whole warp.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kPickThreads)
-fa_page_pick_kernel(const SelectArgs p) {
-  __shared__ uint32_t held[kPickSmem];
-  __shared__ int counters[3][3], warp_sums[kPickThreads / 32];
-  __shared__ float warp_max_a[kPickThreads / 32];
+__device__ __forceinline__ unsigned long long exact_key(const SelectArgs& p, int b, int g, int page) {
+  const PagedView& c = p.c;
+  const int lane = threadIdx.x & 31, reps = p.Hq / c.Hkv;
+  const int id = pool_page(c, b, page);
+  if (id < 0) return 0;
+  const uint16_t* lo = c.bounds + (static_cast<int64_t>(id) * c.Hkv + g) * 2 * D;
+  double x[D / 32][2];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    x[i][0] = unpack2<BF16>(lo[lane + 32 * i]).x;
+    x[i][1] = unpack2<BF16>(lo[D + lane + 32 * i]).x;
+  }
+  double best = 0.0;
+  for (int r = 0; r < reps; ++r) {
+    const uint16_t* q = p.q + (static_cast<int64_t>(b) * p.Hq + g * reps + r) * D;
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const double y = unpack2<BF16>(q[lane + 32 * i]).x;
+      const double u = y * x[i][0], v = y * x[i][1];
+      s += u > v || u != u ? u : v;
+    }
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (r == 0 || s > best || s != s) best = s;
+    if (best != best) break;
+  }
+  return order_key(best);
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kSelectThreads)
+fa_page_select_kernel(const SelectArgs p, int ranks) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ int counters[3][3], warp_sums[kSelectWarps];
+  __shared__ uint32_t warp_stats[kSelectWarps][4], rank_stats[kSelectRanks][4];
+  __shared__ unsigned long long tie_key[kFewTies];
+  __shared__ int tie_page[kFewTies], ties_found;
+  uint8_t* qs = dyn;
+  uint32_t* held = reinterpret_cast<uint32_t*>(dyn + (2 * p.head_chunk + 1) * query_pitch(D));
   if (threadIdx.x < 9) counters[threadIdx.x / 3][threadIdx.x % 3] = 0;
+  if (threadIdx.x == 9) ties_found = 0;
+  cluster_arrive_relaxed();  // waited for before the first store into the first CTA
   grid_wait_prior();
   grid_release_next();
   const PagedView& c = p.c;
-  const int unit = blockIdx.x, b = unit / c.Hkv, g = unit - b * c.Hkv;
+  const int unit = blockIdx.x / ranks, rank = blockIdx.x - unit * ranks;
+  const int b = unit / c.Hkv, g = unit - b * c.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pages = page_count(c, b);
+  // pages keep_first + i, i < n, compete for `need` places
+  const int need = p.n_sel - p.keep_first - p.keep_last;
+  const int n = pages - p.keep_first - p.keep_last;
+  const bool all = pages <= p.n_sel;  // the same in every CTA of the cluster
+  const bool in_smem = n <= kHeld;
+  uint32_t* far = p.scores + static_cast<int64_t>(unit) * c.max_pages;
+  cluster_wait();
+  if (!all && need > 0) {
+    const int begin = static_cast<int>(static_cast<long long>(n) * rank / ranks);
+    const int end = static_cast<int>(static_cast<long long>(n) * (rank + 1) / ranks);
+    ScoreStats st;
+    if (ranks == 1 && in_smem)
+      st = score_pages<D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { held[i] = k; },
+                                [&](int i) { return held[i]; });
+    else if (in_smem && p.Hq / c.Hkv <= p.head_chunk)
+      st = score_pages<D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { st_first(held + i, k); },
+                                [&](int) { return 0u; });
+    else
+      st = score_pages<D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { far[i] = k; },
+                                [&](int i) { return far[i]; });
+    st.a = warp_max(st.a);
+    st.odd = __any_sync(0xffffffffu, st.odd);
+    st.lo = __reduce_min_sync(0xffffffffu, st.lo);
+    st.hi = __reduce_max_sync(0xffffffffu, st.hi);
+    if (lane == 0) {
+      warp_stats[warp][0] = __float_as_uint(st.a);
+      warp_stats[warp][1] = static_cast<uint32_t>(st.odd);
+      warp_stats[warp][2] = st.lo;
+      warp_stats[warp][3] = st.hi;
+    }
+    __syncthreads();
+    if (threadIdx.x < 4) {
+      uint32_t x = warp_stats[0][threadIdx.x];
+      for (int w = 1; w < kSelectWarps; ++w) {
+        const uint32_t y = warp_stats[w][threadIdx.x];
+        x = threadIdx.x == 2 ? min(x, y) : max(x, y);  // A is not negative: its bits order like it
+      }
+      st_first(&rank_stats[rank][threadIdx.x], x);
+    }
+    __syncwarp();
+    cluster_barrier();  // every CTA's scores are with the first
+  }
+  if (rank != 0) return;
+
   int* sel = p.sel + static_cast<int64_t>(unit) * p.n_sel;
   if (threadIdx.x == 0) p.sel_lens[unit] = min(pages, p.n_sel);
-  if (pages <= p.n_sel) {
-    for (int i = threadIdx.x; i < p.n_sel; i += kPickThreads) sel[i] = i < pages ? i : -1;
+  if (all) {
+    for (int i = threadIdx.x; i < p.n_sel; i += kSelectThreads) sel[i] = i < pages ? i : -1;
     return;
   }
-  for (int i = threadIdx.x; i < p.keep_first; i += kPickThreads) sel[i] = i;
-  for (int i = threadIdx.x; i < p.keep_last; i += kPickThreads) sel[p.n_sel - p.keep_last + i] = pages - p.keep_last + i;
-  const int need = p.n_sel - p.keep_first - p.keep_last;
+  for (int i = threadIdx.x; i < p.keep_first; i += kSelectThreads) sel[i] = i;
+  for (int i = threadIdx.x; i < p.keep_last; i += kSelectThreads) sel[p.n_sel - p.keep_last + i] = pages - p.keep_last + i;
   if (need == 0) return;
-  // pages keep_first + i, i < n, compete for `need` places
-  const int n = pages - p.keep_first - p.keep_last;
-  const float2* scores = p.scores + static_cast<int64_t>(unit) * c.max_pages + p.keep_first;
-  unsigned long long* keys = p.keys + static_cast<int64_t>(unit) * c.max_pages + p.keep_first;
-
+  const bool local = in_smem && (ranks == 1 || p.Hq / c.Hkv <= p.head_chunk);
+  auto key32 = [&](int i) { return local ? held[i] : far[i]; };
   float a_max = 0.f;
-  bool odd = false;  // a score or bound that is no number
-  for (int i = threadIdx.x; i < n; i += kPickThreads) {
-    const float2 s = scores[i];
-    odd |= s.x != s.x || !(s.y < INFINITY) || (isinf(s.x) && s.y != 0.f);
-    a_max = fmaxf(a_max, s.y);
-    if (i < kPickSmem) held[i] = order_key(s.x);
+  uint32_t odd = 0, key_lo = ~0u, key_hi = 0u;
+  for (int r = 0; r < ranks; ++r) {
+    a_max = fmaxf(a_max, __uint_as_float(rank_stats[r][0]));
+    odd |= rank_stats[r][1];
+    key_lo = min(key_lo, rank_stats[r][2]);
+    key_hi = max(key_hi, rank_stats[r][3]);
   }
-  a_max = warp_max(a_max);
-  if (lane == 0) warp_max_a[warp] = a_max;
-  odd = __syncthreads_or(odd);
-  for (int w = 0; w < kPickThreads / 32; ++w) a_max = fmaxf(a_max, warp_max_a[w]);
-  auto key32 = [&](int i) { return i < kPickSmem ? held[i] : order_key(scores[i].x); };
 
   BlockCounts counts{counters, 0};
   uint32_t low = 0, high = ~0u;  // keys above `high` are in, under `low` out
   int sum[3];
   int sure = 0, between = n;
   if (!odd) {
-    const uint32_t tau = kth_largest<uint32_t>(counts, n, need, [&](int i, uint32_t* k) {
+    const uint32_t tau = kth_largest<uint32_t>(counts, n, need, key_lo, key_hi, [&](int i, uint32_t* k) {
       *k = key32(i);
       return true;
     });
     const float t = order_value(tau);
-    const float err = 2.02f * 40.f * 5.9604645e-8f * a_max + fabsf(t) * 2.4e-7f;
+    // 2 E, with room for the error of A and the roundings of t -+ err
+    const float err = 2.02f * D * 1.1920929e-7f * a_max + fabsf(t) * 2.4e-7f;
     if (t > -INFINITY) {
       low = order_key(t - err);
       high = order_key(t + err);
@@ -324,45 +420,46 @@ fa_page_pick_kernel(const SelectArgs p) {
       low = high = tau;
     }
     int in = 0, mid = 0;
-    for (int i = threadIdx.x; i < n; i += kPickThreads) {
+    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
       const uint32_t k = key32(i);
       in += k > high;
-      mid += k >= low && k <= high;
+      if (k >= low && k <= high) {
+        ++mid;
+        const int at = atomicAdd(&ties_found, 1);
+        if (at < kFewTies) tie_page[at] = i;
+      }
     }
     counts.add(in, mid, 0, sum);
     sure = sum[0];
     between = sum[1];
-  } else {
-    high = ~0u;  // every page is computed again; no key is above ~0
   }
-  const int places = need - sure;  // for the pages in between
-  unsigned long long cut = 0;      // their keys above `cut` are in, and the first `equal` at it
-  int equal = between;
-  if (between > places) {
-    const int reps = p.Hq / c.Hkv;
-    for (int i = warp; i < n; i += kPickThreads / 32) {
+  const int places = need - sure;   // for the pages in between
+  const bool ranked = between > places;
+  unsigned long long cut = 0;       // their keys above `cut` are in, and the first `equal` at it
+  int equal = 0;
+  const bool few = ranked && !odd && between <= kFewTies && local;
+  if (few) {
+    // rank each against the others; the keys of those that lose or win leave [low, high]
+    for (int t = warp; t < between; t += kSelectWarps) {
+      const unsigned long long k = exact_key<D, BF16>(p, b, g, p.keep_first + tie_page[t]);
+      if (lane == 0) tie_key[t] = k;
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < between) {
+      const unsigned long long k = tie_key[threadIdx.x];
+      const int page = tie_page[threadIdx.x];
+      int above = 0;
+      for (int t = 0; t < between; ++t) above += tie_key[t] > k || (tie_key[t] == k && tie_page[t] < page);
+      held[page] = above < places ? ~0u : 0u;
+    }
+    __syncthreads();
+  } else if (ranked) {
+    unsigned long long* keys = p.keys + static_cast<int64_t>(unit) * c.max_pages;
+    for (int i = warp; i < n; i += kSelectWarps) {
       const uint32_t k = key32(i);
       if (k < low || k > high) continue;
-      const int id = pool_page(c, b, p.keep_first + i);
-      unsigned long long key = 0;
-      if (id >= 0) {
-        const uint16_t* lo = c.bounds + (static_cast<int64_t>(id) * c.Hkv + g) * 2 * D;
-        double best = 0.0;
-        for (int r = 0; r < reps; ++r) {
-          const uint16_t* q = p.q + (static_cast<int64_t>(b) * p.Hq + g * reps + r) * D;
-          double s = 0.0;
-          for (int d = lane; d < D; d += 32) {
-            const double x = unpack2<BF16>(q[d]).x;
-            const double u = x * unpack2<BF16>(lo[d]).x, v = x * unpack2<BF16>(lo[D + d]).x;
-            s += u > v || u != u ? u : v;
-          }
-          for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-          if (r == 0 || s > best || s != s) best = s;
-          if (best != best) break;
-        }
-        key = order_key(best);
-      }
-      if (lane == 0) keys[i] = key;
+      const unsigned long long k64 = exact_key<D, BF16>(p, b, g, p.keep_first + i);
+      if (lane == 0) keys[i] = k64;
     }
     __syncthreads();
     auto key64 = [&](int i, unsigned long long* k) {
@@ -371,9 +468,9 @@ fa_page_pick_kernel(const SelectArgs p) {
       *k = keys[i];
       return true;
     };
-    cut = kth_largest<unsigned long long>(counts, n, places, key64);
+    cut = kth_largest<unsigned long long>(counts, n, places, 0ull, ~0ull, key64);
     int above = 0;
-    for (int i = threadIdx.x; i < n; i += kPickThreads) {
+    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
       unsigned long long k;
       above += key64(i, &k) && k > cut;
     }
@@ -381,20 +478,20 @@ fa_page_pick_kernel(const SelectArgs p) {
     equal = places - sum[0];
   }
   // places in ascending order: a thread takes a run of pages
-  const int per = (n + kPickThreads - 1) / kPickThreads;
+  const int per = (n + kSelectThreads - 1) / kSelectThreads;
   const int i0 = min(n, static_cast<int>(threadIdx.x) * per), i1 = min(n, i0 + per);
-  const bool ranked = between > places;
   // 2: in, 1: in if early enough among its equals, 0: out
   auto state = [&](int i) {
     const uint32_t k = key32(i);
     if (k > high) return 2;
     if (k < low) return 0;
     if (!ranked) return 2;
-    const unsigned long long k64 = keys[i];
+    if (few) return k == ~0u ? 2 : 0;
+    const unsigned long long k64 = p.keys[static_cast<int64_t>(unit) * c.max_pages + i];
     return k64 > cut ? 2 : k64 == cut ? 1 : 0;
   };
   int ties = 0;
-  if (ranked) {
+  if (ranked && !few) {
     for (int i = i0; i < i1; ++i) ties += state(i) == 1;
     ties = block_before(ties, warp_sums);
   }
@@ -419,36 +516,21 @@ cudaError_t run_select(const SelectLaunch& a) {
   p.Hq = a.Hq; p.n_sel = a.n_sel; p.keep_first = a.keep_first; p.keep_last = a.keep_last;
   p.sel = a.sel; p.sel_lens = a.sel_lens;
   const int64_t units = static_cast<int64_t>(a.c.B) * a.c.Hkv;
-  p.scores = static_cast<float2*>(a.ws);
-  p.keys = reinterpret_cast<unsigned long long*>(p.scores + units * a.c.max_pages);
-  // as many query heads, then KV heads, as shared memory holds
-  const int reps = a.Hq / a.c.Hkv;
-  p.head_chunk = std::min(reps, kScoreSmem / 4 / D - 2);
-  const int pitch_bytes = 4 * score_pitch(p.head_chunk, D);
-  p.group = std::max(1, std::min(std::min(a.c.Hkv, kScoreSlots<D>), kScoreSmem / pitch_bytes));
-  const int per_pass = kScoreSlots<D> / p.group * kScorePages;
-  // enough blocks to fill the GPU a few times over, but few enough that loading
-  // the queries stays small beside the bounds
-  const int64_t group_blocks = (a.c.Hkv + p.group - 1) / p.group;
-  const int64_t want = std::max<int64_t>(1, static_cast<int64_t>(device_sm_count()) * 4 / std::max<int64_t>(1, a.c.B * group_blocks));
-  int64_t chunk = (a.c.max_pages + want - 1) / want;
-  chunk = std::max<int64_t>((chunk + per_pass - 1) / per_pass, 1) * per_pass;
-  while ((a.c.max_pages + chunk - 1) / chunk > 65535) chunk *= 2;
-  p.chunk = static_cast<int>(chunk);
-  if (group_blocks > 65535) return cudaErrorInvalidConfiguration;
-  if (a.c.max_pages > a.n_sel) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attrs[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(a.c.B), static_cast<unsigned>((a.c.max_pages + chunk - 1) / chunk),
-                       static_cast<unsigned>(group_blocks));
-    cfg.blockDim = dim3(kScoreThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.group) * pitch_bytes;
-    cfg.stream = a.stream;
-    allow_early_launch(&cfg, attrs);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_page_score_kernel<D, BF16>, p);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_kernel(fa_page_pick_kernel<D, BF16>, units, kPickThreads, 0, a.stream, 1, p);
+  p.keys = static_cast<unsigned long long*>(a.ws);
+  p.scores = reinterpret_cast<uint32_t*>(p.keys + units * a.c.max_pages);
+  // query heads in eights, as many as shared memory is set aside for
+  p.head_chunk = std::min((a.Hq / a.c.Hkv + 7) / 8, (kQuerySmem / query_pitch(D) - 1) / 16) * 8;
+  // a cluster large enough that each CTA has one pass over its pages
+  int ranks = 1;
+  while (ranks < kSelectRanks && ranks * kScorePages < a.c.max_pages) ranks *= 2;
+  const int64_t held = std::min<int64_t>(kHeld, a.c.max_pages);
+  const size_t smem = static_cast<size_t>(query_bytes(p.head_chunk, D)) + held * 4;
+  auto kern = fa_page_select_kernel<D, BF16>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kQuerySmem + kHeld * 4);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, units * ranks, kSelectThreads, static_cast<int>(smem), a.stream,
+                       static_cast<unsigned>(ranks), p, ranks);
 }
 
 template <bool BF16>

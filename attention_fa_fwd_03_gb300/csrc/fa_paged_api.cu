@@ -224,7 +224,7 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
 
 size_t fa_page_select_workspace_size(int B, int Hkv, int max_pages) {
   if (B < 1 || Hkv < 1 || max_pages < 1) return 0;
-  const size_t bytes = static_cast<size_t>(B) * Hkv * max_pages * 16;  // fp32 score and bound, 64-bit score
+  const size_t bytes = static_cast<size_t>(B) * Hkv * max_pages * 12;  // scores in 32 and in 64 bits
   return (bytes + 255) / 256 * 256;
 }
 
