@@ -20,9 +20,11 @@
 // the D additions at least single precision in an order and with a rounding that
 // are left open). With tau the last place's value among the fp32 scores, its true
 // value is within E of tau: pages above tau + 2 E are chosen, pages under tau - 2 E
-// are not, and only the few in between are computed again in 64 bits and ranked by
-// (score, lower page). Where there are no more of them than places, nothing is
-// computed again.
+// are not. Where those in between are more than the places left, they are computed
+// again as exact products summed in two fp32 words (E2 = D 2^-45 A + 2^-130, the
+// latter for products that underflow), and those that this leaves open too in 64
+// bits, ranked by (score, lower page): the 64-bit units are so few that one page
+// costs microseconds.
 #include "fa_inst.cuh"
 #include "fa_paged_launch.h"
 #include "fa_paged_mma.cuh"
@@ -103,10 +105,34 @@ __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* 
   const int row = lane >> 2, col = lane & 3;
   uint8_t* qmag = qs + 2 * p.head_chunk * PITCH;
   ScoreStats st = {0.f, 0, ~0u, 0u};
+  // this thread's rows of a pass: pages base + row and base + row + 8
+  const uint4* src[2];
+  bool there[2];
+  uint4 lo[2][BATCH], hi[2][BATCH];
+  auto find_rows = [&](int base) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = base + row + 8 * k;
+      const int id = i < end ? pool_page(c, b, p.keep_first + i) : -1;
+      there[k] = id >= 0;
+      src[k] = reinterpret_cast<const uint4*>(c.bounds + (static_cast<int64_t>(max(id, 0)) * c.Hkv + g) * 2 * D) + col;
+    }
+  };
+  auto load_rows = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        lo[k][i] = there[k] ? __ldg(src[k] + 4 * (i0 + i)) : make_uint4(0, 0, 0, 0);
+        hi[k][i] = there[k] ? __ldg(src[k] + D / 8 + 4 * (i0 + i)) : make_uint4(0, 0, 0, 0);
+      }
+  };
   for (int h0 = 0; h0 < reps; h0 += p.head_chunk) {
     const int heads = min(p.head_chunk, reps - h0), tiles = (heads + 7) / 8;
     const bool last = h0 + heads == reps;
     if (h0 > 0) __syncthreads();
+    find_rows(begin + 16 * warp);  // under way while the queries are laid out
+    load_rows(0);
     // behind the last head it again, which changes no maximum
     for (int i = threadIdx.x; i < tiles * 8 * (D / 2); i += kSelectThreads) {
       const int r = i / (D / 2), d2 = i - r * (D / 2);
@@ -128,29 +154,16 @@ __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* 
     }
     __syncthreads();
     for (int base = begin + 16 * warp; base < end; base += kScorePages) {
-      // this thread's rows: pages base + row and base + row + 8
-      const uint4* src[2];
-      bool there[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int i = base + row + 8 * k;
-        const int id = i < end ? pool_page(c, b, p.keep_first + i) : -1;
-        there[k] = id >= 0;
-        src[k] = reinterpret_cast<const uint4*>(c.bounds + (static_cast<int64_t>(max(id, 0)) * c.Hkv + g) * 2 * D) + col;
+      if (base != begin + 16 * warp) {
+        find_rows(base);
+        load_rows(0);
       }
       float best[2] = {-INFINITY, -INFINITY}, most[2] = {0.f, 0.f};
       for (int t = 0; t < tiles; ++t) {
         float s[4] = {0.f, 0.f, 0.f, 0.f}, a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i0 = 0; i0 < CH; i0 += BATCH) {
-          uint4 lo[2][BATCH], hi[2][BATCH];
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-              lo[k][i] = there[k] ? __ldg(src[k] + 4 * (i0 + i)) : make_uint4(0, 0, 0, 0);
-              hi[k][i] = there[k] ? __ldg(src[k] + D / 8 + 4 * (i0 + i)) : make_uint4(0, 0, 0, 0);
-            }
+          if (CH > BATCH && (i0 > 0 || t > 0)) load_rows(i0);
 #pragma unroll
           for (int i = 0; i < BATCH; ++i) {
             const int at = 16 * (col + 4 * (i0 + i));
@@ -263,8 +276,8 @@ __device__ __forceinline__ K kth_largest(BlockCounts& counts, int n, int need, K
   return t;
 }
 
-// Exclusive prefix sum over the block's threads.
-__device__ __forceinline__ int block_before(int x, int* warp_sums) {
+// Exclusive prefix sum over the block's threads, and the total. Three barriers.
+__device__ __forceinline__ int block_before(int x, int* warp_sums, int* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int incl = x;
 #pragma unroll
@@ -275,9 +288,90 @@ __device__ __forceinline__ int block_before(int x, int* warp_sums) {
   __syncthreads();  // the previous use of warp_sums is over
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  int before = incl - x;
-  for (int w = 0; w < warp; ++w) before += warp_sums[w];
-  return before;
+  static_assert(kSelectWarps <= 32, "one warp adds the warps' sums");
+  int sums = lane < kSelectWarps ? warp_sums[lane] : 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, sums, off);
+    if (lane >= off) sums += y;
+  }
+  *total = __shfl_sync(0xffffffffu, sums, 31);
+  const int before = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
+  return incl - x + (warp > 0 ? before : 0);
+}
+
+// The need-th largest of the n keys in [lo, hi] that get(i) gives: a histogram of
+// kBins equal ranges, the range of the wanted place, again within it until it
+// holds few keys, which are ranked against each other. Bins of scores are nearly
+// evenly filled, so one round is the rule; each round divides the range by kBins.
+constexpr int kBins = 2048;
+constexpr int kFewKeys = 256;
+struct SearchSmem {
+  int bins[kBins];
+  uint32_t keys[kFewKeys];
+  int warp_sums[kSelectWarps];
+  int bin, above, inside, count;
+  uint32_t found;
+};
+template <class Get>
+__device__ __forceinline__ uint32_t kth_largest_score(SearchSmem& sm, int n, int need, uint32_t lo, uint32_t hi,
+                                                      const Get& get) {
+  constexpr int PER = kBins / kSelectThreads;
+  while (true) {
+    if (lo == hi) return lo;
+    const int shift = max(0, 32 - __clz(hi - lo) - 11);
+    static_assert(kBins == 1 << 11, "bins cover the range");
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sm.bins[threadIdx.x + i * kSelectThreads] = 0;
+    if (threadIdx.x == 0) sm.count = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+      const uint32_t k = get(i);
+      if (k >= lo && k <= hi) atomicAdd(&sm.bins[(k - lo) >> shift], 1);
+    }
+    __syncthreads();
+    // thread t: bins from the top, kBins - 1 - PER t down
+    int mine = 0, total;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine += sm.bins[kBins - 1 - PER * threadIdx.x - i];
+    int above = block_before(mine, sm.warp_sums, &total);
+    if (above < need && need <= above + mine) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int bin = kBins - 1 - PER * threadIdx.x - i, x = sm.bins[bin];
+        if (above < need && need <= above + x) {
+          sm.bin = bin;
+          sm.above = above;
+          sm.inside = x;
+        }
+        above += x;
+      }
+    }
+    __syncthreads();
+    need -= sm.above;
+    lo += static_cast<uint32_t>(sm.bin) << shift;
+    hi = min(hi, lo + ((1u << shift) - 1));
+    const int inside = sm.inside;
+    if (inside <= kFewKeys) {
+      for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+        const uint32_t k = get(i);
+        if (k >= lo && k <= hi) sm.keys[atomicAdd(&sm.count, 1)] = k;
+      }
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < inside) {
+        const uint32_t k = sm.keys[threadIdx.x];
+        int more = 0, equal = 0;
+        for (int i = 0; i < inside; ++i) {
+          more += sm.keys[i] > k;
+          equal += sm.keys[i] == k;
+        }
+        if (more < need && need <= more + equal) sm.found = k;  // equal keys write the same value
+      }
+      __syncthreads();
+      return sm.found;
+    }
+    __syncthreads();  // before the bins are cleared again
+  }
 }
 
 // Store to the first CTA of the cluster, at the place `at` has in this one's
@@ -317,13 +411,64 @@ __device__ __forceinline__ unsigned long long exact_key(const SelectArgs& p, int
   return order_key(best);
 }
 
+// s + e exactly, as the rounded sum and its error.
+__device__ __forceinline__ void two_sum(float a, float b, float* s, float* e) {
+  *s = __fadd_rn(a, b);
+  const float t = __fsub_rn(*s, a);
+  *e = __fadd_rn(__fsub_rn(a, __fsub_rn(*s, t)), __fsub_rn(b, t));
+}
+
+// The score of a page that is there, as the sum of two fp32 words, by a whole
+// warp: products are exact in fp32 (16-bit factors), errors of the sums are kept.
+template <int D, bool BF16>
+__device__ __forceinline__ float2 two_word_score(const SelectArgs& p, int b, int g, int page) {
+  const PagedView& c = p.c;
+  const int lane = threadIdx.x & 31, reps = p.Hq / c.Hkv;
+  const int id = max(pool_page(c, b, page), 0);
+  const uint16_t* lo = c.bounds + (static_cast<int64_t>(id) * c.Hkv + g) * 2 * D;
+  float x[D / 32][2];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    x[i][0] = unpack2<BF16>(lo[lane + 32 * i]).x;
+    x[i][1] = unpack2<BF16>(lo[D + lane + 32 * i]).x;
+  }
+  float2 best = make_float2(-INFINITY, 0.f);
+#pragma unroll 4
+  for (int r = 0; r < reps; ++r) {
+    const uint16_t* q = p.q + (static_cast<int64_t>(b) * p.Hq + g * reps + r) * D;
+    float s = 0.f, e = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const float y = unpack2<BF16>(q[lane + 32 * i]).x;
+      float err;
+      two_sum(s, __fmul_rn(y, y < 0.f ? x[i][0] : x[i][1]), &s, &err);
+      e = __fadd_rn(e, err);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      // both lanes of a pair add in the same order, so all lanes agree
+      const float s2 = __shfl_xor_sync(0xffffffffu, s, off), e2 = __shfl_xor_sync(0xffffffffu, e, off);
+      const bool low = (lane & off) == 0;
+      float err;
+      two_sum(low ? s : s2, low ? s2 : s, &s, &err);
+      e = __fadd_rn(__fadd_rn(e, e2), err);
+    }
+    float hi, rest;
+    two_sum(s, e, &hi, &rest);
+    if (hi > best.x || (hi == best.x && rest > best.y)) best = make_float2(hi, rest);
+  }
+  return best;
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kSelectThreads)
 fa_page_select_kernel(const SelectArgs p, int ranks) {
   extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ int counters[3][3], warp_sums[kSelectWarps];
+  __shared__ int counters[3][3];
+  __shared__ SearchSmem search;
   __shared__ uint32_t warp_stats[kSelectWarps][4], rank_stats[kSelectRanks][4];
   __shared__ unsigned long long tie_key[kFewTies];
+  __shared__ float2 tie_score[kFewTies], tie_cut;
   __shared__ int tie_page[kFewTies], ties_found;
   uint8_t* qs = dyn;
   uint32_t* held = reinterpret_cast<uint32_t*>(dyn + (2 * p.head_chunk + 1) * query_pitch(D));
@@ -406,10 +551,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   int sum[3];
   int sure = 0, between = n;
   if (!odd) {
-    const uint32_t tau = kth_largest<uint32_t>(counts, n, need, key_lo, key_hi, [&](int i, uint32_t* k) {
-      *k = key32(i);
-      return true;
-    });
+    const uint32_t tau = kth_largest_score(search, n, need, key_lo, key_hi, key32);
     const float t = order_value(tau);
     // 2 E, with room for the error of A and the roundings of t -+ err
     const float err = 2.02f * D * 1.1920929e-7f * a_max + fabsf(t) * 2.4e-7f;
@@ -437,20 +579,60 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   const bool ranked = between > places;
   unsigned long long cut = 0;       // their keys above `cut` are in, and the first `equal` at it
   int equal = 0;
-  const bool few = ranked && !odd && between <= kFewTies && local;
+  const bool few = ranked && !odd && between <= kFewTies && local && low != order_key(-INFINITY);
   if (few) {
-    // rank each against the others; the keys of those that lose or win leave [low, high]
-    for (int t = warp; t < between; t += kSelectWarps) {
-      const unsigned long long k = exact_key<D, BF16>(p, b, g, p.keep_first + tie_page[t]);
-      if (lane == 0) tie_key[t] = k;
+    // Each against the others; the keys of those that win or lose leave
+    // [low, high]. A bad page is in between only where all of them are.
+    const int t = threadIdx.x;
+    for (int i = warp; i < between; i += kSelectWarps) {
+      const float2 x = two_word_score<D, BF16>(p, b, g, p.keep_first + tie_page[i]);
+      if (lane == 0) tie_score[i] = x;
     }
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < between) {
-      const unsigned long long k = tie_key[threadIdx.x];
-      const int page = tie_page[threadIdx.x];
+    // the last place's score, and which are within 2 E2 of it
+    auto minus = [](float2 x, float2 y) { return (x.x - y.x) + (x.y - y.y); };
+    if (t < between) {
+      const float2 x = tie_score[t];
       int above = 0;
-      for (int t = 0; t < between; ++t) above += tie_key[t] > k || (tie_key[t] == k && tie_page[t] < page);
-      held[page] = above < places ? ~0u : 0u;
+      for (int i = 0; i < between; ++i) {
+        const float2 y = tie_score[i];
+        above += y.x > x.x || (y.x == x.x && (y.y > x.y || (y.y == x.y && i < t)));
+      }
+      if (above == places - 1) tie_cut = x;
+    }
+    __syncthreads();
+    const float err2 = 2.02f * (D * 2.8421709e-14f * a_max + 7.3468397e-40f);
+    int in = 0, open = 0;
+    if (t < between) {
+      const float d = minus(tie_score[t], tie_cut);
+      in = d > err2;
+      open = fabsf(d) <= err2;
+    }
+    counts.add(in, open, 0, sum);
+    const int left = places - sum[0];
+    const bool exact = sum[1] > left;
+    if (exact) {
+      for (int i = warp; i < between; i += kSelectWarps) {
+        if (!(fabsf(minus(tie_score[i], tie_cut)) <= err2)) continue;
+        const unsigned long long k = exact_key<D, BF16>(p, b, g, p.keep_first + tie_page[i]);
+        if (lane == 0) tie_key[i] = k;
+      }
+      __syncthreads();
+    }
+    if (t < between) {
+      if (open && exact) {
+        const int page = tie_page[t];
+        const unsigned long long k = tie_key[t];
+        int above = 0;
+        for (int i = 0; i < between; ++i) {
+          if (!(fabsf(minus(tie_score[i], tie_cut)) <= err2)) continue;
+          above += tie_key[i] > k || (tie_key[i] == k && tie_page[i] < page);
+        }
+        in = above < left;
+      } else {
+        in |= open;
+      }
+      held[tie_page[t]] = in ? ~0u : 0u;
     }
     __syncthreads();
   } else if (ranked) {
@@ -477,12 +659,8 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     counts.add(above, 0, 0, sum);
     equal = places - sum[0];
   }
-  // places in ascending order: a thread takes a run of pages
-  const int per = (n + kSelectThreads - 1) / kSelectThreads;
-  const int i0 = min(n, static_cast<int>(threadIdx.x) * per), i1 = min(n, i0 + per);
   // 2: in, 1: in if early enough among its equals, 0: out
-  auto state = [&](int i) {
-    const uint32_t k = key32(i);
+  auto state = [&](int i, uint32_t k) {
     if (k > high) return 2;
     if (k < low) return 0;
     if (!ranked) return 2;
@@ -490,21 +668,40 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     const unsigned long long k64 = p.keys[static_cast<int64_t>(unit) * c.max_pages + i];
     return k64 > cut ? 2 : k64 == cut ? 1 : 0;
   };
-  int ties = 0;
-  if (ranked && !few) {
-    for (int i = i0; i < i1; ++i) ties += state(i) == 1;
-    ties = block_before(ties, warp_sums);
-  }
-  int mine = 0, t = ties;
-  for (int i = i0; i < i1; ++i) {
-    const int s = state(i);
-    mine += s == 2 || (s == 1 && t++ < equal);
-  }
-  int at = p.keep_first + block_before(mine, warp_sums);
-  t = ties;
-  for (int i = i0; i < i1; ++i) {
-    const int s = state(i);
-    if (s == 2 || (s == 1 && t++ < equal)) sel[at++] = p.keep_first + i;
+  // places in ascending order: a thread takes runs of four pages
+  int at = p.keep_first, seen = 0;  // places given and equals met before this stretch
+  for (int base = 0; base < n; base += 4 * kSelectThreads) {
+    const int i0 = base + 4 * threadIdx.x;
+    uint32_t k[4] = {0, 0, 0, 0};
+    if (local && i0 + 3 < n) {
+      const uint4 x = *reinterpret_cast<const uint4*>(held + i0);
+      k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i0 + j < n) k[j] = key32(i0 + j);
+    }
+    int st[4], ties = 0, total;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      st[j] = i0 + j < n ? state(i0 + j, k[j]) : 0;
+      ties += st[j] == 1;
+    }
+    if (ranked && !few) {
+      int t = seen + block_before(ties, search.warp_sums, &total);
+      seen += total;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (st[j] == 1) st[j] = t++ < equal ? 2 : 0;
+    }
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine += st[j] == 2;
+    int to = at + block_before(mine, search.warp_sums, &total);
+    at += total;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (st[j] == 2) sel[to++] = p.keep_first + i0 + j;
   }
 }
 
@@ -521,8 +718,9 @@ cudaError_t run_select(const SelectLaunch& a) {
   // query heads in eights, as many as shared memory is set aside for
   p.head_chunk = std::min((a.Hq / a.c.Hkv + 7) / 8, (kQuerySmem / query_pitch(D) - 1) / 16) * 8;
   // a cluster large enough that each CTA has one pass over its pages
+  // (and not more CTAs than fill the GPU)
   int ranks = 1;
-  while (ranks < kSelectRanks && ranks * kScorePages < a.c.max_pages) ranks *= 2;
+  while (ranks < kSelectRanks && ranks * kScorePages < a.c.max_pages && units * ranks < device_sm_count()) ranks *= 2;
   const int64_t held = std::min<int64_t>(kHeld, a.c.max_pages);
   const size_t smem = static_cast<size_t>(query_bytes(p.head_chunk, D)) + held * 4;
   auto kern = fa_page_select_kernel<D, BF16>;

@@ -296,6 +296,11 @@ SELECT = [  # B, Hq, Hkv, D, page, lengths, n_sel, keep_first, keep_last, dtype
     (4, 2, 1, 64, 128, [1, 128, 129, 4000], 1, 0, 1, "fp16"),
     (2, 2, 1, 64, 16, [4000, 600], 7, 3, 4, "fp16"),      # only what is always kept
     (1, 2, 1, 64, 16, [60000], 200, 2, 2, "bf16"),        # more pages than threads
+    (1, 2, 1, 64, 16, [210000], 777, 1, 3, "fp16"),       # more pages than shared memory holds scores of
+    (1, 40, 1, 256, 16, [2000], 30, 1, 1, "bf16"),        # more query heads than are held at a time
+    (1, 40, 1, 256, 16, [9000], 30, 0, 1, "fp16"),
+    (1, 128, 1, 128, 32, [9000], 33, 0, 1, "bf16"),
+    (30, 2, 2, 96, 16, [(i * 331) % 5000 for i in range(30)], 50, 1, 1, "bf16"),
 ]
 
 
@@ -329,6 +334,20 @@ def test_select_matches_the_definition(case):
     table, P = make_table(g, B, max(-(-max(lens) // page), 1))
     check_select(randn(g, B, Hq, 1, D, dtype=DT[dt]), bounds_for(g, P, Hkv, D, DT[dt]), table, lens, page, n_sel, kf, kl)
     assert status_clear()
+
+
+def test_select_where_one_score_is_far_from_the_rest():
+    """Scores that fill their range most unevenly: one page is 2^20 times the others, which differ by little."""
+    g = gen(14)
+    lens, page = [9600], 16
+    table, P = make_table(g, 1, 600)
+    bounds, q = bounds_for(g, P, 1, 128, torch.bfloat16), randn(g, 1, 3, 1, 128, dtype=torch.bfloat16)
+    bounds[int(table[0, 123])] *= 2.0 ** 20
+    for n_sel in (1, 2, 100, 599):
+        check_select(q, bounds, table, lens, page, n_sel, 0, 0)
+    bounds[int(table[0, 5])] *= 2.0 ** -100  # and products below the smallest fp32 number
+    q2 = q * 2.0 ** -80
+    check_select(q2, bounds * 2.0 ** -30, table, lens, page, 300, 0, 0)
 
 
 @pytest.mark.parametrize("kind", ["equal", "pairs", "zero_query", "two_values"])
