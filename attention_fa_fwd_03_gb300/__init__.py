@@ -242,7 +242,8 @@ class PagedKV:
     """
 
     __slots__ = ("k", "v", "page_table", "kv_lens", "k_bounds", "device", "dtype", "B", "Hkv", "D",
-                 "num_pages", "page_size", "max_pages", "_struct", "_ref")
+                 "num_pages", "page_size", "max_pages", "_struct", "_ref", "_index", "_lib", "_cuda",
+                 "_i32", "_f32", "_lens_shape", "_sel_lens_shape")
 
     def __init__(self, k, v, page_table, kv_lens, k_bounds=None):
         import torch
@@ -252,58 +253,83 @@ class PagedKV:
         self.B, self.max_pages = page_table.shape
         self.device, self.dtype = k.device, k.dtype
         code = _dtype_code(k)
-        _expect("v", v, tuple(k.shape), k.dtype, k.device)
-        _expect("page_table", page_table, None, torch.int32, k.device)
-        _expect("kv_lens", kv_lens, (self.B,), torch.int32, k.device)
-        if k_bounds is not None:
-            _expect("k_bounds", k_bounds, (self.num_pages, self.Hkv, 2, self.D), k.dtype, k.device)
+        self._index = k.get_device()
+        self._i32, self._f32 = torch.int32, torch.float32
+        self._lens_shape, self._sel_lens_shape = (self.B,), (self.B, self.Hkv)
+        ptrs = [_ptr(k), _address("v", v, k.shape, k.dtype, self),
+                None if k_bounds is None else
+                _address("k_bounds", k_bounds, (self.num_pages, self.Hkv, 2, self.D), k.dtype, self),
+                _address("page_table", page_table, page_table.shape, torch.int32, self),
+                _address("kv_lens", kv_lens, self._lens_shape, torch.int32, self)]
         self.k, self.v, self.k_bounds = k, v, k_bounds
         self.page_table, self.kv_lens = page_table, kv_lens
-        self._struct = _PagedKVStruct(_ptr(k), _ptr(v), None if k_bounds is None else _ptr(k_bounds),
-                                      _ptr(page_table), _ptr(kv_lens), self.B, self.Hkv, self.D,
-                                      self.num_pages, self.page_size, self.max_pages, code)
+        self._lib, self._cuda = library(), torch.cuda
+        self._struct = _PagedKVStruct(*ptrs, self.B, self.Hkv, self.D, self.num_pages, self.page_size,
+                                      self.max_pages, code)
         self._ref = ctypes.byref(self._struct)
 
 
-def _expect(name: str, t, shape, dtype, device) -> int:
-    """Address of a contiguous tensor of this shape (None: any), dtype and device."""
-    if t.dtype != dtype or (shape is not None and t.shape != shape):
-        want = dtype if shape is None else f"{dtype} of shape {list(shape)}"
-        raise ValueError(f"{name}: expected {want}, got {t.dtype} of shape {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected on {device}, got {t.device}")
-    return _ptr(t)
+def _address(name: str, t, shape, dtype, kv) -> int:
+    """Address of a contiguous tensor of this shape and dtype on the cache's device."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} of shape {list(shape)}, got {t.dtype} of shape {list(t.shape)}")
+    if t.get_device() != kv._index:
+        raise ValueError(f"{name}: expected on {kv.device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
 
 
 def _token_view(name: str, t, shape, kv):
     """Address and strides of a [B, H, T, D] view whose innermost index is contiguous."""
-    if t.dtype != kv.dtype or t.device != kv.device or t.shape != shape:
+    if t.dtype is not kv.dtype or t.shape != shape or t.get_device() != kv._index:
         raise ValueError(f"{name}: expected {kv.dtype} of shape {list(shape)} on {kv.device}, got "
                          f"{t.dtype} of shape {list(t.shape)} on {t.device}")
     sb, sh, st, sd = t.stride()
-    if sd != 1 and shape[3] > 1:
+    if sd != 1:
         raise ValueError(f"{name}: the innermost index must be contiguous")
     # the stride of an index of size 1 is never used and can be anything
     B, H, T, _ = shape
-    strides = (ctypes.c_int64 * 3)(sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0)
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
-    return t.data_ptr(), strides
+    return t.data_ptr(), _Strides(sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0)
 
 
-def _launch(kv, fn, what: str, args, stream) -> None:
+_Strides = ctypes.c_int64 * 3
+
+
+def _workspace(t, kv, what: str):
+    """Address and bytes of a workspace tensor."""
+    if t is None:
+        raise ValueError(f"{what} needs a workspace tensor (the library never allocates)")
+    if t.get_device() != kv._index:
+        raise ValueError(f"workspace: expected on {kv.device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return t.data_ptr(), t.nbytes
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream of device ``index``. PyTorch's own accessor of the raw handle where it
+    has one: a Stream object costs as much as a kernel launch."""
+    global _raw_stream
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = get or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)
+
+
+def _launch(kv, fn, what: str, stream, *args) -> None:
     """Call ``fn`` on ``stream`` (default: the current stream of the cache's
     device) with that device current."""
-    import torch
+    index = kv._index
     if stream is None:
-        stream = torch.cuda.current_stream(kv.device).cuda_stream
+        stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == kv.device.index:
-        st = fn(*args, stream)
+    if kv._cuda.current_device() == index:
+        st = fn(kv._ref, *args, stream)
     else:
-        with torch.cuda.device(kv.device):
-            st = fn(*args, stream)
+        with kv._cuda.device(index):
+            st = fn(kv._ref, *args, stream)
     if st != 0:
         raise FaError(st, what)
 
@@ -320,33 +346,33 @@ def fa_kv_append(kv: PagedKV, k, v, cos=None, sin=None, interleaved: bool = Fals
     None for no rotation. ``kv.kv_lens`` counts the new tokens already;
     ``new_lens`` [B] int32 says how many of the T rows of each sequence are
     tokens (None: all)."""
-    import torch
+    B, Hkv, D = kv.B, kv.Hkv, kv.D
     T = k.shape[2] if k.dim() == 4 else 0
-    kp, ks = _token_view("k", k, (kv.B, kv.Hkv, T, kv.D), kv)
-    vp, vs = _token_view("v", v, (kv.B, kv.Hkv, T, kv.D), kv)
-    qp = qs = qo = None
-    Hq = 0
+    kp, ks = _token_view("k", k, (B, Hkv, T, D), kv)
+    vp, vs = _token_view("v", v, (B, Hkv, T, D), kv)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
+    qp = qs = qo = None
+    Hq = 0
     if q is not None:
-        Hq = q.shape[1] if q.dim() == 4 else 0
-        qp, qs = _token_view("q", q, (kv.B, Hq, T, kv.D), kv)
-        qo = _expect("q_out", q_out, (kv.B, Hq, T, kv.D), kv.dtype, kv.device)
+        shape = q.shape
+        Hq = shape[1] if len(shape) == 4 else 0
+        qp, qs = _token_view("q", q, (B, Hq, T, D), kv)
+        qo = _address("q_out", q_out, shape, kv.dtype, kv)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     cp = sp = None
     rope_len = rot_dim = 0
     if cos is not None:
-        if cos.dim() != 2:
+        shape = cos.shape
+        if len(shape) != 2:
             raise ValueError("cos and sin are [positions, rot_dim / 2]")
-        rope_len, half = cos.shape
-        rot_dim = 2 * half
-        cp = _expect("cos", cos, None, torch.float32, kv.device)
-        sp = _expect("sin", sin, cos.shape, torch.float32, kv.device)
-    nl = None if new_lens is None else _expect("new_lens", new_lens, (kv.B,), torch.int32, kv.device)
-    _launch(kv, library().fa_kv_append, "fa_kv_append",
-            (kv._ref, kp, ks, vp, vs, qp, qs, qo, Hq, T, nl, cp, sp, rope_len, rot_dim,
-             int(bool(interleaved))), stream)
+        rope_len, rot_dim = shape[0], 2 * shape[1]
+        cp = _address("cos", cos, shape, kv._f32, kv)
+        sp = _address("sin", sin, shape, kv._f32, kv)
+    nl = None if new_lens is None else _address("new_lens", new_lens, kv._lens_shape, kv._i32, kv)
+    _launch(kv, kv._lib.fa_kv_append, "fa_kv_append", stream, kp, ks, vp, vs, qp, qs, qo, Hq, T, nl, cp,
+            sp, rope_len, rot_dim, 1 if interleaved else 0)
 
 
 def fa_paged_workspace_size(Hq: int, Hkv: int, Tq: int, D: int) -> int:
@@ -362,30 +388,23 @@ def fa_paged_fwd(kv: PagedKV, q, o, lse, scale: float, causal: bool = False, win
     and window masks go by position in the sequence. ``sel`` [B, Hkv, n_sel]
     and ``sel_lens`` [B, Hkv] int32 restrict each KV head to these pages.
     ``workspace`` has fa_paged_workspace_size(Hq, Hkv, Tq, D) bytes."""
-    import torch
-    if workspace is None:
-        raise ValueError("fa_paged_fwd needs a workspace tensor (the library never allocates)")
-    if q.dim() != 4 or q.shape[0] != kv.B or q.shape[3] != kv.D:
-        raise ValueError(f"q: expected [{kv.B}, Hq, Tq, {kv.D}], got {list(q.shape)}")
-    _, Hq, Tq, _ = shape = q.shape
-    dev = kv.device
+    wp, wn = _workspace(workspace, kv, "fa_paged_fwd")
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != kv.B or shape[3] != kv.D:
+        raise ValueError(f"q: expected [{kv.B}, Hq, Tq, {kv.D}], got {list(shape)}")
     if (sel is None) != (sel_lens is None):
         raise ValueError("sel and sel_lens go together")
     sp = slp = nl = None
     n_sel = 0
     if sel is not None:
         n_sel = sel.shape[-1]
-        sp = _expect("sel", sel, (kv.B, kv.Hkv, n_sel), torch.int32, dev)
-        slp = _expect("sel_lens", sel_lens, (kv.B, kv.Hkv), torch.int32, dev)
+        sp = _address("sel", sel, (kv.B, kv.Hkv, n_sel), kv._i32, kv)
+        slp = _address("sel_lens", sel_lens, kv._sel_lens_shape, kv._i32, kv)
     if new_lens is not None:
-        nl = _expect("new_lens", new_lens, (kv.B,), torch.int32, dev)
-    if workspace.device != dev:
-        raise ValueError(f"workspace: expected on {dev}, got {workspace.device}")
-    _launch(kv, library().fa_paged_fwd, "fa_paged_fwd",
-            (kv._ref, _expect("q", q, shape, kv.dtype, dev), _expect("o", o, shape, kv.dtype, dev),
-             _expect("lse", lse, shape[:3], torch.float32, dev), Hq, Tq, float(scale),
-             int(bool(causal)), int(window), nl, sp, slp, n_sel, _ptr(workspace),
-             workspace.numel() * workspace.element_size()), stream)
+        nl = _address("new_lens", new_lens, kv._lens_shape, kv._i32, kv)
+    _launch(kv, kv._lib.fa_paged_fwd, "fa_paged_fwd", stream, _address("q", q, shape, kv.dtype, kv),
+            _address("o", o, shape, kv.dtype, kv), _address("lse", lse, shape[:3], kv._f32, kv),
+            shape[1], shape[2], scale, 1 if causal else 0, window, nl, sp, slp, n_sel, wp, wn)
 
 
 def fa_page_select_workspace_size(B: int, Hkv: int, max_pages: int) -> int:
@@ -400,20 +419,15 @@ def fa_page_select(kv: PagedKV, q, sel, sel_lens, keep_first: int = 0, keep_last
     ``sel_lens`` [B, Hkv] int32 how many. ``q`` [B, Hq, 1, D]. The first
     ``keep_first`` and last ``keep_last`` pages are always chosen.
     ``workspace`` has fa_page_select_workspace_size(B, Hkv, max_pages) bytes."""
-    import torch
-    if workspace is None:
-        raise ValueError("fa_page_select needs a workspace tensor (the library never allocates)")
-    if q.dim() != 4 or q.shape[0] != kv.B or q.shape[2] != 1 or q.shape[3] != kv.D:
-        raise ValueError(f"q: expected [{kv.B}, Hq, 1, {kv.D}], got {list(q.shape)}")
-    dev = kv.device
+    wp, wn = _workspace(workspace, kv, "fa_page_select")
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != kv.B or shape[2] != 1 or shape[3] != kv.D:
+        raise ValueError(f"q: expected [{kv.B}, Hq, 1, {kv.D}], got {list(shape)}")
     n_sel = sel.shape[-1]
-    if workspace.device != dev:
-        raise ValueError(f"workspace: expected on {dev}, got {workspace.device}")
-    _launch(kv, library().fa_page_select, "fa_page_select",
-            (kv._ref, _expect("q", q, q.shape, kv.dtype, dev), q.shape[1], n_sel, int(keep_first),
-             int(keep_last), _expect("sel", sel, (kv.B, kv.Hkv, n_sel), torch.int32, dev),
-             _expect("sel_lens", sel_lens, (kv.B, kv.Hkv), torch.int32, dev), _ptr(workspace),
-             workspace.numel() * workspace.element_size()), stream)
+    _launch(kv, kv._lib.fa_page_select, "fa_page_select", stream, _address("q", q, shape, kv.dtype, kv),
+            shape[1], n_sel, keep_first, keep_last,
+            _address("sel", sel, (kv.B, kv.Hkv, n_sel), kv._i32, kv),
+            _address("sel_lens", sel_lens, kv._sel_lens_shape, kv._i32, kv), wp, wn)
 
 
 def fa_selftest_wait_timeout(timeout_ms: int, stream=None) -> None:
