@@ -115,8 +115,8 @@ fa_kv_append_kernel(const AppendArgs p) {
   const int row = item / units, u = item - row * units;
   const int hq = p.q != nullptr ? p.Hq : 0;
   if (row >= 2 * c.Hkv + hq) return;
-  const int n = new_len(c, p.new_lens, b, p.T);
-  const int pos = cache_len(c, b) - n + t;
+  const SeqLens sl = seq_lens(c, p.new_lens, b, p.T);
+  const int n = sl.n, pos = sl.len - n + t;
   const bool valid = t < n && position_ok(p, pos);
   const bool is_v = row < c.Hkv, is_q = !is_v && row < c.Hkv + hq;
   UnitPos at = unit_pos(p, u);
@@ -166,8 +166,8 @@ fa_kv_bounds_kernel(const AppendArgs p, int pages_per_seq) {
   const int g = blockIdx.x % c.Hkv;
   const int bp = blockIdx.x / c.Hkv;
   const int b = bp / pages_per_seq;
-  const int n = new_len(c, p.new_lens, b, p.T), len = cache_len(c, b);
-  int first = len - n, last = len;  // positions written
+  const SeqLens sl = seq_lens(c, p.new_lens, b, p.T);
+  int first = sl.len - sl.n, last = sl.len;  // positions written
   if (first < 0) first = 0;
   if (p.rot_dim > 0 && last > p.rope_len) last = p.rope_len;
   const int page = (first >> c.page_shift) + (bp - b * pages_per_seq);

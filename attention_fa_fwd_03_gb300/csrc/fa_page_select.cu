@@ -43,7 +43,7 @@ struct SelectArgs {
 };
 
 __device__ __forceinline__ int page_count(const PagedView& c, int b) {
-  return (cache_len(c, b) + (1 << c.page_shift) - 1) >> c.page_shift;
+  return (seq_lens(c, nullptr, b, 0).len + (1 << c.page_shift) - 1) >> c.page_shift;
 }
 
 // Larger of two with NaN the largest.

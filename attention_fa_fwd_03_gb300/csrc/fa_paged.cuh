@@ -28,21 +28,21 @@ __device__ __forceinline__ void flag_bad_index(const PagedView& c) {
   atomicOr(c.status, kStatusBadIndex);
 }
 
-// Keys of sequence b, new ones included, clamped to what its table can hold.
-__device__ __forceinline__ int cache_len(const PagedView& c, int b) {
-  const int n = __ldg(c.lens + b), most = c.max_pages << c.page_shift;
-  if (n >= 0 && n <= most) return n;
+// A count that has to be in [0, most], clamped to it.
+__device__ __forceinline__ int checked_count(const PagedView& c, int n, int most) {
+  if (static_cast<unsigned>(n) <= static_cast<unsigned>(most)) return n;
   flag_bad_index(c);
   return n < 0 ? 0 : most;
 }
 
-// New tokens of sequence b among the call's T rows.
-__device__ __forceinline__ int new_len(const PagedView& c, const int* new_lens, int b, int T) {
-  if (new_lens == nullptr) return T;
-  const int n = __ldg(new_lens + b);
-  if (n >= 0 && n <= T) return n;
-  flag_bad_index(c);
-  return n < 0 ? 0 : T;
+// Keys of sequence b (new ones included) and new tokens among the call's T rows,
+// loaded together: callers wait for both once.
+struct SeqLens {
+  int len, n;
+};
+__device__ __forceinline__ SeqLens seq_lens(const PagedView& c, const int* new_lens, int b, int T) {
+  const int len = __ldg(c.lens + b), n = new_lens ? __ldg(new_lens + b) : T;
+  return {checked_count(c, len, c.max_pages << c.page_shift), checked_count(c, n, T)};
 }
 
 // Pool page of page `p` of sequence b (0 <= p < max_pages), or -1.

@@ -81,8 +81,10 @@ struct PagedCfg {
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
   static constexpr int OFF_O = OFF_Q + KREG * QREGION;
   static constexpr int OFF_ML = OFF_O + ROWS * OP * 4;
-  static constexpr int OFF_ROW = OFF_ML + KW * ROWS * 8;  // (max, sum) of the CTA's rows
-  static constexpr int SMEM_BYTES = OFF_ROW + ROWS * 8 + 1024;
+  static constexpr int OFF_PML = OFF_ML + KW * ROWS * 8;  // clusters: (max, sum) beside every piece received
+  static constexpr int SMEM_BYTES = OFF_PML + (CLUSTER ? ROWS * D : 0) + 1024;
+  // clusters: the warps' rows at the end, over the stages and the queries
+  static_assert(KW * ROWS * OP * 4 <= OFF_O, "warps' rows");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -103,17 +105,14 @@ struct Item {
 __device__ __forceinline__ Item load_item(const PagedFwdArgs& p, int i) {
   Item it;
   it.b = p.sel ? i / p.c.Hkv : i;
-  it.len = cache_len(p.c, it.b);
-  it.n = new_len(p.c, p.new_lens, it.b, p.Tq);
+  const int listed = p.sel ? __ldg(p.sel_lens + i) : 0;
+  const SeqLens sl = seq_lens(p.c, p.new_lens, it.b, p.Tq);
+  it.len = sl.len;
+  it.n = sl.n;
   it.first = 0;
   int keys = it.len;
   if (p.sel) {
-    int m = __ldg(p.sel_lens + i);
-    if (m < 0 || m > p.n_sel) {
-      flag_bad_index(p.c);
-      m = m < 0 ? 0 : p.n_sel;
-    }
-    keys = m << p.c.page_shift;  // at most 2^20 entries of 2^8 keys
+    keys = checked_count(p.c, listed, p.n_sel) << p.c.page_shift;  // at most 2^20 entries of 2^8 keys
   } else if (p.window > 0) {
     it.first = max(0, it.len - it.n - p.window + 1) / kPagedTile;
   }
@@ -259,18 +258,15 @@ __device__ __forceinline__ float2 warps_max_sum(const float2* mls, int r) {
   return make_float2(m, l);
 }
 
-// Loads from CTA `rank`'s shared memory, at the place `at` has in this CTA's.
-__device__ __forceinline__ float2 ld_peer_f2(const void* at, uint32_t rank) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_addr(smem_u32(at), rank)));
-  return v;
+// Stores to CTA `rank`'s shared memory, at the place `at` has in this CTA's.
+__device__ __forceinline__ void st_peer_f2(const void* at, uint32_t rank, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_addr(smem_u32(at), rank)), "f"(v.x), "f"(v.y)
+               : "memory");
 }
-__device__ __forceinline__ float4 ld_peer_f4(const void* at, uint32_t rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(peer_addr(smem_u32(at), rank)));
-  return v;
+__device__ __forceinline__ void st_peer_f4(const void* at, uint32_t rank, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer_addr(smem_u32(at), rank)), "f"(v.x),
+               "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 
 // A position no query reaches: the key's slot was not loaded.
@@ -304,6 +300,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
+  if constexpr (C::CLUSTER) cluster_arrive_relaxed();  // waited for before the first store into a peer
   grid_wait_prior();
   grid_release_next();
   const int rank = C::CLUSTER ? part % ranks : 0, unit = C::CLUSTER ? part / ranks : 0;
@@ -393,9 +390,9 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
     // after a wait gave up: let the loads still in flight land before the CTA exits
     if (lane == 0 && abort_flag) drain_ring(smem_u32(&full[0]), C::STAGES, issued, p.wc.drain_cycles, p.wc.status);
-    if constexpr (C::CLUSTER) {  // the consumers' two cluster barriers
+    if constexpr (C::CLUSTER) {  // as the consumers do
       __syncwarp();
-      cluster_barrier();
+      cluster_wait();
       cluster_barrier();
     }
     return;
@@ -428,6 +425,20 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (tid == 0) p.joins[part] = make_int4(-1, 0, 0, 0);
   }
 
+  // a block's query rows to shared memory, rows behind the last one zero
+  auto stage_queries = [&](int64_t row0, int rows) {
+    for (int i = tid; i < C::ROWS * (D / 8); i += 32 * C::WARPS) {
+      const int r = i / (D / 8), ch = i - r * (D / 8);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D) + ch);
+      *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(r, ch & 7)) = x;
+    }
+  };
+  if constexpr (C::CLUSTER) {  // where the unit's rows are does not depend on the lengths
+    const int rb = unit % p.row_blocks;
+    stage_queries(static_cast<int64_t>(unit / p.row_blocks) * p.rows + rb * C::ROWS, min(C::ROWS, p.rows - rb * C::ROWS));
+  }
+
   int consumed = 0;
   bool ok = true;
   // (with clusters: one segment, which may be empty)
@@ -438,13 +449,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int64_t row0 = block_row0(p, w.it.b, g, rb, C::ROWS);
     const int len = w.it.len, n = w.it.n;
     const int p_lo = len - n, p_hi = len - 1;  // positions of the new tokens
-    // the block's query rows to shared memory, rows behind the last one zero
-    for (int i = tid; i < C::ROWS * (D / 8); i += 32 * C::WARPS) {
-      const int r = i / (D / 8), ch = i - r * (D / 8);
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D) + ch);
-      *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(r, ch & 7)) = x;
-    }
+    if constexpr (!C::CLUSTER) stage_queries(row0, rows);
     sync_rows();
     // this thread's two rows and their tokens
     const int r0 = rw * 16 + (lane >> 2);
@@ -466,9 +471,12 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       if (some) {
         const bool all = j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) && !(p.window > 0 && j0 <= p_hi - p.window);
         // S = q K^T: B fragments of keys 0-7 and 8-15
-        float s[2][4];
+        // (two accumulators each: half as long a chain of products)
+        float s[2][4], s2[2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][e] = s2[i][e] = 0.f;
         const int qr = rw * 16 + (lane & 15), kr = kw * 16 + ((lane >> 4) << 3) + (lane & 7);
         const int qc = lane >> 4, kc = (lane >> 3) & 1;
 #pragma unroll
@@ -476,9 +484,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           uint32_t a[4], b[4];
           ldsm4(a, sbase + C::OFF_Q + (k >> 2) * C::QREGION + sw128_offset(qr, (2 * k + qc) & 7));
           ldsm4(b, ks + (k >> 2) * C::REGION + sw128_offset(kr, (2 * k + kc) & 7));
-          mma16816<C::BF16>(s[0], a, b[0], b[1]);
-          mma16816<C::BF16>(s[1], a, b[2], b[3]);
+          mma16816<C::BF16>(k & 1 ? s2[0] : s[0], a, b[0], b[1]);
+          mma16816<C::BF16>(k & 1 ? s2[1] : s[1], a, b[2], b[3]);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][e] += s2[i][e];
         // element e of tile i: row r0 + 8 (e / 2), key j0 + 8 i + 2 (lane % 4) + e % 2
         uint32_t keep0 = ~0u, keep1 = ~0u;  // keys of this thread's V fragments that some row sees
         const int jt = j0 + 2 * (lane & 3);
@@ -598,7 +610,75 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       if ((lane & 3) == 0) mls[kw * C::ROWS + r0 + 8 * h] = make_float2(m[h], l[h]);
     }
-    sync_rows();
+    sync_rows();  // and nobody reads stages any more
+    if constexpr (C::CLUSTER) {
+      // The warps' rows side by side; a thread adds up the four of an 8-column
+      // piece and sends the sum with its maximum and sum of weights to the CTA
+      // that owns the piece (i mod ranks), which joins what all CTAs sent.
+      float* wm = reinterpret_cast<float*>(smem);  // [KW][ROWS][OP]
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(wm + (kw * C::ROWS + r0 + 8 * h) * C::OP + 8 * i + 2 * (lane & 3)) =
+              make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+      sync_rows();
+      const int pieces = rows * (D / 8), share_of = C::ROWS * (D / 8) / ranks;
+      float2* pml = reinterpret_cast<float2*>(smem + C::OFF_PML);  // [ranks][share_of]
+      __syncwarp();
+      cluster_wait();  // every CTA of the cluster is running
+      for (int i = tid; i < pieces; i += 32 * C::WARPS) {
+        const int r = i / (D / 8), ch = i - r * (D / 8);
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const float2 ml = warps_max_sum<C>(mls, r);
+#pragma unroll
+        for (int k = 0; k < C::KW; ++k) {
+          const float mk = mls[k * C::ROWS + r].x;
+          if (mk == -INFINITY) continue;  // nothing seen: not even 0 * inf
+          const float f = ex2(mk - ml.x);
+          const float* x = wm + (k * C::ROWS + r) * C::OP + 8 * ch;
+          const float4 u = *reinterpret_cast<const float4*>(x), v = *reinterpret_cast<const float4*>(x + 4);
+          sum[0] = fmaf(u.x, f, sum[0]);
+          sum[1] = fmaf(u.y, f, sum[1]);
+          sum[2] = fmaf(u.z, f, sum[2]);
+          sum[3] = fmaf(u.w, f, sum[3]);
+          sum[4] = fmaf(v.x, f, sum[4]);
+          sum[5] = fmaf(v.y, f, sum[5]);
+          sum[6] = fmaf(v.z, f, sum[6]);
+          sum[7] = fmaf(v.w, f, sum[7]);
+        }
+        const uint32_t owner = i % ranks;
+        const int slot = rank * share_of + i / ranks;
+        st_peer_f4(om + 8 * slot, owner, make_float4(sum[0], sum[1], sum[2], sum[3]));
+        st_peer_f4(om + 8 * slot + 4, owner, make_float4(sum[4], sum[5], sum[6], sum[7]));
+        st_peer_f2(pml + slot, owner, ml);
+      }
+      __syncwarp();
+      cluster_barrier();  // what was sent has arrived; nobody touches a peer after it
+      for (int j = tid; rank + j * ranks < pieces; j += 32 * C::WARPS) {
+        const int i = rank + j * ranks, r = i / (D / 8), ch = i - r * (D / 8);
+        float mt = -INFINITY, lt = 0.f, sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < ranks; ++k) mt = fmaxf(mt, pml[k * share_of + j].x);
+        for (int k = 0; k < ranks; ++k) {
+          const float2 ml = pml[k * share_of + j];
+          const float f = exp2_rel(ml.x, mt);
+          const float* x = om + 8 * (k * share_of + j);
+          const float4 u = *reinterpret_cast<const float4*>(x), v = *reinterpret_cast<const float4*>(x + 4);
+          lt += ml.y * f;
+          sum[0] = fmaf(u.x, f, sum[0]);
+          sum[1] = fmaf(u.y, f, sum[1]);
+          sum[2] = fmaf(u.z, f, sum[2]);
+          sum[3] = fmaf(u.w, f, sum[3]);
+          sum[4] = fmaf(v.x, f, sum[4]);
+          sum[5] = fmaf(v.y, f, sum[5]);
+          sum[6] = fmaf(v.z, f, sum[6]);
+          sum[7] = fmaf(v.w, f, sum[7]);
+        }
+        store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, sum, lt == 0.f ? 0.f : 1.f / lt);
+        if (ch == 0) p.lse[row0 + r] = row_lse(mt, lt);
+      }
+      return;
+    }
     float f[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -631,52 +711,6 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       sync_rows();
     }
-    if constexpr (C::CLUSTER) {
-      // join through distributed shared memory: every CTA takes a share of the
-      // unit's 8-column pieces and adds up its peers' rows
-      float2* row_ml = reinterpret_cast<float2*>(smem + C::OFF_ROW);
-      for (int r = tid; r < rows; r += 32 * C::WARPS) row_ml[r] = warps_max_sum<C>(mls, r);
-      sync_rows();
-      __syncwarp();
-      cluster_barrier();
-      for (int i = rank * 32 * C::WARPS + tid; i < rows * (D / 8); i += ranks * 32 * C::WARPS) {
-        const int r = i / (D / 8), ch = i - r * (D / 8);
-        float2 ml[kPagedMaxRanks];
-        float4 x[kPagedMaxRanks], y[kPagedMaxRanks];
-#pragma unroll
-        for (int k = 0; k < kPagedMaxRanks; ++k) {
-          ml[k] = make_float2(-INFINITY, 0.f);
-          if (k < ranks) {
-            ml[k] = ld_peer_f2(row_ml + r, k);
-            x[k] = ld_peer_f4(om + r * C::OP + 8 * ch, k);
-            y[k] = ld_peer_f4(om + r * C::OP + 8 * ch + 4, k);
-          }
-        }
-        float mt = -INFINITY, lt = 0.f, sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < kPagedMaxRanks; ++k) mt = fmaxf(mt, ml[k].x);
-#pragma unroll
-        for (int k = 0; k < kPagedMaxRanks; ++k) {
-          if (k >= ranks) continue;
-          const float f = exp2_rel(ml[k].x, mt);
-          lt += ml[k].y * f;
-          sum[0] = fmaf(x[k].x, f, sum[0]);
-          sum[1] = fmaf(x[k].y, f, sum[1]);
-          sum[2] = fmaf(x[k].z, f, sum[2]);
-          sum[3] = fmaf(x[k].w, f, sum[3]);
-          sum[4] = fmaf(y[k].x, f, sum[4]);
-          sum[5] = fmaf(y[k].y, f, sum[5]);
-          sum[6] = fmaf(y[k].z, f, sum[6]);
-          sum[7] = fmaf(y[k].w, f, sum[7]);
-        }
-        store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, sum, lt == 0.f ? 0.f : 1.f / lt);
-        if (ch == 0) p.lse[row0 + r] = row_lse(mt, lt);
-      }
-      __syncwarp();
-      cluster_barrier();  // no CTA leaves while a peer reads its rows
-      return;
-    }
-    // whole unit: O and LSE; else the part
     const bool begins = w.t0 == 0, ends = w.t1 == w.it.tiles;
     const int part_slot = 2 * part + (begins ? 1 : 0);
     for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS) {
