@@ -20,13 +20,17 @@
 // results are the same on every run.
 //
 // Inside a CTA one warp looks up pages and loads tiles by TMA (one box per page
-// piece and 64 columns, 128-byte swizzle) into a ring of stages; KW warps per
+// piece and 64 columns, 128-byte swizzle) into a ring of stages; four warps per
 // row block each take 16 keys of a tile and keep a running maximum and sum of
 // their own, so tiles need no barrier between warps. Scores and outputs are
-// m16n8k16 tensor-core products fed by ldmatrix: a 128-row tcgen05 tile would be
-// at least half padding here (at most 64 rows, usually 4 to 8), and at these few
-// rows the warp-level products take under a third of the time the tile's bytes
-// need.
+// m16n8k16 tensor-core products computed transposed, S^T = K Q^T and O^T = V^T P^T:
+// keys and columns of V are the 16 rows of a fragment (read by ldmatrix straight
+// from the tile), query rows its 8 columns, so a group of up to 8 heads fills a
+// fragment that would be half empty the other way round, and each K or V fragment
+// is loaded once for all row groups. A tcgen05 tile would need 64 keys of one page
+// set per instruction and its accumulators back from TMEM twice a tile; at these
+// few rows the warp-level products take under a third of the time that the tile's
+// bytes need, so the simpler instruction wins.
 #pragma once
 
 #include "fa_inst.cuh"
@@ -59,24 +63,32 @@ struct PagedFwdArgs {
   WaitCfg wc;
 };
 
-template <int D_, int RW_, bool BF16_, bool CLUSTER_>
+// NT: groups of 8 query rows that a warp holds; RW: warps of other rows beside it.
+template <int D_, int NT_, int RW_, bool BF16_, bool CLUSTER_>
 struct PagedCfg {
-  static constexpr int D = D_, RW = RW_;
+  static constexpr int D = D_, NT = NT_, RW = RW_;
   static constexpr bool BF16 = BF16_;
   static constexpr bool CLUSTER = CLUSTER_;          // a cluster per unit instead of equal shares
   static constexpr int KW = kPagedKeyWarps;
-  static constexpr int ROWS = 16 * RW;               // rows of a block
-  static constexpr int WARPS = KW * RW;              // consumer warps; one producer warp beside them
-  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int ROWS = 8 * NT * RW;           // rows of a block
+  static constexpr int WARPS = KW * RW;              // consumer warps
+  // One producer warp beside them; where accumulators need more registers than an
+  // equal split leaves, a warpgroup of producers (one works) that gives its own up.
+  static constexpr bool SPLIT = NT * RW * D >= 1024;
+  static constexpr int THREADS = 32 * (WARPS + (SPLIT ? 4 : 1));
+  static constexpr int REG_PRODUCER = 24, REG_CONSUMER = RW == 4 ? 112 : 224;
+  static constexpr int REG_NEEDED = SPLIT ? 128 * REG_PRODUCER + 32 * WARPS * REG_CONSUMER : 0;
   static constexpr int KREG = (D + 63) / 64;         // 64-column regions of a row
   static constexpr int REGION = kPagedTile * 128;
   static constexpr int TILE = KREG * REGION;         // K (or V) rows of a stage
-  // RW = 1: two CTAs per SM (three at D = 64) with about 100 KB in flight each;
-  // more rows: one CTA per SM
-  static constexpr int STAGES = D == 256 ? (RW == 1 ? 3 : 2) : D == 64 ? (RW == 1 ? 4 : 6) : (RW == 1 ? 3 : 5);
-  static constexpr int CTAS = RW == 1 && D < 256 ? (D == 64 ? 3 : 2) : 1;
+  // Up to 16 rows two CTAs (D = 64: three) share an SM with about 100 KB in flight
+  // each; with more rows, or 64 KB stages, one does.
+  static constexpr int CTAS = D == 256 || (RW > 1 && D > 64) || RW > 2 ? 1 : D == 64 && RW == 1 ? 3 : 2;
+  static constexpr int STAGES = D == 256 ? (RW == 1 ? 3 : 2) : CTAS == 1 ? (D == 64 ? 8 : 5) : D == 64 ? (CTAS == 3 ? 4 : 5) : 3;
+  // Queries as B fragments in registers where they fit, else read again each tile
+  static constexpr bool QREG = NT * D <= (CTAS == 1 && RW == 1 ? 256 : 128);
   static constexpr int QREGION = ROWS * 128;
-  static constexpr int OP = D + 8;                   // row pitch of the merge buffer (floats)
+  static constexpr int OP = D + 4;                   // row pitch of the merge buffers (floats): no bank conflicts
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
   static constexpr int OFF_O = OFF_Q + KREG * QREGION;
@@ -85,8 +97,13 @@ struct PagedCfg {
   static constexpr int SMEM_BYTES = OFF_PML + (CLUSTER ? ROWS * D : 0) + 1024;
   // clusters: the warps' rows at the end, over the stages and the queries
   static_assert(KW * ROWS * OP * 4 <= OFF_O, "warps' rows");
-  static_assert(SMEM_BYTES <= 232448, "shared memory");
+  static_assert(SMEM_BYTES <= 231000, "shared memory");  // beside the static variables
+  static_assert(ROWS * (D / 8) % kPagedMaxRanks == 0, "pieces of a cluster");
 };
+
+// Running maxima may be behind by this much (in the exp2 domain) before the sums
+// are rescaled: weights then reach 2^8 instead of 1, which costs no precision.
+constexpr float kPagedSlack = 8.f;
 
 // ----------------------------------------------------------------- the list
 // An item is a sequence (every KV head and row block of it has the same tiles)
@@ -269,6 +286,13 @@ __device__ __forceinline__ void st_peer_f4(const void* at, uint32_t rank, float4
                : "memory");
 }
 
+// Whether one of two packed values is infinite or NaN (exponent bits all set).
+template <bool BF16>
+__device__ __forceinline__ bool not_finite2(uint32_t x) {
+  constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
+  return (x & e) == e || (x & (e << 16)) == e << 16;
+}
+
 // A position no query reaches: the key's slot was not loaded.
 constexpr int kNoPosition = 0x7fffff00;
 
@@ -311,8 +335,18 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     share = find_share<C::THREADS>(p, part, parts);  // barriers inside
   Walk w;
 
-  if (warp == C::WARPS) {
+  if (warp >= C::WARPS) {
     // ---------------------------------------------------------- producer warp
+    if constexpr (C::SPLIT) {
+      regs_release<C::REG_PRODUCER>();
+      if (warp > C::WARPS) {
+        if constexpr (C::CLUSTER) {
+          cluster_wait();
+          cluster_barrier();
+        }
+        return;
+      }
+    }
     const int piece = min(1 << c.page_shift, kPagedTile);  // keys of a page in one tile
     const int pieces = kPagedTile / piece;
     const uint32_t box = static_cast<uint32_t>(piece) * 128u;
@@ -399,6 +433,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   }
 
   // ------------------------------------------------------------ consumer warps
+  if constexpr (C::SPLIT) regs_claim<C::REG_CONSUMER>();
   const int kw = warp % C::KW, rw = warp / C::KW;
   const int tid = threadIdx.x;
   float* om = reinterpret_cast<float*>(smem + C::OFF_O);
@@ -406,22 +441,6 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   auto sync_rows = [&] { named_bar_sync(1, 32 * C::WARPS); };
 
   if constexpr (!C::CLUSTER) {
-    // units without tiles: nothing is visible to any of their rows
-    {
-      const int mult = item_mult(p);
-      const int64_t units = static_cast<int64_t>(item_count(p)) * mult;
-      for (int64_t u = part; u < units; u += parts) {
-        const int item = static_cast<int>(u / mult), sub = static_cast<int>(u - static_cast<int64_t>(item) * mult);
-        const Item it = load_item(p, item);
-        if (it.tiles > 0) continue;
-        const int g = p.sel ? item % c.Hkv : sub / p.row_blocks, rb = sub % p.row_blocks;
-        const int64_t row0 = block_row0(p, it.b, g, rb, C::ROWS);
-        const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
-        for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS)
-          reinterpret_cast<uint4*>(p.o + row0 * D)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = tid; i < rows; i += 32 * C::WARPS) p.lse[row0 + i] = -INFINITY;
-      }
-    }
     if (tid == 0) p.joins[part] = make_int4(-1, 0, 0, 0);
   }
 
@@ -451,13 +470,39 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int p_lo = len - n, p_hi = len - 1;  // positions of the new tokens
     if constexpr (!C::CLUSTER) stage_queries(row0, rows);
     sync_rows();
-    // this thread's two rows and their tokens
-    const int r0 = rw * 16 + (lane >> 2);
-    const int tok0 = (rb * C::ROWS + r0) % p.Tq, tok1 = (rb * C::ROWS + r0 + 8) % p.Tq;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float acc[D / 8][4];
+    // B fragments of the queries: two products' worth per 8 rows and 32 columns
+    const uint32_t qs = sbase + C::OFF_Q;
+    auto query_frag = [&](uint32_t (&f)[4], int nt, int k2) {
+      const int row = (rw * C::NT + nt) * 8 + (lane & 7), ch = 4 * k2 + (lane >> 3);
+      ldsm4(f, qs + (ch >> 3) * C::QREGION + sw128_offset(row, ch & 7));
+    };
+    uint32_t qf[C::QREG ? C::NT : 1][C::QREG ? D / 32 : 1][4];
+    if constexpr (C::QREG) {
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+      for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+        for (int k2 = 0; k2 < D / 32; ++k2) query_frag(qf[nt][k2], nt, k2);
+    }
+    // groups of 8 rows of this warp that hold any; this thread's columns are rows
+    // 2 (lane % 4) and the next of each group
+    const int groups = min(C::NT, max(0, (rows - rw * C::NT * 8 + 7) / 8));
+    const int col0 = rw * C::NT * 8 + 2 * (lane & 3);
+    float m[C::NT][2], l[C::NT][2], acc[C::NT][D / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < C::NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+    }
+    // tokens of this thread's rows, four bits each
+    uint64_t tokens = 0;
+#pragma unroll
+    for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        tokens |= static_cast<uint64_t>((rb * C::ROWS + col0 + 8 * nt + e) % p.Tq) << (8 * nt + 4 * e);
+    auto token = [&](int nt, int e) { return static_cast<int>(tokens >> (8 * nt + 4 * e)) & 15; };
 
     for (int t = w.t0; t < w.t1; ++t, ++consumed) {
       const int slot = consumed % C::STAGES;
@@ -467,127 +512,161 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       const int j0 = key_pos[slot][kw];
       const uint32_t ks = sbase + C::OFF_KV + slot * 2 * C::TILE, vs = ks + C::TILE;
       // does any row see any of the 16 keys; do all rows see all of them
-      const bool some = j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window);
+      const bool some = groups > 0 && j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window);
       if (some) {
         const bool all = j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) && !(p.window > 0 && j0 <= p_hi - p.window);
-        // S = q K^T: B fragments of keys 0-7 and 8-15
-        // (two accumulators each: half as long a chain of products)
-        float s[2][4], s2[2][4];
+        // S^T = K Q^T: element e of group nt is key j0 + lane / 4 + 8 (e / 2), row
+        // col0 + 8 nt + e % 2. One group: two accumulators, half as long a chain.
+        float s[C::NT][4], s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int nt = 0; nt < C::NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        const int kr = kw * 16 + (lane & 15), kc = lane >> 4;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][e] = s2[i][e] = 0.f;
-        const int qr = rw * 16 + (lane & 15), kr = kw * 16 + ((lane >> 4) << 3) + (lane & 7);
-        const int qc = lane >> 4, kc = (lane >> 3) & 1;
+        for (int k2 = 0; k2 < D / 32; ++k2) {
+          uint32_t a0[4], a1[4];
+          ldsm4(a0, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + kc) & 7));
+          ldsm4(a1, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + 2 + kc) & 7));
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t a[4], b[4];
-          ldsm4(a, sbase + C::OFF_Q + (k >> 2) * C::QREGION + sw128_offset(qr, (2 * k + qc) & 7));
-          ldsm4(b, ks + (k >> 2) * C::REGION + sw128_offset(kr, (2 * k + kc) & 7));
-          mma16816<C::BF16>(k & 1 ? s2[0] : s[0], a, b[0], b[1]);
-          mma16816<C::BF16>(k & 1 ? s2[1] : s[1], a, b[2], b[3]);
+          for (int nt = 0; nt < C::NT; ++nt) {
+            if (nt >= groups) continue;
+            uint32_t b[4];
+            if constexpr (C::QREG) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] = qf[nt][k2][e];
+            } else {
+              query_frag(b, nt, k2);
+            }
+            mma16816<C::BF16>(s[nt], a0, b[0], b[1]);
+            mma16816<C::BF16>(C::NT == 1 ? s2 : s[nt], a1, b[2], b[3]);
+          }
         }
+        if constexpr (C::NT == 1) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][e] += s2[i][e];
-        // element e of tile i: row r0 + 8 (e / 2), key j0 + 8 i + 2 (lane % 4) + e % 2
+          for (int e = 0; e < 4; ++e) s[0][e] += s2[e];
+        }
         uint32_t keep0 = ~0u, keep1 = ~0u;  // keys of this thread's V fragments that some row sees
-        const int jt = j0 + 2 * (lane & 3);
+        const int jv = j0 + 2 * (lane & 3);
         if (all) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[i][e] *= p.scale_log2;
+            for (int e = 0; e < 4; ++e) s[nt][e] *= p.scale_log2;
         } else {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = jt + 8 * i + (e & 1), pos = p_lo + (e < 2 ? tok0 : tok1);
+              const int j = j0 + (lane >> 2) + 8 * (e >> 1), pos = p_lo + token(nt, e & 1);
               const bool see = j < len && !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
-              s[i][e] = see ? s[i][e] * p.scale_log2 : -INFINITY;
+              s[nt][e] = see ? s[nt][e] * p.scale_log2 : -INFINITY;
             }
           auto seen = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window); };
-          keep0 = (seen(jt) ? 0xffffu : 0u) | (seen(jt + 1) ? 0xffff0000u : 0u);
-          keep1 = (seen(jt + 8) ? 0xffffu : 0u) | (seen(jt + 9) ? 0xffff0000u : 0u);
+          keep0 = (seen(jv) ? 0xffffu : 0u) | (seen(jv + 1) ? 0xffff0000u : 0u);
+          keep1 = (seen(jv + 8) ? 0xffffu : 0u) | (seen(jv + 9) ? 0xffff0000u : 0u);
         }
-        // running maximum and sum of this warp's keys
-        uint32_t pa[4];
-        {
-          float mn[2], alpha[2];
+        // running maxima of this warp's keys: looked at across lanes only when some
+        // score is above its row's by more than the slack
+        bool above = false;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            mn[h] = fmaxf(m[h], x);
-            alpha[h] = exp2_rel(m[h], mn[h]);
-          }
-          if (__any_sync(0xffffffffu, mn[0] != m[0] || mn[1] != m[1])) {
+        for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              acc[i][0] *= alpha[0];
-              acc[i][1] *= alpha[0];
-              acc[i][2] *= alpha[1];
-              acc[i][3] *= alpha[1];
+          for (int e = 0; e < 4; ++e) above |= s[nt][e] > m[nt][e & 1] + kPagedSlack;
+        if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+          for (int nt = 0; nt < C::NT; ++nt) {
+            if (nt >= groups) continue;
+            float alpha[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float x = fmaxf(s[nt][h], s[nt][2 + h]);
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              const float mn = fmaxf(m[nt][h], x);
+              alpha[h] = exp2_rel(m[nt][h], mn);
+              m[nt][h] = mn;
+              l[nt][h] *= alpha[h];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              acc[nt][i][0] *= alpha[0];
+              acc[nt][i][1] *= alpha[1];
+              acc[nt][i][2] *= alpha[0];
+              acc[nt][i][3] *= alpha[1];
             }
           }
+        }
+        // weights, rounded to the cache's type for the product with V (the sums keep
+        // them in fp32), and transposed into B fragments
+        uint32_t pb[C::NT][2];
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            m[h] = mn[h];
-            const float ref = mn[h] == -INFINITY ? 0.f : mn[h];
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                s[i][2 * h + e] = ex2(s[i][2 * h + e] - ref);
-                sum += s[i][2 * h + e];
-              }
-            l[h] = l[h] * alpha[h] + sum;
+            const float ref = m[nt][h] == -INFINITY ? 0.f : m[nt][h];
+            s[nt][h] = ex2(s[nt][h] - ref);
+            s[nt][2 + h] = ex2(s[nt][2 + h] - ref);
+            l[nt][h] += s[nt][h] + s[nt][2 + h];
           }
-          // weights rounded to the cache's type for the product with V (the
-          // sum above keeps them in fp32)
-          pa[0] = pack2<C::BF16>(s[0][0], s[0][1]);
-          pa[1] = pack2<C::BF16>(s[0][2], s[0][3]);
-          pa[2] = pack2<C::BF16>(s[1][0], s[1][1]);
-          pa[3] = pack2<C::BF16>(s[1][2], s[1][3]);
+          pb[nt][0] = transpose8(pack2<C::BF16>(s[nt][0], s[nt][1]));
+          pb[nt][1] = transpose8(pack2<C::BF16>(s[nt][2], s[nt][3]));
         }
-        // O += P V. A key hidden from every row gets V = 0 (its slot may hold
-        // anything; 0 * NaN would not be 0). Where rows differ in what they
-        // see, each token's product is taken with the keys it sees and only
-        // its rows are kept.
-        const int vr = kw * 16 + (lane & 15), vc = lane >> 4;
+        // O^T += V^T P^T. A key hidden from every row gets V = 0 (its slot may hold
+        // anything; 0 * NaN would not be 0). Where rows differ in what they see and
+        // some of these values are no finite numbers, each token's product is
+        // taken with the keys it sees and only its rows are kept.
+        const int vr = kw * 16 + ((lane >> 4) << 3) + (lane & 7), vc = (lane >> 3) & 1;
         const bool differ = !all && n > 1 &&
                             ((p.causal && j0 + 15 > p_lo && j0 <= p_hi) ||
                              (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
-        if (!differ) {
+        bool apart = false;
+        if (differ) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            uint32_t b[4];
-            ldsm4_trans(b, vs + (i >> 2) * C::REGION + sw128_offset(vr, (2 * i + vc) & 7));
-            mma16816<C::BF16>(acc[2 * i], pa, b[0] & keep0, b[1] & keep1);
-            mma16816<C::BF16>(acc[2 * i + 1], pa, b[2] & keep0, b[3] & keep1);
+            uint32_t a[4];
+            ldsm4_trans(a, vs + (i >> 2) * C::REGION + sw128_offset(vr, (2 * i + vc) & 7));
+            apart |= not_finite2<C::BF16>(a[0] & keep0) | not_finite2<C::BF16>(a[1] & keep0) |
+                     not_finite2<C::BF16>(a[2] & keep1) | not_finite2<C::BF16>(a[3] & keep1);
+          }
+          apart = __any_sync(0xffffffffu, apart);
+        }
+        if (!apart) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t a[4];
+            ldsm4_trans(a, vs + (i >> 2) * C::REGION + sw128_offset(vr, (2 * i + vc) & 7));
+            a[0] &= keep0;
+            a[1] &= keep0;
+            a[2] &= keep1;
+            a[3] &= keep1;
+#pragma unroll
+            for (int nt = 0; nt < C::NT; ++nt)
+              if (nt < groups) mma16816<C::BF16>(acc[nt][i], a, pb[nt][0], pb[nt][1]);
           }
         } else {
+#pragma unroll 1
           for (int tok = 0; tok < n; ++tok) {
             const int pos = p_lo + tok;
             auto seen = [&](int j) {
               return j < len && !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
             };
-            const uint32_t k0 = (seen(jt) ? 0xffffu : 0u) | (seen(jt + 1) ? 0xffff0000u : 0u);
-            const uint32_t k1 = (seen(jt + 8) ? 0xffffu : 0u) | (seen(jt + 9) ? 0xffff0000u : 0u);
+            const uint32_t k0 = (seen(jv) ? 0xffffu : 0u) | (seen(jv + 1) ? 0xffff0000u : 0u);
+            const uint32_t k1 = (seen(jv + 8) ? 0xffffu : 0u) | (seen(jv + 9) ? 0xffff0000u : 0u);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-              uint32_t b[4];
-              ldsm4_trans(b, vs + (i >> 2) * C::REGION + sw128_offset(vr, (2 * i + vc) & 7));
+              uint32_t a[4];
+              ldsm4_trans(a, vs + (i >> 2) * C::REGION + sw128_offset(vr, (2 * i + vc) & 7));
+              a[0] &= k0;
+              a[1] &= k0;
+              a[2] &= k1;
+              a[3] &= k1;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float x[4] = {acc[2 * i + h][0], acc[2 * i + h][1], acc[2 * i + h][2], acc[2 * i + h][3]};
-                mma16816<C::BF16>(x, pa, b[2 * h] & k0, b[2 * h + 1] & k1);
-                if (tok0 == tok) acc[2 * i + h][0] = x[0], acc[2 * i + h][1] = x[1];
-                if (tok1 == tok) acc[2 * i + h][2] = x[2], acc[2 * i + h][3] = x[3];
+              for (int nt = 0; nt < C::NT; ++nt) {
+                if (nt >= groups) continue;
+                float x[4] = {acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]};
+                mma16816<C::BF16>(x, a, pb[nt][0], pb[nt][1]);
+                if (token(nt, 0) == tok) acc[nt][i][0] = x[0], acc[nt][i][2] = x[2];
+                if (token(nt, 1) == tok) acc[nt][i][1] = x[1], acc[nt][i][3] = x[3];
               }
             }
           }
@@ -597,19 +676,22 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
     }
 
-    // merge the key warps: common maximum, then each quarter of the columns is
-    // summed by the warps in turn (warp q, q - 1, q - 2, q - 3 for quarter q)
+    // merge the key warps
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      // padding rows (tokens the sequence does not have) see nothing
-      if ((h ? tok1 : tok0) >= n) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
+    for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float& x = l[nt][h];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        // padding rows (tokens the sequence does not have) see nothing
+        if (token(nt, h) >= n) {
+          m[nt][h] = -INFINITY;
+          x = 0.f;
+        }
+        if (lane < 4) mls[kw * C::ROWS + col0 + 8 * nt + h] = make_float2(m[nt][h], x);
       }
-      if ((lane & 3) == 0) mls[kw * C::ROWS + r0 + 8 * h] = make_float2(m[h], l[h]);
-    }
     sync_rows();  // and nobody reads stages any more
     if constexpr (C::CLUSTER) {
       // The warps' rows side by side; a thread adds up the four of an 8-column
@@ -617,11 +699,12 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       // that owns the piece (i mod ranks), which joins what all CTAs sent.
       float* wm = reinterpret_cast<float*>(smem);  // [KW][ROWS][OP]
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(wm + (kw * C::ROWS + r0 + 8 * h) * C::OP + 8 * i + 2 * (lane & 3)) =
-              make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            wm[(kw * C::ROWS + col0 + 8 * nt + (e & 1)) * C::OP + 16 * i + (lane >> 2) + 8 * (e >> 1)] = acc[nt][i][e];
       sync_rows();
       const int pieces = rows * (D / 8), share_of = C::ROWS * (D / 8) / ranks;
       float2* pml = reinterpret_cast<float2*>(smem + C::OFF_PML);  // [ranks][share_of]
@@ -679,35 +762,34 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       return;
     }
-    float f[2];
+    // a common maximum, then each quarter of the columns is summed by the warps in
+    // turn (warp q, q - 1, q - 2, q - 3 for quarter q)
+    float f[C::NT][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float mt = -INFINITY;
+    for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < C::KW; ++k) mt = fmaxf(mt, mls[k * C::ROWS + r0 + 8 * h].x);
-      f[h] = exp2_rel(m[h], mt);
-    }
+      for (int h = 0; h < 2; ++h) {
+        float mt = -INFINITY;
 #pragma unroll
+        for (int k = 0; k < C::KW; ++k) mt = fmaxf(mt, mls[k * C::ROWS + col0 + 8 * nt + h].x);
+        f[nt][h] = exp2_rel(m[nt][h], mt);
+      }
+    constexpr int QUARTER = (D / 16 + C::KW - 1) / C::KW;
+#pragma unroll 1
     for (int round = 0; round < C::KW; ++round) {
       const int quarter = (kw + round) % C::KW;
 #pragma unroll
-      for (int qq = 0; qq < C::KW; ++qq) {
-        if (qq != quarter) continue;
+      for (int i = 0; i < D / 16; ++i) {
+        if (i / QUARTER != quarter) continue;
 #pragma unroll
-        for (int i = qq * (D / 32); i < (qq + 1) * (D / 32); ++i) {
+        for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float2* at = reinterpret_cast<float2*>(om + (r0 + 8 * h) * C::OP + 8 * i + 2 * (lane & 3));
-            float2 x = make_float2(acc[i][2 * h] * f[h], acc[i][2 * h + 1] * f[h]);
-            if (m[h] == -INFINITY) x = make_float2(0.f, 0.f);  // nothing seen: not even 0 * inf
-            if (round > 0) {
-              const float2 y = *at;
-              x.x += y.x;
-              x.y += y.y;
-            }
-            *at = x;
+          for (int e = 0; e < 4; ++e) {
+            float* at = om + (col0 + 8 * nt + (e & 1)) * C::OP + 16 * i + (lane >> 2) + 8 * (e >> 1);
+            // nothing seen: not even 0 * inf
+            const float x = m[nt][e & 1] == -INFINITY ? 0.f : acc[nt][i][e] * f[nt][e & 1];
+            *at = round > 0 ? *at + x : x;
           }
-        }
       }
       sync_rows();
     }
@@ -740,6 +822,22 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                                 static_cast<int>(last), rows);
     }
     sync_rows();
+  }
+  if constexpr (!C::CLUSTER) {
+    // units without tiles: nothing is visible to any of their rows
+    const int mult = item_mult(p);
+    const int64_t units = static_cast<int64_t>(item_count(p)) * mult;
+    for (int64_t u = part; u < units; u += parts) {
+      const int item = static_cast<int>(u / mult), sub = static_cast<int>(u - static_cast<int64_t>(item) * mult);
+      const Item it = load_item(p, item);
+      if (it.tiles > 0) continue;
+      const int g = p.sel ? item % c.Hkv : sub / p.row_blocks, rb = sub % p.row_blocks;
+      const int64_t row0 = block_row0(p, it.b, g, rb, C::ROWS);
+      const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
+      for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS)
+        reinterpret_cast<uint4*>(p.o + row0 * D)[i] = make_uint4(0, 0, 0, 0);
+      for (int i = tid; i < rows; i += 32 * C::WARPS) p.lse[row0 + i] = -INFINITY;
+    }
   }
 }
 
@@ -859,12 +957,14 @@ cudaError_t launch_paged(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t grid,
   auto kern = fa_paged_fwd_kernel<C>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
+  if (!register_split_fits(reinterpret_cast<const void*>(kern), C::THREADS, C::REG_NEEDED))
+    return cudaErrorInvalidConfiguration;
   return launch_kernel(kern, grid, C::THREADS, C::SMEM_BYTES, a.stream, static_cast<unsigned>(ranks), mk, mv, p, ranks);
 }
 
-template <int D, int RW, bool BF16>
+template <int D, int NT, int RW, bool BF16>
 cudaError_t run_paged(const PagedFwdLaunch& a) {
-  using C = PagedCfg<D, RW, BF16, false>;
+  using C = PagedCfg<D, NT, RW, BF16, false>;
   PagedFwdArgs p;
   p.c = a.c;
   p.q = a.q; p.o = a.o; p.lse = a.lse;
@@ -888,7 +988,7 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   int ranks = 1;
   while (ranks < kPagedMaxRanks && ranks < tiles) ranks *= 2;
   if (tiles <= kPagedClusterTiles * ranks && units * ranks <= wave)
-    return launch_paged<PagedCfg<D, RW, BF16, true>>(a, p, units * ranks, ranks);
+    return launch_paged<PagedCfg<D, NT, RW, BF16, true>>(a, p, units * ranks, ranks);
   // no more CTAs than the longest possible list has tiles
   const int64_t parts = std::min(wave, units * tiles);
   const cudaError_t e = launch_paged<C>(a, p, parts, 1);
@@ -905,10 +1005,11 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
 template <int D, bool BF16>
 cudaError_t run_paged_rows(const PagedFwdLaunch& a) {
   switch (paged_block_rows(a.Hq / a.c.Hkv * a.Tq, D)) {
-    case 16: return run_paged<D, 1, BF16>(a);
-    case 32: return run_paged<D, 2, BF16>(a);
+    case 8: return run_paged<D, 1, 1, BF16>(a);
+    case 16: return run_paged<D, 2, 1, BF16>(a);
+    case 32: return run_paged<D, 2, 2, BF16>(a);
   }
-  if constexpr (D < 256) return run_paged<D, 4, BF16>(a);
+  if constexpr (D < 256) return run_paged<D, 2, 4, BF16>(a);
   return cudaErrorInvalidValue;
 }
 

@@ -61,10 +61,12 @@ cudaError_t launch_paged_fwd_d256(const PagedFwdLaunch& a);
 // CTAs of the attention kernel that can leave parts of units to be joined.
 constexpr int kPagedMaxParts = 608;
 
-// Query rows of a block: 16 (usual decoding), 32 or 64 where a KV head has more,
-// so that its keys are loaded once for all of them (D = 256: at most 32, what
-// shared memory holds).
-inline int paged_block_rows(int rows, int D) { return rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64; }
+// Query rows of a block: 8 (usual decoding), 16, 32 or 64 where a KV head has
+// more, so that its keys are loaded once for all of them (D = 256: at most 32,
+// what registers hold).
+inline int paged_block_rows(int rows, int D) {
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64;
+}
 
 // Device workspace of launch_paged_fwd_d* in bytes: per CTA two parts of a
 // block (fp32 rows, maximum and sum) and a record of what is to be joined.
