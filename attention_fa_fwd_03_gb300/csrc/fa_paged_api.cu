@@ -179,6 +179,11 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
   if (!q || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
   if ((sel == nullptr) != (sel_lens == nullptr)) return FA_ERR_INVALID_ARG;
   if (sel && (n_sel < 1 || n_sel > kMaxSelected)) return FA_ERR_INVALID_ARG;
+  // tiles are counted in 32 bits
+  const int block = paged_block_rows(Hq / kv->Hkv * Tq, kv->D);
+  const int64_t all_units = static_cast<int64_t>(kv->B) * kv->Hkv * ((Hq / kv->Hkv * Tq + block - 1) / block);
+  if (paged_tiles(all_units, static_cast<int64_t>(sel ? n_sel : kv->max_pages) * kv->page_size) > INT32_MAX)
+    return FA_ERR_INVALID_ARG;
   const size_t need = fa_paged_workspace_size(Hq, kv->Hkv, Tq, kv->D);
   if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(workspace) ||

@@ -39,7 +39,6 @@
 
 namespace fa {
 
-constexpr int kPagedTile = 64;       // keys of a tile
 constexpr int kPagedKeyWarps = 4;    // warps that share a tile's keys, 16 each
 constexpr int kPagedMaxRanks = 8;    // CTAs of a cluster
 constexpr int kPagedClusterTiles = 8;  // tiles per CTA up to which clusters are used
@@ -74,17 +73,17 @@ struct PagedCfg {
   static constexpr int WARPS = KW * RW;              // consumer warps
   // One producer warp beside them; where accumulators need more registers than an
   // equal split leaves, a warpgroup of producers (one works) that gives its own up.
-  static constexpr bool SPLIT = NT * RW * D >= 1024;
+  static constexpr bool SPLIT = RW > 1 && NT * D >= 384;
   static constexpr int THREADS = 32 * (WARPS + (SPLIT ? 4 : 1));
-  static constexpr int REG_PRODUCER = 24, REG_CONSUMER = RW == 4 ? 112 : 224;
+  static constexpr int REG_PRODUCER = 40, REG_CONSUMER = 224;
   static constexpr int REG_NEEDED = SPLIT ? 128 * REG_PRODUCER + 32 * WARPS * REG_CONSUMER : 0;
   static constexpr int KREG = (D + 63) / 64;         // 64-column regions of a row
   static constexpr int REGION = kPagedTile * 128;
   static constexpr int TILE = KREG * REGION;         // K (or V) rows of a stage
   // Up to 16 rows two CTAs (D = 64: three) share an SM with about 100 KB in flight
   // each; with more rows, or 64 KB stages, one does.
-  static constexpr int CTAS = D == 256 || (RW > 1 && D > 64) || RW > 2 ? 1 : D == 64 && RW == 1 ? 3 : 2;
-  static constexpr int STAGES = D == 256 ? (RW == 1 ? 3 : 2) : CTAS == 1 ? (D == 64 ? 8 : 5) : D == 64 ? (CTAS == 3 ? 4 : 5) : 3;
+  static constexpr int CTAS = D == 256 || RW > 1 ? 1 : D == 64 ? 3 : 2;
+  static constexpr int STAGES = D == 256 ? (RW == 1 ? 3 : 2) : D == 64 ? (RW == 1 ? 4 : 8) : (RW == 1 ? 3 : 5);
   // Queries as B fragments in registers where they fit, else read again each tile
   static constexpr bool QREG = NT * D <= (CTAS == 1 && RW == 1 ? 256 : 128);
   static constexpr int QREGION = ROWS * 128;
@@ -104,6 +103,9 @@ struct PagedCfg {
 // Running maxima may be behind by this much (in the exp2 domain) before the sums
 // are rescaled: weights then reach 2^8 instead of 1, which costs no precision.
 constexpr float kPagedSlack = 8.f;
+// Running maximum of a row that has seen no key: finite, so that a hidden score of
+// -inf less it is -inf, and so low that any score raises it.
+constexpr float kNoMax = -3e38f;
 
 // ----------------------------------------------------------------- the list
 // An item is a sequence (every KV head and row block of it has the same tiles)
@@ -137,48 +139,55 @@ __device__ __forceinline__ Item load_item(const PagedFwdArgs& p, int i) {
   return it;
 }
 
-// One CTA's share of the list, found by all its threads.
+// One CTA's share of the list, found by all its threads: `total` tiles in equal
+// runs, the first total % parts of them one longer. (The host has checked that the
+// longest possible list stays below 2^31 tiles.)
 struct Share {
-  long long total, lo, hi;
-  int parts;       // CTAs with a share: every one of them has a tile
-  int item;        // where lo falls
-  long long rest;  // tiles of that item before lo
+  int parts;      // CTAs with a share: every one of them has a tile
+  int base, more; // tiles of a share, and how many have one more
+  int lo, hi;
+  int item, rest; // where lo falls: item, and tiles of it before lo
+  // CTA whose share holds tile x of the list
+  __device__ __forceinline__ int part_of(int x) const {
+    const int longer = more * (base + 1);
+    return x < longer ? x / (base + 1) : more + (x - longer) / base;
+  }
 };
 template <int THREADS>
 __device__ __forceinline__ Share find_share(const PagedFwdArgs& p, int part, int parts) {
-  __shared__ long long sums[THREADS / 32];
-  __shared__ long long found_rest;
-  __shared__ int found_item;
+  __shared__ int sums[THREADS / 32];
+  __shared__ int found_rest, found_item;
   const int items = item_count(p), mult = item_mult(p);
   const int per = (items + THREADS - 1) / THREADS;
-  const int i0 = threadIdx.x * per, i1 = min(items, i0 + per);
+  const int i0 = min(items, static_cast<int>(threadIdx.x) * per), i1 = min(items, i0 + per);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += static_cast<long long>(load_item(p, i).tiles) * mult;
-  long long incl = mine;
+  int mine = 0;
+  for (int i = i0; i < i1; ++i) mine += load_item(p, i).tiles * mult;
+  int incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+    const int x = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += x;
   }
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  long long before = incl - mine, total = 0;
+  int before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += sums[w];
     total += sums[w];
   }
   Share s;
-  s.total = total;
-  s.parts = static_cast<int>(min(total, static_cast<long long>(parts)));
-  s.lo = part < s.parts ? total * part / s.parts : total;
-  s.hi = part < s.parts ? total * (part + 1) / s.parts : total;
+  s.parts = min(total, parts);
+  s.base = total / parts;
+  s.more = total - s.base * parts;
+  s.lo = part * s.base + min(part, s.more);
+  s.hi = s.lo + s.base + (part < s.more ? 1 : 0);
   if (s.lo >= before && s.lo < before + mine) {
-    long long rest = s.lo - before;
+    int rest = s.lo - before;
     int i = i0;
     for (; i < i1 - 1; ++i) {
-      const long long n = static_cast<long long>(load_item(p, i).tiles) * mult;
+      const int n = load_item(p, i).tiles * mult;
       if (rest < n) break;
       rest -= n;
     }
@@ -195,8 +204,7 @@ __device__ __forceinline__ Share find_share(const PagedFwdArgs& p, int part, int
 struct Walk {
   Item it;
   int item, sub, mult, items;
-  int t0, t1;
-  long long left;
+  int t0, t1, left;
   __device__ __forceinline__ bool start(const PagedFwdArgs& p, const Share& s) {
     left = s.hi - s.lo;
     if (left <= 0) return false;
@@ -207,9 +215,9 @@ struct Walk {
     // tiles and sub are in range unless the lengths change under the call,
     // which must not lead out of the buffers either
     const int tiles = max(it.tiles, 1);
-    sub = static_cast<int>(min(s.rest / tiles, static_cast<long long>(mult - 1)));
-    t0 = static_cast<int>(min(s.rest - static_cast<long long>(sub) * tiles, static_cast<long long>(tiles - 1)));
-    t1 = static_cast<int>(min(static_cast<long long>(it.tiles), t0 + left));
+    sub = min(s.rest / tiles, mult - 1);
+    t0 = min(s.rest - sub * tiles, tiles - 1);
+    t1 = min(it.tiles, t0 + left);
     return true;
   }
   // The slice of rank `rank` of the `ranks` CTAs that share unit `unit`; false
@@ -220,8 +228,9 @@ struct Walk {
     item = unit / mult;
     sub = unit - item * mult;
     it = load_item(p, item);
-    t0 = static_cast<int>(static_cast<long long>(it.tiles) * rank / ranks);
-    t1 = static_cast<int>(static_cast<long long>(it.tiles) * (rank + 1) / ranks);
+    const int base = it.tiles / ranks, more = it.tiles - base * ranks;
+    t0 = rank * base + min(rank, more);
+    t1 = t0 + base + (rank < more ? 1 : 0);
     left = t1 - t0;
     return left > 0;
   }
@@ -236,7 +245,7 @@ struct Walk {
       } while (it.tiles == 0);
     }
     t0 = 0;
-    t1 = static_cast<int>(min(static_cast<long long>(it.tiles), left));
+    t1 = min(it.tiles, left);
     return true;
   }
   __device__ __forceinline__ int kv_head(const PagedFwdArgs& p) const {
@@ -458,7 +467,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     stage_queries(static_cast<int64_t>(unit / p.row_blocks) * p.rows + rb * C::ROWS, min(C::ROWS, p.rows - rb * C::ROWS));
   }
 
-  int consumed = 0;
+  int slot = 0;
+  uint32_t phase = 0;
   bool ok = true;
   // (with clusters: one segment, which may be empty)
   for (bool more = C::CLUSTER ? w.start_slice(p, unit, rank, ranks) || true : w.start(p, share); more;
@@ -470,10 +480,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int p_lo = len - n, p_hi = len - 1;  // positions of the new tokens
     if constexpr (!C::CLUSTER) stage_queries(row0, rows);
     sync_rows();
+    // this thread's columns are rows 2 (lane % 4) and the next of each group of 8
+    const int group0 = rw * C::NT, col0 = group0 * 8 + 2 * (lane & 3);
+    const bool has_rows = group0 * 8 < rows;
     // B fragments of the queries: two products' worth per 8 rows and 32 columns
     const uint32_t qs = sbase + C::OFF_Q;
     auto query_frag = [&](uint32_t (&f)[4], int nt, int k2) {
-      const int row = (rw * C::NT + nt) * 8 + (lane & 7), ch = 4 * k2 + (lane >> 3);
+      const int row = (group0 + nt) * 8 + (lane & 7), ch = 4 * k2 + (lane >> 3);
       ldsm4(f, qs + (ch >> 3) * C::QREGION + sw128_offset(row, ch & 7));
     };
     uint32_t qf[C::QREG ? C::NT : 1][C::QREG ? D / 32 : 1][4];
@@ -483,14 +496,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) query_frag(qf[nt][k2], nt, k2);
     }
-    // groups of 8 rows of this warp that hold any; this thread's columns are rows
-    // 2 (lane % 4) and the next of each group
-    const int groups = min(C::NT, max(0, (rows - rw * C::NT * 8 + 7) / 8));
-    const int col0 = rw * C::NT * 8 + 2 * (lane & 3);
     float m[C::NT][2], l[C::NT][2], acc[C::NT][D / 16][4];
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kNoMax;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
@@ -504,22 +513,19 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         tokens |= static_cast<uint64_t>((rb * C::ROWS + col0 + 8 * nt + e) % p.Tq) << (8 * nt + 4 * e);
     auto token = [&](int nt, int e) { return static_cast<int>(tokens >> (8 * nt + 4 * e)) & 15; };
 
-    for (int t = w.t0; t < w.t1; ++t, ++consumed) {
-      const int slot = consumed % C::STAGES;
-      ok = ok && mbar_wait(smem_u32(&full[slot]), (consumed / C::STAGES) & 1, tmo, &abort_flag, p.wc.status);
+    for (int t = w.t0; t < w.t1; ++t) {
+      ok = ok && mbar_wait(smem_u32(&full[slot]), phase, tmo, &abort_flag, p.wc.status);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) continue;
+      if (!ok) break;
       const int j0 = key_pos[slot][kw];
       const uint32_t ks = sbase + C::OFF_KV + slot * 2 * C::TILE, vs = ks + C::TILE;
       // does any row see any of the 16 keys; do all rows see all of them
-      const bool some = groups > 0 && j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window);
+      const bool some = has_rows && j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window);
       if (some) {
         const bool all = j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) && !(p.window > 0 && j0 <= p_hi - p.window);
         // S^T = K Q^T: element e of group nt is key j0 + lane / 4 + 8 (e / 2), row
         // col0 + 8 nt + e % 2. One group: two accumulators, half as long a chain.
-        float s[C::NT][4], s2[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int nt = 0; nt < C::NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        float s[C::NT][4], s2[4];
         const int kr = kw * 16 + (lane & 15), kc = lane >> 4;
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) {
@@ -528,7 +534,6 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           ldsm4(a1, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + 2 + kc) & 7));
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt) {
-            if (nt >= groups) continue;
             uint32_t b[4];
             if constexpr (C::QREG) {
 #pragma unroll
@@ -536,8 +541,14 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             } else {
               query_frag(b, nt, k2);
             }
-            mma16816<C::BF16>(s[nt], a0, b[0], b[1]);
-            mma16816<C::BF16>(C::NT == 1 ? s2 : s[nt], a1, b[2], b[3]);
+            if (k2 == 0)
+              mma16816_first<C::BF16>(s[nt], a0, b[0], b[1]);
+            else
+              mma16816<C::BF16>(s[nt], a0, b[0], b[1]);
+            if (C::NT == 1 && k2 == 0)
+              mma16816_first<C::BF16>(s2, a1, b[2], b[3]);
+            else
+              mma16816<C::BF16>(C::NT == 1 ? s2 : s[nt], a1, b[2], b[3]);
           }
         }
         if constexpr (C::NT == 1) {
@@ -546,44 +557,43 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         }
         uint32_t keep0 = ~0u, keep1 = ~0u;  // keys of this thread's V fragments that some row sees
         const int jv = j0 + 2 * (lane & 3);
-        if (all) {
-#pragma unroll
-          for (int nt = 0; nt < C::NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] *= p.scale_log2;
-        } else {
+        if (!all) {
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int j = j0 + (lane >> 2) + 8 * (e >> 1), pos = p_lo + token(nt, e & 1);
               const bool see = j < len && !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
-              s[nt][e] = see ? s[nt][e] * p.scale_log2 : -INFINITY;
+              if (!see) s[nt][e] = -INFINITY;
             }
           auto seen = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window); };
           keep0 = (seen(jv) ? 0xffffu : 0u) | (seen(jv + 1) ? 0xffff0000u : 0u);
           keep1 = (seen(jv + 8) ? 0xffffu : 0u) | (seen(jv + 9) ? 0xffff0000u : 0u);
         }
-        // running maxima of this warp's keys: looked at across lanes only when some
-        // score is above its row's by more than the slack
+        // Exponents against the running maxima of this warp's keys, which are looked
+        // at across lanes only when some exponent is above the slack.
+        float x[C::NT][4];
         bool above = false;
 #pragma unroll
-        for (int nt = 0; nt < C::NT; ++nt)
+        for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) above |= s[nt][e] > m[nt][e & 1] + kPagedSlack;
+          for (int e = 0; e < 4; ++e) {
+            x[nt][e] = fmaf(s[nt][e], p.scale_log2, -m[nt][e & 1]);
+            above |= x[nt][e] > kPagedSlack;
+          }
+        }
         if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt) {
-            if (nt >= groups) continue;
             float alpha[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float x = fmaxf(s[nt][h], s[nt][2 + h]);
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              const float mn = fmaxf(m[nt][h], x);
-              alpha[h] = exp2_rel(m[nt][h], mn);
+              float y = fmaxf(s[nt][h], s[nt][2 + h]);
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+              const float mn = fmaxf(m[nt][h], y * p.scale_log2);
+              alpha[h] = ex2(m[nt][h] - mn);
               m[nt][h] = mn;
               l[nt][h] *= alpha[h];
             }
@@ -594,6 +604,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               acc[nt][i][2] *= alpha[0];
               acc[nt][i][3] *= alpha[1];
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], p.scale_log2, -m[nt][e & 1]);
           }
         }
         // weights, rounded to the cache's type for the product with V (the sums keep
@@ -603,9 +615,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float ref = m[nt][h] == -INFINITY ? 0.f : m[nt][h];
-            s[nt][h] = ex2(s[nt][h] - ref);
-            s[nt][2 + h] = ex2(s[nt][2 + h] - ref);
+            s[nt][h] = ex2(x[nt][h]);
+            s[nt][2 + h] = ex2(x[nt][2 + h]);
             l[nt][h] += s[nt][h] + s[nt][2 + h];
           }
           pb[nt][0] = transpose8(pack2<C::BF16>(s[nt][0], s[nt][1]));
@@ -641,7 +652,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             a[3] &= keep1;
 #pragma unroll
             for (int nt = 0; nt < C::NT; ++nt)
-              if (nt < groups) mma16816<C::BF16>(acc[nt][i], a, pb[nt][0], pb[nt][1]);
+              mma16816<C::BF16>(acc[nt][i], a, pb[nt][0], pb[nt][1]);
           }
         } else {
 #pragma unroll 1
@@ -662,7 +673,6 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               a[3] &= k1;
 #pragma unroll
               for (int nt = 0; nt < C::NT; ++nt) {
-                if (nt >= groups) continue;
                 float x[4] = {acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]};
                 mma16816<C::BF16>(x, a, pb[nt][0], pb[nt][1]);
                 if (token(nt, 0) == tok) acc[nt][i][0] = x[0], acc[nt][i][2] = x[2];
@@ -674,6 +684,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+      if (++slot == C::STAGES) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
 
     // merge the key warps
@@ -686,7 +700,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         // padding rows (tokens the sequence does not have) see nothing
-        if (token(nt, h) >= n) {
+        if (token(nt, h) >= n || m[nt][h] == kNoMax) {
           m[nt][h] = -INFINITY;
           x = 0.f;
         }
@@ -704,7 +718,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            wm[(kw * C::ROWS + col0 + 8 * nt + (e & 1)) * C::OP + 16 * i + (lane >> 2) + 8 * (e >> 1)] = acc[nt][i][e];
+            wm[(kw * C::ROWS + col0 + 8 * nt + (e & 1)) * C::OP + 16 * i + (lane >> 2) + 8 * (e >> 1)] =
+                  acc[nt][i][e];
       sync_rows();
       const int pieces = rows * (D / 8), share_of = C::ROWS * (D / 8) / ranks;
       float2* pml = reinterpret_cast<float2*>(smem + C::OFF_PML);  // [ranks][share_of]
@@ -813,13 +828,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
     }
     if (tid == 0 && begins && !ends) {
-      // the unit ends at tile `end` of the list: its last part is the CTA whose share holds end - 1
-      const long long end = share.hi - w.t1 + w.it.tiles;
-      long long last = (end * share.parts - 1) / share.total;
-      while (share.total * last / share.parts >= end) --last;
-      while (last < share.parts - 1 && share.total * (last + 1) / share.parts < end) ++last;
+      // the unit goes on to tile share.hi - t1 + tiles of the list
+      const int last = min(share.part_of(share.hi - w.t1 + w.it.tiles - 1), share.parts - 1);
       p.joins[part] = make_int4(static_cast<int>(row0 >> 31), static_cast<int>(row0 & 0x7fffffff),
-                                static_cast<int>(last), rows);
+                                last, rows);
     }
     sync_rows();
   }
@@ -981,7 +993,7 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   p.wc = a.wc;
   // tiles of the longest list a unit can have
   const int64_t keys = (a.sel ? static_cast<int64_t>(a.n_sel) : a.c.max_pages) << a.c.page_shift;
-  const int64_t tiles = (keys + kPagedTile - 1) / kPagedTile;
+  const int64_t tiles = paged_tiles(1, keys);
   const int64_t units = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks;
   const int64_t wave = std::min<int64_t>(static_cast<int64_t>(device_sm_count()) * C::CTAS, kPagedMaxParts);
   // Few short units: a cluster each, joined in the same launch.
@@ -1008,8 +1020,12 @@ cudaError_t run_paged_rows(const PagedFwdLaunch& a) {
     case 8: return run_paged<D, 1, 1, BF16>(a);
     case 16: return run_paged<D, 2, 1, BF16>(a);
     case 32: return run_paged<D, 2, 2, BF16>(a);
+    case 48:
+      if constexpr (D < 256) return run_paged<D, 3, 2, BF16>(a);
+      break;
+    default:
+      if constexpr (D < 256) return run_paged<D, 4, 2, BF16>(a);
   }
-  if constexpr (D < 256) return run_paged<D, 2, 4, BF16>(a);
   return cudaErrorInvalidValue;
 }
 

@@ -61,12 +61,16 @@ cudaError_t launch_paged_fwd_d256(const PagedFwdLaunch& a);
 // CTAs of the attention kernel that can leave parts of units to be joined.
 constexpr int kPagedMaxParts = 608;
 
-// Query rows of a block: 8 (usual decoding), 16, 32 or 64 where a KV head has
+// Query rows of a block: 8 (usual decoding), 16, 32, 48 or 64 where a KV head has
 // more, so that its keys are loaded once for all of them (D = 256: at most 32,
 // what registers hold).
 inline int paged_block_rows(int rows, int D) {
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : rows <= 48 ? 48 : 64;
 }
+
+// Keys of a tile, and the most tiles a call may have (32-bit counts on the device).
+constexpr int kPagedTile = 64;
+inline int64_t paged_tiles(int64_t units, int64_t keys) { return units * ((keys + kPagedTile - 1) / kPagedTile); }
 
 // Device workspace of launch_paged_fwd_d* in bytes: per CTA two parts of a
 // block (fp32 rows, maximum and sum) and a record of what is to be joined.

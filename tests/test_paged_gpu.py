@@ -170,6 +170,12 @@ ATTEND = [  # B, Hq, Hkv, D, page, Tq, lengths, new lengths, causal, window, dty
     (1, 64, 1, 128, 16, 8, [1000], None, True, 0, "fp16"),                 # 512 rows
     (2, 17, 1, 64, 128, 2, [150, 129], None, True, 100, "bf16"),
     (1, 32, 8, 128, 64, 1, [30001], None, True, 0, "bf16"),                # many parts per sequence
+    (2, 14, 2, 128, 32, 5, [5000, 321], None, True, 0, "bf16"),            # 35 rows
+    (2, 14, 2, 96, 64, 5, [5000, 321], None, True, 0, "fp16"),
+    (2, 28, 1, 128, 16, 2, [3001, 77], None, True, 0, "fp16"),             # 56 rows
+    (2, 24, 1, 96, 16, 1, [3001, 77], None, True, 0, "bf16"),              # 24 rows
+    (1, 40, 1, 256, 64, 1, [2500], None, True, 700, "bf16"),
+    (6, 14, 2, 64, 32, 5, [900, 5, 64, 65, 1, 0], [5, 4, 5, 1, 1, 0], True, 30, "bf16"),
     (40, 2, 1, 64, 16, 1, [(37 * i) % 211 for i in range(40)], None, True, 0, "fp16"),
     (300, 1, 1, 64, 16, 2, [(i * i) % 97 for i in range(300)], None, True, 0, "bf16"),  # more sequences than threads
 ]

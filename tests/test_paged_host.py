@@ -137,6 +137,11 @@ def test_page_select_refusals(lib, kw, code):
     assert select(lib, **kw) == code
 
 
+def test_paged_fwd_refuses_more_tiles_than_it_counts(lib):
+    big = dict(B=1 << 20, Hkv=16, max_pages=1 << 20)
+    assert paged_fwd(lib, cache_kw=big, Hq=16, sel=None, sel_lens=None) == INVALID
+
+
 def test_page_select_needs_bounds(lib):
     assert select(lib, cache_kw=dict(k_bounds=None)) == INVALID
 
