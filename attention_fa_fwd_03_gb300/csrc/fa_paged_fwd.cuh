@@ -259,14 +259,27 @@ __device__ __forceinline__ int64_t block_row0(const PagedFwdArgs& p, int b, int 
   return (static_cast<int64_t>(b) * p.c.Hkv + g) * p.rows + rb * block_rows;
 }
 
+__device__ __forceinline__ void scale4(float4& a, float f) {
+  a.x *= f;
+  a.y *= f;
+  a.z *= f;
+  a.w *= f;
+}
+__device__ __forceinline__ void add4(float4& a, const float4& x, float f) {
+  a.x = fmaf(x.x, f, a.x);
+  a.y = fmaf(x.y, f, a.y);
+  a.z = fmaf(x.z, f, a.z);
+  a.w = fmaf(x.w, f, a.w);
+}
+
 // O = sum / l and LSE of one row chunk of 8 values.
 template <bool BF16>
-__device__ __forceinline__ void store_out8(uint16_t* dst, const float (&x)[8], float inv) {
+__device__ __forceinline__ void store_out8(uint16_t* dst, const float4& x, const float4& y, float inv) {
   uint4 w;
-  w.x = pack2<BF16>(x[0] * inv, x[1] * inv);
-  w.y = pack2<BF16>(x[2] * inv, x[3] * inv);
-  w.z = pack2<BF16>(x[4] * inv, x[5] * inv);
-  w.w = pack2<BF16>(x[6] * inv, x[7] * inv);
+  w.x = pack2<BF16>(x.x * inv, x.y * inv);
+  w.y = pack2<BF16>(x.z * inv, x.w * inv);
+  w.z = pack2<BF16>(y.x * inv, y.y * inv);
+  w.w = pack2<BF16>(y.z * inv, y.w * inv);
   *reinterpret_cast<uint4*>(dst) = w;
 }
 __device__ __forceinline__ float row_lse(float m, float l) {
@@ -293,6 +306,10 @@ __device__ __forceinline__ void st_peer_f4(const void* at, uint32_t rank, float4
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer_addr(smem_u32(at), rank)), "f"(v.x),
                "f"(v.y), "f"(v.z), "f"(v.w)
                : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* at) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
 }
 
 // Whether one of two packed values is infinite or NaN (exponent bits all set).
@@ -336,6 +353,15 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   if constexpr (C::CLUSTER) cluster_arrive_relaxed();  // waited for before the first store into a peer
   grid_wait_prior();
   grid_release_next();
+  // What the lengths will lead to, on its way into L2 meanwhile: this CTA's part of
+  // the page table (or of the selections) and of the queries.
+  {
+    const int64_t t = static_cast<int64_t>(part) * C::THREADS + threadIdx.x;
+    const int64_t entries = p.sel ? static_cast<int64_t>(c.B) * c.Hkv * p.n_sel : static_cast<int64_t>(c.B) * c.max_pages;
+    const int64_t q_lines = static_cast<int64_t>(c.B) * c.Hkv * p.rows * (D / 64);
+    if (t * 32 < entries) prefetch_l2((p.sel ? p.sel : c.table) + t * 32);
+    if (t < q_lines) prefetch_l2(p.q + t * 64);
+  }
   const int rank = C::CLUSTER ? part % ranks : 0, unit = C::CLUSTER ? part / ranks : 0;
   Share share;
   if constexpr (C::CLUSTER)
@@ -727,7 +753,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       cluster_wait();  // every CTA of the cluster is running
       for (int i = tid; i < pieces; i += 32 * C::WARPS) {
         const int r = i / (D / 8), ch = i - r * (D / 8);
-        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
         const float2 ml = warps_max_sum<C>(mls, r);
 #pragma unroll
         for (int k = 0; k < C::KW; ++k) {
@@ -736,26 +762,21 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           const float f = ex2(mk - ml.x);
           const float* x = wm + (k * C::ROWS + r) * C::OP + 8 * ch;
           const float4 u = *reinterpret_cast<const float4*>(x), v = *reinterpret_cast<const float4*>(x + 4);
-          sum[0] = fmaf(u.x, f, sum[0]);
-          sum[1] = fmaf(u.y, f, sum[1]);
-          sum[2] = fmaf(u.z, f, sum[2]);
-          sum[3] = fmaf(u.w, f, sum[3]);
-          sum[4] = fmaf(v.x, f, sum[4]);
-          sum[5] = fmaf(v.y, f, sum[5]);
-          sum[6] = fmaf(v.z, f, sum[6]);
-          sum[7] = fmaf(v.w, f, sum[7]);
+          add4(s0, u, f);
+          add4(s1, v, f);
         }
         const uint32_t owner = i % ranks;
         const int slot = rank * share_of + i / ranks;
-        st_peer_f4(om + 8 * slot, owner, make_float4(sum[0], sum[1], sum[2], sum[3]));
-        st_peer_f4(om + 8 * slot + 4, owner, make_float4(sum[4], sum[5], sum[6], sum[7]));
+        st_peer_f4(om + 8 * slot, owner, s0);
+        st_peer_f4(om + 8 * slot + 4, owner, s1);
         st_peer_f2(pml + slot, owner, ml);
       }
       __syncwarp();
       cluster_barrier();  // what was sent has arrived; nobody touches a peer after it
       for (int j = tid; rank + j * ranks < pieces; j += 32 * C::WARPS) {
         const int i = rank + j * ranks, r = i / (D / 8), ch = i - r * (D / 8);
-        float mt = -INFINITY, lt = 0.f, sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float mt = -INFINITY, lt = 0.f;
+        float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
         for (int k = 0; k < ranks; ++k) mt = fmaxf(mt, pml[k * share_of + j].x);
         for (int k = 0; k < ranks; ++k) {
           const float2 ml = pml[k * share_of + j];
@@ -763,16 +784,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           const float* x = om + 8 * (k * share_of + j);
           const float4 u = *reinterpret_cast<const float4*>(x), v = *reinterpret_cast<const float4*>(x + 4);
           lt += ml.y * f;
-          sum[0] = fmaf(u.x, f, sum[0]);
-          sum[1] = fmaf(u.y, f, sum[1]);
-          sum[2] = fmaf(u.z, f, sum[2]);
-          sum[3] = fmaf(u.w, f, sum[3]);
-          sum[4] = fmaf(v.x, f, sum[4]);
-          sum[5] = fmaf(v.y, f, sum[5]);
-          sum[6] = fmaf(v.z, f, sum[6]);
-          sum[7] = fmaf(v.w, f, sum[7]);
+          add4(s0, u, f);
+          add4(s1, v, f);
         }
-        store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, sum, lt == 0.f ? 0.f : 1.f / lt);
+        store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, s0, s1, lt == 0.f ? 0.f : 1.f / lt);
         if (ch == 0) p.lse[row0 + r] = row_lse(mt, lt);
       }
       return;
@@ -812,18 +827,17 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int part_slot = 2 * part + (begins ? 1 : 0);
     for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS) {
       const int r = i / (D / 8), ch = i - r * (D / 8);
-      float x[8];
-      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch);
-      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch + 4);
+      const float4 x = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch);
+      const float4 y = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch + 4);
       const float2 ml = warps_max_sum<C>(mls, r);
       const float mt = ml.x, lt = ml.y;
       if (begins && ends) {
-        store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, x, lt == 0.f ? 0.f : 1.f / lt);
+        store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, x, y, lt == 0.f ? 0.f : 1.f / lt);
         if (ch == 0) p.lse[row0 + r] = row_lse(mt, lt);
       } else {
         float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(part_slot) * C::ROWS + r) * D + 8 * ch);
-        dst[0] = *reinterpret_cast<const float4*>(x);
-        dst[1] = *reinterpret_cast<const float4*>(x + 4);
+        dst[0] = x;
+        dst[1] = y;
         if (ch == 0) p.part_ml[part_slot * C::ROWS + r] = make_float2(mt, lt);
       }
     }
@@ -854,17 +868,18 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 }
 
 // Joins the parts of the units that CTA blockIdx.x of the split kernel began
-// and did not finish: its slot 1 and slot 0 of the CTAs after it. A warp takes
-// every 8th part, four at a time with all their loads in flight, a lane 4
-// columns (D = 256: 8); blockIdx.y strides over rows.
+// and did not finish: its slot 1 and slot 0 of the CTAs after it. A row's parts are
+// shared by up to 8 warps, four or more each with all their loads in flight, a lane
+// 4 columns (D = 256: 8); with few parts the block's warps take several rows at a
+// time.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 16;  // grid.y at most
+constexpr int kJoinBlocks = 8;  // blocks per split unit at most
 template <int D, int ROWS, bool BF16>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 fa_paged_join_kernel(const PagedFwdArgs p) {
   constexpr int NV = (D / 4 + 31) / 32, UN = 4;
   __shared__ float4 sm_o[kJoinWarps][D / 4];
-  __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
+  __shared__ float2 sm_ml[kJoinWarps];
   grid_wait_prior();
   grid_release_next();
   const int4 join = p.joins[blockIdx.x];
@@ -872,21 +887,26 @@ fa_paged_join_kernel(const PagedFwdArgs p) {
   const int64_t row0 = (static_cast<int64_t>(join.x) << 31) + join.y;
   const int first = blockIdx.x, nparts = join.z - first + 1, rows = join.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+  // warps of a row, and this warp's place among them
+  const int team = nparts <= UN ? 1 : nparts <= 2 * UN ? 2 : nparts <= 4 * UN ? 4 : 8;
+  const int mate = warp % team, per_pass = kJoinWarps / team;
+  for (int base = blockIdx.y * per_pass; base < rows; base += gridDim.y * per_pass) {
+    const int r = base + warp / team;
+    const int mine = r < rows ? nparts : 0;
     float m = -INFINITY, l = 0.f;
     float4 acc[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = warp; i0 < nparts; i0 += kJoinWarps * UN) {
+    for (int i0 = mate; i0 < mine; i0 += team * UN) {
       float2 ml[UN];
       float4 x[UN][NV];
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
-        const int i = i0 + u * kJoinWarps;
+        const int i = i0 + u * team;
         ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) x[u][v] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i >= nparts) continue;
+        if (i >= mine) continue;
         const int slot = i == 0 ? 2 * first + 1 : 2 * (first + i);
         ml[u] = p.part_ml[slot * ROWS + r];
         const float4* src = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(slot) * ROWS + r) * D);
@@ -901,60 +921,49 @@ fa_paged_join_kernel(const PagedFwdArgs p) {
       m = mn;
       l *= alpha;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        acc[v].x *= alpha;
-        acc[v].y *= alpha;
-        acc[v].z *= alpha;
-        acc[v].w *= alpha;
-      }
+      for (int v = 0; v < NV; ++v) scale4(acc[v], alpha);
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
         const float f = exp2_rel(ml[u].x, mn);
         l += ml[u].y * f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          acc[v].x = fmaf(x[u][v].x, f, acc[v].x);
-          acc[v].y = fmaf(x[u][v].y, f, acc[v].y);
-          acc[v].z = fmaf(x[u][v].z, f, acc[v].z);
-          acc[v].w = fmaf(x[u][v].w, f, acc[v].w);
-        }
+        for (int v = 0; v < NV; ++v) add4(acc[v], x[u][v], f);
       }
     }
+    if (team > 1) {
+      __syncthreads();  // the rows of the pass before are read
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if (lane + 32 * v < D / 4) sm_o[warp][lane + 32 * v] = acc[v];
-    if (lane == 0) {
-      sm_m[warp] = m;
-      sm_l[warp] = l;
-    }
-    __syncthreads();
-    float mt = -INFINITY, lt = 0.f;
+      for (int v = 0; v < NV; ++v)
+        if (lane + 32 * v < D / 4) sm_o[warp][lane + 32 * v] = acc[v];
+      if (lane == 0) sm_ml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (mate > 0) continue;
+      const float own = m;
+      for (int k = 1; k < team; ++k) m = fmaxf(m, sm_ml[warp + k].x);
+      const float f0 = exp2_rel(own, m);
+      l *= f0;
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) mt = fmaxf(mt, sm_m[k]);
-    float f[kJoinWarps];
+      for (int v = 0; v < NV; ++v) scale4(acc[v], f0);
+      for (int k = 1; k < team; ++k) {
+        const float2 ml = sm_ml[warp + k];
+        const float f = exp2_rel(ml.x, m);
+        l += ml.y * f;
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) {
-      f[k] = exp2_rel(sm_m[k], mt);
-      lt += sm_l[k] * f[k];
-    }
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
-    for (int d = threadIdx.x; d < D / 4; d += 32 * kJoinWarps) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kJoinWarps; ++k) {
-        const float4 y = sm_o[k][d];
-        x.x = fmaf(y.x, f[k], x.x);
-        x.y = fmaf(y.y, f[k], x.y);
-        x.z = fmaf(y.z, f[k], x.z);
-        x.w = fmaf(y.w, f[k], x.w);
+        for (int v = 0; v < NV; ++v)
+          if (lane + 32 * v < D / 4) add4(acc[v], sm_o[warp + k][lane + 32 * v], f);
       }
+    }
+    if (r >= rows) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (lane + 32 * v >= D / 4) continue;
       uint2 out;
-      out.x = pack2<BF16>(x.x * inv, x.y * inv);
-      out.y = pack2<BF16>(x.z * inv, x.w * inv);
-      *reinterpret_cast<uint2*>(p.o + (row0 + r) * D + 4 * d) = out;
+      out.x = pack2<BF16>(acc[v].x * inv, acc[v].y * inv);
+      out.y = pack2<BF16>(acc[v].z * inv, acc[v].w * inv);
+      *reinterpret_cast<uint2*>(p.o + (row0 + r) * D + 4 * (lane + 32 * v)) = out;
     }
-    if (threadIdx.x == 0) p.lse[row0 + r] = row_lse(mt, lt);
-    __syncthreads();
+    if (lane == 0) p.lse[row0 + r] = row_lse(m, l);
   }
 }
 
@@ -1007,7 +1016,7 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(parts), static_cast<unsigned>(std::min(std::min(p.rows, C::ROWS), kJoinRows)), 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(parts), static_cast<unsigned>(std::min(std::min(p.rows, C::ROWS), kJoinBlocks)), 1);
   cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
   cfg.stream = a.stream;
   allow_early_launch(&cfg, attrs);
