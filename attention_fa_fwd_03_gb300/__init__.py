@@ -281,7 +281,7 @@ def _address(name: str, t, shape, dtype, kv) -> int:
 
 
 def _token_view(name: str, t, shape, kv):
-    """Address and strides of a [B, H, T, D] view whose innermost index is contiguous."""
+    """Address and three strides of a [B, H, T, D] view whose innermost index is contiguous."""
     if t.dtype is not kv.dtype or t.shape != shape or t.get_device() != kv._index:
         raise ValueError(f"{name}: expected {kv.dtype} of shape {list(shape)} on {kv.device}, got "
                          f"{t.dtype} of shape {list(t.shape)} on {t.device}")
@@ -290,10 +290,10 @@ def _token_view(name: str, t, shape, kv):
         raise ValueError(f"{name}: the innermost index must be contiguous")
     # the stride of an index of size 1 is never used and can be anything
     B, H, T, _ = shape
-    return t.data_ptr(), _Strides(sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0)
+    return t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0
 
 
-_Strides = ctypes.c_int64 * 3
+_Strides = ctypes.c_int64 * 9  # of k, v and q, three each
 
 
 def _workspace(t, kv, what: str):
@@ -348,16 +348,16 @@ def fa_kv_append(kv: PagedKV, k, v, cos=None, sin=None, interleaved: bool = Fals
     tokens (None: all)."""
     B, Hkv, D = kv.B, kv.Hkv, kv.D
     T = k.shape[2] if k.dim() == 4 else 0
-    kp, ks = _token_view("k", k, (B, Hkv, T, D), kv)
-    vp, vs = _token_view("v", v, (B, Hkv, T, D), kv)
+    kp, k0, k1, k2 = _token_view("k", k, (B, Hkv, T, D), kv)
+    vp, v0, v1, v2 = _token_view("v", v, (B, Hkv, T, D), kv)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    qp = qs = qo = None
-    Hq = 0
+    qp = qo = None
+    Hq = q0 = q1 = q2 = 0
     if q is not None:
         shape = q.shape
         Hq = shape[1] if len(shape) == 4 else 0
-        qp, qs = _token_view("q", q, (B, Hq, T, D), kv)
+        qp, q0, q1, q2 = _token_view("q", q, (B, Hq, T, D), kv)
         qo = _address("q_out", q_out, shape, kv.dtype, kv)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
@@ -371,8 +371,10 @@ def fa_kv_append(kv: PagedKV, k, v, cos=None, sin=None, interleaved: bool = Fals
         cp = _address("cos", cos, shape, kv._f32, kv)
         sp = _address("sin", sin, shape, kv._f32, kv)
     nl = None if new_lens is None else _address("new_lens", new_lens, kv._lens_shape, kv._i32, kv)
-    _launch(kv, kv._lib.fa_kv_append, "fa_kv_append", stream, kp, ks, vp, vs, qp, qs, qo, Hq, T, nl, cp,
-            sp, rope_len, rot_dim, 1 if interleaved else 0)
+    strides = _Strides(k0, k1, k2, v0, v1, v2, q0, q1, q2)
+    at = ctypes.addressof(strides)
+    _launch(kv, kv._lib.fa_kv_append, "fa_kv_append", stream, kp, at, vp, at + 24, qp, at + 48, qo, Hq, T,
+            nl, cp, sp, rope_len, rot_dim, 1 if interleaved else 0)
 
 
 def fa_paged_workspace_size(Hq: int, Hkv: int, Tq: int, D: int) -> int:

@@ -18,6 +18,7 @@ constexpr int kMaxTokens = 1 << 22;
 constexpr int64_t kMaxUnits = 1 << 24;     // B * heads
 constexpr int64_t kMaxPool = 1 << 30;      // num_pages * Hkv, and positions of a sequence
 constexpr int kMaxSelected = 1 << 20;
+constexpr int kMaxHeads = 1 << 14;         // of one token of fa_kv_append
 
 fa_status check_cache(const fa_paged_kv* kv, bool need_bounds) {
   if (!kv) return FA_ERR_INVALID_ARG;
@@ -106,9 +107,9 @@ fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* 
   if (!k_new || !v_new || !k_strides || !v_strides) return FA_ERR_INVALID_ARG;
   if ((q == nullptr) != (q_out == nullptr)) return FA_ERR_INVALID_ARG;
   if (q && (!q_strides || Hq < 1 || Hq % kv->Hkv != 0 || static_cast<int64_t>(kv->B) * Hq > kMaxUnits ||
-            Hq > (1 << 16)))
+            Hq > kMaxHeads))
     return FA_ERR_INVALID_ARG;
-  if (kv->Hkv > (1 << 16)) return FA_ERR_INVALID_ARG;
+  if (kv->Hkv > kMaxHeads) return FA_ERR_INVALID_ARG;
   if ((cos_table == nullptr) != (sin_table == nullptr)) return FA_ERR_INVALID_ARG;
   if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_ARG;
   if (cos_table ? (rot_dim < 16 || rot_dim > kv->D || rot_dim % 16 != 0 || rope_len < 1) : rot_dim != 0)
