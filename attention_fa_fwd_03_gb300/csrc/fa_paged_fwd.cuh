@@ -634,9 +634,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], p.scale_log2, -m[nt][e & 1]);
           }
         }
-        // weights, rounded to the cache's type for the product with V (the sums keep
-        // them in fp32), and transposed into B fragments
-        uint32_t pb[C::NT][2];
+        // Weights in two words of the cache's type, p = hi + lo to 2^-17 (bf16) or
+        // 2^-22 (fp16) of p, and transposed into B fragments: with hi alone O would be
+        // off by 1.4 times as much as its own rounding makes it. The products with lo
+        // cost no time where the tiles' bytes bound the kernel.
+        uint32_t pb[C::NT][2], pl[C::NT][2];
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
@@ -645,8 +647,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             s[nt][2 + h] = ex2(x[nt][2 + h]);
             l[nt][h] += s[nt][h] + s[nt][2 + h];
           }
-          pb[nt][0] = transpose8(pack2<C::BF16>(s[nt][0], s[nt][1]));
-          pb[nt][1] = transpose8(pack2<C::BF16>(s[nt][2], s[nt][3]));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t hi = pack2<C::BF16>(s[nt][2 * h], s[nt][2 * h + 1]);
+            const float2 f = unpack2<C::BF16>(hi);
+            pb[nt][h] = transpose8(hi);
+            pl[nt][h] = transpose8(pack2<C::BF16>(s[nt][2 * h] - f.x, s[nt][2 * h + 1] - f.y));
+          }
         }
         // O^T += V^T P^T. A key hidden from every row gets V = 0 (its slot may hold
         // anything; 0 * NaN would not be 0). Where rows differ in what they see and
@@ -679,6 +686,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
             for (int nt = 0; nt < C::NT; ++nt)
               mma16816<C::BF16>(acc[nt][i], a, pb[nt][0], pb[nt][1]);
+#pragma unroll
+            for (int nt = 0; nt < C::NT; ++nt) mma16816<C::BF16>(acc[nt][i], a, pl[nt][0], pl[nt][1]);
           }
         } else {
 #pragma unroll 1
@@ -701,6 +710,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               for (int nt = 0; nt < C::NT; ++nt) {
                 float x[4] = {acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]};
                 mma16816<C::BF16>(x, a, pb[nt][0], pb[nt][1]);
+                mma16816<C::BF16>(x, a, pl[nt][0], pl[nt][1]);
                 if (token(nt, 0) == tok) acc[nt][i][0] = x[0], acc[nt][i][2] = x[2];
                 if (token(nt, 1) == tok) acc[nt][i][1] = x[1], acc[nt][i][3] = x[3];
               }
