@@ -49,14 +49,10 @@ __device__ __forceinline__ int page_count(const PagedView& c, int b) {
 // Larger of two with NaN the largest.
 __device__ __forceinline__ float max_or_nan(float x, float y) { return y > x || y != y ? y : x; }
 
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectRanks = 8;       // CTAs of a cluster at most
 constexpr int kHeld = 12 * 1024;      // pages whose scores are held in shared memory
 constexpr int kFewTies = 256;         // pages in between that are ranked directly
 constexpr int kQuerySmem = 36 * 1024;
-
-constexpr int kScorePages = 16 * kSelectWarps;  // pages of a pass
 
 // Query heads in shared memory: rows of q+, rows of q-, then the row of largest
 // magnitudes, 16-bit, padded by 16 bytes so that 8 rows' chunks have other banks.
@@ -94,10 +90,10 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t x, uint32_t y) {
 
 // Scores of pages keep_first + [begin, end) of (b, g): put(i, key) for each, by
 // one lane; get(i) gives back what was put (heads beyond head_chunk).
-template <int D, bool BF16, class Put, class Get>
+template <int T, int D, bool BF16, class Put, class Get>
 __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* qs, int b, int g, int begin, int end,
                                                   const Put& put, const Get& get) {
-  constexpr int CH = D / 32, BATCH = CH < 4 ? CH : 4;  // a thread's chunks of a row, and how many at a time
+  constexpr int CH = D / 32, BATCH = CH == 3 ? 3 : 2;  // a thread's chunks of a row, and how many at a time
   constexpr int PITCH = query_pitch(D);
   const PagedView& c = p.c;
   const int reps = p.Hq / c.Hkv;
@@ -134,7 +130,7 @@ __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* 
     find_rows(begin + 16 * warp);  // under way while the queries are laid out
     load_rows(0);
     // behind the last head it again, which changes no maximum
-    for (int i = threadIdx.x; i < tiles * 8 * (D / 2); i += kSelectThreads) {
+    for (int i = threadIdx.x; i < tiles * 8 * (D / 2); i += T) {
       const int r = i / (D / 2), d2 = i - r * (D / 2);
       const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(
                                    p.q + (static_cast<int64_t>(b) * p.Hq + g * reps + h0 + min(r, heads - 1)) * D) + d2);
@@ -144,7 +140,7 @@ __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* 
           pack2<BF16>(f.x > 0.f ? 0.f : f.x, f.y > 0.f ? 0.f : f.y);
     }
     __syncthreads();
-    for (int d2 = threadIdx.x; d2 < D / 2; d2 += kSelectThreads) {
+    for (int d2 = threadIdx.x; d2 < D / 2; d2 += T) {
       uint32_t m = 0;
       for (int r = 0; r < heads; ++r) {
         m = abs_max2<BF16>(m, *reinterpret_cast<const uint32_t*>(qs + r * PITCH + 4 * d2));
@@ -153,7 +149,7 @@ __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* 
       *reinterpret_cast<uint32_t*>(qmag + 4 * d2) = m;
     }
     __syncthreads();
-    for (int base = begin + 16 * warp; base < end; base += kScorePages) {
+    for (int base = begin + 16 * warp; base < end; base += T / 2) {
       if (base != begin + 16 * warp) {
         find_rows(base);
         load_rows(0);
@@ -252,7 +248,7 @@ struct BlockCounts {
 // The need-th largest of the keys that get(i, &key) gives for i in [0, n), all of
 // them in [lo, hi]: the largest T with at least `need` keys >= T, two bits at a
 // time from the first bit in which lo and hi differ.
-template <class K, class Get>
+template <int T, class K, class Get>
 __device__ __forceinline__ K kth_largest(BlockCounts& counts, int n, int need, K lo, K hi, const Get& get) {
   if (lo == hi) return lo;
   int bit = 63 - __clzll(static_cast<long long>(lo ^ hi));
@@ -262,7 +258,7 @@ __device__ __forceinline__ K kth_largest(BlockCounts& counts, int n, int need, K
   for (; bit >= 0; bit -= 2) {
     const K t1 = t | (static_cast<K>(1) << bit), t2 = t | (static_cast<K>(2) << bit), t3 = t | (static_cast<K>(3) << bit);
     int a = 0, b = 0, e = 0;
-    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+    for (int i = threadIdx.x; i < n; i += T) {
       K k;
       if (!get(i, &k)) continue;
       a += k >= t1;
@@ -277,6 +273,7 @@ __device__ __forceinline__ K kth_largest(BlockCounts& counts, int n, int need, K
 }
 
 // Exclusive prefix sum over the block's threads, and the total. Three barriers.
+template <int T>
 __device__ __forceinline__ int block_before(int x, int* warp_sums, int* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int incl = x;
@@ -288,8 +285,8 @@ __device__ __forceinline__ int block_before(int x, int* warp_sums, int* total) {
   __syncthreads();  // the previous use of warp_sums is over
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  static_assert(kSelectWarps <= 32, "one warp adds the warps' sums");
-  int sums = lane < kSelectWarps ? warp_sums[lane] : 0;
+  static_assert(T / 32 <= 32, "one warp adds the warps' sums");
+  int sums = lane < (T / 32) ? warp_sums[lane] : 0;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, sums, off);
@@ -306,26 +303,27 @@ __device__ __forceinline__ int block_before(int x, int* warp_sums, int* total) {
 // evenly filled, so one round is the rule; each round divides the range by kBins.
 constexpr int kBins = 2048;
 constexpr int kFewKeys = 256;
+template <int T>
 struct SearchSmem {
   int bins[kBins];
   uint32_t keys[kFewKeys];
-  int warp_sums[kSelectWarps];
+  int warp_sums[(T / 32)];
   int bin, above, inside, count;
   uint32_t found;
 };
-template <class Get>
-__device__ __forceinline__ uint32_t kth_largest_score(SearchSmem& sm, int n, int need, uint32_t lo, uint32_t hi,
+template <int T, class Get>
+__device__ __forceinline__ uint32_t kth_largest_score(SearchSmem<T>& sm, int n, int need, uint32_t lo, uint32_t hi,
                                                       const Get& get) {
-  constexpr int PER = kBins / kSelectThreads;
+  constexpr int PER = kBins / T;
   while (true) {
     if (lo == hi) return lo;
     const int shift = max(0, 32 - __clz(hi - lo) - 11);
     static_assert(kBins == 1 << 11, "bins cover the range");
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sm.bins[threadIdx.x + i * kSelectThreads] = 0;
+    for (int i = 0; i < PER; ++i) sm.bins[threadIdx.x + i * T] = 0;
     if (threadIdx.x == 0) sm.count = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+    for (int i = threadIdx.x; i < n; i += T) {
       const uint32_t k = get(i);
       if (k >= lo && k <= hi) atomicAdd(&sm.bins[(k - lo) >> shift], 1);
     }
@@ -334,7 +332,7 @@ __device__ __forceinline__ uint32_t kth_largest_score(SearchSmem& sm, int n, int
     int mine = 0, total;
 #pragma unroll
     for (int i = 0; i < PER; ++i) mine += sm.bins[kBins - 1 - PER * threadIdx.x - i];
-    int above = block_before(mine, sm.warp_sums, &total);
+    int above = block_before<T>(mine, sm.warp_sums, &total);
     if (above < need && need <= above + mine) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
@@ -353,7 +351,7 @@ __device__ __forceinline__ uint32_t kth_largest_score(SearchSmem& sm, int n, int
     hi = min(hi, lo + ((1u << shift) - 1));
     const int inside = sm.inside;
     if (inside <= kFewKeys) {
-      for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+      for (int i = threadIdx.x; i < n; i += T) {
         const uint32_t k = get(i);
         if (k >= lo && k <= hi) sm.keys[atomicAdd(&sm.count, 1)] = k;
       }
@@ -460,13 +458,15 @@ __device__ __forceinline__ float2 two_word_score(const SelectArgs& p, int b, int
   return best;
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kSelectThreads)
+// T = 512: few sequences, the block alone on its SM; T = 256: three blocks share
+// one, so that one's choice overlaps the others' loads.
+template <int T, int D, bool BF16>
+__global__ void __launch_bounds__(T, T == 512 ? 1 : 3)
 fa_page_select_kernel(const SelectArgs p, int ranks) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ int counters[3][3];
-  __shared__ SearchSmem search;
-  __shared__ uint32_t warp_stats[kSelectWarps][4], rank_stats[kSelectRanks][4];
+  __shared__ SearchSmem<T> search;
+  __shared__ uint32_t warp_stats[(T / 32)][4], rank_stats[kSelectRanks][4];
   __shared__ unsigned long long tie_key[kFewTies];
   __shared__ float2 tie_score[kFewTies], tie_cut;
   __shared__ int tie_page[kFewTies], ties_found;
@@ -490,17 +490,17 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   uint32_t* far = p.scores + static_cast<int64_t>(unit) * c.max_pages;
   cluster_wait();
   if (!all && need > 0) {
-    const int begin = static_cast<int>(static_cast<long long>(n) * rank / ranks);
-    const int end = static_cast<int>(static_cast<long long>(n) * (rank + 1) / ranks);
+    const int share = (n + ranks - 1) / ranks;
+    const int begin = min(n, rank * share), end = min(n, begin + share);
     ScoreStats st;
     if (ranks == 1 && in_smem)
-      st = score_pages<D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { held[i] = k; },
+      st = score_pages<T, D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { held[i] = k; },
                                 [&](int i) { return held[i]; });
     else if (in_smem && p.Hq / c.Hkv <= p.head_chunk)
-      st = score_pages<D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { st_first(held + i, k); },
+      st = score_pages<T, D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { st_first(held + i, k); },
                                 [&](int) { return 0u; });
     else
-      st = score_pages<D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { far[i] = k; },
+      st = score_pages<T, D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { far[i] = k; },
                                 [&](int i) { return far[i]; });
     st.a = warp_max(st.a);
     st.odd = __any_sync(0xffffffffu, st.odd);
@@ -515,7 +515,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     __syncthreads();
     if (threadIdx.x < 4) {
       uint32_t x = warp_stats[0][threadIdx.x];
-      for (int w = 1; w < kSelectWarps; ++w) {
+      for (int w = 1; w < (T / 32); ++w) {
         const uint32_t y = warp_stats[w][threadIdx.x];
         x = threadIdx.x == 2 ? min(x, y) : max(x, y);  // A is not negative: its bits order like it
       }
@@ -529,11 +529,11 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   int* sel = p.sel + static_cast<int64_t>(unit) * p.n_sel;
   if (threadIdx.x == 0) p.sel_lens[unit] = min(pages, p.n_sel);
   if (all) {
-    for (int i = threadIdx.x; i < p.n_sel; i += kSelectThreads) sel[i] = i < pages ? i : -1;
+    for (int i = threadIdx.x; i < p.n_sel; i += T) sel[i] = i < pages ? i : -1;
     return;
   }
-  for (int i = threadIdx.x; i < p.keep_first; i += kSelectThreads) sel[i] = i;
-  for (int i = threadIdx.x; i < p.keep_last; i += kSelectThreads) sel[p.n_sel - p.keep_last + i] = pages - p.keep_last + i;
+  for (int i = threadIdx.x; i < p.keep_first; i += T) sel[i] = i;
+  for (int i = threadIdx.x; i < p.keep_last; i += T) sel[p.n_sel - p.keep_last + i] = pages - p.keep_last + i;
   if (need == 0) return;
   const bool local = in_smem && (ranks == 1 || p.Hq / c.Hkv <= p.head_chunk);
   auto key32 = [&](int i) { return local ? held[i] : far[i]; };
@@ -551,7 +551,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   int sum[3];
   int sure = 0, between = n;
   if (!odd) {
-    const uint32_t tau = kth_largest_score(search, n, need, key_lo, key_hi, key32);
+    const uint32_t tau = kth_largest_score<T>(search, n, need, key_lo, key_hi, key32);
     const float t = order_value(tau);
     // 2 E, with room for the error of A and the roundings of t -+ err
     const float err = 2.02f * D * 1.1920929e-7f * a_max + fabsf(t) * 2.4e-7f;
@@ -562,7 +562,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
       low = high = tau;
     }
     int in = 0, mid = 0;
-    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+    for (int i = threadIdx.x; i < n; i += T) {
       const uint32_t k = key32(i);
       in += k > high;
       if (k >= low && k <= high) {
@@ -584,7 +584,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     // Each against the others; the keys of those that win or lose leave
     // [low, high]. A bad page is in between only where all of them are.
     const int t = threadIdx.x;
-    for (int i = warp; i < between; i += kSelectWarps) {
+    for (int i = warp; i < between; i += (T / 32)) {
       const float2 x = two_word_score<D, BF16>(p, b, g, p.keep_first + tie_page[i]);
       if (lane == 0) tie_score[i] = x;
     }
@@ -612,7 +612,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     const int left = places - sum[0];
     const bool exact = sum[1] > left;
     if (exact) {
-      for (int i = warp; i < between; i += kSelectWarps) {
+      for (int i = warp; i < between; i += (T / 32)) {
         if (!(fabsf(minus(tie_score[i], tie_cut)) <= err2)) continue;
         const unsigned long long k = exact_key<D, BF16>(p, b, g, p.keep_first + tie_page[i]);
         if (lane == 0) tie_key[i] = k;
@@ -637,7 +637,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     __syncthreads();
   } else if (ranked) {
     unsigned long long* keys = p.keys + static_cast<int64_t>(unit) * c.max_pages;
-    for (int i = warp; i < n; i += kSelectWarps) {
+    for (int i = warp; i < n; i += (T / 32)) {
       const uint32_t k = key32(i);
       if (k < low || k > high) continue;
       const unsigned long long k64 = exact_key<D, BF16>(p, b, g, p.keep_first + i);
@@ -650,9 +650,9 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
       *k = keys[i];
       return true;
     };
-    cut = kth_largest<unsigned long long>(counts, n, places, 0ull, ~0ull, key64);
+    cut = kth_largest<T, unsigned long long>(counts, n, places, 0ull, ~0ull, key64);
     int above = 0;
-    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
+    for (int i = threadIdx.x; i < n; i += T) {
       unsigned long long k;
       above += key64(i, &k) && k > cut;
     }
@@ -670,7 +670,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   };
   // places in ascending order: a thread takes runs of four pages
   int at = p.keep_first, seen = 0;  // places given and equals met before this stretch
-  for (int base = 0; base < n; base += 4 * kSelectThreads) {
+  for (int base = 0; base < n; base += 4 * T) {
     const int i0 = base + 4 * threadIdx.x;
     uint32_t k[4] = {0, 0, 0, 0};
     if (local && i0 + 3 < n) {
@@ -688,7 +688,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
       ties += st[j] == 1;
     }
     if (ranked && !few) {
-      int t = seen + block_before(ties, search.warp_sums, &total);
+      int t = seen + block_before<T>(ties, search.warp_sums, &total);
       seen += total;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -697,7 +697,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     int mine = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) mine += st[j] == 2;
-    int to = at + block_before(mine, search.warp_sums, &total);
+    int to = at + block_before<T>(mine, search.warp_sums, &total);
     at += total;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -705,7 +705,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   }
 }
 
-template <int D, bool BF16>
+template <int T, int D, bool BF16>
 cudaError_t run_select(const SelectLaunch& a) {
   SelectArgs p;
   p.c = a.c;
@@ -717,27 +717,36 @@ cudaError_t run_select(const SelectLaunch& a) {
   p.scores = reinterpret_cast<uint32_t*>(p.keys + units * a.c.max_pages);
   // query heads in eights, as many as shared memory is set aside for
   p.head_chunk = std::min((a.Hq / a.c.Hkv + 7) / 8, (kQuerySmem / query_pitch(D) - 1) / 16) * 8;
-  // a cluster large enough that each CTA has one pass over its pages
-  // (and not more CTAs than fill the GPU)
+  // a cluster large enough that each CTA has one pass of T / 2 pages, but not many
+  // more CTAs than the GPU holds at a time (B32 ragged to 1024 pages, T = 256: 35 us
+  // with one CTA per unit, 26 with two, 32 with four)
   int ranks = 1;
-  while (ranks < kSelectRanks && ranks * kScorePages < a.c.max_pages && units * ranks < device_sm_count()) ranks *= 2;
+  while (ranks < kSelectRanks && ranks * (T / 2) < a.c.max_pages && units * ranks < 3 * device_sm_count()) ranks *= 2;
   const int64_t held = std::min<int64_t>(kHeld, a.c.max_pages);
   const size_t smem = static_cast<size_t>(query_bytes(p.head_chunk, D)) + held * 4;
-  auto kern = fa_page_select_kernel<D, BF16>;
+  auto kern = fa_page_select_kernel<T, D, BF16>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kQuerySmem + kHeld * 4);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, units * ranks, kSelectThreads, static_cast<int>(smem), a.stream,
-                       static_cast<unsigned>(ranks), p, ranks);
+  return launch_kernel(kern, units * ranks, T, static_cast<int>(smem), a.stream, static_cast<unsigned>(ranks), p,
+                       ranks);
+}
+
+// Few units: more threads each (one sequence of 2048 pages and 8 KV heads: 11.4
+// us with 512, 13.7 with 256); many: more blocks per SM (B32 ragged: 35 and 26).
+template <int D, bool BF16>
+cudaError_t run_select_threads(const SelectLaunch& a) {
+  const bool few = static_cast<int64_t>(a.c.B) * a.c.Hkv * kSelectRanks <= device_sm_count();
+  return few ? run_select<512, D, BF16>(a) : run_select<256, D, BF16>(a);
 }
 
 template <bool BF16>
 cudaError_t run_select_dt(const SelectLaunch& a) {
   switch (a.c.D) {
-    case 64: return run_select<64, BF16>(a);
-    case 96: return run_select<96, BF16>(a);
-    case 128: return run_select<128, BF16>(a);
-    default: return run_select<256, BF16>(a);
+    case 64: return run_select_threads<64, BF16>(a);
+    case 96: return run_select_threads<96, BF16>(a);
+    case 128: return run_select_threads<128, BF16>(a);
+    default: return run_select_threads<256, BF16>(a);
   }
 }
 

@@ -356,10 +356,11 @@ def test_select_where_one_score_is_far_from_the_rest():
     check_select(q2, bounds * 2.0 ** -30, table, lens, page, 300, 0, 0)
 
 
+@pytest.mark.parametrize("copies", [1, 6])  # few and many blocks
 @pytest.mark.parametrize("kind", ["equal", "pairs", "zero_query", "two_values"])
-def test_select_ties_go_to_the_lower_page(kind):
+def test_select_ties_go_to_the_lower_page(kind, copies):
     g = gen(31)
-    B, Hq, Hkv, D, page, lens = 2, 4, 2, 128, 16, [4800, 1605]
+    B, Hq, Hkv, D, page, lens = 2 * copies, 4, 2, 128, 16, [4800, 1605] * copies
     table, P = make_table(g, B, 300)
     bounds, q = bounds_for(g, P, Hkv, D, torch.bfloat16), randn(g, B, Hq, 1, D, dtype=torch.bfloat16)
     if kind == "equal":
@@ -376,13 +377,16 @@ def test_select_ties_go_to_the_lower_page(kind):
         check_select(q, bounds, table, lens, page, n_sel, 1, 1)
 
 
+@pytest.mark.parametrize("B", [1, 20])
 @pytest.mark.parametrize("dt", ["fp16", "bf16"])
-def test_select_near_ties_as_in_64_bits(dt):
+def test_select_near_ties_as_in_64_bits(dt, B):
     """Scores whose large parts cancel and whose small rest decides: sums in 32 bits would rank them by their rounding."""
     g = gen(77)
-    B, Hq, Hkv, D, page, lens = 1, 1, 1, 256, 16, [6400]
+    Hq, Hkv, D, page, lens = 1, 1, 256, 16, [6400] + [1600] * (B - 1)
     dtype = DT[dt]
-    table, P = make_table(g, B, 400)
+    table, P = make_table(g, B, 400, spare=0)
+    table = table % 400  # every sequence over the same 400 pages
+    P = 400
     q = torch.ones(B, Hq, 1, D).to(dtype)
     big = randn(g, D // 2, dtype=dtype) * 512
     row = torch.cat([big, -big])
