@@ -658,6 +658,42 @@ def test_decoding_step_in_a_graph_replayed_at_other_lengths():
     assert torch.equal(s["kv"].k, eager["kv"].k) and torch.equal(s["kv"].k_bounds, eager["kv"].k_bounds)
 
 
+def test_calls_of_different_shapes_and_graphs_share_a_workspace():
+    """One workspace for calls of several shapes in turn, eagerly and as graphs replayed in between: what one leaves there
+    is nothing to the next, and a replay finds its counters as at first."""
+    shapes = [(2, 8, 2, 128, 64, 1, [9000, 7001]), (1, 14, 2, 64, 16, 5, [12345]), (3, 4, 1, 256, 32, 1, [3000, 1, 5000]),
+              (1, 64, 1, 128, 128, 1, [20000]), (1, 1, 1, 96, 16, 1, [40000])]
+    size = max(fa.fa_paged_workspace_size(hq, hkv, tq, d) for _, hq, hkv, d, _, tq, _ in shapes)
+    ws = torch.full((size,), 77, dtype=torch.uint8, device="cuda")
+    calls = []
+    for i, (B, Hq, Hkv, D, page, Tq, lens) in enumerate(shapes):
+        k, v, table, q = paged_inputs(B, Hq, Hkv, D, page, Tq, lens, torch.bfloat16, seed=70 + i)
+        kv, qd = handle(k, v, table, i32(lens)), q.cuda()
+        o, lse = torch.empty_like(qd), torch.empty(qd.shape[:3], device="cuda")
+        ref = paged_ref.attend(q, k, v, table, lens, 0.1, True, 0)
+        calls.append((lambda kv=kv, qd=qd, o=o, lse=lse: fa.fa_paged_fwd(kv, qd, o, lse, 0.1, causal=True, workspace=ws),
+                      o, lse, ref))
+    firsts = []
+    for call, o, lse, ref in calls:
+        call()
+        check_attend(o, lse, ref)
+        firsts.append((o.clone(), lse.clone()))
+    graphs = []
+    for call, *_ in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append(graph)
+    g = gen(3)
+    for n in range(60):
+        i = int(torch.randint(0, len(calls), (1,), generator=g))
+        call, o, lse, _ = calls[i]
+        o.fill_(NAN)
+        graphs[i].replay() if n % 3 else call()
+        assert torch.equal(o, firsts[i][0]) and torch.equal(lse, firsts[i][1]), (n, i)
+    assert status_clear()
+
+
 def test_two_streams_with_a_workspace_each():
     lens = [3000, 2000]
     a = paged_inputs(2, 8, 2, 128, 64, 1, lens, torch.bfloat16, seed=60)
