@@ -4,7 +4,9 @@ Thin Python binding over the C ABI of ``libfa_gb300.so`` (declared in
 ``include/fa.h``): it only turns torch tensors into pointers and sizes, calls
 the C function, and raises ``FaError`` on a non-zero status. Every step of the
 computation runs in the library's CUDA kernels; there is no fallback. If the
-library has not been built, every call raises.
+library has not been built, every call raises. The paged-cache calls, made once
+per layer and token, go through a compiled binding (csrc/paged_binding.cpp)
+instead of ctypes.
 
     import attention_fa_fwd_03_gb300 as fa
     fa.fa_fwd(q, k, v, o, lse, scale, causal=True)
@@ -242,8 +244,7 @@ class PagedKV:
     """
 
     __slots__ = ("k", "v", "page_table", "kv_lens", "k_bounds", "device", "dtype", "B", "Hkv", "D",
-                 "num_pages", "page_size", "max_pages", "_struct", "_ref", "_index", "_lib", "_cuda",
-                 "_i32", "_f32", "_lens_shape", "_sel_lens_shape")
+                 "num_pages", "page_size", "max_pages", "_handle", "_calls")
 
     def __init__(self, k, v, page_table, kv_lens, k_bounds=None):
         import torch
@@ -253,85 +254,36 @@ class PagedKV:
         self.B, self.max_pages = page_table.shape
         self.device, self.dtype = k.device, k.dtype
         code = _dtype_code(k)
-        self._index = k.get_device()
-        self._i32, self._f32 = torch.int32, torch.float32
-        self._lens_shape, self._sel_lens_shape = (self.B,), (self.B, self.Hkv)
-        ptrs = [_ptr(k), _address("v", v, k.shape, k.dtype, self),
-                None if k_bounds is None else
-                _address("k_bounds", k_bounds, (self.num_pages, self.Hkv, 2, self.D), k.dtype, self),
-                _address("page_table", page_table, page_table.shape, torch.int32, self),
-                _address("kv_lens", kv_lens, self._lens_shape, torch.int32, self)]
+        ptrs = [_ptr(k), self._pointer("v", v, k.shape, k.dtype),
+                0 if k_bounds is None else
+                self._pointer("k_bounds", k_bounds, (self.num_pages, self.Hkv, 2, self.D), k.dtype),
+                self._pointer("page_table", page_table, page_table.shape, torch.int32),
+                self._pointer("kv_lens", kv_lens, (self.B,), torch.int32)]
+        if max(self.num_pages, self.Hkv, self.page_size, self.D, self.B, self.max_pages) > 2 ** 31 - 1:
+            raise ValueError("a size is beyond 32 bits")
         self.k, self.v, self.k_bounds = k, v, k_bounds
         self.page_table, self.kv_lens = page_table, kv_lens
-        self._lib, self._cuda = library(), torch.cuda
-        self._struct = _PagedKVStruct(*ptrs, self.B, self.Hkv, self.D, self.num_pages, self.page_size,
-                                      self.max_pages, code)
-        self._ref = ctypes.byref(self._struct)
+        self._calls = _paged_calls()
+        self._handle = self._calls.handle(*ptrs, self.B, self.Hkv, self.D, self.num_pages, self.page_size,
+                                          self.max_pages, code, self.device.index)
+
+    def _pointer(self, name: str, t, shape, dtype) -> int:
+        if t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"{name}: expected {dtype} of shape {list(shape)}, got {t.dtype} of shape {list(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{name}: expected on {self.device}, got {t.device}")
+        return _ptr(t)
 
 
-def _address(name: str, t, shape, dtype, kv) -> int:
-    """Address of a contiguous tensor of this shape and dtype on the cache's device."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name}: expected {dtype} of shape {list(shape)}, got {t.dtype} of shape {list(t.shape)}")
-    if t.get_device() != kv._index:
-        raise ValueError(f"{name}: expected on {kv.device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
-
-
-def _token_view(name: str, t, shape, kv):
-    """Address and three strides of a [B, H, T, D] view whose innermost index is contiguous."""
-    if t.dtype is not kv.dtype or t.shape != shape or t.get_device() != kv._index:
-        raise ValueError(f"{name}: expected {kv.dtype} of shape {list(shape)} on {kv.device}, got "
-                         f"{t.dtype} of shape {list(t.shape)} on {t.device}")
-    sb, sh, st, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name}: the innermost index must be contiguous")
-    # the stride of an index of size 1 is never used and can be anything
-    B, H, T, _ = shape
-    return t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0
-
-
-_Strides = ctypes.c_int64 * 9  # of k, v and q, three each
-
-
-def _workspace(t, kv, what: str):
-    """Address and bytes of a workspace tensor."""
-    if t is None:
-        raise ValueError(f"{what} needs a workspace tensor (the library never allocates)")
-    if t.get_device() != kv._index:
-        raise ValueError(f"workspace: expected on {kv.device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
-    return t.data_ptr(), t.nbytes
-
-
-def _raw_stream(index: int) -> int:
-    """The current stream of device ``index``. PyTorch's own accessor of the raw handle where it
-    has one: a Stream object costs as much as a kernel launch."""
-    global _raw_stream
-    import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _raw_stream = get or (lambda i: torch.cuda.current_stream(i).cuda_stream)
-    return _raw_stream(index)
-
-
-def _launch(kv, fn, what: str, stream, *args) -> None:
-    """Call ``fn`` on ``stream`` (default: the current stream of the cache's
-    device) with that device current."""
-    index = kv._index
-    if stream is None:
-        stream = _raw_stream(index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if kv._cuda.current_device() == index:
-        st = fn(kv._ref, *args, stream)
-    else:
-        with kv._cuda.device(index):
-            st = fn(kv._ref, *args, stream)
-    if st != 0:
-        raise FaError(st, what)
+def _paged_calls():
+    """The compiled binding of the paged calls."""
+    library()
+    try:
+        from . import _paged
+    except ImportError as e:
+        raise RuntimeError("binding of the paged calls not built: _paged.so is missing or does not load "
+                           f"(run `python -c 'import __graft_entry__ as g; g.build()'`): {e}") from e
+    return _paged
 
 
 def fa_kv_append(kv: PagedKV, k, v, cos=None, sin=None, interleaved: bool = False, q=None,
@@ -346,35 +298,9 @@ def fa_kv_append(kv: PagedKV, k, v, cos=None, sin=None, interleaved: bool = Fals
     None for no rotation. ``kv.kv_lens`` counts the new tokens already;
     ``new_lens`` [B] int32 says how many of the T rows of each sequence are
     tokens (None: all)."""
-    B, Hkv, D = kv.B, kv.Hkv, kv.D
-    T = k.shape[2] if k.dim() == 4 else 0
-    kp, k0, k1, k2 = _token_view("k", k, (B, Hkv, T, D), kv)
-    vp, v0, v1, v2 = _token_view("v", v, (B, Hkv, T, D), kv)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    qp = qo = None
-    Hq = q0 = q1 = q2 = 0
-    if q is not None:
-        shape = q.shape
-        Hq = shape[1] if len(shape) == 4 else 0
-        qp, q0, q1, q2 = _token_view("q", q, (B, Hq, T, D), kv)
-        qo = _address("q_out", q_out, shape, kv.dtype, kv)
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin go together")
-    cp = sp = None
-    rope_len = rot_dim = 0
-    if cos is not None:
-        shape = cos.shape
-        if len(shape) != 2:
-            raise ValueError("cos and sin are [positions, rot_dim / 2]")
-        rope_len, rot_dim = shape[0], 2 * shape[1]
-        cp = _address("cos", cos, shape, kv._f32, kv)
-        sp = _address("sin", sin, shape, kv._f32, kv)
-    nl = None if new_lens is None else _address("new_lens", new_lens, kv._lens_shape, kv._i32, kv)
-    strides = _Strides(k0, k1, k2, v0, v1, v2, q0, q1, q2)
-    at = ctypes.addressof(strides)
-    _launch(kv, kv._lib.fa_kv_append, "fa_kv_append", stream, kp, at, vp, at + 24, qp, at + 48, qo, Hq, T,
-            nl, cp, sp, rope_len, rot_dim, 1 if interleaved else 0)
+    st = kv._calls.kv_append(kv._handle, k, v, cos, sin, interleaved, q, q_out, new_lens, stream)
+    if st != 0:
+        raise FaError(st, "fa_kv_append")
 
 
 def fa_paged_workspace_size(Hq: int, Hkv: int, Tq: int, D: int) -> int:
@@ -390,23 +316,10 @@ def fa_paged_fwd(kv: PagedKV, q, o, lse, scale: float, causal: bool = False, win
     and window masks go by position in the sequence. ``sel`` [B, Hkv, n_sel]
     and ``sel_lens`` [B, Hkv] int32 restrict each KV head to these pages.
     ``workspace`` has fa_paged_workspace_size(Hq, Hkv, Tq, D) bytes."""
-    wp, wn = _workspace(workspace, kv, "fa_paged_fwd")
-    shape = q.shape
-    if len(shape) != 4 or shape[0] != kv.B or shape[3] != kv.D:
-        raise ValueError(f"q: expected [{kv.B}, Hq, Tq, {kv.D}], got {list(shape)}")
-    if (sel is None) != (sel_lens is None):
-        raise ValueError("sel and sel_lens go together")
-    sp = slp = nl = None
-    n_sel = 0
-    if sel is not None:
-        n_sel = sel.shape[-1]
-        sp = _address("sel", sel, (kv.B, kv.Hkv, n_sel), kv._i32, kv)
-        slp = _address("sel_lens", sel_lens, kv._sel_lens_shape, kv._i32, kv)
-    if new_lens is not None:
-        nl = _address("new_lens", new_lens, kv._lens_shape, kv._i32, kv)
-    _launch(kv, kv._lib.fa_paged_fwd, "fa_paged_fwd", stream, _address("q", q, shape, kv.dtype, kv),
-            _address("o", o, shape, kv.dtype, kv), _address("lse", lse, shape[:3], kv._f32, kv),
-            shape[1], shape[2], scale, 1 if causal else 0, window, nl, sp, slp, n_sel, wp, wn)
+    st = kv._calls.paged_fwd(kv._handle, q, o, lse, scale, causal, window, new_lens, sel, sel_lens,
+                             workspace, stream)
+    if st != 0:
+        raise FaError(st, "fa_paged_fwd")
 
 
 def fa_page_select_workspace_size(B: int, Hkv: int, max_pages: int) -> int:
@@ -421,15 +334,9 @@ def fa_page_select(kv: PagedKV, q, sel, sel_lens, keep_first: int = 0, keep_last
     ``sel_lens`` [B, Hkv] int32 how many. ``q`` [B, Hq, 1, D]. The first
     ``keep_first`` and last ``keep_last`` pages are always chosen.
     ``workspace`` has fa_page_select_workspace_size(B, Hkv, max_pages) bytes."""
-    wp, wn = _workspace(workspace, kv, "fa_page_select")
-    shape = q.shape
-    if len(shape) != 4 or shape[0] != kv.B or shape[2] != 1 or shape[3] != kv.D:
-        raise ValueError(f"q: expected [{kv.B}, Hq, 1, {kv.D}], got {list(shape)}")
-    n_sel = sel.shape[-1]
-    _launch(kv, kv._lib.fa_page_select, "fa_page_select", stream, _address("q", q, shape, kv.dtype, kv),
-            shape[1], n_sel, keep_first, keep_last,
-            _address("sel", sel, (kv.B, kv.Hkv, n_sel), kv._i32, kv),
-            _address("sel_lens", sel_lens, kv._sel_lens_shape, kv._i32, kv), wp, wn)
+    st = kv._calls.page_select(kv._handle, q, sel, sel_lens, keep_first, keep_last, workspace, stream)
+    if st != 0:
+        raise FaError(st, "fa_page_select")
 
 
 def fa_selftest_wait_timeout(timeout_ms: int, stream=None) -> None:

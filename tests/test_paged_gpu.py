@@ -729,3 +729,54 @@ def test_an_explicit_stream_is_used():
         fa.fa_paged_fwd(kv, q, o, lse, 0.1, causal=True, workspace=ws, stream=handle_)
         st.synchronize()
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_binding_refusals_on_the_gpu():
+    """What the binding checks of the tensors, and what the library refuses, raise and launch nothing."""
+    lens = [40, 33]
+    k, v, table, q = paged_inputs(2, 4, 2, 64, 16, 1, lens, torch.float16, seed=90)
+    kv = handle(k, v, table, i32(lens), torch.zeros(k.shape[0], 2, 2, 64, dtype=torch.float16))
+    bare = handle(k, v, table, i32(lens))
+    q, ws = q.cuda(), torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    o, lse = torch.zeros_like(q), torch.zeros(2, 4, 1, device="cuda")
+    sel, n = torch.zeros(2, 2, 3, dtype=torch.int32, device="cuda"), torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+
+    def fwd(kv=kv, **kw):
+        a = dict(q=q, o=o, lse=lse, scale=0.1, causal=True, workspace=ws)
+        a.update(kw)
+        fa.fa_paged_fwd(kv, a.pop("q"), a.pop("o"), a.pop("lse"), a.pop("scale"), **a)
+
+    for bad in (dict(q=q.bfloat16()), dict(o=o.float()), dict(lse=lse.half()), dict(o=o[:1]), dict(lse=lse[..., 0]),
+                dict(q=q.cpu()), dict(workspace=None), dict(workspace=ws.cpu()), dict(sel=sel), dict(sel_lens=n),
+                dict(sel=sel.long(), sel_lens=n), dict(sel=sel, sel_lens=n[:1]), dict(new_lens=i32([1, 1])),
+                dict(new_lens=i32([1]).cuda()), dict(q=q.transpose(1, 2)), dict(workspace=ws[::2])):
+        with pytest.raises(ValueError):
+            fwd(**bad)
+    for bad in (dict(scale=0.0), dict(window=-1), dict(workspace=ws[:64]), dict(o=q)):
+        with pytest.raises(fa.FaError):
+            fwd(**bad)
+    with pytest.raises(fa.FaError):  # misaligned
+        buf = torch.zeros(q.numel() + 8, dtype=q.dtype, device="cuda")
+        fwd(q=buf[4:4 + q.numel()].view(q.shape))
+    with pytest.raises((ValueError, OverflowError)):
+        fwd(window=2 ** 40)
+    with pytest.raises(fa.FaError):
+        fa.fa_page_select(bare, q, sel, n, workspace=ws)  # no bounds
+    with pytest.raises(fa.FaError):
+        fa.fa_page_select(kv, q, sel, n, keep_first=2, keep_last=2, workspace=ws)
+    new = torch.zeros(2, 2, 1, 64, dtype=torch.float16, device="cuda")
+    cos = torch.ones(64, 32, device="cuda")
+    for bad in (dict(cos=cos), dict(cos=cos, sin=cos[:3]), dict(q=q), dict(q=q, q_out=o[:, :2]), dict(cos=cos.half(), sin=cos)):
+        with pytest.raises(ValueError):
+            fa.fa_kv_append(kv, new, new.clone(), **bad)
+    with pytest.raises(ValueError):
+        fa.fa_kv_append(kv, new.transpose(2, 3).contiguous().transpose(2, 3)[..., ::2], new)
+    odd = torch.zeros(2, 2, 1, 68, dtype=torch.float16, device="cuda")[..., :64]  # head stride no multiple of 8
+    with pytest.raises(fa.FaError):
+        fa.fa_kv_append(kv, odd, new)
+    with pytest.raises(fa.FaError):
+        fa.fa_kv_append(kv, new, new.clone(), cos=cos[:, :12].contiguous(), sin=cos[:, :12].contiguous())  # rot_dim 24
+    torch.cuda.synchronize()
+    assert (o == 0).all() and status_clear()
+    fwd()
+    assert status_clear() and torch.isfinite(o).all()

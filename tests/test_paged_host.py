@@ -177,3 +177,51 @@ def test_binding_refuses_cpu_and_mismatched_tensors(lib):
         fa.PagedKV(pool, pool.clone(), table, torch.ones(2, dtype=torch.int32))
     with pytest.raises(fa.FaError):
         fa.PagedKV(pool.float(), pool.float(), table, lens)  # fp32 pools
+
+
+# ------------------------------------------------------------------ the compiled binding
+@pytest.fixture(scope="module")
+def calls(lib):
+    return fa._paged_calls()
+
+
+def fake_handle(calls, dt=0):
+    """A cache of B 2, Hkv 2, D 64 on device 0 at addresses that nothing is at: every call below is refused before it
+    would use them."""
+    return calls.handle(addr(0), addr(1), addr(2), addr(3), addr(4), 2, 2, 64, 40, 16, 8, dt, 0)
+
+
+def half(*shape):
+    return torch.zeros(shape, dtype=torch.float16)
+
+
+def test_binding_refuses_what_is_no_tensor_or_not_on_the_device(calls):
+    h = fake_handle(calls)
+    q, lse, ws = half(2, 4, 1, 64), torch.zeros(2, 4, 1), torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        calls.paged_fwd(h, q, q)                                                     # too few arguments
+    with pytest.raises(ValueError, match="workspace"):
+        calls.paged_fwd(h, q, q.clone(), lse, 0.1, True, 0, None, None, None, None, None)
+    with pytest.raises(ValueError):                                                  # CPU tensors
+        calls.paged_fwd(h, q, q.clone(), lse, 0.1, True, 0, None, None, None, ws, None)
+    with pytest.raises(TypeError):
+        calls.kv_append(h, 3, q, None, None, False, None, None, None, None)
+    k = half(2, 2, 1, 64)
+    with pytest.raises(ValueError, match="k"):
+        calls.kv_append(h, k, k.clone(), None, None, False, None, None, None, None)  # CPU tensors
+    with pytest.raises(ValueError, match="k"):
+        calls.kv_append(h, k.float(), k, None, None, False, None, None, None, None)  # dtype
+    with pytest.raises(ValueError, match="k"):
+        calls.kv_append(h, half(2, 2, 64), k, None, None, False, None, None, None, None)  # three dimensions
+    with pytest.raises(ValueError):
+        calls.page_select(h, q, torch.zeros(2, 2, 4, dtype=torch.int32), torch.zeros(2, 2, dtype=torch.int32), 0, 1, ws, None)
+    with pytest.raises(ValueError):
+        calls.paged_fwd(object(), q, q, lse, 0.1, True, 0, None, None, None, ws, None)  # no handle
+
+
+def test_missing_binding_fails_loudly(lib, monkeypatch):
+    import sys
+    monkeypatch.setitem(sys.modules, "attention_fa_fwd_03_gb300._paged", None)
+    monkeypatch.delattr(fa, "_paged", raising=False)
+    with pytest.raises(RuntimeError, match="not built"):
+        fa._paged_calls()
