@@ -88,11 +88,28 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t x, uint32_t y) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Scores of pages keep_first + [begin, end) of (b, g): put(i, key) for each, by
-// one lane; get(i) gives back what was put (heads beyond head_chunk).
+// Pool pages of the rows that this thread of CTA `rank` takes in its first pass, as
+// the page table has them: read before the lengths are known, checked after.
+struct FirstRows {
+  int id[2];
+};
+template <int T>
+__device__ __forceinline__ FirstRows first_rows(const SelectArgs& p, int b, int rank) {
+  FirstRows f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int page = p.keep_first + rank * (T / 2) + 16 * (threadIdx.x >> 5) + ((threadIdx.x & 31) >> 2) + 8 * k;
+    f.id[k] = page < p.c.max_pages ? __ldg(p.c.table + static_cast<int64_t>(b) * p.c.max_pages + page) : -1;
+  }
+  return f;
+}
+
+// Scores of the pages keep_first + i, i < end, of (b, g) that are rank `rank`'s of
+// `ranks`: passes of T / 2 in turn. put(i, key) for each, by one lane; get(i) gives
+// back what was put (heads beyond head_chunk).
 template <int T, int D, bool BF16, class Put, class Get>
-__device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* qs, int b, int g, int begin, int end,
-                                                  const Put& put, const Get& get) {
+__device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* qs, int b, int g, int rank, int ranks,
+                                                  int end, const FirstRows& firsts, const Put& put, const Get& get) {
   constexpr int CH = D / 32, BATCH = CH == 3 ? 3 : 2;  // a thread's chunks of a row, and how many at a time
   constexpr int PITCH = query_pitch(D);
   const PagedView& c = p.c;
@@ -105,11 +122,16 @@ __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* 
   const uint4* src[2];
   bool there[2];
   uint4 lo[2][BATCH], hi[2][BATCH];
+  const int begin = rank * (T / 2), step = ranks * (T / 2);
   auto find_rows = [&](int base) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = base + row + 8 * k;
-      const int id = i < end ? pool_page(c, b, p.keep_first + i) : -1;
+      int id = -1;
+      if (base == begin + 16 * warp)
+        id = i < end ? checked_page(c, firsts.id[k]) : -1;
+      else if (i < end)
+        id = pool_page(c, b, p.keep_first + i);
       there[k] = id >= 0;
       src[k] = reinterpret_cast<const uint4*>(c.bounds + (static_cast<int64_t>(max(id, 0)) * c.Hkv + g) * 2 * D) + col;
     }
@@ -149,7 +171,7 @@ __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* 
       *reinterpret_cast<uint32_t*>(qmag + 4 * d2) = m;
     }
     __syncthreads();
-    for (int base = begin + 16 * warp; base < end; base += T / 2) {
+    for (int base = begin + 16 * warp; base < end; base += step) {
       if (base != begin + 16 * warp) {
         find_rows(base);
         load_rows(0);
@@ -272,9 +294,11 @@ __device__ __forceinline__ K kth_largest(BlockCounts& counts, int n, int need, K
   return t;
 }
 
-// Exclusive prefix sum over the block's threads, and the total. Three barriers.
+// Exclusive prefix sum over the block's threads, and the total. One barrier: calls
+// in a row take the two halves of warp_sums in turn.
 template <int T>
-__device__ __forceinline__ int block_before(int x, int* warp_sums, int* total) {
+__device__ __forceinline__ int block_before(int x, int (*halves)[T / 32], int turn, int* total) {
+  int* warp_sums = halves[turn & 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int incl = x;
 #pragma unroll
@@ -282,7 +306,6 @@ __device__ __forceinline__ int block_before(int x, int* warp_sums, int* total) {
     const int y = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += y;
   }
-  __syncthreads();  // the previous use of warp_sums is over
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
   static_assert(T / 32 <= 32, "one warp adds the warps' sums");
@@ -307,7 +330,7 @@ template <int T>
 struct SearchSmem {
   int bins[kBins];
   uint32_t keys[kFewKeys];
-  int warp_sums[(T / 32)];
+  int warp_sums[2][T / 32];
   int bin, above, inside, count;
   uint32_t found;
 };
@@ -315,6 +338,25 @@ template <int T, class Get>
 __device__ __forceinline__ uint32_t kth_largest_score(SearchSmem<T>& sm, int n, int need, uint32_t lo, uint32_t hi,
                                                       const Get& get) {
   constexpr int PER = kBins / T;
+  if (lo == hi) return lo;
+  if (n <= T) {
+    // few keys: each against all of them
+    const int i = threadIdx.x;
+    if (i < n) {
+      const uint32_t k = get(i);
+      int more = 0, equal = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        const uint32_t x = get(j);
+        more += x > k;
+        equal += x == k;
+      }
+      if (more < need && need <= more + equal) sm.found = k;  // equal keys write the same value
+    }
+    __syncthreads();
+    return sm.found;
+  }
+  int turn = 0;
   while (true) {
     if (lo == hi) return lo;
     const int shift = max(0, 32 - __clz(hi - lo) - 11);
@@ -332,7 +374,7 @@ __device__ __forceinline__ uint32_t kth_largest_score(SearchSmem<T>& sm, int n, 
     int mine = 0, total;
 #pragma unroll
     for (int i = 0; i < PER; ++i) mine += sm.bins[kBins - 1 - PER * threadIdx.x - i];
-    int above = block_before<T>(mine, sm.warp_sums, &total);
+    int above = block_before<T>(mine, sm.warp_sums, turn++, &total);
     if (above < need && need <= above + mine) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
@@ -481,6 +523,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   const int unit = blockIdx.x / ranks, rank = blockIdx.x - unit * ranks;
   const int b = unit / c.Hkv, g = unit - b * c.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const FirstRows firsts = first_rows<T>(p, b, rank);
   const int pages = page_count(c, b);
   // pages keep_first + i, i < n, compete for `need` places
   const int need = p.n_sel - p.keep_first - p.keep_last;
@@ -490,17 +533,15 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   uint32_t* far = p.scores + static_cast<int64_t>(unit) * c.max_pages;
   cluster_wait();
   if (!all && need > 0) {
-    const int share = (n + ranks - 1) / ranks;
-    const int begin = min(n, rank * share), end = min(n, begin + share);
     ScoreStats st;
     if (ranks == 1 && in_smem)
-      st = score_pages<T, D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { held[i] = k; },
+      st = score_pages<T, D, BF16>(p, qs, b, g, rank, ranks, n, firsts, [&](int i, uint32_t k) { held[i] = k; },
                                 [&](int i) { return held[i]; });
     else if (in_smem && p.Hq / c.Hkv <= p.head_chunk)
-      st = score_pages<T, D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { st_first(held + i, k); },
+      st = score_pages<T, D, BF16>(p, qs, b, g, rank, ranks, n, firsts, [&](int i, uint32_t k) { st_first(held + i, k); },
                                 [&](int) { return 0u; });
     else
-      st = score_pages<T, D, BF16>(p, qs, b, g, begin, end, [&](int i, uint32_t k) { far[i] = k; },
+      st = score_pages<T, D, BF16>(p, qs, b, g, rank, ranks, n, firsts, [&](int i, uint32_t k) { far[i] = k; },
                                 [&](int i) { return far[i]; });
     st.a = warp_max(st.a);
     st.odd = __any_sync(0xffffffffu, st.odd);
@@ -522,7 +563,10 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
       st_first(&rank_stats[rank][threadIdx.x], x);
     }
     __syncwarp();
-    cluster_barrier();  // every CTA's scores are with the first
+    if (ranks > 1)
+      cluster_barrier();  // every CTA's scores are with the first
+    else
+      __syncthreads();
   }
   if (rank != 0) return;
 
@@ -669,6 +713,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     return k64 > cut ? 2 : k64 == cut ? 1 : 0;
   };
   // places in ascending order: a thread takes runs of four pages
+  int turn = 0;
   int at = p.keep_first, seen = 0;  // places given and equals met before this stretch
   for (int base = 0; base < n; base += 4 * T) {
     const int i0 = base + 4 * threadIdx.x;
@@ -688,7 +733,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
       ties += st[j] == 1;
     }
     if (ranked && !few) {
-      int t = seen + block_before<T>(ties, search.warp_sums, &total);
+      int t = seen + block_before<T>(ties, search.warp_sums, turn++, &total);
       seen += total;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -697,7 +742,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     int mine = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) mine += st[j] == 2;
-    int to = at + block_before<T>(mine, search.warp_sums, &total);
+    int to = at + block_before<T>(mine, search.warp_sums, turn++, &total);
     at += total;
 #pragma unroll
     for (int j = 0; j < 4; ++j)

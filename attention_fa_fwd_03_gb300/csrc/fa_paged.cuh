@@ -45,12 +45,16 @@ __device__ __forceinline__ SeqLens seq_lens(const PagedView& c, const int* new_l
   return {checked_count(c, len, c.max_pages << c.page_shift), checked_count(c, n, T)};
 }
 
-// Pool page of page `p` of sequence b (0 <= p < max_pages), or -1.
-__device__ __forceinline__ int pool_page(const PagedView& c, int b, int p) {
-  const int id = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + p);
+// A pool page, or -1 where the table holds none.
+__device__ __forceinline__ int checked_page(const PagedView& c, int id) {
   if (static_cast<unsigned>(id) < static_cast<unsigned>(c.num_pages)) return id;
   flag_bad_index(c);
   return -1;
+}
+
+// Pool page of page `p` of sequence b (0 <= p < max_pages), or -1.
+__device__ __forceinline__ int pool_page(const PagedView& c, int b, int p) {
+  return checked_page(c, __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + p));
 }
 
 // First element of row `slot` of KV head g in pool page `id`.

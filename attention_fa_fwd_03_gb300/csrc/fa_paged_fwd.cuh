@@ -40,7 +40,7 @@
 namespace fa {
 
 constexpr int kPagedKeyWarps = 4;    // warps that share a tile's keys, 16 each
-constexpr int kPagedMaxRanks = 8;    // CTAs of a cluster
+constexpr int kPagedMaxRanks = 16;   // CTAs of a cluster (above 8: allowed per kernel)
 constexpr int kPagedClusterTiles = 8;  // tiles per CTA up to which clusters are used
 
 struct PagedFwdArgs {
@@ -220,19 +220,17 @@ struct Walk {
     t1 = min(it.tiles, t0 + left);
     return true;
   }
-  // The slice of rank `rank` of the `ranks` CTAs that share unit `unit`; false
-  // when it is empty (it and sub are set all the same).
-  __device__ __forceinline__ bool start_slice(const PagedFwdArgs& p, int unit, int rank, int ranks) {
+  // Clusters: unit `unit` as one segment, of whose tiles rank `rank` takes every
+  // `ranks`-th, a power of two, from its own number on: [t0, t1) counts them.
+  __device__ __forceinline__ void start_unit(const PagedFwdArgs& p, int unit, int rank, int ranks) {
     mult = item_mult(p);
     items = item_count(p);
     item = unit / mult;
     sub = unit - item * mult;
     it = load_item(p, item);
-    const int base = it.tiles / ranks, more = it.tiles - base * ranks;
-    t0 = rank * base + min(rank, more);
-    t1 = t0 + base + (rank < more ? 1 : 0);
-    left = t1 - t0;
-    return left > 0;
+    t0 = 0;
+    t1 = (max(it.tiles - rank, 0) + ranks - 1) >> (31 - __clz(ranks));
+    left = t1;
   }
   __device__ __forceinline__ bool next(const PagedFwdArgs& p) {
     left -= t1 - t0;
@@ -386,8 +384,86 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int pieces = kPagedTile / piece;
     const uint32_t box = static_cast<uint32_t>(piece) * 128u;
     int issued = 0;
-    bool ok = C::CLUSTER ? w.start_slice(p, unit, rank, ranks) : w.start(p, share);
-    while (ok) {
+    bool ok = true;
+    // One tile of KV head g into the next stage: lane i < pieces has the page (in the
+    // sequence, and in the pool or -1) of its piece i, whose first key is key `x` of
+    // the list plus i pieces.
+    auto load_tile = [&](int x, int pg, int id, int g) {
+      const int slot = issued % C::STAGES;
+      if (issued >= C::STAGES)
+        ok = mbar_wait(smem_u32(&empty[slot]), ((issued / C::STAGES) - 1) & 1, tmo, &abort_flag, p.wc.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const int off = (x + lane * piece) & ((1 << c.page_shift) - 1);
+      const bool load = lane < pieces && id >= 0;
+      if (lane < C::KW) {
+        const int pl = (lane * 16) / piece;  // piece that holds this warp's keys
+        const int kpage = __shfl_sync(0xfu, pg, pl), kid = __shfl_sync(0xfu, id, pl), koff = __shfl_sync(0xfu, off, pl);
+        key_pos[slot][lane] = kid >= 0 ? (kpage << c.page_shift) + koff + lane * 16 - pl * piece : kNoPosition;
+      }
+      const unsigned loads = __ballot_sync(0xffffffffu, load);
+      const uint32_t bar = smem_u32(&full[slot]);
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
+      __syncwarp();
+      if (load) {
+        const uint32_t dst = sbase + C::OFF_KV + slot * 2 * C::TILE + lane * box;
+        const int z = id * c.Hkv + g;
+#pragma unroll
+        for (int r = 0; r < C::KREG; ++r) {
+          tma_load_3d(dst + r * C::REGION, &map_k, bar, r * 64, off, z);
+          tma_load_3d(dst + C::TILE + r * C::REGION, &map_v, bar, r * 64, off, z);
+        }
+      }
+      __syncwarp();
+      ++issued;
+    };
+    if constexpr (C::CLUSTER) {
+      // Lane k * pieces + i looks up piece i of the CTA's k-th tile, all at once
+      // (kPagedClusterTiles tiles of at most 4 pieces), and where no window moves the
+      // first tile, while the lengths that say which of it counts are still on
+      // their way: what is read too much is not used.
+      static_assert(kPagedClusterTiles * 4 <= 32, "one look-up for all tiles");
+      const int mult = item_mult(p), item = unit / mult;
+      const int b = p.sel ? item / c.Hkv : item;
+      const int g = p.sel ? item % c.Hkv : (unit - item * mult) / p.row_blocks;
+      const int64_t u = static_cast<int64_t>(b) * c.Hkv + g;
+      const int64_t row = static_cast<int64_t>(b) * c.max_pages;
+      const int tile = rank + lane / pieces * ranks, key = (lane & (pieces - 1)) * piece;
+      int pg = -1, id = -1, e = (tile * kPagedTile + key) >> c.page_shift;
+      auto read = [&] {
+        pg = e;
+        if (p.sel) pg = e < p.n_sel ? __ldg(p.sel + u * p.n_sel + e) : -1;
+        if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.max_pages)) id = __ldg(c.table + row + pg);
+      };
+      const bool at_once = p.sel != nullptr || p.window == 0;
+      if (at_once) read();
+      w.start_unit(p, unit, rank, ranks);
+      const int first = w.it.first * kPagedTile;
+      if (!at_once) {
+        e = (first + tile * kPagedTile + key) >> c.page_shift;
+        read();
+      }
+      const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
+      const int count = p.sel ? max(0, min(p.n_sel, __ldg(p.sel_lens + u))) : pages;
+      const bool counts = lane / pieces < w.t1 && e < count;
+      if (counts && static_cast<unsigned>(pg) < static_cast<unsigned>(pages)) {
+        if (static_cast<unsigned>(id) >= static_cast<unsigned>(c.num_pages)) {
+          flag_bad_index(c);
+          id = -1;
+        }
+      } else {
+        if (counts) flag_bad_index(c);  // a selected page that the sequence does not have
+        id = -1;
+      }
+      for (int t = 0; t < w.t1 && ok; ++t) {
+        const int from = t * pieces + (lane & (pieces - 1));
+        load_tile(first + (rank + t * ranks) * kPagedTile, __shfl_sync(0xffffffffu, pg, from),
+                  __shfl_sync(0xffffffffu, id, from), g);
+      }
+    } else {
+      ok = w.start(p, share);
+    }
+    while (!C::CLUSTER && ok) {
       const int g = w.kv_head(p);
       const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
       const int64_t u = static_cast<int64_t>(w.it.b) * c.Hkv + g;
@@ -413,7 +489,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       int page0, id0, page1, id1;
       look_up(e0 + lane, &page0, &id0);
       look_up(e0 + 32 + lane, &page1, &id1);
-      for (int t = w.t0; t < w.t1 && ok; ++t, ++issued) {
+      for (int t = w.t0; t < w.t1 && ok; ++t) {
         const int x = (w.it.first + t) * kPagedTile;  // first key of the tile in the list
         int e = (x >> c.page_shift) - e0;
         if (e >= 32) {
@@ -423,37 +499,9 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           id0 = id1;
           look_up(e0 + 32 + lane, &page1, &id1);
         }
-        const int slot = issued % C::STAGES;
-        if (issued >= C::STAGES)
-          ok = mbar_wait(smem_u32(&empty[slot]), ((issued / C::STAGES) - 1) & 1, tmo, &abort_flag, p.wc.status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
         // lane i looks at piece i of the tile
         const int my = e + ((lane * piece) >> c.page_shift);  // below 32: pages of 16 start tiles at multiples of 4
-        const int pg = __shfl_sync(0xffffffffu, page0, my & 31), id = __shfl_sync(0xffffffffu, id0, my & 31);
-        const int off = (x + lane * piece) & ((1 << c.page_shift) - 1);
-        const bool load = lane < pieces && id >= 0;
-        if (lane < C::KW) {
-          const int pl = (lane * 16) / piece;  // piece that holds this warp's keys
-          const int kpage = __shfl_sync(0xfu, pg, pl), kid = __shfl_sync(0xfu, id, pl), koff = __shfl_sync(0xfu, off, pl);
-          key_pos[slot][lane] = kid >= 0 ? (kpage << c.page_shift) + koff + lane * 16 - pl * piece : kNoPosition;
-        }
-        const unsigned loads = __ballot_sync(0xffffffffu, load);
-        const uint32_t bar = smem_u32(&full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
-        __syncwarp();
-        if (load) {
-          const uint32_t dst = sbase + C::OFF_KV + slot * 2 * C::TILE + lane * box;
-          const int z = id * c.Hkv + g;
-#pragma unroll
-          for (int r = 0; r < C::KREG; ++r) {
-            tma_load_3d(dst + r * C::REGION, &map_k, bar, r * 64, off, z);
-            tma_load_3d(dst + C::TILE + r * C::REGION, &map_v, bar, r * 64, off, z);
-          }
-        }
-        __syncwarp();
+        load_tile(x, __shfl_sync(0xffffffffu, page0, my & 31), __shfl_sync(0xffffffffu, id0, my & 31), g);
       }
       ok = ok && w.next(p);
     }
@@ -496,9 +544,12 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
-  // (with clusters: one segment, which may be empty)
-  for (bool more = C::CLUSTER ? w.start_slice(p, unit, rank, ranks) || true : w.start(p, share); more;
-       more = !C::CLUSTER && w.next(p)) {
+  bool more = true;  // clusters: one segment, which may be empty
+  if constexpr (C::CLUSTER)
+    w.start_unit(p, unit, rank, ranks);
+  else
+    more = w.start(p, share);
+  for (; more; more = !C::CLUSTER && w.next(p)) {
     const int g = w.kv_head(p), rb = w.row_block(p);
     const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
     const int64_t row0 = block_row0(p, w.it.b, g, rb, C::ROWS);
@@ -986,7 +1037,8 @@ cudaError_t launch_paged(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t grid,
       !encode_tile_map(&mv, a.c.v, C::BF16, C::D, page, a.c.num_pages * a.c.Hkv, piece))
     return cudaErrorInvalidValue;
   auto kern = fa_paged_fwd_kernel<C>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   if (!register_split_fits(reinterpret_cast<const void*>(kern), C::THREADS, C::REG_NEEDED))
     return cudaErrorInvalidConfiguration;
@@ -1015,10 +1067,15 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   const int64_t tiles = paged_tiles(1, keys);
   const int64_t units = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks;
   const int64_t wave = std::min<int64_t>(static_cast<int64_t>(device_sm_count()) * C::CTAS, kPagedMaxParts);
-  // Few short units: a cluster each, joined in the same launch.
+  // Short units: a cluster each (16 CTAs only on a whole GPU), joined in the same
+  // launch, where all clusters run at once or one CTA does for a unit. Measured: 16
+  // tiles, 4 units 4.6 us against 12.0 with the split list and its join; 64 tiles, 8
+  // units 7.1 us with 16 CTAs, 8.0 with 8 and 11.2 split.
   int ranks = 1;
-  while (ranks < kPagedMaxRanks && ranks < tiles) ranks *= 2;
-  if (tiles <= kPagedClusterTiles * ranks && units * ranks <= wave)
+  const int most_ranks = device_sm_count() >= 128 ? kPagedMaxRanks : 8;
+  while (ranks < most_ranks && ranks < tiles) ranks *= 2;
+  while (ranks > 1 && units * ranks > wave) ranks /= 2;
+  if (tiles <= kPagedClusterTiles * ranks)
     return launch_paged<PagedCfg<D, NT, RW, BF16, true>>(a, p, units * ranks, ranks);
   // no more CTAs than the longest possible list has tiles
   const int64_t parts = std::min(wave, units * tiles);
