@@ -324,6 +324,7 @@ __device__ __forceinline__ int block_before(int x, int (*halves)[T / 32], int tu
 // kBins equal ranges, the range of the wanted place, again within it until it
 // holds few keys, which are ranked against each other. Bins of scores are nearly
 // evenly filled, so one round is the rule; each round divides the range by kBins.
+// No more keys than threads, all `held` in shared memory, are ranked at once.
 constexpr int kBins = 2048;
 constexpr int kFewKeys = 256;
 template <int T>
@@ -336,20 +337,25 @@ struct SearchSmem {
 };
 template <int T, class Get>
 __device__ __forceinline__ uint32_t kth_largest_score(SearchSmem<T>& sm, int n, int need, uint32_t lo, uint32_t hi,
-                                                      const Get& get) {
+                                                      const uint32_t* held, const Get& get) {
   constexpr int PER = kBins / T;
   if (lo == hi) return lo;
-  if (n <= T) {
+  if (held != nullptr && n <= T) {
     // few keys: each against all of them
     const int i = threadIdx.x;
     if (i < n) {
-      const uint32_t k = get(i);
+      const uint32_t k = held[i];
       int more = 0, equal = 0;
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) {
-        const uint32_t x = get(j);
-        more += x > k;
-        equal += x == k;
+#pragma unroll 2
+      for (int j = 0; j + 3 < n; j += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(held + j);
+        more += (x.x > k) + (x.y > k) + (x.z > k) + (x.w > k);
+        equal += (x.x == k) + (x.y == k) + (x.z == k) + (x.w == k);
+      }
+#pragma unroll 1
+      for (int j = n & ~3; j < n; ++j) {
+        more += held[j] > k;
+        equal += held[j] == k;
       }
       if (more < need && need <= more + equal) sm.found = k;  // equal keys write the same value
     }
@@ -529,20 +535,20 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   const int need = p.n_sel - p.keep_first - p.keep_last;
   const int n = pages - p.keep_first - p.keep_last;
   const bool all = pages <= p.n_sel;  // the same in every CTA of the cluster
-  const bool in_smem = n <= kHeld;
+  // scores go to the first CTA's shared memory where they fit and are final at once
+  const bool local = n <= kHeld && p.Hq / c.Hkv <= p.head_chunk;
   uint32_t* far = p.scores + static_cast<int64_t>(unit) * c.max_pages;
   cluster_wait();
   if (!all && need > 0) {
-    ScoreStats st;
-    if (ranks == 1 && in_smem)
-      st = score_pages<T, D, BF16>(p, qs, b, g, rank, ranks, n, firsts, [&](int i, uint32_t k) { held[i] = k; },
-                                [&](int i) { return held[i]; });
-    else if (in_smem && p.Hq / c.Hkv <= p.head_chunk)
-      st = score_pages<T, D, BF16>(p, qs, b, g, rank, ranks, n, firsts, [&](int i, uint32_t k) { st_first(held + i, k); },
-                                [&](int) { return 0u; });
-    else
-      st = score_pages<T, D, BF16>(p, qs, b, g, rank, ranks, n, firsts, [&](int i, uint32_t k) { far[i] = k; },
-                                [&](int i) { return far[i]; });
+    ScoreStats st = score_pages<T, D, BF16>(
+        p, qs, b, g, rank, ranks, n, firsts,
+        [&](int i, uint32_t k) {
+          if (local)
+            st_first(held + i, k);
+          else
+            far[i] = k;
+        },
+        [&](int i) { return far[i]; });
     st.a = warp_max(st.a);
     st.odd = __any_sync(0xffffffffu, st.odd);
     st.lo = __reduce_min_sync(0xffffffffu, st.lo);
@@ -579,7 +585,6 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   for (int i = threadIdx.x; i < p.keep_first; i += T) sel[i] = i;
   for (int i = threadIdx.x; i < p.keep_last; i += T) sel[p.n_sel - p.keep_last + i] = pages - p.keep_last + i;
   if (need == 0) return;
-  const bool local = in_smem && (ranks == 1 || p.Hq / c.Hkv <= p.head_chunk);
   auto key32 = [&](int i) { return local ? held[i] : far[i]; };
   float a_max = 0.f;
   uint32_t odd = 0, key_lo = ~0u, key_hi = 0u;
@@ -595,7 +600,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   int sum[3];
   int sure = 0, between = n;
   if (!odd) {
-    const uint32_t tau = kth_largest_score<T>(search, n, need, key_lo, key_hi, key32);
+    const uint32_t tau = kth_largest_score<T>(search, n, need, key_lo, key_hi, local ? held : nullptr, key32);
     const float t = order_value(tau);
     // 2 E, with room for the error of A and the roundings of t -+ err
     const float err = 2.02f * D * 1.1920929e-7f * a_max + fabsf(t) * 2.4e-7f;
