@@ -244,64 +244,72 @@ fa_kv_append_kernel(const AppendArgs p) {
   }
 }
 
-// Many tokens. Warps in order of work: first, with bounds, (sequence, page, KV
-// head); then (sequence, group of consecutive tokens, rows of a few heads).
+// Many tokens. Blocks in order of work: first, with bounds, new keys by (sequence,
+// page, KV head), shared by one to eight warps; then, a warp each, (sequence, group of consecutive tokens, rows of a few heads).
 constexpr int kRowBatch = 4;  // rows of a thread, all loads in flight
 constexpr int kKeyBatch = 4;  // keys of a page likewise
 constexpr int kManyBlocks = 3;  // blocks per SM that registers are to allow
 constexpr int kAppendWarps = kAppendThreads / 32;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kAppendThreads, kManyBlocks)
-fa_kv_append_many_kernel(const AppendArgs p, int pages_per_seq, int64_t key_items, int groups_per_seq,
-                         int row_chunks, int64_t items) {
+fa_kv_append_many_kernel(const AppendArgs p, int pages_per_seq, int key_blocks, int key_warps, int groups_per_seq,
+                         int row_chunks, int64_t row_items) {
   constexpr int U = D / 16, TL = 32 / U;  // lanes of a row, rows side by side
+  __shared__ UnitBounds<BF16> sums[kAppendWarps][U];
+  __shared__ int filled[kAppendWarps];
   grid_wait_prior();
   grid_release_next();
   const PagedView& c = p.c;
-  const int lane = threadIdx.x & 31, u = lane % U, tl = lane / U;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
-  if (w >= items) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % U, tl = lane / U;
   const UnitPos at = unit_pos(p, u);
-  if (w < key_items) {
-    const int g = static_cast<int>(w % c.Hkv);
-    const int bp = static_cast<int>(w / c.Hkv);
+  if (blockIdx.x < key_blocks) {
+    // key_warps warps share an item, each the rows share * TL + tl, then key_warps * TL on
+    const int share = warp % key_warps;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kAppendWarps / key_warps) + warp / key_warps;
+    const int g = static_cast<int>(item % c.Hkv);
+    const int bp = static_cast<int>(item / c.Hkv);
     const int b = bp / pages_per_seq;
-    const NewTokens nt = new_tokens(p, b);
-    const int first = nt.first + nt.t0;  // first position written
-    const int page = (first >> c.page_shift) + (bp - b * pages_per_seq);
-    const int base = page << c.page_shift;
-    const int lo = max(first - base, 0), hi = min(nt.first + nt.t1 - base, 1 << c.page_shift);
-    if (lo >= hi || nt.t0 >= nt.t1) return;
-    const int id = pool_page(c, b, page);
-    if (id < 0) return;
-    const uint16_t* src = p.k + b * p.ks.b + g * p.ks.h + static_cast<int64_t>(base - nt.first) * p.ks.t;
-    uint16_t* dst = c.k + pool_row(c, id, g, 0);
     UnitBounds<BF16> bd;
+    int id = -1, lo = 0;
     bool any = false;
-    if (tl < TL) {
-      for (int s0 = lo + tl; s0 < hi; s0 += kKeyBatch * TL) {
-        Unit x[kKeyBatch];
+    if (b < c.B) {
+      const NewTokens nt = new_tokens(p, b);
+      const int first = nt.first + nt.t0;  // first position written
+      const int page = (first >> c.page_shift) + (bp - b * pages_per_seq);
+      const int base = page << c.page_shift;
+      lo = max(first - base, 0);
+      const int hi = min(nt.first + nt.t1 - base, 1 << c.page_shift);
+      if (lo < hi && nt.t0 < nt.t1) id = pool_page(c, b, page);
+      if (id >= 0 && tl < TL) {
+        const uint16_t* src = p.k + b * p.ks.b + g * p.ks.h + static_cast<int64_t>(base - nt.first) * p.ks.t;
+        uint16_t* dst = c.k + pool_row(c, id, g, 0);
+        const int step = key_warps * TL;
+        for (int s0 = lo + share * TL + tl; s0 < hi; s0 += kKeyBatch * step) {
+          Unit x[kKeyBatch];
 #pragma unroll
-        for (int i = 0; i < kKeyBatch; ++i)
-          if (s0 + i * TL < hi) x[i] = load_unit(src + (s0 + i * TL) * p.ks.t, at);
+          for (int i = 0; i < kKeyBatch; ++i)
+            if (s0 + i * step < hi) x[i] = load_unit(src + (s0 + i * step) * p.ks.t, at);
 #pragma unroll
-        for (int i = 0; i < kKeyBatch; ++i) {
-          const int s = s0 + i * TL;
-          if (s >= hi) break;
-          if (at.rotated) rotate_unit<BF16>(x[i].a, x[i].b, load_angles(p, base + s, u), p.interleaved);
-          store_unit(dst + s * D, at, x[i]);
-          if (!any)
-            bd.start(x[i]);
-          else
-            bd.widen(x[i], x[i]);
-          any = true;
+          for (int i = 0; i < kKeyBatch; ++i) {
+            const int s = s0 + i * step;
+            if (s >= hi) break;
+            if (at.rotated) rotate_unit<BF16>(x[i].a, x[i].b, load_angles(p, base + s, u), p.interleaved);
+            store_unit(dst + s * D, at, x[i]);
+            if (!any)
+              bd.start(x[i]);
+            else
+              bd.widen(x[i], x[i]);
+            any = true;
+          }
         }
       }
     }
-    // join the rows side by side: lanes without a key take lane u's, which has one
+    // join the rows side by side (lanes without a key take lane u's, which has one
+    // if any of its warp's has), then the item's warps
     Unit mn0, mx0;
     shuffle_unit(bd.mn, u, &mn0);
     shuffle_unit(bd.mx, u, &mx0);
+    const bool warp_any = __any_sync(0xffffffffu, any);
     if (!any) {
       bd.mn = mn0;
       bd.mx = mx0;
@@ -313,7 +321,12 @@ fa_kv_append_many_kernel(const AppendArgs p, int pages_per_seq, int64_t key_item
       shuffle_unit(bd.mx, (u + k * U) & 31, &x);
       if (tl == 0) bd.widen(m, x);
     }
-    if (tl == 0) {
+    if (tl == 0) sums[warp][u] = bd;
+    if (lane == 0) filled[warp] = warp_any;
+    __syncthreads();
+    if (share == 0 && tl == 0 && id >= 0) {  // the item's first warp has its first key
+      for (int k = 1; k < key_warps; ++k)
+        if (filled[warp + k]) bd.widen(sums[warp + k][u].mn, sums[warp + k][u].mx);
       uint16_t* br = bounds_row(c, id, g);
       if (lo > 0) {
         const Unit om = {*reinterpret_cast<const uint4*>(br + at.a), *reinterpret_cast<const uint4*>(br + at.b)};
@@ -325,7 +338,8 @@ fa_kv_append_many_kernel(const AppendArgs p, int pages_per_seq, int64_t key_item
     }
     return;
   }
-  const int64_t r = w - key_items;
+  const int64_t r = static_cast<int64_t>(blockIdx.x - key_blocks) * kAppendWarps + warp;
+  if (r >= row_items) return;
   int chunk = static_cast<int>(r % row_chunks);
   const int bg = static_cast<int>(r / row_chunks);
   const int b = bg / groups_per_seq;
@@ -379,12 +393,20 @@ cudaError_t run_append_many(const AppendLaunch& a, const AppendArgs& p) {
   const int page = 1 << a.c.page_shift;
   const int pages = (a.T + page - 2) / page + 1;  // that T tokens can touch
   const int64_t key_items = bounds ? static_cast<int64_t>(a.c.B) * pages * a.c.Hkv : 0;
+  // Few pages: more warps each, down to 16 keys (B2 T413, 128 keys a page: 19.3 us
+  // with one, 5.3 with eight); one warp each where that fills the GPU (B4 T4096, 64
+  // keys a page: 63.0 us with one, 68.2 with four).
+  int key_warps = 1;
+  while (key_warps < kAppendWarps && 16 * key_warps < page && key_items * key_warps < 8 * device_sm_count()) key_warps *= 2;
+  const int64_t key_blocks = (key_items * key_warps + kAppendWarps - 1) / kAppendWarps;
   const int groups = (a.T + TL - 1) / TL;
   const int kv_chunks = (a.c.Hkv + kRowBatch - 1) / kRowBatch;
   const int chunks = (bounds ? 1 : 2) * kv_chunks + (p.Hq + kRowBatch - 1) / kRowBatch;
-  const int64_t items = key_items + static_cast<int64_t>(a.c.B) * groups * chunks;
-  return launch_kernel(fa_kv_append_many_kernel<D, BF16>, (items + kAppendWarps - 1) / kAppendWarps, kAppendThreads, 0,
-                       a.stream, 1, p, pages, key_items, groups, chunks, items);
+  const int64_t row_items = static_cast<int64_t>(a.c.B) * groups * chunks;
+  const int64_t blocks = key_blocks + (row_items + kAppendWarps - 1) / kAppendWarps;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch_kernel(fa_kv_append_many_kernel<D, BF16>, blocks, kAppendThreads, 0, a.stream, 1, p, pages,
+                       static_cast<int>(key_blocks), key_warps, groups, chunks, row_items);
 }
 
 template <bool BF16>

@@ -41,7 +41,7 @@ namespace fa {
 
 constexpr int kPagedKeyWarps = 4;    // warps that share a tile's keys, 16 each
 constexpr int kPagedMaxRanks = 16;   // CTAs of a cluster (above 8: allowed per kernel)
-constexpr int kPagedClusterTiles = 8;  // tiles per CTA up to which clusters are used
+constexpr int kPagedClusterTiles = 16;  // tiles per CTA up to which clusters are used
 
 struct PagedFwdArgs {
   PagedView c;
@@ -418,47 +418,44 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       ++issued;
     };
     if constexpr (C::CLUSTER) {
-      // Lane k * pieces + i looks up piece i of the CTA's k-th tile, all at once
-      // (kPagedClusterTiles tiles of at most 4 pieces), and where no window moves the
-      // first tile, while the lengths that say which of it counts are still on
-      // their way: what is read too much is not used.
-      static_assert(kPagedClusterTiles * 4 <= 32, "one look-up for all tiles");
+      // Lane k * pieces + i looks up piece i of the k-th tile of a batch of as many of
+      // the CTA's tiles as 32 lanes hold, the first batch, where no window moves the
+      // first tile, while the lengths that say which of it counts are still on their
+      // way: what is read too much is not used.
       const int mult = item_mult(p), item = unit / mult;
       const int b = p.sel ? item / c.Hkv : item;
       const int g = p.sel ? item % c.Hkv : (unit - item * mult) / p.row_blocks;
       const int64_t u = static_cast<int64_t>(b) * c.Hkv + g;
       const int64_t row = static_cast<int64_t>(b) * c.max_pages;
-      const int tile = rank + lane / pieces * ranks, key = (lane & (pieces - 1)) * piece;
-      int pg = -1, id = -1, e = (tile * kPagedTile + key) >> c.page_shift;
-      auto read = [&] {
+      const int batch = 32 / pieces, mine = lane / pieces, key = (lane & (pieces - 1)) * piece;
+      int first = 0, pg = -1, id = -1, e = 0;
+      auto read = [&](int t0) {
+        e = (first + (rank + (t0 + mine) * ranks) * kPagedTile + key) >> c.page_shift;
         pg = e;
+        id = -1;
         if (p.sel) pg = e < p.n_sel ? __ldg(p.sel + u * p.n_sel + e) : -1;
         if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.max_pages)) id = __ldg(c.table + row + pg);
       };
-      const bool at_once = p.sel != nullptr || p.window == 0;
-      if (at_once) read();
+      const bool early = p.sel != nullptr || p.window == 0;
+      if (early) read(0);
       w.start_unit(p, unit, rank, ranks);
-      const int first = w.it.first * kPagedTile;
-      if (!at_once) {
-        e = (first + tile * kPagedTile + key) >> c.page_shift;
-        read();
-      }
+      first = w.it.first * kPagedTile;
       const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
       const int count = p.sel ? max(0, min(p.n_sel, __ldg(p.sel_lens + u))) : pages;
-      const bool counts = lane / pieces < w.t1 && e < count;
-      if (counts && static_cast<unsigned>(pg) < static_cast<unsigned>(pages)) {
-        if (static_cast<unsigned>(id) >= static_cast<unsigned>(c.num_pages)) {
-          flag_bad_index(c);
+      for (int t0 = 0; t0 < w.t1 && ok; t0 += batch) {
+        if (t0 > 0 || !early) read(t0);
+        const bool counts = t0 + mine < w.t1 && e < count;
+        if (counts && static_cast<unsigned>(pg) < static_cast<unsigned>(pages)) {
+          id = checked_page(c, id);
+        } else {
+          if (counts) flag_bad_index(c);  // a selected page that the sequence does not have
           id = -1;
         }
-      } else {
-        if (counts) flag_bad_index(c);  // a selected page that the sequence does not have
-        id = -1;
-      }
-      for (int t = 0; t < w.t1 && ok; ++t) {
-        const int from = t * pieces + (lane & (pieces - 1));
-        load_tile(first + (rank + t * ranks) * kPagedTile, __shfl_sync(0xffffffffu, pg, from),
-                  __shfl_sync(0xffffffffu, id, from), g);
+        for (int t = t0; t < min(w.t1, t0 + batch) && ok; ++t) {
+          const int from = (t - t0) * pieces + (lane & (pieces - 1));
+          load_tile(first + (rank + t * ranks) * kPagedTile, __shfl_sync(0xffffffffu, pg, from),
+                    __shfl_sync(0xffffffffu, id, from), g);
+        }
       }
     } else {
       ok = w.start(p, share);
@@ -1064,7 +1061,9 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   p.wc = a.wc;
   // tiles of the longest list a unit can have
   const int64_t keys = (a.sel ? static_cast<int64_t>(a.n_sel) : a.c.max_pages) << a.c.page_shift;
-  const int64_t tiles = paged_tiles(1, keys);
+  int64_t tiles = paged_tiles(1, keys);
+  if (a.window > 0 && !a.sel)  // window + Tq - 1 keys, wherever they start in a tile
+    tiles = std::min(tiles, (static_cast<int64_t>(a.window) + a.Tq - 2) / kPagedTile + 2);
   const int64_t units = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks;
   const int64_t wave = std::min<int64_t>(static_cast<int64_t>(device_sm_count()) * C::CTAS, kPagedMaxParts);
   // Short units: a cluster each (16 CTAs only on a whole GPU), joined in the same
