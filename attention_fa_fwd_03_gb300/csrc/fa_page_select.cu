@@ -324,9 +324,11 @@ __device__ __forceinline__ int block_before(int x, int (*halves)[T / 32], int tu
 // kBins equal ranges, the range of the wanted place, again within it until it
 // holds few keys, which are ranked against each other. Bins of scores are nearly
 // evenly filled, so one round is the rule; each round divides the range by kBins.
-// No more keys than threads, all `held` in shared memory, are ranked at once.
+// Up to kDirectKeys of them, `held` in shared memory, are ranked at once (123 keys:
+// 2.5 K cycles against 3.3 K; 343: 8.8 K).
 constexpr int kBins = 2048;
 constexpr int kFewKeys = 256;
+constexpr int kDirectKeys = 128;
 template <int T>
 struct SearchSmem {
   int bins[kBins];
@@ -340,7 +342,7 @@ __device__ __forceinline__ uint32_t kth_largest_score(SearchSmem<T>& sm, int n, 
                                                       const uint32_t* held, const Get& get) {
   constexpr int PER = kBins / T;
   if (lo == hi) return lo;
-  if (held != nullptr && n <= T) {
+  if (held != nullptr && n <= kDirectKeys) {
     // few keys: each against all of them
     const int i = threadIdx.x;
     if (i < n) {
