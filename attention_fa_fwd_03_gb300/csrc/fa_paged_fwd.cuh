@@ -502,8 +502,9 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       ok = ok && w.next(p);
     }
-    // after a wait gave up: let the loads still in flight land before the CTA exits
-    if (lane == 0 && abort_flag) drain_ring(smem_u32(&full[0]), C::STAGES, issued, p.wc.drain_cycles, p.wc.status);
+    // Stay until the last loads have landed: the consumers have waited for them too,
+    // unless one of their waits gave up.
+    if (lane == 0) drain_ring(smem_u32(&full[0]), C::STAGES, issued, p.wc.drain_cycles, p.wc.status);
     if constexpr (C::CLUSTER) {  // as the consumers do
       __syncwarp();
       cluster_wait();
@@ -1059,8 +1060,9 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   p.part_ml = reinterpret_cast<float2*>(a.ws + static_cast<size_t>(2 * kPagedMaxParts) * C::ROWS * C::D);
   p.joins = reinterpret_cast<int4*>(p.part_ml + 2 * kPagedMaxParts * C::ROWS);
   p.wc = a.wc;
-  // tiles of the longest list a unit can have
-  const int64_t keys = (a.sel ? static_cast<int64_t>(a.n_sel) : a.c.max_pages) << a.c.page_shift;
+  // tiles of the longest list a unit can have in earnest (of distinct pages; the
+  // kernels take any)
+  const int64_t keys = static_cast<int64_t>(a.sel ? std::min(a.n_sel, a.c.max_pages) : a.c.max_pages) << a.c.page_shift;
   int64_t tiles = paged_tiles(1, keys);
   if (a.window > 0 && !a.sel)  // window + Tq - 1 keys, wherever they start in a tile
     tiles = std::min(tiles, (static_cast<int64_t>(a.window) + a.Tq - 2) / kPagedTile + 2);

@@ -259,7 +259,8 @@ size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D);
  *     [0, n_sel], is a bad index.
  * Limit: B * Hkv * ceil(rows / 64) * ceil(keys / 64) < 2^31, rows = (Hq / Hkv) * Tq
  * (D = 256: / 32), keys = max_pages * page_size, with sel n_sel * page_size.
- * A row that sees no key, and every padding row, gets O = 0 and LSE = -inf.
+ * A row that sees no key (or whose every score is -inf), and every padding row,
+ * gets O = 0 and LSE = -inf.
  * Values of keys that no row sees never reach a result, whatever they hold. A
  * key that is visible to one row and hidden from another adds exactly nothing to
  * the latter as well.

@@ -780,3 +780,62 @@ def test_binding_refusals_on_the_gpu():
     assert (o == 0).all() and status_clear()
     fwd()
     assert status_clear() and torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("case", [(1, 8, 2, 128, 64, 1, [9000]), (2, 8, 2, 64, 16, 1, [700, 100]), (1, 14, 1, 128, 32, 5, [20000]),
+                                  (1, 24, 1, 256, 64, 1, [3000]), (1, 40, 1, 128, 64, 1, [600])],
+                         ids=lambda c: f"h{c[1]}x{c[2]}d{c[3]}T{c[5]}")
+def test_waits_that_give_up_end_cleanly(case):
+    """With a bound of a few cycles the first waits give up: the call returns, reports it and leaves nothing in flight; the
+    same call with the default bound computes as ever. (Split list and clusters, one and two row warps.)"""
+    import time
+    B, Hq, Hkv, D, page, Tq, lens = case
+    k, v, table, q = paged_inputs(B, Hq, Hkv, D, page, Tq, lens, torch.bfloat16, seed=95)
+    kv = handle(k, v, table, i32(lens))
+    want = attend(kv, q, 0.1)
+    torch.cuda.synchronize()
+    fa.fa_set_wait_limit_cycles(8)
+    try:
+        t = time.time()
+        attend(kv, q, 0.1)
+        torch.cuda.synchronize()
+        assert time.time() - t < 2
+        assert fa.fa_device_status() & 1
+    finally:
+        fa.fa_set_wait_limit_cycles(0)
+    o, lse = attend(kv, q, 0.1)
+    assert status_clear()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing of the paged calls needs a call before a capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, attention_fa_fwd_03_gb300 as fa
+dev = "cuda"
+z = lambda *s, dt=torch.float16: torch.zeros(s, dtype=dt, device=dev)
+kv = fa.PagedKV(z(9, 2, 16, 64), z(9, 2, 16, 64), torch.arange(8, dtype=torch.int32, device=dev).view(1, 8),
+                torch.full((1,), 100, dtype=torch.int32, device=dev), k_bounds=z(9, 2, 2, 64))
+q, o, lse, k = z(1, 4, 1, 64), z(1, 4, 1, 64), z(1, 4, 1, dt=torch.float32), torch.ones(1, 2, 1, 64, dtype=torch.float16, device=dev)
+sel, n = z(1, 2, 3, dt=torch.int32), z(1, 2, dt=torch.int32)
+ws, ws2 = z(fa.fa_paged_workspace_size(4, 2, 1, 64), dt=torch.uint8), z(fa.fa_page_select_workspace_size(1, 2, 8), dt=torch.uint8)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    fa.fa_kv_append(kv, k, k)
+    fa.fa_page_select(kv, q, sel, n, workspace=ws2)
+    fa.fa_paged_fwd(kv, q, o, lse, 0.1, causal=True, sel=sel, sel_lens=n, workspace=ws)
+g.replay()
+torch.cuda.synchronize()
+assert fa.fa_device_status() == 0
+assert sel.tolist() == [[[0, 1, 6]] * 2] and n.tolist() == [[3, 3]], sel
+assert abs(float(lse[0, 0, 0]) - 3.5835) < 1e-3, lse  # ln 36: two whole pages and four keys of the last
+assert float(o[0, 0, 0, 0]) > 0
+print("fine")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
