@@ -80,10 +80,13 @@ struct PagedCfg {
   static constexpr int KREG = (D + 63) / 64;         // 64-column regions of a row
   static constexpr int REGION = kPagedTile * 128;
   static constexpr int TILE = KREG * REGION;         // K (or V) rows of a stage
-  // Up to 16 rows two CTAs (D = 64: three) share an SM with about 100 KB in flight
-  // each; with more rows, or 64 KB stages, one does.
-  static constexpr int CTAS = D == 256 || RW > 1 ? 1 : D == 64 ? 3 : 2;
-  static constexpr int STAGES = D == 256 ? (RW == 1 ? 3 : 2) : D == 64 ? (RW == 1 ? 4 : 8) : (RW == 1 ? 3 : 5);
+  // Up to 16 rows two CTAs share an SM with about 100 KB in flight each (D = 64 and
+  // up to 8 rows: three; with 16, whose registers that would spill, 80% of the copy
+  // rate against 84); with more rows, or 64 KB stages, one does.
+  static constexpr int CTAS = D == 256 || RW > 1 ? 1 : D == 64 && NT == 1 ? 3 : 2;
+  static constexpr int STAGES = D == 256  ? (RW == 1 ? 3 : 2)
+                                : D == 64 ? (RW > 1 ? 8 : NT == 1 ? 4 : 6)
+                                          : (RW == 1 ? 3 : 5);
   // Queries as B fragments in registers where they fit, else read again each tile
   static constexpr bool QREG = NT * D <= (CTAS == 1 && RW == 1 ? 256 : 128);
   static constexpr int QREGION = ROWS * 128;
@@ -310,11 +313,12 @@ __device__ __forceinline__ void prefetch_l2(const void* at) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
 }
 
-// Whether one of two packed values is infinite or NaN (exponent bits all set).
+// Not 0 where one of two packed values is infinite or NaN: exponent bits all set, so
+// that one more in the lowest of them carries into the sign's place.
 template <bool BF16>
-__device__ __forceinline__ bool not_finite2(uint32_t x) {
-  constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
-  return (x & e) == e || (x & (e << 16)) == e << 16;
+__device__ __forceinline__ uint32_t not_finite2(uint32_t x) {
+  constexpr uint32_t e = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
+  return ((x & e) + one) & 0x80008000u;
 }
 
 // A position no query reaches: the key's slot was not loaded.
@@ -633,13 +637,18 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         uint32_t keep0 = ~0u, keep1 = ~0u;  // keys of this thread's V fragments that some row sees
         const int jv = j0 + 2 * (lane & 3);
         if (!all) {
+          // keys [j0 + lo, j0 + lo + span) are seen by a column's row; this thread's are
+          // j0 + lane / 4 and 8 behind it
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = j0 + (lane >> 2) + 8 * (e >> 1), pos = p_lo + token(nt, e & 1);
-              const bool see = j < len && !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
-              if (!see) s[nt][e] = -INFINITY;
+            for (int h = 0; h < 2; ++h) {
+              const int pos = p_lo + token(nt, h);
+              const int lo = p.window > 0 ? pos - p.window + 1 - j0 : -j0;
+              const int hi = (p.causal ? min(len, pos + 1) : len) - j0;
+              const unsigned span = static_cast<unsigned>(max(hi - lo, 0)), j = (lane >> 2) - lo;
+              if (j >= span) s[nt][h] = -INFINITY;
+              if (j + 8 >= span) s[nt][2 + h] = -INFINITY;
             }
           auto seen = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window); };
           keep0 = (seen(jv) ? 0xffffu : 0u) | (seen(jv + 1) ? 0xffff0000u : 0u);
@@ -714,14 +723,15 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                              (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
         bool apart = false;
         if (differ) {
+          uint32_t odd = 0;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             uint32_t a[4];
             ldsm4_trans(a, vs + (i >> 2) * C::REGION + sw128_offset(vr, (2 * i + vc) & 7));
-            apart |= not_finite2<C::BF16>(a[0] & keep0) | not_finite2<C::BF16>(a[1] & keep0) |
-                     not_finite2<C::BF16>(a[2] & keep1) | not_finite2<C::BF16>(a[3] & keep1);
+            odd |= not_finite2<C::BF16>(a[0] & keep0) | not_finite2<C::BF16>(a[1] & keep0) |
+                   not_finite2<C::BF16>(a[2] & keep1) | not_finite2<C::BF16>(a[3] & keep1);
           }
-          apart = __any_sync(0xffffffffu, apart);
+          apart = __any_sync(0xffffffffu, odd != 0);
         }
         if (!apart) {
 #pragma unroll
