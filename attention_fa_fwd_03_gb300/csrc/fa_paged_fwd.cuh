@@ -352,7 +352,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
-  if constexpr (C::CLUSTER) cluster_arrive_relaxed();  // waited for before the first store into a peer
+  // (a cluster of one has no peers and needs no barriers)
+  if (C::CLUSTER && ranks > 1) cluster_arrive_relaxed();  // waited for before the first store into a peer
   grid_wait_prior();
   grid_release_next();
   // What the lengths will lead to, on its way into L2 meanwhile: this CTA's part of
@@ -377,7 +378,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if constexpr (C::SPLIT) {
       regs_release<C::REG_PRODUCER>();
       if (warp > C::WARPS) {
-        if constexpr (C::CLUSTER) {
+        if (C::CLUSTER && ranks > 1) {
           cluster_wait();
           cluster_barrier();
         }
@@ -509,7 +510,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     // Stay until the last loads have landed: the consumers have waited for them too,
     // unless one of their waits gave up.
     if (lane == 0) drain_ring(smem_u32(&full[0]), C::STAGES, issued, p.wc.drain_cycles, p.wc.status);
-    if constexpr (C::CLUSTER) {  // as the consumers do
+    if (C::CLUSTER && ranks > 1) {  // as the consumers do
       __syncwarp();
       cluster_wait();
       cluster_barrier();
@@ -819,7 +820,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       const int pieces = rows * (D / 8), share_of = C::ROWS * (D / 8) / ranks;
       float2* pml = reinterpret_cast<float2*>(smem + C::OFF_PML);  // [ranks][share_of]
       __syncwarp();
-      cluster_wait();  // every CTA of the cluster is running
+      if (ranks > 1) cluster_wait();  // every CTA of the cluster is running
       for (int i = tid; i < pieces; i += 32 * C::WARPS) {
         const int r = i / (D / 8), ch = i - r * (D / 8);
         float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
@@ -834,12 +835,18 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           add4(s0, u, f);
           add4(s1, v, f);
         }
+        if (ranks == 1) {
+          store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, s0, s1, ml.y == 0.f ? 0.f : 1.f / ml.y);
+          if (ch == 0) p.lse[row0 + r] = row_lse(ml.x, ml.y);
+          continue;
+        }
         const uint32_t owner = i % ranks;
         const int slot = rank * share_of + i / ranks;
         st_peer_f4(om + 8 * slot, owner, s0);
         st_peer_f4(om + 8 * slot + 4, owner, s1);
         st_peer_f2(pml + slot, owner, ml);
       }
+      if (ranks == 1) return;
       __syncwarp();
       cluster_barrier();  // what was sent has arrived; nobody touches a peer after it
       for (int j = tid; rank + j * ranks < pieces; j += 32 * C::WARPS) {
