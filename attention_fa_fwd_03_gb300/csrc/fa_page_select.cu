@@ -25,6 +25,12 @@
 // latter for products that underflow), and those that this leaves open too in 64
 // bits, ranked by (score, lower page): the 64-bit units are so few that one page
 // costs microseconds.
+//
+// Measured in a chain of calls: 12 units of 126 pages 6.4 us, 8 units of 2048 pages
+// (8.4 MB) 11.0 us, both bound by dependent loads, barriers and instruction fetch
+// (scoring 7 K cycles, search 4 K, places 4 K); 256 ragged units of up to 1024 pages (67
+// MB) 26 us, of which scoring moves 5.5 TB/s and the largest units and their choice
+// are the rest. L2 prefetch of the next pass's bounds made that 28 us.
 #include "fa_inst.cuh"
 #include "fa_paged_launch.h"
 #include "fa_paged_mma.cuh"

@@ -9,15 +9,15 @@
 // at most a few tens of flops per byte, far below the tensor cores' ridge. So
 // the kernel is built around keeping HBM busy.
 //
-// Split. A unit is a (sequence, KV head, block of up to 16 RW rows); its keys
-// are cut into tiles of 64. Only the device knows the lengths, so every CTA of a
-// grid that fills the GPU once sums the tiles of all units and takes an equal
-// share of the whole list, whatever the lengths of the sequences: CTA c the
-// tiles [T c / G, T (c + 1) / G). A share is a run of segments; the segments
-// that cover a whole unit write O and LSE themselves, the others (at most the
-// first and the last of a CTA) leave (m, l, unnormalised O) in the workspace and
-// a second kernel joins them. Nothing depends on which CTA finishes first, so
-// results are the same on every run.
+// Split. A unit is a (sequence, KV head, block of 8 to 64 rows); its keys are cut
+// into tiles of 64. Only the device knows the lengths, so every CTA of a grid that
+// fills the GPU once sums the tiles of all units and takes an equal share of the
+// whole list, whatever the lengths of the sequences. A share is a run of segments;
+// those that cover a whole unit write O and LSE themselves, the others (at most the
+// first and the last of a CTA) leave (m, l, unnormalised O) in the workspace and a
+// second kernel joins them. Short lists skip all that: a cluster of CTAs takes a
+// unit, tiles in turn, and joins through distributed shared memory. Either way the
+// parts are joined in a fixed order, so results are the same on every run.
 //
 // Inside a CTA one warp looks up pages and loads tiles by TMA (one box per page
 // piece and 64 columns, 128-byte swizzle) into a ring of stages; four warps per
@@ -26,11 +26,14 @@
 // m16n8k16 tensor-core products computed transposed, S^T = K Q^T and O^T = V^T P^T:
 // keys and columns of V are the 16 rows of a fragment (read by ldmatrix straight
 // from the tile), query rows its 8 columns, so a group of up to 8 heads fills a
-// fragment that would be half empty the other way round, and each K or V fragment
-// is loaded once for all row groups. A tcgen05 tile would need 64 keys of one page
-// set per instruction and its accumulators back from TMEM twice a tile; at these
-// few rows the warp-level products take under a third of the time that the tile's
-// bytes need, so the simpler instruction wins.
+// fragment that would be half empty the other way round.
+//
+// Measured, share of the copy rate (6787 GB/s): up to 8 rows 95% (D 64, 96, 128; B1
+// 131072 keys of 8 KV heads, 537 MB, 84-87 us), 90% (D 256); 16 rows 84-86%. There the
+// tensor pipe is 14% active and the loads bound the kernel: a tcgen05 tile with its
+// round trip through TMEM has nothing to gain. 24 rows 63%, 32 rows 73%, 40 rows
+// 55%, 64 rows 29%: bound by issue (about 270 instructions per warp and tile with two
+// warps per scheduler); 16 consumer warps instead of 8 gave the same.
 #pragma once
 
 #include "fa_inst.cuh"
@@ -39,8 +42,8 @@
 
 namespace fa {
 
-constexpr int kPagedKeyWarps = 4;    // warps that share a tile's keys, 16 each
-constexpr int kPagedMaxRanks = 16;   // CTAs of a cluster (above 8: allowed per kernel)
+constexpr int kPagedKeyWarps = 4;       // warps that share a tile's keys, 16 each
+constexpr int kPagedMaxRanks = 16;      // CTAs of a cluster (above 8: allowed per kernel)
 constexpr int kPagedClusterTiles = 16;  // tiles per CTA up to which clusters are used
 
 struct PagedFwdArgs {
@@ -943,6 +946,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   }
 }
 
+// A launch of its own: in a chain of calls it takes 4.5 us, but a join by the CTA
+// that is last with a part (counters in the workspace) took as long, in the fence,
+// the counting and one CTA's reading of up to 40 parts (B1 131072 keys 86 us with the
+// second launch, 90 without).
 // Joins the parts of the units that CTA blockIdx.x of the split kernel began
 // and did not finish: its slot 1 and slot 0 of the CTAs after it. A row's parts are
 // shared by up to 8 warps, four or more each with all their loads in flight, a lane
@@ -1091,7 +1098,7 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   // units 7.1 us with 16 CTAs, 8.0 with 8 and 11.2 split.
   int ranks = 1;
   const int most_ranks = device_sm_count() >= 128 ? kPagedMaxRanks : 8;
-  while (ranks < most_ranks && ranks < tiles) ranks *= 2;
+  while (tiles > 2 && ranks < most_ranks && ranks < tiles) ranks *= 2;  // 2 tiles: 5.7 us in one CTA, 6.6 in two
   while (ranks > 1 && units * ranks > wave) ranks /= 2;
   if (tiles <= kPagedClusterTiles * ranks)
     return launch_paged<PagedCfg<D, NT, RW, BF16, true>>(a, p, units * ranks, ranks);

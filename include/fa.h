@@ -191,11 +191,12 @@ size_t fa_bwd_noalloc_max_rows(void);
  *
  * k_bounds (may be null: then fa_kv_append keeps none and fa_page_select
  * refuses) is [num_pages, Hkv, 2, D]: the element-wise minimum and maximum of
- * the keys written to the page since its slot 0 was last written.
+ * the keys written to the page since its slot 0 was last written (a NaN is left
+ * out where there is a number).
  *
  * page_table and kv_lens live on the device and are read by the kernels, so
  * calls can be captured into a graph and replayed with other lengths and
- * pages. Entries of page_table past a sequence's last page are not read. What
+ * pages. Entries of page_table past a sequence's last page are not used. What
  * the host cannot check the kernels do: a page outside [0, num_pages), a length
  * outside [0, max_pages * page_size], a position outside the angle tables or a
  * new_lens[b] outside [0, T] raises a bit that fa_device_status() reports as
@@ -232,7 +233,8 @@ typedef struct {
  * touched. With k_bounds the bounds of every page that receives a token are
  * updated: started afresh where the page's slot 0 is among the new tokens, else
  * widened (so after tokens were taken back they may be wider than needed).
- * 1 <= T <= 2^22, B * T < 2^31, Hq and Hkv <= 2^14. Two sequences of one call must not append to the same page.
+ * 1 <= T <= 2^22, B * T < 2^31, Hq and Hkv <= 2^14. Two sequences of one call
+ * must not append to the same page.
  * One kernel launch. Returns FA_OK or an error code (nothing launched on error). */
 fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* k_strides,
                        const void* v_new, const int64_t* v_strides, const void* q,
