@@ -798,8 +798,9 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
-        // padding rows (tokens the sequence does not have) see nothing
-        if (token(nt, h) >= n || m[nt][h] == kNoMax) {
+        // padding rows (tokens the sequence does not have) see nothing; a row that has
+        // met nothing but NaN keeps it
+        if (token(nt, h) >= n || (m[nt][h] == kNoMax && x == 0.f)) {
           m[nt][h] = -INFINITY;
           x = 0.f;
         }

@@ -221,7 +221,7 @@ typedef struct {
  *                 and Hq is not used). Each is read through its strides
  *                 (elements) of the batch, head and token index; the innermost
  *                 index is contiguous. Bases are 16-byte aligned and strides
- *                 multiples of 8, so slices of a fused projection
+ *                 multiples of 8 (at most 2^38), so slices of a fused projection
  *                 [B, T, (Hq + 2 Hkv) * D] are read in place.
  *   q_out         [B, Hq, T, D] dense; padding rows are set to zero.
  *   cos_table, sin_table  fp32 [rope_len, rot_dim / 2], row p for position p;
@@ -265,7 +265,8 @@ size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D);
  * gets O = 0 and LSE = -inf.
  * Values of keys that no row sees never reach a result, whatever they hold. A
  * key that is visible to one row and hidden from another adds exactly nothing to
- * the latter as well.
+ * the latter as well. A NaN in a row's query or in a key that the row sees makes
+ * that row's O and LSE NaN.
  *   workspace  fa_paged_workspace_size bytes, 16-byte aligned; contents
  *     undefined before and after. Calls that may overlap need one each.
  * The result does not depend on what else runs and is the same on every run.
@@ -275,8 +276,8 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
                        const int* sel_lens, int n_sel, void* workspace, size_t workspace_bytes,
                        cudaStream_t stream);
 
-/* Bytes of device workspace fa_page_select needs. Returns 0 for non-positive
- * sizes. */
+/* Bytes of device workspace fa_page_select needs. Returns 0 for sizes it
+ * refuses. */
 size_t fa_page_select_workspace_size(int B, int Hkv, int max_pages);
 
 /* Choose, for one new token per sequence, the pages its attention reads: per

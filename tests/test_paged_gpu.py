@@ -253,6 +253,33 @@ def test_attend_hidden_keys_add_nothing(what):
             assert torch.equal(o[0, :, r], clean[0][0, :, r]), (bad, r)
 
 
+@pytest.mark.parametrize("case", [(1, 8, 2, 128, 64, 1, [40]), (1, 8, 2, 128, 64, 1, [700]), (2, 6, 2, 64, 16, 3, [1, 300]),
+                                  (1, 8, 2, 96, 32, 1, [70000]), (1, 48, 1, 128, 64, 1, [70000]), (1, 8, 2, 256, 64, 1, [40000])],
+                         ids=lambda c: f"h{c[1]}x{c[2]}d{c[3]}T{c[5]}n{max(c[6])}")
+def test_attend_nan_that_a_row_sees_reaches_it(case):
+    """A query that is NaN, and a NaN in the only key: the rows are NaN, no others change (one launch and split list)."""
+    B, Hq, Hkv, D, page, Tq, lens = case
+    k, v, table, q = paged_inputs(B, Hq, Hkv, D, page, Tq, lens, torch.bfloat16, seed=12)
+    kv = handle(k, v, table, i32(lens))
+    clean, clean_lse = attend(kv, q, 0.1)
+    q[0, Hq // 2, 0, D - 1] = NAN
+    o, lse = attend(kv, q, 0.1)
+    assert status_clear()
+    row = torch.zeros(q.shape[:3], dtype=torch.bool, device="cuda")
+    # of several new tokens the first ones of a one-key sequence have no position and see nothing
+    row[0, Hq // 2, 0] = lens[0] >= Tq
+    assert torch.isnan(o[row]).all() and torch.isnan(lse[row]).all()
+    assert torch.equal(o[~row], clean[~row]) and torch.equal(lse[~row], clean_lse[~row])
+
+
+def test_attend_nan_in_the_only_key():
+    k, v, table, q = paged_inputs(2, 4, 2, 64, 16, 1, [1, 20], torch.float16, seed=13)
+    k[int(table[0, 0]), 1, 0, 3] = NAN
+    o, lse = attend(handle(k, v, table, i32([1, 20])), q, 0.1)
+    assert torch.isnan(o[0, 2:]).all() and torch.isnan(lse[0, 2:]).all()
+    assert torch.isfinite(o[0, :2]).all() and torch.isfinite(o[1]).all() and torch.isfinite(lse[1]).all()
+
+
 SELECTED = [  # B, Hq, Hkv, D, page, Tq, lengths, n_sel, dtype
     (2, 8, 2, 128, 16, 1, [1000, 333], 7, "bf16"),
     (3, 6, 3, 96, 64, 1, [640, 64, 1], 4, "fp16"),
@@ -797,10 +824,13 @@ def test_waits_that_give_up_end_cleanly(case):
     fa.fa_set_wait_limit_cycles(8)
     try:
         t = time.time()
-        attend(kv, q, 0.1)
+        got = attend(kv, q, 0.1)
         torch.cuda.synchronize()
         assert time.time() - t < 2
-        assert fa.fa_device_status() & 1
+        o, lse = got
+        # A CTA of the short cases has one tile, which may have landed before anybody looks: no wait gives up then, and
+        # the result is right. With several tiles per CTA some wait always comes too early.
+        assert fa.fa_device_status() & 1 or (max(lens) <= 700 and torch.equal(o, want[0]) and torch.equal(lse, want[1]))
     finally:
         fa.fa_set_wait_limit_cycles(0)
     o, lse = attend(kv, q, 0.1)
