@@ -25,6 +25,7 @@ Serving from a paged key/value cache (a pool of pages and a page table):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -240,7 +241,9 @@ class PagedKV:
     256; ``page_table`` [B, max_pages] and ``kv_lens`` [B] int32; ``k_bounds``
     [num_pages, Hkv, 2, D] or None. All contiguous on one CUDA device. The
     object keeps the tensors alive and is made once: page_table and kv_lens are
-    read by every call and updated in place by the caller.
+    read by every call and updated in place by the caller. Its attributes cannot
+    be assigned (``kv.kv_lens += 1`` updates in place): calls go to the tensors
+    it was made with.
     """
 
     __slots__ = ("k", "v", "page_table", "kv_lens", "k_bounds", "device", "dtype", "B", "Hkv", "D",
@@ -250,9 +253,10 @@ class PagedKV:
         import torch
         if k.dim() != 4 or page_table.dim() != 2:
             raise ValueError("k and v are [num_pages, Hkv, page_size, D], page_table is [B, max_pages]")
-        self.num_pages, self.Hkv, self.page_size, self.D = k.shape
-        self.B, self.max_pages = page_table.shape
-        self.device, self.dtype = k.device, k.dtype
+        put = functools.partial(object.__setattr__, self)
+        for name, value in zip(("num_pages", "Hkv", "page_size", "D", "B", "max_pages", "device", "dtype"),
+                               (*k.shape, *page_table.shape, k.device, k.dtype)):
+            put(name, value)
         code = _dtype_code(k)
         ptrs = [_ptr(k), self._pointer("v", v, k.shape, k.dtype),
                 0 if k_bounds is None else
@@ -261,11 +265,20 @@ class PagedKV:
                 self._pointer("kv_lens", kv_lens, (self.B,), torch.int32)]
         if max(self.num_pages, self.Hkv, self.page_size, self.D, self.B, self.max_pages) > 2 ** 31 - 1:
             raise ValueError("a size is beyond 32 bits")
-        self.k, self.v, self.k_bounds = k, v, k_bounds
-        self.page_table, self.kv_lens = page_table, kv_lens
-        self._calls = _paged_calls()
-        self._handle = self._calls.handle(*ptrs, self.B, self.Hkv, self.D, self.num_pages, self.page_size,
-                                          self.max_pages, code, self.device.index)
+        calls = _paged_calls()
+        for name, value in (("k", k), ("v", v), ("k_bounds", k_bounds), ("page_table", page_table), ("kv_lens", kv_lens),
+                            ("_calls", calls),
+                            ("_handle", calls.handle(*ptrs, self.B, self.Hkv, self.D, self.num_pages, self.page_size,
+                                                     self.max_pages, code, self.device.index))):
+            put(name, value)
+
+    def __setattr__(self, name: str, value) -> None:
+        if value is getattr(self, name, self):
+            return  # `kv.kv_lens += 1` has updated the tensor and assigns it again
+        raise AttributeError(f"PagedKV.{name} cannot be assigned: update the tensor in place or make a new PagedKV")
+
+    def __delattr__(self, name: str) -> None:
+        raise AttributeError(f"PagedKV.{name} cannot be deleted")
 
     def _pointer(self, name: str, t, shape, dtype) -> int:
         if t.dtype != dtype or t.shape != shape:

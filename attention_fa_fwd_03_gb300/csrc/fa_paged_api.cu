@@ -84,11 +84,12 @@ PagedView make_view(const fa_paged_kv* kv, uint32_t* status) {
   return c;
 }
 
-// Strides of a [B, H, T, D] view: whole 16-byte chunks, not negative. Returns
-// the elements from the first to behind the last one read, or -1.
+// Strides of a [B, H, T, D] view: whole 16-byte chunks, not negative, at most 2^38
+// elements (so the extent in bytes stays in 64 bits). Returns the elements from the
+// first to behind the last one read, or -1.
 int64_t view_extent(const int64_t* s, int64_t B, int64_t H, int64_t T, int64_t D) {
   for (int i = 0; i < 3; ++i)
-    if (s[i] < 0 || s[i] % 8 != 0 || s[i] > (int64_t(1) << 40)) return -1;
+    if (s[i] < 0 || s[i] % 8 != 0 || s[i] > (int64_t(1) << 38)) return -1;
   return (B - 1) * s[0] + (H - 1) * s[1] + (T - 1) * s[2] + D;
 }
 
@@ -162,7 +163,7 @@ fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* 
 }
 
 size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D) {
-  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Tq < 1 || Tq > kDecodeMaxTq) return 0;
+  if (Hq < 1 || Hq > kMaxUnits || Hkv < 1 || Hq % Hkv != 0 || Tq < 1 || Tq > kDecodeMaxTq) return 0;
   if (!(D == 64 || D == 96 || D == 128 || D == 256)) return 0;
   return paged_fwd_workspace(Hq / Hkv * Tq, D);
 }
@@ -199,6 +200,7 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
   r.in(q, rows * kv->D * 2);
   r.in(kv->k, pool_bytes(kv));
   r.in(kv->v, pool_bytes(kv));
+  r.in(kv->k_bounds, bounds_bytes(kv));
   r.in(kv->page_table, table_bytes(kv));
   r.in(kv->kv_lens, static_cast<size_t>(kv->B) * 4);
   r.in(new_lens, static_cast<size_t>(kv->B) * 4);
@@ -229,7 +231,7 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
 }
 
 size_t fa_page_select_workspace_size(int B, int Hkv, int max_pages) {
-  if (B < 1 || Hkv < 1 || max_pages < 1) return 0;
+  if (B < 1 || Hkv < 1 || max_pages < 1 || max_pages > kMaxPool || static_cast<int64_t>(B) * Hkv > kMaxUnits) return 0;
   const size_t bytes = static_cast<size_t>(B) * Hkv * max_pages * 12;  // scores in 32 and in 64 bits
   return (bytes + 255) / 256 * 256;
 }
@@ -255,6 +257,8 @@ fa_status fa_page_select(const fa_paged_kv* kv, const void* q, int Hq, int n_sel
   r.out(workspace, workspace_bytes);
   r.in(q, static_cast<size_t>(kv->B) * Hq * kv->D * 2);
   r.in(kv->k_bounds, bounds_bytes(kv));
+  r.in(kv->k, pool_bytes(kv));
+  r.in(kv->v, pool_bytes(kv));
   r.in(kv->page_table, table_bytes(kv));
   r.in(kv->kv_lens, static_cast<size_t>(kv->B) * 4);
   if (r.clash()) return FA_ERR_INVALID_ARG;

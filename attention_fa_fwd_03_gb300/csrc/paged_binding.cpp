@@ -5,6 +5,8 @@
 // microseconds, and ctypes with checks in Python took 8 to 10 of them per call.
 #include <climits>
 #include <cstdint>
+#include <exception>
+#include <new>
 
 #include <Python.h>
 
@@ -108,7 +110,11 @@ struct OnDevice {
     if (moved) c10::cuda::set_device(static_cast<c10::DeviceIndex>(device));
   }
   ~OnDevice() {
-    if (moved) c10::cuda::set_device(was);
+    if (!moved) return;
+    try {
+      c10::cuda::set_device(was);
+    } catch (...) {  // it was current a moment ago; a destructor may not throw
+    }
   }
 };
 
@@ -144,7 +150,8 @@ PyObject* make_handle(PyObject*, PyObject* args) {
   if (!PyArg_ParseTuple(args, "KKKKKiiiiiiii", &k, &v, &kb, &table, &lens, &B, &Hkv, &D, &num_pages, &page_size,
                         &max_pages, &dt, &device))
     return nullptr;
-  Handle* h = new Handle;
+  Handle* h = new (std::nothrow) Handle;
+  if (!h) return PyErr_NoMemory();
   h->kv.k = reinterpret_cast<void*>(k);
   h->kv.v = reinterpret_cast<void*>(v);
   h->kv.k_bounds = reinterpret_cast<void*>(kb);

@@ -142,6 +142,44 @@ def test_paged_fwd_refuses_more_tiles_than_it_counts(lib):
     assert paged_fwd(lib, cache_kw=big, Hq=16, sel=None, sel_lens=None) == INVALID
 
 
+def test_append_refuses_strides_whose_extent_leaves_64_bits(lib):
+    # 2^23 sequences, 2^40 elements apart: the extent in bytes is 2^64
+    big = dict(B=1 << 23, Hkv=1, num_pages=1, max_pages=1)
+    assert append(lib, cache_kw=big, Hq=1, ks=strides(1 << 40, 0, 0)) == INVALID
+    for name in ("ks", "vs", "qs"):
+        for i in range(3):
+            assert append(lib, **{name: strides(*((1 << 39) if j == i else 256 for j in range(3)))}) == INVALID
+
+
+def test_outputs_inside_parts_of_the_cache_that_a_call_does_not_read_are_refused(lib):
+    assert paged_fwd(lib, o=CACHE["k_bounds"]) == INVALID
+    assert paged_fwd(lib, ws=CACHE["k_bounds"]) == INVALID
+    assert select(lib, sel=CACHE["k"]) == INVALID
+    assert select(lib, ws=CACHE["v"]) == INVALID
+
+
+def test_workspace_sizes_beyond_the_limits_are_zero(lib):
+    assert fa.fa_paged_workspace_size(1 << 30, 1, 8, 64) == 0            # 2^33 rows
+    assert fa.fa_page_select_workspace_size(2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1) == 0
+    assert fa.fa_page_select_workspace_size(1 << 20, 16, 1 << 30) == 12 << 54
+
+
+def test_attributes_of_a_cache_cannot_be_assigned():
+    """Calls go to the tensors that the object was made with: an assignment would be silently without effect."""
+    kv = fa.PagedKV.__new__(fa.PagedKV)
+    for name in ("kv_lens", "page_table", "k", "B"):
+        with pytest.raises(AttributeError, match="in place"):
+            setattr(kv, name, torch.ones(2, dtype=torch.int32))
+        with pytest.raises(AttributeError):
+            delattr(kv, name)
+    lens = torch.ones(2, dtype=torch.int32)
+    object.__setattr__(kv, "kv_lens", lens)
+    kv.kv_lens += 1                            # in place
+    assert kv.kv_lens is lens and lens.tolist() == [2, 2]
+    with pytest.raises(AttributeError):
+        kv.kv_lens = lens + 1
+
+
 def test_page_select_needs_bounds(lib):
     assert select(lib, cache_kw=dict(k_bounds=None)) == INVALID
 
