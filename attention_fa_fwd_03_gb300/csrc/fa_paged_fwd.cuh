@@ -61,7 +61,10 @@ struct PagedFwdArgs {
   // earlier CTA, 1: it goes on in the next one)
   float* part_o;   // [2 parts][block rows][D]
   float2* part_ml; // [2 parts][block rows] (max, sum)
-  int4* joins;     // [parts]: unit, first part, last part, or unit = -1
+  // split units: (unit, first part | last part << 16), or unit = -1; by unit where
+  // units are no more than CTAs, else by the CTA that began the unit
+  int2* joins;
+  int by_unit;
   WaitCfg wc;
 };
 
@@ -530,7 +533,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   auto sync_rows = [&] { named_bar_sync(1, 32 * C::WARPS); };
 
   if constexpr (!C::CLUSTER) {
-    if (tid == 0) p.joins[part] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !p.by_unit) p.joins[part] = make_int2(-1, 0);
   }
 
   // a block's query rows to shared memory, rows behind the last one zero
@@ -921,11 +924,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         if (ch == 0) p.part_ml[part_slot * C::ROWS + r] = make_float2(mt, lt);
       }
     }
-    if (tid == 0 && begins && !ends) {
+    if (tid == 0 && begins && (p.by_unit || !ends)) {
+      const int unit = w.item * w.mult + w.sub;
       // the unit goes on to tile share.hi - t1 + tiles of the list
-      const int last = min(share.part_of(share.hi - w.t1 + w.it.tiles - 1), share.parts - 1);
-      p.joins[part] = make_int4(static_cast<int>(row0 >> 31), static_cast<int>(row0 & 0x7fffffff),
-                                last, rows);
+      const int last = ends ? 0 : min(share.part_of(share.hi - w.t1 + w.it.tiles - 1), share.parts - 1);
+      p.joins[p.by_unit ? unit : part] = make_int2(ends ? -1 : unit, part | last << 16);
     }
     sync_rows();
   }
@@ -943,6 +946,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS)
         reinterpret_cast<uint4*>(p.o + row0 * D)[i] = make_uint4(0, 0, 0, 0);
       for (int i = tid; i < rows; i += 32 * C::WARPS) p.lse[row0 + i] = -INFINITY;
+      if (tid == 0 && p.by_unit) p.joins[u] = make_int2(-1, 0);
     }
   }
 }
@@ -951,13 +955,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 // that is last with a part (counters in the workspace) took as long, in the fence,
 // the counting and one CTA's reading of up to 40 parts (B1 131072 keys 86 us with the
 // second launch, 90 without).
-// Joins the parts of the units that CTA blockIdx.x of the split kernel began
-// and did not finish: its slot 1 and slot 0 of the CTAs after it. A row's parts are
+// Joins the parts of record blockIdx.x's unit: slot 1 of the CTA that began it and
+// slot 0 of the CTAs after it. A row's parts are
 // shared by up to 8 warps, four or more each with all their loads in flight, a lane
 // 4 columns (D = 256: 8); with few parts the block's warps take several rows at a
 // time.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinBlocks = 8;  // blocks per split unit at most
+constexpr int kJoinBlocks = 8;  // blocks per record that split units can have at least
 template <int D, int ROWS, bool BF16>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 fa_paged_join_kernel(const PagedFwdArgs p) {
@@ -966,10 +970,15 @@ fa_paged_join_kernel(const PagedFwdArgs p) {
   __shared__ float2 sm_ml[kJoinWarps];
   grid_wait_prior();
   grid_release_next();
-  const int4 join = p.joins[blockIdx.x];
+  const int2 join = p.joins[blockIdx.x];
   if (join.x < 0) return;
-  const int64_t row0 = (static_cast<int64_t>(join.x) << 31) + join.y;
-  const int first = blockIdx.x, nparts = join.z - first + 1, rows = join.w;
+  // (the bounds hold for any record: lengths that change under the call may leave an
+  // old one)
+  const int unit = p.by_unit ? blockIdx.x : join.x;
+  const int rb = unit % p.row_blocks, rows = min(ROWS, p.rows - rb * ROWS);
+  const int64_t row0 = static_cast<int64_t>(unit / p.row_blocks) * p.rows + rb * ROWS;
+  const int first = min(join.y & 0xffff, kPagedMaxParts - 1);
+  const int nparts = min(static_cast<int>(static_cast<uint32_t>(join.y) >> 16), kPagedMaxParts - 1) - first + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // warps of a row, and this warp's place among them
   const int team = nparts <= UN ? 1 : nparts <= 2 * UN ? 2 : nparts <= 4 * UN ? 4 : 8;
@@ -1083,7 +1092,8 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   p.row_blocks = (p.rows + C::ROWS - 1) / C::ROWS;
   p.part_o = a.ws;
   p.part_ml = reinterpret_cast<float2*>(a.ws + static_cast<size_t>(2 * kPagedMaxParts) * C::ROWS * C::D);
-  p.joins = reinterpret_cast<int4*>(p.part_ml + 2 * kPagedMaxParts * C::ROWS);
+  p.joins = reinterpret_cast<int2*>(p.part_ml + 2 * kPagedMaxParts * C::ROWS);
+  p.by_unit = 0;
   p.wc = a.wc;
   // tiles of the longest list a unit can have in earnest (of distinct pages; the
   // kernels take any)
@@ -1105,11 +1115,17 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
     return launch_paged<PagedCfg<D, NT, RW, BF16, true>>(a, p, units * ranks, ranks);
   // no more CTAs than the longest possible list has tiles
   const int64_t parts = std::min(wave, units * tiles);
+  p.by_unit = units <= parts;
   const cudaError_t e = launch_paged<C>(a, p, parts, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(parts), static_cast<unsigned>(std::min(std::min(p.rows, C::ROWS), kJoinBlocks)), 1);
+  // eight blocks per record, more where records are few (39 units of 35 rows: 24.7 us
+  // with 8, 22.7 with 24 and above)
+  const int64_t records = std::min(parts, units);
+  const int64_t per_record = std::max<int64_t>(kJoinBlocks, kJoinBlocks * device_sm_count() / records);
+  cfg.gridDim = dim3(static_cast<unsigned>(records),
+                     static_cast<unsigned>(std::min<int64_t>(std::min(p.rows, C::ROWS), per_record)), 1);
   cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
   cfg.stream = a.stream;
   allow_early_launch(&cfg, attrs);

@@ -76,7 +76,7 @@ inline int64_t paged_tiles(int64_t units, int64_t keys) { return units * ((keys 
 // block (fp32 rows, maximum and sum) and a record of what is to be joined.
 inline size_t paged_fwd_workspace(int rows, int D) {
   const size_t bytes = static_cast<size_t>(2 * kPagedMaxParts) * paged_block_rows(rows, D) * (D * 4 + 8) +
-                       kPagedMaxParts * 16;
+                       kPagedMaxParts * 8;
   return (bytes + 255) / 256 * 256;
 }
 cudaError_t launch_page_select(const SelectLaunch& a);
