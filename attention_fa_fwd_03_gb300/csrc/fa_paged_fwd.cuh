@@ -304,6 +304,51 @@ __device__ __forceinline__ float2 warps_max_sum(const float2* mls, int r) {
   return make_float2(m, l);
 }
 
+// Eight columns of a row of a segment, the sums not normalised: the output where the
+// segment is the whole unit, else the part `part_slot`.
+template <class C>
+__device__ __forceinline__ void put_piece(const PagedFwdArgs& p, bool whole, int part_slot, int64_t row0, int r, int ch,
+                                          const float4& x, const float4& y, float2 ml) {
+  if (whole) {
+    store_out8<C::BF16>(p.o + (row0 + r) * C::D + 8 * ch, x, y, ml.y == 0.f ? 0.f : 1.f / ml.y);
+    if (ch == 0) p.lse[row0 + r] = row_lse(ml.x, ml.y);
+  } else {
+    float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(part_slot) * C::ROWS + r) * C::D + 8 * ch);
+    dst[0] = x;
+    dst[1] = y;
+    if (ch == 0) p.part_ml[part_slot * C::ROWS + r] = ml;
+  }
+}
+
+// By one thread after a segment: whether the unit it began is split, and over which parts.
+__device__ __forceinline__ void record_unit(const PagedFwdArgs& p, const Share& share, const Walk& w, int part) {
+  const bool ends = w.t1 == w.it.tiles;
+  if (w.t0 != 0 || (ends && !p.by_unit)) return;
+  const int unit = w.item * w.mult + w.sub;
+  // the unit goes on to tile share.hi - t1 + tiles of the list
+  const int last = ends ? 0 : min(share.part_of(share.hi - w.t1 + w.it.tiles - 1), share.parts - 1);
+  p.joins[p.by_unit ? unit : part] = make_int2(ends ? -1 : unit, part | last << 16);
+}
+
+// Units without tiles: nothing is visible to any of their rows.
+template <class C>
+__device__ __forceinline__ void write_empty_units(const PagedFwdArgs& p, int part, int parts, int tid, int threads) {
+  const int mult = item_mult(p);
+  const int64_t units = static_cast<int64_t>(item_count(p)) * mult;
+  for (int64_t u = part; u < units; u += parts) {
+    const int item = static_cast<int>(u / mult), sub = static_cast<int>(u - static_cast<int64_t>(item) * mult);
+    const Item it = load_item(p, item);
+    if (it.tiles > 0) continue;
+    const int g = p.sel ? item % p.c.Hkv : sub / p.row_blocks, rb = sub % p.row_blocks;
+    const int64_t row0 = block_row0(p, it.b, g, rb, C::ROWS);
+    const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
+    for (int i = tid; i < rows * (C::D / 8); i += threads)
+      reinterpret_cast<uint4*>(p.o + row0 * C::D)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < rows; i += threads) p.lse[row0 + i] = -INFINITY;
+    if (tid == 0 && p.by_unit) p.joins[u] = make_int2(-1, 0);
+  }
+}
+
 // Stores to CTA `rank`'s shared memory, at the place `at` has in this CTA's.
 __device__ __forceinline__ void st_peer_f2(const void* at, uint32_t rank, float2 v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_addr(smem_u32(at), rank)), "f"(v.x), "f"(v.y)
@@ -319,6 +364,18 @@ __device__ __forceinline__ void prefetch_l2(const void* at) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
 }
 
+// What the lengths will lead to, on its way into L2 before they are known: this
+// CTA's part of the page table (or of the selections) and of the queries.
+template <class C>
+__device__ __forceinline__ void prefetch_inputs(const PagedFwdArgs& p, int part) {
+  const PagedView& c = p.c;
+  const int64_t t = static_cast<int64_t>(part) * C::THREADS + threadIdx.x;
+  const int64_t entries = p.sel ? static_cast<int64_t>(c.B) * c.Hkv * p.n_sel : static_cast<int64_t>(c.B) * c.max_pages;
+  const int64_t q_lines = static_cast<int64_t>(c.B) * c.Hkv * p.rows * (C::D / 64);
+  if (t * 32 < entries) prefetch_l2((p.sel ? p.sel : c.table) + t * 32);
+  if (t < q_lines) prefetch_l2(p.q + t * 64);
+}
+
 // Not 0 where one of two packed values is infinite or NaN: exponent bits all set, so
 // that one more in the lowest of them carries into the sign's place.
 template <bool BF16>
@@ -329,6 +386,110 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t x) {
 
 // A position no query reaches: the key's slot was not loaded.
 constexpr int kNoPosition = 0x7fffff00;
+
+// The producer warp's side of a CTA's ring of K and V tiles.
+template <class C>
+struct TileRing {
+  const PagedFwdArgs& p;
+  const CUtensorMap &map_k, &map_v;
+  uint32_t kv, full, empty;          // shared addresses: stages, barriers
+  int (*key_pos)[kPagedKeyWarps];    // position of the first of each 16 keys of a stage
+  int* abort_flag;
+  int piece, pieces;                 // keys of a page in one tile, pages of a tile
+  int lane, issued = 0;
+  bool ok = true;
+  __device__ __forceinline__ TileRing(const PagedFwdArgs& p_, const CUtensorMap& mk, const CUtensorMap& mv, uint32_t kv_,
+                                      uint64_t* full_, uint64_t* empty_, int (*key_pos_)[kPagedKeyWarps], int* abort_)
+      : p(p_), map_k(mk), map_v(mv), kv(kv_), full(smem_u32(full_)), empty(smem_u32(empty_)), key_pos(key_pos_),
+        abort_flag(abort_), piece(min(1 << p_.c.page_shift, kPagedTile)), pieces(kPagedTile / piece),
+        lane(threadIdx.x & 31) {}
+  // One tile of KV head g into the next stage: lane i < pieces has the page (in the
+  // sequence, and in the pool or -1) of its piece i, whose first key is key `x` of
+  // the list plus i pieces.
+  __device__ __forceinline__ void load(int x, int pg, int id, int g) {
+    const PagedView& c = p.c;
+    const int slot = issued % C::STAGES;
+    if (issued >= C::STAGES)
+      ok = mbar_wait(empty + 8 * slot, ((issued / C::STAGES) - 1) & 1, p.wc.timeout_cycles, abort_flag, p.wc.status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return;
+    const int off = (x + lane * piece) & ((1 << c.page_shift) - 1);
+    const bool load = lane < pieces && id >= 0;
+    if (lane < kPagedKeyWarps) {
+      const int pl = (lane * 16) / piece;  // piece that holds these 16 keys
+      const int kpage = __shfl_sync(0xfu, pg, pl), kid = __shfl_sync(0xfu, id, pl), koff = __shfl_sync(0xfu, off, pl);
+      key_pos[slot][lane] = kid >= 0 ? (kpage << c.page_shift) + koff + lane * 16 - pl * piece : kNoPosition;
+    }
+    const unsigned loads = __ballot_sync(0xffffffffu, load);
+    const uint32_t bar = full + 8 * slot, box = static_cast<uint32_t>(piece) * 128u;
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
+    __syncwarp();
+    if (load) {
+      const uint32_t dst = kv + slot * 2 * C::TILE + lane * box;
+      const int z = id * c.Hkv + g;
+#pragma unroll
+      for (int r = 0; r < C::KREG; ++r) {
+        tma_load_3d(dst + r * C::REGION, &map_k, bar, r * 64, off, z);
+        tma_load_3d(dst + C::TILE + r * C::REGION, &map_v, bar, r * 64, off, z);
+      }
+    }
+    __syncwarp();
+    ++issued;
+  }
+  // Stay until the last loads have landed: the consumers have waited for them too,
+  // unless one of their waits gave up.
+  __device__ __forceinline__ void drain() const {
+    if (lane == 0) drain_ring(full, C::STAGES, issued, p.wc.drain_cycles, p.wc.status);
+  }
+};
+
+// All tiles of a share, by the producer warp.
+template <class C>
+__device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const Share& share, Walk& w, TileRing<C>& ring) {
+  const PagedView& c = p.c;
+  const int lane = ring.lane;
+  for (bool more = w.start(p, share); more && ring.ok; more = w.next(p)) {
+    const int g = w.kv_head(p);
+    const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
+    const int64_t u = static_cast<int64_t>(w.it.b) * c.Hkv + g;
+    const int list = p.sel ? (w.it.tiles * kPagedTile) >> c.page_shift : pages;  // entries that tiles reach
+    const int count = p.sel ? min(list, max(0, min(p.n_sel, __ldg(p.sel_lens + u)))) : pages;
+    // pages of list entries [e0, e0 + 32) and the next 32, one per lane
+    auto look_up = [&](int e, int* page, int* id) {
+      *page = -1;
+      *id = -1;
+      if (e >= count) return;
+      int pg = e;
+      if (p.sel) {
+        pg = __ldg(p.sel + u * p.n_sel + e);
+        if (pg < 0 || pg >= pages) {
+          flag_bad_index(c);
+          return;
+        }
+      }
+      *page = pg;
+      *id = pool_page(c, w.it.b, pg);
+    };
+    int e0 = ((w.it.first + w.t0) * kPagedTile) >> c.page_shift;
+    int page0, id0, page1, id1;
+    look_up(e0 + lane, &page0, &id0);
+    look_up(e0 + 32 + lane, &page1, &id1);
+    for (int t = w.t0; t < w.t1 && ring.ok; ++t) {
+      const int x = (w.it.first + t) * kPagedTile;  // first key of the tile in the list
+      int e = (x >> c.page_shift) - e0;
+      if (e >= 32) {
+        e0 += 32;
+        e -= 32;
+        page0 = page1;
+        id0 = id1;
+        look_up(e0 + 32 + lane, &page1, &id1);
+      }
+      // lane i looks at piece i of the tile
+      const int my = e + ((lane * ring.piece) >> c.page_shift);  // below 32: pages of 16 start tiles at multiples of 4
+      ring.load(x, __shfl_sync(0xffffffffu, page0, my & 31), __shfl_sync(0xffffffffu, id0, my & 31), g);
+    }
+  }
+}
 
 // ------------------------------------------------------------------- kernel
 template <class C>
@@ -362,15 +523,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   if (C::CLUSTER && ranks > 1) cluster_arrive_relaxed();  // waited for before the first store into a peer
   grid_wait_prior();
   grid_release_next();
-  // What the lengths will lead to, on its way into L2 meanwhile: this CTA's part of
-  // the page table (or of the selections) and of the queries.
-  {
-    const int64_t t = static_cast<int64_t>(part) * C::THREADS + threadIdx.x;
-    const int64_t entries = p.sel ? static_cast<int64_t>(c.B) * c.Hkv * p.n_sel : static_cast<int64_t>(c.B) * c.max_pages;
-    const int64_t q_lines = static_cast<int64_t>(c.B) * c.Hkv * p.rows * (D / 64);
-    if (t * 32 < entries) prefetch_l2((p.sel ? p.sel : c.table) + t * 32);
-    if (t < q_lines) prefetch_l2(p.q + t * 64);
-  }
+  prefetch_inputs<C>(p, part);
   const int rank = C::CLUSTER ? part % ranks : 0, unit = C::CLUSTER ? part / ranks : 0;
   Share share;
   if constexpr (C::CLUSTER)
@@ -391,43 +544,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         return;
       }
     }
-    const int piece = min(1 << c.page_shift, kPagedTile);  // keys of a page in one tile
-    const int pieces = kPagedTile / piece;
-    const uint32_t box = static_cast<uint32_t>(piece) * 128u;
-    int issued = 0;
-    bool ok = true;
-    // One tile of KV head g into the next stage: lane i < pieces has the page (in the
-    // sequence, and in the pool or -1) of its piece i, whose first key is key `x` of
-    // the list plus i pieces.
-    auto load_tile = [&](int x, int pg, int id, int g) {
-      const int slot = issued % C::STAGES;
-      if (issued >= C::STAGES)
-        ok = mbar_wait(smem_u32(&empty[slot]), ((issued / C::STAGES) - 1) & 1, tmo, &abort_flag, p.wc.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      const int off = (x + lane * piece) & ((1 << c.page_shift) - 1);
-      const bool load = lane < pieces && id >= 0;
-      if (lane < C::KW) {
-        const int pl = (lane * 16) / piece;  // piece that holds this warp's keys
-        const int kpage = __shfl_sync(0xfu, pg, pl), kid = __shfl_sync(0xfu, id, pl), koff = __shfl_sync(0xfu, off, pl);
-        key_pos[slot][lane] = kid >= 0 ? (kpage << c.page_shift) + koff + lane * 16 - pl * piece : kNoPosition;
-      }
-      const unsigned loads = __ballot_sync(0xffffffffu, load);
-      const uint32_t bar = smem_u32(&full[slot]);
-      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
-      __syncwarp();
-      if (load) {
-        const uint32_t dst = sbase + C::OFF_KV + slot * 2 * C::TILE + lane * box;
-        const int z = id * c.Hkv + g;
-#pragma unroll
-        for (int r = 0; r < C::KREG; ++r) {
-          tma_load_3d(dst + r * C::REGION, &map_k, bar, r * 64, off, z);
-          tma_load_3d(dst + C::TILE + r * C::REGION, &map_v, bar, r * 64, off, z);
-        }
-      }
-      __syncwarp();
-      ++issued;
-    };
+    TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag);
+    const int piece = ring.piece, pieces = ring.pieces;
     if constexpr (C::CLUSTER) {
       // Lane k * pieces + i looks up piece i of the k-th tile of a batch of as many of
       // the CTA's tiles as 32 lanes hold, the first batch, where no window moves the
@@ -453,7 +571,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       first = w.it.first * kPagedTile;
       const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
       const int count = p.sel ? max(0, min(p.n_sel, __ldg(p.sel_lens + u))) : pages;
-      for (int t0 = 0; t0 < w.t1 && ok; t0 += batch) {
+      for (int t0 = 0; t0 < w.t1 && ring.ok; t0 += batch) {
         if (t0 > 0 || !early) read(t0);
         const bool counts = t0 + mine < w.t1 && e < count;
         if (counts && static_cast<unsigned>(pg) < static_cast<unsigned>(pages)) {
@@ -462,60 +580,16 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           if (counts) flag_bad_index(c);  // a selected page that the sequence does not have
           id = -1;
         }
-        for (int t = t0; t < min(w.t1, t0 + batch) && ok; ++t) {
+        for (int t = t0; t < min(w.t1, t0 + batch) && ring.ok; ++t) {
           const int from = (t - t0) * pieces + (lane & (pieces - 1));
-          load_tile(first + (rank + t * ranks) * kPagedTile, __shfl_sync(0xffffffffu, pg, from),
+          ring.load(first + (rank + t * ranks) * kPagedTile, __shfl_sync(0xffffffffu, pg, from),
                     __shfl_sync(0xffffffffu, id, from), g);
         }
       }
     } else {
-      ok = w.start(p, share);
+      produce_share(p, share, w, ring);
     }
-    while (!C::CLUSTER && ok) {
-      const int g = w.kv_head(p);
-      const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
-      const int64_t u = static_cast<int64_t>(w.it.b) * c.Hkv + g;
-      const int list = p.sel ? (w.it.tiles * kPagedTile) >> c.page_shift : pages;  // entries that tiles reach
-      const int count = p.sel ? min(list, max(0, min(p.n_sel, __ldg(p.sel_lens + u)))) : pages;
-      // pages of list entries [e0, e0 + 32) and the next 32, one per lane
-      auto look_up = [&](int e, int* page, int* id) {
-        *page = -1;
-        *id = -1;
-        if (e >= count) return;
-        int pg = e;
-        if (p.sel) {
-          pg = __ldg(p.sel + u * p.n_sel + e);
-          if (pg < 0 || pg >= pages) {
-            flag_bad_index(c);
-            return;
-          }
-        }
-        *page = pg;
-        *id = pool_page(c, w.it.b, pg);
-      };
-      int e0 = ((w.it.first + w.t0) * kPagedTile) >> c.page_shift;
-      int page0, id0, page1, id1;
-      look_up(e0 + lane, &page0, &id0);
-      look_up(e0 + 32 + lane, &page1, &id1);
-      for (int t = w.t0; t < w.t1 && ok; ++t) {
-        const int x = (w.it.first + t) * kPagedTile;  // first key of the tile in the list
-        int e = (x >> c.page_shift) - e0;
-        if (e >= 32) {
-          e0 += 32;
-          e -= 32;
-          page0 = page1;
-          id0 = id1;
-          look_up(e0 + 32 + lane, &page1, &id1);
-        }
-        // lane i looks at piece i of the tile
-        const int my = e + ((lane * piece) >> c.page_shift);  // below 32: pages of 16 start tiles at multiples of 4
-        load_tile(x, __shfl_sync(0xffffffffu, page0, my & 31), __shfl_sync(0xffffffffu, id0, my & 31), g);
-      }
-      ok = ok && w.next(p);
-    }
-    // Stay until the last loads have landed: the consumers have waited for them too,
-    // unless one of their waits gave up.
-    if (lane == 0) drain_ring(smem_u32(&full[0]), C::STAGES, issued, p.wc.drain_cycles, p.wc.status);
+    ring.drain();
     if (C::CLUSTER && ranks > 1) {  // as the consumers do
       __syncwarp();
       cluster_wait();
@@ -913,43 +987,19 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       const float4 x = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch);
       const float4 y = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch + 4);
       const float2 ml = warps_max_sum<C>(mls, r);
-      const float mt = ml.x, lt = ml.y;
-      if (begins && ends) {
-        store_out8<C::BF16>(p.o + (row0 + r) * D + 8 * ch, x, y, lt == 0.f ? 0.f : 1.f / lt);
-        if (ch == 0) p.lse[row0 + r] = row_lse(mt, lt);
-      } else {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(part_slot) * C::ROWS + r) * D + 8 * ch);
-        dst[0] = x;
-        dst[1] = y;
-        if (ch == 0) p.part_ml[part_slot * C::ROWS + r] = make_float2(mt, lt);
-      }
+      put_piece<C>(p, begins && ends, part_slot, row0, r, ch, x, y, ml);
     }
-    if (tid == 0 && begins && (p.by_unit || !ends)) {
-      const int unit = w.item * w.mult + w.sub;
-      // the unit goes on to tile share.hi - t1 + tiles of the list
-      const int last = ends ? 0 : min(share.part_of(share.hi - w.t1 + w.it.tiles - 1), share.parts - 1);
-      p.joins[p.by_unit ? unit : part] = make_int2(ends ? -1 : unit, part | last << 16);
-    }
+    if (tid == 0) record_unit(p, share, w, part);
     sync_rows();
   }
-  if constexpr (!C::CLUSTER) {
-    // units without tiles: nothing is visible to any of their rows
-    const int mult = item_mult(p);
-    const int64_t units = static_cast<int64_t>(item_count(p)) * mult;
-    for (int64_t u = part; u < units; u += parts) {
-      const int item = static_cast<int>(u / mult), sub = static_cast<int>(u - static_cast<int64_t>(item) * mult);
-      const Item it = load_item(p, item);
-      if (it.tiles > 0) continue;
-      const int g = p.sel ? item % c.Hkv : sub / p.row_blocks, rb = sub % p.row_blocks;
-      const int64_t row0 = block_row0(p, it.b, g, rb, C::ROWS);
-      const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
-      for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS)
-        reinterpret_cast<uint4*>(p.o + row0 * D)[i] = make_uint4(0, 0, 0, 0);
-      for (int i = tid; i < rows; i += 32 * C::WARPS) p.lse[row0 + i] = -INFINITY;
-      if (tid == 0 && p.by_unit) p.joins[u] = make_int2(-1, 0);
-    }
-  }
+  if constexpr (!C::CLUSTER) write_empty_units<C>(p, part, parts, tid, 32 * C::WARPS);
 }
+
+}  // namespace fa
+
+#include "fa_paged_tc.cuh"
+
+namespace fa {
 
 // A launch of its own: in a chain of calls it takes 4.5 us, but a join by the CTA
 // that is last with a part (counters in the workspace) took as long, in the fence,
@@ -977,8 +1027,9 @@ fa_paged_join_kernel(const PagedFwdArgs p) {
   const int unit = p.by_unit ? blockIdx.x : join.x;
   const int rb = unit % p.row_blocks, rows = min(ROWS, p.rows - rb * ROWS);
   const int64_t row0 = static_cast<int64_t>(unit / p.row_blocks) * p.rows + rb * ROWS;
-  const int first = min(join.y & 0xffff, kPagedMaxParts - 1);
-  const int nparts = min(static_cast<int>(static_cast<uint32_t>(join.y) >> 16), kPagedMaxParts - 1) - first + 1;
+  constexpr int LAST = paged_max_parts(ROWS) - 1;
+  const int first = min(join.y & 0xffff, LAST);
+  const int nparts = min(static_cast<int>(static_cast<uint32_t>(join.y) >> 16), LAST) - first + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // warps of a row, and this warp's place among them
   const int team = nparts <= UN ? 1 : nparts <= 2 * UN ? 2 : nparts <= 4 * UN ? 4 : 8;
@@ -1061,13 +1112,16 @@ fa_paged_join_kernel(const PagedFwdArgs p) {
 }
 
 // ------------------------------------------------------------------- launch
+inline bool encode_maps(const PagedFwdLaunch& a, int D, CUtensorMap* mk, CUtensorMap* mv) {
+  const int page = 1 << a.c.page_shift, piece = page < kPagedTile ? page : kPagedTile;
+  return encode_tile_map(mk, a.c.k, a.bf16, D, page, a.c.num_pages * a.c.Hkv, piece) &&
+         encode_tile_map(mv, a.c.v, a.bf16, D, page, a.c.num_pages * a.c.Hkv, piece);
+}
+
 template <class C>
 cudaError_t launch_paged(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t grid, int ranks) {
   CUtensorMap mk, mv;
-  const int page = 1 << a.c.page_shift, piece = page < kPagedTile ? page : kPagedTile;
-  if (!encode_tile_map(&mk, a.c.k, C::BF16, C::D, page, a.c.num_pages * a.c.Hkv, piece) ||
-      !encode_tile_map(&mv, a.c.v, C::BF16, C::D, page, a.c.num_pages * a.c.Hkv, piece))
-    return cudaErrorInvalidValue;
+  if (!encode_maps(a, C::D, &mk, &mv)) return cudaErrorInvalidValue;
   auto kern = fa_paged_fwd_kernel<C>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1076,47 +1130,35 @@ cudaError_t launch_paged(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t grid,
     return cudaErrorInvalidConfiguration;
   return launch_kernel(kern, grid, C::THREADS, C::SMEM_BYTES, a.stream, static_cast<unsigned>(ranks), mk, mv, p, ranks);
 }
+template <class C>
+cudaError_t launch_paged_tc(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t grid) {
+  CUtensorMap mk, mv;
+  if (!encode_maps(a, C::D, &mk, &mv)) return cudaErrorInvalidValue;
+  auto kern = fa_paged_tc_kernel<C>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, grid, C::THREADS, C::SMEM_BYTES, a.stream, 1, mk, mv, p);
+}
 
-template <int D, int NT, int RW, bool BF16>
-cudaError_t run_paged(const PagedFwdLaunch& a) {
-  using C = PagedCfg<D, NT, RW, BF16, false>;
-  PagedFwdArgs p;
-  p.c = a.c;
-  p.q = a.q; p.o = a.o; p.lse = a.lse;
-  p.Hq = a.Hq; p.Tq = a.Tq; p.causal = a.causal;
-  p.window = std::min(a.window, 1 << 30);  // positions end below 2^30: a longer window hides nothing either
-  p.scale_log2 = a.scale_log2;
-  p.new_lens = a.new_lens;
-  p.sel = a.sel; p.sel_lens = a.sel_lens; p.n_sel = a.n_sel;
+inline void set_row_blocks(const PagedFwdLaunch& a, PagedFwdArgs& p, int block) {
   p.rows = a.Hq / a.c.Hkv * a.Tq;
-  p.row_blocks = (p.rows + C::ROWS - 1) / C::ROWS;
+  p.row_blocks = (p.rows + block - 1) / block;
+}
+
+// The split list and its join, `ctas` CTAs per SM, for units of at most `tiles` tiles
+// in earnest.
+template <class C, class Launch>
+cudaError_t run_split(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t tiles, int ctas, const Launch& launch) {
+  constexpr int max_parts = paged_max_parts(C::ROWS);
+  set_row_blocks(a, p, C::ROWS);
   p.part_o = a.ws;
-  p.part_ml = reinterpret_cast<float2*>(a.ws + static_cast<size_t>(2 * kPagedMaxParts) * C::ROWS * C::D);
-  p.joins = reinterpret_cast<int2*>(p.part_ml + 2 * kPagedMaxParts * C::ROWS);
-  p.by_unit = 0;
-  p.wc = a.wc;
-  // tiles of the longest list a unit can have in earnest (of distinct pages; the
-  // kernels take any)
-  const int64_t keys = static_cast<int64_t>(a.sel ? std::min(a.n_sel, a.c.max_pages) : a.c.max_pages) << a.c.page_shift;
-  int64_t tiles = paged_tiles(1, keys);
-  if (a.window > 0 && !a.sel)  // window + Tq - 1 keys, wherever they start in a tile
-    tiles = std::min(tiles, (static_cast<int64_t>(a.window) + a.Tq - 2) / kPagedTile + 2);
+  p.part_ml = reinterpret_cast<float2*>(a.ws + static_cast<size_t>(2 * max_parts) * C::ROWS * C::D);
+  p.joins = reinterpret_cast<int2*>(p.part_ml + 2 * max_parts * C::ROWS);
   const int64_t units = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks;
-  const int64_t wave = std::min<int64_t>(static_cast<int64_t>(device_sm_count()) * C::CTAS, kPagedMaxParts);
-  // Short units: a cluster each (16 CTAs only on a whole GPU), joined in the same
-  // launch, where all clusters run at once or one CTA does for a unit. Measured: 16
-  // tiles, 4 units 4.6 us against 12.0 with the split list and its join; 64 tiles, 8
-  // units 7.1 us with 16 CTAs, 8.0 with 8 and 11.2 split.
-  int ranks = 1;
-  const int most_ranks = device_sm_count() >= 128 ? kPagedMaxRanks : 8;
-  while (tiles > 2 && ranks < most_ranks && ranks < tiles) ranks *= 2;  // 2 tiles: 5.7 us in one CTA, 6.6 in two
-  while (ranks > 1 && units * ranks > wave) ranks /= 2;
-  if (tiles <= kPagedClusterTiles * ranks)
-    return launch_paged<PagedCfg<D, NT, RW, BF16, true>>(a, p, units * ranks, ranks);
   // no more CTAs than the longest possible list has tiles
-  const int64_t parts = std::min(wave, units * tiles);
+  const int64_t parts = std::min(std::min<int64_t>(static_cast<int64_t>(device_sm_count()) * ctas, max_parts), units * tiles);
   p.by_unit = units <= parts;
-  const cudaError_t e = launch_paged<C>(a, p, parts, 1);
+  const cudaError_t e = launch(parts);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[1];
@@ -1130,6 +1172,54 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   cfg.stream = a.stream;
   allow_early_launch(&cfg, attrs);
   return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<C::D, C::ROWS, C::BF16>, p);
+}
+
+template <int D, int RG, bool BF16>
+cudaError_t run_split_tc(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t tiles) {
+  using C = PagedTcCfg<D, RG, BF16>;
+  return run_split<C>(a, p, tiles, 1, [&](int64_t parts) { return launch_paged_tc<C>(a, p, parts); });
+}
+
+template <int D, int NT, int RW, bool BF16>
+cudaError_t run_paged(const PagedFwdLaunch& a) {
+  using C = PagedCfg<D, NT, RW, BF16, true>;
+  PagedFwdArgs p = {};
+  p.c = a.c;
+  p.q = a.q; p.o = a.o; p.lse = a.lse;
+  p.Hq = a.Hq; p.Tq = a.Tq; p.causal = a.causal;
+  p.window = std::min(a.window, 1 << 30);  // positions end below 2^30: a longer window hides nothing either
+  p.scale_log2 = a.scale_log2;
+  p.new_lens = a.new_lens;
+  p.sel = a.sel; p.sel_lens = a.sel_lens; p.n_sel = a.n_sel;
+  p.wc = a.wc;
+  set_row_blocks(a, p, C::ROWS);
+  // tiles of the longest list a unit can have in earnest (of distinct pages; the
+  // kernels take any)
+  const int64_t keys = static_cast<int64_t>(a.sel ? std::min(a.n_sel, a.c.max_pages) : a.c.max_pages) << a.c.page_shift;
+  int64_t tiles = paged_tiles(1, keys);
+  if (a.window > 0 && !a.sel)  // window + Tq - 1 keys, wherever they start in a tile
+    tiles = std::min(tiles, (static_cast<int64_t>(a.window) + a.Tq - 2) / kPagedTile + 2);
+  const int64_t units = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks;
+  const int64_t wave = static_cast<int64_t>(device_sm_count()) * C::CTAS;
+  // Short units: a cluster each (16 CTAs only on a whole GPU), joined in the same
+  // launch, where all clusters run at once or one CTA does for a unit. Measured: 16
+  // tiles, 4 units 4.6 us against 12.0 with the split list and its join; 64 tiles, 8
+  // units 7.1 us with 16 CTAs, 8.0 with 8 and 11.2 split.
+  int ranks = 1;
+  const int most_ranks = device_sm_count() >= 128 ? kPagedMaxRanks : 8;
+  while (tiles > 2 && ranks < most_ranks && ranks < tiles) ranks *= 2;  // 2 tiles: 5.7 us in one CTA, 6.6 in two
+  while (ranks > 1 && units * ranks > wave) ranks /= 2;
+  if (tiles <= kPagedClusterTiles * ranks) return launch_paged<C>(a, p, units * ranks, ranks);
+  if constexpr (D < 256 && RW > 1) {  // more than 16 rows
+    switch (paged_split_rows(p.rows, D)) {
+      case 32: return run_split_tc<D, 1, BF16>(a, p, tiles);
+      case 64: return run_split_tc<D, 2, BF16>(a, p, tiles);
+      default: return run_split_tc<D, 4, BF16>(a, p, tiles);
+    }
+  } else {
+    using S = PagedCfg<D, NT, RW, BF16, false>;
+    return run_split<S>(a, p, tiles, S::CTAS, [&](int64_t parts) { return launch_paged<S>(a, p, parts, 1); });
+  }
 }
 
 template <int D, bool BF16>

@@ -58,15 +58,19 @@ cudaError_t launch_paged_fwd_d96(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd_d128(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd_d256(const PagedFwdLaunch& a);
 
-// CTAs of the attention kernel that can leave parts of units to be joined.
-constexpr int kPagedMaxParts = 608;
-
-// Query rows of a block: 8 (usual decoding), 16, 32, 48 or 64 where a KV head has
-// more, so that its keys are loaded once for all of them (D = 256: at most 32,
-// what registers hold).
+// Query rows of a block where a cluster takes a unit: 8 (usual decoding), 16, 32, 48
+// or 64 where a KV head has more, so that its keys are loaded once for all of them
+// (D = 256: at most 32, what registers hold).
 inline int paged_block_rows(int rows, int D) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : rows <= 48 ? 48 : 64;
 }
+// The same where the list is split: above 16 rows by tcgen05, up to 128.
+inline int paged_split_rows(int rows, int D) {
+  return rows <= 16 || D == 256 ? paged_block_rows(rows, D) : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+
+// CTAs of a split list at most: they leave parts of units to be joined.
+__host__ __device__ constexpr int paged_max_parts(int block_rows) { return block_rows <= 16 ? 608 : 304; }
 
 // Keys of a tile, and the most tiles a call may have (32-bit counts on the device).
 constexpr int kPagedTile = 64;
@@ -75,8 +79,8 @@ inline int64_t paged_tiles(int64_t units, int64_t keys) { return units * ((keys 
 // Device workspace of launch_paged_fwd_d* in bytes: per CTA two parts of a
 // block (fp32 rows, maximum and sum) and a record of what is to be joined.
 inline size_t paged_fwd_workspace(int rows, int D) {
-  const size_t bytes = static_cast<size_t>(2 * kPagedMaxParts) * paged_block_rows(rows, D) * (D * 4 + 8) +
-                       kPagedMaxParts * 8;
+  const int block = paged_split_rows(rows, D), parts = paged_max_parts(block);
+  const size_t bytes = static_cast<size_t>(2 * parts) * block * (D * 4 + 8) + parts * 8;
   return (bytes + 255) / 256 * 256;
 }
 cudaError_t launch_page_select(const SelectLaunch& a);

@@ -1,0 +1,481 @@
+// Attention over the paged cache where a KV head has many query rows (drafted
+// tokens times a group of heads): the split list of fa_paged_fwd.cuh with its
+// products on tcgen05.
+//
+// With R rows per KV head every key takes 6 R D flops for 4 D bytes (the product
+// with V twice, see below): at 64 rows 96 flops per byte, 650 TFLOP/s at the copy
+// rate. Warp-level products do not get there: their fragments go through registers
+// and two warps per scheduler wait for each other's chains.
+//
+// The 128 rows of an MMA are TMEM lanes, and a warp can read 32 of them only. So a
+// block of 32 or 64 rows is there four times or twice: copy k of a row takes keys
+// [64 k / copies, ...) of each tile, with a running maximum, a sum and an
+// accumulator of its own, and the copies are joined at the end of the segment, as
+// the warps' keys are in the other kernel. Every thread of the softmax warps then
+// has one row and 16, 32 or 64 keys of a tile, whatever the number of rows. What a
+// copy does not take has P = 0, written once: the columns of the other copies are
+// never touched.
+//
+// Roles: warps 0-3 softmax (thread = TMEM lane = row), warp 4 page look-up and TMA,
+// warp 5 issues the MMAs: S(t) = Q K(t)^T into one of two buffers; the softmax
+// writes P(t) = 2^(S - m) in two words of the cache's type beside it, P_hi + P_lo;
+// O += P_hi V + P_lo V. S(t + 1) is computed while the softmax has S(t). O is
+// rescaled in TMEM when a maximum grows by more than 2^8.
+#pragma once
+
+namespace fa {
+
+// RG: groups of 32 rows.
+template <int D_, int RG_, bool BF16_>
+struct PagedTcCfg {
+  static constexpr int D = D_, RG = RG_;
+  static constexpr bool BF16 = BF16_;
+  static constexpr int ROWS = 32 * RG;           // rows of a block
+  static constexpr int COPIES = 4 / RG;          // of each row
+  static constexpr int KEYS = kPagedTile / COPIES;  // of a tile that a copy takes
+  static constexpr int SOFT = 128, THREADS = SOFT + 64;
+  static constexpr int KREG = (D + 63) / 64, REGION = kPagedTile * 128, TILE = KREG * REGION;
+  static constexpr int QREGION = 128 * 128;
+  static constexpr int STAGES = D == 64 ? 8 : RG == 2 ? 4 : 5;
+  static constexpr int OP = D + 4;               // row pitch of the merge buffer (floats)
+  static constexpr int OFF_KV = 0;
+  static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
+  static constexpr int OFF_O = OFF_Q + KREG * QREGION;
+  static constexpr int OFF_ML = OFF_O + (COPIES > 1 ? ROWS * OP * 4 : 0);  // [copies][rows]
+  static constexpr int SMEM_BYTES = OFF_ML + SOFT * 8 + 1024;
+  static_assert(SMEM_BYTES <= 231000, "shared memory");
+  // TMEM columns
+  __host__ __device__ static constexpr int S_COL(int b) { return kPagedTile * b; }
+  __host__ __device__ static constexpr int P_COL(int b) { return 2 * kPagedTile + kPagedTile * b; }  // P_hi, then P_lo
+  static constexpr int P_LO = kPagedTile / 2;
+  static constexpr int O_COL = 4 * kPagedTile;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static_assert(O_COL + KREG * 64 <= 512, "TMEM");
+};
+
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 16) {
+    tmem_ld16(taddr, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tmem_ld32(taddr + i, *reinterpret_cast<uint32_t(*)[32]>(&r[i]));
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[N]) {
+  if constexpr (N == 8)
+    tmem_st8(taddr, r);
+  else if constexpr (N == 16)
+    tmem_st16(taddr, r);
+  else
+    tmem_st32(taddr, r);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const PagedFwdArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES], s_full[2], p_full[2], o_ready[2], q_ready, drained,
+      meet;
+  __shared__ __align__(16) int key_pos[C::STAGES][kPagedKeyWarps];
+  __shared__ int odd_flags[2][4];
+  __shared__ int abort_flag;
+  __shared__ uint32_t tmem_slot;
+  constexpr int D = C::D;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = blockIdx.x, parts = gridDim.x;
+  const uint64_t tmo = p.wc.timeout_cycles;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&s_full[b]), 1);
+      mbar_init(smem_u32(&p_full[b]), 4);   // one per softmax warp
+      mbar_init(smem_u32(&o_ready[b]), 1);  // by tile parity: a waiter is never two phases off
+    }
+    mbar_init(smem_u32(&q_ready), 4);
+    mbar_init(smem_u32(&drained), 1);
+    mbar_init(smem_u32(&meet), 4);
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == C::SOFT) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  grid_wait_prior();
+  grid_release_next();
+  prefetch_inputs<C>(p, part);
+  tc_fence_before();
+  const Share share = find_share<C::THREADS>(p, part, parts);  // barriers inside
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  Walk w;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer warp
+    TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag);
+    produce_share(p, share, w, ring);
+    ring.drain();
+  } else if (warp == 5) {
+    // --------------------------------------------------------------- MMA issuer
+    const bool leader = elect_one_sync();
+    constexpr uint32_t idesc_s = make_idesc_f16(128, kPagedTile, C::BF16 ? 1 : 0, 0, 0);
+    constexpr uint32_t idesc_o = make_idesc_f16(128, D, C::BF16 ? 1 : 0, 0, 1);
+    bool ok = true;
+    auto wait = [&](uint64_t& bar, int parity) {
+      ok = ok && mbar_wait_poll(smem_u32(&bar), parity & 1, tmo, &abort_flag, p.wc.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) tc_fence_after();
+    };
+    auto issue_s = [&](int gi) {  // tile gi's scores, once its keys are there
+      const int slot = gi % C::STAGES, b = gi & 1;
+      wait(full[slot], gi / C::STAGES);
+      if (!ok || !leader) return;
+      const uint32_t qa = sbase + C::OFF_Q, ka = sbase + C::OFF_KV + slot * 2 * C::TILE;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk & 3) * 32;  // 16 elements along K
+        mma_ss(tmem + C::S_COL(b), make_sdesc(qa + (kk >> 2) * C::QREGION + off, 16, 1024, 2),
+               make_sdesc(ka + (kk >> 2) * C::REGION + off, 16, 1024, 2), idesc_s, kk > 0);
+      }
+      mma_commit(smem_u32(&s_full[b]));
+    };
+    int gi = 0, seg = 0;
+    for (bool more = w.start(p, share); more && ok; more = w.next(p), ++seg) {
+      const int tiles = w.t1 - w.t0;
+      wait(q_ready, seg);
+      for (int i = 0; i < min(2, tiles) && ok; ++i) issue_s(gi + i);
+      for (int i = 0; i < tiles && ok; ++i, ++gi) {
+        const int slot = gi % C::STAGES, b = gi & 1;
+        wait(p_full[b], gi >> 1);
+        if (!ok) break;
+        if (leader) {
+          const uint32_t va = sbase + C::OFF_KV + slot * 2 * C::TILE + C::TILE;
+#pragma unroll
+          for (int word = 0; word < 2; ++word)
+#pragma unroll
+            for (int kk = 0; kk < kPagedTile / 16; ++kk)
+              mma_ts(tmem + C::O_COL, tmem + C::P_COL(b) + word * C::P_LO + kk * 8,
+                     make_sdesc(va + kk * 16 * 128, C::REGION, 1024, 2), idesc_o, 1);
+          mma_commit(smem_u32(&o_ready[b]));
+          mma_commit(smem_u32(&empty[slot]));
+        }
+        if (i + 2 < tiles) issue_s(gi + 2);  // its buffer's P is written, its scores read
+      }
+    }
+    // nothing is in flight when TMEM is released
+    if (leader) mma_commit(smem_u32(&drained));
+    mbar_wait(smem_u32(&drained), 0, p.wc.drain_cycles, nullptr, p.wc.status);
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int tid = threadIdx.x;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const int copy = warp / C::RG, row = tid % C::ROWS;
+    float* om = reinterpret_cast<float*>(smem + C::OFF_O);
+    float2* mls = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    auto sync_rows = [&] { named_bar_sync(1, C::SOFT); };
+    if (tid == 0 && !p.by_unit) p.joins[part] = make_int2(-1, 0);
+    {  // P = 0 where this warp's copy takes no keys
+      const uint32_t zero[32] = {};
+      for (int col = 0; col < 2 * kPagedTile; col += 32) tmem_store(lanes + C::P_COL(0) + col, zero);
+    }
+    int gi = 0, meets = 0;
+    bool ok = true;
+    // all four warps are here (bounded: a warp that gave up does not come)
+    auto meet_warps = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&meet));
+      ok = ok && mbar_wait(smem_u32(&meet), meets & 1, tmo, &abort_flag, p.wc.status);
+      ok = __all_sync(0xffffffffu, ok);
+      ++meets;
+    };
+    for (bool more = w.start(p, share); more; more = w.next(p)) {
+      const int g = w.kv_head(p), rb = w.row_block(p);
+      const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
+      const int64_t row0 = block_row0(p, w.it.b, g, rb, C::ROWS);
+      const int len = w.it.len, n = w.it.n;
+      const int p_lo = len - n, p_hi = len - 1;  // positions of the new tokens
+      const int tok = (rb * C::ROWS + row) % p.Tq, pos = p_lo + tok;
+      // queries, every copy; rows behind the last one zero
+      for (int i = tid; i < C::ROWS * (D / 8); i += C::SOFT) {
+        const int r = i / (D / 8), ch = i - r * (D / 8);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D) + ch);
+#pragma unroll
+        for (int k = 0; k < C::COPIES; ++k)
+          *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(k * C::ROWS + r, ch & 7)) = x;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&q_ready));
+      {
+        const uint32_t zero[32] = {};
+#pragma unroll
+        for (int col = 0; col < D; col += 32) tmem_store(lanes + C::O_COL + col, zero);
+      }
+      float m = kNoMax, l = 0.f;
+      for (int t = w.t0; t < w.t1; ++t, ++gi) {
+        const int slot = gi % C::STAGES, b = gi & 1;
+        ok = ok && mbar_wait(smem_u32(&full[slot]), (gi / C::STAGES) & 1, tmo, &abort_flag, p.wc.status) &&
+             mbar_wait(smem_u32(&s_full[b]), (gi >> 1) & 1, tmo, &abort_flag, p.wc.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[C::KEYS];
+        tmem_load(lanes + C::S_COL(b) + copy * C::KEYS, sv);
+        const int4 kp = *reinterpret_cast<const int4*>(key_pos[slot]);
+        const int j0s[4] = {kp.x, kp.y, kp.z, kp.w};
+        // does every row see all keys of a group; does some group hide keys from some
+        // rows only
+        bool all_seen = true, differ = false;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j0 = j0s[q];
+          all_seen &= j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) && !(p.window > 0 && j0 <= p_hi - p.window);
+          differ |= n > 1 && j0 < len &&
+                    ((p.causal && j0 + 15 > p_lo) ||
+                     (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
+        }
+        tmem_ld_wait();
+        if (!all_seen) {
+#pragma unroll
+          for (int q = 0; q < C::RG; ++q) {
+            const int j0 = key_pos[slot][copy * C::RG + q];
+            const int lo = p.window > 0 ? pos - p.window + 1 - j0 : -j0;
+            const int hi = (p.causal ? min(len, pos + 1) : len) - j0;
+            const unsigned span = static_cast<unsigned>(max(hi - lo, 0));
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (static_cast<unsigned>(e - lo) >= span) sv[16 * q + e] = __float_as_uint(-INFINITY);
+          }
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < C::KEYS; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sv[e]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+        const bool grow = mx - m > kPagedSlack;
+        float alpha = 1.f;
+        if (grow) {
+          alpha = ex2(m - mx);
+          m = mx;
+          l *= alpha;
+        }
+        // weights in two words of the cache's type (see the other kernel)
+        uint32_t hi[C::KEYS / 2], lo[C::KEYS / 2];
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < C::KEYS / 2; ++e) {
+          const float p0 = ex2(fmaf(__uint_as_float(sv[2 * e]), p.scale_log2, -m));
+          const float p1 = ex2(fmaf(__uint_as_float(sv[2 * e + 1]), p.scale_log2, -m));
+          sum[0] += p0;
+          sum[1] += p1;
+          hi[e] = pack2<C::BF16>(p0, p1);
+          const float2 f = unpack2<C::BF16>(hi[e]);
+          lo[e] = pack2<C::BF16>(p0 - f.x, p1 - f.y);
+        }
+        l += sum[0] + sum[1];
+        // (the products that read this buffer before were issued before S of this tile)
+        tmem_store(lanes + C::P_COL(b) + copy * (C::KEYS / 2), hi);
+        tmem_store(lanes + C::P_COL(b) + C::P_LO + copy * (C::KEYS / 2), lo);
+        bool o_idle = t == w.t0;  // no products are adding to O
+        auto wait_o = [&] {
+          if (o_idle) return;
+          ok = ok && mbar_wait(smem_u32(&o_ready[b ^ 1]), ((gi - 1) >> 1) & 1, tmo, &abort_flag, p.wc.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) tc_fence_after();
+          o_idle = ok;
+        };
+        if (t > w.t0 && __any_sync(0xffffffffu, grow)) {
+          wait_o();
+          if (!ok) break;
+#pragma unroll 1
+          for (int col = 0; col < D; col += 32) {
+            uint32_t o[32];
+            tmem_load(lanes + C::O_COL + col, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_store(lanes + C::O_COL + col, o);
+          }
+        }
+        if (!all_seen) {
+          // A key that no row sees gets V = 0 (its slot may hold anything, and 0 * NaN is
+          // not 0); warp w looks after keys 16 w on. Where rows differ in what they see
+          // and some of these values are no finite numbers, those keys are added row by
+          // row and get V = 0 as well.
+          const uint32_t vs = sbase + C::OFF_KV + slot * 2 * C::TILE + C::TILE;
+          uint8_t* v_rows = smem + (vs - sbase);
+          auto kept = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window); };
+          auto partial = [&](int j) {
+            return kept(j) && ((p.causal && j > p_lo) || (p.window > 0 && j <= p_hi - p.window));
+          };
+          const int own = key_pos[slot][warp];
+          auto chunk = [&](int i) {  // 16 bytes of this warp's keys
+            const int e = i / (8 * C::KREG), x = i - e * 8 * C::KREG;
+            return v_rows + (x >> 3) * C::REGION + (16 * warp + e) * 128 + (x & 7) * 16;
+          };
+          bool apart = false;
+          if (differ) {
+            uint32_t odd = 0;
+            for (int i = lane; i < 16 * 8 * C::KREG; i += 32) {
+              if (!partial(own + i / (8 * C::KREG))) continue;
+              const uint4 x = *reinterpret_cast<const uint4*>(chunk(i));
+              odd |= not_finite2<C::BF16>(x.x) | not_finite2<C::BF16>(x.y) | not_finite2<C::BF16>(x.z) |
+                     not_finite2<C::BF16>(x.w);
+            }
+            odd = __any_sync(0xffffffffu, odd != 0);
+            int* flags = odd_flags[meets & 1];
+            if (lane == 0) flags[warp] = static_cast<int>(odd);
+            meet_warps();
+            if (!ok) break;
+            apart = (flags[0] | flags[1] | flags[2] | flags[3]) != 0;
+            if (apart) {
+              wait_o();
+              if (!ok) break;
+              for (int e = 0; e < C::KEYS; ++e) {
+                const int key = copy * C::KEYS + e, j = key_pos[slot][key >> 4] + (key & 15);
+                if (!partial(j)) continue;
+                const float s = __uint_as_float(tmem_ld1(lanes + C::S_COL(b) + key));
+                tmem_ld_wait();
+                const bool seen = !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
+                const float x = ex2(fmaf(s, p.scale_log2, -m));
+#pragma unroll 1
+                for (int col = 0; col < D; col += 32) {
+                  uint32_t o[32];
+                  tmem_load(lanes + C::O_COL + col, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 32; i += 2) {
+                    const int at = col + i;
+                    const float2 v = unpack2<C::BF16>(*reinterpret_cast<const uint32_t*>(
+                        v_rows + (at >> 6) * C::REGION + sw128_offset(key, (at & 63) >> 3) + (at & 7) * 2));
+                    if (seen) {
+                      o[i] = __float_as_uint(fmaf(x, v.x, __uint_as_float(o[i])));
+                      o[i + 1] = __float_as_uint(fmaf(x, v.y, __uint_as_float(o[i + 1])));
+                    }
+                  }
+                  tmem_store(lanes + C::O_COL + col, o);
+                  tmem_st_wait();
+                }
+              }
+              meet_warps();  // before anybody overwrites what others read
+              if (!ok) break;
+            }
+          }
+          for (int i = lane; i < 16 * 8 * C::KREG; i += 32) {
+            const int j = own + i / (8 * C::KREG);
+            if (!kept(j) || (apart && partial(j))) *reinterpret_cast<uint4*>(chunk(i)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[b]));
+      }
+
+      // ------------------------------------------------------ end of a segment
+      if (ok) {  // the last products: they and those before are done
+        ok = mbar_wait(smem_u32(&o_ready[(gi - 1) & 1]), ((gi - 1) >> 1) & 1, tmo, &abort_flag, p.wc.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) tc_fence_after();
+      }
+      // padding rows (tokens the sequence does not have) see nothing; a row that has
+      // met nothing but NaN keeps it
+      if (tok >= n || (m == kNoMax && l == 0.f)) {
+        m = -INFINITY;
+        l = 0.f;
+      }
+      const bool begins = w.t0 == 0, ends = w.t1 == w.it.tiles;
+      const int part_slot = 2 * part + (begins ? 1 : 0);
+      if constexpr (C::COPIES == 1) {
+#pragma unroll 1
+        for (int ch = 0; ch < D / 8; ch += 2) {
+          uint32_t o[16];
+          tmem_load(lanes + C::O_COL + 8 * ch, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = m == -INFINITY ? 0u : o[e];  // nothing seen: not even 0 * inf
+          auto four = [&](int e) {
+            return make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                               __uint_as_float(o[e + 3]));
+          };
+          if (row < rows) {
+            put_piece<C>(p, begins && ends, part_slot, row0, row, ch, four(0), four(4), make_float2(m, l));
+            put_piece<C>(p, begins && ends, part_slot, row0, row, ch + 1, four(8), four(12), make_float2(m, l));
+          }
+          __syncwarp();
+        }
+      } else {
+        mls[copy * C::ROWS + row] = make_float2(m, l);
+        sync_rows();
+        float mt = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < C::COPIES; ++k) mt = fmaxf(mt, mls[k * C::ROWS + row].x);
+        const float f = exp2_rel(m, mt);
+        // each share of the columns is summed by the copies in turn
+        constexpr int SHARE = (D / 16 + C::COPIES - 1) / C::COPIES;
+#pragma unroll 1
+        for (int round = 0; round < C::COPIES; ++round) {
+          const int first = (copy + round) % C::COPIES * SHARE;
+#pragma unroll 1
+          for (int i = first; i < min(first + SHARE, D / 16); ++i) {
+            uint32_t o[16];
+            tmem_load(lanes + C::O_COL + 16 * i, o);
+            tmem_ld_wait();
+            float4* at = reinterpret_cast<float4*>(om + row * C::OP + 16 * i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float4 x = round > 0 ? at[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+              if (m > -INFINITY)  // nothing seen: not even 0 * inf
+                add4(x, make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                    __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])), f);
+              at[k] = x;
+            }
+            __syncwarp();
+          }
+          sync_rows();
+        }
+        for (int i = tid; i < rows * (D / 8); i += C::SOFT) {
+          const int r = i / (D / 8), ch = i - r * (D / 8);
+          const float4 x = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch);
+          const float4 y = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch + 4);
+          float2 ml = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int k = 0; k < C::COPIES; ++k) ml.x = fmaxf(ml.x, mls[k * C::ROWS + r].x);
+#pragma unroll
+          for (int k = 0; k < C::COPIES; ++k) ml.y += mls[k * C::ROWS + r].y * exp2_rel(mls[k * C::ROWS + r].x, ml.x);
+          put_piece<C>(p, begins && ends, part_slot, row0, r, ch, x, y, ml);
+        }
+        sync_rows();
+      }
+      if (tid == 0) record_unit(p, share, w, part);
+      tc_fence_before();
+    }
+    write_empty_units<C>(p, part, parts, tid, C::SOFT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+}  // namespace fa
