@@ -16,11 +16,15 @@
 // copy does not take has P = 0, written once: the columns of the other copies are
 // never touched.
 //
-// Roles: warps 0-3 softmax (thread = TMEM lane = row), warp 4 page look-up and TMA,
-// warp 5 issues the MMAs: S(t) = Q K(t)^T into one of two buffers; the softmax
-// writes P(t) = 2^(S - m) in two words of the cache's type beside it, P_hi + P_lo;
-// O += P_hi V + P_lo V. S(t + 1) is computed while the softmax has S(t). O is
-// rescaled in TMEM when a maximum grows by more than 2^8.
+// Roles: two warpgroups of softmax (thread = TMEM lane = row), which take tiles in
+// turn, each with its own buffers, maxima, sums and accumulator: a tile is a chain of
+// waits and TMEM round trips of over 1100 cycles, more than its bytes take. Warp 8
+// looks pages up and loads by TMA. Warp 9 issues S(t) = Q K(t)^T; the softmax reads
+// it (then S(t + 2) may overwrite it) and writes P(t) = 2^(S - m) in two words of the
+// cache's type, P_hi + P_lo; warp 10 issues O += P_hi V + P_lo V. (One warp for both
+// takes 1500 cycles a tile, in a hundred or more per wait.) O is rescaled in
+// TMEM when a maximum grows by more than 2^8. At the end of a segment both
+// warpgroups read both accumulators, half of the columns each.
 #pragma once
 
 namespace fa {
@@ -33,7 +37,7 @@ struct PagedTcCfg {
   static constexpr int ROWS = 32 * RG;           // rows of a block
   static constexpr int COPIES = 4 / RG;          // of each row
   static constexpr int KEYS = kPagedTile / COPIES;  // of a tile that a copy takes
-  static constexpr int SOFT = 128, THREADS = SOFT + 64;
+  static constexpr int SOFT = 256, THREADS = SOFT + 96;
   static constexpr int KREG = (D + 63) / 64, REGION = kPagedTile * 128, TILE = KREG * REGION;
   static constexpr int QREGION = 128 * 128;
   static constexpr int STAGES = D == 64 ? 8 : RG == 2 ? 4 : 5;
@@ -41,16 +45,16 @@ struct PagedTcCfg {
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
   static constexpr int OFF_O = OFF_Q + KREG * QREGION;
-  static constexpr int OFF_ML = OFF_O + (COPIES > 1 ? ROWS * OP * 4 : 0);  // [copies][rows]
+  static constexpr int OFF_ML = OFF_O + (COPIES > 1 ? ROWS * OP * 4 : 0);  // [warpgroup][copies][rows]
   static constexpr int SMEM_BYTES = OFF_ML + SOFT * 8 + 1024;
   static_assert(SMEM_BYTES <= 231000, "shared memory");
   // TMEM columns
   __host__ __device__ static constexpr int S_COL(int b) { return kPagedTile * b; }
   __host__ __device__ static constexpr int P_COL(int b) { return 2 * kPagedTile + kPagedTile * b; }  // P_hi, then P_lo
   static constexpr int P_LO = kPagedTile / 2;
-  static constexpr int O_COL = 4 * kPagedTile;
+  __host__ __device__ static constexpr int O_COL(int b) { return 4 * kPagedTile + KREG * 64 * b; }
   static constexpr uint32_t TMEM_COLS = 512;
-  static_assert(O_COL + KREG * 64 <= 512, "TMEM");
+  static_assert(4 * kPagedTile + 2 * KREG * 64 <= 512, "TMEM");
 };
 
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
@@ -82,10 +86,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const PagedFwdArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES], s_full[2], p_full[2], o_ready[2], q_ready, drained,
-      meet;
+  __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES], s_full[2], s_free[2], p_full[2], o_ready[2],
+      q_ready, s_drained, o_drained, meet[2];
   __shared__ __align__(16) int key_pos[C::STAGES][kPagedKeyWarps];
-  __shared__ int odd_flags[2][4];
+  __shared__ int odd_flags[2][2][4];
   __shared__ int abort_flag;
   __shared__ uint32_t tmem_slot;
   constexpr int D = C::D;
@@ -102,15 +106,17 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&s_full[b]), 1);
-      mbar_init(smem_u32(&p_full[b]), 4);   // one per softmax warp
-      mbar_init(smem_u32(&o_ready[b]), 1);  // by tile parity: a waiter is never two phases off
+      mbar_init(smem_u32(&s_free[b]), 4);   // one per warp of a warpgroup
+      mbar_init(smem_u32(&p_full[b]), 4);
+      mbar_init(smem_u32(&o_ready[b]), 1);
+      mbar_init(smem_u32(&meet[b]), 4);
     }
-    mbar_init(smem_u32(&q_ready), 4);
-    mbar_init(smem_u32(&drained), 1);
-    mbar_init(smem_u32(&meet), 4);
+    mbar_init(smem_u32(&q_ready), 8);
+    mbar_init(smem_u32(&s_drained), 1);
+    mbar_init(smem_u32(&o_drained), 1);
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(smem_u32(&tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -127,14 +133,15 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   const uint32_t tmem = tmem_slot;
   Walk w;
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ------------------------------------------------------------ producer warp
     TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag);
     produce_share(p, share, w, ring);
     ring.drain();
-  } else if (warp == 5) {
-    // --------------------------------------------------------------- MMA issuer
-    const bool leader = elect_one_sync();
+  } else if (warp >= 9) {
+    // -------------------------------------------------------------- MMA issuers
+    // (all lanes compute the descriptors and one issues)
+    const bool leader = elect_one_sync(), scores = warp == 9;
     constexpr uint32_t idesc_s = make_idesc_f16(128, kPagedTile, C::BF16 ? 1 : 0, 0, 0);
     constexpr uint32_t idesc_o = make_idesc_f16(128, D, C::BF16 ? 1 : 0, 0, 1);
     bool ok = true;
@@ -143,65 +150,64 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       ok = __all_sync(0xffffffffu, ok);
       if (ok) tc_fence_after();
     };
-    auto issue_s = [&](int gi) {  // tile gi's scores, once its keys are there
-      const int slot = gi % C::STAGES, b = gi & 1;
-      wait(full[slot], gi / C::STAGES);
-      if (!ok || !leader) return;
-      const uint32_t qa = sbase + C::OFF_Q, ka = sbase + C::OFF_KV + slot * 2 * C::TILE;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk & 3) * 32;  // 16 elements along K
-        mma_ss(tmem + C::S_COL(b), make_sdesc(qa + (kk >> 2) * C::QREGION + off, 16, 1024, 2),
-               make_sdesc(ka + (kk >> 2) * C::REGION + off, 16, 1024, 2), idesc_s, kk > 0);
-      }
-      mma_commit(smem_u32(&s_full[b]));
-    };
     int gi = 0, seg = 0;
     for (bool more = w.start(p, share); more && ok; more = w.next(p), ++seg) {
-      const int tiles = w.t1 - w.t0;
-      wait(q_ready, seg);
-      for (int i = 0; i < min(2, tiles) && ok; ++i) issue_s(gi + i);
-      for (int i = 0; i < tiles && ok; ++i, ++gi) {
+      const int first = gi, end = gi + w.t1 - w.t0;
+      if (scores) wait(q_ready, seg);
+      for (; gi < end && ok; ++gi) {
         const int slot = gi % C::STAGES, b = gi & 1;
-        wait(p_full[b], gi >> 1);
-        if (!ok) break;
-        if (leader) {
-          const uint32_t va = sbase + C::OFF_KV + slot * 2 * C::TILE + C::TILE;
+        const uint32_t kv = sbase + C::OFF_KV + slot * 2 * C::TILE;
+        if (scores) {
+          wait(full[slot], gi / C::STAGES);
+          if (gi - 2 >= first) wait(s_free[b], (gi - 2) >> 1);  // (before: read at the end of the segment)
+          if (!ok) break;
 #pragma unroll
-          for (int word = 0; word < 2; ++word)
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk & 3) * 32;  // 16 elements along K
+            const uint64_t qd = make_sdesc(sbase + C::OFF_Q + (kk >> 2) * C::QREGION + off, 16, 1024, 2);
+            const uint64_t kd = make_sdesc(kv + (kk >> 2) * C::REGION + off, 16, 1024, 2);
+            if (leader) mma_ss(tmem + C::S_COL(b), qd, kd, idesc_s, kk > 0);
+          }
+          if (leader) mma_commit(smem_u32(&s_full[b]));
+        } else {
+          wait(p_full[b], gi >> 1);
+          if (!ok) break;
 #pragma unroll
-            for (int kk = 0; kk < kPagedTile / 16; ++kk)
-              mma_ts(tmem + C::O_COL, tmem + C::P_COL(b) + word * C::P_LO + kk * 8,
-                     make_sdesc(va + kk * 16 * 128, C::REGION, 1024, 2), idesc_o, 1);
-          mma_commit(smem_u32(&o_ready[b]));
-          mma_commit(smem_u32(&empty[slot]));
+          for (int kk = 0; kk < kPagedTile / 16; ++kk) {
+            const uint64_t vd = make_sdesc(kv + C::TILE + kk * 16 * 128, C::REGION, 1024, 2);
+            const uint32_t pc = tmem + C::P_COL(b) + kk * 8;
+            if (leader) mma_ts(tmem + C::O_COL(b), pc, vd, idesc_o, 1);
+            if (leader) mma_ts(tmem + C::O_COL(b), pc + C::P_LO, vd, idesc_o, 1);
+          }
+          if (leader) mma_commit(smem_u32(&o_ready[b]));
+          if (leader) mma_commit(smem_u32(&empty[slot]));
         }
-        if (i + 2 < tiles) issue_s(gi + 2);  // its buffer's P is written, its scores read
       }
     }
     // nothing is in flight when TMEM is released
+    uint64_t& drained = scores ? s_drained : o_drained;
     if (leader) mma_commit(smem_u32(&drained));
     mbar_wait(smem_u32(&drained), 0, p.wc.drain_cycles, nullptr, p.wc.status);
   } else {
     // ------------------------------------------------------------------ softmax
-    const int tid = threadIdx.x;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-    const int copy = warp / C::RG, row = tid % C::ROWS;
+    const int tid = threadIdx.x, b = warp >> 2, quarter = warp & 3;  // warpgroup b: tiles and buffers of parity b
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    const int copy = quarter / C::RG, row = tid % C::ROWS;
     float* om = reinterpret_cast<float*>(smem + C::OFF_O);
     float2* mls = reinterpret_cast<float2*>(smem + C::OFF_ML);
     auto sync_rows = [&] { named_bar_sync(1, C::SOFT); };
     if (tid == 0 && !p.by_unit) p.joins[part] = make_int2(-1, 0);
     {  // P = 0 where this warp's copy takes no keys
       const uint32_t zero[32] = {};
-      for (int col = 0; col < 2 * kPagedTile; col += 32) tmem_store(lanes + C::P_COL(0) + col, zero);
+      for (int col = 0; col < kPagedTile; col += 32) tmem_store(lanes + C::P_COL(b) + col, zero);
     }
-    int gi = 0, meets = 0;
+    int begin = 0, meets = 0;  // tiles of the segments before
     bool ok = true;
-    // all four warps are here (bounded: a warp that gave up does not come)
+    // all four warps of the warpgroup are here (bounded: a warp that gave up does not come)
     auto meet_warps = [&] {
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&meet));
-      ok = ok && mbar_wait(smem_u32(&meet), meets & 1, tmo, &abort_flag, p.wc.status);
+      if (lane == 0) mbar_arrive(smem_u32(&meet[b]));
+      ok = ok && mbar_wait(smem_u32(&meet[b]), meets & 1, tmo, &abort_flag, p.wc.status);
       ok = __all_sync(0xffffffffu, ok);
       ++meets;
     };
@@ -227,11 +233,20 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       {
         const uint32_t zero[32] = {};
 #pragma unroll
-        for (int col = 0; col < D; col += 32) tmem_store(lanes + C::O_COL + col, zero);
+        for (int col = 0; col < D; col += 32) tmem_store(lanes + C::O_COL(b) + col, zero);
       }
       float m = kNoMax, l = 0.f;
-      for (int t = w.t0; t < w.t1; ++t, ++gi) {
-        const int slot = gi % C::STAGES, b = gi & 1;
+      const int end = begin + w.t1 - w.t0;
+      // products of this warpgroup's tile before gi are done (before the segment: waited
+      // for at the end of the last one)
+      auto wait_o = [&](int gi) {
+        if (gi - 2 < begin) return;
+        ok = ok && mbar_wait(smem_u32(&o_ready[b]), ((gi - 2) >> 1) & 1, tmo, &abort_flag, p.wc.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) tc_fence_after();
+      };
+      for (int gi = begin + ((begin ^ b) & 1); gi < end; gi += 2) {
+        const int slot = gi % C::STAGES;
         ok = ok && mbar_wait(smem_u32(&full[slot]), (gi / C::STAGES) & 1, tmo, &abort_flag, p.wc.status) &&
              mbar_wait(smem_u32(&s_full[b]), (gi >> 1) & 1, tmo, &abort_flag, p.wc.status);
         ok = __all_sync(0xffffffffu, ok);
@@ -253,6 +268,12 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                      (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
         }
         tmem_ld_wait();
+        auto free_scores = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s_free[b]));
+        };
+        if (!differ) free_scores();  // (else they may be read again below)
         if (!all_seen) {
 #pragma unroll
           for (int q = 0; q < C::RG; ++q) {
@@ -290,33 +311,24 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           lo[e] = pack2<C::BF16>(p0 - f.x, p1 - f.y);
         }
         l += sum[0] + sum[1];
-        // (the products that read this buffer before were issued before S of this tile)
+        wait_o(gi);  // the products that read the last P, and added to O
+        if (!ok) break;
         tmem_store(lanes + C::P_COL(b) + copy * (C::KEYS / 2), hi);
         tmem_store(lanes + C::P_COL(b) + C::P_LO + copy * (C::KEYS / 2), lo);
-        bool o_idle = t == w.t0;  // no products are adding to O
-        auto wait_o = [&] {
-          if (o_idle) return;
-          ok = ok && mbar_wait(smem_u32(&o_ready[b ^ 1]), ((gi - 1) >> 1) & 1, tmo, &abort_flag, p.wc.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) tc_fence_after();
-          o_idle = ok;
-        };
-        if (t > w.t0 && __any_sync(0xffffffffu, grow)) {
-          wait_o();
-          if (!ok) break;
+        if (gi - 2 >= begin && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
           for (int col = 0; col < D; col += 32) {
             uint32_t o[32];
-            tmem_load(lanes + C::O_COL + col, o);
+            tmem_load(lanes + C::O_COL(b) + col, o);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_store(lanes + C::O_COL + col, o);
+            tmem_store(lanes + C::O_COL(b) + col, o);
           }
         }
         if (!all_seen) {
           // A key that no row sees gets V = 0 (its slot may hold anything, and 0 * NaN is
-          // not 0); warp w looks after keys 16 w on. Where rows differ in what they see
+          // not 0); warp w of the four looks after keys 16 w on. Where rows differ in what they see
           // and some of these values are no finite numbers, those keys are added row by
           // row and get V = 0 as well.
           const uint32_t vs = sbase + C::OFF_KV + slot * 2 * C::TILE + C::TILE;
@@ -325,10 +337,10 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           auto partial = [&](int j) {
             return kept(j) && ((p.causal && j > p_lo) || (p.window > 0 && j <= p_hi - p.window));
           };
-          const int own = key_pos[slot][warp];
+          const int own = key_pos[slot][quarter];
           auto chunk = [&](int i) {  // 16 bytes of this warp's keys
             const int e = i / (8 * C::KREG), x = i - e * 8 * C::KREG;
-            return v_rows + (x >> 3) * C::REGION + (16 * warp + e) * 128 + (x & 7) * 16;
+            return v_rows + (x >> 3) * C::REGION + (16 * quarter + e) * 128 + (x & 7) * 16;
           };
           bool apart = false;
           if (differ) {
@@ -340,14 +352,13 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                      not_finite2<C::BF16>(x.w);
             }
             odd = __any_sync(0xffffffffu, odd != 0);
-            int* flags = odd_flags[meets & 1];
-            if (lane == 0) flags[warp] = static_cast<int>(odd);
+            int* flags = odd_flags[b][meets & 1];
+            if (lane == 0) flags[quarter] = static_cast<int>(odd);
             meet_warps();
             if (!ok) break;
             apart = (flags[0] | flags[1] | flags[2] | flags[3]) != 0;
             if (apart) {
-              wait_o();
-              if (!ok) break;
+              tmem_st_wait();
               for (int e = 0; e < C::KEYS; ++e) {
                 const int key = copy * C::KEYS + e, j = key_pos[slot][key >> 4] + (key & 15);
                 if (!partial(j)) continue;
@@ -358,7 +369,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
 #pragma unroll 1
                 for (int col = 0; col < D; col += 32) {
                   uint32_t o[32];
-                  tmem_load(lanes + C::O_COL + col, o);
+                  tmem_load(lanes + C::O_COL(b) + col, o);
                   tmem_ld_wait();
 #pragma unroll
                   for (int i = 0; i < 32; i += 2) {
@@ -370,13 +381,14 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                       o[i + 1] = __float_as_uint(fmaf(x, v.y, __uint_as_float(o[i + 1])));
                     }
                   }
-                  tmem_store(lanes + C::O_COL + col, o);
+                  tmem_store(lanes + C::O_COL(b) + col, o);
                   tmem_st_wait();
                 }
               }
               meet_warps();  // before anybody overwrites what others read
               if (!ok) break;
             }
+            free_scores();
           }
           for (int i = lane; i < 16 * 8 * C::KREG; i += 32) {
             const int j = own + i / (8 * C::KREG);
@@ -391,11 +403,14 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       }
 
       // ------------------------------------------------------ end of a segment
-      if (ok) {  // the last products: they and those before are done
-        ok = mbar_wait(smem_u32(&o_ready[(gi - 1) & 1]), ((gi - 1) >> 1) & 1, tmo, &abort_flag, p.wc.status);
+      // The last products of both warpgroups. (Nobody starts the next segment, whose
+      // products would move these barriers on, before all have come to sync_rows.)
+      for (int gi = max(begin, end - 2); gi < end; ++gi) {
+        ok = ok && mbar_wait(smem_u32(&o_ready[gi & 1]), (gi >> 1) & 1, tmo, &abort_flag, p.wc.status);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) tc_fence_after();
       }
+      begin = end;
       // padding rows (tokens the sequence does not have) see nothing; a row that has
       // met nothing but NaN keeps it
       if (tok >= n || (m == kNoMax && l == 0.f)) {
@@ -404,51 +419,69 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       }
       const bool begins = w.t0 == 0, ends = w.t1 == w.it.tiles;
       const int part_slot = 2 * part + (begins ? 1 : 0);
-      if constexpr (C::COPIES == 1) {
-#pragma unroll 1
-        for (int ch = 0; ch < D / 8; ch += 2) {
-          uint32_t o[16];
-          tmem_load(lanes + C::O_COL + 8 * ch, o);
-          tmem_ld_wait();
+      mls[tid] = make_float2(m, l);  // [warpgroup][copy][row]
+      sync_rows();
+      const float2 ml0 = mls[tid & 127], ml1 = mls[128 + (tid & 127)];
+      float mt = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = m == -INFINITY ? 0u : o[e];  // nothing seen: not even 0 * inf
-          auto four = [&](int e) {
-            return make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                               __uint_as_float(o[e + 3]));
+      for (int k = 0; k < 2 * C::COPIES; ++k) mt = fmaxf(mt, mls[k * C::ROWS + row].x);
+      const float f0 = exp2_rel(ml0.x, mt), f1 = exp2_rel(ml1.x, mt);
+      // columns [16 i, 16 i + 16) of this lane's row over both warpgroups
+      auto sum16 = [&](int i, float4 (&x)[4]) {
+        uint32_t o0[16], o1[16];
+        tmem_load(lanes + C::O_COL(0) + 16 * i, o0);
+        tmem_load(lanes + C::O_COL(1) + 16 * i, o1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          auto four = [&](const uint32_t (&o)[16]) {
+            return make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                               __uint_as_float(o[4 * k + 3]));
           };
+          if (ml0.x > -INFINITY) add4(x[k], four(o0), f0);  // nothing seen: not even 0 * inf
+          if (ml1.x > -INFINITY) add4(x[k], four(o1), f1);
+        }
+        __syncwarp();
+      };
+      auto row_sum = [&](int r) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int k = 0; k < 2 * C::COPIES; ++k) ml.x = fmaxf(ml.x, mls[k * C::ROWS + r].x);
+#pragma unroll
+        for (int k = 0; k < 2 * C::COPIES; ++k) ml.y += mls[k * C::ROWS + r].y * exp2_rel(mls[k * C::ROWS + r].x, ml.x);
+        return ml;
+      };
+      if constexpr (C::COPIES == 1) {
+        const float2 ml = row_sum(row);
+#pragma unroll 1
+        for (int i = b; i < D / 16; i += 2) {
+          float4 x[4];
+          sum16(i, x);
           if (row < rows) {
-            put_piece<C>(p, begins && ends, part_slot, row0, row, ch, four(0), four(4), make_float2(m, l));
-            put_piece<C>(p, begins && ends, part_slot, row0, row, ch + 1, four(8), four(12), make_float2(m, l));
+            put_piece<C>(p, begins && ends, part_slot, row0, row, 2 * i, x[0], x[1], ml);
+            put_piece<C>(p, begins && ends, part_slot, row0, row, 2 * i + 1, x[2], x[3], ml);
           }
           __syncwarp();
         }
       } else {
-        mls[copy * C::ROWS + row] = make_float2(m, l);
-        sync_rows();
-        float mt = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < C::COPIES; ++k) mt = fmaxf(mt, mls[k * C::ROWS + row].x);
-        const float f = exp2_rel(m, mt);
-        // each share of the columns is summed by the copies in turn
+        // each share of the columns is summed by the copies in turn, half of it by each
+        // warpgroup
         constexpr int SHARE = (D / 16 + C::COPIES - 1) / C::COPIES;
 #pragma unroll 1
         for (int round = 0; round < C::COPIES; ++round) {
           const int first = (copy + round) % C::COPIES * SHARE;
 #pragma unroll 1
           for (int i = first; i < min(first + SHARE, D / 16); ++i) {
-            uint32_t o[16];
-            tmem_load(lanes + C::O_COL + 16 * i, o);
-            tmem_ld_wait();
+            if ((i & 1) != b) continue;
+            float4 x[4];
+            sum16(i, x);
             float4* at = reinterpret_cast<float4*>(om + row * C::OP + 16 * i);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              float4 x = round > 0 ? at[k] : make_float4(0.f, 0.f, 0.f, 0.f);
-              if (m > -INFINITY)  // nothing seen: not even 0 * inf
-                add4(x, make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                    __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])), f);
-              at[k] = x;
+              if (round > 0) add4(x[k], at[k], 1.f);
+              at[k] = x[k];
             }
-            __syncwarp();
           }
           sync_rows();
         }
@@ -456,23 +489,19 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           const int r = i / (D / 8), ch = i - r * (D / 8);
           const float4 x = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch);
           const float4 y = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch + 4);
-          float2 ml = make_float2(-INFINITY, 0.f);
-#pragma unroll
-          for (int k = 0; k < C::COPIES; ++k) ml.x = fmaxf(ml.x, mls[k * C::ROWS + r].x);
-#pragma unroll
-          for (int k = 0; k < C::COPIES; ++k) ml.y += mls[k * C::ROWS + r].y * exp2_rel(mls[k * C::ROWS + r].x, ml.x);
-          put_piece<C>(p, begins && ends, part_slot, row0, r, ch, x, y, ml);
+          put_piece<C>(p, begins && ends, part_slot, row0, r, ch, x, y, row_sum(r));
         }
-        sync_rows();
       }
-      if (tid == 0) record_unit(p, share, w, part);
       tc_fence_before();
+      sync_rows();  // accumulators, rows and sums are read
+      tc_fence_after();
+      if (tid == 0) record_unit(p, share, w, part);
     }
     write_empty_units<C>(p, part, parts, tid, C::SOFT);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
