@@ -158,9 +158,16 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         const int slot = gi % C::STAGES, b = gi & 1;
         const uint32_t kv = sbase + C::OFF_KV + slot * 2 * C::TILE;
         if (scores) {
-          wait(full[slot], gi / C::STAGES);
-          if (gi - 2 >= first) wait(s_free[b], (gi - 2) >> 1);  // (before: read at the end of the segment)
-          if (!ok) break;
+          // (scores of the segment before: read at its end)
+          const bool there = mbar_test_wait(smem_u32(&full[slot]), gi / C::STAGES & 1);
+          const bool read = gi - 2 < first || mbar_test_wait(smem_u32(&s_free[b]), ((gi - 2) >> 1) & 1);
+          if (__all_sync(0xffffffffu, there && read)) {
+            tc_fence_after();
+          } else {
+            wait(full[slot], gi / C::STAGES);
+            if (gi - 2 >= first) wait(s_free[b], (gi - 2) >> 1);
+            if (!ok) break;
+          }
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk & 3) * 32;  // 16 elements along K
@@ -240,17 +247,24 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       // products of this warpgroup's tile before gi are done (before the segment: waited
       // for at the end of the last one)
       auto wait_o = [&](int gi) {
-        if (gi - 2 < begin) return;
         ok = ok && mbar_wait(smem_u32(&o_ready[b]), ((gi - 2) >> 1) & 1, tmo, &abort_flag, p.wc.status);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) tc_fence_after();
       };
       for (int gi = begin + ((begin ^ b) & 1); gi < end; gi += 2) {
         const int slot = gi % C::STAGES;
-        ok = ok && mbar_wait(smem_u32(&full[slot]), (gi / C::STAGES) & 1, tmo, &abort_flag, p.wc.status) &&
-             mbar_wait(smem_u32(&s_full[b]), (gi >> 1) & 1, tmo, &abort_flag, p.wc.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        // a wait that finds its phase complete still takes a hundred cycles and more: all
+        // three are tried at once
+        const uint32_t bar_kv = smem_u32(&full[slot]), bar_s = smem_u32(&s_full[b]);
+        const bool there = mbar_test_wait(bar_kv, (gi / C::STAGES) & 1), scored = mbar_test_wait(bar_s, (gi >> 1) & 1);
+        const bool added = gi - 2 < begin || mbar_test_wait(smem_u32(&o_ready[b]), ((gi - 2) >> 1) & 1);
+        const bool o_idle = __all_sync(0xffffffffu, added);
+        if (!__all_sync(0xffffffffu, there && scored)) {
+          ok = ok && mbar_wait(bar_kv, (gi / C::STAGES) & 1, tmo, &abort_flag, p.wc.status) &&
+               mbar_wait(bar_s, (gi >> 1) & 1, tmo, &abort_flag, p.wc.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
         tc_fence_after();
         uint32_t sv[C::KEYS];
         tmem_load(lanes + C::S_COL(b) + copy * C::KEYS, sv);
@@ -311,7 +325,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           lo[e] = pack2<C::BF16>(p0 - f.x, p1 - f.y);
         }
         l += sum[0] + sum[1];
-        wait_o(gi);  // the products that read the last P, and added to O
+        if (!o_idle) wait_o(gi);  // the products that read the last P, and added to O
         if (!ok) break;
         tmem_store(lanes + C::P_COL(b) + copy * (C::KEYS / 2), hi);
         tmem_store(lanes + C::P_COL(b) + C::P_LO + copy * (C::KEYS / 2), lo);
