@@ -28,12 +28,16 @@
 // from the tile), query rows its 8 columns, so a group of up to 8 heads fills a
 // fragment that would be half empty the other way round.
 //
+// Split lists of more than 16 rows per KV head (D up to 128) go to the kernel of
+// fa_paged_tc.cuh, whose products are on tcgen05.
+//
 // Measured, share of the copy rate (6787 GB/s): up to 8 rows 95% (D 64, 96, 128; B1
 // 131072 keys of 8 KV heads, 537 MB, 84-87 us), 90% (D 256); 16 rows 84-86%. There the
 // tensor pipe is 14% active and the loads bound the kernel: a tcgen05 tile with its
-// round trip through TMEM has nothing to gain. 24 rows 63%, 32 rows 73%, 40 rows
-// 55%, 64 rows 29%: bound by issue (about 270 instructions per warp and tile with two
-// warps per scheduler); 16 consumer warps instead of 8 gave the same.
+// round trip through TMEM has nothing to gain. With more rows these products are
+// bound by issue (about 270 instructions per warp and tile with two warps per
+// scheduler; 16 consumer warps instead of 8 gave the same): 32 rows 73%, 40 rows 55%,
+// 64 rows 29%.
 #pragma once
 
 #include "fa_inst.cuh"
@@ -44,7 +48,6 @@ namespace fa {
 
 constexpr int kPagedKeyWarps = 4;       // warps that share a tile's keys, 16 each
 constexpr int kPagedMaxRanks = 16;      // CTAs of a cluster (above 8: allowed per kernel)
-constexpr int kPagedClusterTiles = 16;  // tiles per CTA up to which clusters are used
 
 struct PagedFwdArgs {
   PagedView c;
@@ -74,6 +77,9 @@ struct PagedCfg {
   static constexpr int D = D_, NT = NT_, RW = RW_;
   static constexpr bool BF16 = BF16_;
   static constexpr bool CLUSTER = CLUSTER_;          // a cluster per unit instead of equal shares
+  // Tiles per CTA up to which clusters are used. 64 rows, D 128, 16 units of 64 tiles (16
+  // per CTA): 28.7 us, split 21.7; of 32 tiles: 18.0 and 18.4; 24 rows, 64 tiles 17.6 and 19.4.
+  static constexpr int CLUSTER_TILES = NT == 4 ? 8 : 16;
   static constexpr int KW = kPagedKeyWarps;
   static constexpr int ROWS = 8 * NT * RW;           // rows of a block
   static constexpr int WARPS = KW * RW;              // consumer warps
@@ -81,6 +87,7 @@ struct PagedCfg {
   // equal split leaves, a warpgroup of producers (one works) that gives its own up.
   static constexpr bool SPLIT = RW > 1 && NT * D >= 384;
   static constexpr int THREADS = 32 * (WARPS + (SPLIT ? 4 : 1));
+  static constexpr int PRODUCERS = 1;
   static constexpr int REG_PRODUCER = 40, REG_CONSUMER = 224;
   static constexpr int REG_NEEDED = SPLIT ? 128 * REG_PRODUCER + 32 * WARPS * REG_CONSUMER : 0;
   static constexpr int KREG = (D + 63) / 64;         // 64-column regions of a row
@@ -387,7 +394,8 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t x) {
 // A position no query reaches: the key's slot was not loaded.
 constexpr int kNoPosition = 0x7fffff00;
 
-// The producer warp's side of a CTA's ring of K and V tiles.
+// A producer warp's side of a CTA's ring of K and V tiles: all of them, or with two
+// producers (C::PRODUCERS) every other one.
 template <class C>
 struct TileRing {
   const PagedFwdArgs& p;
@@ -396,18 +404,24 @@ struct TileRing {
   int (*key_pos)[kPagedKeyWarps];    // position of the first of each 16 keys of a stage
   int* abort_flag;
   int piece, pieces;                 // keys of a page in one tile, pages of a tile
-  int lane, issued = 0;
+  int lane, producer, issued = 0;      // (those of the other producer count too)
   bool ok = true;
   __device__ __forceinline__ TileRing(const PagedFwdArgs& p_, const CUtensorMap& mk, const CUtensorMap& mv, uint32_t kv_,
-                                      uint64_t* full_, uint64_t* empty_, int (*key_pos_)[kPagedKeyWarps], int* abort_)
+                                      uint64_t* full_, uint64_t* empty_, int (*key_pos_)[kPagedKeyWarps], int* abort_,
+                                      int producer_ = 0)
       : p(p_), map_k(mk), map_v(mv), kv(kv_), full(smem_u32(full_)), empty(smem_u32(empty_)), key_pos(key_pos_),
         abort_flag(abort_), piece(min(1 << p_.c.page_shift, kPagedTile)), pieces(kPagedTile / piece),
-        lane(threadIdx.x & 31) {}
+        lane(threadIdx.x & 31), producer(producer_) {}
+  __device__ __forceinline__ bool mine(int tile) const { return C::PRODUCERS == 1 || tile % C::PRODUCERS == producer; }
   // One tile of KV head g into the next stage: lane i < pieces has the page (in the
   // sequence, and in the pool or -1) of its piece i, whose first key is key `x` of
   // the list plus i pieces.
   __device__ __forceinline__ void load(int x, int pg, int id, int g) {
     const PagedView& c = p.c;
+    if (!mine(issued)) {
+      ++issued;
+      return;
+    }
     const int slot = issued % C::STAGES;
     if (issued >= C::STAGES)
       ok = mbar_wait(empty + 8 * slot, ((issued / C::STAGES) - 1) & 1, p.wc.timeout_cycles, abort_flag, p.wc.status);
@@ -439,7 +453,9 @@ struct TileRing {
   // Stay until the last loads have landed: the consumers have waited for them too,
   // unless one of their waits gave up.
   __device__ __forceinline__ void drain() const {
-    if (lane == 0) drain_ring(full, C::STAGES, issued, p.wc.drain_cycles, p.wc.status);
+    if (lane != 0) return;
+    for (int i = max(0, issued - C::STAGES); i < issued; ++i)
+      if (mine(i)) mbar_wait(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, p.wc.drain_cycles, nullptr, p.wc.status);
   }
 };
 
@@ -1118,6 +1134,42 @@ inline bool encode_maps(const PagedFwdLaunch& a, int D, CUtensorMap* mk, CUtenso
          encode_tile_map(mv, a.c.v, a.bf16, D, page, a.c.num_pages * a.c.Hkv, piece);
 }
 
+// Clusters of `ranks` CTAs that run at once on the current device, which is less than
+// its CTAs over `ranks`: a cluster stays within a GPC (a CTA per SM, 152 SMs: 36 of 4,
+// 15 of 8, 7 of 16). 0 where the size is not possible. Kept per device.
+template <class C>
+int resident_clusters(int ranks) {
+  constexpr int kDevices = 16;
+  static std::atomic<int> known[kDevices][5];  // one more than the answer
+  int dev = 0, slot = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  while ((1 << slot) < ranks) ++slot;
+  if (dev < kDevices) {
+    const int k = known[dev][slot].load(std::memory_order_relaxed);
+    if (k > 0) return k - 1;
+  }
+  auto kern = fa_paged_fwd_kernel<C>;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = static_cast<unsigned>(ranks);
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(ranks), 1, 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  int n = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess ||
+      (ranks > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (dev < kDevices) known[dev][slot].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 template <class C>
 cudaError_t launch_paged(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t grid, int ranks) {
   CUtensorMap mk, mv;
@@ -1200,16 +1252,14 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   if (a.window > 0 && !a.sel)  // window + Tq - 1 keys, wherever they start in a tile
     tiles = std::min(tiles, (static_cast<int64_t>(a.window) + a.Tq - 2) / kPagedTile + 2);
   const int64_t units = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks;
-  const int64_t wave = static_cast<int64_t>(device_sm_count()) * C::CTAS;
-  // Short units: a cluster each (16 CTAs only on a whole GPU), joined in the same
-  // launch, where all clusters run at once or one CTA does for a unit. Measured: 16
-  // tiles, 4 units 4.6 us against 12.0 with the split list and its join; 64 tiles, 8
-  // units 7.1 us with 16 CTAs, 8.0 with 8 and 11.2 split.
+  // Short units: a cluster each, joined in the same launch, where all clusters run at
+  // once or one CTA does for a unit. Measured: 16 tiles, 4 units 4.6 us against 12.0
+  // with the split list and its join; 64 tiles, 8 units 7.1 us with 16 CTAs, 8.0 with
+  // 8 and 11.2 split.
   int ranks = 1;
-  const int most_ranks = device_sm_count() >= 128 ? kPagedMaxRanks : 8;
-  while (tiles > 2 && ranks < most_ranks && ranks < tiles) ranks *= 2;  // 2 tiles: 5.7 us in one CTA, 6.6 in two
-  while (ranks > 1 && units * ranks > wave) ranks /= 2;
-  if (tiles <= kPagedClusterTiles * ranks) return launch_paged<C>(a, p, units * ranks, ranks);
+  while (tiles > 2 && ranks < kPagedMaxRanks && ranks < tiles) ranks *= 2;  // 2 tiles: 5.7 us in one CTA, 6.6 in two
+  while (ranks > 1 && units > resident_clusters<C>(ranks)) ranks /= 2;
+  if (tiles <= C::CLUSTER_TILES * ranks) return launch_paged<C>(a, p, units * ranks, ranks);
   if constexpr (D < 256 && RW > 1) {  // more than 16 rows
     switch (paged_split_rows(p.rows, D)) {
       case 32: return run_split_tc<D, 1, BF16>(a, p, tiles);

@@ -18,13 +18,20 @@
 //
 // Roles: two warpgroups of softmax (thread = TMEM lane = row), which take tiles in
 // turn, each with its own buffers, maxima, sums and accumulator: a tile is a chain of
-// waits and TMEM round trips of over 1100 cycles, more than its bytes take. Warp 8
-// looks pages up and loads by TMA. Warp 9 issues S(t) = Q K(t)^T; the softmax reads
+// waits and TMEM round trips of over 1100 cycles, more than its bytes take. One or two
+// warps look pages up and load by TMA (one takes 1000 cycles a tile and more). One
+// warp issues S(t) = Q K(t)^T; the softmax reads
 // it (then S(t + 2) may overwrite it) and writes P(t) = 2^(S - m) in two words of the
-// cache's type, P_hi + P_lo; warp 10 issues O += P_hi V + P_lo V. (One warp for both
+// cache's type, P_hi + P_lo; another issues O += P_hi V + P_lo V. (One warp for both
 // takes 1500 cycles a tile, in a hundred or more per wait.) O is rescaled in
 // TMEM when a maximum grows by more than 2^8. At the end of a segment both
 // warpgroups read both accumulators, half of the columns each.
+//
+// Measured (269 MB of bf16 keys and values, 16 units, start and join of some 10 us
+// included; warp-level products in brackets): D 128, 32 rows 56 us (64), 64 rows 61
+// (111), 128 rows 69 (190); D 64, 32 rows 60 (80), 64 rows 67 (128), 128 rows 95
+// (233). At D 128 the loads bound it up to 64 rows (537 MB 93 us, 85% of the copy
+// rate), at D 64, with half the bytes per tile, the softmax's chain.
 #pragma once
 
 namespace fa {
@@ -37,7 +44,10 @@ struct PagedTcCfg {
   static constexpr int ROWS = 32 * RG;           // rows of a block
   static constexpr int COPIES = 4 / RG;          // of each row
   static constexpr int KEYS = kPagedTile / COPIES;  // of a tile that a copy takes
-  static constexpr int SOFT = 256, THREADS = SOFT + 96;
+  // (128 rows, where the softmax bounds the kernel: 68.8 us with one producer, 75.2
+  // with two; 64 rows D = 64 in pages of 16: 92.9 and 72.5)
+  static constexpr int PRODUCERS = RG == 4 ? 1 : 2;
+  static constexpr int SOFT = 256, THREADS = SOFT + 32 * PRODUCERS + 64, SCORE_WARP = 8 + PRODUCERS;
   static constexpr int KREG = (D + 63) / 64, REGION = kPagedTile * 128, TILE = KREG * REGION;
   static constexpr int QREGION = 128 * 128;
   static constexpr int STAGES = D == 64 ? 8 : RG == 2 ? 4 : 5;
@@ -116,7 +126,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     mbar_init(smem_u32(&o_drained), 1);
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == C::SCORE_WARP) {
     tmem_alloc(smem_u32(&tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -133,15 +143,15 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   const uint32_t tmem = tmem_slot;
   Walk w;
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ producer warp
-    TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag);
+  if (warp >= 8 && warp < 8 + C::PRODUCERS) {
+    // ----------------------------------------------------------- producer warps
+    TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag, warp - 8);
     produce_share(p, share, w, ring);
     ring.drain();
-  } else if (warp >= 9) {
+  } else if (warp >= 8) {
     // -------------------------------------------------------------- MMA issuers
     // (all lanes compute the descriptors and one issues)
-    const bool leader = elect_one_sync(), scores = warp == 9;
+    const bool leader = elect_one_sync(), scores = warp == C::SCORE_WARP;
     constexpr uint32_t idesc_s = make_idesc_f16(128, kPagedTile, C::BF16 ? 1 : 0, 0, 0);
     constexpr uint32_t idesc_o = make_idesc_f16(128, D, C::BF16 ? 1 : 0, 0, 1);
     bool ok = true;
@@ -515,7 +525,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::SCORE_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }

@@ -253,6 +253,114 @@ def test_attend_hidden_keys_add_nothing(what):
             assert torch.equal(o[0, :, r], clean[0][0, :, r]), (bad, r)
 
 
+# Units too many or lists too long for clusters, with more than 16 rows per KV head: one, two or four groups of 32 rows.
+# B, Hq, Hkv, D, page, Tq, lengths, new lengths, causal, window, dtype
+MANY_ROWS = [
+    (1, 17, 1, 64, 64, 1, [17000], None, True, 0, "bf16"),
+    (1, 33, 1, 64, 256, 1, [16500], None, False, 0, "fp16"),
+    (1, 70, 1, 64, 16, 1, [20001], None, True, 0, "bf16"),
+    (1, 130, 1, 64, 64, 1, [9001], None, True, 0, "fp16"),
+    (1, 4, 1, 96, 32, 5, [17003], None, True, 0, "bf16"),
+    (1, 48, 1, 96, 16, 1, [17003], None, True, 0, "fp16"),
+    (1, 100, 1, 96, 128, 1, [17003], None, True, 5000, "bf16"),
+    (1, 24, 1, 128, 16, 1, [17003], None, True, 0, "bf16"),
+    (1, 8, 1, 128, 64, 8, [17003], None, True, 0, "fp16"),
+    (1, 16, 1, 128, 64, 8, [17000], None, True, 0, "bf16"),
+    (80, 20, 1, 64, 16, 1, [1100, 0, 1, 1025, 64] + [3] * 75, None, True, 0, "bf16"),
+    (40, 10, 2, 128, 32, 4, [1100, 2, 0, 2100, 65] + [5] * 35, [4, 1, 0, 3, 2] + [4] * 35, True, 0, "fp16"),
+    (40, 16, 2, 96, 64, 7, [2200, 2, 0, 2100, 65] + [70] * 35, [7, 1, 3, 6, 2] + [4] * 35, True, 70, "bf16"),
+    (40, 40, 2, 64, 16, 3, [2200, 2, 0, 2100, 65] + [70] * 35, [3, 1, 3, 0, 2] + [3] * 35, False, 1500, "fp16"),
+    (3, 24, 1, 256, 64, 1, [17003, 64, 5000], None, True, 0, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", MANY_ROWS, ids=lambda c: f"B{c[0]}h{c[1]}x{c[2]}d{c[3]}p{c[4]}T{c[5]}c{int(c[8])}w{c[9]}{c[10]}")
+def test_attend_many_rows_of_long_lists(case):
+    B, Hq, Hkv, D, page, Tq, lens, new, causal, window, dt = case
+    k, v, table, q = paged_inputs(B, Hq, Hkv, D, page, Tq, lens, DT[dt], seed=Hq * 100 + D)
+    scale = 1.0 / math.sqrt(D)
+    kv = handle(k, v, table, i32(lens))
+    o, lse = attend(kv, q, scale, causal, window, None if new is None else i32(new))
+    assert status_clear()
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, scale, causal, window, new))
+    again = attend(kv, q, scale, causal, window, None if new is None else i32(new))
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("heads", [5, 10, 20])
+@pytest.mark.parametrize("what", [NAN, math.inf])
+def test_attend_many_rows_hidden_keys_add_nothing(D, heads, what):
+    """As test_attend_hidden_keys_add_nothing, in split lists of 20, 40 and 80 rows."""
+    B, Tq, window = 80, 4, 1000
+    lens = [1300] + [1100] + [9] * (B - 2)
+    inputs = lambda: paged_inputs(B, heads, 1, D, 16, Tq, lens, torch.bfloat16, seed=6)
+    k, v, table, q = inputs()
+    clean = attend(handle(k, v, table, i32(lens)), q, 0.1, True, window)
+    # rows 0..3 of sequence 0 have positions 1296..1299 and see keys from 297, 298, 299 and 300
+    for bad, ok_rows, hit in (((1299, 1298, 20), [0, 1], [3]), ((297, 298, 20), [2, 3], [0])):
+        k, v, table, q = inputs()
+        for j in bad:
+            for pool in (k, v):
+                pool[int(table[0, j // 16]), :, j % 16] = what
+        o, lse = attend(handle(k, v, table, i32(lens)), q, 0.1, True, window)
+        assert status_clear()
+        for r in ok_rows:
+            assert torch.isfinite(o[0, :, r]).all() and torch.isfinite(lse[0, :, r]).all(), (bad, r)
+            # the same keys, in another order where values are no finite numbers: one step of the output's type at most
+            assert (o[0, :, r].float() - clean[0][0, :, r].float()).abs().max() <= 2.0 ** -7 * clean[0][0, :, r].float().abs().max()
+            assert torch.equal(lse[0, :, r], clean[1][0, :, r]), (bad, r)
+        for r in hit:
+            assert not torch.isfinite(o[0, :, r]).any(), (bad, r)
+        assert torch.equal(o[1:], clean[0][1:]) and torch.equal(lse[1:], clean[1][1:])
+
+
+@pytest.mark.parametrize("D,heads", [(64, 40), (96, 70), (128, 20)])
+def test_attend_many_rows_sharp_softmax_and_selected_pages(D, heads):
+    """Scores spread over hundreds, over 600 chosen pages in any order; a bad entry is reported and left out."""
+    lens, n_sel = [17000, 9000], 600
+    g = gen(21)
+    k, v, table, q = paged_inputs(2, heads, 1, D, 32, 1, lens, torch.bfloat16, seed=22, mult=6.0)
+    pages = [-(-n // 32) for n in lens]
+    sel = torch.full((2, 1, n_sel), -1, dtype=torch.int32)
+    counts = [min(n_sel, 500), 200]
+    for b in range(2):
+        sel[b, 0, :counts[b]] = torch.randperm(pages[b], generator=g)[:counts[b]].int()
+    scale = 4.0 / math.sqrt(D)
+    kv = handle(k, v, table, i32(lens))
+    o, lse = attend(kv, q, scale, sel=sel, sel_lens=i32([[c] for c in counts]))
+    assert status_clear()
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, scale, True, 0, None, sel, i32([[c] for c in counts])))
+    sel[1, 0, 7] = pages[1]
+    o2, lse2 = attend(kv, q, scale, sel=sel, sel_lens=i32([[c] for c in counts]))
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 4 and status_clear()
+    assert torch.equal(o2[0], o[0]) and torch.isfinite(o2).all()
+
+
+@pytest.mark.parametrize("case", [(1, 24, 1, 128, 64, 1, [40000]), (2, 80, 1, 64, 16, 1, [20000, 100]), (80, 40, 1, 96, 32, 1, [1100] * 80)],
+                         ids=lambda c: f"B{c[0]}h{c[1]}d{c[3]}")
+def test_many_rows_waits_that_give_up_end_cleanly(case):
+    import time
+    B, Hq, Hkv, D, page, Tq, lens = case
+    k, v, table, q = paged_inputs(B, Hq, Hkv, D, page, Tq, lens, torch.bfloat16, seed=95)
+    kv = handle(k, v, table, i32(lens))
+    want = attend(kv, q, 0.1)
+    torch.cuda.synchronize()
+    fa.fa_set_wait_limit_cycles(8)
+    try:
+        t = time.time()
+        attend(kv, q, 0.1)
+        torch.cuda.synchronize()
+        assert time.time() - t < 2
+        assert fa.fa_device_status() & 1
+    finally:
+        fa.fa_set_wait_limit_cycles(0)
+    o, lse = attend(kv, q, 0.1)
+    assert status_clear()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("case", [(1, 8, 2, 128, 64, 1, [40]), (1, 8, 2, 128, 64, 1, [700]), (2, 6, 2, 64, 16, 3, [1, 300]),
                                   (1, 8, 2, 96, 32, 1, [70000]), (1, 48, 1, 128, 64, 1, [70000]), (1, 8, 2, 256, 64, 1, [40000])],
                          ids=lambda c: f"h{c[1]}x{c[2]}d{c[3]}T{c[5]}n{max(c[6])}")
