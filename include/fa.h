@@ -266,7 +266,8 @@ size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D);
  * Values of keys that no row sees never reach a result, whatever they hold. A
  * key that is visible to one row and hidden from another adds exactly nothing to
  * the latter as well. A NaN in a row's query or in a key that the row sees makes
- * that row's O and LSE NaN.
+ * that row's O and LSE NaN; an infinite value of V that it sees makes O infinite or
+ * NaN there.
  *   workspace  fa_paged_workspace_size bytes, 16-byte aligned; contents
  *     undefined before and after. Calls that may overlap need one each.
  * The result does not depend on what else runs and is the same on every run.

@@ -848,6 +848,33 @@ def test_two_streams_with_a_workspace_each():
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
 
 
+def test_many_rows_on_two_streams_beside_the_forward():
+    """Kernels that allocate tensor memory, from three streams at once."""
+    lens = [9000, 17000]
+    a = paged_inputs(2, 40, 1, 128, 64, 1, lens, torch.bfloat16, seed=63)
+    b = paged_inputs(2, 20, 1, 64, 16, 5, lens, torch.float16, seed=64)
+    ka, kb = handle(a[0], a[1], a[2], i32(lens)), handle(b[0], b[1], b[2], i32(lens))
+    qkv = [randn(gen(65 + i), 1, 8, 1024, 64, dtype=torch.bfloat16).cuda() for i in range(3)]
+
+    def forward():
+        o, lse = torch.empty_like(qkv[0]), torch.empty(1, 8, 1024, device="cuda")
+        fa.fa_fwd(*qkv, o, lse, 0.125, causal=True)
+        return o, lse
+
+    calls = [lambda: attend(ka, a[3], 0.09), lambda: attend(kb, b[3], 0.125), forward]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in calls], [[] for _ in calls]
+    for _ in range(20):
+        for st, call, out in zip(streams, calls, got):
+            with torch.cuda.stream(st):
+                out.append(call())
+    assert status_clear()
+    for w, out in zip(want, got):
+        for o, lse in out:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
 def test_an_explicit_stream_is_used():
     lens = [500]
     k, v, table, q = paged_inputs(1, 4, 2, 64, 16, 1, lens, torch.float16, seed=62)
@@ -972,6 +999,40 @@ assert fa.fa_device_status() == 0
 assert sel.tolist() == [[[0, 1, 6]] * 2] and n.tolist() == [[3, 3]], sel
 assert abs(float(lse[0, 0, 0]) - 3.5835) < 1e-3, lse  # ln 36: two whole pages and four keys of the last
 assert float(o[0, 0, 0, 0]) > 0
+print("fine")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("B,Hq,D,page,pages", [(1, 4, 64, 16, 64), (80, 20, 64, 16, 70), (80, 20, 128, 64, 20), (1, 8, 128, 256, 90)],
+                         ids=["clusters", "many_rows64", "many_rows128", "split"])
+def test_first_attention_of_a_process_inside_a_capture(B, Hq, D, page, pages):
+    """The same for every way the attention is launched; the graph then runs at other lengths."""
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import math, torch, attention_fa_fwd_03_gb300 as fa
+B, Hq, D, page, pages = {B}, {Hq}, {D}, {page}, {pages}
+dev = "cuda"
+z = lambda *s, dt=torch.float16: torch.zeros(s, dtype=dt, device=dev)
+lens = torch.full((B,), page * pages, dtype=torch.int32, device=dev)
+kv = fa.PagedKV(z(pages, 1, page, D), z(pages, 1, page, D) + 2, torch.arange(pages, dtype=torch.int32, device=dev).repeat(B, 1), lens)
+q, o, lse = z(B, Hq, 1, D), z(B, Hq, 1, D), z(B, Hq, 1, dt=torch.float32)
+ws = z(fa.fa_paged_workspace_size(Hq, 1, 1, D), dt=torch.uint8)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    fa.fa_paged_fwd(kv, q, o, lse, 0.1, causal=True, workspace=ws)
+for n in (page * pages, 7, page * pages - 3):
+    lens.fill_(n)
+    o.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    assert (o == 2).all() and (lse - math.log(n)).abs().max() < 1e-5, (n, o, lse)
 print("fine")
 """
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
