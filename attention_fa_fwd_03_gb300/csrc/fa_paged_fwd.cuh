@@ -28,8 +28,8 @@
 // from the tile), query rows its 8 columns, so a group of up to 8 heads fills a
 // fragment that would be half empty the other way round.
 //
-// Split lists of more than 16 rows per KV head (D up to 128) go to the kernel of
-// fa_paged_tc.cuh, whose products are on tcgen05.
+// Split lists of more than 16 rows per KV head go to the kernel of fa_paged_tc.cuh,
+// whose products are on tcgen05.
 //
 // Measured, share of the copy rate (6787 GB/s): up to 8 rows 95% (D 64, 96, 128; B1
 // 131072 keys of 8 KV heads, 537 MB, 84-87 us), 90% (D 256); 16 rows 84-86%. There the
@@ -1260,8 +1260,8 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   while (tiles > 2 && ranks < kPagedMaxRanks && ranks < tiles) ranks *= 2;  // 2 tiles: 5.7 us in one CTA, 6.6 in two
   while (ranks > 1 && units > resident_clusters<C>(ranks)) ranks /= 2;
   if (tiles <= C::CLUSTER_TILES * ranks) return launch_paged<C>(a, p, units * ranks, ranks);
-  if constexpr (D < 256 && RW > 1) {  // more than 16 rows
-    switch (paged_split_rows(p.rows, D)) {
+  if constexpr (RW > 1) {  // more than 16 rows
+    switch (paged_split_rows(p.rows)) {
       case 32: return run_split_tc<D, 1, BF16>(a, p, tiles);
       case 64: return run_split_tc<D, 2, BF16>(a, p, tiles);
       default: return run_split_tc<D, 4, BF16>(a, p, tiles);

@@ -65,12 +65,12 @@ inline int paged_block_rows(int rows, int D) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : rows <= 48 ? 48 : 64;
 }
 // The same where the list is split: above 16 rows by tcgen05, up to 128.
-inline int paged_split_rows(int rows, int D) {
-  return rows <= 16 || D == 256 ? paged_block_rows(rows, D) : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+inline int paged_split_rows(int rows) {
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
 // CTAs of a split list at most: they leave parts of units to be joined.
-__host__ __device__ constexpr int paged_max_parts(int block_rows) { return block_rows <= 16 ? 608 : 304; }
+__host__ __device__ constexpr int paged_max_parts(int block_rows) { return block_rows <= 16 ? 608 : 192; }
 
 // Keys of a tile, and the most tiles a call may have (32-bit counts on the device).
 constexpr int kPagedTile = 64;
@@ -79,7 +79,7 @@ inline int64_t paged_tiles(int64_t units, int64_t keys) { return units * ((keys 
 // Device workspace of launch_paged_fwd_d* in bytes: per CTA two parts of a
 // block (fp32 rows, maximum and sum) and a record of what is to be joined.
 inline size_t paged_fwd_workspace(int rows, int D) {
-  const int block = paged_split_rows(rows, D), parts = paged_max_parts(block);
+  const int block = paged_split_rows(rows), parts = paged_max_parts(block);
   const size_t bytes = static_cast<size_t>(2 * parts) * block * (D * 4 + 8) + parts * 8;
   return (bytes + 255) / 256 * 256;
 }

@@ -16,8 +16,8 @@
 // copy does not take has P = 0, written once: the columns of the other copies are
 // never touched.
 //
-// Roles: two warpgroups of softmax (thread = TMEM lane = row), which take tiles in
-// turn, each with its own buffers, maxima, sums and accumulator: a tile is a chain of
+// Roles: two warpgroups of softmax (D 256: one; thread = TMEM lane = row), which take
+// tiles in turn, each with its own buffers, maxima, sums and accumulator: a tile is a chain of
 // waits and TMEM round trips of over 1100 cycles, more than its bytes take. One or two
 // warps look pages up and load by TMA (one takes 1000 cycles a tile and more). One
 // warp issues S(t) = Q K(t)^T; the softmax reads
@@ -46,12 +46,16 @@ struct PagedTcCfg {
   static constexpr int KEYS = kPagedTile / COPIES;  // of a tile that a copy takes
   // (128 rows, where the softmax bounds the kernel: 68.8 us with one producer, 75.2
   // with two; 64 rows D = 64 in pages of 16: 92.9 and 72.5)
-  static constexpr int PRODUCERS = RG == 4 ? 1 : 2;
-  static constexpr int SOFT = 256, THREADS = SOFT + 32 * PRODUCERS + 64, SCORE_WARP = 8 + PRODUCERS;
+  static constexpr int PRODUCERS = RG == 4 || D == 256 ? 1 : 2;
+  // D = 256: one accumulator is all that TMEM holds beside the scores and weights, and a
+  // tile's bytes take longer than the softmax's chain
+  static constexpr int WGS = D == 256 ? 1 : 2;
+  static constexpr int SOFT = 128 * WGS, THREADS = SOFT + 32 * PRODUCERS + 64, SCORE_WARP = 4 * WGS + PRODUCERS;
   static constexpr int KREG = (D + 63) / 64, REGION = kPagedTile * 128, TILE = KREG * REGION;
   static constexpr int QREGION = 128 * 128;
-  static constexpr int STAGES = D == 64 ? 8 : RG == 2 ? 4 : 5;
-  static constexpr int OP = D + 4;               // row pitch of the merge buffer (floats)
+  static constexpr int STAGES = D == 256 ? 2 : D == 64 ? 8 : RG == 2 ? 4 : 5;
+  static constexpr int MC = D == 256 ? 64 : D;   // columns merged at a time
+  static constexpr int OP = MC + 4;              // row pitch of the merge buffer (floats)
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
   static constexpr int OFF_O = OFF_Q + KREG * QREGION;
@@ -64,7 +68,7 @@ struct PagedTcCfg {
   static constexpr int P_LO = kPagedTile / 2;
   __host__ __device__ static constexpr int O_COL(int b) { return 4 * kPagedTile + KREG * 64 * b; }
   static constexpr uint32_t TMEM_COLS = 512;
-  static_assert(4 * kPagedTile + 2 * KREG * 64 <= 512, "TMEM");
+  static_assert(4 * kPagedTile + WGS * KREG * 64 <= 512, "TMEM");
 };
 
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
@@ -121,7 +125,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       mbar_init(smem_u32(&o_ready[b]), 1);
       mbar_init(smem_u32(&meet[b]), 4);
     }
-    mbar_init(smem_u32(&q_ready), 8);
+    mbar_init(smem_u32(&q_ready), 4 * C::WGS);
     mbar_init(smem_u32(&s_drained), 1);
     mbar_init(smem_u32(&o_drained), 1);
     fence_mbar_init();
@@ -143,12 +147,12 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   const uint32_t tmem = tmem_slot;
   Walk w;
 
-  if (warp >= 8 && warp < 8 + C::PRODUCERS) {
+  if (warp >= 4 * C::WGS && warp < C::SCORE_WARP) {
     // ----------------------------------------------------------- producer warps
-    TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag, warp - 8);
+    TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag, warp - 4 * C::WGS);
     produce_share(p, share, w, ring);
     ring.drain();
-  } else if (warp >= 8) {
+  } else if (warp >= C::SCORE_WARP) {
     // -------------------------------------------------------------- MMA issuers
     // (all lanes compute the descriptors and one issues)
     const bool leader = elect_one_sync(), scores = warp == C::SCORE_WARP;
@@ -193,8 +197,8 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           for (int kk = 0; kk < kPagedTile / 16; ++kk) {
             const uint64_t vd = make_sdesc(kv + C::TILE + kk * 16 * 128, C::REGION, 1024, 2);
             const uint32_t pc = tmem + C::P_COL(b) + kk * 8;
-            if (leader) mma_ts(tmem + C::O_COL(b), pc, vd, idesc_o, 1);
-            if (leader) mma_ts(tmem + C::O_COL(b), pc + C::P_LO, vd, idesc_o, 1);
+            if (leader) mma_ts(tmem + C::O_COL(C::WGS > 1 ? b : 0), pc, vd, idesc_o, 1);
+            if (leader) mma_ts(tmem + C::O_COL(C::WGS > 1 ? b : 0), pc + C::P_LO, vd, idesc_o, 1);
           }
           if (leader) mma_commit(smem_u32(&o_ready[b]));
           if (leader) mma_commit(smem_u32(&empty[slot]));
@@ -207,7 +211,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     mbar_wait(smem_u32(&drained), 0, p.wc.drain_cycles, nullptr, p.wc.status);
   } else {
     // ------------------------------------------------------------------ softmax
-    const int tid = threadIdx.x, b = warp >> 2, quarter = warp & 3;  // warpgroup b: tiles and buffers of parity b
+    const int tid = threadIdx.x, wg = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const int copy = quarter / C::RG, row = tid % C::ROWS;
     float* om = reinterpret_cast<float*>(smem + C::OFF_O);
@@ -216,15 +220,16 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     if (tid == 0 && !p.by_unit) p.joins[part] = make_int2(-1, 0);
     {  // P = 0 where this warp's copy takes no keys
       const uint32_t zero[32] = {};
-      for (int col = 0; col < kPagedTile; col += 32) tmem_store(lanes + C::P_COL(b) + col, zero);
+      for (int b = wg; b < 2; b += C::WGS)
+        for (int col = 0; col < kPagedTile; col += 32) tmem_store(lanes + C::P_COL(b) + col, zero);
     }
     int begin = 0, meets = 0;  // tiles of the segments before
     bool ok = true;
     // all four warps of the warpgroup are here (bounded: a warp that gave up does not come)
     auto meet_warps = [&] {
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&meet[b]));
-      ok = ok && mbar_wait(smem_u32(&meet[b]), meets & 1, tmo, &abort_flag, p.wc.status);
+      if (lane == 0) mbar_arrive(smem_u32(&meet[wg]));
+      ok = ok && mbar_wait(smem_u32(&meet[wg]), meets & 1, tmo, &abort_flag, p.wc.status);
       ok = __all_sync(0xffffffffu, ok);
       ++meets;
     };
@@ -250,25 +255,25 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       {
         const uint32_t zero[32] = {};
 #pragma unroll
-        for (int col = 0; col < D; col += 32) tmem_store(lanes + C::O_COL(b) + col, zero);
+        for (int col = 0; col < D; col += 32) tmem_store(lanes + C::O_COL(wg) + col, zero);
       }
       float m = kNoMax, l = 0.f;
       const int end = begin + w.t1 - w.t0;
-      // products of this warpgroup's tile before gi are done (before the segment: waited
-      // for at the end of the last one)
-      auto wait_o = [&](int gi) {
-        ok = ok && mbar_wait(smem_u32(&o_ready[b]), ((gi - 2) >> 1) & 1, tmo, &abort_flag, p.wc.status);
+      // the products of tile t (of segments before: waited for at their ends)
+      auto wait_products = [&](int t) {
+        if (t < begin) return;
+        ok = ok && mbar_wait(smem_u32(&o_ready[t & 1]), (t >> 1) & 1, tmo, &abort_flag, p.wc.status);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) tc_fence_after();
       };
-      for (int gi = begin + ((begin ^ b) & 1); gi < end; gi += 2) {
-        const int slot = gi % C::STAGES;
+      for (int gi = begin + (C::WGS > 1 ? (begin ^ wg) & 1 : 0); gi < end; gi += C::WGS) {
+        const int slot = gi % C::STAGES, b = gi & 1;
         // a wait that finds its phase complete still takes a hundred cycles and more: all
         // three are tried at once
         const uint32_t bar_kv = smem_u32(&full[slot]), bar_s = smem_u32(&s_full[b]);
         const bool there = mbar_test_wait(bar_kv, (gi / C::STAGES) & 1), scored = mbar_test_wait(bar_s, (gi >> 1) & 1);
         const bool added = gi - 2 < begin || mbar_test_wait(smem_u32(&o_ready[b]), ((gi - 2) >> 1) & 1);
-        const bool o_idle = __all_sync(0xffffffffu, added);
+        const bool p_idle = __all_sync(0xffffffffu, added);
         if (!__all_sync(0xffffffffu, there && scored)) {
           ok = ok && mbar_wait(bar_kv, (gi / C::STAGES) & 1, tmo, &abort_flag, p.wc.status) &&
                mbar_wait(bar_s, (gi >> 1) & 1, tmo, &abort_flag, p.wc.status);
@@ -335,19 +340,21 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           lo[e] = pack2<C::BF16>(p0 - f.x, p1 - f.y);
         }
         l += sum[0] + sum[1];
-        if (!o_idle) wait_o(gi);  // the products that read the last P, and added to O
+        if (!p_idle) wait_products(gi - 2);  // they read this buffer's last P
         if (!ok) break;
         tmem_store(lanes + C::P_COL(b) + copy * (C::KEYS / 2), hi);
         tmem_store(lanes + C::P_COL(b) + C::P_LO + copy * (C::KEYS / 2), lo);
-        if (gi - 2 >= begin && __any_sync(0xffffffffu, grow)) {
+        if (gi - C::WGS >= begin && __any_sync(0xffffffffu, grow)) {
+          if (C::WGS == 1) wait_products(gi - 1);  // they add to O
+          if (!ok) break;
 #pragma unroll 1
           for (int col = 0; col < D; col += 32) {
             uint32_t o[32];
-            tmem_load(lanes + C::O_COL(b) + col, o);
+            tmem_load(lanes + C::O_COL(wg) + col, o);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_store(lanes + C::O_COL(b) + col, o);
+            tmem_store(lanes + C::O_COL(wg) + col, o);
           }
         }
         if (!all_seen) {
@@ -376,12 +383,14 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                      not_finite2<C::BF16>(x.w);
             }
             odd = __any_sync(0xffffffffu, odd != 0);
-            int* flags = odd_flags[b][meets & 1];
+            int* flags = odd_flags[wg][meets & 1];
             if (lane == 0) flags[quarter] = static_cast<int>(odd);
             meet_warps();
             if (!ok) break;
             apart = (flags[0] | flags[1] | flags[2] | flags[3]) != 0;
             if (apart) {
+              if (C::WGS == 1) wait_products(gi - 1);
+              if (!ok) break;
               tmem_st_wait();
               for (int e = 0; e < C::KEYS; ++e) {
                 const int key = copy * C::KEYS + e, j = key_pos[slot][key >> 4] + (key & 15);
@@ -393,7 +402,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
 #pragma unroll 1
                 for (int col = 0; col < D; col += 32) {
                   uint32_t o[32];
-                  tmem_load(lanes + C::O_COL(b) + col, o);
+                  tmem_load(lanes + C::O_COL(wg) + col, o);
                   tmem_ld_wait();
 #pragma unroll
                   for (int i = 0; i < 32; i += 2) {
@@ -405,7 +414,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                       o[i + 1] = __float_as_uint(fmaf(x, v.y, __uint_as_float(o[i + 1])));
                     }
                   }
-                  tmem_store(lanes + C::O_COL(b) + col, o);
+                  tmem_store(lanes + C::O_COL(wg) + col, o);
                   tmem_st_wait();
                 }
               }
@@ -445,16 +454,16 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       const int part_slot = 2 * part + (begins ? 1 : 0);
       mls[tid] = make_float2(m, l);  // [warpgroup][copy][row]
       sync_rows();
-      const float2 ml0 = mls[tid & 127], ml1 = mls[128 + (tid & 127)];
+      const float2 ml0 = mls[tid & 127], ml1 = mls[128 * (C::WGS - 1) + (tid & 127)];
       float mt = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 2 * C::COPIES; ++k) mt = fmaxf(mt, mls[k * C::ROWS + row].x);
+      for (int k = 0; k < C::WGS * C::COPIES; ++k) mt = fmaxf(mt, mls[k * C::ROWS + row].x);
       const float f0 = exp2_rel(ml0.x, mt), f1 = exp2_rel(ml1.x, mt);
-      // columns [16 i, 16 i + 16) of this lane's row over both warpgroups
+      // columns [16 i, 16 i + 16) of this lane's row over the warpgroups
       auto sum16 = [&](int i, float4 (&x)[4]) {
         uint32_t o0[16], o1[16];
         tmem_load(lanes + C::O_COL(0) + 16 * i, o0);
-        tmem_load(lanes + C::O_COL(1) + 16 * i, o1);
+        if constexpr (C::WGS > 1) tmem_load(lanes + C::O_COL(1) + 16 * i, o1);
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -464,22 +473,22 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                                __uint_as_float(o[4 * k + 3]));
           };
           if (ml0.x > -INFINITY) add4(x[k], four(o0), f0);  // nothing seen: not even 0 * inf
-          if (ml1.x > -INFINITY) add4(x[k], four(o1), f1);
+          if (C::WGS > 1 && ml1.x > -INFINITY) add4(x[k], four(o1), f1);
         }
         __syncwarp();
       };
       auto row_sum = [&](int r) {
         float2 ml = make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int k = 0; k < 2 * C::COPIES; ++k) ml.x = fmaxf(ml.x, mls[k * C::ROWS + r].x);
+        for (int k = 0; k < C::WGS * C::COPIES; ++k) ml.x = fmaxf(ml.x, mls[k * C::ROWS + r].x);
 #pragma unroll
-        for (int k = 0; k < 2 * C::COPIES; ++k) ml.y += mls[k * C::ROWS + r].y * exp2_rel(mls[k * C::ROWS + r].x, ml.x);
+        for (int k = 0; k < C::WGS * C::COPIES; ++k) ml.y += mls[k * C::ROWS + r].y * exp2_rel(mls[k * C::ROWS + r].x, ml.x);
         return ml;
       };
       if constexpr (C::COPIES == 1) {
         const float2 ml = row_sum(row);
 #pragma unroll 1
-        for (int i = b; i < D / 16; i += 2) {
+        for (int i = wg; i < D / 16; i += C::WGS) {
           float4 x[4];
           sum16(i, x);
           if (row < rows) {
@@ -490,30 +499,34 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         }
       } else {
         // each share of the columns is summed by the copies in turn, half of it by each
-        // warpgroup
-        constexpr int SHARE = (D / 16 + C::COPIES - 1) / C::COPIES;
+        // of two warpgroups
+        constexpr int SHARE = (C::MC / 16 + C::COPIES - 1) / C::COPIES;
 #pragma unroll 1
-        for (int round = 0; round < C::COPIES; ++round) {
-          const int first = (copy + round) % C::COPIES * SHARE;
+        for (int c0 = 0; c0 < D; c0 += C::MC) {
+          if (c0 > 0) sync_rows();  // the columns before are read
 #pragma unroll 1
-          for (int i = first; i < min(first + SHARE, D / 16); ++i) {
-            if ((i & 1) != b) continue;
-            float4 x[4];
-            sum16(i, x);
-            float4* at = reinterpret_cast<float4*>(om + row * C::OP + 16 * i);
+          for (int round = 0; round < C::COPIES; ++round) {
+            const int first = (copy + round) % C::COPIES * SHARE;
+#pragma unroll 1
+            for (int i = first; i < min(first + SHARE, C::MC / 16); ++i) {
+              if (C::WGS > 1 && (i & 1) != wg) continue;
+              float4 x[4];
+              sum16(c0 / 16 + i, x);
+              float4* at = reinterpret_cast<float4*>(om + row * C::OP + 16 * i);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (round > 0) add4(x[k], at[k], 1.f);
-              at[k] = x[k];
+              for (int k = 0; k < 4; ++k) {
+                if (round > 0) add4(x[k], at[k], 1.f);
+                at[k] = x[k];
+              }
             }
+            sync_rows();
           }
-          sync_rows();
-        }
-        for (int i = tid; i < rows * (D / 8); i += C::SOFT) {
-          const int r = i / (D / 8), ch = i - r * (D / 8);
-          const float4 x = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch);
-          const float4 y = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch + 4);
-          put_piece<C>(p, begins && ends, part_slot, row0, r, ch, x, y, row_sum(r));
+          for (int i = tid; i < rows * (C::MC / 8); i += C::SOFT) {
+            const int r = i / (C::MC / 8), ch = i - r * (C::MC / 8);
+            const float4 x = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch);
+            const float4 y = *reinterpret_cast<const float4*>(om + r * C::OP + 8 * ch + 4);
+            put_piece<C>(p, begins && ends, part_slot, row0, r, c0 / 8 + ch, x, y, row_sum(r));
+          }
         }
       }
       tc_fence_before();

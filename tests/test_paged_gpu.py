@@ -271,6 +271,9 @@ MANY_ROWS = [
     (40, 16, 2, 96, 64, 7, [2200, 2, 0, 2100, 65] + [70] * 35, [7, 1, 3, 6, 2] + [4] * 35, True, 70, "bf16"),
     (40, 40, 2, 64, 16, 3, [2200, 2, 0, 2100, 65] + [70] * 35, [3, 1, 3, 0, 2] + [3] * 35, False, 1500, "fp16"),
     (3, 24, 1, 256, 64, 1, [17003, 64, 5000], None, True, 0, "bf16"),
+    (1, 8, 1, 256, 16, 7, [17003], None, True, 3000, "fp16"),
+    (1, 130, 1, 256, 128, 1, [9000], None, True, 0, "bf16"),
+    (40, 20, 2, 256, 32, 4, [1100, 2, 0, 2100, 65] + [70] * 35, [4, 1, 0, 3, 2] + [4] * 35, True, 0, "bf16"),
 ]
 
 
@@ -287,7 +290,7 @@ def test_attend_many_rows_of_long_lists(case):
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
-@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
 @pytest.mark.parametrize("heads", [5, 10, 20])
 @pytest.mark.parametrize("what", [NAN, math.inf])
 def test_attend_many_rows_hidden_keys_add_nothing(D, heads, what):
@@ -315,7 +318,7 @@ def test_attend_many_rows_hidden_keys_add_nothing(D, heads, what):
         assert torch.equal(o[1:], clean[0][1:]) and torch.equal(lse[1:], clean[1][1:])
 
 
-@pytest.mark.parametrize("D,heads", [(64, 40), (96, 70), (128, 20)])
+@pytest.mark.parametrize("D,heads", [(64, 40), (96, 70), (128, 20), (256, 40)])
 def test_attend_many_rows_sharp_softmax_and_selected_pages(D, heads):
     """Scores spread over hundreds, over 600 chosen pages in any order; a bad entry is reported and left out."""
     lens, n_sel = [17000, 9000], 600
@@ -338,7 +341,8 @@ def test_attend_many_rows_sharp_softmax_and_selected_pages(D, heads):
     assert torch.equal(o2[0], o[0]) and torch.isfinite(o2).all()
 
 
-@pytest.mark.parametrize("case", [(1, 24, 1, 128, 64, 1, [40000]), (2, 80, 1, 64, 16, 1, [20000, 100]), (80, 40, 1, 96, 32, 1, [1100] * 80)],
+@pytest.mark.parametrize("case", [(1, 24, 1, 128, 64, 1, [40000]), (2, 80, 1, 64, 16, 1, [20000, 100]), (80, 40, 1, 96, 32, 1, [1100] * 80),
+                                  (1, 70, 1, 256, 64, 1, [20000])],
                          ids=lambda c: f"B{c[0]}h{c[1]}d{c[3]}")
 def test_many_rows_waits_that_give_up_end_cleanly(case):
     import time
