@@ -17,21 +17,24 @@
 // never touched.
 //
 // Roles: two warpgroups of softmax (D 256: one; thread = TMEM lane = row), which take
-// tiles in turn, each with its own buffers, maxima, sums and accumulator: a tile is a chain of
-// waits and TMEM round trips of over 1100 cycles, more than its bytes take. One or two
-// warps look pages up and load by TMA (one takes 1000 cycles a tile and more). One
-// warp issues S(t) = Q K(t)^T; the softmax reads
-// it (then S(t + 2) may overwrite it) and writes P(t) = 2^(S - m) in two words of the
-// cache's type, P_hi + P_lo; another issues O += P_hi V + P_lo V. (One warp for both
-// takes 1500 cycles a tile, in a hundred or more per wait.) O is rescaled in
-// TMEM when a maximum grows by more than 2^8. At the end of a segment both
-// warpgroups read both accumulators, half of the columns each.
+// tiles in turn, each with its own buffers, maxima, sums and accumulator: a tile is a
+// chain of waits and TMEM round trips of over 1100 cycles, more than its bytes take.
+// One or two warps look pages up and load by TMA (one takes 1000 cycles a tile and
+// more). One warp issues S(t) = Q K(t)^T; the softmax reads it (then S(t + 2) may
+// overwrite it) and writes P(t) = 2^(S - m) in two words of the cache's type, P_hi +
+// P_lo; another warp issues O += P_hi V + P_lo V. (One warp for both takes 1500 cycles
+// a tile, a hundred and more in each wait.) O is rescaled in TMEM when a maximum grows
+// by more than 2^8. At the end of a segment both warpgroups read both accumulators,
+// half of the columns each.
 //
 // Measured (269 MB of bf16 keys and values, 16 units, start and join of some 10 us
-// included; warp-level products in brackets): D 128, 32 rows 56 us (64), 64 rows 61
-// (111), 128 rows 69 (190); D 64, 32 rows 60 (80), 64 rows 67 (128), 128 rows 95
-// (233). At D 128 the loads bound it up to 64 rows (537 MB 93 us, 85% of the copy
-// rate), at D 64, with half the bytes per tile, the softmax's chain.
+// included; warp-level products in brackets): D 128, 32 rows 57 us (64), 64 rows 59
+// (111), 128 rows 71 (190); D 64, 32 rows 59 (80), 64 rows 67 (128), 128 rows 95
+// (233); D 256, 32 rows 66 (65), 64 rows 74 (106), 128 rows 90 (190). At D 128 the
+// loads bound it up to 64 rows (537 MB 93 us, 85% of the copy rate), at D 64, with
+// half the bytes per tile, the softmax's chain, at D 256 the two stages that fit.
+// Rings of their own for K and V (D 256 62 us with 32 rows, but D 64 67 and five drafts
+// of short lists 8% slower) add waits and commits where D 64 has no time for them.
 #pragma once
 
 namespace fa {
@@ -53,8 +56,8 @@ struct PagedTcCfg {
   static constexpr int SOFT = 128 * WGS, THREADS = SOFT + 32 * PRODUCERS + 64, SCORE_WARP = 4 * WGS + PRODUCERS;
   static constexpr int KREG = (D + 63) / 64, REGION = kPagedTile * 128, TILE = KREG * REGION;
   static constexpr int QREGION = 128 * 128;
-  static constexpr int STAGES = D == 256 ? 2 : D == 64 ? 8 : RG == 2 ? 4 : 5;
-  static constexpr int MC = D == 256 ? 64 : D;   // columns merged at a time
+  static constexpr int STAGES = D == 256 ? 2 : D == 64 ? 8 : 5;
+  static constexpr int MC = D == 96 ? 48 : 64;   // columns merged at a time (all at once would cost a stage)
   static constexpr int OP = MC + 4;              // row pitch of the merge buffer (floats)
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
