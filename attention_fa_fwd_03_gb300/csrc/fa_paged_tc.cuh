@@ -28,9 +28,9 @@
 // half of the columns each.
 //
 // Measured (269 MB of bf16 keys and values, 16 units, start and join of some 10 us
-// included; warp-level products in brackets): D 128, 32 rows 57 us (64), 64 rows 59
-// (111), 128 rows 71 (190); D 64, 32 rows 59 (80), 64 rows 67 (128), 128 rows 95
-// (233); D 256, 32 rows 66 (65), 64 rows 74 (106), 128 rows 90 (190). At D 128 the
+// included; warp-level products in brackets): D 128, 32 rows 56 us (64), 64 rows 58
+// (111), 128 rows 68 (190); D 64, 32 rows 60 (80), 64 rows 67 (128), 128 rows 95
+// (233); D 256, 32 rows 66 (65), 64 rows 71 (106), 128 rows 84 (190). At D 128 the
 // loads bound it up to 64 rows (537 MB 93 us, 85% of the copy rate), at D 64, with
 // half the bytes per tile, the softmax's chain, at D 256 the two stages that fit.
 // Rings of their own for K and V (D 256 62 us with 32 rows, but D 64 67 and five drafts
@@ -47,8 +47,8 @@ struct PagedTcCfg {
   static constexpr int ROWS = 32 * RG;           // rows of a block
   static constexpr int COPIES = 4 / RG;          // of each row
   static constexpr int KEYS = kPagedTile / COPIES;  // of a tile that a copy takes
-  // (128 rows, where the softmax bounds the kernel: 68.8 us with one producer, 75.2
-  // with two; 64 rows D = 64 in pages of 16: 92.9 and 72.5)
+  // (128 rows, where the softmax bounds the kernel, D 128: 68.8 us with one producer,
+  // 75.2 with two; 64 rows, D 64 in pages of 16: 92.9 and 72.5)
   static constexpr int PRODUCERS = RG == 4 || D == 256 ? 1 : 2;
   // D = 256: one accumulator is all that TMEM holds beside the scores and weights, and a
   // tile's bytes take longer than the softmax's chain
@@ -244,22 +244,30 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       const int p_lo = len - n, p_hi = len - 1;  // positions of the new tokens
       const int tok = (rb * C::ROWS + row) % p.Tq, pos = p_lo + tok;
       // queries, every copy; rows behind the last one zero
-      for (int i = tid; i < C::ROWS * (D / 8); i += C::SOFT) {
-        const int r = i / (D / 8), ch = i - r * (D / 8);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D) + ch);
+      constexpr int CHUNKS = C::ROWS * (D / 8), LOADS = (CHUNKS + C::SOFT - 1) / C::SOFT;
+      uint4 x[LOADS];
 #pragma unroll
-        for (int k = 0; k < C::COPIES; ++k)
-          *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(k * C::ROWS + r, ch & 7)) = x;
+      for (int i = 0; i < LOADS; ++i) {  // all under way at once
+        const int at = tid + i * C::SOFT, r = at / (D / 8);
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (r < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + row0 * D) + at);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&q_ready));
       {
         const uint32_t zero[32] = {};
 #pragma unroll
         for (int col = 0; col < D; col += 32) tmem_store(lanes + C::O_COL(wg) + col, zero);
       }
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int at = tid + i * C::SOFT, r = at / (D / 8), ch = at - r * (D / 8);
+        if (at >= CHUNKS) break;
+#pragma unroll
+        for (int k = 0; k < C::COPIES; ++k)
+          *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(k * C::ROWS + r, ch & 7)) = x[i];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&q_ready));
       float m = kNoMax, l = 0.f;
       const int end = begin + w.t1 - w.t0;
       // the products of tile t (of segments before: waited for at their ends)
