@@ -112,7 +112,7 @@ struct PagedCfg {
   static constexpr int SMEM_BYTES = OFF_PML + (CLUSTER ? ROWS * D : 0) + 1024;
   // clusters: the warps' rows at the end, over the stages and the queries
   static_assert(KW * ROWS * OP * 4 <= OFF_O, "warps' rows");
-  static_assert(SMEM_BYTES <= 231000, "shared memory");  // beside the static variables
+  static_assert(SMEM_BYTES <= 229000, "shared memory");  // beside the static variables
   static_assert(ROWS * (D / 8) % kPagedMaxRanks == 0, "pieces of a cluster");
 };
 
@@ -124,61 +124,73 @@ constexpr float kPagedSlack = 8.f;
 constexpr float kNoMax = -3e38f;
 
 // ----------------------------------------------------------------- the list
-// An item is a sequence (every KV head and row block of it has the same tiles)
-// or, with selected pages, a (sequence, KV head); `mult` units each.
-__device__ __forceinline__ int item_count(const PagedFwdArgs& p) { return p.sel ? p.c.B * p.c.Hkv : p.c.B; }
-__device__ __forceinline__ int item_mult(const PagedFwdArgs& p) {
-  return (p.sel ? 1 : p.c.Hkv) * p.row_blocks;
+__device__ __forceinline__ ListShape list_shape(const PagedFwdArgs& p) {
+  return {p.sel ? p.c.B * p.c.Hkv : p.c.B, (p.sel ? 1 : p.c.Hkv) * p.row_blocks, p.sel != nullptr, p.window,
+          p.c.page_shift};
 }
-
-struct Item {
-  int b;       // sequence
-  int len, n;  // keys and new tokens
-  int first;   // first tile of the list that holds a visible key
-  int tiles;   // tiles of each unit
-};
-__device__ __forceinline__ Item load_item(const PagedFwdArgs& p, int i) {
-  Item it;
-  it.b = p.sel ? i / p.c.Hkv : i;
-  const int listed = p.sel ? __ldg(p.sel_lens + i) : 0;
-  const SeqLens sl = seq_lens(p.c, p.new_lens, it.b, p.Tq);
-  it.len = sl.len;
-  it.n = sl.n;
-  it.first = 0;
-  int keys = it.len;
-  if (p.sel) {
-    keys = checked_count(p.c, listed, p.n_sel) << p.c.page_shift;  // at most 2^20 entries of 2^8 keys
-  } else if (p.window > 0) {
-    it.first = max(0, it.len - it.n - p.window + 1) / kPagedTile;
-  }
-  it.tiles = it.n > 0 ? (keys + kPagedTile - 1) / kPagedTile - it.first : 0;
-  return it;
+__device__ __forceinline__ int item_seq(const PagedFwdArgs& p, int item) { return p.sel ? item / p.c.Hkv : item; }
+__device__ __forceinline__ ItemLens load_lens(const PagedFwdArgs& p, int item) {
+  const int listed = p.sel ? __ldg(p.sel_lens + item) : 0;
+  const SeqLens sl = seq_lens(p.c, p.new_lens, item_seq(p, item), p.Tq);
+  return ItemLens::of(sl.len, sl.n, p.sel ? checked_count(p.c, listed, p.n_sel) : 0);
 }
+// Clusters: a warp's own reading of its unit's lengths, one value for all its lanes.
+// Warps differ only if somebody writes the lengths under the call. They then wait for
+// tiles that never come, up to the time limit, and no longer: barriers without one are
+// met the same number of times whatever the lengths are.
+__device__ __forceinline__ ItemLens load_lens_warp(const PagedFwdArgs& p, int item) {
+  ItemLens x = load_lens(p, item);
+  x.len = __shfl_sync(0xffffffffu, x.len, 0);
+  x.rest = __shfl_sync(0xffffffffu, x.rest, 0);
+  return x;
+}
+__device__ __forceinline__ int kv_head(const PagedFwdArgs& p, const Walk& w) {
+  return p.sel ? w.item % p.c.Hkv : w.sub / p.row_blocks;
+}
+__device__ __forceinline__ int row_block(const PagedFwdArgs& p, const Walk& w) { return w.sub % p.row_blocks; }
 
-// One CTA's share of the list, found by all its threads: `total` tiles in equal
-// runs, the first total % parts of them one longer. (The host has checked that the
-// longest possible list stays below 2^31 tiles.)
-struct Share {
-  int parts;      // CTAs with a share: every one of them has a tile
-  int base, more; // tiles of a share, and how many have one more
-  int lo, hi;
-  int item, rest; // where lo falls: item, and tiles of it before lo
-  // CTA whose share holds tile x of the list
-  __device__ __forceinline__ int part_of(int x) const {
-    const int longer = more * (base + 1);
-    return x < longer ? x / (base + 1) : more + (x - longer) / base;
-  }
-};
+// The CTA's copy of items' lengths, in shared memory: items [base, base + kItemWindow).
+// Every warp of the CTA has one of these and walks the whole share with it, so all
+// come to the barriers of a window that moves on.
 template <int THREADS>
-__device__ __forceinline__ Share find_share(const PagedFwdArgs& p, int part, int parts) {
+struct ItemWindow {
+  const PagedFwdArgs& p;
+  ItemLens* slots;
+  int items, base;
+  // by all threads, with a barrier behind it
+  __device__ __forceinline__ void fill(int from) {
+    base = from;
+    const int i = threadIdx.x;
+    if (i < kItemWindow && base + i < items) slots[i] = load_lens(p, base + i);
+  }
+  __device__ __forceinline__ ItemLens operator()(int item) {
+    if (item - base >= kItemWindow) {
+      __syncwarp();
+      named_bar_sync(2, THREADS);  // all have read what they need of the old window
+      fill(item);
+      named_bar_sync(2, THREADS);
+    }
+    return slots[item - base];
+  }
+};
+
+// A CTA's share, found by all its threads, which also fill the window for its walk.
+template <int THREADS>
+__device__ __forceinline__ Share find_share(const PagedFwdArgs& p, const ListShape& list, int part, int parts,
+                                            ItemWindow<THREADS>& window) {
+  static_assert(THREADS >= kItemWindow, "one item per thread");
   __shared__ int sums[THREADS / 32];
   __shared__ int found_rest, found_item;
-  const int items = item_count(p), mult = item_mult(p);
-  const int per = (items + THREADS - 1) / THREADS;
-  const int i0 = min(items, static_cast<int>(threadIdx.x) * per), i1 = min(items, i0 + per);
+  const int per = (list.items + THREADS - 1) / THREADS;
+  const int i0 = min(list.items, static_cast<int>(threadIdx.x) * per), i1 = min(list.items, i0 + per);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool whole = list.items <= kItemWindow;  // the window holds the list: one item per thread
   int mine = 0;
-  for (int i = i0; i < i1; ++i) mine += load_item(p, i).tiles * mult;
+  for (int i = i0; i < i1; ++i) {
+    const ItemLens x = load_lens(p, i);
+    if (whole) window.slots[i] = x;
+    mine += make_item(list, x).tiles * list.mult;
+  }
   int incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -186,6 +198,7 @@ __device__ __forceinline__ Share find_share(const PagedFwdArgs& p, int part, int
     if (lane >= off) incl += x;
   }
   if (lane == 31) sums[warp] = incl;
+  if (threadIdx.x == 0) found_item = found_rest = 0;
   __syncthreads();
   int before = incl - mine, total = 0;
 #pragma unroll
@@ -194,16 +207,12 @@ __device__ __forceinline__ Share find_share(const PagedFwdArgs& p, int part, int
     total += sums[w];
   }
   Share s;
-  s.parts = min(total, parts);
-  s.base = total / parts;
-  s.more = total - s.base * parts;
-  s.lo = part * s.base + min(part, s.more);
-  s.hi = s.lo + s.base + (part < s.more ? 1 : 0);
+  s.divide(total, part, parts);
   if (s.lo >= before && s.lo < before + mine) {
     int rest = s.lo - before;
     int i = i0;
     for (; i < i1 - 1; ++i) {
-      const int n = load_item(p, i).tiles * mult;
+      const int n = make_item(list, load_lens(p, i)).tiles * list.mult;
       if (rest < n) break;
       rest -= n;
     }
@@ -213,60 +222,12 @@ __device__ __forceinline__ Share find_share(const PagedFwdArgs& p, int part, int
   __syncthreads();
   s.item = found_item;
   s.rest = found_rest;
+  if (!whole) {
+    window.fill(s.item);
+    __syncthreads();
+  }
   return s;
 }
-
-// Walks the segments of a share: unit (item, sub), its tiles [t0, t1).
-struct Walk {
-  Item it;
-  int item, sub, mult, items;
-  int t0, t1, left;
-  __device__ __forceinline__ bool start(const PagedFwdArgs& p, const Share& s) {
-    left = s.hi - s.lo;
-    if (left <= 0) return false;
-    mult = item_mult(p);
-    items = item_count(p);
-    item = s.item;
-    it = load_item(p, item);
-    // tiles and sub are in range unless the lengths change under the call,
-    // which must not lead out of the buffers either
-    const int tiles = max(it.tiles, 1);
-    sub = min(s.rest / tiles, mult - 1);
-    t0 = min(s.rest - sub * tiles, tiles - 1);
-    t1 = min(it.tiles, t0 + left);
-    return true;
-  }
-  // Clusters: unit `unit` as one segment, of whose tiles rank `rank` takes every
-  // `ranks`-th, a power of two, from its own number on: [t0, t1) counts them.
-  __device__ __forceinline__ void start_unit(const PagedFwdArgs& p, int unit, int rank, int ranks) {
-    mult = item_mult(p);
-    items = item_count(p);
-    item = unit / mult;
-    sub = unit - item * mult;
-    it = load_item(p, item);
-    t0 = 0;
-    t1 = (max(it.tiles - rank, 0) + ranks - 1) >> (31 - __clz(ranks));
-    left = t1;
-  }
-  __device__ __forceinline__ bool next(const PagedFwdArgs& p) {
-    left -= t1 - t0;
-    if (left <= 0) return false;
-    if (++sub == mult) {
-      sub = 0;
-      do {
-        if (++item >= items) return false;  // the lengths changed under the call: stay inside the list
-        it = load_item(p, item);
-      } while (it.tiles == 0);
-    }
-    t0 = 0;
-    t1 = min(it.tiles, left);
-    return true;
-  }
-  __device__ __forceinline__ int kv_head(const PagedFwdArgs& p) const {
-    return p.sel ? item % p.c.Hkv : sub / p.row_blocks;
-  }
-  __device__ __forceinline__ int row_block(const PagedFwdArgs& p) const { return sub % p.row_blocks; }
-};
 
 // Row 0 of block `rb` of (b, g) among the rows of q, o and lse.
 __device__ __forceinline__ int64_t block_row0(const PagedFwdArgs& p, int b, int g, int rb, int block_rows) {
@@ -328,10 +289,11 @@ __device__ __forceinline__ void put_piece(const PagedFwdArgs& p, bool whole, int
 }
 
 // By one thread after a segment: whether the unit it began is split, and over which parts.
-__device__ __forceinline__ void record_unit(const PagedFwdArgs& p, const Share& share, const Walk& w, int part) {
+__device__ __forceinline__ void record_unit(const PagedFwdArgs& p, const ListShape& list, const Share& share,
+                                            const Walk& w, int part) {
   const bool ends = w.t1 == w.it.tiles;
   if (w.t0 != 0 || (ends && !p.by_unit)) return;
-  const int unit = w.item * w.mult + w.sub;
+  const int unit = w.item * list.mult + w.sub;
   // the unit goes on to tile share.hi - t1 + tiles of the list
   const int last = ends ? 0 : min(share.part_of(share.hi - w.t1 + w.it.tiles - 1), share.parts - 1);
   p.joins[p.by_unit ? unit : part] = make_int2(ends ? -1 : unit, part | last << 16);
@@ -339,15 +301,14 @@ __device__ __forceinline__ void record_unit(const PagedFwdArgs& p, const Share& 
 
 // Units without tiles: nothing is visible to any of their rows.
 template <class C>
-__device__ __forceinline__ void write_empty_units(const PagedFwdArgs& p, int part, int parts, int tid, int threads) {
-  const int mult = item_mult(p);
-  const int64_t units = static_cast<int64_t>(item_count(p)) * mult;
+__device__ __forceinline__ void write_empty_units(const PagedFwdArgs& p, const ListShape& list, int part, int parts, int tid,
+                                                  int threads) {
+  const int64_t units = static_cast<int64_t>(list.items) * list.mult;
   for (int64_t u = part; u < units; u += parts) {
-    const int item = static_cast<int>(u / mult), sub = static_cast<int>(u - static_cast<int64_t>(item) * mult);
-    const Item it = load_item(p, item);
-    if (it.tiles > 0) continue;
+    const int item = static_cast<int>(u / list.mult), sub = static_cast<int>(u - static_cast<int64_t>(item) * list.mult);
+    if (make_item(list, load_lens(p, item)).tiles > 0) continue;
     const int g = p.sel ? item % p.c.Hkv : sub / p.row_blocks, rb = sub % p.row_blocks;
-    const int64_t row0 = block_row0(p, it.b, g, rb, C::ROWS);
+    const int64_t row0 = block_row0(p, item_seq(p, item), g, rb, C::ROWS);
     const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
     for (int i = tid; i < rows * (C::D / 8); i += threads)
       reinterpret_cast<uint4*>(p.o + row0 * C::D)[i] = make_uint4(0, 0, 0, 0);
@@ -459,17 +420,20 @@ struct TileRing {
   }
 };
 
-// All tiles of a share, by the producer warp.
+// All tiles of a share, by the producer warp. (A wait that gave up ends the loads, not
+// the walk: the window moves on with every warp.)
 template <class C>
-__device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const Share& share, Walk& w, TileRing<C>& ring) {
+__device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListShape& list, const Share& share,
+                                              ItemWindow<C::THREADS>& window, TileRing<C>& ring) {
   const PagedView& c = p.c;
   const int lane = ring.lane;
-  for (bool more = w.start(p, share); more && ring.ok; more = w.next(p)) {
-    const int g = w.kv_head(p);
+  Walk w;
+  for (bool more = w.start(list, share, window); more; more = w.next(list, window)) {
+    if (!ring.ok) continue;
+    const int b = item_seq(p, w.item), g = kv_head(p, w);
     const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
-    const int64_t u = static_cast<int64_t>(w.it.b) * c.Hkv + g;
-    const int list = p.sel ? (w.it.tiles * kPagedTile) >> c.page_shift : pages;  // entries that tiles reach
-    const int count = p.sel ? min(list, max(0, min(p.n_sel, __ldg(p.sel_lens + u)))) : pages;
+    const int64_t u = static_cast<int64_t>(b) * c.Hkv + g;
+    const int count = p.sel ? w.it.listed : pages;
     // pages of list entries [e0, e0 + 32) and the next 32, one per lane
     auto look_up = [&](int e, int* page, int* id) {
       *page = -1;
@@ -484,7 +448,7 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const Share
         }
       }
       *page = pg;
-      *id = pool_page(c, w.it.b, pg);
+      *id = pool_page(c, b, pg);
     };
     int e0 = ((w.it.first + w.t0) * kPagedTile) >> c.page_shift;
     int page0, id0, page1, id1;
@@ -515,12 +479,14 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES];
   __shared__ int key_pos[C::STAGES][C::KW];  // position of the first of each warp's 16 keys
+  __shared__ ItemLens item_lens[C::CLUSTER ? 1 : kItemWindow];
   __shared__ int abort_flag;
   constexpr int D = C::D;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedView& c = p.c;
+  const ListShape list = list_shape(p);
   const int part = blockIdx.x, parts = gridDim.x;
   const uint64_t tmo = p.wc.timeout_cycles;
   if (threadIdx.x == 0) {
@@ -542,11 +508,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   prefetch_inputs<C>(p, part);
   const int rank = C::CLUSTER ? part % ranks : 0, unit = C::CLUSTER ? part / ranks : 0;
   Share share;
+  ItemWindow<C::THREADS> window{p, item_lens, list.items, 0};
   if constexpr (C::CLUSTER)
     __syncthreads();
   else
-    share = find_share<C::THREADS>(p, part, parts);  // barriers inside
-  Walk w;
+    share = find_share<C::THREADS>(p, list, part, parts, window);  // barriers inside
 
   if (warp >= C::WARPS) {
     // ---------------------------------------------------------- producer warp
@@ -567,9 +533,9 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       // the CTA's tiles as 32 lanes hold, the first batch, where no window moves the
       // first tile, while the lengths that say which of it counts are still on their
       // way: what is read too much is not used.
-      const int mult = item_mult(p), item = unit / mult;
-      const int b = p.sel ? item / c.Hkv : item;
-      const int g = p.sel ? item % c.Hkv : (unit - item * mult) / p.row_blocks;
+      Walk w;
+      w.place_unit(list, unit);
+      const int b = item_seq(p, w.item), g = kv_head(p, w);
       const int64_t u = static_cast<int64_t>(b) * c.Hkv + g;
       const int64_t row = static_cast<int64_t>(b) * c.max_pages;
       const int batch = 32 / pieces, mine = lane / pieces, key = (lane & (pieces - 1)) * piece;
@@ -583,10 +549,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       };
       const bool early = p.sel != nullptr || p.window == 0;
       if (early) read(0);
-      w.start_unit(p, unit, rank, ranks);
+      w.start_unit(list, rank, ranks, load_lens_warp(p, w.item));
       first = w.it.first * kPagedTile;
       const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
-      const int count = p.sel ? max(0, min(p.n_sel, __ldg(p.sel_lens + u))) : pages;
+      const int count = p.sel ? w.it.listed : pages;
       for (int t0 = 0; t0 < w.t1 && ring.ok; t0 += batch) {
         if (t0 > 0 || !early) read(t0);
         const bool counts = t0 + mine < w.t1 && e < count;
@@ -603,7 +569,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         }
       }
     } else {
-      produce_share(p, share, w, ring);
+      produce_share(p, list, share, window, ring);
     }
     ring.drain();
     if (C::CLUSTER && ranks > 1) {  // as the consumers do
@@ -644,21 +610,30 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   uint32_t phase = 0;
   bool ok = true;
   bool more = true;  // clusters: one segment, which may be empty
-  if constexpr (C::CLUSTER)
-    w.start_unit(p, unit, rank, ranks);
-  else
-    more = w.start(p, share);
-  for (; more; more = !C::CLUSTER && w.next(p)) {
-    const int g = w.kv_head(p), rb = w.row_block(p);
+  Walk w;
+  if constexpr (C::CLUSTER) {
+    w.place_unit(list, unit);
+    w.start_unit(list, rank, ranks, load_lens_warp(p, w.item));
+  } else {
+    more = w.start(list, share, window);
+  }
+  for (; more; more = !C::CLUSTER && w.next(list, window)) {
+    const int g = kv_head(p, w), rb = row_block(p, w);
     const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
-    const int64_t row0 = block_row0(p, w.it.b, g, rb, C::ROWS);
-    const int len = w.it.len, n = w.it.n;
-    const int p_lo = len - n, p_hi = len - 1;  // positions of the new tokens
-    if constexpr (!C::CLUSTER) stage_queries(row0, rows);
-    sync_rows();
+    const int64_t row0 = block_row0(p, item_seq(p, w.item), g, rb, C::ROWS);
     // this thread's columns are rows 2 (lane % 4) and the next of each group of 8
     const int group0 = rw * C::NT, col0 = group0 * 8 + 2 * (lane & 3);
     const bool has_rows = group0 * 8 < rows;
+    // tokens of this thread's rows, four bits each
+    uint64_t tokens = 0;
+#pragma unroll
+    for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        tokens |= static_cast<uint64_t>((rb * C::ROWS + col0 + 8 * nt + e) % p.Tq) << (8 * nt + 4 * e);
+    auto token = [&](int nt, int e) { return static_cast<int>(tokens >> (8 * nt + 4 * e)) & 15; };
+    if constexpr (!C::CLUSTER) stage_queries(row0, rows);
+    sync_rows();
     // B fragments of the queries: two products' worth per 8 rows and 32 columns
     const uint32_t qs = sbase + C::OFF_Q;
     auto query_frag = [&](uint32_t (&f)[4], int nt, int k2) {
@@ -680,14 +655,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
     }
-    // tokens of this thread's rows, four bits each
-    uint64_t tokens = 0;
-#pragma unroll
-    for (int nt = 0; nt < C::NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        tokens |= static_cast<uint64_t>((rb * C::ROWS + col0 + 8 * nt + e) % p.Tq) << (8 * nt + 4 * e);
-    auto token = [&](int nt, int e) { return static_cast<int>(tokens >> (8 * nt + 4 * e)) & 15; };
+    const int len = w.it.len, n = w.it.n;
+    const int p_lo = len - n, p_hi = len - 1;  // positions of the new tokens
 
     for (int t = w.t0; t < w.t1; ++t) {
       ok = ok && mbar_wait(smem_u32(&full[slot]), phase, tmo, &abort_flag, p.wc.status);
@@ -1005,10 +974,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       const float2 ml = warps_max_sum<C>(mls, r);
       put_piece<C>(p, begins && ends, part_slot, row0, r, ch, x, y, ml);
     }
-    if (tid == 0) record_unit(p, share, w, part);
+    if (tid == 0) record_unit(p, list, share, w, part);
     sync_rows();
   }
-  if constexpr (!C::CLUSTER) write_empty_units<C>(p, part, parts, tid, 32 * C::WARPS);
+  if constexpr (!C::CLUSTER) write_empty_units<C>(p, list, part, parts, tid, 32 * C::WARPS);
 }
 
 }  // namespace fa
@@ -1034,12 +1003,16 @@ fa_paged_join_kernel(const PagedFwdArgs p) {
   constexpr int NV = (D / 4 + 31) / 32, UN = 4;
   __shared__ float4 sm_o[kJoinWarps][D / 4];
   __shared__ float2 sm_ml[kJoinWarps];
+  __shared__ int2 record;
   grid_wait_prior();
   grid_release_next();
-  const int2 join = p.joins[blockIdx.x];
-  if (join.x < 0) return;
-  // (the bounds hold for any record: lengths that change under the call may leave an
-  // old one)
+  // read once, and within bounds whatever it holds: lengths that change under the call
+  // may leave an old record, and a call that shares the workspace its own
+  if (threadIdx.x == 0) record = p.joins[blockIdx.x];
+  __syncthreads();
+  const int2 join = record;
+  const ListShape list = list_shape(p);
+  if (join.x < 0 || join.x >= static_cast<int64_t>(list.items) * list.mult) return;
   const int unit = p.by_unit ? blockIdx.x : join.x;
   const int rb = unit % p.row_blocks, rows = min(ROWS, p.rows - rb * ROWS);
   const int64_t row0 = static_cast<int64_t>(unit / p.row_blocks) * p.rows + rb * ROWS;

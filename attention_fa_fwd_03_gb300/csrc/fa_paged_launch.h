@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "fa_paged.cuh"
+#include "fa_paged_walk.h"
 
 namespace fa {
 
@@ -72,8 +73,7 @@ inline int paged_split_rows(int rows) {
 // CTAs of a split list at most: they leave parts of units to be joined.
 __host__ __device__ constexpr int paged_max_parts(int block_rows) { return block_rows <= 16 ? 608 : 192; }
 
-// Keys of a tile, and the most tiles a call may have (32-bit counts on the device).
-constexpr int kPagedTile = 64;
+// Tiles of a call's list (32-bit counts on the device).
 inline int64_t paged_tiles(int64_t units, int64_t keys) { return units * ((keys + kPagedTile - 1) / kPagedTile); }
 
 // Device workspace of launch_paged_fwd_d* in bytes: per CTA two parts of a

@@ -64,7 +64,7 @@ struct PagedTcCfg {
   static constexpr int OFF_O = OFF_Q + KREG * QREGION;
   static constexpr int OFF_ML = OFF_O + (COPIES > 1 ? ROWS * OP * 4 : 0);  // [warpgroup][copies][rows]
   static constexpr int SMEM_BYTES = OFF_ML + SOFT * 8 + 1024;
-  static_assert(SMEM_BYTES <= 231000, "shared memory");
+  static_assert(SMEM_BYTES <= 229000, "shared memory");
   // TMEM columns
   __host__ __device__ static constexpr int S_COL(int b) { return kPagedTile * b; }
   __host__ __device__ static constexpr int P_COL(int b) { return 2 * kPagedTile + kPagedTile * b; }  // P_hi, then P_lo
@@ -107,6 +107,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       q_ready, s_drained, o_drained, meet[2];
   __shared__ __align__(16) int key_pos[C::STAGES][kPagedKeyWarps];
   __shared__ int odd_flags[2][2][4];
+  __shared__ ItemLens item_lens[kItemWindow];
   __shared__ int abort_flag;
   __shared__ uint32_t tmem_slot;
   constexpr int D = C::D;
@@ -145,15 +146,18 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   grid_release_next();
   prefetch_inputs<C>(p, part);
   tc_fence_before();
-  const Share share = find_share<C::THREADS>(p, part, parts);  // barriers inside
+  const ListShape list = list_shape(p);
+  ItemWindow<C::THREADS> window{p, item_lens, list.items, 0};
+  const Share share = find_share<C::THREADS>(p, list, part, parts, window);  // barriers inside
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  Walk w;
+  // Every warp walks the share to its end, whether or not its waits gave up: the window
+  // moves on with all of them.
 
   if (warp >= 4 * C::WGS && warp < C::SCORE_WARP) {
     // ----------------------------------------------------------- producer warps
     TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag, warp - 4 * C::WGS);
-    produce_share(p, share, w, ring);
+    produce_share(p, list, share, window, ring);
     ring.drain();
   } else if (warp >= C::SCORE_WARP) {
     // -------------------------------------------------------------- MMA issuers
@@ -168,7 +172,9 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       if (ok) tc_fence_after();
     };
     int gi = 0, seg = 0;
-    for (bool more = w.start(p, share); more && ok; more = w.next(p), ++seg) {
+    Walk w;
+    for (bool more = w.start(list, share, window); more; more = w.next(list, window), ++seg) {
+      if (!ok) continue;
       const int first = gi, end = gi + w.t1 - w.t0;
       if (scores) wait(q_ready, seg);
       for (; gi < end && ok; ++gi) {
@@ -236,10 +242,11 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       ok = __all_sync(0xffffffffu, ok);
       ++meets;
     };
-    for (bool more = w.start(p, share); more; more = w.next(p)) {
-      const int g = w.kv_head(p), rb = w.row_block(p);
+    Walk w;
+    for (bool more = w.start(list, share, window); more; more = w.next(list, window)) {
+      const int g = kv_head(p, w), rb = row_block(p, w);
       const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
-      const int64_t row0 = block_row0(p, w.it.b, g, rb, C::ROWS);
+      const int64_t row0 = block_row0(p, item_seq(p, w.item), g, rb, C::ROWS);
       const int len = w.it.len, n = w.it.n;
       const int p_lo = len - n, p_hi = len - 1;  // positions of the new tokens
       const int tok = (rb * C::ROWS + row) % p.Tq, pos = p_lo + tok;
@@ -543,9 +550,9 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       tc_fence_before();
       sync_rows();  // accumulators, rows and sums are read
       tc_fence_after();
-      if (tid == 0) record_unit(p, share, w, part);
+      if (tid == 0) record_unit(p, list, share, w, part);
     }
-    write_empty_units<C>(p, part, parts, tid, C::SOFT);
+    write_empty_units<C>(p, list, part, parts, tid, C::SOFT);
   }
   tc_fence_before();
   __syncthreads();

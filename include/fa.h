@@ -201,7 +201,9 @@ size_t fa_bwd_noalloc_max_rows(void);
  * outside [0, max_pages * page_size], a position outside the angle tables or a
  * new_lens[b] outside [0, T] raises a bit that fa_device_status() reports as
  * FA_ERR_BAD_INDEX. Lengths are clamped to their range; keys of a bad page are
- * neither written nor read (hidden from every query).
+ * neither written nor read (hidden from every query). These arrays must not be
+ * written while a call that reads them runs (write them in the call's stream order);
+ * the outputs of such a call are undefined, and it may report FA_ERR_TIMEOUT.
  *
  * Limits: B * Hkv <= 2^24, num_pages * Hkv <= 2^30, max_pages * page_size <= 2^30;
  * page_size is 16, 32, 64, 128 or 256. Pool offsets are 64-bit. */

@@ -1,0 +1,85 @@
+"""Edges of the paged-cache operators on the GPU: lists of more items than a CTA holds at a time, rankings full of ties,
+scores at the ends of the range, weights whose second word decides, calls that meet a full launch queue."""
+import math
+
+import pytest
+import torch
+
+import attention_fa_fwd_03_gb300 as fa
+import paged_ref
+from test_paged_gpu import attend, check_attend, gen, handle, i32, make_table, randn, status_clear
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------- walks past the window
+def scattered(heads, D, dtype, seed=31):
+    """3000 sequences, five of them with keys and hundreds without between them: shares of several tiles, so that a CTA
+    that comes to the end of one sequence has to look for the next behind many windows of items."""
+    B, Hkv, page = 3000, 2, 64
+    lens = [0] * B
+    for i, n in ((5, 9000), (700, 8970), (705, 9001), (1500, 8999), (2999, 64 * 140 + 1)):
+        lens[i] = n
+    g = gen(seed)
+    mp = 141
+    table = torch.zeros(B, mp, dtype=torch.int32)
+    live = [i for i in range(B) if lens[i]]
+    pool = torch.randperm(len(live) * mp + 2, generator=g)[: len(live) * mp].view(len(live), mp)
+    table[live] = pool.to(torch.int32)
+    P = len(live) * mp + 2
+    k, v = randn(g, P, Hkv, page, D, dtype=dtype), randn(g, P, Hkv, page, D, dtype=dtype)
+    return k, v, table, randn(g, B, Hkv * heads, 2, D, dtype=dtype), lens
+
+
+@pytest.mark.parametrize("heads,D", [(2, 64), (4, 128), (10, 128), (20, 64), (40, 96), (9, 256)])
+def test_attend_over_sequences_far_apart(heads, D):
+    k, v, table, q, lens = scattered(heads, D, torch.bfloat16)
+    new = [2 if i % 3 else 1 for i in range(len(lens))]
+    kv = handle(k, v, table, i32(lens))
+    o, lse = attend(kv, q, 1 / math.sqrt(D), True, 0, i32(new))
+    assert status_clear()
+    check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, 1 / math.sqrt(D), True, 0, new))
+
+
+@pytest.mark.parametrize("heads,D", [(2, 64), (20, 128), (9, 256)])
+def test_waits_that_give_up_end_cleanly_in_sequences_far_apart(heads, D):
+    import time
+    k, v, table, q, lens = scattered(heads, D, torch.bfloat16)
+    kv = handle(k, v, table, i32(lens))
+    want = attend(kv, q, 0.1)
+    assert status_clear()
+    fa.fa_set_wait_limit_cycles(8)
+    try:
+        t = time.time()
+        attend(kv, q, 0.1)
+        torch.cuda.synchronize()
+        assert time.time() - t < 2
+        assert fa.fa_device_status() & 1
+    finally:
+        fa.fa_set_wait_limit_cycles(0)
+    o, lse = attend(kv, q, 0.1)
+    assert status_clear()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("heads", [2, 20])
+def test_attend_more_short_sequences_than_a_window_holds(heads):
+    """40000 sequences of one to three tiles in a table 17 pages wide: shares of more than a hundred items."""
+    B, page, D, mp = 40000, 64, 64, 17
+    g = gen(32)
+    kinds = [1, 64, 65, 130, 0]
+    P = 40
+    k, v = randn(g, P, 1, page, D, dtype=torch.float16), randn(g, P, 1, page, D, dtype=torch.float16)
+    kind = torch.arange(B) % 5
+    lens = torch.tensor(kinds)[kind]
+    table = (kind[:, None] * 7 + torch.arange(mp)[None] % 3).to(torch.int32)  # read only: sequences share pages
+    q = randn(g, 5, heads, 1, D, dtype=torch.float16)
+    kv = handle(k, v, table, lens.to(torch.int32))
+    o, lse = attend(kv, q[kind], 0.125)
+    assert status_clear()
+    few = paged_ref.attend(q, k, v, table[:5], kinds, 0.125, True, 0)
+    o, lse = o.view(-1, 5, heads, 1, D), lse.view(-1, 5, heads, 1)
+    for part in (0, o.shape[0] - 1):
+        check_attend(o[part], lse[part], few)
+    check_attend(o.double().mean(0), lse[0], few)
+    assert torch.isfinite(o).all() and (o.float() - o[:1].float()).abs().max() <= 2 * few[2].max()
