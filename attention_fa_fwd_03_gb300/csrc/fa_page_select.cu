@@ -105,7 +105,7 @@ __device__ __forceinline__ FirstRows first_rows(const SelectArgs& p, int b, int 
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int page = p.keep_first + rank * (T / 2) + 16 * (threadIdx.x >> 5) + ((threadIdx.x & 31) >> 2) + 8 * k;
-    f.id[k] = page < p.c.max_pages ? __ldg(p.c.table + static_cast<int64_t>(b) * p.c.max_pages + page) : -1;
+    f.id[k] = page < p.c.max_pages ? p.c.table[static_cast<int64_t>(b) * p.c.max_pages + page] : -1;
   }
   return f;
 }
@@ -371,7 +371,10 @@ __device__ __forceinline__ uint32_t kth_largest_score(SearchSmem<T>& sm, int n, 
     return sm.found;
   }
   int turn = 0;
-  while (true) {
+  // A round leaves a range of at most 2^21 keys, then 2^10, then one. (The limit is for
+  // keys in a workspace that somebody else writes.)
+#pragma unroll 1
+  for (int round = 0; round < 4; ++round) {
     if (lo == hi) return lo;
     const int shift = max(0, 32 - __clz(hi - lo) - 11);
     static_assert(kBins == 1 << 11, "bins cover the range");
@@ -409,7 +412,9 @@ __device__ __forceinline__ uint32_t kth_largest_score(SearchSmem<T>& sm, int n, 
     if (inside <= kFewKeys) {
       for (int i = threadIdx.x; i < n; i += T) {
         const uint32_t k = get(i);
-        if (k >= lo && k <= hi) sm.keys[atomicAdd(&sm.count, 1)] = k;
+        if (k < lo || k > hi) continue;
+        const int at = atomicAdd(&sm.count, 1);
+        if (at < kFewKeys) sm.keys[at] = k;
       }
       __syncthreads();
       if (static_cast<int>(threadIdx.x) < inside) {
@@ -426,6 +431,7 @@ __device__ __forceinline__ uint32_t kth_largest_score(SearchSmem<T>& sm, int n, 
     }
     __syncthreads();  // before the bins are cleared again
   }
+  return lo;
 }
 
 // Store to the first CTA of the cluster, at the place `at` has in this one's
@@ -522,7 +528,8 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ int counters[3][3];
   __shared__ SearchSmem<T> search;
-  __shared__ uint32_t warp_stats[(T / 32)][4], rank_stats[kSelectRanks][4];
+  __shared__ uint32_t warp_stats[(T / 32)][4], rank_stats[kSelectRanks][5];
+  __shared__ int cta_pages;
   __shared__ unsigned long long tie_key[kFewTies];
   __shared__ float2 tie_score[kFewTies], tie_cut;
   __shared__ int tie_page[kFewTies], ties_found;
@@ -538,11 +545,16 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   const int b = unit / c.Hkv, g = unit - b * c.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const FirstRows firsts = first_rows<T>(p, b, rank);
-  const int pages = page_count(c, b);
+  // One reading of the length for the whole CTA, whose threads meet at barriers that
+  // depend on it. CTAs of a cluster that read different ones (somebody writes them under
+  // the call) find that out below.
+  if (threadIdx.x == 0) cta_pages = page_count(c, b);
+  __syncthreads();
+  const int pages = cta_pages;
   // pages keep_first + i, i < n, compete for `need` places
   const int need = p.n_sel - p.keep_first - p.keep_last;
   const int n = pages - p.keep_first - p.keep_last;
-  const bool all = pages <= p.n_sel;  // the same in every CTA of the cluster
+  const bool all = pages <= p.n_sel;
   // scores go to the first CTA's shared memory where they fit and are final at once
   const bool local = n <= kHeld && p.Hq / c.Hkv <= p.head_chunk;
   uint32_t* far = p.scores + static_cast<int64_t>(unit) * c.max_pages;
@@ -576,17 +588,30 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
       }
       st_first(&rank_stats[rank][threadIdx.x], x);
     }
-    __syncwarp();
-    if (ranks > 1)
-      cluster_barrier();  // every CTA's scores are with the first
-    else
-      __syncthreads();
   }
+  if (threadIdx.x == 32) st_first(&rank_stats[rank][4], static_cast<uint32_t>(pages));
+  __syncwarp();
+  if (ranks > 1)
+    cluster_barrier();  // every CTA's scores are with the first
+  else
+    __syncthreads();
   if (rank != 0) return;
 
   int* sel = p.sel + static_cast<int64_t>(unit) * p.n_sel;
   if (threadIdx.x == 0) p.sel_lens[unit] = min(pages, p.n_sel);
-  if (all) {
+  float a_max = 0.f;
+  uint32_t odd = 0, key_lo = ~0u, key_hi = 0u;
+  bool agree = true;
+#pragma unroll
+  for (int r = 0; r < kSelectRanks; ++r) {
+    if (r >= ranks) break;
+    a_max = fmaxf(a_max, __uint_as_float(rank_stats[r][0]));
+    odd |= rank_stats[r][1];
+    key_lo = min(key_lo, rank_stats[r][2]);
+    key_hi = max(key_hi, rank_stats[r][3]);
+    agree &= rank_stats[r][4] == static_cast<uint32_t>(pages);
+  }
+  if (all || !agree) {
     for (int i = threadIdx.x; i < p.n_sel; i += T) sel[i] = i < pages ? i : -1;
     return;
   }
@@ -594,15 +619,6 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   for (int i = threadIdx.x; i < p.keep_last; i += T) sel[p.n_sel - p.keep_last + i] = pages - p.keep_last + i;
   if (need == 0) return;
   auto key32 = [&](int i) { return local ? held[i] : far[i]; };
-  float a_max = 0.f;
-  uint32_t odd = 0, key_lo = ~0u, key_hi = 0u;
-  for (int r = 0; r < ranks; ++r) {
-    a_max = fmaxf(a_max, __uint_as_float(rank_stats[r][0]));
-    odd |= rank_stats[r][1];
-    key_lo = min(key_lo, rank_stats[r][2]);
-    key_hi = max(key_hi, rank_stats[r][3]);
-  }
-
   BlockCounts counts{counters, 0};
   uint32_t low = 0, high = ~0u;  // keys above `high` are in, under `low` out
   int sum[3];
@@ -725,7 +741,8 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     const unsigned long long k64 = p.keys[static_cast<int64_t>(unit) * c.max_pages + i];
     return k64 > cut ? 2 : k64 == cut ? 1 : 0;
   };
-  // places in ascending order: a thread takes runs of four pages
+  // places in ascending order: a thread takes runs of four pages (there are as many as
+  // pages chosen, unless the scores changed under the call)
   int turn = 0;
   int at = p.keep_first, seen = 0;  // places given and equals met before this stretch
   for (int base = 0; base < n; base += 4 * T) {
@@ -759,7 +776,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     at += total;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (st[j] == 2) sel[to++] = p.keep_first + i0 + j;
+      if (st[j] == 2 && to < p.n_sel - p.keep_last) sel[to++] = p.keep_first + i0 + j;
   }
 }
 

@@ -83,3 +83,44 @@ def test_attend_more_short_sequences_than_a_window_holds(heads):
         check_attend(o[part], lse[part], few)
     check_attend(o.double().mean(0), lse[0], few)
     assert torch.isfinite(o).all() and (o.float() - o[:1].float()).abs().max() <= 2 * few[2].max()
+
+
+# ------------------------------------------------------------- lengths written between calls
+def test_calls_follow_lengths_written_between_them():
+    """Selection and attention over the chosen pages, queued behind writes of the lengths that move sequences between no
+    pages, fewer pages than places and many more: each call gives what it gives alone."""
+    B, Hq, Hkv, D, page, mp, n_sel = 5, 8, 2, 128, 16, 700, 24
+    g = gen(61)
+    table, P = make_table(g, B, mp)
+    a, b = randn(g, P, Hkv, D, dtype=torch.bfloat16), randn(g, P, Hkv, D, dtype=torch.bfloat16)
+    bounds = torch.stack([torch.minimum(a, b), torch.maximum(a, b)], 2).contiguous()
+    k, v = randn(g, P, Hkv, page, D, dtype=torch.bfloat16), randn(g, P, Hkv, page, D, dtype=torch.bfloat16)
+    q = randn(g, B, Hq, 1, D, dtype=torch.bfloat16).cuda()
+    kv = handle(k, v, table, i32([0] * B), bounds)
+    steps = [torch.randint(0, hi + 1, (B,), generator=g).to(torch.int32) for hi in (0, 16, 390, 11200, 400, 11200) * 10]
+    steps = torch.stack(steps).cuda()
+    wf = torch.empty(fa.fa_paged_workspace_size(Hq, Hkv, 1, D), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fa.fa_page_select_workspace_size(B, Hkv, mp), dtype=torch.uint8, device="cuda")
+    sel = torch.empty(B, Hkv, n_sel, dtype=torch.int32, device="cuda")
+    count = torch.empty(B, Hkv, dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(B, Hq, 1, device="cuda")
+
+    def run(apart):
+        out = []
+        for n in steps:
+            kv.kv_lens.copy_(n)
+            if apart:
+                torch.cuda.synchronize()
+            fa.fa_page_select(kv, q, sel, count, keep_first=1, keep_last=2, workspace=ws)
+            if apart:
+                torch.cuda.synchronize()
+            fa.fa_paged_fwd(kv, q, o, lse, 0.1, causal=True, sel=sel, sel_lens=count, workspace=wf)
+            out.append([t.clone() for t in (sel, count, o, lse)])
+        assert status_clear()
+        return out
+
+    for x, y in zip(run(True), run(False)):
+        assert all(torch.equal(s, t) for s, t in zip(x, y))
+    for n, (s, c, _, _) in list(zip(steps.tolist(), run(False)))[:6]:
+        want, wc = paged_ref.select(q.cpu(), bounds, table, n, page, n_sel, 1, 2)
+        assert torch.equal(s.cpu(), want) and torch.equal(c.cpu(), wc)
