@@ -21,8 +21,8 @@ namespace fa {
 // stores nothing).
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256)
-fa_bwd_dvec_kernel(const uint4* __restrict__ o, const uint4* __restrict__ dout,
-                   float* __restrict__ dvec, int64_t nrows) {
+fa_bwd_dvec_kernel(const uint4* o, const uint4* dout,
+                   float* dvec, int64_t nrows) {
   constexpr int CHUNKS = D / 8;  // 16-byte chunks per row
   constexpr int TPR = CHUNKS <= 8 ? 8 : (CHUNKS <= 16 ? 16 : 32);
   constexpr int ROWS_PER_BLOCK = 256 / TPR;
@@ -43,8 +43,8 @@ fa_bwd_dvec_kernel(const uint4* __restrict__ o, const uint4* __restrict__ dout,
         const int ch = sub + c * TPR;
         av[u][c] = bv[u][c] = make_uint4(0u, 0u, 0u, 0u);
         if (row < nrows && ch < CHUNKS) {
-          av[u][c] = __ldg(o + row * CHUNKS + ch);
-          bv[u][c] = __ldg(dout + row * CHUNKS + ch);
+          av[u][c] = o[row * CHUNKS + ch];
+          bv[u][c] = dout[row * CHUNKS + ch];
         }
       }
     }

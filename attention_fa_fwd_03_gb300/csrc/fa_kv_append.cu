@@ -65,7 +65,7 @@ __device__ __forceinline__ Angles load_angles(const AppendArgs& p, int pos, int 
   const float4* s = reinterpret_cast<const float4*>(p.sin_table + at);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float4 x = __ldg(c + i), y = __ldg(s + i);
+    const float4 x = c[i], y = s[i];
     g.c[4 * i] = x.x; g.c[4 * i + 1] = x.y; g.c[4 * i + 2] = x.z; g.c[4 * i + 3] = x.w;
     g.s[4 * i] = y.x; g.s[4 * i + 1] = y.y; g.s[4 * i + 2] = y.z; g.s[4 * i + 3] = y.w;
   }
@@ -108,7 +108,7 @@ struct Unit {
   uint4 a, b;
 };
 __device__ __forceinline__ Unit load_unit(const uint16_t* src, const UnitPos& at) {
-  return {__ldg(reinterpret_cast<const uint4*>(src + at.a)), __ldg(reinterpret_cast<const uint4*>(src + at.b))};
+  return {*reinterpret_cast<const uint4*>(src + at.a), *reinterpret_cast<const uint4*>(src + at.b)};
 }
 __device__ __forceinline__ void shuffle_unit(const Unit& x, int lane, Unit* y) {
   const uint32_t* s = reinterpret_cast<const uint32_t*>(&x);

@@ -147,8 +147,8 @@ __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* 
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        lo[k][i] = there[k] ? __ldg(src[k] + 4 * (i0 + i)) : make_uint4(0, 0, 0, 0);
-        hi[k][i] = there[k] ? __ldg(src[k] + D / 8 + 4 * (i0 + i)) : make_uint4(0, 0, 0, 0);
+        lo[k][i] = there[k] ? src[k][4 * (i0 + i)] : make_uint4(0, 0, 0, 0);
+        hi[k][i] = there[k] ? src[k][D / 8 + 4 * (i0 + i)] : make_uint4(0, 0, 0, 0);
       }
   };
   for (int h0 = 0; h0 < reps; h0 += p.head_chunk) {
@@ -160,8 +160,8 @@ __device__ __forceinline__ ScoreStats score_pages(const SelectArgs& p, uint8_t* 
     // behind the last head it again, which changes no maximum
     for (int i = threadIdx.x; i < tiles * 8 * (D / 2); i += T) {
       const int r = i / (D / 2), d2 = i - r * (D / 2);
-      const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(
-                                   p.q + (static_cast<int64_t>(b) * p.Hq + g * reps + h0 + min(r, heads - 1)) * D) + d2);
+      const uint32_t x = reinterpret_cast<const uint32_t*>(
+          p.q + (static_cast<int64_t>(b) * p.Hq + g * reps + h0 + min(r, heads - 1)) * D)[d2];
       const float2 f = unpack2<BF16>(x);
       *reinterpret_cast<uint32_t*>(qs + r * PITCH + 4 * d2) = pack2<BF16>(f.x < 0.f ? 0.f : f.x, f.y < 0.f ? 0.f : f.y);
       *reinterpret_cast<uint32_t*>(qs + (p.head_chunk + r) * PITCH + 4 * d2) =

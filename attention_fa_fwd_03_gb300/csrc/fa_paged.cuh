@@ -10,6 +10,12 @@
 
 namespace fa {
 
+// The kernels start before the one ahead of them in the stream has ended
+// (programmatic serialisation) and may read what it writes: the lengths, the rotated
+// queries, the selection, the bounds. So they read global memory by ordinary loads
+// behind grid_wait_prior(): the read-only path (__ldg) is for memory that nobody writes
+// while the kernel runs, and its loads may be moved above the wait.
+
 // Bit of the device status word beside those of sm103_ptx.cuh: a page, length,
 // position or selected page out of range. The access is skipped.
 constexpr uint32_t kStatusBadIndex = 4u;
@@ -41,7 +47,7 @@ struct SeqLens {
   int len, n;
 };
 __device__ __forceinline__ SeqLens seq_lens(const PagedView& c, const int* new_lens, int b, int T) {
-  const int len = __ldg(c.lens + b), n = new_lens ? __ldg(new_lens + b) : T;
+  const int len = c.lens[b], n = new_lens ? new_lens[b] : T;
   return {checked_count(c, len, c.max_pages << c.page_shift), checked_count(c, n, T)};
 }
 
@@ -54,7 +60,7 @@ __device__ __forceinline__ int checked_page(const PagedView& c, int id) {
 
 // Pool page of page `p` of sequence b (0 <= p < max_pages), or -1.
 __device__ __forceinline__ int pool_page(const PagedView& c, int b, int p) {
-  return checked_page(c, __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + p));
+  return checked_page(c, c.table[static_cast<int64_t>(b) * c.max_pages + p]);
 }
 
 // First element of row `slot` of KV head g in pool page `id`.

@@ -130,7 +130,7 @@ __device__ __forceinline__ ListShape list_shape(const PagedFwdArgs& p) {
 }
 __device__ __forceinline__ int item_seq(const PagedFwdArgs& p, int item) { return p.sel ? item / p.c.Hkv : item; }
 __device__ __forceinline__ ItemLens load_lens(const PagedFwdArgs& p, int item) {
-  const int listed = p.sel ? __ldg(p.sel_lens + item) : 0;
+  const int listed = p.sel ? p.sel_lens[item] : 0;
   const SeqLens sl = seq_lens(p.c, p.new_lens, item_seq(p, item), p.Tq);
   return ItemLens::of(sl.len, sl.n, p.sel ? checked_count(p.c, listed, p.n_sel) : 0);
 }
@@ -441,7 +441,7 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
       if (e >= count) return;
       int pg = e;
       if (p.sel) {
-        pg = __ldg(p.sel + u * p.n_sel + e);
+        pg = p.sel[u * p.n_sel + e];
         if (pg < 0 || pg >= pages) {
           flag_bad_index(c);
           return;
@@ -544,8 +544,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         e = (first + (rank + (t0 + mine) * ranks) * kPagedTile + key) >> c.page_shift;
         pg = e;
         id = -1;
-        if (p.sel) pg = e < p.n_sel ? __ldg(p.sel + u * p.n_sel + e) : -1;
-        if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.max_pages)) id = __ldg(c.table + row + pg);
+        if (p.sel) pg = e < p.n_sel ? p.sel[u * p.n_sel + e] : -1;
+        if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.max_pages)) id = c.table[row + pg];
       };
       const bool early = p.sel != nullptr || p.window == 0;
       if (early) read(0);
@@ -597,7 +597,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     for (int i = tid; i < C::ROWS * (D / 8); i += 32 * C::WARPS) {
       const int r = i / (D / 8), ch = i - r * (D / 8);
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D) + ch);
+      if (r < rows) x = reinterpret_cast<const uint4*>(p.q + (row0 + r) * D)[ch];
       *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(r, ch & 7)) = x;
     }
   };

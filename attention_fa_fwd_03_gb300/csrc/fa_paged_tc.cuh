@@ -257,7 +257,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       for (int i = 0; i < LOADS; ++i) {  // all under way at once
         const int at = tid + i * C::SOFT, r = at / (D / 8);
         x[i] = make_uint4(0, 0, 0, 0);
-        if (r < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + row0 * D) + at);
+        if (r < rows) x[i] = reinterpret_cast<const uint4*>(p.q + row0 * D)[at];
       }
       {
         const uint32_t zero[32] = {};
