@@ -397,6 +397,7 @@ struct TileRing {
     }
     const unsigned loads = __ballot_sync(0xffffffffu, load);
     const uint32_t bar = full + 8 * slot, box = static_cast<uint32_t>(piece) * 128u;
+    __syncwarp();  // lane 0 arrives for the positions of all four lanes (a vote orders no memory)
     if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
     __syncwarp();
     if (load) {

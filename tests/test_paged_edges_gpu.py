@@ -7,7 +7,7 @@ import torch
 
 import attention_fa_fwd_03_gb300 as fa
 import paged_ref
-from test_paged_gpu import attend, check_attend, gen, handle, i32, make_table, randn, status_clear
+from test_paged_gpu import attend, bounds_for, check_attend, gen, handle, i32, make_table, paged_inputs, randn, select, status_clear
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,26 @@ def test_calls_follow_lengths_written_between_them():
     for n, (s, c, _, _) in list(zip(steps.tolist(), run(False)))[:6]:
         want, wc = paged_ref.select(q.cpu(), bounds, table, n, page, n_sel, 1, 2)
         assert torch.equal(s.cpu(), want) and torch.equal(c.cpu(), wc)
+
+
+# ------------------------------------------------------------- tiles without a load
+@pytest.mark.parametrize("heads,D,page", [(4, 128, 16), (4, 128, 64), (16, 64, 16), (40, 128, 16), (24, 256, 32)])
+@pytest.mark.parametrize("n", [900, 40000])
+def test_attend_tiles_of_bad_pages_alone(heads, D, page, n):
+    """Tiles whose pages are all bad bring no bytes, so that their stage is full as soon as the positions of its keys are
+    written: no consumer may take the positions of the tile that held the stage before."""
+    k, v, table, q = paged_inputs(1, heads, 1, D, page, 1, [n], torch.bfloat16, seed=41)
+    r = torch.Generator().manual_seed(42)
+    for t in range(-(-n // 64)):  # about every other tile, in runs
+        if (t // 3) % 2 and torch.rand(1, generator=r) < 0.9:
+            table[0, t * 64 // page:(t + 1) * 64 // page if page < 64 else t * 64 // page + 1] = -5
+    kv = handle(k, v, table, i32([n]))
+    ref = paged_ref.attend(q, k, v, table, [n], 0.1, True, 0)
+    first = None
+    for _ in range(5):
+        o, lse = attend(kv, q, 0.1)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status() == 4
+        check_attend(o, lse, ref)
+        first = first or (o, lse)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
