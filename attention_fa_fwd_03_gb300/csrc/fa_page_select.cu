@@ -24,13 +24,19 @@
 // again as exact products summed in two fp32 words (E2 = D 2^-45 A + 2^-130, the
 // latter for products that underflow), and those that this leaves open too in 64
 // bits, ranked by (score, lower page): the 64-bit units are so few that one page
-// costs microseconds.
+// costs microseconds. Where more pages are in between than can be ranked directly, or
+// bounds are no numbers, each gets a 64-bit score from sums of three fp32 words, eight
+// pages to a warp. Where their scores are all one (a query of zeros, as padding has),
+// the lower pages win and nothing is computed again.
 //
 // Measured in a chain of calls: 12 units of 126 pages 6.4 us, 8 units of 2048 pages
 // (8.4 MB) 11.0 us, both bound by dependent loads, barriers and instruction fetch
 // (scoring 7 K cycles, search 4 K, places 4 K); 256 ragged units of up to 1024 pages (67
 // MB) 26 us, of which scoring moves 5.5 TB/s and the largest units and their choice
 // are the rest. L2 prefetch of the next pass's bounds made that 28 us.
+// 8 units of 2048 pages that all tie: 9.8 us with a query of zeros, 344 with equal bounds
+// in bf16 (156 in fp16, which need no look-out for products beyond fp32); 2634 when each
+// page's score was summed in 64 bits.
 #include "fa_inst.cuh"
 #include "fa_paged_launch.h"
 #include "fa_paged_mma.cuh"
@@ -520,17 +526,208 @@ __device__ __forceinline__ float2 two_word_score(const SelectArgs& p, int b, int
   return best;
 }
 
+// The 64-bit key of a page (-1: none) by 4 lanes, eight pages to a warp: sums in three
+// fp32 words, s + e + f, which hold more than 64 bits' 53, made one number at the end.
+// Terms that are no finite numbers are summed apart, where they decide. `lossy`: a bf16 product was too small or too large for fp32. Which
+// lane adds which dimensions depends on the page's bounds and the query only, so pages
+// with the same bounds get the same key. Called by whole warps.
+template <int D, bool BF16>
+__device__ __forceinline__ unsigned long long three_word_key(const SelectArgs& p, int b, int g, int page, bool* lossy) {
+  const PagedView& c = p.c;
+  const int lane = threadIdx.x & 31, col = lane & 3, reps = p.Hq / c.Hkv;
+  const int id = page >= 0 ? pool_page(c, b, page) : -1;
+  const uint4* lo4 = reinterpret_cast<const uint4*>(c.bounds + (static_cast<int64_t>(max(id, 0)) * c.Hkv + g) * 2 * D);
+  bool lost = false;
+  double best = 0.0;
+  for (int r = 0; r < reps; ++r) {
+    const uint4* q4 = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(b) * p.Hq + g * reps + r) * D);
+    float s = 0.f, e = 0.f, f = 0.f, special = 0.f;
+#pragma unroll 1
+    for (int ch = col; ch < D / 8; ch += 4) {
+      const uint4 xl = lo4[ch], xh = lo4[D / 8 + ch], xq = q4[ch];
+      const uint32_t wl[4] = {xl.x, xl.y, xl.z, xl.w}, wh[4] = {xh.x, xh.y, xh.z, xh.w}, wq[4] = {xq.x, xq.y, xq.z, xq.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 l2 = unpack2<BF16>(wl[i / 2]), h2 = unpack2<BF16>(wh[i / 2]), q2 = unpack2<BF16>(wq[i / 2]);
+        const float l = i & 1 ? l2.y : l2.x, h = i & 1 ? h2.y : h2.x, y = i & 1 ? q2.y : q2.x;
+        const float u = __fmul_rn(y, l), v = __fmul_rn(y, h);
+        const float t = u > v || u != u ? u : v;
+        if (BF16) {
+          // 2^-125: a product of 16 bits above it is exact
+          lost |= y != 0.f && ((l != 0.f && fabsf(u) < 2.3509887e-38f) || (h != 0.f && fabsf(v) < 2.3509887e-38f));
+          lost |= fabsf(y) < INFINITY && ((fabsf(l) < INFINITY && isinf(u)) || (fabsf(h) < INFINITY && isinf(v)));
+        }
+        const bool finite = fabsf(t) < INFINITY;
+        if (!finite) special += t;
+        float e1, e2;
+        two_sum(s, finite ? t : 0.f, &s, &e1);
+        two_sum(e, e1, &e, &e2);
+        f = __fadd_rn(f, e2);
+      }
+    }
+#pragma unroll
+    for (int off = 1; off <= 2; off <<= 1) {
+      // both lanes of a pair add in the same order, so both have the same words
+      const float s2 = __shfl_xor_sync(0xffffffffu, s, off), e2 = __shfl_xor_sync(0xffffffffu, e, off);
+      const float f2 = __shfl_xor_sync(0xffffffffu, f, off);
+      special += __shfl_xor_sync(0xffffffffu, special, off);
+      const bool low = (lane & off) == 0;
+      float s_err, e_err, e_err2;
+      two_sum(low ? s : s2, low ? s2 : s, &s, &s_err);
+      two_sum(low ? e : e2, low ? e2 : e, &e, &e_err);
+      two_sum(e, s_err, &e, &e_err2);
+      f = __fadd_rn(__fadd_rn(low ? f : f2, low ? f2 : f), __fadd_rn(e_err, e_err2));
+    }
+    if (BF16) lost |= special == 0.f && !(fabsf(s) < INFINITY);  // finite terms beyond fp32
+    const double x = special != 0.f ? static_cast<double>(special)
+                                    : static_cast<double>(s) + (static_cast<double>(e) + static_cast<double>(f));
+    if (r == 0 || x > best || x != x) best = x;  // a NaN stays
+  }
+  lost |= __shfl_xor_sync(0xffffffffu, lost, 1);
+  lost |= __shfl_xor_sync(0xffffffffu, lost, 2);
+  *lossy = lost && id >= 0;
+  return id < 0 ? 0ull : order_key(best);
+}
+
+// The chosen of pages i < n into their places, in ascending order: a thread takes runs
+// of four. state(i, key): 2 chosen, 0 not, 1 (where `ties`) chosen if among the first
+// `equal` of its kind. (There are as many chosen as places, unless the scores changed
+// under the call.)
+template <int T, class Get4, class State>
+__device__ __forceinline__ void place_pages(int* sel, int first, int limit, int n, int (*warp_sums)[T / 32], bool ties,
+                                            int equal, const Get4& get4, const State& state) {
+  int turn = 0;
+  int at = first, seen = 0;  // places given and equals met before this stretch
+  for (int base = 0; base < n; base += 4 * T) {
+    const int i0 = base + 4 * threadIdx.x;
+    uint32_t k[4] = {0, 0, 0, 0};
+    get4(i0, k);
+    int st[4], same = 0, total;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      st[j] = i0 + j < n ? state(i0 + j, k[j]) : 0;
+      same += st[j] == 1;
+    }
+    if (ties) {
+      int t = seen + block_before<T>(same, warp_sums, turn++, &total);
+      seen += total;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (st[j] == 1) st[j] = t++ < equal ? 2 : 0;
+    }
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine += st[j] == 2;
+    int to = at + block_before<T>(mine, warp_sums, turn++, &total);
+    at += total;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (st[j] == 2 && to < limit) sel[to++] = first + i0 + j;
+  }
+}
+
+// The choice where many pages compete for the last places: those with an fp32 key in
+// [low, high] are ranked by their 64-bit keys, left in the workspace. By all threads, as
+// the kernel's last step. (A function of its own, called where nothing is needed after
+// it: its registers and code are not the common path's.)
+template <int T>
+struct WideSmem {
+  int (*counters)[3];
+  int round;
+  int (*warp_sums)[T / 32];
+  unsigned long long* key_range;
+};
+template <int T, int D, bool BF16>
+__device__ __noinline__ void choose_wide(const SelectArgs& p, WideSmem<T> sm, const uint32_t* keys32, int unit, int b,
+                                         int g, int n, int places, uint32_t low, uint32_t high, bool odd) {
+  BlockCounts counts{sm.counters, sm.round};
+  unsigned long long* key_range = sm.key_range;
+  unsigned long long* keys = p.keys + static_cast<int64_t>(unit) * p.c.max_pages;
+  int* sel = p.sel + static_cast<int64_t>(unit) * p.n_sel;
+  auto keys4 = [&](int i, uint32_t (&k)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) k[j] = keys32[i + j];
+  };
+  // one score for all of them: bad pages only, or a query of zeros over numbers
+  const int reps = p.Hq / p.c.Hkv;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(b) * p.Hq + g * reps) * D);
+  uint32_t any = 0;
+  for (int i = threadIdx.x; i < reps * (D / 2); i += T) any |= q[i] & 0x7fff7fffu;
+  const bool zero = !__syncthreads_or(any != 0);
+  if (!odd && (zero || high == order_key(-INFINITY))) {
+    place_pages<T>(sel, p.keep_first, p.n_sel - p.keep_last, n, sm.warp_sums, true, places, keys4,
+                   [&](int, uint32_t k) { return k > high ? 2 : k < low ? 0 : 1; });
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int i0 = 8 * (threadIdx.x >> 5); i0 < n; i0 += 8 * (T / 32)) {
+    const int i = i0 + (lane >> 2);
+    const uint32_t k = i < n ? keys32[i] : 0;
+    const bool mine = i < n && k >= low && k <= high;
+    if (!__any_sync(0xffffffffu, mine)) continue;
+    bool lossy;
+    const unsigned long long k64 = three_word_key<D, BF16>(p, b, g, mine ? p.keep_first + i : -1, &lossy);
+    if (mine && (lane & 3) == 0) keys[i] = k64;
+    for (unsigned left = __ballot_sync(0xffffffffu, lossy && (lane & 3) == 0); left != 0; left &= left - 1) {
+      const int at = i0 + ((__ffs(left) - 1) >> 2);
+      const unsigned long long x = exact_key<D, BF16>(p, b, g, p.keep_first + at);
+      if (lane == 0) keys[at] = x;
+    }
+  }
+  __syncthreads();
+  auto key64 = [&](int i, unsigned long long* k) {
+    const uint32_t k32 = keys32[i];
+    if (k32 < low || k32 > high) return false;
+    *k = keys[i];
+    return true;
+  };
+  // the range they are in, often one value
+  if (threadIdx.x == 0) {
+    key_range[0] = ~0ull;
+    key_range[1] = 0ull;
+  }
+  __syncthreads();
+  unsigned long long least = ~0ull, most = 0ull;
+  for (int i = threadIdx.x; i < n; i += T) {
+    unsigned long long k;
+    if (!key64(i, &k)) continue;
+    least = min(least, k);
+    most = max(most, k);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    least = min(least, __shfl_xor_sync(0xffffffffu, least, off));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+  }
+  if (lane == 0) {
+    atomicMin(&key_range[0], least);
+    atomicMax(&key_range[1], most);
+  }
+  __syncthreads();
+  const unsigned long long cut = kth_largest<T, unsigned long long>(counts, n, places, key_range[0], key_range[1], key64);
+  int above = 0;
+  for (int i = threadIdx.x; i < n; i += T) {
+    unsigned long long k;
+    above += key64(i, &k) && k > cut;
+  }
+  int sum[3];
+  counts.add(above, 0, 0, sum);
+  place_pages<T>(sel, p.keep_first, p.n_sel - p.keep_last, n, sm.warp_sums, true, places - sum[0], keys4,
+                 [&](int i, uint32_t k) { return k > high ? 2 : k < low ? 0 : keys[i] > cut ? 2 : keys[i] == cut ? 1 : 0; });
+}
+
 // T = 512: few sequences, the block alone on its SM; T = 256: three blocks share
 // one, so that one's choice overlaps the others' loads.
 template <int T, int D, bool BF16>
 __global__ void __launch_bounds__(T, T == 512 ? 1 : 3)
-fa_page_select_kernel(const SelectArgs p, int ranks) {
+fa_page_select_kernel(const __grid_constant__ SelectArgs p, int ranks) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ int counters[3][3];
   __shared__ SearchSmem<T> search;
   __shared__ uint32_t warp_stats[(T / 32)][4], rank_stats[kSelectRanks][5];
   __shared__ int cta_pages;
-  __shared__ unsigned long long tie_key[kFewTies];
+  __shared__ unsigned long long tie_key[kFewTies], key_range[2];
   __shared__ float2 tie_score[kFewTies], tie_cut;
   __shared__ int tie_page[kFewTies], ties_found;
   uint8_t* qs = dyn;
@@ -632,7 +829,7 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
       low = order_key(t - err);
       high = order_key(t + err);
     } else {
-      low = high = tau;
+      low = high = tau;  // bad pages
     }
     int in = 0, mid = 0;
     for (int i = threadIdx.x; i < n; i += T) {
@@ -650,8 +847,6 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
   }
   const int places = need - sure;   // for the pages in between
   const bool ranked = between > places;
-  unsigned long long cut = 0;       // their keys above `cut` are in, and the first `equal` at it
-  int equal = 0;
   const bool few = ranked && !odd && between <= kFewTies && local && low != order_key(-INFINITY);
   if (few) {
     // Each against the others; the keys of those that win or lose leave
@@ -709,75 +904,22 @@ fa_page_select_kernel(const SelectArgs p, int ranks) {
     }
     __syncthreads();
   } else if (ranked) {
-    unsigned long long* keys = p.keys + static_cast<int64_t>(unit) * c.max_pages;
-    for (int i = warp; i < n; i += (T / 32)) {
-      const uint32_t k = key32(i);
-      if (k < low || k > high) continue;
-      const unsigned long long k64 = exact_key<D, BF16>(p, b, g, p.keep_first + i);
-      if (lane == 0) keys[i] = k64;
-    }
-    __syncthreads();
-    auto key64 = [&](int i, unsigned long long* k) {
-      const uint32_t k32 = key32(i);
-      if (k32 < low || k32 > high) return false;
-      *k = keys[i];
-      return true;
-    };
-    cut = kth_largest<T, unsigned long long>(counts, n, places, 0ull, ~0ull, key64);
-    int above = 0;
-    for (int i = threadIdx.x; i < n; i += T) {
-      unsigned long long k;
-      above += key64(i, &k) && k > cut;
-    }
-    counts.add(above, 0, 0, sum);
-    equal = places - sum[0];
+    return choose_wide<T, D, BF16>(p, {counts.c, counts.round, search.warp_sums, key_range}, local ? held : far, unit, b, g,
+                                   n, places, low, high, odd != 0);
   }
-  // 2: in, 1: in if early enough among its equals, 0: out
-  auto state = [&](int i, uint32_t k) {
-    if (k > high) return 2;
-    if (k < low) return 0;
-    if (!ranked) return 2;
-    if (few) return k == ~0u ? 2 : 0;
-    const unsigned long long k64 = p.keys[static_cast<int64_t>(unit) * c.max_pages + i];
-    return k64 > cut ? 2 : k64 == cut ? 1 : 0;
-  };
-  // places in ascending order: a thread takes runs of four pages (there are as many as
-  // pages chosen, unless the scores changed under the call)
-  int turn = 0;
-  int at = p.keep_first, seen = 0;  // places given and equals met before this stretch
-  for (int base = 0; base < n; base += 4 * T) {
-    const int i0 = base + 4 * threadIdx.x;
-    uint32_t k[4] = {0, 0, 0, 0};
-    if (local && i0 + 3 < n) {
-      const uint4 x = *reinterpret_cast<const uint4*>(held + i0);
-      k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
-    } else {
+  place_pages<T>(
+      sel, p.keep_first, p.n_sel - p.keep_last, n, search.warp_sums, false, 0,
+      [&](int i, uint32_t (&k)[4]) {
+        if (local && i + 3 < n) {
+          const uint4 x = *reinterpret_cast<const uint4*>(held + i);
+          k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
+        } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i0 + j < n) k[j] = key32(i0 + j);
-    }
-    int st[4], ties = 0, total;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      st[j] = i0 + j < n ? state(i0 + j, k[j]) : 0;
-      ties += st[j] == 1;
-    }
-    if (ranked && !few) {
-      int t = seen + block_before<T>(ties, search.warp_sums, turn++, &total);
-      seen += total;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (st[j] == 1) st[j] = t++ < equal ? 2 : 0;
-    }
-    int mine = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mine += st[j] == 2;
-    int to = at + block_before<T>(mine, search.warp_sums, turn++, &total);
-    at += total;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (st[j] == 2 && to < p.n_sel - p.keep_last) sel[to++] = p.keep_first + i0 + j;
-  }
+          for (int j = 0; j < 4; ++j)
+            if (i + j < n) k[j] = key32(i + j);
+        }
+      },
+      [&](int, uint32_t k) { return k > high ? 2 : k < low ? 0 : !ranked || k == ~0u ? 2 : 0; });
 }
 
 template <int T, int D, bool BF16>

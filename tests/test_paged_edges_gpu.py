@@ -7,7 +7,8 @@ import torch
 
 import attention_fa_fwd_03_gb300 as fa
 import paged_ref
-from test_paged_gpu import attend, bounds_for, check_attend, gen, handle, i32, make_table, paged_inputs, randn, select, status_clear
+from test_paged_gpu import (attend, bounds_for, check_attend, check_select, gen, handle, i32, make_table, paged_inputs, randn, select,
+                            status_clear)
 
 pytestmark = pytest.mark.gpu
 
@@ -147,3 +148,102 @@ def test_attend_tiles_of_bad_pages_alone(heads, D, page, n):
         check_attend(o, lse, ref)
         first = first or (o, lse)
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
+# ------------------------------------------------------------- rankings full of ties
+def tied_inputs(kind, B, pages, dtype, D=128, Hq=4, Hkv=2, seed=71):
+    g = gen(seed)
+    table, P = make_table(g, B, pages)
+    bounds, q = bounds_for(g, P, Hkv, D, dtype), randn(g, B, Hq, 1, D, dtype=dtype)
+    if kind == "zero_query":
+        q.zero_()
+    elif kind == "one_zero_query":
+        q[:, :-1].zero_()
+    elif kind == "zero_query_bad_pages":
+        q.zero_()
+        table[:, 5::7] = -1
+    elif kind == "bad_pages":
+        table[:, 40:] = P
+    elif kind == "equal":
+        bounds[:] = bounds[:1]
+    elif kind == "zero_bounds":
+        bounds.zero_()
+    elif kind == "classes":
+        bounds[:] = bounds[torch.randint(0, 5, (P,), generator=g)]
+    elif kind == "nan_bound":
+        bounds[int(table[0, 77]), :, :, 3] = float("nan")
+    elif kind == "infinite_bounds":
+        bounds[int(table[0, 77]), :, 1, 3] = math.inf
+        bounds[int(table[0, 78]), :, 0, 3] = -math.inf
+        bounds[int(table[0, 79])] = -math.inf
+        bounds[int(table[0, 80])] = math.inf
+    elif kind == "nan_query":
+        q[..., 5] = float("nan")
+    elif kind == "infinite_query":
+        q[..., 5] = math.inf
+    elif kind == "cancelling":  # large parts that cancel in every page, in another order each; a small rest decides
+        big = randn(g, D // 2 - 4, dtype=dtype) * 256
+        for i in range(P):
+            perm = torch.randperm(D - 8, generator=g)
+            x = torch.cat([torch.cat([big, -big])[perm], (randn(g, 8, dtype=dtype) * 2.0 ** -10).to(dtype)])
+            bounds[i, :, 0] = bounds[i, :, 1] = x
+        q.fill_(1.0)
+    return q, bounds, table
+
+
+KINDS = ["zero_query", "one_zero_query", "zero_query_bad_pages", "bad_pages", "equal", "zero_bounds", "classes", "nan_bound",
+         "infinite_bounds", "nan_query", "infinite_query", "cancelling"]
+
+
+@pytest.mark.parametrize("B", [1, 11])  # few and many blocks
+@pytest.mark.parametrize("kind", KINDS)
+def test_select_more_ties_than_are_ranked_directly(kind, B):
+    lens = [16 * 700 - 3] + [16 * (90 * i % 640) + 7 for i in range(1, B)]
+    for dtype, D in ((torch.bfloat16, 128), (torch.float16, 96)):
+        q, bounds, table = tied_inputs(kind, B, 700, dtype, D)
+        for n_sel in (3, 333):
+            check_select(q, bounds, table, lens, 16, n_sel, 1, 1)
+        fa.fa_device_status()
+
+
+@pytest.mark.parametrize("kind", ["zero_query", "classes", "nan_bound"])
+def test_select_ties_beyond_shared_memory(kind):
+    """More pages than scores are held of, and more query heads than are held at a time."""
+    for Hq in (2, 40):
+        q, bounds, table = tied_inputs(kind, 1, 13000, torch.bfloat16, D=64 if Hq == 2 else 256, Hq=Hq, Hkv=1)
+        pool = torch.zeros(bounds.shape[0], 1, 16, q.shape[3], dtype=q.dtype)
+        kv = handle(pool, pool, table, i32([16 * 13000]), bounds)
+        sel, count = select(kv, q, 500, 0, 1)
+        assert int(count[0, 0]) == 500
+        b = bounds[table[0].long(), 0].double()
+        x = q[0, :, 0].double()
+        score = torch.maximum(x[:, None] * b[None, :, 0], x[:, None] * b[None, :, 1]).sum(-1).amax(0)[:-1]
+        score = torch.where(score.isnan(), math.inf, score)
+        want = torch.sort(torch.argsort(score, descending=True, stable=True)[:499]).values.tolist() + [12999]
+        assert sel[0, 0].tolist() == want
+
+
+@pytest.mark.parametrize("kind,most", [("zero_query", 4), ("equal", 40), ("nan_bound", 40)])
+def test_select_ties_take_no_milliseconds(kind, most):
+    """A padded sequence's query is zeros: its pages all tie, and its choice must not keep the batch waiting. (With a 64-bit
+    score for every page the factor was 100 and more.)"""
+    def time(kind):
+        q, bounds, table = tied_inputs(kind, 2, 2000, torch.bfloat16, Hq=16, Hkv=4)
+        pool = torch.zeros(bounds.shape[0], 4, 16, 128, dtype=q.dtype)
+        kv = handle(pool, pool, table, i32([32000, 31000]), bounds)
+        q = q.cuda()
+        sel = torch.empty(2, 4, 64, dtype=torch.int32, device="cuda")
+        count = torch.empty(2, 4, dtype=torch.int32, device="cuda")
+        ws = torch.empty(fa.fa_page_select_workspace_size(2, 4, 2000), dtype=torch.uint8, device="cuda")
+        times = []
+        for _ in range(5):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            for _ in range(20):
+                fa.fa_page_select(kv, q, sel, count, keep_first=1, keep_last=2, workspace=ws)
+            e[1].record()
+            torch.cuda.synchronize()
+            times.append(e[0].elapsed_time(e[1]))
+        return min(times)
+
+    assert time(kind) < most * time("ordinary")
