@@ -16,9 +16,10 @@
 //
 // The choice is the one that scores in 64 bits give although nearly all the work
 // is done in 32: with A the largest of sum_d max_h |q_hd| max(|min_d|, |max_d|)
-// over the pages, a score is off by at most E = D 2^-23 A (the products are exact,
-// the D additions at least single precision in an order and with a rounding that
-// are left open). With tau the last place's value among the fp32 scores, its true
+// over the pages, a score is off by at most E = D 2^-23 A + 2 D 2^-126: the products are
+// exact unless they are below fp32's normal numbers (bf16: what becomes of those, and of
+// sums below 2^-126, is left open, at most 2^-126 each), the D additions at least single
+// precision in an order and with a rounding that are left open. With tau the last place's value among the fp32 scores, its true
 // value is within E of tau: pages above tau + 2 E are chosen, pages under tau - 2 E
 // are not. Where those in between are more than the places left, they are computed
 // again as exact products summed in two fp32 words (E2 = D 2^-45 A + 2^-130, the
@@ -823,8 +824,8 @@ fa_page_select_kernel(const __grid_constant__ SelectArgs p, int ranks) {
   if (!odd) {
     const uint32_t tau = kth_largest_score<T>(search, n, need, key_lo, key_hi, local ? held : nullptr, key32);
     const float t = order_value(tau);
-    // 2 E, with room for the error of A and the roundings of t -+ err
-    const float err = 2.02f * D * 1.1920929e-7f * a_max + fabsf(t) * 2.4e-7f;
+    // 2 E, with room for the error of A itself and the roundings of t -+ err
+    const float err = 2.02f * D * 1.1920929e-7f * a_max + fabsf(t) * 2.4e-7f + (BF16 ? 5.f * D * 1.1754944e-38f : 0.f);
     if (t > -INFINITY) {
       low = order_key(t - err);
       high = order_key(t + err);

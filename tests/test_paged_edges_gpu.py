@@ -247,3 +247,18 @@ def test_select_ties_take_no_milliseconds(kind, most):
         return min(times)
 
     assert time(kind) < most * time("ordinary")
+
+
+# ------------------------------------------------------------- scores at the ends of the range
+@pytest.mark.parametrize("exponent", [-60, -66, -70, -72, -73, -74, -76, -80])
+@pytest.mark.parametrize("pages", [200, 600])
+def test_select_tiny_scores_as_in_64_bits(exponent, pages):
+    """bf16 products below fp32's normal numbers, down to where all of them vanish there: the choice stays the one that
+    scores in 64 bits give, with the place cut in the middle of the ranking."""
+    for seed in range(4):
+        g = gen(seed)
+        table, P = make_table(g, 2, pages)
+        bounds = (bounds_for(g, P, 1, 128, torch.float32) * 2.0 ** exponent).to(torch.bfloat16)
+        q = (randn(g, 2, 2, 1, 128, dtype=torch.float32) * 2.0 ** exponent).to(torch.bfloat16)
+        check_select(q, bounds, table, [16 * pages, 8 * pages + 1], 16, pages // 3, 0, 0)
+    assert status_clear()
