@@ -120,8 +120,14 @@ struct PagedCfg {
 // are rescaled: weights then reach 2^8 instead of 1, which costs no precision.
 constexpr float kPagedSlack = 8.f;
 // Running maximum of a row that has seen no key: finite, so that a hidden score of
-// -inf less it is -inf, and so low that any score raises it.
-constexpr float kNoMax = -3e38f;
+// -inf less it is -inf, and the lowest number, so that any score raises it.
+constexpr float kNoMax = -3.402823466e38f;
+// An exponent is s scale - m in one rounding; m is the rounded s scale of some key, so
+// that key's own exponent is up to half a step of m instead of 0. Beyond this magnitude
+// of m a step is no longer small and soon past what an exponent can hold: the scores
+// are then scaled and rounded first, like m.
+constexpr float kLargeMax = 4194304.f;  // 2^22: steps of 1/2
+__device__ __forceinline__ bool large_max(float m) { return fabsf(m) > kLargeMax && m != kNoMax; }
 
 // ----------------------------------------------------------------- the list
 __device__ __forceinline__ ListShape list_shape(const PagedFwdArgs& p) {
@@ -649,6 +655,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         for (int k2 = 0; k2 < D / 32; ++k2) query_frag(qf[nt][k2], nt, k2);
     }
     float m[C::NT][2], l[C::NT][2], acc[C::NT][D / 16][4];
+    bool large = false;  // some row of the warp has a large maximum
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt) {
       m[nt][0] = m[nt][1] = kNoMax;
@@ -724,7 +731,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         // Exponents against the running maxima of this warp's keys, which are looked
         // at across lanes only when some exponent is above the slack.
         float x[C::NT][4];
-        bool above = false;
+        bool above = large;
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
@@ -734,6 +741,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           }
         }
         if (__any_sync(0xffffffffu, above)) {
+          bool any_large = false;
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt) {
             float alpha[2];
@@ -746,6 +754,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               const float mn = fmaxf(m[nt][h], y * p.scale_log2);
               alpha[h] = ex2(m[nt][h] - mn);
               m[nt][h] = mn;
+              any_large |= large_max(mn);
               l[nt][h] *= alpha[h];
             }
 #pragma unroll
@@ -757,6 +766,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], p.scale_log2, -m[nt][e & 1]);
+          }
+          large = __any_sync(0xffffffffu, any_large);
+          if (large) {
+#pragma unroll
+            for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[nt][e] = __fmul_rn(s[nt][e], p.scale_log2) - m[nt][e & 1];
           }
         }
         // Weights in two words of the cache's type, p = hi + lo to 2^-17 (bf16) or

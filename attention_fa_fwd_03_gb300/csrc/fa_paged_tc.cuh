@@ -98,6 +98,21 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[N
     tmem_st32(taddr, r);
 }
 
+// Two fp32 values side by side: both + c, times f.
+__device__ __forceinline__ uint64_t pair_of(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 add_mul2(uint32_t a, uint32_t b, uint64_t c, uint64_t f) {
+  float2 r;
+  asm("{\n .reg .b64 x;\n"
+      " mov.b64 x, {%2, %3};\n add.rn.f32x2 x, x, %4;\n mul.rn.f32x2 x, x, %5;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(a), "r"(b), "l"(c), "l"(f));
+  return r;
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
 fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -275,7 +290,11 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&q_ready));
-      float m = kNoMax, l = 0.f;
+      // The row's running maximum among unscaled scores. An exponent is (s - top) scale: the
+      // difference of near scores is exact, so that it is 0 for the maximum, however large
+      // (s scale - m in one rounding is not, where the steps of m are large).
+      float top = kNoMax, l = 0.f;
+      const uint64_t scale2 = pair_of(p.scale_log2);
       const int end = begin + w.t1 - w.t0;
       // the products of tile t (of segments before: waited for at their ends)
       auto wait_products = [&](int t) {
@@ -336,21 +355,22 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < C::KEYS; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sv[e]));
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-        const bool grow = mx - m > kPagedSlack;
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), rise = (mx - top) * p.scale_log2;
+        const bool grow = rise > kPagedSlack;
         float alpha = 1.f;
         if (grow) {
-          alpha = ex2(m - mx);
-          m = mx;
+          alpha = ex2(-rise);
+          top = mx;
           l *= alpha;
         }
+        const uint64_t top2 = pair_of(-top);
         // weights in two words of the cache's type (see the other kernel)
         uint32_t hi[C::KEYS / 2], lo[C::KEYS / 2];
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < C::KEYS / 2; ++e) {
-          const float p0 = ex2(fmaf(__uint_as_float(sv[2 * e]), p.scale_log2, -m));
-          const float p1 = ex2(fmaf(__uint_as_float(sv[2 * e + 1]), p.scale_log2, -m));
+          const float2 x = add_mul2(sv[2 * e], sv[2 * e + 1], top2, scale2);
+          const float p0 = ex2(x.x), p1 = ex2(x.y);
           sum[0] += p0;
           sum[1] += p1;
           hi[e] = pack2<C::BF16>(p0, p1);
@@ -416,7 +436,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 const float s = __uint_as_float(tmem_ld1(lanes + C::S_COL(b) + key));
                 tmem_ld_wait();
                 const bool seen = !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
-                const float x = ex2(fmaf(s, p.scale_log2, -m));
+                const float x = ex2((s - top) * p.scale_log2);
 #pragma unroll 1
                 for (int col = 0; col < D; col += 32) {
                   uint32_t o[32];
@@ -464,7 +484,8 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       begin = end;
       // padding rows (tokens the sequence does not have) see nothing; a row that has
       // met nothing but NaN keeps it
-      if (tok >= n || (m == kNoMax && l == 0.f)) {
+      float m = top * p.scale_log2;
+      if (tok >= n || (top == kNoMax && l == 0.f)) {
         m = -INFINITY;
         l = 0.f;
       }

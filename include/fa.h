@@ -265,6 +265,8 @@ size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D);
  * (D = 256: / 32), keys = max_pages * page_size, with sel n_sel * page_size.
  * A row that sees no key (or whose every score is -inf), and every padding row,
  * gets O = 0 and LSE = -inf.
+ * Scores are held in fp32 in units of ln 2: |scale q.k| above 2.3e38 counts as
+ * infinite.
  * Values of keys that no row sees never reach a result, whatever they hold. A
  * key that is visible to one row and hidden from another adds exactly nothing to
  * the latter as well. A NaN in a row's query or in a key that the row sees makes

@@ -262,3 +262,60 @@ def test_select_tiny_scores_as_in_64_bits(exponent, pages):
         q = (randn(g, 2, 2, 1, 128, dtype=torch.float32) * 2.0 ** exponent).to(torch.bfloat16)
         check_select(q, bounds, table, [16 * pages, 8 * pages + 1], 16, pages // 3, 0, 0)
     assert status_clear()
+
+
+LARGE = [  # value of the query, of the keys, scale; scores from 5e6 to near what fp32 holds, of both signs
+    ("fp16", 300.0, 303.0, 1.0), ("fp16", 3000.0, 3030.0, 1.0), ("fp16", 3000.0, -3030.0, 0.125),
+    ("fp16", 30000.0, 30310.0, 1.0), ("fp16", 30000.0, -30310.0, 0.3), ("fp16", 65504.0, 65504.0, 1.0),
+    ("bf16", 2.0 ** 20, 2.0 ** 24 * 1.25, 0.7), ("bf16", 2.0 ** 40, -2.0 ** 41, 0.7),
+    ("bf16", 1.28125 * 2.0 ** 60, 2.0 ** 61, 1.0), ("bf16", 1.28125 * 2.0 ** 60, -2.0 ** 61, 1.0),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: f"{c[0]}_{c[1]:.3g}_{c[2]:.3g}")
+@pytest.mark.parametrize("heads,n,D", [(4, 1, 64), (4, 300, 64), (4, 40000, 64), (12, 30000, 64), (24, 9000, 64), (40, 300, 64), (40, 20000, 64),
+                                       (100, 20000, 64), (40, 17003, 64)])
+def test_attend_large_scores(case, heads, n, D):
+    """Keys that are all alike, with scores whose fp32 steps are 1/2 and much more: whatever the scores are rounded to, all
+    weights are equal, so O is the mean of V up to the rounding of its sum and its own (2 (n + 16) u and h), and LSE is
+    score + ln n up to what 64 products, the scaling and the logarithm's two roundings leave."""
+    dt, x, y, scale = case
+    dtype = torch.float16 if dt == "fp16" else torch.bfloat16
+    page = 64
+    g = gen(n + heads)
+    P = -(-n // page) + 1
+    k = torch.full((P, 1, page, D), float("nan"), dtype=dtype)
+    v = torch.full((P, 1, page, D), float("nan"), dtype=dtype)
+    table = torch.randperm(P, generator=g)[: P - 1].view(1, -1).to(torch.int32)
+    for p in range(P - 1):
+        m = min(page, n - p * page)
+        k[int(table[0, p]), :, :m] = y
+        v[int(table[0, p]), :, :m] = randn(g, 1, m, D, dtype=dtype)
+    q = torch.full((1, heads, 1, D), x, dtype=dtype)
+    o, lse = attend(handle(k, v, table, i32([n])), q, scale)
+    assert status_clear()
+    vv = torch.cat([v[int(p), 0] for p in table[0]])[:n].double()
+    u, h = 2.0 ** -24, torch.finfo(dtype).eps / 2
+    want = vv.mean(0)
+    bound = h * want.abs() + 2 * (n + 16) * u * vv.abs().mean(0) * (1 + h) + torch.finfo(dtype).tiny
+    assert ((o[0, :, 0].double().cpu() - want).abs() <= bound).all()
+    s = float(torch.tensor(x, dtype=dtype).double() * torch.tensor(y, dtype=dtype).double()) * D * scale
+    assert (lse.double().cpu() - (s + math.log(n))).abs().max() <= (2 * D + 16) * u * abs(s)
+
+
+@pytest.mark.parametrize("heads,n", [(4, 200), (4, 40000), (40, 20000)])
+def test_attend_large_scores_that_differ(heads, n):
+    """The one key in a hundred with the largest scores has all the weight, wherever it stands."""
+    D, page = 128, 32
+    g = gen(heads)
+    P = -(-n // page)
+    k = torch.full((P, 1, page, D), 20000.0, dtype=torch.float16)
+    v = randn(g, P, 1, page, D, dtype=torch.float16)
+    top = torch.randperm(n, generator=g)[: max(1, n // 100)]
+    k.view(P * page, D)[top] = 20100.0
+    q = torch.full((1, heads, 1, D), 20000.0, dtype=torch.float16)
+    o, lse = attend(handle(k, v, torch.arange(P, dtype=torch.int32).view(1, P), i32([n])), q, 0.5)
+    assert status_clear()
+    vv = v.view(P * page, D)[top].double()
+    want, u, h = vv.mean(0), 2.0 ** -24, 2.0 ** -11
+    assert ((o[0, :, 0].double().cpu() - want).abs() <= h * want.abs() + 2 * (n + 16) * u * vv.abs().mean(0) + 2.0 ** -24).all()
