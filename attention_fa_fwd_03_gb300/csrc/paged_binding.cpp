@@ -102,6 +102,13 @@ cudaStream_t stream_of(PyObject* o, int device) {
   return static_cast<cudaStream_t>(p);
 }
 
+// Other Python threads run while this lives (nothing of Python is touched then): a
+// launch waits where the queue of launches is full, for as long as the GPU takes.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // The cache's device is current while this lives.
 struct OnDevice {
   c10::DeviceIndex was;
@@ -206,9 +213,10 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const bool interleaved = truth(a[5]);
     const int* new_lens = ints(a[8], "new_lens", {c.B}, h.device);
     const cudaStream_t stream = stream_of(a[9], h.device);
+    const int n_heads = dim(Hq, "q"), n_tokens = dim(T, "k"), n_pos = dim(positions, "cos"), rot = dim(2 * half, "cos");
     const OnDevice on(h.device);
-    return fa_kv_append(&c, k, ks, v, vs, q, qs, q_out, dim(Hq, "q"), dim(T, "k"), new_lens, cs, sn,
-                        dim(positions, "cos"), dim(2 * half, "cos"), interleaved, stream);
+    const Unlocked unlocked;
+    return fa_kv_append(&c, k, ks, v, vs, q, qs, q_out, n_heads, n_tokens, new_lens, cs, sn, n_pos, rot, interleaved, stream);
   });
 }
 
@@ -238,9 +246,11 @@ PyObject* paged_fwd(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const int* sel = ints(a[8], "sel", {c.B, c.Hkv, n_sel}, h.device);
     const int* sel_lens = ints(a[9], "sel_lens", {c.B, c.Hkv}, h.device);
     const cudaStream_t stream = stream_of(a[11], h.device);
+    const int n_heads = dim(Hq, "q"), n_tokens = dim(Tq, "q"), n_pages = dim(n_sel, "sel");
     const OnDevice on(h.device);
-    return fa_paged_fwd(&c, q, o, static_cast<float*>(lse), dim(Hq, "q"), dim(Tq, "q"), static_cast<float>(scale),
-                        causal, window, new_lens, sel, sel_lens, dim(n_sel, "sel"), ws, ws_bytes, stream);
+    const Unlocked unlocked;
+    return fa_paged_fwd(&c, q, o, static_cast<float*>(lse), n_heads, n_tokens, static_cast<float>(scale), causal, window,
+                        new_lens, sel, sel_lens, n_pages, ws, ws_bytes, stream);
   });
 }
 
@@ -258,8 +268,10 @@ PyObject* page_select(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     int* sel_lens = static_cast<int*>(address(a[3], "sel_lens", at::kInt, {c.B, c.Hkv}, h.device));
     const int first = integer(a[4], "keep_first"), last = integer(a[5], "keep_last");
     const cudaStream_t stream = stream_of(a[7], h.device);
+    const int n_heads = dim(Hq, "q"), n_pages = dim(n_sel, "sel");
     const OnDevice on(h.device);
-    return fa_page_select(&c, q, dim(Hq, "q"), dim(n_sel, "sel"), first, last, sel, sel_lens, ws, ws_bytes, stream);
+    const Unlocked unlocked;
+    return fa_page_select(&c, q, n_heads, n_pages, first, last, sel, sel_lens, ws, ws_bytes, stream);
   });
 }
 

@@ -319,3 +319,51 @@ def test_attend_large_scores_that_differ(heads, n):
     vv = v.view(P * page, D)[top].double()
     want, u, h = vv.mean(0), 2.0 ** -24, 2.0 ** -11
     assert ((o[0, :, 0].double().cpu() - want).abs() <= h * want.abs() + 2 * (n + 16) * u * vv.abs().mean(0) + 2.0 ** -24).all()
+
+
+# ------------------------------------------------------------- the host's side
+@pytest.mark.parametrize("call", ["append", "attend", "select"])
+def test_other_threads_run_while_a_call_waits_for_the_queue(call):
+    """With the queue of launches full behind a long kernel a call waits. Another thread goes on meanwhile."""
+    import threading
+    import time
+    g = gen(51)
+    table, P = make_table(g, 1, 4)
+    bounds = bounds_for(g, P, 1, 64, torch.bfloat16)
+    k, v = randn(g, P, 1, 16, 64, dtype=torch.bfloat16), randn(g, P, 1, 16, 64, dtype=torch.bfloat16)
+    kv = handle(k, v, table, i32([60]), bounds)
+    q = randn(g, 1, 1, 1, 64, dtype=torch.bfloat16).cuda()
+    o, lse = torch.empty_like(q), torch.empty(1, 1, 1, device="cuda")
+    sel, count = torch.empty(1, 1, 2, dtype=torch.int32, device="cuda"), torch.empty(1, 1, dtype=torch.int32, device="cuda")
+    wf = torch.empty(fa.fa_paged_workspace_size(1, 1, 1, 64), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fa.fa_page_select_workspace_size(1, 1, 4), dtype=torch.uint8, device="cuda")
+    run = {"append": lambda: fa.fa_kv_append(kv, q, q), "attend": lambda: fa.fa_paged_fwd(kv, q, o, lse, 0.1, workspace=wf),
+           "select": lambda: fa.fa_page_select(kv, q, sel, count, workspace=ws)}[call]
+    run()
+    torch.cuda.synchronize()
+    gap, stop = [0.0], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gap[0] = max(gap[0], now - last)
+            last = now
+
+    t = threading.Thread(target=tick)
+    t.start()
+    try:
+        time.sleep(0.05)
+        gap[0] = 0.0
+        begin = time.perf_counter()
+        torch.cuda._sleep(int(0.4e9 * 2))  # cycles: about 0.4 s
+        for _ in range(3000):
+            run()
+        took = time.perf_counter() - begin
+    finally:
+        stop.set()
+        t.join()
+    assert status_clear()
+    assert took > 0.2, "the queue was never full: nothing was tested"
+    assert gap[0] < 0.5 * took
