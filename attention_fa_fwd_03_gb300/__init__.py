@@ -294,7 +294,7 @@ def _paged_calls():
     try:
         from . import _paged
     except ImportError as e:
-        raise RuntimeError("binding of the paged calls not built: _paged.so is missing or does not load "
+        raise RuntimeError("binding of the paged calls not built for this PyTorch: _paged.so is missing or does not load "
                            f"(run `python -c 'import __graft_entry__ as g; g.build()'`): {e}") from e
     return _paged
 
