@@ -367,3 +367,46 @@ def test_other_threads_run_while_a_call_waits_for_the_queue(call):
     assert status_clear()
     assert took > 0.2, "the queue was never full: nothing was tested"
     assert gap[0] < 0.5 * took
+
+
+# ------------------------------------------------------------- weights in two words
+def weights_that_round_alike(dtype):
+    """A key whose weight exp(x) beside weights of 1 is as far from the type's numbers as can be: -> x, exp(x), the weight
+    rounded to the type."""
+    step = torch.finfo(dtype).eps / 2  # below 1
+    xs = torch.linspace(-0.9 * step, -0.1 * step, 400).to(dtype).unique()
+    w = xs.double().exp()
+    i = (w.to(dtype).double() - w).abs().argmax()
+    return float(xs[i]), float(w[i]), float(w[i].to(dtype))
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("B,heads,D,n", [(1, 4, 128, 256), (1, 12, 64, 500), (1, 4, 128, 30000), (1, 16, 256, 20000), (1, 40, 128, 300),  # warps
+                                         (80, 20, 128, 1100), (80, 40, 64, 1100), (80, 100, 96, 1100), (40, 40, 256, 2100)])  # tcgen05
+def test_attend_weights_keep_their_second_word(dt, B, heads, D, n):
+    """Every other key has the weight w < 1 and V = -1, the others 1 and V = 1: O = (1 - w) / (1 + w), next to nothing, and
+    all weights w round alike. With the weights' first word alone O would be off by about (1 - w) / 2 or w's rounding.
+
+    Bound. Both words hold w up to 2^-17 (bf16) or 2^-22 (fp16: and half its smallest number); its exponential is off by
+    2^-21 w and the score's by (2 D + 8) u |x| w. Partial sums of O are at most 64 of one sign beyond what cancels, n (1 - w) / 2
+    in all, so n additions of 2 u each leave 2 u (64 + n (1 - w) / 2) n over a sum of weights of n (1 + w) / 2; joins a few u."""
+    dtype = torch.float16 if dt == "fp16" else torch.bfloat16
+    x, w, rounded = weights_that_round_alike(dtype)
+    page, mp = 64, -(-n // 64)
+    k = torch.zeros(mp, 1, page, D, dtype=dtype)
+    v = torch.ones(mp, 1, page, D, dtype=dtype)
+    k[:, :, 1::2, 0] = x
+    v[:, :, 1::2] = -1
+    q = torch.zeros(B, heads, 1, D, dtype=dtype)
+    q[..., 0] = 1
+    o, lse = attend(handle(k, v, torch.arange(mp, dtype=torch.int32).repeat(B, 1), i32([n] * B)), q, 1.0)
+    assert status_clear()
+    ones, ws = (n + 1) // 2, n // 2
+    want = (ones - ws * w) / (ones + ws * w)
+    u, h = 2.0 ** -24, torch.finfo(dtype).eps / 2
+    second = 2.0 ** -17 if dt == "bf16" else 2.0 ** -22 + 2.0 ** -24
+    bound = h * abs(want) + second + 2.0 ** -20 + (2 * D + 8) * u * abs(x) + 4 * u * (64 + n * (1 - w) / 2) + 16 * u
+    one_word = (ones - ws * rounded) / (ones + ws * w)
+    assert abs(one_word - want) > 5 * bound  # the oracle with one word does not pass
+    assert (o.double().cpu() - want).abs().max() <= bound
+    assert (lse.double().cpu() - math.log(ones + ws * w)).abs().max() <= 2.0 ** -20 + 2 * (n + 16) * u
