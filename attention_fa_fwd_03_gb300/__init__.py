@@ -1,4 +1,4 @@
-"""Exact scaled-dot-product attention for training on GB300 (sm_103a).
+"""Exact scaled-dot-product attention on GB300 (sm_103a), for training and for serving from a paged cache.
 
 Thin Python binding over the C ABI of ``libfa_gb300.so`` (declared in
 ``include/fa.h``): it only turns torch tensors into pointers and sizes, calls

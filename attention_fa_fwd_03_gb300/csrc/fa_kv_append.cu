@@ -17,8 +17,9 @@
 //   many: a warp takes a few consecutive tokens of 4 heads, or with bounds new keys
 //     of one page and KV head, with four rows' loads in flight per thread.
 // Measured: one token of one sequence 1.4 us, of 96 with bounds 2.2 us (a chain of
-// calls; the launch itself); B4 T4096 Hq32 Hkv8 D128 bf16 with bounds, 403 MB, 62.5
-// us = 6.5 TB/s, 96% of the copy rate. That case with (rows, keys in flight, blocks
+// calls; the launch itself); B4 T4096 Hq32 Hkv8 D128 bf16 with bounds, 406 MB, 62.6
+// to 63.2 us = 6.4 to 6.5 TB/s, 95% of the copy rate (the 74 bytes that the key path
+// spills under three blocks per SM included). That case with (rows, keys in flight, blocks
 // per SM): 4/4/3 63.0 us, 4/4/4 73.2, 2/2/4 64.6, 8/4/2 65.0, 2/2/6 90.8.
 #include <type_traits>
 

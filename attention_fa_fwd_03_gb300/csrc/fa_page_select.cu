@@ -30,10 +30,10 @@
 // pages to a warp. Where their scores are all one (a query of zeros, as padding has),
 // the lower pages win and nothing is computed again.
 //
-// Measured in a chain of calls: 12 units of 126 pages 6.4 us, 8 units of 2048 pages
-// (8.4 MB) 11.0 us, both bound by dependent loads, barriers and instruction fetch
+// Measured in a chain of calls: 12 units of 126 pages 6.6 us, 8 units of 2048 pages
+// (8.4 MB) 10.9 us, both bound by dependent loads, barriers and instruction fetch
 // (scoring 7 K cycles, search 4 K, places 4 K); 256 ragged units of up to 1024 pages (67
-// MB) 26 us, of which scoring moves 5.5 TB/s and the largest units and their choice
+// MB) 26 to 27 us, of which scoring moves 5.5 TB/s and the largest units and their choice
 // are the rest. L2 prefetch of the next pass's bounds made that 28 us.
 // 8 units of 2048 pages that all tie: 9.8 us with a query of zeros, 344 with equal bounds
 // in bf16 (156 in fp16, which need no look-out for products beyond fp32); 2634 when each

@@ -31,13 +31,14 @@
 // Split lists of more than 16 rows per KV head go to the kernel of fa_paged_tc.cuh,
 // whose products are on tcgen05.
 //
-// Measured, share of the copy rate (6787 GB/s): up to 8 rows 95% (D 64, 96, 128; B1
-// 131072 keys of 8 KV heads, 537 MB, 84-87 us), 90% (D 256); 16 rows 84-86%. There the
-// tensor pipe is 14% active and the loads bound the kernel: a tcgen05 tile with its
-// round trip through TMEM has nothing to gain. With more rows these products are
-// bound by issue (about 270 instructions per warp and tile with two warps per
-// scheduler; 16 consumer warps instead of 8 gave the same): 32 rows 73%, 40 rows 55%,
-// 64 rows 29%.
+// Measured with 537 MB of keys and values of 8 units, share of the copy rate (6787
+// GB/s): up to 8 rows 89 to 94% (D 64 89, D 96 and 128 91, D 256 94; 131072 keys of
+// D 128 86 to 88 us, of which 4.5 are the join's launch and 3 the start), 16 rows 84 to
+// 88%. There the tensor pipe is 14% active and the loads bound the kernel: a tcgen05 tile
+// with its round trip through TMEM has nothing to gain. With more rows these products
+// are bound by issue (about 270 instructions per warp and tile with two warps per
+// scheduler): 64 rows of 269 MB took 111 us here, 58 on tcgen05. Such rows come here
+// in clusters only.
 #pragma once
 
 #include "fa_inst.cuh"

@@ -29,10 +29,11 @@
 //
 // Measured (269 MB of bf16 keys and values, 16 units, start and join of some 10 us
 // included; warp-level products in brackets): D 128, 32 rows 56 us (64), 64 rows 58
-// (111), 128 rows 68 (190); D 64, 32 rows 60 (80), 64 rows 67 (128), 128 rows 95
-// (233); D 256, 32 rows 66 (65), 64 rows 71 (106), 128 rows 84 (190). At D 128 the
-// loads bound it up to 64 rows (537 MB 93 us, 85% of the copy rate), at D 64, with
-// half the bytes per tile, the softmax's chain, at D 256 the two stages that fit.
+// (111), 128 rows 66 (190); D 96, 52 and 62 us for 64 and 128 rows of 201 MB; D 64, 32
+// rows 59 (80), 64 rows 68 (128), 128 rows 92 (233); D 256, 32 rows 65 (65), 64 rows 71
+// (106), 128 rows 82 (190). At D 128 the loads bound it up to 64 rows (537 MB 93 to 96
+// us, 83 to 85% of the copy rate), at D 64, with half the bytes per tile, the softmax's
+// chain, at D 256 the two stages that fit.
 // Rings of their own for K and V (D 256 62 us with 32 rows, but D 64 67 and five drafts
 // of short lists 8% slower) add waits and commits where D 64 has no time for them.
 #pragma once

@@ -1,10 +1,11 @@
 /*
- * fa.h — exact scaled-dot-product attention for training on sm_103a (GB300).
+ * fa.h — exact scaled-dot-product attention on sm_103a (GB300), for training and
+ * for serving from a paged key/value cache.
  *
  * C ABI of libfa_gb300.so: a forward pass that caches the per-row log-sum-exp
  * (LSE), and its vector-Jacobian product (VJP) split into a D-vector
  * preprocess, a dK/dV kernel and a dQ kernel that recompute P per tile from
- * the cached LSE.
+ * the cached LSE; and, further down, the calls of the paged cache.
  *
  * The operation (page "mlx-bun 0.0.4: package/src/model/flash-attention.ts",
  * forward shader and backward passes 1-3; page "[Metal] Add Flash Attention
