@@ -359,8 +359,9 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t x) {
   return ((x & e) + one) & 0x80008000u;
 }
 
-// A position no query reaches: the key's slot was not loaded.
-constexpr int kNoPosition = 0x7fffff00;
+// A position no query reaches: the key's slot was not loaded. (Positions end below
+// 2^30, and so do windows: differences of any two of these and this stay in 32 bits.)
+constexpr int kNoPosition = 1 << 30;
 
 // A producer warp's side of a CTA's ring of K and V tiles: all of them, or with two
 // producers (C::PRODUCERS) every other one.

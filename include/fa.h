@@ -237,7 +237,8 @@ typedef struct {
  * updated: started afresh where the page's slot 0 is among the new tokens, else
  * widened (so after tokens were taken back they may be wider than needed).
  * 1 <= T <= 2^22, B * T < 2^31, Hq and Hkv <= 2^14. Two sequences of one call
- * must not append to the same page.
+ * must not append to the same page, nor one sequence to a page that its table
+ * holds twice.
  * One kernel launch. Returns FA_OK or an error code (nothing launched on error). */
 fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* k_strides,
                        const void* v_new, const int64_t* v_strides, const void* q,

@@ -410,3 +410,43 @@ def test_attend_weights_keep_their_second_word(dt, B, heads, D, n):
     assert abs(one_word - want) > 5 * bound  # the oracle with one word does not pass
     assert (o.double().cpu() - want).abs().max() <= bound
     assert (lse.double().cpu() - math.log(ones + ws * w)).abs().max() <= 2.0 ** -20 + 2 * (n + 16) * u
+
+
+# ------------------------------------------------------------- masks over what is not there
+@pytest.mark.parametrize("B,heads,D,n", [(1, 4, 128, 700), (1, 4, 64, 30000), (1, 16, 128, 700), (80, 12, 64, 1100), (80, 30, 96, 1100), (40, 10, 256, 2100)])
+@pytest.mark.parametrize("window", [1, 100, 900, 2 ** 31 - 1])
+def test_attend_bad_pages_under_windows(B, heads, D, n, window):
+    """Drafted tokens, windows from one key to more than there are positions, and pages that are not there among those
+    that are seen, hidden and partly hidden."""
+    Tq, page = 3, 32
+    lens = [n] + [max(1, n - 37 * b) for b in range(1, B)]
+    k, v, table, q = paged_inputs(B, heads, 1, D, page, Tq, lens, torch.bfloat16, seed=81)
+    r = gen(82)
+    table[torch.rand(table.shape, generator=r) < 0.2] = -1
+    table[0, (n - 1) // page - 1] = k.shape[0]
+    kv = handle(k, v, table, i32(lens))
+    for causal in (True, False):
+        o, lse = attend(kv, q, 0.1, causal, window)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status() == 4
+        check_attend(o, lse, paged_ref.attend(q, k, v, table, lens, 0.1, causal, window))
+
+
+@pytest.mark.parametrize("B,heads,D,n", [(1, 4, 128, 300), (1, 4, 128, 40000), (80, 20, 64, 1100), (80, 100, 128, 1100), (40, 40, 256, 2100)])
+@pytest.mark.parametrize("scale", [0.01, 3.0])
+def test_attend_nan_with_small_and_large_scales(B, heads, D, n, scale):
+    """A NaN query row is NaN whatever the scale; a NaN key makes every row that sees it NaN; no other row changes."""
+    k, v, table, q = paged_inputs(B, heads, 1, D, 64, 1, [n] * B, torch.bfloat16, seed=83)
+    kv = handle(k, v, table, i32([n] * B))
+    clean = attend(kv, q, scale)
+    q[0, heads // 2, 0, 7] = float("nan")
+    o, lse = attend(kv, q, scale)
+    row = torch.zeros(q.shape[:3], dtype=torch.bool, device="cuda")
+    row[0, heads // 2, 0] = True
+    assert torch.isnan(o[row]).all() and torch.isnan(lse[row]).all()
+    assert torch.equal(o[~row], clean[0][~row]) and torch.equal(lse[~row], clean[1][~row])
+    kv.k[int(table[0, 0]), 0, 5, 3] = float("nan")
+    o, lse = attend(kv, q, scale)
+    assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.equal(o[1:], clean[0][1:]) and torch.equal(lse[1:], clean[1][1:])
+    assert status_clear()
