@@ -32,7 +32,7 @@ import threading
 __all__ = ["FA_FP16", "FA_BF16", "FaError", "fa_fwd", "fa_bwd", "fa_bwd_preprocess", "fa_bwd_dkv",
            "fa_bwd_dq", "fa_bwd_workspace_size",
            "PagedKV", "fa_kv_append", "fa_paged_fwd", "fa_paged_workspace_size", "fa_page_select",
-           "fa_page_select_workspace_size",
+           "fa_page_select_workspace_size", "fa_page_assign",
            "fa_status_string", "fa_device_status", "fa_abi_version", "fa_selftest_wait_timeout",
            "fa_set_wait_limit_cycles", "library", "library_path"]
 
@@ -54,6 +54,14 @@ class _PagedKVStruct(ctypes.Structure):
                 ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
                 ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("max_pages", ctypes.c_int), ("dt", ctypes.c_int)]
+
+
+class _PagedKV8Struct(ctypes.Structure):
+    """fa_paged_kv8 of include/fa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 class FaError(RuntimeError):
@@ -98,6 +106,16 @@ def library():
         lib.fa_kv_append.restype = i
         lib.fa_paged_fwd.argtypes = [kvp, vp, vp, vp, i, i, f, i, i, vp, vp, vp, i, vp, sz, vp]
         lib.fa_paged_fwd.restype = i
+        lib.fa_paged_fwd_sinks.argtypes = [kvp, vp, vp, vp, i, i, f, i, i, i, vp, vp, vp, i, vp, sz, vp]
+        lib.fa_paged_fwd_sinks.restype = i
+        kv8p = ctypes.POINTER(_PagedKV8Struct)
+        lib.fa_kv_append8.argtypes = [kv8p, vp, i64p, vp, i64p, vp, i64p, vp, i, i, vp, vp, vp, i, i,
+                                      i, i, vp]
+        lib.fa_kv_append8.restype = i
+        lib.fa_paged_fwd8.argtypes = [kv8p, vp, vp, vp, i, i, f, i, i, i, vp, vp, vp, i, i, vp, sz, vp]
+        lib.fa_paged_fwd8.restype = i
+        lib.fa_page_assign.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, i, i, vp, vp]
+        lib.fa_page_assign.restype = i
         lib.fa_paged_workspace_size.argtypes = [i, i, i, i]
         lib.fa_paged_workspace_size.restype = sz
         lib.fa_page_select.argtypes = [kvp, vp, i, i, i, i, vp, vp, vp, sz, vp]
@@ -239,17 +257,19 @@ class PagedKV:
 
     ``k`` and ``v`` [num_pages, Hkv, page_size, D] fp16 or bf16, page_size 16 to
     256; ``page_table`` [B, max_pages] and ``kv_lens`` [B] int32; ``k_bounds``
-    [num_pages, Hkv, 2, D] or None. All contiguous on one CUDA device. The
+    [num_pages, Hkv, 2, D] or None. Held in 8 bits, ``k`` and ``v`` are
+    float8_e4m3fn with ``k_scales`` and ``v_scales`` [num_pages, Hkv] fp32, and
+    there are no bounds (so no fa_page_select). All contiguous on one CUDA device. The
     object keeps the tensors alive and is made once: page_table and kv_lens are
     read by every call and updated in place by the caller. Its attributes cannot
     be assigned (``kv.kv_lens += 1`` updates in place): calls go to the tensors
     it was made with.
     """
 
-    __slots__ = ("k", "v", "page_table", "kv_lens", "k_bounds", "device", "dtype", "B", "Hkv", "D",
+    __slots__ = ("k", "v", "page_table", "kv_lens", "k_bounds", "k_scales", "v_scales", "device", "dtype", "B", "Hkv", "D",
                  "num_pages", "page_size", "max_pages", "_handle", "_calls")
 
-    def __init__(self, k, v, page_table, kv_lens, k_bounds=None):
+    def __init__(self, k, v, page_table, kv_lens, k_bounds=None, k_scales=None, v_scales=None):
         import torch
         if k.dim() != 4 or page_table.dim() != 2:
             raise ValueError("k and v are [num_pages, Hkv, page_size, D], page_table is [B, max_pages]")
@@ -257,7 +277,14 @@ class PagedKV:
         for name, value in zip(("num_pages", "Hkv", "page_size", "D", "B", "max_pages", "device", "dtype"),
                                (*k.shape, *page_table.shape, k.device, k.dtype)):
             put(name, value)
-        code = _dtype_code(k)
+        held = k.dtype == torch.float8_e4m3fn
+        if (k_scales is None) == held or (v_scales is None) == held:
+            raise ValueError("k_scales and v_scales go with pools of float8_e4m3fn, and with no others")
+        if held and k_bounds is not None:
+            raise ValueError("a cache held in 8 bits keeps no k_bounds")
+        code = 0 if held else _dtype_code(k)
+        scales = [0, 0] if not held else [self._pointer(name, t, (self.num_pages, self.Hkv), torch.float32)
+                                          for name, t in (("k_scales", k_scales), ("v_scales", v_scales))]
         ptrs = [_ptr(k), self._pointer("v", v, k.shape, k.dtype),
                 0 if k_bounds is None else
                 self._pointer("k_bounds", k_bounds, (self.num_pages, self.Hkv, 2, self.D), k.dtype),
@@ -266,10 +293,10 @@ class PagedKV:
         if max(self.num_pages, self.Hkv, self.page_size, self.D, self.B, self.max_pages) > 2 ** 31 - 1:
             raise ValueError("a size is beyond 32 bits")
         calls = _paged_calls()
-        for name, value in (("k", k), ("v", v), ("k_bounds", k_bounds), ("page_table", page_table), ("kv_lens", kv_lens),
-                            ("_calls", calls),
+        for name, value in (("k", k), ("v", v), ("k_bounds", k_bounds), ("k_scales", k_scales), ("v_scales", v_scales),
+                            ("page_table", page_table), ("kv_lens", kv_lens), ("_calls", calls),
                             ("_handle", calls.handle(*ptrs, self.B, self.Hkv, self.D, self.num_pages, self.page_size,
-                                                     self.max_pages, code, self.device.index))):
+                                                     self.max_pages, code, self.device.index, *scales))):
             put(name, value)
 
     def __setattr__(self, name: str, value) -> None:
@@ -302,7 +329,9 @@ def _paged_calls():
 def fa_kv_append(kv: PagedKV, k, v, cos=None, sin=None, interleaved: bool = False, q=None,
                  q_out=None, new_lens=None, stream=None) -> None:
     """Append T new tokens per sequence to the cache: keys rotated by their
-    position, values copied, page bounds updated where the cache keeps them.
+    position, values copied, page bounds updated where the cache keeps them. Into a
+    cache held in 8 bits both are rounded to e4m3 under their page's and head's
+    scale, which grows where it has to (see include/fa.h).
 
     ``k`` and ``v`` [B, Hkv, T, D] and ``q`` [B, Hq, T, D] may be any views
     with a contiguous innermost index and other strides in multiples of 8, such
@@ -321,16 +350,18 @@ def fa_paged_workspace_size(Hq: int, Hkv: int, Tq: int, D: int) -> int:
 
 
 def fa_paged_fwd(kv: PagedKV, q, o, lse, scale: float, causal: bool = False, window: int = 0,
-                 new_lens=None, sel=None, sel_lens=None, workspace=None, stream=None) -> None:
+                 new_lens=None, sel=None, sel_lens=None, workspace=None, stream=None, sinks: int = 0) -> None:
     """O and LSE of Tq <= 8 new tokens per sequence over the paged cache.
 
     ``q`` and ``o`` [B, Hq, Tq, D], ``lse`` [B, Hq, Tq] fp32, contiguous. The new
     tokens are the last keys of the cache (``kv.kv_lens`` counts them); causal
-    and window masks go by position in the sequence. ``sel`` [B, Hkv, n_sel]
+    and window masks go by position in the sequence; the first ``sinks`` keys stay
+    visible behind a window. ``q`` and ``o`` have the cache's type, or fp16 or bf16
+    where it is held in 8 bits. ``sel`` [B, Hkv, n_sel]
     and ``sel_lens`` [B, Hkv] int32 restrict each KV head to these pages.
     ``workspace`` has fa_paged_workspace_size(Hq, Hkv, Tq, D) bytes."""
     st = kv._calls.paged_fwd(kv._handle, q, o, lse, scale, causal, window, new_lens, sel, sel_lens,
-                             workspace, stream)
+                             workspace, stream, sinks)
     if st != 0:
         raise FaError(st, "fa_paged_fwd")
 
@@ -350,6 +381,25 @@ def fa_page_select(kv: PagedKV, q, sel, sel_lens, keep_first: int = 0, keep_last
     st = kv._calls.page_select(kv._handle, q, sel, sel_lens, keep_first, keep_last, workspace, stream)
     if st != 0:
         raise FaError(st, "fa_page_select")
+
+
+def fa_page_assign(page_table, kv_lens, held, free_pages, free_count, page_size: int, T: int, new_lens=None,
+                   window: int = 0, sinks: int = 0, slots=None, stream=None) -> None:
+    """Pool pages for a step's T new tokens per sequence, and pages that nobody
+    will see again back to the pool (see include/fa.h).
+
+    int32 and contiguous on one CUDA device: ``page_table`` [B, max_pages], written;
+    ``kv_lens`` [B], the new tokens (``new_lens`` [B], None: T each) among them;
+    ``held`` [B, 3], what each sequence holds, zeros at first; ``free_pages``
+    [num_pages] and ``free_count`` [2], the stack of free pool pages and how many
+    it has, with the number of pages that were missing behind it. With ``window`` pages that only hold
+    keys behind it, the first ``sinks`` apart, go back. ``slots`` [B, T] int64 gets each new token's row
+    of the pool (table entry * page_size + slot), -1 for padding. A sequence of
+    ``kv_lens`` 0 gives everything back."""
+    st = _paged_calls().page_assign(page_table, kv_lens, held, free_pages, free_count, page_size, T, new_lens, window,
+                                    sinks, slots, stream)
+    if st != 0:
+        raise FaError(st, "fa_page_assign")
 
 
 def fa_selftest_wait_timeout(timeout_ms: int, stream=None) -> None:

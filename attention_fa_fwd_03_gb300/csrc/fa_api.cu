@@ -126,21 +126,35 @@ bool launch_waits(WaitCfg* wc) {
   return true;
 }
 
-bool encode_tile_map(CUtensorMap* map, const void* base, bool bf16, int D, int T, int BH,
-                     int box_rows) {
+namespace {
+
+// [z, y, x] = [BH, T, D] elements of `bytes` bytes, boxes of 128 bytes x box_rows x 1.
+bool encode_map(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void* base, int D, int T, int BH,
+                int box_rows) {
   std::call_once(g_encode_once, load_encode);
   if (!g_encode) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T),
                               static_cast<cuuint64_t>(BH)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
-                                 static_cast<cuuint64_t>(D) * 2 * static_cast<cuuint64_t>(T)};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * bytes;
+  const cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(T)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / bytes), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t elem_strides[3] = {1, 1, 1};
-  const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                              3, const_cast<void*>(base), dims, strides, box, elem_strides,
+  const CUresult r = g_encode(map, type, 3, const_cast<void*>(base), dims, strides, box, elem_strides,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool encode_tile_map(CUtensorMap* map, const void* base, bool bf16, int D, int T, int BH,
+                     int box_rows) {
+  return encode_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, D, T,
+                    BH, box_rows);
+}
+
+bool encode_byte_map(CUtensorMap* map, const void* base, int D, int T, int BH, int box_rows) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, D, T, BH, box_rows);
 }
 
 int device_sm_count() {

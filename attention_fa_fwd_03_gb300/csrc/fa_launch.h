@@ -39,6 +39,9 @@ struct BwdLaunch {
 bool encode_tile_map(CUtensorMap* map, const void* base, bool bf16, int D, int T, int BH,
                      int box_rows);
 
+// The same over bytes: a box of 128 x box_rows x 1, columns beyond D zero.
+bool encode_byte_map(CUtensorMap* map, const void* base, int D, int T, int BH, int box_rows);
+
 // Status word and wait bounds of a launch on the current device. Returns false
 // when the status word's address cannot be had.
 bool launch_waits(WaitCfg* wc);

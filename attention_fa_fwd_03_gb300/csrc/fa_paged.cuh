@@ -21,9 +21,10 @@ namespace fa {
 constexpr uint32_t kStatusBadIndex = 4u;
 
 struct PagedView {
-  uint16_t* k;       // [num_pages, Hkv, page, D], 16-bit values
+  uint16_t* k;       // [num_pages, Hkv, page, D], 16-bit values (with scales: e4m3)
   uint16_t* v;
   uint16_t* bounds;  // [num_pages, Hkv, 2, D] or null
+  float *k_scales, *v_scales;  // [num_pages, Hkv], or null where the cache holds 16-bit values
   const int* table;  // [B, max_pages]
   const int* lens;   // [B]
   int B, Hkv, D, num_pages, page_shift, max_pages;

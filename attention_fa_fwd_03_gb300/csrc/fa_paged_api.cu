@@ -20,8 +20,38 @@ constexpr int64_t kMaxPool = 1 << 30;      // num_pages * Hkv, and positions of 
 constexpr int kMaxSelected = 1 << 20;
 constexpr int kMaxHeads = 1 << 14;         // of one token of fa_kv_append
 
-fa_status check_cache(const fa_paged_kv* kv, bool need_bounds) {
-  if (!kv) return FA_ERR_INVALID_ARG;
+// A cache of either kind: k_scales and v_scales are null where it holds the calls' own type.
+struct Cache {
+  void *k, *v, *k_bounds;
+  float *k_scales, *v_scales;
+  const int *page_table, *kv_lens;
+  int B, Hkv, D, num_pages, page_size, max_pages;
+  fa_dtype dt;  // of new keys and values, queries and outputs
+  bool there, e4m3;
+  explicit Cache(const fa_paged_kv* kv) : there(kv != nullptr), e4m3(false) {
+    if (!kv) return;
+    k = kv->k; v = kv->v; k_bounds = kv->k_bounds;
+    k_scales = v_scales = nullptr;
+    page_table = kv->page_table; kv_lens = kv->kv_lens;
+    B = kv->B; Hkv = kv->Hkv; D = kv->D;
+    num_pages = kv->num_pages; page_size = kv->page_size; max_pages = kv->max_pages;
+    dt = kv->dt;
+  }
+  Cache(const fa_paged_kv8* kv, fa_dtype type) : there(kv != nullptr), e4m3(true) {
+    if (!kv) return;
+    k = kv->k; v = kv->v; k_bounds = nullptr;
+    k_scales = kv->k_scales; v_scales = kv->v_scales;
+    page_table = kv->page_table; kv_lens = kv->kv_lens;
+    B = kv->B; Hkv = kv->Hkv; D = kv->D;
+    num_pages = kv->num_pages; page_size = kv->page_size; max_pages = kv->max_pages;
+    dt = type;
+  }
+};
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+fa_status check_cache(const Cache* kv, bool need_bounds) {
+  if (!kv->there) return FA_ERR_INVALID_ARG;
   if (kv->B < 1 || kv->Hkv < 1 || kv->num_pages < 1 || kv->max_pages < 1) return FA_ERR_INVALID_ARG;
   const int ps = kv->page_size;
   if (!(ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256)) return FA_ERR_INVALID_ARG;
@@ -33,21 +63,21 @@ fa_status check_cache(const fa_paged_kv* kv, bool need_bounds) {
   if (kv->dt != FA_FP16 && kv->dt != FA_BF16) return FA_ERR_UNSUPPORTED_DTYPE;
   if (!kv->k || !kv->v || !kv->page_table || !kv->kv_lens) return FA_ERR_INVALID_ARG;
   if (need_bounds && !kv->k_bounds) return FA_ERR_INVALID_ARG;
+  if (kv->e4m3 && (!kv->k_scales || !kv->v_scales)) return FA_ERR_INVALID_ARG;
   if (!aligned16(kv->k) || !aligned16(kv->v) || !aligned16(kv->k_bounds)) return FA_ERR_MISALIGNED;
-  if ((reinterpret_cast<uintptr_t>(kv->page_table) | reinterpret_cast<uintptr_t>(kv->kv_lens)) & 3u)
+  if (misaligned4(kv->page_table) || misaligned4(kv->kv_lens) || misaligned4(kv->k_scales) || misaligned4(kv->v_scales))
     return FA_ERR_MISALIGNED;
   return FA_OK;
 }
 
-bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
-
-size_t pool_bytes(const fa_paged_kv* kv) {
-  return static_cast<size_t>(kv->num_pages) * kv->Hkv * kv->page_size * kv->D * 2;
+size_t pool_bytes(const Cache* kv) {
+  return static_cast<size_t>(kv->num_pages) * kv->Hkv * kv->page_size * kv->D * (kv->e4m3 ? 1 : 2);
 }
-size_t bounds_bytes(const fa_paged_kv* kv) {
+size_t bounds_bytes(const Cache* kv) {
   return kv->k_bounds ? static_cast<size_t>(kv->num_pages) * kv->Hkv * 2 * kv->D * 2 : 0;
 }
-size_t table_bytes(const fa_paged_kv* kv) { return static_cast<size_t>(kv->B) * kv->max_pages * 4; }
+size_t scales_bytes(const Cache* kv) { return kv->e4m3 ? static_cast<size_t>(kv->num_pages) * kv->Hkv * 4 : 0; }
+size_t table_bytes(const Cache* kv) { return static_cast<size_t>(kv->B) * kv->max_pages * 4; }
 
 // Byte ranges of a call, with the rule that an output meets nothing else.
 struct Ranges {
@@ -69,11 +99,13 @@ struct Ranges {
   }
 };
 
-PagedView make_view(const fa_paged_kv* kv, uint32_t* status) {
+PagedView make_view(const Cache* kv, uint32_t* status) {
   PagedView c;
   c.k = static_cast<uint16_t*>(kv->k);
   c.v = static_cast<uint16_t*>(kv->v);
   c.bounds = static_cast<uint16_t*>(kv->k_bounds);
+  c.k_scales = kv->k_scales;
+  c.v_scales = kv->v_scales;
   c.table = kv->page_table;
   c.lens = kv->kv_lens;
   c.B = kv->B; c.Hkv = kv->Hkv; c.D = kv->D;
@@ -93,15 +125,11 @@ int64_t view_extent(const int64_t* s, int64_t B, int64_t H, int64_t T, int64_t D
   return (B - 1) * s[0] + (H - 1) * s[1] + (T - 1) * s[2] + D;
 }
 
-}  // namespace
-
-extern "C" {
-
-fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* k_strides,
-                       const void* v_new, const int64_t* v_strides, const void* q,
-                       const int64_t* q_strides, void* q_out, int Hq, int T, const int* new_lens,
-                       const float* cos_table, const float* sin_table, int rope_len, int rot_dim,
-                       int interleaved, cudaStream_t stream) {
+fa_status append(const Cache* kv, const void* k_new, const int64_t* k_strides,
+                 const void* v_new, const int64_t* v_strides, const void* q,
+                 const int64_t* q_strides, void* q_out, int Hq, int T, const int* new_lens,
+                 const float* cos_table, const float* sin_table, int rope_len, int rot_dim,
+                 int interleaved, cudaStream_t stream) {
   fa_status st = check_cache(kv, false);
   if (st != FA_OK) return st;
   if (T < 1 || T > kMaxTokens || static_cast<int64_t>(kv->B) * T > INT32_MAX) return FA_ERR_INVALID_ARG;
@@ -127,6 +155,8 @@ fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* 
   r.out(kv->k, pool_bytes(kv));
   r.out(kv->v, pool_bytes(kv));
   r.out(kv->k_bounds, bounds_bytes(kv));
+  r.out(kv->k_scales, scales_bytes(kv));
+  r.out(kv->v_scales, scales_bytes(kv));
   if (q) r.out(q_out, static_cast<size_t>(kv->B) * Hq * T * kv->D * 2);
   r.in(k_new, static_cast<size_t>(nk) * 2);
   r.in(v_new, static_cast<size_t>(nv) * 2);
@@ -159,25 +189,25 @@ fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* 
   a.interleaved = interleaved;
   a.bf16 = kv->dt == FA_BF16;
   a.stream = stream;
-  return launch_kv_append(a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  return (kv->e4m3 ? launch_kv_append8(a) : launch_kv_append(a)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D) {
+size_t fwd_workspace(int Hq, int Hkv, int Tq, int D) {
   if (Hq < 1 || Hq > kMaxUnits || Hkv < 1 || Hq % Hkv != 0 || Tq < 1 || Tq > kDecodeMaxTq) return 0;
   if (!(D == 64 || D == 96 || D == 128 || D == 256)) return 0;
   return paged_fwd_workspace(Hq / Hkv * Tq, D);
 }
 
-fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse, int Hq, int Tq,
-                       float scale, int causal, int window, const int* new_lens, const int* sel,
-                       const int* sel_lens, int n_sel, void* workspace, size_t workspace_bytes,
-                       cudaStream_t stream) {
+fa_status paged_fwd(const Cache* kv, const void* q, void* o, float* lse, int Hq, int Tq,
+                    float scale, int causal, int window, int sinks, const int* new_lens, const int* sel,
+                    const int* sel_lens, int n_sel, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream) {
   fa_status st = check_cache(kv, false);
   if (st != FA_OK) return st;
   if (Tq < 1 || Tq > kDecodeMaxTq || Hq < 1 || Hq % kv->Hkv != 0) return FA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(kv->B) * Hq > kMaxUnits) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
-  if ((causal != 0 && causal != 1) || window < 0) return FA_ERR_INVALID_ARG;
+  if ((causal != 0 && causal != 1) || window < 0 || sinks < 0) return FA_ERR_INVALID_ARG;
   if (!q || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
   if ((sel == nullptr) != (sel_lens == nullptr)) return FA_ERR_INVALID_ARG;
   if (sel && (n_sel < 1 || n_sel > kMaxSelected)) return FA_ERR_INVALID_ARG;
@@ -186,7 +216,7 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
   const int64_t all_units = static_cast<int64_t>(kv->B) * kv->Hkv * ((Hq / kv->Hkv * Tq + block - 1) / block);
   if (paged_tiles(all_units, static_cast<int64_t>(sel ? n_sel : kv->max_pages) * kv->page_size) > INT32_MAX)
     return FA_ERR_INVALID_ARG;
-  const size_t need = fa_paged_workspace_size(Hq, kv->Hkv, Tq, kv->D);
+  const size_t need = fwd_workspace(Hq, kv->Hkv, Tq, kv->D);
   if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(workspace) ||
       misaligned4(new_lens) || misaligned4(sel) || misaligned4(sel_lens))
@@ -201,6 +231,8 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
   r.in(kv->k, pool_bytes(kv));
   r.in(kv->v, pool_bytes(kv));
   r.in(kv->k_bounds, bounds_bytes(kv));
+  r.in(kv->k_scales, scales_bytes(kv));
+  r.in(kv->v_scales, scales_bytes(kv));
   r.in(kv->page_table, table_bytes(kv));
   r.in(kv->kv_lens, static_cast<size_t>(kv->B) * 4);
   r.in(new_lens, static_cast<size_t>(kv->B) * 4);
@@ -213,7 +245,7 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
   a.q = static_cast<const uint16_t*>(q);
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
-  a.Hq = Hq; a.Tq = Tq; a.causal = causal; a.window = window;
+  a.Hq = Hq; a.Tq = Tq; a.causal = causal; a.window = window; a.sinks = sinks;
   a.scale_log2 = scale * kLog2e;
   a.new_lens = new_lens;
   a.sel = sel; a.sel_lens = sel_lens; a.n_sel = n_sel;
@@ -222,12 +254,65 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
   a.stream = stream;
   cudaError_t e;
   switch (kv->D) {
-    case 64: e = launch_paged_fwd_d64(a); break;
-    case 96: e = launch_paged_fwd_d96(a); break;
-    case 128: e = launch_paged_fwd_d128(a); break;
-    default: e = launch_paged_fwd_d256(a); break;
+    case 64: e = kv->e4m3 ? launch_paged_fwd8_d64(a) : launch_paged_fwd_d64(a); break;
+    case 96: e = kv->e4m3 ? launch_paged_fwd8_d96(a) : launch_paged_fwd_d96(a); break;
+    case 128: e = kv->e4m3 ? launch_paged_fwd8_d128(a) : launch_paged_fwd_d128(a); break;
+    default: e = kv->e4m3 ? launch_paged_fwd8_d256(a) : launch_paged_fwd_d256(a); break;
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_kv_append(const fa_paged_kv* kv, const void* k_new, const int64_t* k_strides,
+                       const void* v_new, const int64_t* v_strides, const void* q,
+                       const int64_t* q_strides, void* q_out, int Hq, int T, const int* new_lens,
+                       const float* cos_table, const float* sin_table, int rope_len, int rot_dim,
+                       int interleaved, cudaStream_t stream) {
+  const Cache c(kv);
+  return append(&c, k_new, k_strides, v_new, v_strides, q, q_strides, q_out, Hq, T, new_lens, cos_table,
+                sin_table, rope_len, rot_dim, interleaved, stream);
+}
+
+fa_status fa_kv_append8(const fa_paged_kv8* kv, const void* k_new, const int64_t* k_strides,
+                        const void* v_new, const int64_t* v_strides, const void* q,
+                        const int64_t* q_strides, void* q_out, int Hq, int T, const int* new_lens,
+                        const float* cos_table, const float* sin_table, int rope_len, int rot_dim,
+                        int interleaved, fa_dtype dt, cudaStream_t stream) {
+  const Cache c(kv, dt);
+  return append(&c, k_new, k_strides, v_new, v_strides, q, q_strides, q_out, Hq, T, new_lens, cos_table,
+                sin_table, rope_len, rot_dim, interleaved, stream);
+}
+
+size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D) { return fwd_workspace(Hq, Hkv, Tq, D); }
+
+fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse, int Hq, int Tq,
+                       float scale, int causal, int window, const int* new_lens, const int* sel,
+                       const int* sel_lens, int n_sel, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+  const Cache c(kv);
+  return paged_fwd(&c, q, o, lse, Hq, Tq, scale, causal, window, 0, new_lens, sel, sel_lens, n_sel, workspace,
+                   workspace_bytes, stream);
+}
+
+fa_status fa_paged_fwd_sinks(const fa_paged_kv* kv, const void* q, void* o, float* lse, int Hq, int Tq,
+                             float scale, int causal, int window, int sinks, const int* new_lens,
+                             const int* sel, const int* sel_lens, int n_sel, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream) {
+  const Cache c(kv);
+  return paged_fwd(&c, q, o, lse, Hq, Tq, scale, causal, window, sinks, new_lens, sel, sel_lens, n_sel, workspace,
+                   workspace_bytes, stream);
+}
+
+fa_status fa_paged_fwd8(const fa_paged_kv8* kv, const void* q, void* o, float* lse, int Hq, int Tq,
+                        float scale, int causal, int window, int sinks, const int* new_lens,
+                        const int* sel, const int* sel_lens, int n_sel, fa_dtype dt, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+  const Cache c(kv, dt);
+  return paged_fwd(&c, q, o, lse, Hq, Tq, scale, causal, window, sinks, new_lens, sel, sel_lens, n_sel, workspace,
+                   workspace_bytes, stream);
 }
 
 size_t fa_page_select_workspace_size(int B, int Hkv, int max_pages) {
@@ -236,9 +321,10 @@ size_t fa_page_select_workspace_size(int B, int Hkv, int max_pages) {
   return (bytes + 255) / 256 * 256;
 }
 
-fa_status fa_page_select(const fa_paged_kv* kv, const void* q, int Hq, int n_sel, int keep_first,
+fa_status fa_page_select(const fa_paged_kv* cache, const void* q, int Hq, int n_sel, int keep_first,
                          int keep_last, int* sel, int* sel_lens, void* workspace,
                          size_t workspace_bytes, cudaStream_t stream) {
+  const Cache kept(cache), *kv = &kept;
   fa_status st = check_cache(kv, true);
   if (st != FA_OK) return st;
   if (Hq < 1 || Hq % kv->Hkv != 0 || static_cast<int64_t>(kv->B) * Hq > kMaxUnits) return FA_ERR_INVALID_ARG;

@@ -55,7 +55,7 @@ struct PagedFwdArgs {
   const uint16_t* q;
   uint16_t* o;
   float* lse;
-  int Hq, Tq, causal, window;
+  int Hq, Tq, causal, window, sinks;
   float scale_log2;
   const int* new_lens;
   const int *sel, *sel_lens;
@@ -73,10 +73,12 @@ struct PagedFwdArgs {
 };
 
 // NT: groups of 8 query rows that a warp holds; RW: warps of other rows beside it.
-template <int D_, int NT_, int RW_, bool BF16_, bool CLUSTER_>
+// E8: the cache is held in e4m3 with scales (see the products).
+template <int D_, int NT_, int RW_, bool BF16_, bool CLUSTER_, bool E8_ = false>
 struct PagedCfg {
   static constexpr int D = D_, NT = NT_, RW = RW_;
-  static constexpr bool BF16 = BF16_;
+  static constexpr bool BF16 = BF16_, E8 = E8_;
+  static constexpr bool MMA_BF16 = BF16 && !E8;      // type of the products' operands
   static constexpr bool CLUSTER = CLUSTER_;          // a cluster per unit instead of equal shares
   // Tiles per CTA up to which clusters are used. 64 rows, D 128, 16 units of 64 tiles (16
   // per CTA): 28.7 us, split 21.7; of 32 tiles: 18.0 and 18.4; 24 rows, 64 tiles 17.6 and 19.4.
@@ -91,23 +93,25 @@ struct PagedCfg {
   static constexpr int PRODUCERS = 1;
   static constexpr int REG_PRODUCER = 40, REG_CONSUMER = 224;
   static constexpr int REG_NEEDED = SPLIT ? 128 * REG_PRODUCER + 32 * WARPS * REG_CONSUMER : 0;
-  static constexpr int KREG = (D + 63) / 64;         // 64-column regions of a row
+  static constexpr int COLS = E8 ? 128 : 64;         // columns of a region, 128 bytes of each row
+  static constexpr int KREG = (D + COLS - 1) / COLS;
   static constexpr int REGION = kPagedTile * 128;
   static constexpr int TILE = KREG * REGION;         // K (or V) rows of a stage
   // Up to 16 rows two CTAs share an SM with about 100 KB in flight each (D = 64 and
   // up to 8 rows: three; with 16, whose registers that would spill, 80% of the copy
   // rate against 84); with more rows, or 64 KB stages, one does.
-  static constexpr int CTAS = D == 256 || RW > 1 ? 1 : D == 64 && NT == 1 ? 3 : 2;
-  static constexpr int STAGES = D == 256  ? (RW == 1 ? 3 : 2)
+  static constexpr int CTAS = RW > 1 || (D == 256 && !E8) ? 1 : D == 64 && NT == 1 ? 3 : 2;
+  static constexpr int STAGES = E8        ? (D == 256 ? (RW == 1 ? 3 : 5) : RW > 1 ? 8 : CTAS == 3 ? 4 : 5)
+                                : D == 256  ? (RW == 1 ? 3 : 2)
                                 : D == 64 ? (RW > 1 ? 8 : NT == 1 ? 4 : 6)
                                           : (RW == 1 ? 3 : 5);
   // Queries as B fragments in registers where they fit, else read again each tile
   static constexpr bool QREG = NT * D <= (CTAS == 1 && RW == 1 ? 256 : 128);
-  static constexpr int QREGION = ROWS * 128;
+  static constexpr int QREGION = ROWS * 128, QREGS = (D + 63) / 64;
   static constexpr int OP = D + 4;                   // row pitch of the merge buffers (floats): no bank conflicts
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
-  static constexpr int OFF_O = OFF_Q + KREG * QREGION;
+  static constexpr int OFF_O = OFF_Q + QREGS * QREGION;
   static constexpr int OFF_ML = OFF_O + ROWS * OP * 4;
   static constexpr int OFF_PML = OFF_ML + KW * ROWS * 8;  // clusters: (max, sum) beside every piece received
   static constexpr int SMEM_BYTES = OFF_PML + (CLUSTER ? ROWS * D : 0) + 1024;
@@ -133,7 +137,7 @@ __device__ __forceinline__ bool large_max(float m) { return fabsf(m) > kLargeMax
 // ----------------------------------------------------------------- the list
 __device__ __forceinline__ ListShape list_shape(const PagedFwdArgs& p) {
   return {p.sel ? p.c.B * p.c.Hkv : p.c.B, (p.sel ? 1 : p.c.Hkv) * p.row_blocks, p.sel != nullptr, p.window,
-          p.c.page_shift};
+          p.c.page_shift, p.sinks};
 }
 __device__ __forceinline__ int item_seq(const PagedFwdArgs& p, int item) { return p.sel ? item / p.c.Hkv : item; }
 __device__ __forceinline__ ItemLens load_lens(const PagedFwdArgs& p, int item) {
@@ -371,21 +375,22 @@ struct TileRing {
   const CUtensorMap &map_k, &map_v;
   uint32_t kv, full, empty;          // shared addresses: stages, barriers
   int (*key_pos)[kPagedKeyWarps];    // position of the first of each 16 keys of a stage
+  float2 (*scales)[kPagedKeyWarps];  // and their scales as keys and as values
   int* abort_flag;
   int piece, pieces;                 // keys of a page in one tile, pages of a tile
   int lane, producer, issued = 0;      // (those of the other producer count too)
   bool ok = true;
   __device__ __forceinline__ TileRing(const PagedFwdArgs& p_, const CUtensorMap& mk, const CUtensorMap& mv, uint32_t kv_,
                                       uint64_t* full_, uint64_t* empty_, int (*key_pos_)[kPagedKeyWarps], int* abort_,
-                                      int producer_ = 0)
+                                      int producer_ = 0, float2 (*scales_)[kPagedKeyWarps] = nullptr)
       : p(p_), map_k(mk), map_v(mv), kv(kv_), full(smem_u32(full_)), empty(smem_u32(empty_)), key_pos(key_pos_),
-        abort_flag(abort_), piece(min(1 << p_.c.page_shift, kPagedTile)), pieces(kPagedTile / piece),
+        scales(scales_), abort_flag(abort_), piece(min(1 << p_.c.page_shift, kPagedTile)), pieces(kPagedTile / piece),
         lane(threadIdx.x & 31), producer(producer_) {}
   __device__ __forceinline__ bool mine(int tile) const { return C::PRODUCERS == 1 || tile % C::PRODUCERS == producer; }
   // One tile of KV head g into the next stage: lane i < pieces has the page (in the
   // sequence, and in the pool or -1) of its piece i, whose first key is key `x` of
-  // the list plus i pieces.
-  __device__ __forceinline__ void load(int x, int pg, int id, int g) {
+  // the list plus i pieces, and lane `from` has the scales of that page in `sc`.
+  __device__ __forceinline__ void load(int x, int pg, int id, int g, float2 sc = {}, int from = 0) {
     const PagedView& c = p.c;
     if (!mine(issued)) {
       ++issued;
@@ -405,19 +410,30 @@ struct TileRing {
     }
     const unsigned loads = __ballot_sync(0xffffffffu, load);
     const uint32_t bar = full + 8 * slot, box = static_cast<uint32_t>(piece) * 128u;
-    __syncwarp();  // lane 0 arrives for the positions of all four lanes (a vote orders no memory)
-    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
-    __syncwarp();
+    auto arrive = [&] {
+      __syncwarp();  // lane 0 arrives for what the other lanes wrote (a vote orders no memory)
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
+      __syncwarp();
+    };
+    if constexpr (!C::E8) arrive();
     if (load) {
       const uint32_t dst = kv + slot * 2 * C::TILE + lane * box;
       const int z = id * c.Hkv + g;
 #pragma unroll
       for (int r = 0; r < C::KREG; ++r) {
-        tma_load_3d(dst + r * C::REGION, &map_k, bar, r * 64, off, z);
-        tma_load_3d(dst + C::TILE + r * C::REGION, &map_v, bar, r * 64, off, z);
+        tma_load_3d(dst + r * C::REGION, &map_k, bar, r * C::COLS, off, z);
+        tma_load_3d(dst + C::TILE + r * C::REGION, &map_v, bar, r * C::COLS, off, z);
       }
     }
     __syncwarp();
+    if constexpr (C::E8) {
+      // the scales may still be on their way: the phase cannot complete before this arrival,
+      // whatever has landed by then
+      const int of = __shfl_sync(0xffffffffu, from, ((lane & 3) * 16) / piece);
+      const float2 mine = {__shfl_sync(0xffffffffu, sc.x, of), __shfl_sync(0xffffffffu, sc.y, of)};
+      if (lane < kPagedKeyWarps) scales[slot][lane] = mine;
+      arrive();
+    }
     ++issued;
   }
   // Stay until the last loads have landed: the consumers have waited for them too,
@@ -428,6 +444,29 @@ struct TileRing {
       if (mine(i)) mbar_wait(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, p.wc.drain_cycles, nullptr, p.wc.status);
   }
 };
+
+// First key that the window shows to a new token of the item, apart from the first keys;
+// 0 where no window moves it. (Selected pages are loaded whatever it shows.)
+__device__ __forceinline__ int first_shown(const PagedFwdArgs& p, const Item& it) {
+  return p.window > 0 && !p.sel ? it.len - it.n - p.window + 1 : 0;
+}
+// Pool page of keys [key, key + piece), for which the table has `id`, or -1: also where
+// none of them is shown. Their page may have been given back, and the table then has -1.
+__device__ __forceinline__ int piece_page(const PagedFwdArgs& p, int shown, int key, int piece, int id) {
+  const bool seen = key + piece > shown || key < p.sinks;
+  if (!seen && id == -1) return -1;
+  id = checked_page(p.c, id);
+  return seen ? id : -1;
+}
+
+// Scales of pool page `id` (any number; 0 where it is no page) as keys and as values.
+template <class C>
+__device__ __forceinline__ float2 page_scales(const PagedView& c, int id, int g) {
+  if constexpr (!C::E8) return {};
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(c.num_pages)) return make_float2(0.f, 0.f);
+  const int64_t at = static_cast<int64_t>(id) * c.Hkv + g;
+  return make_float2(c.k_scales[at], c.v_scales[at]);
+}
 
 // All tiles of a share, by the producer warp. (A wait that gave up ends the loads, not
 // the walk: the window moves on with every warp.)
@@ -443,7 +482,8 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
     const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
     const int64_t u = static_cast<int64_t>(b) * c.Hkv + g;
     const int count = p.sel ? w.it.listed : pages;
-    // pages of list entries [e0, e0 + 32) and the next 32, one per lane
+    // pages of list entries [e0, e0 + 32) and the next 32, one per lane (whether the table
+    // holds a pool page there matters only for those that are loaded)
     auto look_up = [&](int e, int* page, int* id) {
       *page = -1;
       *id = -1;
@@ -457,26 +497,138 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
         }
       }
       *page = pg;
-      *id = pool_page(c, b, pg);
+      *id = c.table[static_cast<int64_t>(b) * c.max_pages + pg];
     };
-    int e0 = ((w.it.first + w.t0) * kPagedTile) >> c.page_shift;
+    const int shown = first_shown(p, w.it);
+    int e0 = (w.it.tile(w.t0) * kPagedTile) >> c.page_shift;
     int page0, id0, page1, id1;
     look_up(e0 + lane, &page0, &id0);
     look_up(e0 + 32 + lane, &page1, &id1);
+    // scales are looked up a batch ahead too, by pages that are known by then
+    int page2 = -1, id2 = -1;
+    float2 sc0 = {}, sc1 = {};
+    auto look_up_scales = [&] {
+      if constexpr (C::E8) {
+        look_up(e0 + 64 + lane, &page2, &id2);
+        sc0 = page_scales<C>(c, id0, g);
+        sc1 = page_scales<C>(c, id1, g);
+      }
+    };
+    look_up_scales();
     for (int t = w.t0; t < w.t1 && ring.ok; ++t) {
-      const int x = (w.it.first + t) * kPagedTile;  // first key of the tile in the list
+      const int x = w.it.tile(t) * kPagedTile;  // first key of the tile in the list
       int e = (x >> c.page_shift) - e0;
-      if (e >= 32) {
+      if (e >= 64) {  // the tiles behind the first keys of a window are further on
+        e0 += e;
+        e = 0;
+        look_up(e0 + lane, &page0, &id0);
+        look_up(e0 + 32 + lane, &page1, &id1);
+        look_up_scales();
+      } else if (e >= 32) {
         e0 += 32;
         e -= 32;
         page0 = page1;
         id0 = id1;
-        look_up(e0 + 32 + lane, &page1, &id1);
+        if constexpr (C::E8) {
+          page1 = page2;
+          id1 = id2;
+          sc0 = sc1;
+          sc1 = page_scales<C>(c, id1, g);
+          look_up(e0 + 64 + lane, &page2, &id2);
+        } else {
+          look_up(e0 + 32 + lane, &page1, &id1);
+        }
       }
       // lane i looks at piece i of the tile
       const int my = e + ((lane * ring.piece) >> c.page_shift);  // below 32: pages of 16 start tiles at multiples of 4
-      ring.load(x, __shfl_sync(0xffffffffu, page0, my & 31), __shfl_sync(0xffffffffu, id0, my & 31), g);
+      const int pg = __shfl_sync(0xffffffffu, page0, my & 31);
+      int id = __shfl_sync(0xffffffffu, id0, my & 31);
+      if (lane < ring.pieces && pg >= 0) id = piece_page(p, shown, x + lane * ring.piece, ring.piece, id);
+      ring.load(x, pg, id, g, sc0, my & 31);
     }
+  }
+}
+
+// ------------------------------------------------- products of held 8-bit values
+// e4m3 values are fp16 numbers, so fragments are read as they are held, two columns to a
+// 16-bit place, and converted in registers (64 pairs per clock and SM; with integer
+// operations a third of that, and NaN would be lost).
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t two_e4m3) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two_e4m3)));
+  return r;
+}
+// Keys: a thread has columns 4 (lane % 4) to the third behind it of 16 of a key (x) and of
+// the eighth behind it (y). Pairs of them make the fragment; its columns are thereby in another
+// order, and so are the staged queries'.
+__device__ __forceinline__ void keys_f16(uint32_t (&a)[4], uint32_t x, uint32_t y) {
+  a[0] = f16x2_of(x);
+  a[1] = f16x2_of(y);
+  a[2] = f16x2_of(x >> 16);
+  a[3] = f16x2_of(y >> 16);
+}
+// Values, read transposed: a place holds columns 2 (lane / 4) and the next of one key. The
+// fragment's first eight rows are the even columns, the others the odd ones.
+__device__ __forceinline__ void values_f16(uint32_t (&a)[4], uint32_t x, uint32_t y) {
+  const uint32_t u = __byte_perm(x, 0, 0x3120), v = __byte_perm(y, 0, 0x3120);
+  a[0] = f16x2_of(u);
+  a[1] = f16x2_of(u >> 16);
+  a[2] = f16x2_of(v);
+  a[3] = f16x2_of(v >> 16);
+}
+// Column of element e of a thread's accumulator i.
+template <class C>
+__device__ __forceinline__ int acc_column(int i, int lane, int e) {
+  return C::E8 ? 16 * i + 2 * (lane >> 2) + (e >> 1) : 16 * i + (lane >> 2) + 8 * (e >> 1);
+}
+// Not 0 where one of four e4m3 values is NaN.
+__device__ __forceinline__ uint32_t nan4_e4m3(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// A block's query rows in fp16, in the order of columns that keys_f16 gives. A bf16 row is
+// brought to a largest magnitude in [2^14, 2^15): its elements down to 2^-28 of that are
+// exact, and the rest is off by at most 2^-40 of it. `scales`: what undoes it.
+template <class C>
+__device__ __forceinline__ void stage_rows_f16(const PagedFwdArgs& p, uint8_t* dst, float* scales, int64_t row0, int rows,
+                                               int warp, int lane) {
+  constexpr int EACH = C::ROWS / C::WARPS, CHUNKS = C::D / 8;
+  uint4 x[EACH];
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {  // all under way at once
+    const int r = warp + k * C::WARPS;
+    x[k] = make_uint4(0, 0, 0, 0);
+    if (r < rows && lane < CHUNKS) x[k] = reinterpret_cast<const uint4*>(p.q + (row0 + r) * C::D)[lane];
+  }
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    const int r = warp + k * C::WARPS;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x[k]);
+    float undo = 1.f;
+    if constexpr (C::BF16) {
+      float most = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<true>(w[i]);
+        if (fabsf(f.x) < INFINITY) most = fmaxf(most, fabsf(f.x));
+        if (fabsf(f.y) < INFINITY) most = fmaxf(most, fabsf(f.y));
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+      // 2^(e - 14) of a magnitude in [2^e, 2^(e + 1)), within normal numbers
+      const int field = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 14, 1), 253);
+      undo = __uint_as_float(static_cast<uint32_t>(field) << 23);
+      const float f = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2<true>(w[i]);
+        w[i] = pack2<false>(v.x * f, v.y * f);
+      }
+    }
+    if (lane == 0) scales[r] = undo;
+    // pairs 0 2 4 6 of 16 columns to the first chunk, 1 3 5 7 to the second
+    const bool odd = lane & 1;
+    const uint32_t s0 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1), s1 = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+    const uint4 y = odd ? make_uint4(s0, s1, w[1], w[3]) : make_uint4(w[0], w[2], s0, s1);
+    if (lane < CHUNKS) *reinterpret_cast<uint4*>(dst + (lane >> 3) * C::QREGION + sw128_offset(r, lane & 7)) = y;
   }
 }
 
@@ -488,6 +640,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES];
   __shared__ int key_pos[C::STAGES][C::KW];  // position of the first of each warp's 16 keys
+  __shared__ float2 kv_scale[C::E8 ? C::STAGES : 1][C::KW];  // and the scales of their page
+  __shared__ float row_scale[C::E8 ? C::ROWS : 1];           // that the staged query rows are to be multiplied by
   __shared__ ItemLens item_lens[C::CLUSTER ? 1 : kItemWindow];
   __shared__ int abort_flag;
   constexpr int D = C::D;
@@ -535,7 +689,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         return;
       }
     }
-    TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag);
+    TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag, 0, kv_scale);
     const int piece = ring.piece, pieces = ring.pieces;
     if constexpr (C::CLUSTER) {
       // Lane k * pieces + i looks up piece i of the k-th tile of a batch of as many of
@@ -548,9 +702,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       const int64_t u = static_cast<int64_t>(b) * c.Hkv + g;
       const int64_t row = static_cast<int64_t>(b) * c.max_pages;
       const int batch = 32 / pieces, mine = lane / pieces, key = (lane & (pieces - 1)) * piece;
-      int first = 0, pg = -1, id = -1, e = 0;
+      int pg = -1, id = -1, e = 0, x = 0;
+      w.it.head = w.it.skip = 0;
       auto read = [&](int t0) {
-        e = (first + (rank + (t0 + mine) * ranks) * kPagedTile + key) >> c.page_shift;
+        x = w.it.tile(rank + (t0 + mine) * ranks) * kPagedTile + key;
+        e = x >> c.page_shift;
         pg = e;
         id = -1;
         if (p.sel) pg = e < p.n_sel ? p.sel[u * p.n_sel + e] : -1;
@@ -559,22 +715,23 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       const bool early = p.sel != nullptr || p.window == 0;
       if (early) read(0);
       w.start_unit(list, rank, ranks, load_lens_warp(p, w.item));
-      first = w.it.first * kPagedTile;
+      const int shown = first_shown(p, w.it);
       const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
       const int count = p.sel ? w.it.listed : pages;
       for (int t0 = 0; t0 < w.t1 && ring.ok; t0 += batch) {
         if (t0 > 0 || !early) read(t0);
         const bool counts = t0 + mine < w.t1 && e < count;
         if (counts && static_cast<unsigned>(pg) < static_cast<unsigned>(pages)) {
-          id = checked_page(c, id);
+          id = piece_page(p, shown, x, piece, id);
         } else {
           if (counts) flag_bad_index(c);  // a selected page that the sequence does not have
           id = -1;
         }
+        const float2 sc = page_scales<C>(c, id, g);
         for (int t = t0; t < min(w.t1, t0 + batch) && ring.ok; ++t) {
           const int from = (t - t0) * pieces + (lane & (pieces - 1));
-          ring.load(first + (rank + t * ranks) * kPagedTile, __shfl_sync(0xffffffffu, pg, from),
-                    __shfl_sync(0xffffffffu, id, from), g);
+          ring.load(w.it.tile(rank + t * ranks) * kPagedTile, __shfl_sync(0xffffffffu, pg, from),
+                    __shfl_sync(0xffffffffu, id, from), g, sc, from);
         }
       }
     } else {
@@ -603,6 +760,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 
   // a block's query rows to shared memory, rows behind the last one zero
   auto stage_queries = [&](int64_t row0, int rows) {
+    if constexpr (C::E8) {
+      stage_rows_f16<C>(p, smem + C::OFF_Q, row_scale, row0, rows, warp, lane);
+      return;
+    }
     for (int i = tid; i < C::ROWS * (D / 8); i += 32 * C::WARPS) {
       const int r = i / (D / 8), ch = i - r * (D / 8);
       uint4 x = make_uint4(0, 0, 0, 0);
@@ -656,6 +817,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) query_frag(qf[nt][k2], nt, k2);
     }
+    float2 rs[C::E8 ? C::NT : 1];  // of this thread's columns
+    if constexpr (C::E8) {
+#pragma unroll
+      for (int nt = 0; nt < C::NT; ++nt) rs[nt] = make_float2(row_scale[col0 + 8 * nt], row_scale[col0 + 8 * nt + 1]);
+    }
     float m[C::NT][2], l[C::NT][2], acc[C::NT][D / 16][4];
     bool large = false;  // some row of the warp has a large maximum
 #pragma unroll
@@ -675,9 +841,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       const int j0 = key_pos[slot][kw];
       const uint32_t ks = sbase + C::OFF_KV + slot * 2 * C::TILE, vs = ks + C::TILE;
       // does any row see any of the 16 keys; do all rows see all of them
-      const bool some = has_rows && j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window);
+      const bool some = has_rows && j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window && j0 >= p.sinks);
       if (some) {
-        const bool all = j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) && !(p.window > 0 && j0 <= p_hi - p.window);
+        const bool all = j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) &&
+                         !(p.window > 0 && j0 <= p_hi - p.window && j0 + 15 >= p.sinks);
         // S^T = K Q^T: element e of group nt is key j0 + lane / 4 + 8 (e / 2), row
         // col0 + 8 nt + e % 2. One group: two accumulators, half as long a chain.
         float s[C::NT][4], s2[4];
@@ -685,8 +852,15 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) {
           uint32_t a0[4], a1[4];
-          ldsm4(a0, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + kc) & 7));
-          ldsm4(a1, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + 2 + kc) & 7));
+          if constexpr (C::E8) {
+            uint32_t x[4];
+            ldsm4(x, ks + (k2 >> 2) * C::REGION + sw128_offset(kr, (2 * k2 + kc) & 7));
+            keys_f16(a0, x[0], x[1]);
+            keys_f16(a1, x[2], x[3]);
+          } else {
+            ldsm4(a0, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + kc) & 7));
+            ldsm4(a1, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + 2 + kc) & 7));
+          }
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt) {
             uint32_t b[4];
@@ -697,24 +871,37 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               query_frag(b, nt, k2);
             }
             if (k2 == 0)
-              mma16816_first<C::BF16>(s[nt], a0, b[0], b[1]);
+              mma16816_first<C::MMA_BF16>(s[nt], a0, b[0], b[1]);
             else
-              mma16816<C::BF16>(s[nt], a0, b[0], b[1]);
+              mma16816<C::MMA_BF16>(s[nt], a0, b[0], b[1]);
             if (C::NT == 1 && k2 == 0)
-              mma16816_first<C::BF16>(s2, a1, b[2], b[3]);
+              mma16816_first<C::MMA_BF16>(s2, a1, b[2], b[3]);
             else
-              mma16816<C::BF16>(C::NT == 1 ? s2 : s[nt], a1, b[2], b[3]);
+              mma16816<C::MMA_BF16>(C::NT == 1 ? s2 : s[nt], a1, b[2], b[3]);
           }
         }
         if constexpr (C::NT == 1) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[0][e] += s2[e];
         }
+        float2 scale = {};  // of the keys and of the values
+        if constexpr (C::E8) {
+          // powers of two: exact, the smaller one first so that it is only what the score is
+          // that can leave the range
+          scale = kv_scale[slot][kw];
+#pragma unroll
+          for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float f = e & 1 ? rs[nt].y : rs[nt].x;
+              s[nt][e] = s[nt][e] * fminf(f, scale.x) * fmaxf(f, scale.x);
+            }
+        }
         uint32_t keep0 = ~0u, keep1 = ~0u;  // keys of this thread's V fragments that some row sees
         const int jv = j0 + 2 * (lane & 3);
         if (!all) {
-          // keys [j0 + lo, j0 + lo + span) are seen by a column's row; this thread's are
-          // j0 + lane / 4 and 8 behind it
+          // keys [j0 + lo, j0 + lo + span) are seen by a column's row, and the first ones below
+          // j0 + keep; this thread's are j0 + lane / 4 and 8 behind it
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
@@ -723,10 +910,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               const int lo = p.window > 0 ? pos - p.window + 1 - j0 : -j0;
               const int hi = (p.causal ? min(len, pos + 1) : len) - j0;
               const unsigned span = static_cast<unsigned>(max(hi - lo, 0)), j = (lane >> 2) - lo;
-              if (j >= span) s[nt][h] = -INFINITY;
-              if (j + 8 >= span) s[nt][2 + h] = -INFINITY;
+              const int keep = min(p.sinks - j0, hi);
+              if (j >= span && (lane >> 2) >= keep) s[nt][h] = -INFINITY;
+              if (j + 8 >= span && (lane >> 2) + 8 >= keep) s[nt][2 + h] = -INFINITY;
             }
-          auto seen = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window); };
+          auto seen = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window && j >= p.sinks); };
           keep0 = (seen(jv) ? 0xffffu : 0u) | (seen(jv + 1) ? 0xffff0000u : 0u);
           keep1 = (seen(jv + 8) ? 0xffffu : 0u) | (seen(jv + 9) ? 0xffff0000u : 0u);
         }
@@ -792,10 +980,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t hi = pack2<C::BF16>(s[nt][2 * h], s[nt][2 * h + 1]);
-            const float2 f = unpack2<C::BF16>(hi);
+            const uint32_t hi = pack2<C::MMA_BF16>(s[nt][2 * h], s[nt][2 * h + 1]);
+            const float2 f = unpack2<C::MMA_BF16>(hi);
             pb[nt][h] = transpose8(hi);
-            pl[nt][h] = transpose8(pack2<C::BF16>(s[nt][2 * h] - f.x, s[nt][2 * h + 1] - f.y));
+            pl[nt][h] = transpose8(pack2<C::MMA_BF16>(s[nt][2 * h] - f.x, s[nt][2 * h + 1] - f.y));
           }
         }
         // O^T += V^T P^T. A key hidden from every row gets V = 0 (its slot may hold
@@ -807,7 +995,23 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                             ((p.causal && j0 + 15 > p_lo && j0 <= p_hi) ||
                              (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
         bool apart = false;
-        if (differ) {
+        // two times 16 columns of V^T, from one read of the held values
+        auto values_of = [&](uint32_t (&a)[2][4], int i2, uint32_t m0, uint32_t m1) {
+          uint32_t x[4];
+          ldsm4_trans(x, vs + (i2 >> 2) * C::REGION + sw128_offset(vr, (2 * i2 + vc) & 7));
+          values_f16(a[0], x[0] & m0, x[2] & m1);
+          values_f16(a[1], x[1] & m0, x[3] & m1);
+        };
+        if (C::E8 && differ) {
+          uint32_t odd = 0;
+#pragma unroll
+          for (int i2 = 0; i2 < D / 32; ++i2) {
+            uint32_t x[4];
+            ldsm4_trans(x, vs + (i2 >> 2) * C::REGION + sw128_offset(vr, (2 * i2 + vc) & 7));
+            odd |= nan4_e4m3(x[0] & keep0) | nan4_e4m3(x[1] & keep0) | nan4_e4m3(x[2] & keep1) | nan4_e4m3(x[3] & keep1);
+          }
+          apart = __any_sync(0xffffffffu, odd != 0);
+        } else if (differ) {
           uint32_t odd = 0;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -818,7 +1022,23 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           }
           apart = __any_sync(0xffffffffu, odd != 0);
         }
-        if (!apart) {
+        if (C::E8 && !apart) {
+#pragma unroll
+          for (int i2 = 0; i2 < D / 32; ++i2) {
+            uint32_t a[2][4];
+            values_of(a, i2, keep0, keep1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int nt = 0; nt < C::NT; ++nt) {
+                float x[4];
+                mma16816_first<false>(x, a[h], pb[nt][0], pb[nt][1]);
+                mma16816<false>(x, a[h], pl[nt][0], pl[nt][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][2 * i2 + h][e] = fmaf(x[e], scale.y, acc[nt][2 * i2 + h][e]);
+              }
+          }
+        } else if (!apart) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             uint32_t a[4];
@@ -829,19 +1049,38 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             a[3] &= keep1;
 #pragma unroll
             for (int nt = 0; nt < C::NT; ++nt)
-              mma16816<C::BF16>(acc[nt][i], a, pb[nt][0], pb[nt][1]);
+              mma16816<C::MMA_BF16>(acc[nt][i], a, pb[nt][0], pb[nt][1]);
 #pragma unroll
-            for (int nt = 0; nt < C::NT; ++nt) mma16816<C::BF16>(acc[nt][i], a, pl[nt][0], pl[nt][1]);
+            for (int nt = 0; nt < C::NT; ++nt) mma16816<C::MMA_BF16>(acc[nt][i], a, pl[nt][0], pl[nt][1]);
           }
         } else {
 #pragma unroll 1
           for (int tok = 0; tok < n; ++tok) {
             const int pos = p_lo + tok;
             auto seen = [&](int j) {
-              return j < len && !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
+              return j < len && !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window && j >= p.sinks);
             };
             const uint32_t k0 = (seen(jv) ? 0xffffu : 0u) | (seen(jv + 1) ? 0xffff0000u : 0u);
             const uint32_t k1 = (seen(jv + 8) ? 0xffffu : 0u) | (seen(jv + 9) ? 0xffff0000u : 0u);
+            if constexpr (C::E8) {
+#pragma unroll
+              for (int i2 = 0; i2 < D / 32; ++i2) {
+                uint32_t a[2][4];
+                values_of(a, i2, k0, k1);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int nt = 0; nt < C::NT; ++nt) {
+                    float x[4];
+                    mma16816_first<false>(x, a[h], pb[nt][0], pb[nt][1]);
+                    mma16816<false>(x, a[h], pl[nt][0], pl[nt][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      if (token(nt, e & 1) == tok) acc[nt][2 * i2 + h][e] = fmaf(x[e], scale.y, acc[nt][2 * i2 + h][e]);
+                  }
+              }
+              continue;
+            }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               uint32_t a[4];
@@ -853,8 +1092,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
               for (int nt = 0; nt < C::NT; ++nt) {
                 float x[4] = {acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]};
-                mma16816<C::BF16>(x, a, pb[nt][0], pb[nt][1]);
-                mma16816<C::BF16>(x, a, pl[nt][0], pl[nt][1]);
+                mma16816<C::MMA_BF16>(x, a, pb[nt][0], pb[nt][1]);
+                mma16816<C::MMA_BF16>(x, a, pl[nt][0], pl[nt][1]);
                 if (token(nt, 0) == tok) acc[nt][i][0] = x[0], acc[nt][i][2] = x[2];
                 if (token(nt, 1) == tok) acc[nt][i][1] = x[1], acc[nt][i][3] = x[3];
               }
@@ -899,8 +1138,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            wm[(kw * C::ROWS + col0 + 8 * nt + (e & 1)) * C::OP + 16 * i + (lane >> 2) + 8 * (e >> 1)] =
-                  acc[nt][i][e];
+            wm[(kw * C::ROWS + col0 + 8 * nt + (e & 1)) * C::OP + acc_column<C>(i, lane, e)] = acc[nt][i][e];
       sync_rows();
       const int pieces = rows * (D / 8), share_of = C::ROWS * (D / 8) / ranks;
       float2* pml = reinterpret_cast<float2*>(smem + C::OFF_PML);  // [ranks][share_of]
@@ -976,7 +1214,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float* at = om + (col0 + 8 * nt + (e & 1)) * C::OP + 16 * i + (lane >> 2) + 8 * (e >> 1);
+            float* at = om + (col0 + 8 * nt + (e & 1)) * C::OP + acc_column<C>(i, lane, e);
             // nothing seen: not even 0 * inf
             const float x = m[nt][e & 1] == -INFINITY ? 0.f : acc[nt][i][e] * f[nt][e & 1];
             *at = round > 0 ? *at + x : x;
@@ -1122,6 +1360,9 @@ fa_paged_join_kernel(const PagedFwdArgs p) {
 // ------------------------------------------------------------------- launch
 inline bool encode_maps(const PagedFwdLaunch& a, int D, CUtensorMap* mk, CUtensorMap* mv) {
   const int page = 1 << a.c.page_shift, piece = page < kPagedTile ? page : kPagedTile;
+  if (a.c.k_scales)
+    return encode_byte_map(mk, a.c.k, D, page, a.c.num_pages * a.c.Hkv, piece) &&
+           encode_byte_map(mv, a.c.v, D, page, a.c.num_pages * a.c.Hkv, piece);
   return encode_tile_map(mk, a.c.k, a.bf16, D, page, a.c.num_pages * a.c.Hkv, piece) &&
          encode_tile_map(mv, a.c.v, a.bf16, D, page, a.c.num_pages * a.c.Hkv, piece);
 }
@@ -1224,14 +1465,15 @@ cudaError_t run_split_tc(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t tiles
   return run_split<C>(a, p, tiles, 1, [&](int64_t parts) { return launch_paged_tc<C>(a, p, parts); });
 }
 
-template <int D, int NT, int RW, bool BF16>
+template <int D, int NT, int RW, bool BF16, bool E8>
 cudaError_t run_paged(const PagedFwdLaunch& a) {
-  using C = PagedCfg<D, NT, RW, BF16, true>;
+  using C = PagedCfg<D, NT, RW, BF16, true, E8>;
   PagedFwdArgs p = {};
   p.c = a.c;
   p.q = a.q; p.o = a.o; p.lse = a.lse;
   p.Hq = a.Hq; p.Tq = a.Tq; p.causal = a.causal;
   p.window = std::min(a.window, 1 << 30);  // positions end below 2^30: a longer window hides nothing either
+  p.sinks = a.window > 0 ? std::min(a.sinks, 1 << 30) : 0;
   p.scale_log2 = a.scale_log2;
   p.new_lens = a.new_lens;
   p.sel = a.sel; p.sel_lens = a.sel_lens; p.n_sel = a.n_sel;
@@ -1241,8 +1483,8 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   // kernels take any)
   const int64_t keys = static_cast<int64_t>(a.sel ? std::min(a.n_sel, a.c.max_pages) : a.c.max_pages) << a.c.page_shift;
   int64_t tiles = paged_tiles(1, keys);
-  if (a.window > 0 && !a.sel)  // window + Tq - 1 keys, wherever they start in a tile
-    tiles = std::min(tiles, (static_cast<int64_t>(a.window) + a.Tq - 2) / kPagedTile + 2);
+  if (a.window > 0 && !a.sel)  // window + Tq - 1 keys, wherever they start in a tile, and the first ones
+    tiles = std::min(tiles, (static_cast<int64_t>(a.window) + a.Tq - 2) / kPagedTile + 2 + paged_tiles(1, p.sinks));
   const int64_t units = static_cast<int64_t>(a.c.B) * a.c.Hkv * p.row_blocks;
   // Short units: a cluster each, joined in the same launch, where all clusters run at
   // once or one CTA does for a unit. Measured: 16 tiles, 4 units 4.6 us against 12.0
@@ -1252,29 +1494,29 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   while (tiles > 2 && ranks < kPagedMaxRanks && ranks < tiles) ranks *= 2;  // 2 tiles: 5.7 us in one CTA, 6.6 in two
   while (ranks > 1 && units > resident_clusters<C>(ranks)) ranks /= 2;
   if (tiles <= C::CLUSTER_TILES * ranks) return launch_paged<C>(a, p, units * ranks, ranks);
-  if constexpr (RW > 1) {  // more than 16 rows
+  if constexpr (RW > 1 && !E8) {  // more than 16 rows
     switch (paged_split_rows(p.rows)) {
       case 32: return run_split_tc<D, 1, BF16>(a, p, tiles);
       case 64: return run_split_tc<D, 2, BF16>(a, p, tiles);
       default: return run_split_tc<D, 4, BF16>(a, p, tiles);
     }
   } else {
-    using S = PagedCfg<D, NT, RW, BF16, false>;
+    using S = PagedCfg<D, NT, RW, BF16, false, E8>;
     return run_split<S>(a, p, tiles, S::CTAS, [&](int64_t parts) { return launch_paged<S>(a, p, parts, 1); });
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool E8 = false>
 cudaError_t run_paged_rows(const PagedFwdLaunch& a) {
   switch (paged_block_rows(a.Hq / a.c.Hkv * a.Tq, D)) {
-    case 8: return run_paged<D, 1, 1, BF16>(a);
-    case 16: return run_paged<D, 2, 1, BF16>(a);
-    case 32: return run_paged<D, 2, 2, BF16>(a);
+    case 8: return run_paged<D, 1, 1, BF16, E8>(a);
+    case 16: return run_paged<D, 2, 1, BF16, E8>(a);
+    case 32: return run_paged<D, 2, 2, BF16, E8>(a);
     case 48:
-      if constexpr (D < 256) return run_paged<D, 3, 2, BF16>(a);
+      if constexpr (D < 256) return run_paged<D, 3, 2, BF16, E8>(a);
       break;
     default:
-      if constexpr (D < 256) return run_paged<D, 4, 2, BF16>(a);
+      if constexpr (D < 256) return run_paged<D, 4, 2, BF16, E8>(a);
   }
   return cudaErrorInvalidValue;
 }
@@ -1285,5 +1527,11 @@ cudaError_t run_paged_rows(const PagedFwdLaunch& a) {
   namespace fa {                                                           \
   cudaError_t launch_paged_fwd_d##DIM(const PagedFwdLaunch& a) {           \
     return a.bf16 ? run_paged_rows<DIM, true>(a) : run_paged_rows<DIM, false>(a); \
+  }                                                                        \
+  }
+#define FA_DEFINE_PAGED8_HEAD_DIM(DIM)                                     \
+  namespace fa {                                                           \
+  cudaError_t launch_paged_fwd8_d##DIM(const PagedFwdLaunch& a) {          \
+    return a.bf16 ? run_paged_rows<DIM, true, true>(a) : run_paged_rows<DIM, false, true>(a); \
   }                                                                        \
   }

@@ -32,7 +32,7 @@ struct PagedFwdLaunch {
   const uint16_t* q;
   uint16_t* o;
   float* lse;
-  int Hq, Tq, causal, window;
+  int Hq, Tq, causal, window, sinks;
   float scale_log2;
   const int* new_lens;
   const int *sel, *sel_lens;
@@ -54,10 +54,15 @@ struct SelectLaunch {
 };
 
 cudaError_t launch_kv_append(const AppendLaunch& a);
+cudaError_t launch_kv_append8(const AppendLaunch& a);  // the cache has scales
 cudaError_t launch_paged_fwd_d64(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd_d96(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd_d128(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd_d256(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd8_d64(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd8_d96(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd8_d128(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd8_d256(const PagedFwdLaunch& a);
 
 // Query rows of a block where a cluster takes a unit: 8 (usual decoding), 16, 32, 48
 // or 64 where a KV head has more, so that its keys are loaded once for all of them

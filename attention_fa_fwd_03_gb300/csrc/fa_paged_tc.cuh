@@ -55,7 +55,8 @@ struct PagedTcCfg {
   // tile's bytes take longer than the softmax's chain
   static constexpr int WGS = D == 256 ? 1 : 2;
   static constexpr int SOFT = 128 * WGS, THREADS = SOFT + 32 * PRODUCERS + 64, SCORE_WARP = 4 * WGS + PRODUCERS;
-  static constexpr int KREG = (D + 63) / 64, REGION = kPagedTile * 128, TILE = KREG * REGION;
+  static constexpr bool E8 = false;
+  static constexpr int COLS = 64, KREG = (D + 63) / 64, REGION = kPagedTile * 128, TILE = KREG * REGION;
   static constexpr int QREGION = 128 * 128;
   static constexpr int STAGES = D == 256 ? 2 : D == 64 ? 8 : 5;
   static constexpr int MC = D == 96 ? 48 : 64;   // columns merged at a time (all at once would cost a stage)
@@ -329,7 +330,8 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int j0 = j0s[q];
-          all_seen &= j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) && !(p.window > 0 && j0 <= p_hi - p.window);
+          all_seen &= j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) &&
+                      !(p.window > 0 && j0 <= p_hi - p.window && j0 + 15 >= p.sinks);
           differ |= n > 1 && j0 < len &&
                     ((p.causal && j0 + 15 > p_lo) ||
                      (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
@@ -348,9 +350,10 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             const int lo = p.window > 0 ? pos - p.window + 1 - j0 : -j0;
             const int hi = (p.causal ? min(len, pos + 1) : len) - j0;
             const unsigned span = static_cast<unsigned>(max(hi - lo, 0));
+            const int keep = min(p.sinks - j0, hi);  // first keys that the window leaves
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (static_cast<unsigned>(e - lo) >= span) sv[16 * q + e] = __float_as_uint(-INFINITY);
+              if (static_cast<unsigned>(e - lo) >= span && e >= keep) sv[16 * q + e] = __float_as_uint(-INFINITY);
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -403,9 +406,9 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           // row and get V = 0 as well.
           const uint32_t vs = sbase + C::OFF_KV + slot * 2 * C::TILE + C::TILE;
           uint8_t* v_rows = smem + (vs - sbase);
-          auto kept = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window); };
+          auto kept = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window && j >= p.sinks); };
           auto partial = [&](int j) {
-            return kept(j) && ((p.causal && j > p_lo) || (p.window > 0 && j <= p_hi - p.window));
+            return kept(j) && ((p.causal && j > p_lo) || (p.window > 0 && j <= p_hi - p.window && j >= p.sinks));
           };
           const int own = key_pos[slot][quarter];
           auto chunk = [&](int i) {  // 16 bytes of this warp's keys
@@ -436,7 +439,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 if (!partial(j)) continue;
                 const float s = __uint_as_float(tmem_ld1(lanes + C::S_COL(b) + key));
                 tmem_ld_wait();
-                const bool seen = !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window);
+                const bool seen = !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window && j >= p.sinks);
                 const float x = ex2((s - top) * p.scale_log2);
 #pragma unroll 1
                 for (int col = 0; col < D; col += 32) {

@@ -40,6 +40,7 @@ FA_WALK_FN int walk_log2(int x) {
 struct ListShape {
   int items, mult;
   int sel, window, page_shift;
+  int sinks;  // first keys that a window does not hide
 };
 
 // What the kernels read of an item, range-checked: keys, and new tokens (0 to 8)
@@ -52,21 +53,27 @@ struct ItemLens {
 struct Item {
   int len, n;  // keys and new tokens
   int listed;  // selected pages
-  int first;   // first tile of the list that holds a visible key
+  int head;    // first tiles of the list, kept for their visible first keys,
+  int skip;    // and tiles behind them that hold no visible key
   int tiles;   // tiles of each unit
+  // place in the list of the unit's tile t
+  FA_WALK_FN int tile(int t) const { return t < head ? t : t + skip; }
 };
 FA_WALK_FN Item make_item(const ListShape& s, const ItemLens& x) {
   Item it;
   it.len = x.len;
   it.n = x.rest & 15;
   it.listed = x.rest >> 4;
-  it.first = 0;
+  it.head = it.skip = 0;
   int keys = it.len;
-  if (s.sel)
+  if (s.sel) {
     keys = it.listed << s.page_shift;  // at most 2^20 entries of 2^8 keys
-  else if (s.window > 0)
-    it.first = walk_max(0, it.len - it.n - s.window + 1) / kPagedTile;
-  it.tiles = it.n > 0 ? (keys + kPagedTile - 1) / kPagedTile - it.first : 0;
+  } else if (s.window > 0) {
+    const int first = walk_max(0, it.len - it.n - s.window + 1) / kPagedTile;
+    it.head = walk_min(first, (s.sinks + kPagedTile - 1) / kPagedTile);
+    it.skip = first - it.head;
+  }
+  it.tiles = it.n > 0 ? (keys + kPagedTile - 1) / kPagedTile - it.skip : 0;
   return it;
 }
 

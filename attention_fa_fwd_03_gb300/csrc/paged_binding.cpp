@@ -1,5 +1,5 @@
 // Python binding of the paged-cache calls (fa_kv_append, fa_paged_fwd,
-// fa_page_select): checks the tensors, makes the device current and calls the C
+// fa_page_select, fa_page_assign): checks the tensors, makes the device current and calls the C
 // ABI on the stream. It holds no arithmetic. The other calls go through ctypes;
 // these are made once per layer and token, where a kernel takes a few
 // microseconds, and ctypes with checks in Python took 8 to 10 of them per call.
@@ -23,8 +23,14 @@ const char kCapsule[] = "attention_fa_fwd_03_gb300.PagedKV";
 
 // What a PagedKV object has checked once.
 struct Handle {
-  fa_paged_kv kv;
+  fa_paged_kv kv;  // with scales: k_bounds and dt are not used
+  float *k_scales, *v_scales;
   int device;
+  bool e4m3() const { return k_scales != nullptr; }
+  fa_paged_kv8 kv8() const {
+    return {kv.k, kv.v, k_scales, v_scales, kv.page_table, kv.kv_lens, kv.B, kv.Hkv, kv.D, kv.num_pages,
+            kv.page_size, kv.max_pages};
+  }
 };
 
 // A Python error is set; carried to the function's end as an exception.
@@ -35,7 +41,14 @@ struct Failed {};
   throw Failed{};
 }
 
-at::ScalarType cache_type(const Handle& h) { return h.kv.dt == FA_BF16 ? at::kBFloat16 : at::kHalf; }
+// Type of a call's keys, values, queries and outputs: the cache's, or, where it is held in
+// 8 bits, that of `t`.
+at::ScalarType call_type(const Handle& h, const at::Tensor& t, const char* name) {
+  if (!h.e4m3()) return h.kv.dt == FA_BF16 ? at::kBFloat16 : at::kHalf;
+  if (t.scalar_type() != at::kHalf && t.scalar_type() != at::kBFloat16) fail(PyExc_ValueError, "%s: fp16 or bf16", name);
+  return t.scalar_type();
+}
+fa_dtype code_of(at::ScalarType t) { return t == at::kBFloat16 ? FA_BF16 : FA_FP16; }
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s: expected a tensor", name);
@@ -59,8 +72,8 @@ int* ints(PyObject* o, const char* name, at::IntArrayRef shape, int device) {
 }
 
 // A [B, H, T, D] view whose innermost index is contiguous.
-void* view(PyObject* o, const char* name, const Handle& h, at::IntArrayRef shape, int64_t* strides) {
-  const at::Tensor& t = checked(o, name, cache_type(h), shape, h.device);
+void* view(PyObject* o, const char* name, const Handle& h, at::ScalarType type, at::IntArrayRef shape, int64_t* strides) {
+  const at::Tensor& t = checked(o, name, type, shape, h.device);
   if (t.stride(3) != 1) fail(PyExc_ValueError, "%s: the innermost index must be contiguous", name);
   // the stride of an index of size 1 is never used and can be anything
   for (int i = 0; i < 3; ++i) strides[i] = shape[i] > 1 ? t.stride(i) : 0;
@@ -149,19 +162,21 @@ PyObject* guarded(Py_ssize_t nargs, Py_ssize_t want, const Body& body) {
   return nullptr;
 }
 
-// handle(k, v, k_bounds, page_table, kv_lens, B, Hkv, D, num_pages, page_size, max_pages, dt, device): addresses
-// (k_bounds 0 for none) and sizes, as the PagedKV class has checked them
+// handle(k, v, k_bounds, page_table, kv_lens, B, Hkv, D, num_pages, page_size, max_pages, dt, device[, k_scales,
+// v_scales]): addresses (k_bounds 0 for none) and sizes, as the PagedKV class has checked them
 PyObject* make_handle(PyObject*, PyObject* args) {
-  unsigned long long k, v, kb, table, lens;
+  unsigned long long k, v, kb, table, lens, ks = 0, vs = 0;
   int B, Hkv, D, num_pages, page_size, max_pages, dt, device;
-  if (!PyArg_ParseTuple(args, "KKKKKiiiiiiii", &k, &v, &kb, &table, &lens, &B, &Hkv, &D, &num_pages, &page_size,
-                        &max_pages, &dt, &device))
+  if (!PyArg_ParseTuple(args, "KKKKKiiiiiiii|KK", &k, &v, &kb, &table, &lens, &B, &Hkv, &D, &num_pages, &page_size,
+                        &max_pages, &dt, &device, &ks, &vs))
     return nullptr;
   Handle* h = new (std::nothrow) Handle;
   if (!h) return PyErr_NoMemory();
   h->kv.k = reinterpret_cast<void*>(k);
   h->kv.v = reinterpret_cast<void*>(v);
   h->kv.k_bounds = reinterpret_cast<void*>(kb);
+  h->k_scales = reinterpret_cast<float*>(ks);
+  h->v_scales = reinterpret_cast<float*>(vs);
   h->kv.page_table = reinterpret_cast<const int*>(table);
   h->kv.kv_lens = reinterpret_cast<const int*>(lens);
   h->kv.B = B;
@@ -187,8 +202,9 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     int64_t ks[3], vs[3], qs[3] = {0, 0, 0};
     const at::Tensor& k0 = tensor(a[1], "k");
     const int64_t T = k0.dim() == 4 ? k0.size(2) : 0;
-    const void* k = view(a[1], "k", h, {c.B, c.Hkv, T, c.D}, ks);
-    const void* v = view(a[2], "v", h, {c.B, c.Hkv, T, c.D}, vs);
+    const at::ScalarType type = call_type(h, k0, "k");
+    const void* k = view(a[1], "k", h, type, {c.B, c.Hkv, T, c.D}, ks);
+    const void* v = view(a[2], "v", h, type, {c.B, c.Hkv, T, c.D}, vs);
     if ((a[6] == Py_None) != (a[7] == Py_None)) fail(PyExc_ValueError, "%s go together", "q and q_out");
     const void* q = nullptr;
     void* q_out = nullptr;
@@ -196,8 +212,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (a[6] != Py_None) {
       const at::Tensor& q0 = tensor(a[6], "q");
       Hq = q0.dim() == 4 ? q0.size(1) : 0;
-      q = view(a[6], "q", h, {c.B, Hq, T, c.D}, qs);
-      q_out = address(a[7], "q_out", cache_type(h), {c.B, Hq, T, c.D}, h.device);
+      q = view(a[6], "q", h, type, {c.B, Hq, T, c.D}, qs);
+      q_out = address(a[7], "q_out", type, {c.B, Hq, T, c.D}, h.device);
     }
     if ((a[3] == Py_None) != (a[4] == Py_None)) fail(PyExc_ValueError, "%s go together", "cos and sin");
     const float *cs = nullptr, *sn = nullptr;
@@ -216,26 +232,32 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const int n_heads = dim(Hq, "q"), n_tokens = dim(T, "k"), n_pos = dim(positions, "cos"), rot = dim(2 * half, "cos");
     const OnDevice on(h.device);
     const Unlocked unlocked;
+    if (h.e4m3()) {
+      const fa_paged_kv8 c8 = h.kv8();
+      return fa_kv_append8(&c8, k, ks, v, vs, q, qs, q_out, n_heads, n_tokens, new_lens, cs, sn, n_pos, rot, interleaved,
+                           code_of(type), stream);
+    }
     return fa_kv_append(&c, k, ks, v, vs, q, qs, q_out, n_heads, n_tokens, new_lens, cs, sn, n_pos, rot, interleaved, stream);
   });
 }
 
-// paged_fwd(handle, q, o, lse, scale, causal, window, new_lens, sel, sel_lens, workspace, stream)
+// paged_fwd(handle, q, o, lse, scale, causal, window, new_lens, sel, sel_lens, workspace, stream[, sinks])
 PyObject* paged_fwd(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  return guarded(nargs, 12, [&] {
+  return guarded(nargs, nargs == 13 ? 13 : 12, [&] {
     const Handle& h = handle_of(a[0]);
     const fa_paged_kv& c = h.kv;
     size_t ws_bytes = 0;
     void* ws = workspace(a[10], "fa_paged_fwd", h.device, &ws_bytes);
     const at::Tensor& q0 = tensor(a[1], "q");
     const int64_t Hq = q0.dim() == 4 ? q0.size(1) : 0, Tq = q0.dim() == 4 ? q0.size(2) : 0;
-    const void* q = address(a[1], "q", cache_type(h), {c.B, Hq, Tq, c.D}, h.device);
-    void* o = address(a[2], "o", cache_type(h), {c.B, Hq, Tq, c.D}, h.device);
+    const at::ScalarType type = call_type(h, q0, "q");
+    const void* q = address(a[1], "q", type, {c.B, Hq, Tq, c.D}, h.device);
+    void* o = address(a[2], "o", type, {c.B, Hq, Tq, c.D}, h.device);
     void* lse = address(a[3], "lse", at::kFloat, {c.B, Hq, Tq}, h.device);
     const double scale = PyFloat_AsDouble(a[4]);
     if (scale == -1.0 && PyErr_Occurred()) throw Failed{};
     const bool causal = truth(a[5]);
-    const int window = integer(a[6], "window");
+    const int window = integer(a[6], "window"), sinks = nargs > 12 ? integer(a[12], "sinks") : 0;
     const int* new_lens = ints(a[7], "new_lens", {c.B}, h.device);
     if ((a[8] == Py_None) != (a[9] == Py_None)) fail(PyExc_ValueError, "%s go together", "sel and sel_lens");
     int64_t n_sel = 0;
@@ -249,8 +271,13 @@ PyObject* paged_fwd(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const int n_heads = dim(Hq, "q"), n_tokens = dim(Tq, "q"), n_pages = dim(n_sel, "sel");
     const OnDevice on(h.device);
     const Unlocked unlocked;
-    return fa_paged_fwd(&c, q, o, static_cast<float*>(lse), n_heads, n_tokens, static_cast<float>(scale), causal, window,
-                        new_lens, sel, sel_lens, n_pages, ws, ws_bytes, stream);
+    if (h.e4m3()) {
+      const fa_paged_kv8 c8 = h.kv8();
+      return fa_paged_fwd8(&c8, q, o, static_cast<float*>(lse), n_heads, n_tokens, static_cast<float>(scale), causal, window,
+                           sinks, new_lens, sel, sel_lens, n_pages, code_of(type), ws, ws_bytes, stream);
+    }
+    return fa_paged_fwd_sinks(&c, q, o, static_cast<float*>(lse), n_heads, n_tokens, static_cast<float>(scale), causal, window,
+                              sinks, new_lens, sel, sel_lens, n_pages, ws, ws_bytes, stream);
   });
 }
 
@@ -263,7 +290,8 @@ PyObject* page_select(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     void* ws = workspace(a[6], "fa_page_select", h.device, &ws_bytes);
     const at::Tensor &q0 = tensor(a[1], "q"), &s0 = tensor(a[2], "sel");
     const int64_t Hq = q0.dim() == 4 ? q0.size(1) : 0, n_sel = s0.dim() == 3 ? s0.size(2) : 0;
-    const void* q = address(a[1], "q", cache_type(h), {c.B, Hq, 1, c.D}, h.device);
+    if (h.e4m3()) return FA_ERR_INVALID_ARG;  // it keeps no bounds
+    const void* q = address(a[1], "q", call_type(h, q0, "q"), {c.B, Hq, 1, c.D}, h.device);
     int* sel = static_cast<int*>(address(a[2], "sel", at::kInt, {c.B, c.Hkv, n_sel}, h.device));
     int* sel_lens = static_cast<int*>(address(a[3], "sel_lens", at::kInt, {c.B, c.Hkv}, h.device));
     const int first = integer(a[4], "keep_first"), last = integer(a[5], "keep_last");
@@ -275,11 +303,37 @@ PyObject* page_select(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   });
 }
 
+// page_assign(page_table, kv_lens, held, free_pages, free_count, page_size, T, new_lens, window, sinks, slots, stream)
+PyObject* page_assign(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 12, [&] {
+    const at::Tensor &table = tensor(a[0], "page_table"), &pages = tensor(a[3], "free_pages");
+    if (table.dim() != 2 || pages.dim() != 1) fail(PyExc_ValueError, "%s [B, max_pages], free_pages [num_pages]", "page_table");
+    if (!table.is_cuda()) fail(PyExc_ValueError, "%s: not on a CUDA device", "page_table");
+    const int device = table.get_device();
+    const int64_t B = table.size(0), max_pages = table.size(1), num_pages = pages.size(0);
+    int* t = static_cast<int*>(address(a[0], "page_table", at::kInt, {B, max_pages}, device));
+    const int* lens = static_cast<int*>(address(a[1], "kv_lens", at::kInt, {B}, device));
+    int* held = static_cast<int*>(address(a[2], "held", at::kInt, {B, 3}, device));
+    int* stack = static_cast<int*>(address(a[3], "free_pages", at::kInt, {num_pages}, device));
+    int* count = static_cast<int*>(address(a[4], "free_count", at::kInt, {2}, device));
+    const int page_size = integer(a[5], "page_size"), T = integer(a[6], "T");
+    const int* new_lens = ints(a[7], "new_lens", {B}, device);
+    const int window = integer(a[8], "window"), sinks = integer(a[9], "sinks");
+    int64_t* slots = a[10] == Py_None ? nullptr : static_cast<int64_t*>(address(a[10], "slots", at::kLong, {B, T}, device));
+    const cudaStream_t stream = stream_of(a[11], device);
+    const int nb = dim(B, "page_table"), np = dim(num_pages, "free_pages"), mp = dim(max_pages, "page_table");
+    const OnDevice on(device);
+    const Unlocked unlocked;
+    return fa_page_assign(t, lens, held, stack, count, nb, np, page_size, mp, T, new_lens, window, sinks, slots, stream);
+  });
+}
+
 PyMethodDef kMethods[] = {
     {"handle", make_handle, METH_VARARGS, nullptr},
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL, nullptr},
     {"paged_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_fwd)), METH_FASTCALL, nullptr},
     {"page_select", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(page_select)), METH_FASTCALL, nullptr},
+    {"page_assign", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(page_assign)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_paged", "Binding of the paged-cache calls.", -1, kMethods,

@@ -283,6 +283,89 @@ fa_status fa_paged_fwd(const fa_paged_kv* kv, const void* q, void* o, float* lse
                        const int* sel_lens, int n_sel, void* workspace, size_t workspace_bytes,
                        cudaStream_t stream);
 
+/* fa_paged_fwd with first keys that the window does not hide: a key j is hidden
+ * from the query at position p when
+ *     (causal && j > p)  or  (window > 0 && p >= j && p - j >= window && j >= sinks)
+ * sinks >= 0; without a window it has no effect. Only pages that hold a key which
+ * the window or the first keys show are read (where no pages are selected), so the
+ * table may hold -1 for the others, as where fa_page_assign has given them back.
+ * sinks = 0 is fa_paged_fwd. */
+fa_status fa_paged_fwd_sinks(const fa_paged_kv* kv, const void* q, void* o, float* lse, int Hq, int Tq,
+                             float scale, int causal, int window, int sinks, const int* new_lens,
+                             const int* sel, const int* sel_lens, int n_sel, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/* The cache held in 8 bits: e4m3 (4 exponent and 3 mantissa bits, no infinities, largest
+ * number 448). k and v are [num_pages, Hkv, page_size, D] bytes; k_scales and
+ * v_scales are fp32 [num_pages, Hkv]: a held value stands for itself times its page's and
+ * head's scale, a power of two from 2^-126 on. Everything else is as in fa_paged_kv. */
+typedef struct {
+  void* k;               /* [num_pages, Hkv, page_size, D] e4m3 */
+  void* v;               /* [num_pages, Hkv, page_size, D] e4m3 */
+  float* k_scales;       /* [num_pages, Hkv] */
+  float* v_scales;       /* [num_pages, Hkv] */
+  const int* page_table; /* [B, max_pages] */
+  const int* kv_lens;    /* [B] */
+  int B, Hkv, D, num_pages, page_size, max_pages;
+} fa_paged_kv8;
+
+/* fa_kv_append into a cache of 8 bits: new keys, values and queries of type dt. For each
+ * page that receives tokens, KV head, and keys and values apart:
+ *   s = the least power of two, 2^-126 or above, with |x| <= 448 s for every finite
+ *       element x of the call's new rows in the page (of keys: rotated, in fp32),
+ *   and at least the page's old scale unless the page's slot 0 is among the new rows.
+ * New rows are held as x / s, rounded once; a NaN or an infinity is held as NaN. Where s is
+ * more than the old scale, the page's rows below the first new one are held anew, their
+ * values as before but for those below 2^-6 s, which are rounded to multiples of 2^-9 s.
+ * Nothing else of the pools and scales is touched. Argument rules of fa_kv_append. */
+fa_status fa_kv_append8(const fa_paged_kv8* kv, const void* k_new, const int64_t* k_strides,
+                        const void* v_new, const int64_t* v_strides, const void* q,
+                        const int64_t* q_strides, void* q_out, int Hq, int T, const int* new_lens,
+                        const float* cos_table, const float* sin_table, int rope_len, int rot_dim,
+                        int interleaved, fa_dtype dt, cudaStream_t stream);
+
+/* fa_paged_fwd_sinks over a cache of 8 bits: q and o of type dt; keys and values are the
+ * numbers that the cache stands for. Workspace and rules of fa_paged_fwd; a scale that
+ * fa_kv_append8 would not write (0, negative, no power of two, infinite or NaN) gives
+ * undefined rows. */
+fa_status fa_paged_fwd8(const fa_paged_kv8* kv, const void* q, void* o, float* lse, int Hq, int Tq,
+                        float scale, int causal, int window, int sinks, const int* new_lens,
+                        const int* sel, const int* sel_lens, int n_sel, fa_dtype dt, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
+
+/* Page tables of a batch from its lengths: the step's new tokens get pool pages, and pages
+ * that no query of this step or a later one sees go back to the pool.
+ *   page_table [B, max_pages], written: entries that get a page, and -1 where one is
+ *     given back or none was left; others keep what they hold.
+ *   kv_lens [B]: keys of each sequence, the step's new tokens (new_lens[b], or T) among them.
+ *   held [B, 3]: per sequence (head, first, end): it holds a pool page for its pages
+ *     [0, head) and [first, end), 0 <= head <= first <= end <= max_pages. Kept from
+ *     call to call; zeros for a sequence that holds none.
+ *   free_pages [num_pages], free_count [2]: a stack of the free pool pages, the first
+ *     free_count[0] entries. free_count[1] is written: how many pages were wanted and
+ *     not there.
+ *   slots [B, T] int64 or null: for each new token the place of its row among those of the
+ *     pool seen as [num_pages * page_size] rows, page_table entry * page_size + slot, or -1
+ *     for padding and where there is no page.
+ * A sequence wants its pages [0, end), end = ceil(kv_lens / page_size); with a window only
+ * those of the first `sinks` keys and those from the page of the first key on that the
+ * window shows to its first new token (position kv_lens - n), max(0, kv_lens - n - window + 1).
+ * What was given back does not come again (while held has a gap between head and
+ * first, neither grows into it). Pages held but not wanted are pushed to the stack,
+ * sequence by sequence in ascending order; then wanted pages not held are popped from
+ * it in the same order. Where it runs out the rest get none: those sequences hold the
+ * lowest of what they want, and ask again in the next call.
+ * To end a sequence give it kv_lens[b] = 0 for one call, which returns all its pages.
+ * Lengths, counts and states out of range raise FA_ERR_BAD_INDEX's bit and are clamped; so
+ * does a table entry given back that is no pool page, which goes to the stack as -1.
+ * B <= 65536, num_pages <= 2^30, max_pages * page_size <= 2^30, 1 <= T <= 2^22,
+ * B * T < 2^31, B * max_pages < 2^31; slots 8-byte aligned, the others 4-byte aligned; outputs
+ * meet nothing else. The result does not depend on what else runs.
+ * One or two kernel launches. Returns FA_OK or an error code (nothing launched on error). */
+fa_status fa_page_assign(int* page_table, const int* kv_lens, int* held, int* free_pages, int* free_count,
+                         int B, int num_pages, int page_size, int max_pages, int T, const int* new_lens,
+                         int window, int sinks, int64_t* slots, cudaStream_t stream);
+
 /* Bytes of device workspace fa_page_select needs. Returns 0 for sizes it
  * refuses. */
 size_t fa_page_select_workspace_size(int B, int Hkv, int max_pages);
