@@ -30,7 +30,7 @@ import os
 import threading
 
 __all__ = ["FA_FP16", "FA_BF16", "FaError", "fa_fwd", "fa_bwd", "fa_bwd_preprocess", "fa_bwd_dkv",
-           "fa_bwd_dq", "fa_bwd_workspace_size",
+           "fa_bwd_dq", "fa_bwd_workspace_size", "fa_bwd_sinks_workspace_size",
            "PagedKV", "fa_kv_append", "fa_paged_fwd", "fa_paged_workspace_size", "fa_page_select",
            "fa_page_select_workspace_size", "fa_page_assign",
            "fa_status_string", "fa_device_status", "fa_abi_version", "fa_selftest_wait_timeout",
@@ -91,6 +91,13 @@ def library():
         lib.fa_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i,
                                vp, sz, vp]
         lib.fa_bwd.restype = i
+        lib.fa_fwd_sinks.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i, i, vp]
+        lib.fa_fwd_sinks.restype = i
+        lib.fa_bwd_sinks.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i,
+                                     i, vp, sz, vp]
+        lib.fa_bwd_sinks.restype = i
+        lib.fa_bwd_sinks_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+        lib.fa_bwd_sinks_workspace_size.restype = sz
         lib.fa_bwd_preprocess.argtypes = [vp, vp, vp, i, i, i, i, i, vp]
         lib.fa_bwd_preprocess.restype = i
         lib.fa_bwd_dkv.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i,
@@ -186,12 +193,23 @@ def fa_bwd_workspace_size(B: int, Hq: int, Tq: int) -> int:
     return int(library().fa_bwd_workspace_size(B, Hq, Tq))
 
 
+def fa_bwd_sinks_workspace_size(B: int, Hq: int, Hkv: int, Tq: int, Tkv: int, D: int, window: int, sinks: int) -> int:
+    return int(library().fa_bwd_sinks_workspace_size(B, Hq, Hkv, Tq, Tkv, D, window, sinks))
+
+
 def fa_fwd(q, k, v, o, lse, scale: float, causal: bool = False, window: int = 0,
-           stream=None) -> None:
+           stream=None, sinks: int = 0) -> None:
     """O and LSE for q [B,Hq,Tq,D], k/v [B,Hkv,Tkv,D] (fp16 or bf16, contiguous,
-    on the GPU); o [B,Hq,Tq,D] same dtype, lse [B,Hq,Tq] fp32 are written."""
+    on the GPU); o [B,Hq,Tq,D] same dtype, lse [B,Hq,Tq] fp32 are written. The
+    first ``sinks`` keys stay visible behind a window."""
     B, Hq, Tq, D = q.shape
     Hkv, Tkv = k.shape[1], k.shape[2]
+    if sinks:
+        st = library().fa_fwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Tq, Tkv, D,
+                                    float(scale), int(bool(causal)), int(window), int(sinks), _dtype_code(q),
+                                    _stream(stream))
+        _check(st, "fa_fwd")
+        return
     st = library().fa_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Tq, Tkv, D,
                           float(scale), int(bool(causal)), int(window), _dtype_code(q),
                           _stream(stream))
@@ -199,14 +217,22 @@ def fa_fwd(q, k, v, o, lse, scale: float, causal: bool = False, window: int = 0,
 
 
 def fa_bwd(q, k, v, o, do, lse, dq, dk, dv, scale: float, causal: bool = False,
-           window: int = 0, workspace=None, stream=None) -> None:
+           window: int = 0, workspace=None, stream=None, sinks: int = 0) -> None:
     """dQ, dK, dV for the forward that produced o and lse. ``workspace`` is a
-    device tensor of at least fa_bwd_workspace_size(B, Hq, Tq) bytes."""
+    device tensor of at least fa_bwd_workspace_size(B, Hq, Tq) bytes, with
+    ``sinks`` fa_bwd_sinks_workspace_size(B, Hq, Hkv, Tq, Tkv, D, window, sinks)."""
     B, Hq, Tq, D = q.shape
     Hkv, Tkv = k.shape[1], k.shape[2]
     if workspace is None:
         raise ValueError("fa_bwd needs a workspace tensor (the library never allocates)")
     nbytes = workspace.numel() * workspace.element_size()
+    if sinks:
+        st = library().fa_bwd_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
+                                    _ptr(dk), _ptr(dv), B, Hq, Hkv, Tq, Tkv, D, float(scale),
+                                    int(bool(causal)), int(window), int(sinks), _dtype_code(q), _ptr(workspace),
+                                    nbytes, _stream(stream))
+        _check(st, "fa_bwd")
+        return
     st = library().fa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
                           _ptr(dk), _ptr(dv), B, Hq, Hkv, Tq, Tkv, D, float(scale),
                           int(bool(causal)), int(window), _dtype_code(q), _ptr(workspace),

@@ -23,46 +23,49 @@ import math
 
 import torch
 
-from . import fa_bwd, fa_bwd_workspace_size, fa_fwd
+from . import fa_bwd, fa_bwd_sinks_workspace_size, fa_bwd_workspace_size, fa_fwd
 
 __all__ = ["FlashAttention", "flash_attention"]
 
 
 class FlashAttention(torch.autograd.Function):
-    """(q, k, v, scale, causal, window) -> (O, LSE); gradients for q, k, v only."""
+    """(q, k, v, scale, causal, window[, sinks]) -> (O, LSE); gradients for q, k, v only."""
 
     @staticmethod
-    def forward(ctx, q, k, v, scale: float, causal: bool, window: int):
+    def forward(ctx, q, k, v, scale: float, causal: bool, window: int, sinks: int = 0):
         with torch.cuda.device(q.device):
             o = torch.empty_like(q)
             lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-            fa_fwd(q, k, v, o, lse, scale, causal, window)
+            fa_fwd(q, k, v, o, lse, scale, causal, window, sinks=sinks)
         ctx.save_for_backward(q, k, v, o, lse)
-        ctx.attn = (scale, causal, window)
+        ctx.attn = (scale, causal, window, sinks)
         ctx.mark_non_differentiable(lse)
         return o, lse
 
     @staticmethod
     def backward(ctx, do, _dlse):
         q, k, v, o, lse = ctx.saved_tensors
-        scale, causal, window = ctx.attn
+        scale, causal, window, sinks = ctx.attn
         with torch.cuda.device(q.device):
             do = do.contiguous()
             dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-            ws = torch.empty(fa_bwd_workspace_size(*q.shape[:3]), dtype=torch.uint8,
-                             device=q.device)
-            fa_bwd(q, k, v, o, do, lse, dq, dk, dv, scale, causal, window, workspace=ws)
-        return dq, dk, dv, None, None, None
+            B, Hq, Tq, D = q.shape
+            size = (fa_bwd_sinks_workspace_size(B, Hq, k.shape[1], Tq, k.shape[2], D, window, sinks) if sinks
+                    else fa_bwd_workspace_size(B, Hq, Tq))
+            ws = torch.empty(size, dtype=torch.uint8, device=q.device)
+            fa_bwd(q, k, v, o, do, lse, dq, dk, dv, scale, causal, window, workspace=ws, sinks=sinks)
+        return dq, dk, dv, None, None, None, None
 
 
 def flash_attention(q, k, v, scale: float | None = None, causal: bool = False, window: int = 0,
-                    return_lse: bool = False):
+                    return_lse: bool = False, sinks: int = 0):
     """Exact attention O = softmax(s Q K^T + mask) V with a backward pass.
 
     q [B,Hq,Tq,D], k and v [B,Hkv,Tkv,D] on one CUDA device, fp16 or bf16,
     Hq a multiple of Hkv (query head h reads KV head h // (Hq // Hkv)).
     ``scale`` defaults to 1/sqrt(D). ``causal`` masks keys after the query
-    (top-left aligned); ``window`` W > 0 masks past keys with q - k >= W.
+    (top-left aligned); ``window`` W > 0 masks past keys with q - k >= W, but for
+    the first ``sinks`` keys, which stay visible.
     Non-contiguous inputs are copied to contiguous ones first. With
     ``return_lse`` the natural-log LSE [B,Hq,Tq] (fp32, no gradient) is
     returned beside O.
@@ -70,5 +73,5 @@ def flash_attention(q, k, v, scale: float | None = None, causal: bool = False, w
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     q, k, v = (t.contiguous() for t in (q, k, v))
-    o, lse = FlashAttention.apply(q, k, v, float(scale), bool(causal), int(window))
+    o, lse = FlashAttention.apply(q, k, v, float(scale), bool(causal), int(window), int(sinks))
     return (o, lse) if return_lse else o

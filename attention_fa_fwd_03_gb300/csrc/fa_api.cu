@@ -6,6 +6,7 @@
 // "R/ag_flash_attn.R" (ggmlR), the f32-only backward note: an abort inside the
 // library took the whole session down, so every shape error is reported to
 // the caller instead).
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -116,6 +117,39 @@ AttnShape make_shape(int B, int Hq, int Hkv, int Tq, int Tkv, int causal, int wi
   s.causal = causal; s.window = window;
   s.scale_log2 = scale * kLog2e;
   return s;
+}
+
+// A window with `sinks` first keys that stay visible. Key j is hidden from query i where
+// j >= sinks and j <= i - window: from no query below Tq unless sinks < Tq - window, and
+// there are such keys only if sinks < Tkv. What hides nothing is taken away, so that such
+// calls run as those without a mask (or with the causal one alone) do.
+void drop_idle_window(int Tq, int Tkv, int* window, int* sinks) {
+  if (*sinks == 0) return;
+  if (*window == 0 || static_cast<int64_t>(*sinks) + *window >= Tq || *sinks >= Tkv) *window = *sinks = 0;
+}
+
+// How the dK/dV kernel shares the blocks of first keys. Each sees all Tq queries behind
+// it where the other blocks see a window's, and would be the last item to end: it is cut into
+// items of a window's query tiles, but not into smaller ones than half of what a CTA has to
+// do in all. (B1 Hq16 Hkv2 T16384 D128, window 4096: 1024 tiles in one item against 264, in all
+// 444 per SM.)
+SinkParts sink_parts(int B, int Hq, int Hkv, int Tq, int Tkv, int D, int window, int sinks) {
+  SinkParts p;
+  if (sinks == 0) return p;
+  auto blocks = [](int64_t n) { return (n + kBM - 1) / kBM; };
+  constexpr int kSms = 152;  // of a GB300: the workspace does not depend on the device
+  const int64_t ctas = D == 256 ? kSms / 2 : kSms;
+  const int64_t reps = Hq / Hkv, all = blocks(Tq), win = std::min(all, blocks(window) + 1);
+  p.blocks = static_cast<int>(blocks(sinks));
+  const int64_t rest = std::max<int64_t>(0, blocks(Tkv) - p.blocks);
+  const int64_t total = static_cast<int64_t>(B) * Hq * (p.blocks * all + rest * win);
+  const int64_t target = std::max(reps * win, total / (2 * ctas));
+  p.parts = static_cast<int>(std::min<int64_t>(64, (reps * all + target - 1) / target));
+  return p;
+}
+size_t sink_sums_bytes(const SinkParts& p, int B, int Hkv, int D) {
+  if (p.parts == 1) return 0;
+  return static_cast<size_t>(B) * Hkv * p.blocks * p.parts * 2 * kBM * D * 4;
 }
 
 }  // namespace
@@ -237,9 +271,20 @@ size_t fa_bwd_workspace_size(int B, int Hq, int Tq) {
   return (bytes + 255) / 256 * 256;
 }
 
-fa_status fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
-                 int Hkv, int Tq, int Tkv, int D, float scale, int causal, int window,
-                 fa_dtype dt, cudaStream_t stream) {
+size_t fa_bwd_sinks_workspace_size(int B, int Hq, int Hkv, int Tq, int Tkv, int D, int window, int sinks) {
+  if (check_common(B, Hq, Hkv, Tq, Tkv, D, 1.f, 0, window, FA_FP16) != FA_OK || sinks < 0) return 0;
+  drop_idle_window(Tq, Tkv, &window, &sinks);
+  return fa_bwd_workspace_size(B, Hq, Tq) +
+         sink_sums_bytes(sink_parts(B, Hq, Hkv, Tq, Tkv, D, window, sinks), B, Hkv, D);
+}
+
+}  // extern "C"
+
+namespace {
+
+fa_status fwd_common(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                     int Hkv, int Tq, int Tkv, int D, float scale, int causal, int window, int sinks,
+                     fa_dtype dt, cudaStream_t stream) {
   fa_status st = check_common(B, Hq, Hkv, Tq, Tkv, D, scale, causal, window, dt);
   if (st != FA_OK) return st;
   if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
@@ -252,23 +297,42 @@ fa_status fa_fwd(const void* q, const void* k, const void* v, void* o, float* ls
       overlap(lse, nl, q, nq) || overlap(lse, nl, k, nkv) || overlap(lse, nl, v, nkv) ||
       overlap(lse, nl, o, nq))
     return FA_ERR_INVALID_ARG;
+  if (sinks < 0) return FA_ERR_INVALID_ARG;
+  drop_idle_window(Tq, Tkv, &window, &sinks);
   FwdLaunch a;
   a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
   int hq = Hq, tq = Tq;  // short query blocks keep the split-key kernel
   fold_group_rows(causal, window, Hkv, kDecodeMaxTq, &hq, &tq);
   a.s = make_shape(B, hq, Hkv, tq, Tkv, causal, window, scale);
+  a.s.sinks = sinks;
   a.bf16 = dt == FA_BF16;
   if (!status_ptr(&a.wc.status)) return FA_ERR_LAUNCH;
   set_waits(&a.wc);
   a.stream = stream;
   cudaError_t e;
   switch (D) {
-    case 64: e = launch_fwd_d64(a); break;
-    case 96: e = launch_fwd_d96(a); break;
-    case 128: e = launch_fwd_d128(a); break;
-    default: e = launch_fwd_d256(a); break;
+    case 64: e = sinks ? launch_fwd_sinks_d64(a) : launch_fwd_d64(a); break;
+    case 96: e = sinks ? launch_fwd_sinks_d96(a) : launch_fwd_d96(a); break;
+    case 128: e = sinks ? launch_fwd_sinks_d128(a) : launch_fwd_d128(a); break;
+    default: e = sinks ? launch_fwd_sinks_d256(a) : launch_fwd_d256(a); break;
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                 int Hkv, int Tq, int Tkv, int D, float scale, int causal, int window,
+                 fa_dtype dt, cudaStream_t stream) {
+  return fwd_common(q, k, v, o, lse, B, Hq, Hkv, Tq, Tkv, D, scale, causal, window, 0, dt, stream);
+}
+
+fa_status fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                       int Hkv, int Tq, int Tkv, int D, float scale, int causal, int window, int sinks,
+                       fa_dtype dt, cudaStream_t stream) {
+  return fwd_common(q, k, v, o, lse, B, Hq, Hkv, Tq, Tkv, D, scale, causal, window, sinks, dt, stream);
 }
 
 }  // extern "C"
@@ -280,7 +344,7 @@ namespace {
 fa_status bwd_common(const void* q, const void* k, const void* v, const void* o, const void* dO,
                      const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
                      int Tq, int Tkv, int D, float scale, int causal, int window, fa_dtype dt,
-                     void* dvec, size_t dvec_bytes, cudaStream_t stream, int phases) {
+                     void* dvec, size_t dvec_bytes, cudaStream_t stream, int phases, int sinks = 0) {
   fa_status st = check_common(B, Hq, Hkv, Tq, Tkv, D, scale, causal, window, dt);
   if (st != FA_OK) return st;
   const bool pre = phases & kPhaseDvec, dkv = phases & kPhaseDkv, dqp = phases & kPhaseDq;
@@ -290,7 +354,11 @@ fa_status bwd_common(const void* q, const void* k, const void* v, const void* o,
   if (need_qkv && (!q || !k || !v || !lse)) return FA_ERR_INVALID_ARG;
   if (dkv && (!dk || !dv)) return FA_ERR_INVALID_ARG;
   if (dqp && !dq) return FA_ERR_INVALID_ARG;
-  if (dvec_bytes < fa_bwd_workspace_size(B, Hq, Tq)) return FA_ERR_INVALID_ARG;
+  if (sinks < 0) return FA_ERR_INVALID_ARG;
+  if (dvec_bytes < (sinks ? fa_bwd_sinks_workspace_size(B, Hq, Hkv, Tq, Tkv, D, window, sinks)
+                          : fa_bwd_workspace_size(B, Hq, Tq)))
+    return FA_ERR_INVALID_ARG;
+  drop_idle_window(Tq, Tkv, &window, &sinks);
   const void* all[10] = {q, k, v, o, dO, lse, dq, dk, dv, dvec};
   for (const void* p : all)
     if (p && !aligned16(p)) return FA_ERR_MISALIGNED;
@@ -319,16 +387,19 @@ fa_status bwd_common(const void* q, const void* k, const void* v, const void* o,
   fold_group_rows(causal, window, Hkv, 0, &hq, &tq);
   a.s = make_shape(B, hq, Hkv, tq, Tkv, causal, window, scale);
   a.s_rows = make_shape(B, Hq, Hkv, Tq, Tkv, causal, window, scale);
+  a.s.sinks = a.s_rows.sinks = sinks;
+  a.sink_parts = sink_parts(B, Hq, Hkv, Tq, Tkv, D, window, sinks);
+  a.sink_parts.partial = reinterpret_cast<float*>(static_cast<char*>(dvec) + fa_bwd_workspace_size(B, Hq, Tq));
   a.bf16 = dt == FA_BF16;
   if (!status_ptr(&a.wc.status)) return FA_ERR_LAUNCH;
   set_waits(&a.wc);
   a.stream = stream;
   cudaError_t e;
   switch (D) {
-    case 64: e = launch_bwd_d64(a, phases); break;
-    case 96: e = launch_bwd_d96(a, phases); break;
-    case 128: e = launch_bwd_d128(a, phases); break;
-    default: e = launch_bwd_d256(a, phases); break;
+    case 64: e = sinks ? launch_bwd_sinks_d64(a) : launch_bwd_d64(a, phases); break;
+    case 96: e = sinks ? launch_bwd_sinks_d96(a) : launch_bwd_d96(a, phases); break;
+    case 128: e = sinks ? launch_bwd_sinks_d128(a) : launch_bwd_d128(a, phases); break;
+    default: e = sinks ? launch_bwd_sinks_d256(a) : launch_bwd_d256(a, phases); break;
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
@@ -348,6 +419,17 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
   }
   return bwd_common(q, k, v, o, dO, lse, dq, dk, dv, B, Hq, Hkv, Tq, Tkv, D, scale, causal,
                     window, dt, workspace, workspace_bytes, stream, kPhaseAll);
+}
+
+fa_status fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                       const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Tq,
+                       int Tkv, int D, float scale, int causal, int window, int sinks, fa_dtype dt,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  fa_status st = check_common(B, Hq, Hkv, Tq, Tkv, D, scale, causal, window, dt);
+  if (st != FA_OK) return st;
+  if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv || !workspace) return FA_ERR_INVALID_ARG;
+  return bwd_common(q, k, v, o, dO, lse, dq, dk, dv, B, Hq, Hkv, Tq, Tkv, D, scale, causal,
+                    window, dt, workspace, workspace_bytes, stream, kPhaseAll, sinks);
 }
 
 fa_status fa_bwd_preprocess(const void* o, const void* dO, float* dvec, int B, int Hq, int Tq,

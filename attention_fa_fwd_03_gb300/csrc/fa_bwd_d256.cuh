@@ -60,8 +60,10 @@
 
 namespace fa {
 
-template <bool BF16_, int HALVES_ = 1>
+template <bool BF16_, int HALVES_ = 1, bool SINKS_ = false>
 struct DkvPairCfg {
+  static constexpr bool SINKS = SINKS_;
+  static_assert(!(SINKS_ && HALVES_ > 1), "blocks of first keys are cut into items instead");
   static constexpr int D = 256;
   static constexpr bool BF16 = BF16_;
   static constexpr int HALVES = HALVES_;        // pairs sharing a block's query tiles
@@ -112,7 +114,7 @@ fa_bwd_dkv_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                        const void* __restrict__ k_rows, const void* __restrict__ v_rows,
                        const float* __restrict__ lse, const float* __restrict__ dvec,
                        void* __restrict__ dk_out, void* __restrict__ dv_out, float scale,
-                       AttnShape s, TileOrder order, WaitCfg wc) {
+                       AttnShape s, TileOrder order, WaitCfg wc, SinkParts sp) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const uint32_t rank = cluster_ctarank();   // even: P side, odd: dS side
@@ -128,8 +130,8 @@ fa_bwd_dkv_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
   float* stats = reinterpret_cast<float*>(smem + C::OFF_STATS);
   const uint64_t tmo = wc.timeout_cycles;
   const int reps = s.Hq / s.Hkv;
-  const DkvItem t = dkv_item(static_cast<int>(blockIdx.x) / C::CLUSTER, order, s, C::BMQ,
-                             C::HALVES, pair);
+  const DkvItem t = dkv_item<C::SINKS>(static_cast<int>(blockIdx.x) / C::CLUSTER, order, s, C::BMQ,
+                                       C::HALVES, pair, sp);
   const int n = t.n_iter;
   const bool aligned = (sbase & 1023u) == 0;  // the 128-byte swizzle needs it
 
@@ -363,9 +365,13 @@ fa_bwd_dkv_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
       const float* st_row = stats + slot * C::BMQ + wg * 32;
       if (pside) {
         // P^T = 2^(S^T scale log2 e - LSE log2 e), masked entries 0
-        if (!block_unmasked(s, i0, i0 + C::BMQ, t.k0, t.k0 + kBM)) {
+        if (C::SINKS ? !block_unmasked_sinks(s, i0, i0 + C::BMQ, t.k0, t.k0 + kBM)
+                     : !block_unmasked(s, i0, i0 + C::BMQ, t.k0, t.k0 + kBM)) {
           int lo, hi;
-          visible_queries(s, krow, i0 + wg * 32, &lo, &hi);
+          if constexpr (C::SINKS)
+            visible_queries_sinks(s, krow, i0 + wg * 32, &lo, &hi);
+          else
+            visible_queries(s, krow, i0 + wg * 32, &lo, &hi);
 #pragma unroll
           for (int q = 0; q < 32; ++q)
             sv[q] = (q >= lo && q < hi) ? sv[q] : __float_as_uint(-INFINITY);
@@ -468,6 +474,12 @@ fa_bwd_dkv_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
           *reinterpret_cast<uint4*>(smem + r * C::PART_ROW + (((col / 4 + q) ^ (r & 7)) << 4)) =
               make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       }
+    } else if (ok && C::SINKS && t.slot >= 0) {
+      // fp32 sums of a part of a block of first keys
+      float* dst = sp.partial + ((static_cast<int64_t>(t.slot) * 2 + (pside ? 1 : 0)) * kBM + r) * C::D;
+#pragma unroll 1
+      for (int c = wg; c < C::D / 16; c += C::NWG)
+        store_sums16(tmem + lane_base + C::ACC_COL + 16 * c, have, dst + 16 * c);
     } else if (ok && C::HALVES == 1) {
       const int row0 = t.k0 + quarter * 32;
       const int rows_valid = min(32, s.Tkv - row0);

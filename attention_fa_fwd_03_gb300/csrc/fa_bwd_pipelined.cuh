@@ -83,18 +83,36 @@ __device__ __forceinline__ void exp2_scores32(uint32_t (&sv)[32], uint64_t c2, c
 // cluster, CTA `part` takes the tiles [it0, it0 + n_iter) of that list.
 struct DkvItem {
   int bg, b, g, k0, i_lo, n_qt, it0, n_iter;
+  int slot;  // of the partial sums (SinkParts), or -1
 };
 
+template <bool SINKS = false>
 __device__ __forceinline__ DkvItem dkv_item(int linear, const TileOrder& o, const AttnShape& s,
-                                            int bmq, int split = 1, int part = 0) {
+                                            int bmq, int split = 1, int part = 0, const SinkParts& sp = {}) {
   DkvItem t;
   int kvt;
   decode_tile(linear, o, &t.bg, &kvt);
+  t.slot = -1;
+  if constexpr (SINKS) {
+    // the blocks of first keys come first, `parts` items each
+    const int cut = sp.blocks * sp.parts;
+    if (kvt < cut) {
+      split = sp.parts;
+      part = kvt % sp.parts;
+      if (split > 1) t.slot = t.bg * cut + kvt;
+      kvt /= sp.parts;
+    } else {
+      kvt -= cut - sp.blocks;
+    }
+  }
   t.b = t.bg / s.Hkv;
   t.g = t.bg - t.b * s.Hkv;
   t.k0 = kvt * kBM;
   int qf, ql;
-  query_range(s, t.k0, min(s.Tkv, t.k0 + kBM), &qf, &ql);
+  if constexpr (SINKS)
+    query_range_sinks(s, t.k0, min(s.Tkv, t.k0 + kBM), &qf, &ql);
+  else
+    query_range(s, t.k0, min(s.Tkv, t.k0 + kBM), &qf, &ql);
   t.i_lo = qf / bmq;
   t.n_qt = max(0, (ql + bmq - 1) / bmq - t.i_lo);
   const int total = t.n_qt * (s.Hq / s.Hkv);
@@ -104,14 +122,59 @@ __device__ __forceinline__ DkvItem dkv_item(int linear, const TileOrder& o, cons
   return t;
 }
 
+// 16 columns of a TMEM accumulator row as fp32 (zeros without data).
+__device__ __forceinline__ void store_sums16(uint32_t taddr, bool have, float* dst) {
+  uint32_t v[16] = {};
+  if (have) {
+    tmem_ld16(taddr, v);
+    tmem_ld_wait();
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    reinterpret_cast<uint4*>(dst)[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+}
+
+// dK and dV of the blocks of first keys from the sums of their parts, in the parts' order. A
+// thread has four columns of a row of one of them.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256)
+fa_bwd_sink_sums_kernel(SinkParts sp, void* dk_out, void* dv_out, float scale, int Tkv, int64_t threads) {
+  grid_wait_prior();
+  grid_release_next();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= threads) return;
+  const int at = static_cast<int>(i % (2 * kBM * D / 4));  // within [dK, dV][128][D / 4]
+  const int64_t ub = i / (2 * kBM * D / 4), unit = ub / sp.blocks;
+  const bool is_dv = at >= kBM * D / 4;
+  const int e = at - (is_dv ? kBM * D / 4 : 0), row = static_cast<int>(ub - unit * sp.blocks) * kBM + e / (D / 4);
+  if (row >= Tkv) return;
+  const float4* src = reinterpret_cast<const float4*>(sp.partial) + ub * sp.parts * (2 * kBM * D / 4) + at;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < sp.parts; ++p) {
+    const float4 y = src[static_cast<int64_t>(p) * (2 * kBM * D / 4)];
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  }
+  const float mul = is_dv ? 1.f : scale;
+  uint2 w;
+  w.x = pack2<BF16>(x.x * mul, x.y * mul);
+  w.y = pack2<BF16>(x.z * mul, x.w * mul);
+  reinterpret_cast<uint2*>(is_dv ? dv_out : dk_out)[(unit * Tkv + row) * (D / 4) + e % (D / 4)] = w;
+}
+
 // SPLIT = 2: each work item's tiles are split between the two CTAs of a
 // cluster (for grids with fewer items than half the SMs). Each CTA leaves in
 // its shared memory the fp32 partial sums of the half it does not finish
 // (CTA 0 its dK, CTA 1 its dV); after a cluster barrier CTA 0 adds CTA 1's dV
 // to its own and stores dV, CTA 1 adds CTA 0's dK and stores dK, each through
 // distributed shared memory. One item per cluster (no cluster launch control).
-template <int D_, bool BF16_, int NWG_, int SPLIT_ = 1>
+template <int D_, bool BF16_, int NWG_, int SPLIT_ = 1, bool SINKS_ = false>
 struct DkvCfg {
+  static constexpr bool SINKS = SINKS_;
+  static_assert(!(SINKS_ && SPLIT_ > 1), "blocks of first keys are cut into items instead");
   static constexpr int D = D_;
   static constexpr bool BF16 = BF16_;
   static constexpr int SPLIT = SPLIT_;
@@ -175,7 +238,7 @@ fa_bwd_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                   const float* __restrict__ lse, const float* __restrict__ dvec,
                   void* __restrict__ dk_out, void* __restrict__ dv_out, float scale, AttnShape s,
-                  TileOrder order, WaitCfg wc) {
+                  TileOrder order, WaitCfg wc, SinkParts sp) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // the 128-byte swizzle needs 1024-byte aligned tiles
@@ -200,7 +263,7 @@ fa_bwd_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
     if constexpr (C::SPLIT > 1) return false;
     return clc_next(iq, k, lane, item, tmo, abort_flag, wc.status);
   };
-  auto item_of = [&](int item) { return dkv_item(item, order, s, C::BMQ, C::SPLIT, part); };
+  auto item_of = [&](int item) { return dkv_item<C::SINKS>(item, order, s, C::BMQ, C::SPLIT, part, sp); };
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -470,9 +533,13 @@ fa_bwd_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         tmem_ld_wait();
         const float* nl_s = stats + slot * 2 * C::BMQ + wg * C::CW;  // -LSE * log2(e)
         const float* nd_s = nl_s + C::BMQ;                           // -D
-        if (!block_unmasked(s, i0, i0 + C::BMQ, t.k0, t.k0 + kBM)) {
+        if (C::SINKS ? !block_unmasked_sinks(s, i0, i0 + C::BMQ, t.k0, t.k0 + kBM)
+                     : !block_unmasked(s, i0, i0 + C::BMQ, t.k0, t.k0 + kBM)) {
           int lo, hi;
-          visible_queries(s, krow, i0 + wg * C::CW, &lo, &hi);
+          if constexpr (C::SINKS)
+            visible_queries_sinks(s, krow, i0 + wg * C::CW, &lo, &hi);
+          else
+            visible_queries(s, krow, i0 + wg * C::CW, &lo, &hi);
 #pragma unroll
           for (int q = 0; q < 32; ++q)
             sv[q] = (q >= lo && q < hi) ? sv[q] : __float_as_uint(-INFINITY);
@@ -567,6 +634,24 @@ fa_bwd_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         }
         break;  // one item per cluster
       }
+      if (C::SINKS && t.slot >= 0) {
+        // fp32 sums of a part: 16-column chunks of [dK, dV], one row per thread
+        float* dst = sp.partial + (static_cast<int64_t>(t.slot) * 2 * kBM + quarter * 32 + lane) * C::D;
+#pragma unroll 1
+        for (int c = wg; c < 2 * C::D / 16; c += C::NWG) {
+          const bool is_dv = c >= C::D / 16;
+          const int cc = 16 * (is_dv ? c - C::D / 16 : c);
+          store_sums16(tmem + lane_base + (is_dv ? C::DV_COL : C::DK_COL) + cc, have,
+                       dst + (is_dv ? kBM * C::D : 0) + cc);
+        }
+        if (have) {
+          tc_fence_before();
+          gt += t.n_iter;
+          ++ln;
+        }
+        if (!next_item(k, &item)) break;
+        continue;
+      }
       // blocks of W columns of [dV | dK] dealt round-robin over the warps of
       // this lane quarter
       constexpr int S = (C::D % 64 == 0 && 2 * C::D / 64 >= C::NWG) ? 8 : 4, W = 8 * S;
@@ -659,8 +744,14 @@ fa_bwd_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
 // are the key tiles the block sees.
 struct DqItem {
   int bh, b, g, q0, j_lo, n_iter;
+  int head;  // with SINKS: tiles of first keys before those from j_lo on
+  template <bool SINKS>
+  __device__ __forceinline__ int tile(int it) const {
+    return !SINKS ? j_lo + it : KeyTiles{j_lo, head, 0}.tile(it);
+  }
 };
 
+template <bool SINKS>
 __device__ __forceinline__ DqItem dq_item(int linear, const TileOrder& o, const AttnShape& s,
                                           int bn) {
   DqItem t;
@@ -669,6 +760,14 @@ __device__ __forceinline__ DqItem dq_item(int linear, const TileOrder& o, const 
   t.b = t.bh / s.Hq;
   t.g = (t.bh - t.b * s.Hq) / (s.Hq / s.Hkv);
   t.q0 = qt * kBM;
+  t.head = 0;
+  if constexpr (SINKS) {
+    const KeyTiles k = key_tiles(s, t.q0, min(s.Tq, t.q0 + kBM), bn);
+    t.j_lo = k.first;
+    t.head = k.head;
+    t.n_iter = k.count;
+    return t;
+  }
   int kf, kl;
   key_range(s, t.q0, min(s.Tq, t.q0 + kBM), &kf, &kl);
   t.j_lo = kf / bn;
@@ -689,8 +788,9 @@ __device__ __forceinline__ DqItem dq_item(int linear, const TileOrder& o, const 
 //    columns): tile j computes S into block j % 2, and dP into the same block
 //    once the softmax has read S from it.
 template <int D_, bool BF16_, int NWG_, int BN_ = 128, int KST_ = 3, int VST_ = 2,
-          bool QTM_ = false>
+          bool QTM_ = false, bool SINKS_ = false>
 struct DqCfg {
+  static constexpr bool SINKS = SINKS_;
   static constexpr int D = D_;
   static constexpr bool BF16 = BF16_;
   static constexpr int NWG = NWG_;
@@ -829,7 +929,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     int ln = 0, nq = 0, ndo = 0;  // items with work; Q, dO loads issued
     bool ok = true;
     for (int k = 0, item = blockIdx.x; ok; ++k) {
-      const DqItem t = dq_item(item, order, s, C::BN);
+      const DqItem t = dq_item<C::SINKS>(item, order, s, C::BN);
       if (t.n_iter > 0) {
         if constexpr (!C::QTM) {
           if (ln > 0) ok = mbar_wait(bar(C::B_QEMPTY), (ln - 1) & 1, tmo, abort_flag, wc.status);
@@ -875,10 +975,10 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (!ok) break;
         ++asked;
       }
-      const DqItem t = dq_item(item, order, s, C::BN);
+      const DqItem t = dq_item<C::SINKS>(item, order, s, C::BN);
       const int zkv = t.b * s.Hkv + t.g;
       for (int it = 0; it < t.n_iter; ++it, ++gt) {
-        const int kr = (t.j_lo + it) * C::BN;
+        const int kr = t.template tile<C::SINKS>(it) * C::BN;
         const int st = gt % nst;
         if (gt >= nst) ok = mbar_wait(bar(empty + st), ((gt / nst) - 1) & 1, tmo, abort_flag, wc.status);
         if (!ok) break;
@@ -944,7 +1044,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     int gt = 0, ln = 0;
     bool ok = true;
     for (int k = 0, item = blockIdx.x; ok; ++k) {
-      const DqItem t = dq_item(item, order, s, C::BN);
+      const DqItem t = dq_item<C::SINKS>(item, order, s, C::BN);
       const int n = t.n_iter;
       if (n > 0) {
         // S of the item's first tile: its Q, K(gt), and (Q in shared memory)
@@ -1061,7 +1161,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (lane == 0) mbar_arrive(bar(C::B_QFULL));
       }
     };
-    DqItem t = dq_item(blockIdx.x, order, s, C::BN);
+    DqItem t = dq_item<C::SINKS>(blockIdx.x, order, s, C::BN);
     float L, dv;
     row_stats(t, &L, &dv);
     load_q_rows(t);
@@ -1074,7 +1174,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       const uint64_t nl2x2 = f2_pack(nl2, nl2), ndx2 = f2_pack(-dv, -dv);
       for (int it = 0; it < t.n_iter; ++it) {
         const int gi = gt + it;
-        const int kb = (t.j_lo + it) * C::BN + wg * C::CW;
+        const int kb = t.template tile<C::SINKS>(it) * C::BN + wg * C::CW;
         // with Q in TMEM, S alternates between two blocks (and s_full barriers)
         const int sb = C::QTM ? (gi & 1) : 0;
         ok = mbar_wait(bar(C::B_SFULL + sb), (C::QTM ? (gi >> 1) : gi) & 1, tmo, abort_flag, wc.status);
@@ -1086,7 +1186,9 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_SFREE));  // the next S may overwrite them
-        if (!block_unmasked(s, t.q0, t.q0 + kBM, kb, kb + C::CW)) {
+        if constexpr (C::SINKS) {
+          if (!block_unmasked_sinks(s, t.q0, t.q0 + kBM, kb, kb + C::CW)) mask_keys_sinks(s, row, kb, sv);
+        } else if (!block_unmasked(s, t.q0, t.q0 + kBM, kb, kb + C::CW)) {
           int lo, hi;
           visible_keys(s, row, kb, &lo, &hi);
 #pragma unroll
@@ -1124,7 +1226,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       DqItem tn = t;
       float Ln = -INFINITY, dvn = 0.f;
       if (more) {
-        tn = dq_item(next, order, s, C::BN);
+        tn = dq_item<C::SINKS>(next, order, s, C::BN);
         row_stats(tn, &Ln, &dvn);
         // this item's last S has completed (waited for above), so its Q
         // columns are free for the next item's rows

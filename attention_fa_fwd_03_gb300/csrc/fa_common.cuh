@@ -28,6 +28,7 @@ struct AttnShape {
   int B, Hq, Hkv, Tq, Tkv;
   int causal, window;
   float scale_log2;  // scale * log2(e): scores are handled in the exp2 domain
+  int sinks = 0;     // first keys that the window does not hide (kernels built with SINKS only)
 };
 
 struct WaitCfg {
@@ -160,6 +161,60 @@ __host__ __device__ __forceinline__ bool block_unmasked(const AttnShape& s, int 
   if (s.window > 0 && (q_hi - 1) - k_lo >= s.window) return false;
   return true;
 }
+
+// With first keys that the window leaves visible (key j < sinks): what a query sees are
+// up to two intervals of keys, and the queries that see a key are one still.
+//
+// Key tiles of a query block: those of the first keys, [0, head), then those of its
+// window from tile `first` on.
+struct KeyTiles {
+  int first, head, count;
+  __host__ __device__ __forceinline__ int tile(int it) const { return it < head ? it : first - head + it; }
+};
+__host__ __device__ __forceinline__ KeyTiles key_tiles(const AttnShape& s, int q_lo, int q_hi, int bn) {
+  int lo, hi;
+  key_range(s, q_lo, q_hi, &lo, &hi);
+  KeyTiles t;
+  t.first = lo / bn;
+  t.head = min(t.first, (s.sinks + bn - 1) / bn);
+  t.count = max(0, (hi + bn - 1) / bn - t.first) + t.head;
+  return t;
+}
+// Hides what `row` does not see of the scores of keys k0, k0 + 1, ...
+template <int N>
+__device__ __forceinline__ void mask_keys_sinks(const AttnShape& s, int row, int k0, uint32_t (&sv)[N]) {
+  int lo, hi;
+  visible_keys(s, row, k0, &lo, &hi);
+  const int keep = s.sinks - k0;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    sv[k] = (k < hi && (k >= lo || k < keep)) ? sv[k] : __float_as_uint(-INFINITY);
+}
+__host__ __device__ __forceinline__ void visible_queries_sinks(const AttnShape& s, int j, int i0, int* lo, int* hi) {
+  visible_queries(s, j, i0, lo, hi);
+  if (j < s.sinks) *hi = 1 << 30;
+}
+__host__ __device__ __forceinline__ void query_range_sinks(const AttnShape& s, int k_lo, int k_hi, int* first,
+                                                           int* last) {
+  query_range(s, k_lo, k_hi, first, last);
+  if (k_lo < s.sinks) *last = s.Tq;
+}
+__host__ __device__ __forceinline__ bool block_unmasked_sinks(const AttnShape& s, int q_lo, int q_hi, int k_lo,
+                                                              int k_hi) {
+  if (q_hi > s.Tq || k_hi > s.Tkv) return false;
+  if (s.causal && k_hi - 1 > q_lo) return false;
+  const int first = max(k_lo, s.sinks);  // that a window can hide
+  return first >= k_hi || (q_hi - 1) - first < s.window;
+}
+
+// How the dK/dV kernel shares the blocks of first keys, which every later query sees: the
+// query tiles of each are cut into `parts` work items, whose fp32 sums go to
+// partial[(unit * blocks + block) * parts + part] = [dK, dV][128][D] and are added by
+// another kernel. parts = 1: they are work items like the others.
+struct SinkParts {
+  int blocks = 0, parts = 1;
+  float* partial = nullptr;
+};
 
 // After an abort, wait (bounded by `tmo`, the drain limit, whatever the abort
 // flag says) until the last `nst` loads issued into a ring of `nst` slots have

@@ -49,8 +49,14 @@ constexpr float kRescaleThreshold = 8.0f;
 // its tiles are the key tiles the block sees.
 struct FwdItem {
   int bh, b, g, q0, j_lo, n_iter;
+  int head;  // with SINKS: tiles of first keys before those from j_lo on
+  template <bool SINKS>
+  __device__ __forceinline__ int tile(int it) const {
+    return !SINKS ? j_lo + it : KeyTiles{j_lo, head, 0}.tile(it);
+  }
 };
 
+template <bool SINKS>
 __device__ __forceinline__ FwdItem fwd_item(int linear, const TileOrder& o, const AttnShape& s,
                                             int rows, int bn) {
   FwdItem t;
@@ -59,6 +65,14 @@ __device__ __forceinline__ FwdItem fwd_item(int linear, const TileOrder& o, cons
   t.b = t.bh / s.Hq;
   t.g = (t.bh - t.b * s.Hq) / (s.Hq / s.Hkv);
   t.q0 = qblk * rows;
+  t.head = 0;
+  if constexpr (SINKS) {
+    const KeyTiles k = key_tiles(s, t.q0, min(s.Tq, t.q0 + rows), bn);
+    t.j_lo = k.first;
+    t.head = k.head;
+    t.n_iter = k.count;
+    return t;
+  }
   int k_first, k_last;
   key_range(s, t.q0, min(s.Tq, t.q0 + rows), &k_first, &k_last);
   t.j_lo = k_first / bn;
@@ -66,8 +80,9 @@ __device__ __forceinline__ FwdItem fwd_item(int linear, const TileOrder& o, cons
   return t;
 }
 
-template <int D_, int NQ_, int BN_, int STAGES_, bool BF16_>
+template <int D_, int NQ_, int BN_, int STAGES_, bool BF16_, bool SINKS_ = false>
 struct FwdCfg {
+  static constexpr bool SINKS = SINKS_;
   static constexpr int D = D_;
   static constexpr int NQ = NQ_;
   static constexpr int BN = BN_;
@@ -193,7 +208,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if (!ok) break;
         ++asked;
       }
-      const FwdItem t = fwd_item(item, order, s, ROWS, C::BN);
+      const FwdItem t = fwd_item<C::SINKS>(item, order, s, ROWS, C::BN);
       if (t.n_iter > 0) {
         if (k_ring) {
           if (ln > 0) ok = mbar_wait(bar(C::B_QEMPTY), (ln - 1) & 1, tmo, abort_flag, wc.status);
@@ -216,7 +231,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           for (int r = 0; r < C::KREG; ++r)
             if (leader)
               tma_load_3d_hint(ring + st * C::KV_TILE + r * C::KV_REGION, map, bar(full + st), r * 64,
-                               (t.j_lo + it) * C::BN, zkv, pol_kv);
+                               t.template tile<C::SINKS>(it) * C::BN, zkv, pol_kv);
         }
         if (!ok) break;
       }
@@ -265,7 +280,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     int gk = 0, ln = 0;
     bool ok = true;
     for (int k = 0, item = blockIdx.x; ok; ++k) {
-      const FwdItem t = fwd_item(item, order, s, ROWS, C::BN);
+      const FwdItem t = fwd_item<C::SINKS>(item, order, s, ROWS, C::BN);
       const int n = t.n_iter;
       if (n > 0) {
         // scores of the block's first SBUF key tiles (over score buffers whose
@@ -336,14 +351,14 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     int gk = 0;
     bool ok = true;
     for (int k = 0, item = blockIdx.x; ok; ++k) {
-      const FwdItem t = fwd_item(item, order, s, ROWS, C::BN);
+      const FwdItem t = fwd_item<C::SINKS>(item, order, s, ROWS, C::BN);
       const int tq_lo = t.q0 + tq * kBM;
       const int row = tq_lo + r;
       float m_used = -INFINITY;  // max used for the exponentials (log2 domain)
       float l = 0.f;
       for (int it = 0; it < t.n_iter; ++it) {
         const int gi = gk + it;
-        const int k0 = (t.j_lo + it) * C::BN;
+        const int k0 = t.template tile<C::SINKS>(it) * C::BN;
         const int b = gi % C::SBUF;  // score buffer of this tile
         const uint32_t s_addr = tmem + lane_base + C::S_COL(tq, b);
         ok = mbar_wait(bar(C::sfull(tq, b)), (gi / C::SBUF) & 1, tmo, abort_flag, wc.status);
@@ -356,7 +371,9 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         for (int cc = 0; cc < C::BN; cc += 32)
           tmem_ld32(s_addr + cc, *reinterpret_cast<uint32_t(*)[32]>(&sv[cc]));
         tmem_ld_wait();
-        if (!block_unmasked(s, tq_lo, tq_lo + kBM, k0, k0 + C::BN)) {
+        if constexpr (C::SINKS) {
+          if (!block_unmasked_sinks(s, tq_lo, tq_lo + kBM, k0, k0 + C::BN)) mask_keys_sinks(s, row, k0, sv);
+        } else if (!block_unmasked(s, tq_lo, tq_lo + kBM, k0, k0 + C::BN)) {
           int lo, hi;
           visible_keys(s, row, k0, &lo, &hi);
 #pragma unroll

@@ -93,10 +93,11 @@ inline TileOrder query_block_order(const AttnShape& s, int rows_per_block, int D
 // its tile loads are latency-bound rather than limited by L2 misses.
 constexpr int64_t kDkvChunkBytes = int64_t(1) << 40;
 // KV-row blocks of one group share its reps heads' Q and dO.
-inline TileOrder kv_block_order(const AttnShape& s, int D) {
+inline TileOrder kv_block_order(const AttnShape& s, int D, const SinkParts& sp = {}) {
   const int reps = s.Hq / s.Hkv;
   const int64_t qdo_bytes = int64_t(reps) * s.Tq * D * 2 * 2;
-  return make_order(s.B * s.Hkv, (s.Tkv + kBM - 1) / kBM, qdo_bytes, 1, false, kDkvChunkBytes);
+  return make_order(s.B * s.Hkv, (s.Tkv + kBM - 1) / kBM + sp.blocks * (sp.parts - 1), qdo_bytes, 1, false,
+                    kDkvChunkBytes);
 }
 
 template <class C>
@@ -143,7 +144,7 @@ struct RegSplit<C, std::void_t<decltype(C::REG_NEEDED)>> {
 };
 
 template <class C, class Kern>
-cudaError_t launch_dkv_with(const BwdLaunch& a, Kern kern) {
+cudaError_t launch_dkv_with(const BwdLaunch& a, Kern kern, const SinkParts& sp = {}) {
   const int bhq = a.s.B * a.s.Hq, bhkv = a.s.B * a.s.Hkv;
   CUtensorMap mq, mk, mv, mdo;
   if (!encode_tile_map(&mq, a.q, C::BF16, C::D, a.s.Tq, bhq, C::BMQ) ||
@@ -156,9 +157,9 @@ cudaError_t launch_dkv_with(const BwdLaunch& a, Kern kern) {
   if (e != cudaSuccess) return e;
   if (!register_split_fits(reinterpret_cast<const void*>(kern), C::THREADS, RegSplit<C>::needed))
     return cudaErrorInvalidConfiguration;
-  const TileOrder order = kv_block_order(a.s, C::D);
+  const TileOrder order = kv_block_order(a.s, C::D, sp);
   return launch_kernel(kern, int64_t(order.units) * order.tiles, C::THREADS, C::SMEM_BYTES, a.stream,
-                       1, mq, mk, mv, mdo, a.lse, a.dvec, a.dk, a.dv, a.scale, a.s, order, a.wc);
+                       1, mq, mk, mv, mdo, a.lse, a.dvec, a.dk, a.dv, a.scale, a.s, order, a.wc, sp);
 }
 
 // dK/dV with each item's tiles split over the two CTAs of a cluster (one item
@@ -180,7 +181,7 @@ cudaError_t launch_dkv_split(const BwdLaunch& a) {
   const TileOrder order = kv_block_order(a.s, C::D);
   return launch_kernel(kern, int64_t(C::SPLIT) * order.units * order.tiles, C::THREADS,
                        C::SMEM_BYTES, a.stream, C::SPLIT, mq, mk, mv, mdo, a.lse,
-                       static_cast<const float*>(a.dvec), a.dk, a.dv, a.scale, a.s, order, a.wc);
+                       static_cast<const float*>(a.dvec), a.dk, a.dv, a.scale, a.s, order, a.wc, SinkParts());
 }
 
 // Split each KV block's query tiles over a two-CTA cluster when the blocks
@@ -197,7 +198,7 @@ inline bool dkv_small_grid(const AttnShape& s) {
 // 128-row KV block (fa_bwd_dkv_pair_kernel), non-persistent, heaviest blocks
 // first.
 template <class C>
-cudaError_t launch_dkv_pair(const BwdLaunch& a) {
+cudaError_t launch_dkv_pair(const BwdLaunch& a, const SinkParts& sp = {}) {
   const int bhq = a.s.B * a.s.Hq;
   CUtensorMap mq, mdo;
   if (!encode_tile_map(&mq, a.q, C::BF16, C::D, a.s.Tq, bhq, C::BMQ) ||
@@ -207,10 +208,10 @@ cudaError_t launch_dkv_pair(const BwdLaunch& a) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const TileOrder order = kv_block_order(a.s, C::D);
+  const TileOrder order = kv_block_order(a.s, C::D, sp);
   return launch_kernel(kern, int64_t(C::CLUSTER) * order.units * order.tiles, C::THREADS,
                        C::SMEM_BYTES, a.stream, C::CLUSTER, mq, mdo, a.k, a.v, a.lse,
-                       static_cast<const float*>(a.dvec), a.dk, a.dv, a.scale, a.s, order, a.wc);
+                       static_cast<const float*>(a.dvec), a.dk, a.dv, a.scale, a.s, order, a.wc, sp);
 }
 
 // D = 256 dK/dV: two pairs per KV block when the blocks fit twice over on the
@@ -338,6 +339,34 @@ cudaError_t run_bwd(const BwdLaunch& a, int phases) {
     }
   }
   return e;
+}
+
+// Windows with visible first keys (a.s.sinks > 0; the host has taken away what hides
+// nothing, so Tq > window + sinks): the tile kernels, for any Tq.
+template <int D, bool BF16>
+cudaError_t run_bwd_sinks(const BwdLaunch& a) {
+  cudaError_t e = run_dvec<D, BF16>(a);
+  if (e != cudaSuccess) return e;
+  if constexpr (D <= 128) {
+    using C = DkvCfg<D, BF16, kSoftmaxWarpgroups, 1, true>;
+    e = launch_dkv_with<C>(a, fa_bwd_dkv_kernel<C>, a.sink_parts);
+  } else {
+    e = launch_dkv_pair<DkvPairCfg<BF16, 1, true>>(a, a.sink_parts);
+  }
+  if (e != cudaSuccess) return e;
+  // dQ starts beside dK/dV, as on every masked grid
+  if constexpr (D <= 128) {
+    using C = DqCfg<D, BF16, kSoftmaxWarpgroups, 128, 3, 2, false, true>;
+    e = launch_dq_with<C>(a, fa_bwd_dq_kernel<C>, true);
+  } else {
+    using C = DqCfg<D, BF16, 2, 64, 3, 2, true, true>;
+    e = launch_dq_with<C>(a, fa_bwd_dq_kernel<C>, true);
+  }
+  if (e != cudaSuccess || a.sink_parts.parts == 1) return e;
+  // dQ completes after dK/dV, so this grid, which waits for dQ's, sees all sums
+  const int64_t threads = static_cast<int64_t>(a.s.B) * a.s.Hkv * a.sink_parts.blocks * (2 * kBM * D / 4);
+  return launch_kernel(fa_bwd_sink_sums_kernel<D, BF16>, (threads + 255) / 256, 256, 0, a.stream, 1, a.sink_parts, a.dk,
+                       a.dv, a.scale, a.s.Tkv, threads);
 }
 
 // Short query blocks (Tq <= 8): the split-key kernels of fa_decode.cuh, one
@@ -505,5 +534,22 @@ inline bool fwd_small_grid(const AttnShape& s) {
   }                                                                                       \
   cudaError_t launch_bwd_d##D(const BwdLaunch& a, int phases) {                           \
     return a.bf16 ? run_bwd<D, true>(a, phases) : run_bwd<D, false>(a, phases);           \
+  }                                                                                       \
+  }
+
+// The same for windows with visible first keys.
+#define FA_DEFINE_SINKS_HEAD_DIM(D, FNQ, FBN, FST)                                        \
+  namespace fa {                                                                          \
+  cudaError_t launch_fwd_sinks_d##D(const FwdLaunch& a) {                                 \
+    if constexpr (FNQ == 2) {                                                             \
+      if (fwd_small_grid(a.s))                                                            \
+        return a.bf16 ? run_fwd<FwdCfg<D, 1, FBN, 3, true, true>>(a)                      \
+                      : run_fwd<FwdCfg<D, 1, FBN, 3, false, true>>(a);                    \
+    }                                                                                     \
+    return a.bf16 ? run_fwd<FwdCfg<D, FNQ, FBN, FST, true, true>>(a)                      \
+                  : run_fwd<FwdCfg<D, FNQ, FBN, FST, false, true>>(a);                    \
+  }                                                                                       \
+  cudaError_t launch_bwd_sinks_d##D(const BwdLaunch& a) {                                 \
+    return a.bf16 ? run_bwd_sinks<D, true>(a) : run_bwd_sinks<D, false>(a);               \
   }                                                                                       \
   }

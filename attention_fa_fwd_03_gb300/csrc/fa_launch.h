@@ -28,6 +28,7 @@ struct BwdLaunch {
   float scale;
   AttnShape s;       // shape the tile kernels run (grouped heads may be folded into rows)
   AttnShape s_rows;  // the call's own shape: Hq heads of Tq rows each
+  SinkParts sink_parts;  // with first keys: how their blocks are shared
   bool bf16;
   WaitCfg wc;
   cudaStream_t stream;
@@ -61,6 +62,14 @@ cudaError_t launch_fwd_d64(const FwdLaunch& a);
 cudaError_t launch_fwd_d96(const FwdLaunch& a);
 cudaError_t launch_fwd_d128(const FwdLaunch& a);
 cudaError_t launch_fwd_d256(const FwdLaunch& a);
+cudaError_t launch_fwd_sinks_d64(const FwdLaunch& a);
+cudaError_t launch_fwd_sinks_d96(const FwdLaunch& a);
+cudaError_t launch_fwd_sinks_d128(const FwdLaunch& a);
+cudaError_t launch_fwd_sinks_d256(const FwdLaunch& a);
+cudaError_t launch_bwd_sinks_d64(const BwdLaunch& a);
+cudaError_t launch_bwd_sinks_d96(const BwdLaunch& a);
+cudaError_t launch_bwd_sinks_d128(const BwdLaunch& a);
+cudaError_t launch_bwd_sinks_d256(const BwdLaunch& a);
 // Backward phases, launched in this order when several bits are set.
 enum : int { kPhaseDvec = 1, kPhaseDkv = 2, kPhaseDq = 4, kPhaseAll = 7 };
 cudaError_t launch_bwd_d64(const BwdLaunch& a, int phases);

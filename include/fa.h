@@ -149,6 +149,25 @@ fa_status fa_bwd_dq(const void* q, const void* k, const void* v, const void* dO,
                     int B, int Hq, int Hkv, int Tq, int Tkv, int D, float scale,
                     int causal, int window, fa_dtype dt, cudaStream_t stream);
 
+/* fa_fwd and fa_bwd with first keys that the window does not hide: a key j is hidden from
+ * query i when
+ *     (causal && j > i)  or  (window > 0 && i >= j && i - j >= window && j >= sinks)
+ * sinks >= 0; without a window it has no effect, and sinks = 0 is fa_fwd and fa_bwd.
+ * Every other rule is theirs. The backward's workspace has
+ * fa_bwd_sinks_workspace_size bytes (0 for sizes that it refuses): the D-vector and, where
+ * the blocks of first keys, which every later query sees, are shared by several CTAs, the
+ * fp32 sums of each, added in a fixed order by a last kernel. Calls that may overlap
+ * need a workspace each. */
+fa_status fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                       int B, int Hq, int Hkv, int Tq, int Tkv, int D, float scale,
+                       int causal, int window, int sinks, fa_dtype dt, cudaStream_t stream);
+size_t fa_bwd_sinks_workspace_size(int B, int Hq, int Hkv, int Tq, int Tkv, int D, int window, int sinks);
+fa_status fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                       const float* lse, void* dq, void* dk, void* dv,
+                       int B, int Hq, int Hkv, int Tq, int Tkv, int D, float scale,
+                       int causal, int window, int sinks, fa_dtype dt, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+
 /* fa_bwd without a workspace argument, for callers that cannot allocate any
  * device memory: a plug-in inside a host program that owns every device
  * allocation, or a loop that may not call the allocator (which can

@@ -148,3 +148,52 @@ def assign(table, lens, held, free, count, page, T, num_pages, new=None, window=
             if pos >= 0 and 0 <= table[b][pos // page] < num_pages:
                 slots[b][t] = table[b][pos // page] * page + pos % page
     return table, now, stack, missing, slots
+
+
+def dense(q, k, v, do, scale, causal, window, sinks):
+    """Attention with a window and visible first keys, and its gradients, in float64 on the CPU, with bounds of the errors of
+    kernels that hold P and dS in one word of the inputs' type: -> dicts of values and bounds for o, lse, dq, dk, dv.
+
+    With the notation of paged_ref.py: a score is off by ds, the exponential by 2^-21, a sum of n terms by 2 (n + 16) u. P, from
+    the stored LSE, is off by a factor e = 2 ds + 2^-21 + |lse error|, and by h and the type's smallest step t / 2 where it is
+    rounded; dP by d = 2 (D + 8) u sum |do v|; the D-vector, from the stored O, by sum |do| |o error| + 2 (D + 8) u sum |do o|.
+    Hence dS = P (dP - D) by |dS| (e + h) + P (d + that) + t, twice over where P is rounded on the way, and each gradient by
+    its operands' errors, its own sums and its rounding."""
+    B, Hq, T, D = q.shape
+    Hkv, N = k.shape[1:3]
+    rep = Hq // Hkv
+    h, tiny = half_step(q.dtype), smallest(q.dtype)
+    i, j = torch.arange(T)[:, None], torch.arange(N)
+    hidden = ((i - j >= window) & (j >= sinks)) if window else torch.zeros(T, N, dtype=torch.bool)
+    if causal:
+        hidden = hidden | (j > i)
+    qd, dd = q.double(), do.double()
+    kd, vd = (x.double().repeat_interleave(rep, 1) for x in (k, v))
+    s = (scale * (qd @ kd.transpose(-1, -2))).masked_fill(hidden, -math.inf)
+    ds = ((2 * D + 8) * U32 * scale * (qd.abs() @ kd.abs().transpose(-1, -2))).masked_fill(hidden, 0.0).amax(-1, keepdim=True)
+    lse = torch.logsumexp(s, -1)
+    p = torch.exp(s - lse[..., None]).nan_to_num(0.0)
+    sums = 2 * (N + 16) * U32
+    o = p @ vd
+    bo = h * o.abs() + (h + 2 * (2 * ds + 2.0 ** -21 + sums)) * (p @ vd.abs()) + tiny + N * tiny * p.amax(-1, keepdim=True) * vd.abs().amax()
+    top = s.masked_fill(hidden, 0.0).abs().amax(-1)
+    bl = ds[..., 0] + 2.0 ** -21 + sums + 8 * U32 * (lse.nan_to_num(0.0, 0.0, 0.0).abs() + top)
+    dp = dd @ vd.transpose(-1, -2)
+    dvec = (dd * o).sum(-1, keepdim=True)
+    dsm = p * (dp - dvec)
+    e = 2 * ds + 2.0 ** -21 + bl[..., None] + 2 * h
+    near = 2 * (D + 8) * U32
+    off = near * (dd.abs() @ vd.abs().transpose(-1, -2)) + (dd.abs() * bo).sum(-1, keepdim=True) + near * (dd * o).abs().sum(-1, keepdim=True)
+    ep = p * e + tiny * ~hidden
+    es = dsm.abs() * (e + h) + p * off * (1 + e) + tiny * (1 + (dp - dvec).abs()) * ~hidden
+    sumq = 2 * (T * rep + 16) * U32
+
+    def group(x):
+        return x.view(B, Hkv, rep, N, D).sum(2)
+
+    dq, bdq = scale * (dsm @ kd), scale * ((es + sums * dsm.abs()) @ kd.abs())
+    dk, bdk = group(scale * (dsm.transpose(-1, -2) @ qd)), group(scale * ((es + sumq * dsm.abs()).transpose(-1, -2) @ qd.abs()))
+    dv, bdv = group(p.transpose(-1, -2) @ dd), group((ep + sumq * p).transpose(-1, -2) @ dd.abs())
+    values = {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+    bounds = {"o": bo, "lse": bl, **{n: b + h * (values[n].abs() + b) + tiny for n, b in (("dq", bdq), ("dk", bdk), ("dv", bdv))}}
+    return values, bounds

@@ -211,3 +211,81 @@ def test_tiles_of_a_window_with_first_keys(tmp_path):
                     assert count == len(got) and need <= got
                     first = max(0, length - n - window + 1) // 64
                     assert got == set(range(min(-(-sinks // 64), most))) | set(range(first, most))
+
+
+def test_reference_gradients():
+    """The tests' own gradients of a window with first keys, against torch's and against differences."""
+    import cache8_ref as ref
+    torch.manual_seed(0)
+    for T, N, causal, window, sinks in ((9, 9, True, 3, 2), (8, 5, False, 2, 1), (7, 3, True, 2, 1)):
+        q, do = (torch.randn(1, 2, T, 4, dtype=torch.float64) for _ in range(2))
+        k, v = (torch.randn(1, 1, N, 4, dtype=torch.float64) for _ in range(2))
+        i, j = torch.arange(T)[:, None], torch.arange(N)
+        hidden = (i - j >= window) & (j >= sinks) | ((j > i) if causal else torch.zeros(T, N, dtype=torch.bool))
+
+        def plain(q, k, v):
+            s = (0.3 * q @ k.transpose(-1, -2)).masked_fill(hidden, -1e300)
+            return torch.softmax(s, -1) @ v
+
+        ins = [t.clone().requires_grad_() for t in (q, k, v)]
+        want = torch.autograd.grad(plain(*ins), ins, do)
+        got, _ = ref.dense(q, k, v, do, 0.3, causal, window, sinks)
+        assert torch.allclose(got["o"], plain(q, k, v), rtol=0, atol=1e-13)
+        for n, x, w in zip(("dq", "dk", "dv"), (q, k, v), want):
+            assert torch.allclose(got[n], w, rtol=0, atol=1e-12)
+            d = torch.randn_like(x)
+            at = {"dq": 0, "dk": 1, "dv": 2}[n]
+            ends = []
+            for sign in (1, -1):
+                y = [q, k, v]
+                y[at] = x + sign * 1e-6 * d
+                ends.append((plain(*y) * do).sum())
+            assert abs((ends[0] - ends[1]) / 2e-6 - (got[n] * d).sum()) < 1e-7
+
+
+def dense_args(**kw):
+    a = dict(q=addr(0), k=addr(1), v=addr(2), o=addr(3), do=addr(4), lse=addr(5), dq=addr(6), dk=addr(7), dv=addr(8), B=1, Hq=4, Hkv=2,
+             Tq=500, Tkv=500, D=128, scale=0.1, causal=1, window=50, sinks=5, dt=1, ws=addr(9), bytes=1 << 32)
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(sinks=-1), INVALID), (dict(window=-1), INVALID), (dict(causal=2), INVALID), (dict(scale=0.0), INVALID),
+    (dict(Hkv=3), INVALID), (dict(Tq=0), INVALID), (dict(D=80), HEAD_DIM), (dict(dt=2), DTYPE), (dict(q=None), INVALID),
+    (dict(o=None), INVALID), (dict(lse=addr(5) + 4), MISALIGNED), (dict(o=addr(0)), INVALID), (dict(lse=addr(1)), INVALID),
+])
+def test_dense_refuses(lib, kw, code):
+    a = dense_args(**kw)
+    assert lib.fa_fwd_sinks(a["q"], a["k"], a["v"], a["o"], a["lse"], a["B"], a["Hq"], a["Hkv"], a["Tq"], a["Tkv"], a["D"],
+                            a["scale"], a["causal"], a["window"], a["sinks"], a["dt"], None) == code
+    if kw.keys() != {"o"} and kw.keys() != {"lse"} or kw.get("o", 1) is None:
+        assert bwd_sinks(lib, a) == code
+
+
+def bwd_sinks(lib, a):
+    return lib.fa_bwd_sinks(a["q"], a["k"], a["v"], a["o"], a["do"], a["lse"], a["dq"], a["dk"], a["dv"], a["B"], a["Hq"], a["Hkv"],
+                            a["Tq"], a["Tkv"], a["D"], a["scale"], a["causal"], a["window"], a["sinks"], a["dt"], a["ws"],
+                            a["bytes"], None)
+
+
+def test_dense_backward_refuses(lib):
+    size = fa.fa_bwd_sinks_workspace_size(1, 4, 2, 500, 500, 128, 50, 5)
+    assert size > fa.fa_bwd_workspace_size(1, 4, 500)       # the first block's sums
+    assert bwd_sinks(lib, dense_args(bytes=size - 1)) == INVALID
+    assert bwd_sinks(lib, dense_args(bytes=fa.fa_bwd_workspace_size(1, 4, 500))) == INVALID
+    assert bwd_sinks(lib, dense_args(ws=addr(8))) == INVALID
+    assert bwd_sinks(lib, dense_args(dq=addr(1))) == INVALID
+    assert bwd_sinks(lib, dense_args(ws=addr(9) + 8)) == MISALIGNED
+
+
+def test_dense_workspace_sizes():
+    base = fa.fa_bwd_workspace_size
+    size = fa.fa_bwd_sinks_workspace_size
+    assert size(1, 4, 2, 500, 500, 128, 50, -1) == 0 and size(0, 4, 2, 500, 500, 128, 50, 5) == 0
+    assert size(1, 4, 2, 500, 500, 80, 50, 5) == 0 and size(1, 4, 2, 500, 500, 128, -50, 5) == 0
+    for kw in ((0, 5), (450, 50), (500, 1), (1 << 30, 1 << 30), (10, 500), (50, 0)):  # nothing hidden, or no first keys
+        assert size(1, 4, 2, 500, 500, 128, *kw) == base(1, 4, 500)
+    # however many sequences and first keys, the sums stay small beside the card
+    for B, T, sinks in ((1, 1 << 20, 4), (64, 1 << 16, 1 << 15), (1, 1 << 22, 1 << 21), (512, 2048, 1000)):
+        assert size(B, 64, 8, T, T, 256, 64, sinks) - base(B, 64, T) < 1 << 30

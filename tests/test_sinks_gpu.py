@@ -127,3 +127,180 @@ def test_paged_hidden_keys_hold_anything(rep, T):
     o, lse = paged(kv, q, 0.1, True, window, sinks)
     assert clear()
     check(o, lse, want)
+
+
+# ------------------------------------------------------------------ training
+DENSE = [  # B, Hq, Hkv, Tq, Tkv, D, causal, window, sinks, dtype
+    (1, 2, 1, 300, 300, 64, True, 40, 1, "fp16"),
+    (2, 4, 2, 513, 513, 128, True, 100, 64, "bf16"),
+    (1, 3, 3, 400, 400, 96, True, 129, 5, "bf16"),
+    (1, 4, 1, 640, 640, 256, True, 200, 130, "fp16"),
+    (1, 2, 2, 700, 700, 128, True, 64, 300, "fp16"),       # several blocks of first keys
+    (1, 4, 2, 1100, 1100, 64, True, 128, 128, "bf16"),     # on tile borders
+    (1, 2, 1, 1500, 1500, 256, True, 33, 3, "bf16"),       # parts of the first block
+    (1, 2, 1, 2000, 2000, 128, True, 100, 4, "bf16"),
+    (1, 2, 2, 600, 200, 64, True, 50, 7, "bf16"),          # queries behind the last key see first keys alone
+    (1, 2, 1, 500, 900, 128, False, 60, 9, "fp16"),        # later keys visible
+    (1, 2, 1, 700, 300, 96, False, 20, 150, "bf16"),
+    (1, 4, 2, 800, 100, 256, False, 10, 60, "fp16"),
+    (2, 2, 1, 9, 9, 64, True, 3, 2, "bf16"),
+    (1, 2, 1, 5, 5, 128, True, 1, 1, "fp16"),              # no more tokens than a decoding step's
+    (1, 4, 4, 257, 257, 64, True, 1, 255, "bf16"),
+    (1, 2, 1, 300, 300, 128, True, 200, 100, "bf16"),      # nothing hidden: a causal call
+    (1, 4, 2, 100, 80, 64, False, 30, 80, "fp16"),         # nor here: no mask at all
+    (70, 4, 2, 260, 260, 64, True, 30, 6, "fp16"),         # more items than the GPU takes at once
+]
+
+
+def dense_inputs(case):
+    B, Hq, Hkv, Tq, Tkv, D, causal, window, sinks, dt = case
+    g = gen(Tq + D)
+    q, do = (randn(g, B, Hq, Tq, D, dtype=DT[dt]) for _ in range(2))
+    k, v = (randn(g, B, Hkv, Tkv, D, dtype=DT[dt]) for _ in range(2))
+    return q, k, v, do
+
+
+def dense_call(q, k, v, do, scale, causal, window, sinks):
+    B, Hq, Tq, D = q.shape
+    q, k, v, do = (t.cuda() for t in (q, k, v, do))
+    o, lse = torch.full_like(q, NAN), torch.full(q.shape[:3], NAN, device="cuda")
+    dq, dk, dv = torch.full_like(q, NAN), torch.full_like(k, NAN), torch.full_like(v, NAN)
+    ws = torch.full((fa.fa_bwd_sinks_workspace_size(B, Hq, k.shape[1], Tq, k.shape[2], D, window, sinks),), 255,
+                    dtype=torch.uint8, device="cuda")
+    fa.fa_fwd(q, k, v, o, lse, scale, causal, window, sinks=sinks)
+    fa.fa_bwd(q, k, v, o, do, lse, dq, dk, dv, scale, causal, window, workspace=ws, sinks=sinks)
+    assert clear()
+    return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+
+
+@pytest.mark.parametrize("case", DENSE, ids=lambda c: f"B{c[0]}h{c[1]}x{c[2]}t{c[3]}x{c[4]}d{c[5]}{'c' if c[6] else ''}w{c[7]}s{c[8]}{c[9]}")
+def test_dense_matches_the_definition(case):
+    B, Hq, Hkv, Tq, Tkv, D, causal, window, sinks, dt = case
+    q, k, v, do = dense_inputs(case)
+    scale = 1.0 / math.sqrt(D)
+    got = dense_call(q, k, v, do, scale, causal, window, sinks)
+    part = slice(0, 2) if B > 2 else slice(0, B)
+    values, bounds = ref.dense(q[part], k[part], v[part], do[part], scale, causal, window, sinks)
+    for n, x in values.items():
+        y = got[n][part].double().cpu()
+        empty = x == -math.inf
+        assert torch.equal(y == -math.inf, empty), n
+        bad = ~((y - x).abs()[~empty] <= bounds[n][~empty])
+        assert not bad.any(), f"{n} off by {((y - x).abs()[~empty] / bounds[n][~empty]).max():.3g} bounds"
+    again = dense_call(q, k, v, do, scale, causal, window, sinks)
+    for n in got:
+        assert torch.equal(got[n], again[n]), n
+    if B > 2:  # the batch's last sequence, which another CTA's later item has
+        values, bounds = ref.dense(q[-1:], k[-1:], v[-1:], do[-1:], scale, causal, window, sinks)
+        for n, x in values.items():
+            assert ((got[n][-1:].double().cpu() - x).abs() <= bounds[n]).all(), n
+
+
+def test_dense_equals_the_calls_without_first_keys():
+    """sinks = 0 through the new entries, and sinks whose window hides nothing, give the bits of the older calls."""
+    g = gen(9)
+    B, Hq, Hkv, T, D = 1, 4, 2, 500, 128
+    q, do = (randn(g, B, Hq, T, D, dtype=torch.bfloat16).cuda() for _ in range(2))
+    k, v = (randn(g, B, Hkv, T, D, dtype=torch.bfloat16).cuda() for _ in range(2))
+    lib = fa.library()
+
+    def run(window, sinks, entry):
+        o, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = torch.empty(fa.fa_bwd_sinks_workspace_size(B, Hq, Hkv, T, T, D, window, sinks), dtype=torch.uint8, device="cuda")
+        p = [x.data_ptr() for x in (q, k, v, o, do, lse, dq, dk, dv, ws)]
+        extra = [sinks] if entry else []
+        st = (lib.fa_fwd_sinks if entry else lib.fa_fwd)(p[0], p[1], p[2], p[3], p[5], B, Hq, Hkv, T, T, D, 0.1, 1, window, *extra, 1, None)
+        st |= (lib.fa_bwd_sinks if entry else lib.fa_bwd)(*p[:4], p[4], p[5], p[6], p[7], p[8], B, Hq, Hkv, T, T, D, 0.1, 1, window,
+                                                          *extra, 1, p[9], ws.numel(), None)
+        assert st == 0 and clear()
+        return o, lse, dq, dk, dv
+
+    for window, sinks, like in ((100, 0, 100), (0, 0, 0), (0, 33, 0), (400, 100, 0)):
+        for a, b in zip(run(window, sinks, True), run(like, 0, False)):
+            assert torch.equal(a, b)
+
+
+def test_dense_through_autograd_and_captured():
+    """flash_attention(sinks=) and its gradients: views as inputs, a broadcast cotangent, a shared input, and the same
+    step captured into a graph and replayed on other inputs."""
+    from attention_fa_fwd_03_gb300.autograd import flash_attention
+    g = gen(12)
+    B, Hq, Hkv, T, D, window, sinks = 1, 4, 2, 400, 64, 70, 6
+    qkv = randn(g, B, T, Hq + 2 * Hkv, D, dtype=torch.bfloat16)
+    x = qkv.cuda().requires_grad_()
+    q, k, v = (t.transpose(1, 2) for t in x.split([Hq, Hkv, Hkv], 2))
+    o, lse = flash_attention(q, k, v, causal=True, window=window, sinks=sinks, return_lse=True)
+    do = randn(g, 1, 1, 1, D, dtype=torch.bfloat16).expand(B, Hq, T, D)
+    o.backward(do.cuda())
+    want, bounds = ref.dense(*(t.transpose(1, 2) for t in qkv.split([Hq, Hkv, Hkv], 2)), do, 1 / math.sqrt(D), True, window, sinks)
+    grads = dict(zip(("dq", "dk", "dv"), (t.transpose(1, 2) for t in x.grad.split([Hq, Hkv, Hkv], 2))))
+    for n, y in {"o": o.detach(), "lse": lse, **grads}.items():
+        assert ((y.double().cpu() - want[n]).abs() <= bounds[n]).all(), n
+    # one tensor as keys and as values
+    kv = randn(g, B, Hkv, T, D, dtype=torch.bfloat16)
+    a = kv.cuda().requires_grad_()
+    flash_attention(q.detach(), a, a, causal=True, window=window, sinks=sinks).backward(do.cuda())
+    want, bounds = ref.dense(q.detach().cpu(), kv, kv, do, 1 / math.sqrt(D), True, window, sinks)
+    both, limit = want["dk"] + want["dv"], bounds["dk"] + bounds["dv"]
+    assert ((a.grad.double().cpu() - both).abs() <= limit + 2.0 ** -8 * both.abs()).all()
+    # captured
+    ins = [t.detach().clone().requires_grad_() for t in (q, k, v)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    dog = do.cuda().contiguous()
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            torch.autograd.grad(flash_attention(*ins, causal=True, window=window, sinks=sinks), ins, dog)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        oc = flash_attention(*ins, causal=True, window=window, sinks=sinks)
+        gc = torch.autograd.grad(oc, ins, dog)
+    for seed in (1, 2):
+        new = [randn(gen(seed + n), *t.shape, dtype=torch.bfloat16).cuda() for n, t in enumerate(ins)]
+        with torch.no_grad():
+            for t, y in zip(ins, new):
+                t.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        fresh = [y.clone().requires_grad_() for y in new]
+        oe = flash_attention(*fresh, causal=True, window=window, sinks=sinks)
+        ge = torch.autograd.grad(oe, fresh, dog)
+        assert torch.equal(oc, oe) and all(torch.equal(a, b) for a, b in zip(gc, ge))
+    assert clear()
+
+
+def test_dense_many_times_over():
+    """Enough work items that CTAs take several, with the first blocks in parts: the same bits every time."""
+    case = (2, 8, 2, 4000, 4000, 128, True, 300, 10, "bf16")
+    q, k, v, do = dense_inputs(case)
+    first = dense_call(q, k, v, do, 0.1, True, 300, 10)
+    assert all(x.isfinite().all() for x in first.values())
+    for _ in range(10):
+        again = dense_call(q, k, v, do, 0.1, True, 300, 10)
+        for n in first:
+            assert torch.equal(first[n], again[n]), n
+
+
+def test_dense_waits_give_up():
+    case = (1, 4, 2, 2000, 2000, 128, True, 100, 4, "bf16")
+    q, k, v, do = dense_inputs(case)
+    want = dense_call(q, k, v, do, 0.1, True, 100, 4)
+    for D in (128, 256):
+        x = [t if D == 128 else t.repeat(1, 1, 1, 2).contiguous() for t in (q, k, v, do)]
+        fa.fa_set_wait_limit_cycles(8)
+        try:
+            a = [t.cuda() for t in x]
+            o, lse = torch.empty_like(a[0]), torch.empty(a[0].shape[:3], device="cuda")
+            outs = [torch.empty_like(t) for t in a[:3]]
+            ws = torch.empty(fa.fa_bwd_sinks_workspace_size(1, 4, 2, 2000, 2000, D, 100, 4), dtype=torch.uint8, device="cuda")
+            fa.fa_fwd(a[0], a[1], a[2], o, lse, 0.1, True, 100, sinks=4)
+            fa.fa_bwd(a[0], a[1], a[2], o, a[3], lse, *outs, 0.1, True, 100, workspace=ws, sinks=4)
+            torch.cuda.synchronize()
+        finally:
+            fa.fa_set_wait_limit_cycles(0)
+        assert fa.fa_device_status() & 1
+    got = dense_call(q, k, v, do, 0.1, True, 100, 4)
+    for n in want:
+        assert torch.equal(want[n], got[n]), n
