@@ -214,7 +214,8 @@ fa_status paged_fwd(const Cache* kv, const void* q, void* o, float* lse, int Hq,
   // tiles are counted in 32 bits
   const int block = paged_block_rows(Hq / kv->Hkv * Tq, kv->D);
   const int64_t all_units = static_cast<int64_t>(kv->B) * kv->Hkv * ((Hq / kv->Hkv * Tq + block - 1) / block);
-  if (paged_tiles(all_units, static_cast<int64_t>(sel ? n_sel : kv->max_pages) * kv->page_size) > INT32_MAX)
+  if (paged_tiles(all_units, static_cast<int64_t>(sel ? n_sel : kv->max_pages) * kv->page_size) +
+          (kv->e4m3 ? all_units : 0) > INT32_MAX)  // (a unit counts for a tile more there)
     return FA_ERR_INVALID_ARG;
   const size_t need = fwd_workspace(Hq, kv->Hkv, Tq, kv->D);
   if (workspace_bytes < need) return FA_ERR_INVALID_ARG;

@@ -79,6 +79,9 @@ struct PagedCfg {
   static constexpr int D = D_, NT = NT_, RW = RW_;
   static constexpr bool BF16 = BF16_, E8 = E8_;
   static constexpr bool MMA_BF16 = BF16 && !E8;      // type of the products' operands
+  // Weights of the product with V in two words, except in fp16 for a bf16 output: one is
+  // then off by an eighth of what the output's rounding makes (2^-12 to 2^-9).
+  static constexpr bool TWO_WORDS = !(E8 && BF16);
   static constexpr bool CLUSTER = CLUSTER_;          // a cluster per unit instead of equal shares
   // Tiles per CTA up to which clusters are used. 64 rows, D 128, 16 units of 64 tiles (16
   // per CTA): 28.7 us, split 21.7; of 32 tiles: 18.0 and 18.4; 24 rows, 64 tiles 17.6 and 19.4.
@@ -100,8 +103,8 @@ struct PagedCfg {
   // Up to 16 rows two CTAs share an SM with about 100 KB in flight each (D = 64 and
   // up to 8 rows: three; with 16, whose registers that would spill, 80% of the copy
   // rate against 84); with more rows, or 64 KB stages, one does.
-  static constexpr int CTAS = RW > 1 || (D == 256 && !E8) ? 1 : D == 64 && NT == 1 ? 3 : 2;
-  static constexpr int STAGES = E8        ? (D == 256 ? (RW == 1 ? 3 : 5) : RW > 1 ? 8 : CTAS == 3 ? 4 : 5)
+  static constexpr int CTAS = RW > 1 || (D == 256 && !E8) ? 1 : D == 64 && NT == 1 || (E8 && D <= 128 && NT == 1) ? 3 : 2;
+  static constexpr int STAGES = E8        ? (D == 256 ? (RW == 1 ? 2 : 5) : RW > 1 ? 8 : CTAS == 3 ? 3 : 4)
                                 : D == 256  ? (RW == 1 ? 3 : 2)
                                 : D == 64 ? (RW > 1 ? 8 : NT == 1 ? 4 : 6)
                                           : (RW == 1 ? 3 : 5);
@@ -112,7 +115,13 @@ struct PagedCfg {
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
   static constexpr int OFF_O = OFF_Q + QREGS * QREGION;
-  static constexpr int OFF_ML = OFF_O + ROWS * OP * 4;
+  // Split list, E8: the warps' rows side by side in a buffer of their own, joined behind one
+  // barrier while the next segment's queries are on their way (a tile takes half as long
+  // as with 16 bits, and what is between two segments counts twice).
+  static constexpr bool ASIDE = E8 && !CLUSTER && RW == 1 && !(D == 256 && NT == 2);
+  // A unit's beginning and end take as long as this many of a CTA's tiles.
+  static constexpr int OVER = E8 && !CLUSTER ? 2 : 0;
+  static constexpr int OFF_ML = OFF_O + (ASIDE ? KW : 1) * ROWS * OP * 4;
   static constexpr int OFF_PML = OFF_ML + KW * ROWS * 8;  // clusters: (max, sum) beside every piece received
   static constexpr int SMEM_BYTES = OFF_PML + (CLUSTER ? ROWS * D : 0) + 1024;
   // clusters: the warps' rows at the end, over the stages and the queries
@@ -137,7 +146,7 @@ __device__ __forceinline__ bool large_max(float m) { return fabsf(m) > kLargeMax
 // ----------------------------------------------------------------- the list
 __device__ __forceinline__ ListShape list_shape(const PagedFwdArgs& p) {
   return {p.sel ? p.c.B * p.c.Hkv : p.c.B, (p.sel ? 1 : p.c.Hkv) * p.row_blocks, p.sel != nullptr, p.window,
-          p.c.page_shift, p.sinks};
+          p.c.page_shift, p.sinks, 0};
 }
 __device__ __forceinline__ int item_seq(const PagedFwdArgs& p, int item) { return p.sel ? item / p.c.Hkv : item; }
 __device__ __forceinline__ ItemLens load_lens(const PagedFwdArgs& p, int item) {
@@ -200,7 +209,7 @@ __device__ __forceinline__ Share find_share(const PagedFwdArgs& p, const ListSha
   for (int i = i0; i < i1; ++i) {
     const ItemLens x = load_lens(p, i);
     if (whole) window.slots[i] = x;
-    mine += make_item(list, x).tiles * list.mult;
+    mine += unit_places(list, make_item(list, x)) * list.mult;
   }
   int incl = mine;
 #pragma unroll
@@ -223,7 +232,7 @@ __device__ __forceinline__ Share find_share(const PagedFwdArgs& p, const ListSha
     int rest = s.lo - before;
     int i = i0;
     for (; i < i1 - 1; ++i) {
-      const int n = make_item(list, load_lens(p, i)).tiles * list.mult;
+      const int n = unit_places(list, make_item(list, load_lens(p, i))) * list.mult;
       if (rest < n) break;
       rest -= n;
     }
@@ -299,7 +308,7 @@ __device__ __forceinline__ void put_piece(const PagedFwdArgs& p, bool whole, int
   }
 }
 
-// By one thread after a segment: whether the unit it began is split, and over which parts.
+// By one thread after a segment (places of the list, whatever a unit counts for): whether the unit it began is split, and over which parts.
 __device__ __forceinline__ void record_unit(const PagedFwdArgs& p, const ListShape& list, const Share& share,
                                             const Walk& w, int part) {
   const bool ends = w.t1 == w.it.tiles;
@@ -363,9 +372,26 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t x) {
   return ((x & e) + one) & 0x80008000u;
 }
 
+// Four bytes of global to shared memory without waiting, and an arrival on a barrier (one
+// of its count) once this thread's loads of that kind are there.
+__device__ __forceinline__ void load_word_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_async_loads(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // A position no query reaches: the key's slot was not loaded. (Positions end below
 // 2^30, and so do windows: differences of any two of these and this stay in 32 bits.)
 constexpr int kNoPosition = 1 << 30;
+
+// Whether every new token (positions p_lo to len - 1) sees all of keys j0 to j0 + 15.
+__device__ __forceinline__ bool sees_all(const PagedFwdArgs& p, int len, int p_lo, int j0) {
+  return j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) &&
+         !(p.window > 0 && j0 <= len - 1 - p.window && j0 + 15 >= p.sinks);
+}
+// Beside the position of 16 keys of a stage (E8): that is so.
+constexpr int kSeenByAll = static_cast<int>(0x80000000u);
 
 // A producer warp's side of a CTA's ring of K and V tiles: all of them, or with two
 // producers (C::PRODUCERS) every other one.
@@ -389,8 +415,8 @@ struct TileRing {
   __device__ __forceinline__ bool mine(int tile) const { return C::PRODUCERS == 1 || tile % C::PRODUCERS == producer; }
   // One tile of KV head g into the next stage: lane i < pieces has the page (in the
   // sequence, and in the pool or -1) of its piece i, whose first key is key `x` of
-  // the list plus i pieces, and lane `from` has the scales of that page in `sc`.
-  __device__ __forceinline__ void load(int x, int pg, int id, int g, float2 sc = {}, int from = 0) {
+  // the list plus i pieces. `it`: what the keys belong to.
+  __device__ __forceinline__ void load(int x, int pg, int id, int g, const Item& it) {
     const PagedView& c = p.c;
     if (!mine(issued)) {
       ++issued;
@@ -406,16 +432,26 @@ struct TileRing {
     if (lane < kPagedKeyWarps) {
       const int pl = (lane * 16) / piece;  // piece that holds these 16 keys
       const int kpage = __shfl_sync(0xfu, pg, pl), kid = __shfl_sync(0xfu, id, pl), koff = __shfl_sync(0xfu, off, pl);
-      key_pos[slot][lane] = kid >= 0 ? (kpage << c.page_shift) + koff + lane * 16 - pl * piece : kNoPosition;
+      const int j0 = kid >= 0 ? (kpage << c.page_shift) + koff + lane * 16 - pl * piece : kNoPosition;
+      key_pos[slot][lane] = j0;
+      if constexpr (C::E8) {
+        if (sees_all(p, it.len, it.len - it.n, j0)) key_pos[slot][lane] = j0 | kSeenByAll;
+      }
+      // the scales come as the tile does, into this stage and its barrier
+      if constexpr (C::E8) {
+        if (kid >= 0) {
+          const int64_t at = static_cast<int64_t>(kid) * c.Hkv + g;
+          load_word_async(&scales[slot][lane].x, c.k_scales + at);
+          load_word_async(&scales[slot][lane].y, c.v_scales + at);
+        }
+        mbar_arrive_async_loads(full + 8 * slot);
+      }
     }
     const unsigned loads = __ballot_sync(0xffffffffu, load);
     const uint32_t bar = full + 8 * slot, box = static_cast<uint32_t>(piece) * 128u;
-    auto arrive = [&] {
-      __syncwarp();  // lane 0 arrives for what the other lanes wrote (a vote orders no memory)
-      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
-      __syncwarp();
-    };
-    if constexpr (!C::E8) arrive();
+    __syncwarp();  // lane 0 arrives for the positions of all four lanes (a vote orders no memory)
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(loads) * box * 2 * C::KREG);
+    __syncwarp();
     if (load) {
       const uint32_t dst = kv + slot * 2 * C::TILE + lane * box;
       const int z = id * c.Hkv + g;
@@ -426,14 +462,6 @@ struct TileRing {
       }
     }
     __syncwarp();
-    if constexpr (C::E8) {
-      // the scales may still be on their way: the phase cannot complete before this arrival,
-      // whatever has landed by then
-      const int of = __shfl_sync(0xffffffffu, from, ((lane & 3) * 16) / piece);
-      const float2 mine = {__shfl_sync(0xffffffffu, sc.x, of), __shfl_sync(0xffffffffu, sc.y, of)};
-      if (lane < kPagedKeyWarps) scales[slot][lane] = mine;
-      arrive();
-    }
     ++issued;
   }
   // Stay until the last loads have landed: the consumers have waited for them too,
@@ -459,15 +487,6 @@ __device__ __forceinline__ int piece_page(const PagedFwdArgs& p, int shown, int 
   return seen ? id : -1;
 }
 
-// Scales of pool page `id` (any number; 0 where it is no page) as keys and as values.
-template <class C>
-__device__ __forceinline__ float2 page_scales(const PagedView& c, int id, int g) {
-  if constexpr (!C::E8) return {};
-  if (static_cast<unsigned>(id) >= static_cast<unsigned>(c.num_pages)) return make_float2(0.f, 0.f);
-  const int64_t at = static_cast<int64_t>(id) * c.Hkv + g;
-  return make_float2(c.k_scales[at], c.v_scales[at]);
-}
-
 // All tiles of a share, by the producer warp. (A wait that gave up ends the loads, not
 // the walk: the window moves on with every warp.)
 template <class C>
@@ -482,8 +501,9 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
     const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
     const int64_t u = static_cast<int64_t>(b) * c.Hkv + g;
     const int count = p.sel ? w.it.listed : pages;
-    // pages of list entries [e0, e0 + 32) and the next 32, one per lane (whether the table
-    // holds a pool page there matters only for those that are loaded)
+    // pages of list entries [e0, e0 + 32) and the next 32, one per lane (under a window
+    // whether the table has a pool page matters only where a tile's keys are shown)
+    const int shown = first_shown(p, w.it);
     auto look_up = [&](int e, int* page, int* id) {
       *page = -1;
       *id = -1;
@@ -498,23 +518,12 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
       }
       *page = pg;
       *id = c.table[static_cast<int64_t>(b) * c.max_pages + pg];
+      if (shown <= 0) *id = checked_page(c, *id);
     };
-    const int shown = first_shown(p, w.it);
     int e0 = (w.it.tile(w.t0) * kPagedTile) >> c.page_shift;
     int page0, id0, page1, id1;
     look_up(e0 + lane, &page0, &id0);
     look_up(e0 + 32 + lane, &page1, &id1);
-    // scales are looked up a batch ahead too, by pages that are known by then
-    int page2 = -1, id2 = -1;
-    float2 sc0 = {}, sc1 = {};
-    auto look_up_scales = [&] {
-      if constexpr (C::E8) {
-        look_up(e0 + 64 + lane, &page2, &id2);
-        sc0 = page_scales<C>(c, id0, g);
-        sc1 = page_scales<C>(c, id1, g);
-      }
-    };
-    look_up_scales();
     for (int t = w.t0; t < w.t1 && ring.ok; ++t) {
       const int x = w.it.tile(t) * kPagedTile;  // first key of the tile in the list
       int e = (x >> c.page_shift) - e0;
@@ -523,28 +532,19 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
         e = 0;
         look_up(e0 + lane, &page0, &id0);
         look_up(e0 + 32 + lane, &page1, &id1);
-        look_up_scales();
       } else if (e >= 32) {
         e0 += 32;
         e -= 32;
         page0 = page1;
         id0 = id1;
-        if constexpr (C::E8) {
-          page1 = page2;
-          id1 = id2;
-          sc0 = sc1;
-          sc1 = page_scales<C>(c, id1, g);
-          look_up(e0 + 64 + lane, &page2, &id2);
-        } else {
-          look_up(e0 + 32 + lane, &page1, &id1);
-        }
+        look_up(e0 + 32 + lane, &page1, &id1);
       }
       // lane i looks at piece i of the tile
       const int my = e + ((lane * ring.piece) >> c.page_shift);  // below 32: pages of 16 start tiles at multiples of 4
       const int pg = __shfl_sync(0xffffffffu, page0, my & 31);
       int id = __shfl_sync(0xffffffffu, id0, my & 31);
-      if (lane < ring.pieces && pg >= 0) id = piece_page(p, shown, x + lane * ring.piece, ring.piece, id);
-      ring.load(x, pg, id, g, sc0, my & 31);
+      if (shown > 0 && lane < ring.pieces && pg >= 0) id = piece_page(p, shown, x + lane * ring.piece, ring.piece, id);
+      ring.load(x, pg, id, g, w.it);
     }
   }
 }
@@ -553,34 +553,31 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
 // e4m3 values are fp16 numbers, so fragments are read as they are held, two columns to a
 // 16-bit place, and converted in registers (64 pairs per clock and SM; with integer
 // operations a third of that, and NaN would be lost).
-__device__ __forceinline__ uint32_t f16x2_of(uint32_t two_e4m3) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two_e4m3)));
-  return r;
+__device__ __forceinline__ void f16_of(uint32_t four_e4m3, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four_e4m3));
 }
 // Keys: a thread has columns 4 (lane % 4) to the third behind it of 16 of a key (x) and of
 // the eighth behind it (y). Pairs of them make the fragment; its columns are thereby in another
 // order, and so are the staged queries'.
 __device__ __forceinline__ void keys_f16(uint32_t (&a)[4], uint32_t x, uint32_t y) {
-  a[0] = f16x2_of(x);
-  a[1] = f16x2_of(y);
-  a[2] = f16x2_of(x >> 16);
-  a[3] = f16x2_of(y >> 16);
+  f16_of(x, a[0], a[2]);
+  f16_of(y, a[1], a[3]);
 }
 // Values, read transposed: a place holds columns 2 (lane / 4) and the next of one key. The
 // fragment's first eight rows are the even columns, the others the odd ones.
 __device__ __forceinline__ void values_f16(uint32_t (&a)[4], uint32_t x, uint32_t y) {
-  const uint32_t u = __byte_perm(x, 0, 0x3120), v = __byte_perm(y, 0, 0x3120);
-  a[0] = f16x2_of(u);
-  a[1] = f16x2_of(u >> 16);
-  a[2] = f16x2_of(v);
-  a[3] = f16x2_of(v >> 16);
+  f16_of(__byte_perm(x, 0, 0x3120), a[0], a[1]);
+  f16_of(__byte_perm(y, 0, 0x3120), a[2], a[3]);
 }
 // Column of element e of a thread's accumulator i.
 template <class C>
 __device__ __forceinline__ int acc_column(int i, int lane, int e) {
   return C::E8 ? 16 * i + 2 * (lane >> 2) + (e >> 1) : 16 * i + (lane >> 2) + 8 * (e >> 1);
 }
+// 1 / x of a power of two between 2^-126 and 2^126.
+__device__ __forceinline__ float inverse_power(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 // Not 0 where one of four e4m3 values is NaN.
 __device__ __forceinline__ uint32_t nan4_e4m3(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
@@ -588,16 +585,21 @@ __device__ __forceinline__ uint32_t nan4_e4m3(uint32_t x) { return ((x & 0x7f7f7
 // brought to a largest magnitude in [2^14, 2^15): its elements down to 2^-28 of that are
 // exact, and the rest is off by at most 2^-40 of it. `scales`: what undoes it.
 template <class C>
-__device__ __forceinline__ void stage_rows_f16(const PagedFwdArgs& p, uint8_t* dst, float* scales, int64_t row0, int rows,
-                                               int warp, int lane) {
-  constexpr int EACH = C::ROWS / C::WARPS, CHUNKS = C::D / 8;
+struct QueryRows {
+  static constexpr int EACH = C::ROWS / C::WARPS, CHUNKS = C::D / 8;
   uint4 x[EACH];
+  __device__ __forceinline__ void load(const PagedFwdArgs& p, int64_t row0, int rows, int warp, int lane) {
 #pragma unroll
-  for (int k = 0; k < EACH; ++k) {  // all under way at once
-    const int r = warp + k * C::WARPS;
-    x[k] = make_uint4(0, 0, 0, 0);
-    if (r < rows && lane < CHUNKS) x[k] = reinterpret_cast<const uint4*>(p.q + (row0 + r) * C::D)[lane];
+    for (int k = 0; k < EACH; ++k) {  // all under way at once
+      const int r = warp + k * C::WARPS;
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (r < rows && lane < CHUNKS) x[k] = reinterpret_cast<const uint4*>(p.q + (row0 + r) * C::D)[lane];
+    }
   }
+  __device__ __forceinline__ void store(uint8_t* dst, float* scales, int warp, int lane);
+};
+template <class C>
+__device__ __forceinline__ void QueryRows<C>::store(uint8_t* dst, float* scales, int warp, int lane) {
 #pragma unroll
   for (int k = 0; k < EACH; ++k) {
     const int r = warp + k * C::WARPS;
@@ -613,8 +615,8 @@ __device__ __forceinline__ void stage_rows_f16(const PagedFwdArgs& p, uint8_t* d
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-      // 2^(e - 14) of a magnitude in [2^e, 2^(e + 1)), within normal numbers
-      const int field = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 14, 1), 253);
+      // 2^(e - 14) of a magnitude in [2^e, 2^(e + 1)), within normal numbers; of zeros 1
+      const int field = most > 0.f ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 14, 1), 253) : 127;
       undo = __uint_as_float(static_cast<uint32_t>(field) << 23);
       const float f = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
 #pragma unroll
@@ -649,13 +651,14 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedView& c = p.c;
-  const ListShape list = list_shape(p);
+  ListShape list = list_shape(p);
+  list.over = C::OVER;
   const int part = blockIdx.x, parts = gridDim.x;
   const uint64_t tmo = p.wc.timeout_cycles;
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&full[i]), C::E8 ? 1 + C::KW : 1);  // the scales of each 16 keys
       mbar_init(smem_u32(&empty[i]), C::WARPS);
     }
     fence_mbar_init();
@@ -727,11 +730,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           if (counts) flag_bad_index(c);  // a selected page that the sequence does not have
           id = -1;
         }
-        const float2 sc = page_scales<C>(c, id, g);
         for (int t = t0; t < min(w.t1, t0 + batch) && ring.ok; ++t) {
           const int from = (t - t0) * pieces + (lane & (pieces - 1));
           ring.load(w.it.tile(rank + t * ranks) * kPagedTile, __shfl_sync(0xffffffffu, pg, from),
-                    __shfl_sync(0xffffffffu, id, from), g, sc, from);
+                    __shfl_sync(0xffffffffu, id, from), g, w.it);
         }
       }
     } else {
@@ -761,7 +763,9 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   // a block's query rows to shared memory, rows behind the last one zero
   auto stage_queries = [&](int64_t row0, int rows) {
     if constexpr (C::E8) {
-      stage_rows_f16<C>(p, smem + C::OFF_Q, row_scale, row0, rows, warp, lane);
+      QueryRows<C> x;
+      x.load(p, row0, rows, warp, lane);
+      x.store(smem + C::OFF_Q, row_scale, warp, lane);
       return;
     }
     for (int i = tid; i < C::ROWS * (D / 8); i += 32 * C::WARPS) {
@@ -787,7 +791,16 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   } else {
     more = w.start(list, share, window);
   }
-  for (; more; more = !C::CLUSTER && w.next(list, window)) {
+  std::conditional_t<C::ASIDE, QueryRows<C>, int> ahead;  // of the segment to come
+  auto load_ahead = [&] {
+    if constexpr (C::ASIDE) {
+      const int rb = row_block(p, w);
+      ahead.load(p, block_row0(p, item_seq(p, w.item), kv_head(p, w), rb, C::ROWS), min(C::ROWS, p.rows - rb * C::ROWS),
+                 warp, lane);
+    }
+  };
+  if (C::ASIDE && more) load_ahead();
+  for (; more; more = C::ASIDE ? more : !C::CLUSTER && w.next(list, window)) {
     const int g = kv_head(p, w), rb = row_block(p, w);
     const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
     const int64_t row0 = block_row0(p, item_seq(p, w.item), g, rb, C::ROWS);
@@ -802,7 +815,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       for (int e = 0; e < 2; ++e)
         tokens |= static_cast<uint64_t>((rb * C::ROWS + col0 + 8 * nt + e) % p.Tq) << (8 * nt + 4 * e);
     auto token = [&](int nt, int e) { return static_cast<int>(tokens >> (8 * nt + 4 * e)) & 15; };
-    if constexpr (!C::CLUSTER) stage_queries(row0, rows);
+    if constexpr (C::ASIDE)
+      ahead.store(smem + C::OFF_Q, row_scale, warp, lane);
+    else if constexpr (!C::CLUSTER)
+      stage_queries(row0, rows);
     sync_rows();
     // B fragments of the queries: two products' worth per 8 rows and 32 columns
     const uint32_t qs = sbase + C::OFF_Q;
@@ -824,6 +840,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
     float m[C::NT][2], l[C::NT][2], acc[C::NT][D / 16][4];
     bool large = false;  // some row of the warp has a large maximum
+    float unit = 0.f;    // E8: accumulators are in units of the largest scale of values so far
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt) {
       m[nt][0] = m[nt][1] = kNoMax;
@@ -838,13 +855,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       ok = ok && mbar_wait(smem_u32(&full[slot]), phase, tmo, &abort_flag, p.wc.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const int j0 = key_pos[slot][kw];
+      const int at_keys = key_pos[slot][kw], j0 = C::E8 ? at_keys & ~kSeenByAll : at_keys;
       const uint32_t ks = sbase + C::OFF_KV + slot * 2 * C::TILE, vs = ks + C::TILE;
       // does any row see any of the 16 keys; do all rows see all of them
-      const bool some = has_rows && j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window && j0 >= p.sinks);
+      const bool known = C::E8 && at_keys < 0;
+      const bool some = has_rows && (known || (j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window && j0 >= p.sinks)));
       if (some) {
-        const bool all = j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) &&
-                         !(p.window > 0 && j0 <= p_hi - p.window && j0 + 15 >= p.sinks);
+        const bool all = C::E8 ? known : sees_all(p, len, p_lo, j0);
         // S^T = K Q^T: element e of group nt is key j0 + lane / 4 + 8 (e / 2), row
         // col0 + 8 nt + e % 2. One group: two accumulators, half as long a chain.
         float s[C::NT][4], s2[4];
@@ -884,19 +901,42 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[0][e] += s2[e];
         }
-        float2 scale = {};  // of the keys and of the values
+        float sf[C::E8 ? C::NT : 1][2];  // scores in units of ln 2
+        // The values' scale goes to the weights, as a part of `unit`; where that would cost
+        // them digits (their words are fp16), to the products instead.
+        float part = 1.f;
+        bool fold = true;
         if constexpr (C::E8) {
-          // powers of two: exact, the smaller one first so that it is only what the score is
-          // that can leave the range
-          scale = kv_scale[slot][kw];
+          const float2 scale = kv_scale[slot][kw];  // of the keys and of the values
+          if (scale.y > unit) {
+            const float f = unit * inverse_power(scale.y);
+            unit = scale.y;
+#pragma unroll
+            for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][i][e] *= f;
+          }
+          part = scale.y * inverse_power(unit);
+          fold = part >= 0.0625f;
+          // The keys' and the row's powers of two go to the factor that scores are multiplied by
+          // anyway, where it stays a normal number; else to the scores, the smaller one first
+          // so that it is only what the score is that can leave the range.
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float f = e & 1 ? rs[nt].y : rs[nt].x;
-              s[nt][e] = s[nt][e] * fminf(f, scale.x) * fmaxf(f, scale.x);
+            for (int h = 0; h < 2; ++h) {
+              const float r = h ? rs[nt].y : rs[nt].x;
+              sf[nt][h] = r * scale.x * p.scale_log2;
+              if (!(sf[nt][h] > 1e-36f && sf[nt][h] < 1e36f)) {
+                sf[nt][h] = p.scale_log2;
+#pragma unroll
+                for (int e = h; e < 4; e += 2) s[nt][e] = s[nt][e] * fminf(r, scale.x) * fmaxf(r, scale.x);
+              }
             }
         }
+        auto score_factor = [&](int nt, int h) { return C::E8 ? sf[C::E8 ? nt : 0][h] : p.scale_log2; };
         uint32_t keep0 = ~0u, keep1 = ~0u;  // keys of this thread's V fragments that some row sees
         const int jv = j0 + 2 * (lane & 3);
         if (!all) {
@@ -926,7 +966,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[nt][e] = fmaf(s[nt][e], p.scale_log2, -m[nt][e & 1]);
+            x[nt][e] = fmaf(s[nt][e], score_factor(nt, e & 1), -m[nt][e & 1]);
             above |= x[nt][e] > kPagedSlack;
           }
         }
@@ -941,7 +981,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-              const float mn = fmaxf(m[nt][h], y * p.scale_log2);
+              const float mn = fmaxf(m[nt][h], y * score_factor(nt, h));
               alpha[h] = ex2(m[nt][h] - mn);
               m[nt][h] = mn;
               any_large |= large_max(mn);
@@ -955,14 +995,14 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               acc[nt][i][3] *= alpha[1];
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], p.scale_log2, -m[nt][e & 1]);
+            for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], score_factor(nt, e & 1), -m[nt][e & 1]);
           }
           large = __any_sync(0xffffffffu, any_large);
           if (large) {
 #pragma unroll
             for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[nt][e] = __fmul_rn(s[nt][e], p.scale_log2) - m[nt][e & 1];
+              for (int e = 0; e < 4; ++e) x[nt][e] = __fmul_rn(s[nt][e], score_factor(nt, e & 1)) - m[nt][e & 1];
           }
         }
         // Weights in two words of the cache's type, p = hi + lo to 2^-17 (bf16) or
@@ -978,12 +1018,19 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             s[nt][2 + h] = ex2(x[nt][2 + h]);
             l[nt][h] += s[nt][h] + s[nt][2 + h];
           }
+          if constexpr (C::E8) {
+            const float f = fold ? part : 1.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] *= f;
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t hi = pack2<C::MMA_BF16>(s[nt][2 * h], s[nt][2 * h + 1]);
-            const float2 f = unpack2<C::MMA_BF16>(hi);
             pb[nt][h] = transpose8(hi);
-            pl[nt][h] = transpose8(pack2<C::MMA_BF16>(s[nt][2 * h] - f.x, s[nt][2 * h + 1] - f.y));
+            if constexpr (C::TWO_WORDS) {
+              const float2 f = unpack2<C::MMA_BF16>(hi);
+              pl[nt][h] = transpose8(pack2<C::MMA_BF16>(s[nt][2 * h] - f.x, s[nt][2 * h + 1] - f.y));
+            }
           }
         }
         // O^T += V^T P^T. A key hidden from every row gets V = 0 (its slot may hold
@@ -1022,7 +1069,24 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           }
           apart = __any_sync(0xffffffffu, odd != 0);
         }
-        if (C::E8 && !apart) {
+        const float rest = fold ? 1.f : part;
+        if (C::E8 && all && fold) {
+#pragma unroll
+          for (int i2 = 0; i2 < D / 32; ++i2) {
+            uint32_t a[2][4];
+            values_of(a, i2, ~0u, ~0u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int nt = 0; nt < C::NT; ++nt) mma16816<false>(acc[nt][2 * i2 + h], a[h], pb[nt][0], pb[nt][1]);
+            if constexpr (C::TWO_WORDS) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < C::NT; ++nt) mma16816<false>(acc[nt][2 * i2 + h], a[h], pl[nt][0], pl[nt][1]);
+            }
+          }
+        } else if (C::E8 && !apart) {
 #pragma unroll
           for (int i2 = 0; i2 < D / 32; ++i2) {
             uint32_t a[2][4];
@@ -1033,9 +1097,9 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               for (int nt = 0; nt < C::NT; ++nt) {
                 float x[4];
                 mma16816_first<false>(x, a[h], pb[nt][0], pb[nt][1]);
-                mma16816<false>(x, a[h], pl[nt][0], pl[nt][1]);
+                if constexpr (C::TWO_WORDS) mma16816<false>(x, a[h], pl[nt][0], pl[nt][1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][2 * i2 + h][e] = fmaf(x[e], scale.y, acc[nt][2 * i2 + h][e]);
+                for (int e = 0; e < 4; ++e) acc[nt][2 * i2 + h][e] = fmaf(x[e], rest, acc[nt][2 * i2 + h][e]);
               }
           }
         } else if (!apart) {
@@ -1073,10 +1137,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                   for (int nt = 0; nt < C::NT; ++nt) {
                     float x[4];
                     mma16816_first<false>(x, a[h], pb[nt][0], pb[nt][1]);
-                    mma16816<false>(x, a[h], pl[nt][0], pl[nt][1]);
+                    if constexpr (C::TWO_WORDS) mma16816<false>(x, a[h], pl[nt][0], pl[nt][1]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                      if (token(nt, e & 1) == tok) acc[nt][2 * i2 + h][e] = fmaf(x[e], scale.y, acc[nt][2 * i2 + h][e]);
+                      if (token(nt, e & 1) == tok) acc[nt][2 * i2 + h][e] = fmaf(x[e], rest, acc[nt][2 * i2 + h][e]);
                   }
               }
               continue;
@@ -1110,6 +1174,14 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
 
     // merge the key warps
+    if constexpr (C::E8) {
+#pragma unroll
+      for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][i][e] *= unit;
+    }
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
@@ -1126,6 +1198,37 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         }
         if (lane < 4) mls[kw * C::ROWS + col0 + 8 * nt + h] = make_float2(m[nt][h], x);
       }
+    if constexpr (C::ASIDE) {
+#pragma unroll
+      for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            om[(kw * C::ROWS + col0 + 8 * nt + (e & 1)) * C::OP + acc_column<C>(i, lane, e)] = acc[nt][i][e];
+      const Walk done = w;
+      more = w.next(list, window);
+      if (more) load_ahead();
+      sync_rows();  // (the next segment's first barrier comes before anybody writes here again)
+      const bool begins = done.t0 == 0, ends = done.t1 == done.it.tiles;
+      for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS) {
+        const int r = i / (D / 8), ch = i - r * (D / 8);
+        const float2 ml = warps_max_sum<C>(mls, r);
+        float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+#pragma unroll
+        for (int k = 0; k < C::KW; ++k) {
+          const float mk = mls[k * C::ROWS + r].x;
+          if (mk == -INFINITY) continue;  // nothing seen: not even 0 * inf
+          const float f = ex2(mk - ml.x);
+          const float* x = om + (k * C::ROWS + r) * C::OP + 8 * ch;
+          add4(s0, *reinterpret_cast<const float4*>(x), f);
+          add4(s1, *reinterpret_cast<const float4*>(x + 4), f);
+        }
+        put_piece<C>(p, begins && ends, 2 * part + (begins ? 1 : 0), row0, r, ch, s0, s1, ml);
+      }
+      if (tid == 0) record_unit(p, list, share, done, part);
+      continue;
+    }
     sync_rows();  // and nobody reads stages any more
     if constexpr (C::CLUSTER) {
       // The warps' rows side by side; a thread adds up the four of an 8-column

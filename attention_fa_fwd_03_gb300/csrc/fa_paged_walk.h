@@ -41,6 +41,7 @@ struct ListShape {
   int items, mult;
   int sel, window, page_shift;
   int sinks;  // first keys that a window does not hide
+  int over;   // tiles that a unit counts for beside its own, where beginning and ending one costs as much
 };
 
 // What the kernels read of an item, range-checked: keys, and new tokens (0 to 8)
@@ -77,7 +78,10 @@ FA_WALK_FN Item make_item(const ListShape& s, const ItemLens& x) {
   return it;
 }
 
-// One CTA's share of the list: `total` tiles in equal runs, the first total % parts
+// What a unit of the item counts for when shares are cut: `over` places, then its tiles.
+FA_WALK_FN int unit_places(const ListShape& s, const Item& it) { return it.tiles > 0 ? it.tiles + s.over : 0; }
+
+// One CTA's share of the list: `total` places (tiles, where over is 0) in equal runs, the first total % parts
 // of them one longer. (The host has checked that the longest possible list stays
 // below 2^31 tiles.)
 struct Share {
@@ -92,7 +96,7 @@ struct Share {
     lo = part * base + walk_min(part, more);
     hi = lo + base + (part < more ? 1 : 0);
   }
-  // CTA whose share holds tile x of the list
+  // CTA whose share holds place x of the list
   FA_WALK_FN int part_of(int x) const {
     const int longer = more * (base + 1);
     return x < longer ? x / (base + 1) : more + (x - longer) / base;
@@ -106,6 +110,15 @@ struct Walk {
   Item it;
   int item, sub;
   int t0, t1, left;
+  int used;  // places of the share that the segment takes
+  // The segment from place `r` of the unit on: false where the share ends before its first tile.
+  FA_WALK_FN bool cut(const ListShape& list, int r) {
+    const int tiles = walk_max(it.tiles, 1);
+    t0 = walk_min(walk_max(r - list.over, 0), tiles - 1);
+    t1 = walk_min(it.tiles, walk_max(r + left - list.over, t0));
+    used = t1 - t0 + walk_max(walk_min(list.over, r + left) - r, 0);
+    return list.over == 0 || t1 > t0;
+  }
   template <class Lens>
   FA_WALK_FN bool start(const ListShape& list, const Share& s, Lens& lens) {
     left = s.hi - s.lo;
@@ -114,15 +127,13 @@ struct Walk {
     it = make_item(list, lens(item));
     // tiles and sub are in range unless the lengths have changed since the shares
     // were cut, which must not lead out of the buffers either
-    const int tiles = walk_max(it.tiles, 1);
-    sub = walk_min(s.rest / tiles, list.mult - 1);
-    t0 = walk_min(s.rest - sub * tiles, tiles - 1);
-    t1 = walk_min(it.tiles, t0 + left);
-    return true;
+    const int places = walk_max(unit_places(list, it), 1);
+    sub = walk_min(s.rest / places, list.mult - 1);
+    return cut(list, walk_min(s.rest - sub * places, places - 1));
   }
   template <class Lens>
   FA_WALK_FN bool next(const ListShape& list, Lens& lens) {
-    left -= t1 - t0;
+    left -= used;
     if (left <= 0) return false;
     if (++sub == list.mult) {
       sub = 0;
@@ -131,9 +142,7 @@ struct Walk {
         it = make_item(list, lens(item));
       } while (it.tiles == 0);
     }
-    t0 = 0;
-    t1 = walk_min(it.tiles, left);
-    return true;
+    return cut(list, 0);
   }
   // Clusters: unit `unit` as one segment, whose place does not depend on the lengths.
   // Of its tiles rank `rank` takes every `ranks`-th, a power of two, from its own number
