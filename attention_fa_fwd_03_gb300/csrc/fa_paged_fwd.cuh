@@ -73,15 +73,11 @@ struct PagedFwdArgs {
 };
 
 // NT: groups of 8 query rows that a warp holds; RW: warps of other rows beside it.
-// E8: the cache is held in e4m3 with scales (see the products).
+// E8: the cache is held in e4m3 with scales (fa_paged8.cuh).
 template <int D_, int NT_, int RW_, bool BF16_, bool CLUSTER_, bool E8_ = false>
 struct PagedCfg {
   static constexpr int D = D_, NT = NT_, RW = RW_;
   static constexpr bool BF16 = BF16_, E8 = E8_;
-  static constexpr bool MMA_BF16 = BF16 && !E8;      // type of the products' operands
-  // Weights of the product with V in two words, except in fp16 for a bf16 output: one is
-  // then off by an eighth of what the output's rounding makes (2^-12 to 2^-9).
-  static constexpr bool TWO_WORDS = !(E8 && BF16);
   static constexpr bool CLUSTER = CLUSTER_;          // a cluster per unit instead of equal shares
   // Tiles per CTA up to which clusters are used. 64 rows, D 128, 16 units of 64 tiles (16
   // per CTA): 28.7 us, split 21.7; of 32 tiles: 18.0 and 18.4; 24 rows, 64 tiles 17.6 and 19.4.
@@ -103,8 +99,8 @@ struct PagedCfg {
   // Up to 16 rows two CTAs share an SM with about 100 KB in flight each (D = 64 and
   // up to 8 rows: three; with 16, whose registers that would spill, 80% of the copy
   // rate against 84); with more rows, or 64 KB stages, one does.
-  static constexpr int CTAS = RW > 1 || (D == 256 && !E8) ? 1 : D == 64 && NT == 1 || (E8 && D <= 128 && NT == 1) ? 3 : 2;
-  static constexpr int STAGES = E8        ? (D == 256 ? (RW == 1 ? 2 : 5) : RW > 1 ? 8 : CTAS == 3 ? 3 : 4)
+  static constexpr int CTAS = RW > 1 || (D == 256 && !E8) ? 1 : D == 64 && NT == 1 ? 3 : 2;
+  static constexpr int STAGES = E8        ? (D == 256 ? (RW == 1 ? 3 : 5) : RW > 1 ? 8 : CTAS == 3 ? 3 : 5)
                                 : D == 256  ? (RW == 1 ? 3 : 2)
                                 : D == 64 ? (RW > 1 ? 8 : NT == 1 ? 4 : 6)
                                           : (RW == 1 ? 3 : 5);
@@ -115,13 +111,7 @@ struct PagedCfg {
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
   static constexpr int OFF_O = OFF_Q + QREGS * QREGION;
-  // Split list, E8: the warps' rows side by side in a buffer of their own, joined behind one
-  // barrier while the next segment's queries are on their way (a tile takes half as long
-  // as with 16 bits, and what is between two segments counts twice).
-  static constexpr bool ASIDE = E8 && !CLUSTER && RW == 1 && !(D == 256 && NT == 2);
-  // A unit's beginning and end take as long as this many of a CTA's tiles.
-  static constexpr int OVER = E8 && !CLUSTER ? 2 : 0;
-  static constexpr int OFF_ML = OFF_O + (ASIDE ? KW : 1) * ROWS * OP * 4;
+  static constexpr int OFF_ML = OFF_O + ROWS * OP * 4;
   static constexpr int OFF_PML = OFF_ML + KW * ROWS * 8;  // clusters: (max, sum) beside every piece received
   static constexpr int SMEM_BYTES = OFF_PML + (CLUSTER ? ROWS * D : 0) + 1024;
   // clusters: the warps' rows at the end, over the stages and the queries
@@ -177,18 +167,19 @@ struct ItemWindow {
   const PagedFwdArgs& p;
   ItemLens* slots;
   int items, base;
+  int bar = 2, thread = threadIdx.x;  // barrier and number among the threads that share the window
   // by all threads, with a barrier behind it
   __device__ __forceinline__ void fill(int from) {
     base = from;
-    const int i = threadIdx.x;
+    const int i = thread;
     if (i < kItemWindow && base + i < items) slots[i] = load_lens(p, base + i);
   }
   __device__ __forceinline__ ItemLens operator()(int item) {
     if (item - base >= kItemWindow) {
       __syncwarp();
-      named_bar_sync(2, THREADS);  // all have read what they need of the old window
+      named_bar_sync(bar, THREADS);  // all have read what they need of the old window
       fill(item);
-      named_bar_sync(2, THREADS);
+      named_bar_sync(bar, THREADS);
     }
     return slots[item - base];
   }
@@ -308,7 +299,7 @@ __device__ __forceinline__ void put_piece(const PagedFwdArgs& p, bool whole, int
   }
 }
 
-// By one thread after a segment (places of the list, whatever a unit counts for): whether the unit it began is split, and over which parts.
+// By one thread after a segment: whether the unit it began is split, and over which parts.
 __device__ __forceinline__ void record_unit(const PagedFwdArgs& p, const ListShape& list, const Share& share,
                                             const Walk& w, int part) {
   const bool ends = w.t1 == w.it.tiles;
@@ -437,7 +428,7 @@ struct TileRing {
       if constexpr (C::E8) {
         if (sees_all(p, it.len, it.len - it.n, j0)) key_pos[slot][lane] = j0 | kSeenByAll;
       }
-      // the scales come as the tile does, into this stage and its barrier
+      // the scales come as the tile does, into this stage and to its barrier
       if constexpr (C::E8) {
         if (kid >= 0) {
           const int64_t at = static_cast<int64_t>(kid) * c.Hkv + g;
@@ -489,9 +480,9 @@ __device__ __forceinline__ int piece_page(const PagedFwdArgs& p, int shown, int 
 
 // All tiles of a share, by the producer warp. (A wait that gave up ends the loads, not
 // the walk: the window moves on with every warp.)
-template <class C>
+template <class C, class Window>
 __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListShape& list, const Share& share,
-                                              ItemWindow<C::THREADS>& window, TileRing<C>& ring) {
+                                              Window& window, TileRing<C>& ring) {
   const PagedView& c = p.c;
   const int lane = ring.lane;
   Walk w;
@@ -549,90 +540,11 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
   }
 }
 
-// ------------------------------------------------- products of held 8-bit values
-// e4m3 values are fp16 numbers, so fragments are read as they are held, two columns to a
-// 16-bit place, and converted in registers (64 pairs per clock and SM; with integer
-// operations a third of that, and NaN would be lost).
-__device__ __forceinline__ void f16_of(uint32_t four_e4m3, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(four_e4m3));
-}
-// Keys: a thread has columns 4 (lane % 4) to the third behind it of 16 of a key (x) and of
-// the eighth behind it (y). Pairs of them make the fragment; its columns are thereby in another
-// order, and so are the staged queries'.
-__device__ __forceinline__ void keys_f16(uint32_t (&a)[4], uint32_t x, uint32_t y) {
-  f16_of(x, a[0], a[2]);
-  f16_of(y, a[1], a[3]);
-}
-// Values, read transposed: a place holds columns 2 (lane / 4) and the next of one key. The
-// fragment's first eight rows are the even columns, the others the odd ones.
-__device__ __forceinline__ void values_f16(uint32_t (&a)[4], uint32_t x, uint32_t y) {
-  f16_of(__byte_perm(x, 0, 0x3120), a[0], a[1]);
-  f16_of(__byte_perm(y, 0, 0x3120), a[2], a[3]);
-}
-// Column of element e of a thread's accumulator i.
-template <class C>
-__device__ __forceinline__ int acc_column(int i, int lane, int e) {
-  return C::E8 ? 16 * i + 2 * (lane >> 2) + (e >> 1) : 16 * i + (lane >> 2) + 8 * (e >> 1);
-}
-// 1 / x of a power of two between 2^-126 and 2^126.
-__device__ __forceinline__ float inverse_power(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
-// Not 0 where one of four e4m3 values is NaN.
-__device__ __forceinline__ uint32_t nan4_e4m3(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+}  // namespace fa
 
-// A block's query rows in fp16, in the order of columns that keys_f16 gives. A bf16 row is
-// brought to a largest magnitude in [2^14, 2^15): its elements down to 2^-28 of that are
-// exact, and the rest is off by at most 2^-40 of it. `scales`: what undoes it.
-template <class C>
-struct QueryRows {
-  static constexpr int EACH = C::ROWS / C::WARPS, CHUNKS = C::D / 8;
-  uint4 x[EACH];
-  __device__ __forceinline__ void load(const PagedFwdArgs& p, int64_t row0, int rows, int warp, int lane) {
-#pragma unroll
-    for (int k = 0; k < EACH; ++k) {  // all under way at once
-      const int r = warp + k * C::WARPS;
-      x[k] = make_uint4(0, 0, 0, 0);
-      if (r < rows && lane < CHUNKS) x[k] = reinterpret_cast<const uint4*>(p.q + (row0 + r) * C::D)[lane];
-    }
-  }
-  __device__ __forceinline__ void store(uint8_t* dst, float* scales, int warp, int lane);
-};
-template <class C>
-__device__ __forceinline__ void QueryRows<C>::store(uint8_t* dst, float* scales, int warp, int lane) {
-#pragma unroll
-  for (int k = 0; k < EACH; ++k) {
-    const int r = warp + k * C::WARPS;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&x[k]);
-    float undo = 1.f;
-    if constexpr (C::BF16) {
-      float most = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<true>(w[i]);
-        if (fabsf(f.x) < INFINITY) most = fmaxf(most, fabsf(f.x));
-        if (fabsf(f.y) < INFINITY) most = fmaxf(most, fabsf(f.y));
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-      // 2^(e - 14) of a magnitude in [2^e, 2^(e + 1)), within normal numbers; of zeros 1
-      const int field = most > 0.f ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 14, 1), 253) : 127;
-      undo = __uint_as_float(static_cast<uint32_t>(field) << 23);
-      const float f = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = unpack2<true>(w[i]);
-        w[i] = pack2<false>(v.x * f, v.y * f);
-      }
-    }
-    if (lane == 0) scales[r] = undo;
-    // pairs 0 2 4 6 of 16 columns to the first chunk, 1 3 5 7 to the second
-    const bool odd = lane & 1;
-    const uint32_t s0 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1), s1 = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
-    const uint4 y = odd ? make_uint4(s0, s1, w[1], w[3]) : make_uint4(w[0], w[2], s0, s1);
-    if (lane < CHUNKS) *reinterpret_cast<uint4*>(dst + (lane >> 3) * C::QREGION + sw128_offset(r, lane & 7)) = y;
-  }
-}
+#include "fa_paged8.cuh"
+
+namespace fa {
 
 // ------------------------------------------------------------------- kernel
 template <class C>
@@ -651,8 +563,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedView& c = p.c;
-  ListShape list = list_shape(p);
-  list.over = C::OVER;
+  const ListShape list = list_shape(p);
   const int part = blockIdx.x, parts = gridDim.x;
   const uint64_t tmo = p.wc.timeout_cycles;
   if (threadIdx.x == 0) {
@@ -737,7 +648,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         }
       }
     } else {
-      produce_share(p, list, share, window, ring);
+      produce_share<C>(p, list, share, window, ring);
     }
     ring.drain();
     if (C::CLUSTER && ranks > 1) {  // as the consumers do
@@ -766,13 +677,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       QueryRows<C> x;
       x.load(p, row0, rows, warp, lane);
       x.store(smem + C::OFF_Q, row_scale, warp, lane);
-      return;
-    }
-    for (int i = tid; i < C::ROWS * (D / 8); i += 32 * C::WARPS) {
-      const int r = i / (D / 8), ch = i - r * (D / 8);
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (r < rows) x = reinterpret_cast<const uint4*>(p.q + (row0 + r) * D)[ch];
-      *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(r, ch & 7)) = x;
+    } else {
+      for (int i = tid; i < C::ROWS * (D / 8); i += 32 * C::WARPS) {
+        const int r = i / (D / 8), ch = i - r * (D / 8);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows) x = reinterpret_cast<const uint4*>(p.q + (row0 + r) * D)[ch];
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(r, ch & 7)) = x;
+      }
     }
   };
   if constexpr (C::CLUSTER) {  // where the unit's rows are does not depend on the lengths
@@ -791,16 +702,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   } else {
     more = w.start(list, share, window);
   }
-  std::conditional_t<C::ASIDE, QueryRows<C>, int> ahead;  // of the segment to come
-  auto load_ahead = [&] {
-    if constexpr (C::ASIDE) {
-      const int rb = row_block(p, w);
-      ahead.load(p, block_row0(p, item_seq(p, w.item), kv_head(p, w), rb, C::ROWS), min(C::ROWS, p.rows - rb * C::ROWS),
-                 warp, lane);
-    }
-  };
-  if (C::ASIDE && more) load_ahead();
-  for (; more; more = C::ASIDE ? more : !C::CLUSTER && w.next(list, window)) {
+  for (; more; more = !C::CLUSTER && w.next(list, window)) {
     const int g = kv_head(p, w), rb = row_block(p, w);
     const int rows = min(C::ROWS, p.rows - rb * C::ROWS);
     const int64_t row0 = block_row0(p, item_seq(p, w.item), g, rb, C::ROWS);
@@ -815,10 +717,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       for (int e = 0; e < 2; ++e)
         tokens |= static_cast<uint64_t>((rb * C::ROWS + col0 + 8 * nt + e) % p.Tq) << (8 * nt + 4 * e);
     auto token = [&](int nt, int e) { return static_cast<int>(tokens >> (8 * nt + 4 * e)) & 15; };
-    if constexpr (C::ASIDE)
-      ahead.store(smem + C::OFF_Q, row_scale, warp, lane);
-    else if constexpr (!C::CLUSTER)
-      stage_queries(row0, rows);
+    if constexpr (!C::CLUSTER) stage_queries(row0, rows);
     sync_rows();
     // B fragments of the queries: two products' worth per 8 rows and 32 columns
     const uint32_t qs = sbase + C::OFF_Q;
@@ -860,8 +759,21 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       // does any row see any of the 16 keys; do all rows see all of them
       const bool known = C::E8 && at_keys < 0;
       const bool some = has_rows && (known || (j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window && j0 >= p.sinks)));
-      if (some) {
-        const bool all = C::E8 ? known : sees_all(p, len, p_lo, j0);
+      if constexpr (C::E8) {
+        if (some) {
+          auto query = [&](uint32_t (&b)[4], int nt, int k2) {
+            if constexpr (C::QREG) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] = qf[nt][k2][e];
+            } else {
+              query_frag(b, nt, k2);
+            }
+          };
+          step8<C, C::REGION>(p, ks + kw * 16 * 128, vs + kw * 16 * 128, lane, kv_scale[slot][kw], j0, known, len, n, tokens,
+                              query, rs, m, l, acc, unit, large);
+        }
+      } else if (some) {
+        const bool all = sees_all(p, len, p_lo, j0);
         // S^T = K Q^T: element e of group nt is key j0 + lane / 4 + 8 (e / 2), row
         // col0 + 8 nt + e % 2. One group: two accumulators, half as long a chain.
         float s[C::NT][4], s2[4];
@@ -869,15 +781,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) {
           uint32_t a0[4], a1[4];
-          if constexpr (C::E8) {
-            uint32_t x[4];
-            ldsm4(x, ks + (k2 >> 2) * C::REGION + sw128_offset(kr, (2 * k2 + kc) & 7));
-            keys_f16(a0, x[0], x[1]);
-            keys_f16(a1, x[2], x[3]);
-          } else {
-            ldsm4(a0, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + kc) & 7));
-            ldsm4(a1, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + 2 + kc) & 7));
-          }
+          ldsm4(a0, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + kc) & 7));
+          ldsm4(a1, ks + (k2 >> 1) * C::REGION + sw128_offset(kr, (4 * k2 + 2 + kc) & 7));
 #pragma unroll
           for (int nt = 0; nt < C::NT; ++nt) {
             uint32_t b[4];
@@ -888,55 +793,19 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               query_frag(b, nt, k2);
             }
             if (k2 == 0)
-              mma16816_first<C::MMA_BF16>(s[nt], a0, b[0], b[1]);
+              mma16816_first<C::BF16>(s[nt], a0, b[0], b[1]);
             else
-              mma16816<C::MMA_BF16>(s[nt], a0, b[0], b[1]);
+              mma16816<C::BF16>(s[nt], a0, b[0], b[1]);
             if (C::NT == 1 && k2 == 0)
-              mma16816_first<C::MMA_BF16>(s2, a1, b[2], b[3]);
+              mma16816_first<C::BF16>(s2, a1, b[2], b[3]);
             else
-              mma16816<C::MMA_BF16>(C::NT == 1 ? s2 : s[nt], a1, b[2], b[3]);
+              mma16816<C::BF16>(C::NT == 1 ? s2 : s[nt], a1, b[2], b[3]);
           }
         }
         if constexpr (C::NT == 1) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[0][e] += s2[e];
         }
-        float sf[C::E8 ? C::NT : 1][2];  // scores in units of ln 2
-        // The values' scale goes to the weights, as a part of `unit`; where that would cost
-        // them digits (their words are fp16), to the products instead.
-        float part = 1.f;
-        bool fold = true;
-        if constexpr (C::E8) {
-          const float2 scale = kv_scale[slot][kw];  // of the keys and of the values
-          if (scale.y > unit) {
-            const float f = unit * inverse_power(scale.y);
-            unit = scale.y;
-#pragma unroll
-            for (int nt = 0; nt < C::NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][i][e] *= f;
-          }
-          part = scale.y * inverse_power(unit);
-          fold = part >= 0.0625f;
-          // The keys' and the row's powers of two go to the factor that scores are multiplied by
-          // anyway, where it stays a normal number; else to the scores, the smaller one first
-          // so that it is only what the score is that can leave the range.
-#pragma unroll
-          for (int nt = 0; nt < C::NT; ++nt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float r = h ? rs[nt].y : rs[nt].x;
-              sf[nt][h] = r * scale.x * p.scale_log2;
-              if (!(sf[nt][h] > 1e-36f && sf[nt][h] < 1e36f)) {
-                sf[nt][h] = p.scale_log2;
-#pragma unroll
-                for (int e = h; e < 4; e += 2) s[nt][e] = s[nt][e] * fminf(r, scale.x) * fmaxf(r, scale.x);
-              }
-            }
-        }
-        auto score_factor = [&](int nt, int h) { return C::E8 ? sf[C::E8 ? nt : 0][h] : p.scale_log2; };
         uint32_t keep0 = ~0u, keep1 = ~0u;  // keys of this thread's V fragments that some row sees
         const int jv = j0 + 2 * (lane & 3);
         if (!all) {
@@ -966,7 +835,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         for (int nt = 0; nt < C::NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[nt][e] = fmaf(s[nt][e], score_factor(nt, e & 1), -m[nt][e & 1]);
+            x[nt][e] = fmaf(s[nt][e], p.scale_log2, -m[nt][e & 1]);
             above |= x[nt][e] > kPagedSlack;
           }
         }
@@ -981,7 +850,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-              const float mn = fmaxf(m[nt][h], y * score_factor(nt, h));
+              const float mn = fmaxf(m[nt][h], y * p.scale_log2);
               alpha[h] = ex2(m[nt][h] - mn);
               m[nt][h] = mn;
               any_large |= large_max(mn);
@@ -995,14 +864,14 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               acc[nt][i][3] *= alpha[1];
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], score_factor(nt, e & 1), -m[nt][e & 1]);
+            for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(s[nt][e], p.scale_log2, -m[nt][e & 1]);
           }
           large = __any_sync(0xffffffffu, any_large);
           if (large) {
 #pragma unroll
             for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[nt][e] = __fmul_rn(s[nt][e], score_factor(nt, e & 1)) - m[nt][e & 1];
+              for (int e = 0; e < 4; ++e) x[nt][e] = __fmul_rn(s[nt][e], p.scale_log2) - m[nt][e & 1];
           }
         }
         // Weights in two words of the cache's type, p = hi + lo to 2^-17 (bf16) or
@@ -1018,19 +887,12 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             s[nt][2 + h] = ex2(x[nt][2 + h]);
             l[nt][h] += s[nt][h] + s[nt][2 + h];
           }
-          if constexpr (C::E8) {
-            const float f = fold ? part : 1.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] *= f;
-          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t hi = pack2<C::MMA_BF16>(s[nt][2 * h], s[nt][2 * h + 1]);
+            const uint32_t hi = pack2<C::BF16>(s[nt][2 * h], s[nt][2 * h + 1]);
+            const float2 f = unpack2<C::BF16>(hi);
             pb[nt][h] = transpose8(hi);
-            if constexpr (C::TWO_WORDS) {
-              const float2 f = unpack2<C::MMA_BF16>(hi);
-              pl[nt][h] = transpose8(pack2<C::MMA_BF16>(s[nt][2 * h] - f.x, s[nt][2 * h + 1] - f.y));
-            }
+            pl[nt][h] = transpose8(pack2<C::BF16>(s[nt][2 * h] - f.x, s[nt][2 * h + 1] - f.y));
           }
         }
         // O^T += V^T P^T. A key hidden from every row gets V = 0 (its slot may hold
@@ -1042,23 +904,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                             ((p.causal && j0 + 15 > p_lo && j0 <= p_hi) ||
                              (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
         bool apart = false;
-        // two times 16 columns of V^T, from one read of the held values
-        auto values_of = [&](uint32_t (&a)[2][4], int i2, uint32_t m0, uint32_t m1) {
-          uint32_t x[4];
-          ldsm4_trans(x, vs + (i2 >> 2) * C::REGION + sw128_offset(vr, (2 * i2 + vc) & 7));
-          values_f16(a[0], x[0] & m0, x[2] & m1);
-          values_f16(a[1], x[1] & m0, x[3] & m1);
-        };
-        if (C::E8 && differ) {
-          uint32_t odd = 0;
-#pragma unroll
-          for (int i2 = 0; i2 < D / 32; ++i2) {
-            uint32_t x[4];
-            ldsm4_trans(x, vs + (i2 >> 2) * C::REGION + sw128_offset(vr, (2 * i2 + vc) & 7));
-            odd |= nan4_e4m3(x[0] & keep0) | nan4_e4m3(x[1] & keep0) | nan4_e4m3(x[2] & keep1) | nan4_e4m3(x[3] & keep1);
-          }
-          apart = __any_sync(0xffffffffu, odd != 0);
-        } else if (differ) {
+        if (differ) {
           uint32_t odd = 0;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -1069,40 +915,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           }
           apart = __any_sync(0xffffffffu, odd != 0);
         }
-        const float rest = fold ? 1.f : part;
-        if (C::E8 && all && fold) {
-#pragma unroll
-          for (int i2 = 0; i2 < D / 32; ++i2) {
-            uint32_t a[2][4];
-            values_of(a, i2, ~0u, ~0u);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int nt = 0; nt < C::NT; ++nt) mma16816<false>(acc[nt][2 * i2 + h], a[h], pb[nt][0], pb[nt][1]);
-            if constexpr (C::TWO_WORDS) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int nt = 0; nt < C::NT; ++nt) mma16816<false>(acc[nt][2 * i2 + h], a[h], pl[nt][0], pl[nt][1]);
-            }
-          }
-        } else if (C::E8 && !apart) {
-#pragma unroll
-          for (int i2 = 0; i2 < D / 32; ++i2) {
-            uint32_t a[2][4];
-            values_of(a, i2, keep0, keep1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int nt = 0; nt < C::NT; ++nt) {
-                float x[4];
-                mma16816_first<false>(x, a[h], pb[nt][0], pb[nt][1]);
-                if constexpr (C::TWO_WORDS) mma16816<false>(x, a[h], pl[nt][0], pl[nt][1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][2 * i2 + h][e] = fmaf(x[e], rest, acc[nt][2 * i2 + h][e]);
-              }
-          }
-        } else if (!apart) {
+        if (!apart) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             uint32_t a[4];
@@ -1113,9 +926,9 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             a[3] &= keep1;
 #pragma unroll
             for (int nt = 0; nt < C::NT; ++nt)
-              mma16816<C::MMA_BF16>(acc[nt][i], a, pb[nt][0], pb[nt][1]);
+              mma16816<C::BF16>(acc[nt][i], a, pb[nt][0], pb[nt][1]);
 #pragma unroll
-            for (int nt = 0; nt < C::NT; ++nt) mma16816<C::MMA_BF16>(acc[nt][i], a, pl[nt][0], pl[nt][1]);
+            for (int nt = 0; nt < C::NT; ++nt) mma16816<C::BF16>(acc[nt][i], a, pl[nt][0], pl[nt][1]);
           }
         } else {
 #pragma unroll 1
@@ -1126,25 +939,6 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             };
             const uint32_t k0 = (seen(jv) ? 0xffffu : 0u) | (seen(jv + 1) ? 0xffff0000u : 0u);
             const uint32_t k1 = (seen(jv + 8) ? 0xffffu : 0u) | (seen(jv + 9) ? 0xffff0000u : 0u);
-            if constexpr (C::E8) {
-#pragma unroll
-              for (int i2 = 0; i2 < D / 32; ++i2) {
-                uint32_t a[2][4];
-                values_of(a, i2, k0, k1);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                  for (int nt = 0; nt < C::NT; ++nt) {
-                    float x[4];
-                    mma16816_first<false>(x, a[h], pb[nt][0], pb[nt][1]);
-                    if constexpr (C::TWO_WORDS) mma16816<false>(x, a[h], pl[nt][0], pl[nt][1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      if (token(nt, e & 1) == tok) acc[nt][2 * i2 + h][e] = fmaf(x[e], rest, acc[nt][2 * i2 + h][e]);
-                  }
-              }
-              continue;
-            }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               uint32_t a[4];
@@ -1156,8 +950,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
               for (int nt = 0; nt < C::NT; ++nt) {
                 float x[4] = {acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]};
-                mma16816<C::MMA_BF16>(x, a, pb[nt][0], pb[nt][1]);
-                mma16816<C::MMA_BF16>(x, a, pl[nt][0], pl[nt][1]);
+                mma16816<C::BF16>(x, a, pb[nt][0], pb[nt][1]);
+                mma16816<C::BF16>(x, a, pl[nt][0], pl[nt][1]);
                 if (token(nt, 0) == tok) acc[nt][i][0] = x[0], acc[nt][i][2] = x[2];
                 if (token(nt, 1) == tok) acc[nt][i][1] = x[1], acc[nt][i][3] = x[3];
               }
@@ -1198,37 +992,6 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         }
         if (lane < 4) mls[kw * C::ROWS + col0 + 8 * nt + h] = make_float2(m[nt][h], x);
       }
-    if constexpr (C::ASIDE) {
-#pragma unroll
-      for (int nt = 0; nt < C::NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            om[(kw * C::ROWS + col0 + 8 * nt + (e & 1)) * C::OP + acc_column<C>(i, lane, e)] = acc[nt][i][e];
-      const Walk done = w;
-      more = w.next(list, window);
-      if (more) load_ahead();
-      sync_rows();  // (the next segment's first barrier comes before anybody writes here again)
-      const bool begins = done.t0 == 0, ends = done.t1 == done.it.tiles;
-      for (int i = tid; i < rows * (D / 8); i += 32 * C::WARPS) {
-        const int r = i / (D / 8), ch = i - r * (D / 8);
-        const float2 ml = warps_max_sum<C>(mls, r);
-        float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-#pragma unroll
-        for (int k = 0; k < C::KW; ++k) {
-          const float mk = mls[k * C::ROWS + r].x;
-          if (mk == -INFINITY) continue;  // nothing seen: not even 0 * inf
-          const float f = ex2(mk - ml.x);
-          const float* x = om + (k * C::ROWS + r) * C::OP + 8 * ch;
-          add4(s0, *reinterpret_cast<const float4*>(x), f);
-          add4(s1, *reinterpret_cast<const float4*>(x + 4), f);
-        }
-        put_piece<C>(p, begins && ends, 2 * part + (begins ? 1 : 0), row0, r, ch, s0, s1, ml);
-      }
-      if (tid == 0) record_unit(p, list, share, done, part);
-      continue;
-    }
     sync_rows();  // and nobody reads stages any more
     if constexpr (C::CLUSTER) {
       // The warps' rows side by side; a thread adds up the four of an 8-column
@@ -1528,6 +1291,17 @@ cudaError_t launch_paged_tc(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t gr
   return launch_kernel(kern, grid, C::THREADS, C::SMEM_BYTES, a.stream, 1, mk, mv, p);
 }
 
+template <class C>
+cudaError_t launch_paged8(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t parts) {
+  CUtensorMap mk, mv;
+  if (!encode_maps(a, C::D, &mk, &mv)) return cudaErrorInvalidValue;
+  auto kern = fa_paged8_split_kernel<C>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, (parts + C::GROUPS - 1) / C::GROUPS, C::THREADS, C::SMEM_BYTES, a.stream, 1, mk, mv, p,
+                       static_cast<int>(parts));
+}
+
 inline void set_row_blocks(const PagedFwdLaunch& a, PagedFwdArgs& p, int block) {
   p.rows = a.Hq / a.c.Hkv * a.Tq;
   p.row_blocks = (p.rows + block - 1) / block;
@@ -1603,6 +1377,9 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
       case 64: return run_split_tc<D, 2, BF16>(a, p, tiles);
       default: return run_split_tc<D, 4, BF16>(a, p, tiles);
     }
+  } else if constexpr (E8 && RW == 1) {
+    using S = Paged8Cfg<D, NT, BF16>;
+    return run_split<S>(a, p, tiles, S::CTAS, [&](int64_t parts) { return launch_paged8<S>(a, p, parts); });
   } else {
     using S = PagedCfg<D, NT, RW, BF16, false, E8>;
     return run_split<S>(a, p, tiles, S::CTAS, [&](int64_t parts) { return launch_paged<S>(a, p, parts, 1); });

@@ -174,7 +174,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   if (warp >= 4 * C::WGS && warp < C::SCORE_WARP) {
     // ----------------------------------------------------------- producer warps
     TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag, warp - 4 * C::WGS);
-    produce_share(p, list, share, window, ring);
+    produce_share<C>(p, list, share, window, ring);
     ring.drain();
   } else if (warp >= C::SCORE_WARP) {
     // -------------------------------------------------------------- MMA issuers

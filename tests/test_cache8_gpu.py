@@ -495,21 +495,22 @@ def test_on_another_stream_and_beside_another_call():
 def test_waits_give_up():
     """With a bound of a few cycles the loads' waits give up, the call ends and says so, and the next one is right."""
     g = gen(6)
-    B, Hq, Hkv, D, page, L = 1, 8, 2, 128, 64, 30000
+    B, Hq, Hkv, D, page, L = 1, 8, 2, 128, 64, 130000
     table, P = make_table(g, B, -(-L // page))
-    k, ks = held_pool(g, 4, Hkv, page, D, 1.0)
-    table %= 4
+    k, ks = held_pool(g, 64, Hkv, page, D, 1.0)
+    k, ks = k.cuda().view(torch.uint8).repeat(P // 64 + 1, 1, 1, 1)[:P].view(ref.E4M3), ks.cuda().repeat(P // 64 + 1, 1)[:P].contiguous()
     kv = handle(k, k, ks, ks, table, i32([L]))
     q = randn(g, B, Hq, 1, D, dtype=torch.bfloat16)
     want = attend(kv, q, 0.1)
     assert clear()
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda").fill_(1)  # the keys have to come from memory
     fa.fa_set_wait_limit_cycles(8)
     try:
         attend(kv, q, 0.1)
         torch.cuda.synchronize()
     finally:
         fa.fa_set_wait_limit_cycles(0)
-    assert fa.fa_device_status() & 1
+    assert fa.fa_device_status() & 1 and flush.numel()
     got = attend(kv, q, 0.1)
     assert clear()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
