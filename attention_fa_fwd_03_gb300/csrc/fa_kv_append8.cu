@@ -21,6 +21,8 @@
 //   many: one to eight warps per item with four rows of a thread in registers, so that
 //     rows are read once where a page has no more (64 x 128 elements, 256 threads: 2);
 //     longer pages are read twice, the second time from L2.
+#include <type_traits>
+
 #include "../../include/fa.h"
 #include "fa_append.cuh"
 
@@ -38,10 +40,12 @@ __device__ __forceinline__ float scale_for(float most) {
 }
 __device__ __forceinline__ float inverse_scale(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
-// The larger of m and |x|; an infinity or a NaN counts as nothing.
+// The larger of m and |x|; a NaN counts as nothing. FINITE: an infinity neither. (It is
+// looked for in a second pass, where the first one finds it.)
+template <bool FINITE>
 __device__ __forceinline__ float widen_max(float m, float x) {
   const float a = fabsf(x);
-  return a < INFINITY ? fmaxf(m, a) : m;
+  return !FINITE || a < INFINITY ? fmaxf(m, a) : m;
 }
 
 __device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float d) {
@@ -91,16 +95,18 @@ __device__ __forceinline__ void rotate_values(Values& v, const Angles& g, bool i
     for (int i = 0; i < 8; ++i) turn(v.x[i], v.x[i + 8], i);
   }
 }
-// Rounded and stored; what is not finite becomes NaN (a finite value is at most 448 s).
-__device__ __forceinline__ void store_values(uint8_t* dst, const UnitPos& at, const Values& v, float inv) {
+// Rounded and stored (a finite value is at most 448 s). `odd`: some are infinite, and are
+// to become NaN.
+__device__ __forceinline__ void store_values(uint8_t* dst, const UnitPos& at, const Values& v, float inv, bool odd) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float y[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y[e] = v.x[4 * i + e] * inv;
-      y[e] = fabsf(y[e]) <= 448.f ? y[e] : NAN;
+    for (int e = 0; e < 4; ++e) y[e] = v.x[4 * i + e] * inv;
+    if (odd) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = fabsf(y[e]) <= 448.f ? y[e] : NAN;
     }
     w[i] = pack4_e4m3(y[0], y[1], y[2], y[3]);
   }
@@ -197,30 +203,37 @@ fa_kv_append8_kernel(const AppendArgs p) {
     const int stop = min(nt.t1, t + page_mask + 1 - slot);
     // the first rows of the lanes while the page is looked up
     Values v;
-    float most = 0.f;
     const int mine = t + tl;
     const bool one = tl < TL && mine < stop;
-    if (one) {
-      v = load_values<BF16>(p, src, at, mine, nt.first + mine, u);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) most = widen_max(most, v.x[e]);
-    }
+    if (one) v = load_values<BF16>(p, src, at, mine, nt.first + mine, u);
     const int id = pool_page(c, b, pos >> c.page_shift);
     if (id >= 0) {
       float* scale = src.scales + static_cast<int64_t>(id) * c.Hkv + g;
       const float old = __shfl_sync(0xffffffffu, slot > 0 && lane == 0 ? *scale : 0.f, 0);
-      for (int s = mine + TL; tl < TL && s < stop; s += TL) {
-        const Values x = load_values<BF16>(p, src, at, s, nt.first + s, u);
+      auto largest = [&](auto finite) {
+        float most = 0.f;
+        if (one) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) most = widen_max(most, x.x[e]);
-      }
+          for (int e = 0; e < 16; ++e) most = widen_max<finite.value>(most, v.x[e]);
+        }
+        for (int s = mine + TL; tl < TL && s < stop; s += TL) {
+          const Values x = load_values<BF16>(p, src, at, s, nt.first + s, u);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+          for (int e = 0; e < 16; ++e) most = widen_max<finite.value>(most, x.x[e]);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+        return most;
+      };
+      float most = largest(std::false_type());
+      const bool odd = most == INFINITY;
+      if (odd) most = largest(std::true_type());
       const float s0 = scale_for(most), sc = slot > 0 ? fmaxf(s0, old) : s0, inv = inverse_scale(sc);
       uint8_t* rows = src.pool + pool_row(c, id, g, 0);
-      if (one) store_values(rows + static_cast<int64_t>(slot + tl) * D, at, v, inv);
+      if (one) store_values(rows + static_cast<int64_t>(slot + tl) * D, at, v, inv, odd);
       for (int s = mine + TL; tl < TL && s < stop; s += TL)
-        store_values(rows + static_cast<int64_t>(slot + s - t) * D, at, load_values<BF16>(p, src, at, s, nt.first + s, u), inv);
+        store_values(rows + static_cast<int64_t>(slot + s - t) * D, at, load_values<BF16>(p, src, at, s, nt.first + s, u), inv,
+                     odd);
       if (slot > 0 && s0 > old) rescale_chunks(rows, lane, slot * U, 32, old * inv);
       if (lane == 0 && !(slot > 0 && sc == old)) *scale = sc;
     }
@@ -228,93 +241,13 @@ fa_kv_append8_kernel(const AppendArgs p) {
   }
 }
 
-// Many tokens. Blocks in order of work: keys and values by (sequence, page, KV head, which),
-// `warps` of a block each; then, a warp each, query rows of (sequence, group of consecutive
-// tokens, a few heads).
-constexpr int kRows = 4;      // rows of a thread in registers
-constexpr int kRowBatch = 4;  // query rows of a thread, all loads in flight
+// A warp's query rows `r`: of a sequence, group of consecutive tokens and a few heads.
+constexpr int kRowBatch = 4;  // rows of a thread, all loads in flight
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 2)
-fa_kv_append8_many_kernel(const AppendArgs p, int pages_per_seq, int64_t item_blocks, int warps, int groups_per_seq,
-                          int row_chunks, int64_t row_items) {
+__device__ __forceinline__ void append_queries(const AppendArgs& p, int64_t r, int groups_per_seq, int row_chunks,
+                                               int64_t row_items) {
   constexpr int U = D / 16, TL = 32 / U;
-  __shared__ float tops[kWarps];
-  grid_wait_prior();
-  grid_release_next();
-  const PagedView& c = p.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % U, tl = lane / U;
-  if (blockIdx.x < item_blocks) {
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kWarps / warps) + warp / warps;
-    const int share = warp % warps;
-    const int head = static_cast<int>(item % (2 * c.Hkv)), g = head >> 1;
-    const bool values = head & 1;
-    const int bp = static_cast<int>(item / (2 * c.Hkv)), b = bp / pages_per_seq;
-    const UnitPos at = item_unit(p, u, values);
-    int id = -1, base = 0, lo = 0, hi = 0, first = 0;
-    if (b < c.B) {
-      const NewTokens nt = new_tokens(p, b);
-      first = nt.first;
-      const int from = nt.first + nt.t0;  // first position written
-      const int page = (from >> c.page_shift) + (bp - b * pages_per_seq);
-      base = page << c.page_shift;
-      lo = max(from - base, 0);
-      hi = min(nt.first + nt.t1 - base, 1 << c.page_shift);
-      if (lo < hi && nt.t0 < nt.t1) id = pool_page(c, b, page);
-    }
-    const Source src = id >= 0 ? source_of(p, b, g, values, at) : Source{};
-    const int step = warps * TL, slot0 = lo + share * TL + tl;  // this thread's rows: slot0, slot0 + step, ...
-    const bool works = id >= 0 && tl < TL;
-    Values v[kRows];
-    auto load = [&](int s0) {
-      Unit x[kRows];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        if (s0 + i * step < hi) x[i] = load_unit(src.src + static_cast<int64_t>(base + s0 + i * step - first) * src.step, at);
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        if (s0 + i * step >= hi) break;
-        v[i] = unit_values<BF16>(x[i]);
-        if (src.turn) rotate_values(v[i], load_angles(p, base + s0 + i * step, u), p.interleaved);
-      }
-    };
-    float most = 0.f;
-    if (works) {
-      for (int s0 = slot0; s0 < hi; s0 += kRows * step) {
-        load(s0);
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          if (s0 + i * step >= hi) break;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) most = widen_max(most, v[i].x[e]);
-        }
-      }
-    }
-    float* scale = id >= 0 ? src.scales + static_cast<int64_t>(id) * c.Hkv + g : nullptr;
-    const float old = id >= 0 && lo > 0 ? *scale : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-    if (lane == 0) tops[warp] = most;
-    __syncthreads();
-    if (id < 0) return;
-    for (int i = 0; i < warps; ++i) most = fmaxf(most, tops[warp - share + i]);
-    const float s0 = scale_for(most), sc = lo > 0 ? fmaxf(s0, old) : s0, inv = inverse_scale(sc);
-    uint8_t* rows = src.pool + pool_row(c, id, g, 0);
-    if (works) {
-      const bool kept = slot0 + kRows * step >= hi;  // all of its rows are in registers
-      for (int s = slot0; s < hi; s += kRows * step) {
-        if (!kept) load(s);
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          if (s + i * step >= hi) break;
-          store_values(rows + static_cast<int64_t>(s + i * step) * D, at, v[i], inv);
-        }
-      }
-    }
-    if (lo > 0 && s0 > old) rescale_chunks(rows, share * 32 + lane, lo * U, warps * 32, old * inv);
-    if (share == 0 && lane == 0) *scale = sc;
-    return;
-  }
-  const int64_t r = static_cast<int64_t>(blockIdx.x - item_blocks) * kWarps + warp;
+  const int lane = threadIdx.x & 31, u = lane % U, tl = lane / U;
   if (r >= row_items) return;
   const int chunk = static_cast<int>(r % row_chunks), bg = static_cast<int>(r / row_chunks);
   const int b = bg / groups_per_seq, t = (bg - b * groups_per_seq) * TL + tl;
@@ -341,6 +274,107 @@ fa_kv_append8_many_kernel(const AppendArgs p, int pages_per_seq, int64_t item_bl
     if (i < count) store_unit(dst + static_cast<int64_t>(i) * p.T * D, at, x[i]);
 }
 
+// Many tokens. Keys and values by (sequence, page, KV head, which), `warps` of a block each;
+// query rows of (sequence, group of consecutive tokens, a few heads), a warp each. Blocks of
+// the two kinds take turns evenly over the grid: items are chains of dependent loads and a
+// barrier, rows keep the memory busy meanwhile.
+constexpr int kRows = 2;      // rows of a thread in registers
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 3)
+fa_kv_append8_many_kernel(const AppendArgs p, int pages_per_seq, int64_t item_blocks, int warps, int groups_per_seq,
+                          int row_chunks, int64_t row_items) {
+  constexpr int U = D / 16, TL = 32 / U;
+  __shared__ float tops[2][kWarps];
+  grid_wait_prior();
+  grid_release_next();
+  const PagedView& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % U, tl = lane / U;
+  const int64_t items_before = blockIdx.x * item_blocks / gridDim.x;
+  if ((blockIdx.x + 1) * item_blocks / gridDim.x > items_before) {
+    const int64_t item = items_before * (kWarps / warps) + warp / warps;
+    const int share = warp % warps;
+    const int head = static_cast<int>(item % (2 * c.Hkv)), g = head >> 1;
+    const bool values = head & 1;
+    const int bp = static_cast<int>(item / (2 * c.Hkv)), b = bp / pages_per_seq;
+    const UnitPos at = item_unit(p, u, values);
+    int page = 0, base = 0, lo = 0, hi = 0, first = 0;
+    if (b < c.B) {
+      const NewTokens nt = new_tokens(p, b);
+      first = nt.first;
+      const int from = nt.first + nt.t0;  // first position written
+      page = (from >> c.page_shift) + (bp - b * pages_per_seq);
+      base = page << c.page_shift;
+      lo = max(from - base, 0);
+      hi = nt.t0 < nt.t1 ? min(nt.first + nt.t1 - base, 1 << c.page_shift) : 0;
+    }
+    const bool there = lo < hi;
+    const Source src = there ? source_of(p, b, g, values, at) : Source{};
+    const int step = warps * TL, slot0 = lo + share * TL + tl;  // this thread's rows: slot0, slot0 + step, ...
+    const bool works = there && tl < TL;
+    // rows as they come, so that many are under way; turned when they are needed, twice
+    Unit x[kRows];
+    auto load = [&](int s0) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (s0 + i * step < hi) x[i] = load_unit(src.src + static_cast<int64_t>(base + s0 + i * step - first) * src.step, at);
+    };
+    auto row_values = [&](int i, int s) {
+      Values v = unit_values<BF16>(x[i]);
+      if (src.turn) rotate_values(v, load_angles(p, base + s, u), p.interleaved);
+      return v;
+    };
+    if (works) load(slot0);  // the page's lookup waits beside it
+    const int id = there ? pool_page(c, b, page) : -1;
+    const bool kept = slot0 + kRows * step >= hi;  // all of its rows are in registers
+    auto largest = [&](auto finite) {  // of the item, by all of the block's warps
+      float most = 0.f;
+      if (works) {
+        for (int s0 = slot0; s0 < hi; s0 += kRows * step) {
+          if (!kept) load(s0);
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            if (s0 + i * step >= hi) break;
+            const Values v = row_values(i, s0 + i * step);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) most = widen_max<finite.value>(most, v.x[e]);
+          }
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+      if (lane == 0) tops[finite.value][warp] = most;
+      __syncthreads();
+      for (int i = 0; i < warps; ++i) most = fmaxf(most, tops[finite.value][warp - share + i]);
+      return most;
+    };
+    float* scale = id >= 0 ? src.scales + static_cast<int64_t>(id) * c.Hkv + g : nullptr;
+    const float old = id >= 0 && lo > 0 ? *scale : 0.f;
+    float most = largest(std::false_type());
+    const bool odd = most == INFINITY;
+    if (__syncthreads_or(odd)) {  // of any of the block's items
+      const float finite = largest(std::true_type());
+      if (odd) most = finite;
+    }
+    if (id < 0) return;
+    const float s0 = scale_for(most), sc = lo > 0 ? fmaxf(s0, old) : s0, inv = inverse_scale(sc);
+    uint8_t* rows = src.pool + pool_row(c, id, g, 0);
+    if (works) {
+      for (int s = slot0; s < hi; s += kRows * step) {
+        if (!kept) load(s);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          if (s + i * step >= hi) break;
+          store_values(rows + static_cast<int64_t>(s + i * step) * D, at, row_values(i, s + i * step), inv, odd);
+        }
+      }
+    }
+    if (lo > 0 && s0 > old) rescale_chunks(rows, share * 32 + lane, lo * U, warps * 32, old * inv);
+    if (share == 0 && lane == 0) *scale = sc;
+    return;
+  }
+  append_queries<D, BF16>(p, (blockIdx.x - items_before) * kWarps + warp, groups_per_seq, row_chunks, row_items);
+}
+
 template <int D, bool BF16>
 cudaError_t run_append8(const AppendLaunch& a) {
   constexpr int U = D / 16, TL = 32 / U;
@@ -363,9 +397,9 @@ cudaError_t run_append8(const AppendLaunch& a) {
   const int64_t item_blocks = (items * warps + kWarps - 1) / kWarps;
   const int groups = (a.T + TL - 1) / TL, chunks = (p.Hq + kRowBatch - 1) / kRowBatch;
   const int64_t row_items = static_cast<int64_t>(a.c.B) * groups * chunks;
-  const int64_t blocks = item_blocks + (row_items + kWarps - 1) / kWarps;
-  return launch_kernel(fa_kv_append8_many_kernel<D, BF16>, blocks, kThreads, 0, a.stream, 1, p, pages, item_blocks, warps,
-                       groups, chunks, row_items);
+  const int64_t row_blocks = (row_items + kWarps - 1) / kWarps;
+  return launch_kernel(fa_kv_append8_many_kernel<D, BF16>, item_blocks + row_blocks, kThreads, 0, a.stream, 1, p, pages,
+                       item_blocks, warps, groups, chunks, row_items);
 }
 
 }  // namespace
