@@ -21,6 +21,7 @@
 //   many: one to eight warps per item with four rows of a thread in registers, so that
 //     rows are read once where a page has no more (64 x 128 elements, 256 threads: 2);
 //     longer pages are read twice, the second time from L2.
+#include <climits>
 #include <type_traits>
 
 #include "../../include/fa.h"
@@ -244,13 +245,13 @@ fa_kv_append8_kernel(const AppendArgs p) {
 // A warp's query rows `r`: of a sequence, group of consecutive tokens and a few heads.
 constexpr int kRowBatch = 4;  // rows of a thread, all loads in flight
 template <int D, bool BF16>
-__device__ __forceinline__ void append_queries(const AppendArgs& p, int64_t r, int groups_per_seq, int row_chunks,
-                                               int64_t row_items) {
+__device__ __forceinline__ void append_queries(const AppendArgs& p, uint32_t r, uint32_t groups_per_seq, uint32_t row_chunks,
+                                               uint32_t row_items) {
   constexpr int U = D / 16, TL = 32 / U;
   const int lane = threadIdx.x & 31, u = lane % U, tl = lane / U;
   if (r >= row_items) return;
-  const int chunk = static_cast<int>(r % row_chunks), bg = static_cast<int>(r / row_chunks);
-  const int b = bg / groups_per_seq, t = (bg - b * groups_per_seq) * TL + tl;
+  const uint32_t bg = r / row_chunks, seq = bg / groups_per_seq;
+  const int chunk = r - bg * row_chunks, b = seq, t = (bg - seq * groups_per_seq) * TL + tl;
   if (tl >= TL || t >= p.T) return;
   const UnitPos at = unit_pos(p, u);
   const NewTokens nt = new_tokens(p, b);
@@ -281,28 +282,30 @@ __device__ __forceinline__ void append_queries(const AppendArgs& p, int64_t r, i
 constexpr int kRows = 2;      // rows of a thread in registers
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 3)
-fa_kv_append8_many_kernel(const AppendArgs p, int pages_per_seq, int64_t item_blocks, int warps, int groups_per_seq,
-                          int row_chunks, int64_t row_items) {
+fa_kv_append8_many_kernel(const AppendArgs p, uint32_t pages_per_seq, uint64_t items_per_block, int warps_log2,
+                          uint32_t groups_per_seq, uint32_t row_chunks, uint32_t row_items) {
   constexpr int U = D / 16, TL = 32 / U;
   __shared__ float tops[2][kWarps];
   grid_wait_prior();
   grid_release_next();
   const PagedView& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % U, tl = lane / U;
-  const int64_t items_before = blockIdx.x * item_blocks / gridDim.x;
-  if ((blockIdx.x + 1) * item_blocks / gridDim.x > items_before) {
-    const int64_t item = items_before * (kWarps / warps) + warp / warps;
-    const int share = warp % warps;
-    const int head = static_cast<int>(item % (2 * c.Hkv)), g = head >> 1;
+  // blocks of items before this one (items_per_block: of 2^32; divisions of 64 bits would
+  // take longer than an item's rows)
+  const uint32_t items_before = static_cast<uint32_t>(blockIdx.x * items_per_block >> 32);
+  if (static_cast<uint32_t>((blockIdx.x + 1) * items_per_block >> 32) > items_before) {
+    const int warps = 1 << warps_log2, share = warp & (warps - 1);
+    const uint32_t item = items_before * (kWarps >> warps_log2) + (warp >> warps_log2);
+    const uint32_t bp = item / (2u * c.Hkv), seq = bp / pages_per_seq;
+    const int head = item - bp * (2u * c.Hkv), g = head >> 1, b = seq;
     const bool values = head & 1;
-    const int bp = static_cast<int>(item / (2 * c.Hkv)), b = bp / pages_per_seq;
     const UnitPos at = item_unit(p, u, values);
     int page = 0, base = 0, lo = 0, hi = 0, first = 0;
-    if (b < c.B) {
+    if (seq < static_cast<uint32_t>(c.B)) {
       const NewTokens nt = new_tokens(p, b);
       first = nt.first;
       const int from = nt.first + nt.t0;  // first position written
-      page = (from >> c.page_shift) + (bp - b * pages_per_seq);
+      page = (from >> c.page_shift) + static_cast<int>(bp - seq * pages_per_seq);
       base = page << c.page_shift;
       lo = max(from - base, 0);
       hi = nt.t0 < nt.t1 ? min(nt.first + nt.t1 - base, 1 << c.page_shift) : 0;
@@ -351,7 +354,10 @@ fa_kv_append8_many_kernel(const AppendArgs p, int pages_per_seq, int64_t item_bl
     const float old = id >= 0 && lo > 0 ? *scale : 0.f;
     float most = largest(std::false_type());
     const bool odd = most == INFINITY;
-    if (__syncthreads_or(odd)) {  // of any of the block's items
+    bool any_odd = false;  // of the block's items
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) any_odd |= tops[0][i] == INFINITY;
+    if (any_odd) {
       const float finite = largest(std::true_type());
       if (odd) most = finite;
     }
@@ -392,14 +398,17 @@ cudaError_t run_append8(const AppendLaunch& a) {
   const int page = 1 << a.c.page_shift;
   const int pages = (a.T + page - 2) / page + 1;  // that T tokens can touch
   const int64_t items = static_cast<int64_t>(a.c.B) * pages * a.c.Hkv * 2;
-  int warps = 1;  // of an item: so many that its rows fit the registers
-  while (warps < kWarps && warps * TL * kRows < page) warps *= 2;
-  const int64_t item_blocks = (items * warps + kWarps - 1) / kWarps;
+  int log2 = 0;  // warps of an item: so many that its rows fit the registers
+  while ((1 << log2) < kWarps && (TL * kRows << log2) < page) ++log2;
+  const int64_t item_blocks = ((items << log2) + kWarps - 1) / kWarps;
   const int groups = (a.T + TL - 1) / TL, chunks = (p.Hq + kRowBatch - 1) / kRowBatch;
   const int64_t row_items = static_cast<int64_t>(a.c.B) * groups * chunks;
-  const int64_t row_blocks = (row_items + kWarps - 1) / kWarps;
-  return launch_kernel(fa_kv_append8_many_kernel<D, BF16>, item_blocks + row_blocks, kThreads, 0, a.stream, 1, p, pages,
-                       item_blocks, warps, groups, chunks, row_items);
+  const int64_t blocks = item_blocks + (row_items + kWarps - 1) / kWarps;
+  if (items > INT32_MAX || row_items > INT32_MAX || blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const uint64_t per_block = ((static_cast<uint64_t>(item_blocks) << 32) + blocks - 1) / blocks;
+  return launch_kernel(fa_kv_append8_many_kernel<D, BF16>, blocks, kThreads, 0, a.stream, 1, p, static_cast<uint32_t>(pages),
+                       per_block, log2, static_cast<uint32_t>(groups), static_cast<uint32_t>(chunks),
+                       static_cast<uint32_t>(row_items));
 }
 
 }  // namespace

@@ -44,9 +44,34 @@ __device__ __forceinline__ float inverse_power(float x) { return __uint_as_float
 // Not 0 where one of four e4m3 values is NaN.
 __device__ __forceinline__ uint32_t nan4_e4m3(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// A block's query rows in fp16, in the order of columns that keys_f16 gives. A bf16 row is
-// brought to a largest magnitude in [2^14, 2^15): its elements down to 2^-28 of that are
-// exact, and the rest is off by at most 2^-40 of it. `scales`: what undoes it.
+// A query row in fp16, eight columns to a lane, and what it is to be multiplied by. A bf16 row
+// is brought to a largest magnitude in [2^14, 2^15): its elements down to 2^-28 of that are
+// exact, and the rest is off by at most 2^-40 of it.
+template <bool BF16>
+__device__ __forceinline__ float row_f16(uint4& x) {
+  if constexpr (!BF16) return 1.f;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<true>(w[i]);
+    if (fabsf(f.x) < INFINITY) most = fmaxf(most, fabsf(f.x));
+    if (fabsf(f.y) < INFINITY) most = fmaxf(most, fabsf(f.y));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+  // 2^(e - 14) of a magnitude in [2^e, 2^(e + 1)), within normal numbers; of zeros 1
+  const int field = most > 0.f ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 14, 1), 253) : 127;
+  const float f = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2<true>(w[i]);
+    w[i] = pack2<false>(v.x * f, v.y * f);
+  }
+  return __uint_as_float(static_cast<uint32_t>(field) << 23);
+}
+
+// A block's query rows in fp16, in the order of columns that keys_f16 gives, and their scales.
 template <class C>
 struct QueryRows {
   static constexpr int EACH = C::ROWS / C::WARPS, CHUNKS = C::D / 8;
@@ -67,27 +92,7 @@ __device__ __forceinline__ void QueryRows<C>::store(uint8_t* dst, float* scales,
   for (int k = 0; k < EACH; ++k) {
     const int r = warp + k * C::WARPS;
     uint32_t* w = reinterpret_cast<uint32_t*>(&x[k]);
-    float undo = 1.f;
-    if constexpr (C::BF16) {
-      float most = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<true>(w[i]);
-        if (fabsf(f.x) < INFINITY) most = fmaxf(most, fabsf(f.x));
-        if (fabsf(f.y) < INFINITY) most = fmaxf(most, fabsf(f.y));
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-      // 2^(e - 14) of a magnitude in [2^e, 2^(e + 1)), within normal numbers; of zeros 1
-      const int field = most > 0.f ? min(max(static_cast<int>(__float_as_uint(most) >> 23) - 14, 1), 253) : 127;
-      undo = __uint_as_float(static_cast<uint32_t>(field) << 23);
-      const float f = __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = unpack2<true>(w[i]);
-        w[i] = pack2<false>(v.x * f, v.y * f);
-      }
-    }
+    const float undo = row_f16<C::BF16>(x[k]);
     if (lane == 0) scales[r] = undo;
     // pairs 0 2 4 6 of 16 columns to the first chunk, 1 3 5 7 to the second
     const bool odd = lane & 1;

@@ -1288,6 +1288,8 @@ cudaError_t launch_paged_tc(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t gr
   auto kern = fa_paged_tc_kernel<C>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
+  if (!register_split_fits(reinterpret_cast<const void*>(kern), C::THREADS, C::REG_NEEDED))
+    return cudaErrorInvalidConfiguration;
   return launch_kernel(kern, grid, C::THREADS, C::SMEM_BYTES, a.stream, 1, mk, mv, p);
 }
 
@@ -1336,9 +1338,9 @@ cudaError_t run_split(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t tiles, i
   return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<C::D, C::ROWS, C::BF16>, p);
 }
 
-template <int D, int RG, bool BF16>
+template <int D, int RG, bool BF16, bool E8 = false>
 cudaError_t run_split_tc(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t tiles) {
-  using C = PagedTcCfg<D, RG, BF16>;
+  using C = PagedTcCfg<D, RG, BF16, E8>;
   return run_split<C>(a, p, tiles, 1, [&](int64_t parts) { return launch_paged_tc<C>(a, p, parts); });
 }
 
@@ -1371,11 +1373,11 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   while (tiles > 2 && ranks < kPagedMaxRanks && ranks < tiles) ranks *= 2;  // 2 tiles: 5.7 us in one CTA, 6.6 in two
   while (ranks > 1 && units > resident_clusters<C>(ranks)) ranks /= 2;
   if (tiles <= C::CLUSTER_TILES * ranks) return launch_paged<C>(a, p, units * ranks, ranks);
-  if constexpr (RW > 1 && !E8) {  // more than 16 rows
+  if constexpr (RW > 1 && !(E8 && D == 256)) {  // more than 16 rows
     switch (paged_split_rows(p.rows)) {
-      case 32: return run_split_tc<D, 1, BF16>(a, p, tiles);
-      case 64: return run_split_tc<D, 2, BF16>(a, p, tiles);
-      default: return run_split_tc<D, 4, BF16>(a, p, tiles);
+      case 32: return run_split_tc<D, 1, BF16, E8>(a, p, tiles);
+      case 64: return run_split_tc<D, 2, BF16, E8>(a, p, tiles);
+      default: return run_split_tc<D, 4, BF16, E8>(a, p, tiles);
     }
   } else if constexpr (E8 && RW == 1) {
     using S = Paged8Cfg<D, NT, BF16>;

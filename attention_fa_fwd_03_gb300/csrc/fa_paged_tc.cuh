@@ -40,11 +40,15 @@
 
 namespace fa {
 
-// RG: groups of 32 rows.
-template <int D_, int RG_, bool BF16_>
+// RG: groups of 32 rows. E8: the cache is held in e4m3 with scales. Its tiles come into a ring
+// of their own (Raw), a warpgroup converts them to fp16 into the ring that the MMAs read, and
+// the scales go to the scores and, as parts of the largest one so far, to the weights.
+template <int D_, int RG_, bool BF16_, bool E8_ = false>
 struct PagedTcCfg {
   static constexpr int D = D_, RG = RG_;
-  static constexpr bool BF16 = BF16_;
+  static constexpr bool BF16 = BF16_, E8 = E8_;
+  static constexpr bool MMA_BF16 = BF16 && !E8;   // type of the products' operands
+  static constexpr bool TWO_WORDS = !(E8 && BF16);  // of weights: fp16 for a bf16 output needs one (fa_paged8.cuh)
   static constexpr int ROWS = 32 * RG;           // rows of a block
   static constexpr int COPIES = 4 / RG;          // of each row
   static constexpr int KEYS = kPagedTile / COPIES;  // of a tile that a copy takes
@@ -54,18 +58,30 @@ struct PagedTcCfg {
   // D = 256: one accumulator is all that TMEM holds beside the scores and weights, and a
   // tile's bytes take longer than the softmax's chain
   static constexpr int WGS = D == 256 ? 1 : 2;
-  static constexpr int SOFT = 128 * WGS, THREADS = SOFT + 32 * PRODUCERS + 64, SCORE_WARP = 4 * WGS + PRODUCERS;
-  static constexpr bool E8 = false;
+  // (E8: whole warpgroups, which share the registers unevenly: producers and issuers, converters)
+  static constexpr int SOFT = 128 * WGS, SCORE_WARP = 4 * WGS + PRODUCERS, CONVERT_WARP = 4 * WGS + 4;
+  static constexpr int THREADS = E8 ? SOFT + 256 : SOFT + 32 * PRODUCERS + 64;
+  static constexpr int REG_SOFT = 168, REG_REST = 88;
+  static constexpr int REG_NEEDED = E8 ? SOFT * REG_SOFT + 256 * REG_REST : 0;
   static constexpr int COLS = 64, KREG = (D + 63) / 64, REGION = kPagedTile * 128, TILE = KREG * REGION;
   static constexpr int QREGION = 128 * 128;
-  static constexpr int STAGES = D == 256 ? 2 : D == 64 ? 8 : 5;
+  static constexpr int STAGES = E8 ? (D == 64 ? 5 : 3) : D == 256 ? 2 : D == 64 ? 8 : 5;
+  struct Raw {  // tiles as they are held
+    static constexpr bool E8 = true;
+    static constexpr int COLS = 128, KREG = (D_ + 127) / 128, REGION = kPagedTile * 128, TILE = KREG * REGION;
+    static constexpr int STAGES = 4, PRODUCERS = PagedTcCfg::PRODUCERS;
+  };
   static constexpr int MC = D == 96 ? 48 : 64;   // columns merged at a time (all at once would cost a stage)
   static constexpr int OP = MC + 4;              // row pitch of the merge buffer (floats)
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
   static constexpr int OFF_O = OFF_Q + KREG * QREGION;
   static constexpr int OFF_ML = OFF_O + (COPIES > 1 ? ROWS * OP * 4 : 0);  // [warpgroup][copies][rows]
-  static constexpr int SMEM_BYTES = OFF_ML + SOFT * 8 + 1024;
+  static constexpr int OFF_RAW = (OFF_ML + SOFT * 8 + 1023) / 1024 * 1024;
+  static constexpr int SMEM_BYTES = (E8 ? OFF_RAW + Raw::STAGES * 2 * Raw::TILE : OFF_ML + SOFT * 8) + 1024;
+  // E8: weights are up to 2^8 and parts of scales at most 1; times this they stay within
+  // fp16, and what a small part leaves of its digits is 2^-31 of the largest scale
+  static constexpr float LIFT = 128.f;
   static_assert(SMEM_BYTES <= 229000, "shared memory");
   // TMEM columns
   __host__ __device__ static constexpr int S_COL(int b) { return kPagedTile * b; }
@@ -127,6 +143,14 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   __shared__ ItemLens item_lens[kItemWindow];
   __shared__ int abort_flag;
   __shared__ uint32_t tmem_slot;
+  // E8: the ring of tiles as they are held, scales of a stage's 16 keys, of query rows, and the
+  // accumulators' units
+  using Raw = typename C::Raw;
+  constexpr int RAW = C::E8 ? Raw::STAGES : 1;
+  __shared__ __align__(8) uint64_t raw_full[RAW], raw_empty[RAW];
+  __shared__ int raw_pos[RAW][kPagedKeyWarps];
+  __shared__ float2 raw_scale[RAW][kPagedKeyWarps], kv_scale[C::E8 ? C::STAGES : 1][kPagedKeyWarps];
+  __shared__ float row_scale[C::E8 ? C::ROWS : 1], units[C::E8 ? C::SOFT : 1];
   constexpr int D = C::D;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -136,8 +160,12 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&full[i]), C::E8 ? 4 : 1);  // the converters' warps
       mbar_init(smem_u32(&empty[i]), 1);
+    }
+    for (int i = 0; i < RAW; ++i) {
+      mbar_init(smem_u32(&raw_full[i]), 1 + kPagedKeyWarps);  // the tile, and the scales of each 16 keys
+      mbar_init(smem_u32(&raw_empty[i]), 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&s_full[b]), 1);
@@ -171,17 +199,77 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   // Every warp walks the share to its end, whether or not its waits gave up: the window
   // moves on with all of them.
 
-  if (warp >= 4 * C::WGS && warp < C::SCORE_WARP) {
+  if (C::E8 && warp >= 4 * C::WGS) regs_release<C::REG_REST>();
+  if (C::E8 && warp >= C::CONVERT_WARP) {
+    // --------------------------------------------------------------- converters
+    // A thread takes a row's 64 columns (D 64: 32), 16 at a time; threads of one row in another
+    // order, so that neither reads nor writes meet in a bank.
+    bool ok = true;
+    const int ct = threadIdx.x - 32 * C::CONVERT_WARP, row = ct >> 1, half = ct & 1;
+    constexpr int CHUNKS = D / 32;  // of 16 columns, per thread
+    int gi = 0;
+    Walk w;
+    for (bool more = w.start(list, share, window); more; more = w.next(list, window)) {
+      for (int t = w.t0; t < w.t1 && ok; ++t, ++gi) {
+        const int from = gi % RAW, to = gi % C::STAGES;
+        ok = mbar_wait(smem_u32(&raw_full[from]), (gi / RAW) & 1, tmo, &abort_flag, p.wc.status) &&
+             (gi < C::STAGES || mbar_wait(smem_u32(&empty[to]), (gi / C::STAGES - 1) & 1, tmo, &abort_flag, p.wc.status));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (ct < kPagedKeyWarps) {
+          key_pos[to][ct] = raw_pos[from][ct] & ~kSeenByAll;
+          kv_scale[to][ct] = raw_scale[from][ct];
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {  // keys, values
+          const uint8_t* src = smem + C::OFF_RAW + (2 * from + v) * Raw::TILE;
+          uint8_t* dst = smem + C::OFF_KV + (2 * to + v) * C::TILE;
+          uint4 x[CHUNKS];
+          auto chunk = [&](int j) { return half * CHUNKS + (half && CHUNKS == 4 ? j ^ 2 : j); };
+#pragma unroll
+          for (int j = 0; j < CHUNKS; ++j) x[j] = *reinterpret_cast<const uint4*>(src + sw128_offset(row, chunk(j)));
+#pragma unroll
+          for (int j = 0; j < CHUNKS; ++j) {
+            uint32_t y[8];
+            const uint32_t words[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f16_of(words[e], y[2 * e], y[2 * e + 1]);
+            const int ch = 2 * chunk(j);  // of 8 columns
+            uint8_t* at = dst + (ch >> 3) * C::REGION;
+            *reinterpret_cast<uint4*>(at + sw128_offset(row, ch & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(at + sw128_offset(row, (ch + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&full[to]));
+          mbar_arrive(smem_u32(&raw_empty[from]));
+        }
+      }
+    }
+  } else if (warp >= 4 * C::WGS && warp < C::SCORE_WARP) {
     // ----------------------------------------------------------- producer warps
-    TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag, warp - 4 * C::WGS);
-    produce_share<C>(p, list, share, window, ring);
-    ring.drain();
+    if constexpr (C::E8) {
+      TileRing<Raw> ring(p, map_k, map_v, sbase + C::OFF_RAW, raw_full, raw_empty, raw_pos, &abort_flag, warp - 4 * C::WGS,
+                         raw_scale);
+      produce_share<Raw>(p, list, share, window, ring);
+      ring.drain();
+    } else {
+      TileRing<C> ring(p, map_k, map_v, sbase + C::OFF_KV, full, empty, key_pos, &abort_flag, warp - 4 * C::WGS);
+      produce_share<C>(p, list, share, window, ring);
+      ring.drain();
+    }
+  } else if (C::E8 && warp >= C::SCORE_WARP + 2) {
+    // (a warp that fills the warpgroup: it goes with the window)
+    Walk w;
+    for (bool more = w.start(list, share, window); more;) more = w.next(list, window);
   } else if (warp >= C::SCORE_WARP) {
     // -------------------------------------------------------------- MMA issuers
     // (all lanes compute the descriptors and one issues)
     const bool leader = elect_one_sync(), scores = warp == C::SCORE_WARP;
-    constexpr uint32_t idesc_s = make_idesc_f16(128, kPagedTile, C::BF16 ? 1 : 0, 0, 0);
-    constexpr uint32_t idesc_o = make_idesc_f16(128, D, C::BF16 ? 1 : 0, 0, 1);
+    constexpr uint32_t idesc_s = make_idesc_f16(128, kPagedTile, C::MMA_BF16 ? 1 : 0, 0, 0);
+    constexpr uint32_t idesc_o = make_idesc_f16(128, D, C::MMA_BF16 ? 1 : 0, 0, 1);
     bool ok = true;
     auto wait = [&](uint64_t& bar, int parity) {
       ok = ok && mbar_wait_poll(smem_u32(&bar), parity & 1, tmo, &abort_flag, p.wc.status);
@@ -224,7 +312,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             const uint64_t vd = make_sdesc(kv + C::TILE + kk * 16 * 128, C::REGION, 1024, 2);
             const uint32_t pc = tmem + C::P_COL(b) + kk * 8;
             if (leader) mma_ts(tmem + C::O_COL(C::WGS > 1 ? b : 0), pc, vd, idesc_o, 1);
-            if (leader) mma_ts(tmem + C::O_COL(C::WGS > 1 ? b : 0), pc + C::P_LO, vd, idesc_o, 1);
+            if (C::TWO_WORDS && leader) mma_ts(tmem + C::O_COL(C::WGS > 1 ? b : 0), pc + C::P_LO, vd, idesc_o, 1);
           }
           if (leader) mma_commit(smem_u32(&o_ready[b]));
           if (leader) mma_commit(smem_u32(&empty[slot]));
@@ -237,6 +325,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     mbar_wait(smem_u32(&drained), 0, p.wc.drain_cycles, nullptr, p.wc.status);
   } else {
     // ------------------------------------------------------------------ softmax
+    if constexpr (C::E8) regs_claim<C::REG_SOFT>();
     const int tid = threadIdx.x, wg = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const int copy = quarter / C::RG, row = tid % C::ROWS;
@@ -269,29 +358,58 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       const int tok = (rb * C::ROWS + row) % p.Tq, pos = p_lo + tok;
       // queries, every copy; rows behind the last one zero
       constexpr int CHUNKS = C::ROWS * (D / 8), LOADS = (CHUNKS + C::SOFT - 1) / C::SOFT;
-      uint4 x[LOADS];
+      constexpr int WARP_ROWS = C::ROWS / (4 * C::WGS);  // E8: whole rows to a warp
+      uint4 x[C::E8 ? WARP_ROWS : LOADS];
+      if constexpr (C::E8) {
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) {  // all under way at once
-        const int at = tid + i * C::SOFT, r = at / (D / 8);
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (r < rows) x[i] = reinterpret_cast<const uint4*>(p.q + row0 * D)[at];
+        for (int i = 0; i < WARP_ROWS; ++i) {
+          const int r = warp + i * 4 * C::WGS;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (r < rows && lane < D / 8) x[i] = reinterpret_cast<const uint4*>(p.q + (row0 + r) * D)[lane];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {  // all under way at once
+          const int at = tid + i * C::SOFT, r = at / (D / 8);
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (r < rows) x[i] = reinterpret_cast<const uint4*>(p.q + row0 * D)[at];
+        }
       }
       {
         const uint32_t zero[32] = {};
 #pragma unroll
         for (int col = 0; col < D; col += 32) tmem_store(lanes + C::O_COL(wg) + col, zero);
       }
+      if constexpr (C::E8) {
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        const int at = tid + i * C::SOFT, r = at / (D / 8), ch = at - r * (D / 8);
-        if (at >= CHUNKS) break;
+        for (int i = 0; i < WARP_ROWS; ++i) {
+          const int r = warp + i * 4 * C::WGS;
+          const float undo = row_f16<C::BF16>(x[i]);
+          if (lane == 0) row_scale[r] = undo;
+          if (lane < D / 8) {
 #pragma unroll
-        for (int k = 0; k < C::COPIES; ++k)
-          *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(k * C::ROWS + r, ch & 7)) = x[i];
+            for (int k = 0; k < C::COPIES; ++k)
+              *reinterpret_cast<uint4*>(smem + C::OFF_Q + (lane >> 3) * C::QREGION + sw128_offset(k * C::ROWS + r, lane & 7)) = x[i];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+          const int at = tid + i * C::SOFT, r = at / (D / 8), ch = at - r * (D / 8);
+          if (at >= CHUNKS) break;
+#pragma unroll
+          for (int k = 0; k < C::COPIES; ++k)
+            *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * C::QREGION + sw128_offset(k * C::ROWS + r, ch & 7)) = x[i];
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&q_ready));
+      float own_scale = 1.f, unit = 0.f;  // E8: of this row; what its sums are in units of, less LIFT
+      if constexpr (C::E8) {
+        sync_rows();  // other warps have staged this row
+        own_scale = row_scale[row];
+      }
       // The row's running maximum among unscaled scores. An exponent is (s - top) scale: the
       // difference of near scores is exact, so that it is 0 for the maximum, however large
       // (s scale - m in one rounding is not, where the steps of m are large).
@@ -343,6 +461,36 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           if (lane == 0) mbar_arrive(smem_u32(&s_free[b]));
         };
         if (!differ) free_scores();  // (else they may be read again below)
+        float part[C::E8 ? C::RG : 1], lower = 1.f;  // of `unit`, of each 16 keys; what the sums so far are to be multiplied by
+        if constexpr (C::E8) {
+          float most = 0.f;
+          float2 sc[C::RG];
+#pragma unroll
+          for (int q = 0; q < C::RG; ++q) {
+            sc[q] = kv_scale[slot][copy * C::RG + q];
+            // (keys that were not loaded have no scale)
+            if (key_pos[slot][copy * C::RG + q] == kNoPosition) sc[q] = make_float2(1.f, 0.f);
+            most = fmaxf(most, sc[q].y);
+          }
+          if (most > unit) {
+            lower = unit * inverse_power(most);
+            unit = most;
+          }
+          const float inverse = unit > 0.f ? inverse_power(unit) : 0.f;
+#pragma unroll
+          for (int q = 0; q < C::RG; ++q) {
+            part[q] = sc[q].y * inverse * C::LIFT;
+            const float f = own_scale * sc[q].x;
+            if (f > 1e-36f && f < 1e36f) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) sv[16 * q + e] = __float_as_uint(__uint_as_float(sv[16 * q + e]) * f);
+            } else {  // the smaller one first, so that it is only the score that can leave the range
+              const float f0 = fminf(own_scale, sc[q].x), f1 = fmaxf(own_scale, sc[q].x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) sv[16 * q + e] = __float_as_uint(__uint_as_float(sv[16 * q + e]) * f0 * f1);
+            }
+          }
+        }
         if (!all_seen) {
 #pragma unroll
           for (int q = 0; q < C::RG; ++q) {
@@ -360,13 +508,14 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
 #pragma unroll
         for (int e = 0; e < C::KEYS; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sv[e]));
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), rise = (mx - top) * p.scale_log2;
-        const bool grow = rise > kPagedSlack;
+        const bool rises = rise > kPagedSlack, grow = rises || (C::E8 && lower != 1.f);
         float alpha = 1.f;
-        if (grow) {
+        if (rises) {
           alpha = ex2(-rise);
           top = mx;
           l *= alpha;
         }
+        if constexpr (C::E8) alpha *= lower;
         const uint64_t top2 = pair_of(-top);
         // weights in two words of the cache's type (see the other kernel)
         uint32_t hi[C::KEYS / 2], lo[C::KEYS / 2];
@@ -374,18 +523,24 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
 #pragma unroll
         for (int e = 0; e < C::KEYS / 2; ++e) {
           const float2 x = add_mul2(sv[2 * e], sv[2 * e + 1], top2, scale2);
-          const float p0 = ex2(x.x), p1 = ex2(x.y);
+          float p0 = ex2(x.x), p1 = ex2(x.y);
           sum[0] += p0;
           sum[1] += p1;
-          hi[e] = pack2<C::BF16>(p0, p1);
-          const float2 f = unpack2<C::BF16>(hi[e]);
-          lo[e] = pack2<C::BF16>(p0 - f.x, p1 - f.y);
+          if constexpr (C::E8) {
+            p0 *= part[e / 8];
+            p1 *= part[e / 8];
+          }
+          hi[e] = pack2<C::MMA_BF16>(p0, p1);
+          if constexpr (C::TWO_WORDS) {
+            const float2 f = unpack2<C::MMA_BF16>(hi[e]);
+            lo[e] = pack2<C::MMA_BF16>(p0 - f.x, p1 - f.y);
+          }
         }
         l += sum[0] + sum[1];
         if (!p_idle) wait_products(gi - 2);  // they read this buffer's last P
         if (!ok) break;
         tmem_store(lanes + C::P_COL(b) + copy * (C::KEYS / 2), hi);
-        tmem_store(lanes + C::P_COL(b) + C::P_LO + copy * (C::KEYS / 2), lo);
+        if constexpr (C::TWO_WORDS) tmem_store(lanes + C::P_COL(b) + C::P_LO + copy * (C::KEYS / 2), lo);
         if (gi - C::WGS >= begin && __any_sync(0xffffffffu, grow)) {
           if (C::WGS == 1) wait_products(gi - 1);  // they add to O
           if (!ok) break;
@@ -411,18 +566,19 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             return kept(j) && ((p.causal && j > p_lo) || (p.window > 0 && j <= p_hi - p.window && j >= p.sinks));
           };
           const int own = key_pos[slot][quarter];
+          constexpr int ROW = D / 8;
           auto chunk = [&](int i) {  // 16 bytes of this warp's keys
-            const int e = i / (8 * C::KREG), x = i - e * 8 * C::KREG;
-            return v_rows + (x >> 3) * C::REGION + (16 * quarter + e) * 128 + (x & 7) * 16;
+            const int e = i / ROW, x = i - e * ROW;
+            return v_rows + (x >> 3) * C::REGION + sw128_offset(16 * quarter + e, x & 7);
           };
           bool apart = false;
           if (differ) {
             uint32_t odd = 0;
-            for (int i = lane; i < 16 * 8 * C::KREG; i += 32) {
-              if (!partial(own + i / (8 * C::KREG))) continue;
+            for (int i = lane; i < 16 * ROW; i += 32) {
+              if (!partial(own + i / ROW)) continue;
               const uint4 x = *reinterpret_cast<const uint4*>(chunk(i));
-              odd |= not_finite2<C::BF16>(x.x) | not_finite2<C::BF16>(x.y) | not_finite2<C::BF16>(x.z) |
-                     not_finite2<C::BF16>(x.w);
+              odd |= not_finite2<C::MMA_BF16>(x.x) | not_finite2<C::MMA_BF16>(x.y) | not_finite2<C::MMA_BF16>(x.z) |
+                     not_finite2<C::MMA_BF16>(x.w);
             }
             odd = __any_sync(0xffffffffu, odd != 0);
             int* flags = odd_flags[wg][meets & 1];
@@ -437,10 +593,16 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
               for (int e = 0; e < C::KEYS; ++e) {
                 const int key = copy * C::KEYS + e, j = key_pos[slot][key >> 4] + (key & 15);
                 if (!partial(j)) continue;
-                const float s = __uint_as_float(tmem_ld1(lanes + C::S_COL(b) + key));
+                float s = __uint_as_float(tmem_ld1(lanes + C::S_COL(b) + key));
                 tmem_ld_wait();
+                float share = 1.f;
+                if constexpr (C::E8) {
+                  const float2 sc = kv_scale[slot][key >> 4];
+                  s = s * fminf(own_scale, sc.x) * fmaxf(own_scale, sc.x);
+                  share = sc.y * inverse_power(unit) * C::LIFT;
+                }
                 const bool seen = !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window && j >= p.sinks);
-                const float x = ex2((s - top) * p.scale_log2);
+                const float x = ex2((s - top) * p.scale_log2) * share;
 #pragma unroll 1
                 for (int col = 0; col < D; col += 32) {
                   uint32_t o[32];
@@ -449,7 +611,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
 #pragma unroll
                   for (int i = 0; i < 32; i += 2) {
                     const int at = col + i;
-                    const float2 v = unpack2<C::BF16>(*reinterpret_cast<const uint32_t*>(
+                    const float2 v = unpack2<C::MMA_BF16>(*reinterpret_cast<const uint32_t*>(
                         v_rows + (at >> 6) * C::REGION + sw128_offset(key, (at & 63) >> 3) + (at & 7) * 2));
                     if (seen) {
                       o[i] = __float_as_uint(fmaf(x, v.x, __uint_as_float(o[i])));
@@ -465,8 +627,8 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             }
             free_scores();
           }
-          for (int i = lane; i < 16 * 8 * C::KREG; i += 32) {
-            const int j = own + i / (8 * C::KREG);
+          for (int i = lane; i < 16 * ROW; i += 32) {
+            const int j = own + i / ROW;
             if (!kept(j) || (apart && partial(j))) *reinterpret_cast<uint4*>(chunk(i)) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -496,12 +658,17 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       const bool begins = w.t0 == 0, ends = w.t1 == w.it.tiles;
       const int part_slot = 2 * part + (begins ? 1 : 0);
       mls[tid] = make_float2(m, l);  // [warpgroup][copy][row]
+      if constexpr (C::E8) units[tid] = unit / C::LIFT;
       sync_rows();
       const float2 ml0 = mls[tid & 127], ml1 = mls[128 * (C::WGS - 1) + (tid & 127)];
       float mt = -INFINITY;
 #pragma unroll
       for (int k = 0; k < C::WGS * C::COPIES; ++k) mt = fmaxf(mt, mls[k * C::ROWS + row].x);
-      const float f0 = exp2_rel(ml0.x, mt), f1 = exp2_rel(ml1.x, mt);
+      float f0 = exp2_rel(ml0.x, mt), f1 = exp2_rel(ml1.x, mt);
+      if constexpr (C::E8) {
+        f0 *= units[tid & 127];
+        f1 *= units[128 * (C::WGS - 1) + (tid & 127)];
+      }
       // columns [16 i, 16 i + 16) of this lane's row over the warpgroups
       auto sum16 = [&](int i, float4 (&x)[4]) {
         uint32_t o0[16], o1[16];

@@ -337,12 +337,13 @@ def test_attend_over_selected_pages(D, page, window):
                              sel, count, held=True))
 
 
-@pytest.mark.parametrize("rep,T", [(4, 1), (3, 4), (16, 2), (8, 8)])
-def test_attend_with_values_that_are_no_numbers(rep, T):
+@pytest.mark.parametrize("rep,T,L,window", [(4, 1, 200, 60), (3, 4, 200, 60), (16, 2, 200, 60), (8, 8, 200, 60), (4, 2, 9500, 9000),
+                                            (16, 2, 9500, 9000), (8, 8, 9500, 9000), (32, 4, 9500, 9000)])
+def test_attend_with_values_that_are_no_numbers(rep, T, L, window):
     """NaN in keys and values that some rows see and others do not reaches only those that see it; pages whose scales are
     2^60 apart; queries of every size, zeros among them."""
     g = gen(rep * 10 + T)
-    B, Hkv, D, page, L = 2, 2, 128, 16, 200
+    B, Hkv, D, page = 2, 2, 128, 16
     table, P = make_table(g, B, -(-L // page))
     (k_pool, ks), (v_pool, vs) = held_pool(g, P, Hkv, page, D, 1.0), held_pool(g, P, Hkv, page, D, 20.0)
     lens = [L, L - 5]
@@ -355,10 +356,10 @@ def test_attend_with_values_that_are_no_numbers(rep, T):
         v_pool.view(torch.uint8)[int(table[b, first // page]), 0, first % page, 5] = 127
         k_pool.view(torch.uint8)[int(table[b, last // page]), 1, last % page, 9] = 255
     kv = handle(k_pool, v_pool, ks, vs, table, i32(lens))
-    o, lse = attend(kv, q, 0.1, True, 60, 4)
+    o, lse = attend(kv, q, 0.1, True, window, 4)
     assert clear()
     kd, vd = ref.held_value(k_pool, ks), ref.held_value(v_pool, vs)
-    ro, rl, bo, bl = ref.attend(q, kd.nan_to_num(0.0), vd.nan_to_num(0.0), table, lens, 0.1, True, 60, 4, held=True)
+    ro, rl, bo, bl = ref.attend(q, kd.nan_to_num(0.0), vd.nan_to_num(0.0), table, lens, 0.1, True, window, 4, held=True)
     o, lse = o.double().cpu(), lse.double().cpu()
     nan_o = torch.zeros(o.shape, dtype=torch.bool)
     nan_o[:, :rep, :, 5] = True        # every token sees the first one's value
