@@ -54,7 +54,7 @@ struct PagedTcCfg {
   static constexpr int KEYS = kPagedTile / COPIES;  // of a tile that a copy takes
   // (128 rows, where the softmax bounds the kernel, D 128: 68.8 us with one producer,
   // 75.2 with two; 64 rows, D 64 in pages of 16: 92.9 and 72.5)
-  static constexpr int PRODUCERS = RG == 4 || D == 256 ? 1 : 2;
+  static constexpr int PRODUCERS = (RG == 4 && !E8) || D == 256 ? 1 : 2;
   // D = 256: one accumulator is all that TMEM holds beside the scores and weights, and a
   // tile's bytes take longer than the softmax's chain
   static constexpr int WGS = D == 256 ? 1 : 2;
@@ -65,22 +65,25 @@ struct PagedTcCfg {
   static constexpr int REG_NEEDED = E8 ? SOFT * REG_SOFT + 256 * REG_REST : 0;
   static constexpr int COLS = 64, KREG = (D + 63) / 64, REGION = kPagedTile * 128, TILE = KREG * REGION;
   static constexpr int QREGION = 128 * 128;
-  static constexpr int STAGES = E8 ? (D == 64 ? 5 : 3) : D == 256 ? 2 : D == 64 ? 8 : 5;
+  static constexpr int STAGES = E8 ? (D == 64 ? 6 : 4) : D == 256 ? 2 : D == 64 ? 8 : 5;
   struct Raw {  // tiles as they are held
     static constexpr bool E8 = true;
     static constexpr int COLS = 128, KREG = (D_ + 127) / 128, REGION = kPagedTile * 128, TILE = KREG * REGION;
-    static constexpr int STAGES = 4, PRODUCERS = PagedTcCfg::PRODUCERS;
+    static constexpr int STAGES = D_ == 64 ? 5 : 3, PRODUCERS = PagedTcCfg::PRODUCERS;
   };
   static constexpr int MC = D == 96 ? 48 : 64;   // columns merged at a time (all at once would cost a stage)
   static constexpr int OP = MC + 4;              // row pitch of the merge buffer (floats)
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
-  static constexpr int OFF_O = OFF_Q + KREG * QREGION;
-  static constexpr int OFF_ML = OFF_O + (COPIES > 1 ? ROWS * OP * 4 : 0);  // [warpgroup][copies][rows]
+  // (E8: over the queries, which nobody reads then)
+  static constexpr int Q_BYTES = KREG * QREGION, O_BYTES = COPIES > 1 ? ROWS * OP * 4 : 0;
+  static constexpr int OFF_O = E8 ? OFF_Q : OFF_Q + Q_BYTES;
+  static constexpr int OFF_ML = E8 ? OFF_Q + (Q_BYTES > O_BYTES ? Q_BYTES : O_BYTES) : OFF_O + O_BYTES;  // [warpgroup][copies][rows]
   static constexpr int OFF_RAW = (OFF_ML + SOFT * 8 + 1023) / 1024 * 1024;
   static constexpr int SMEM_BYTES = (E8 ? OFF_RAW + Raw::STAGES * 2 * Raw::TILE : OFF_ML + SOFT * 8) + 1024;
   // E8: weights are up to 2^8 and parts of scales at most 1; times this they stay within
   // fp16, and what a small part leaves of its digits is 2^-31 of the largest scale
+  static constexpr int LIFT_LOG2 = 7;
   static constexpr float LIFT = 128.f;
   static_assert(SMEM_BYTES <= 229000, "shared memory");
   // TMEM columns
@@ -122,6 +125,14 @@ __device__ __forceinline__ uint64_t pair_of(float x) {
   asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float2 fma2(uint32_t a, uint32_t b, uint64_t f, uint64_t c, uint64_t g, uint64_t d) {  // ((a, b) f + c) g + d
+  float2 r;
+  asm("{\n .reg .b64 x;\n"
+      " mov.b64 x, {%2, %3};\n fma.rn.f32x2 x, x, %4, %5;\n fma.rn.f32x2 x, x, %6, %7;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(a), "r"(b), "l"(f), "l"(c), "l"(g), "l"(d));
+  return r;
+}
 __device__ __forceinline__ float2 add_mul2(uint32_t a, uint32_t b, uint64_t c, uint64_t f) {
   float2 r;
   asm("{\n .reg .b64 x;\n"
@@ -150,6 +161,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   __shared__ __align__(8) uint64_t raw_full[RAW], raw_empty[RAW];
   __shared__ int raw_pos[RAW][kPagedKeyWarps];
   __shared__ float2 raw_scale[RAW][kPagedKeyWarps], kv_scale[C::E8 ? C::STAGES : 1][kPagedKeyWarps];
+  __shared__ bool seen[C::E8 ? C::STAGES : 1];  // all keys of the stage, by every row
   __shared__ float row_scale[C::E8 ? C::ROWS : 1], units[C::E8 ? C::SOFT : 1];
   constexpr int D = C::D;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -212,13 +224,22 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     for (bool more = w.start(list, share, window); more; more = w.next(list, window)) {
       for (int t = w.t0; t < w.t1 && ok; ++t, ++gi) {
         const int from = gi % RAW, to = gi % C::STAGES;
-        ok = mbar_wait(smem_u32(&raw_full[from]), (gi / RAW) & 1, tmo, &abort_flag, p.wc.status) &&
-             (gi < C::STAGES || mbar_wait(smem_u32(&empty[to]), (gi / C::STAGES - 1) & 1, tmo, &abort_flag, p.wc.status));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        const uint32_t bar_raw = smem_u32(&raw_full[from]), bar_to = smem_u32(&empty[to]);
+        const bool there = mbar_test_wait(bar_raw, (gi / RAW) & 1);
+        const bool room = gi < C::STAGES || mbar_test_wait(bar_to, (gi / C::STAGES - 1) & 1);
+        if (!__all_sync(0xffffffffu, there && room)) {
+          ok = mbar_wait(bar_raw, (gi / RAW) & 1, tmo, &abort_flag, p.wc.status) &&
+               (gi < C::STAGES || mbar_wait(bar_to, (gi / C::STAGES - 1) & 1, tmo, &abort_flag, p.wc.status));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
         if (ct < kPagedKeyWarps) {
-          key_pos[to][ct] = raw_pos[from][ct] & ~kSeenByAll;
-          kv_scale[to][ct] = raw_scale[from][ct];
+          const int j0 = raw_pos[from][ct];
+          const bool every = __all_sync(0xfu, (j0 & kSeenByAll) != 0);
+          if (ct == 0) seen[to] = every;
+          key_pos[to][ct] = j0 & ~kSeenByAll;
+          // (keys that were not loaded have no scale)
+          kv_scale[to][ct] = j0 == kNoPosition ? make_float2(1.f, 0.f) : raw_scale[from][ct];
         }
 #pragma unroll
         for (int v = 0; v < 2; ++v) {  // keys, values
@@ -445,14 +466,39 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         // does every row see all keys of a group; does some group hide keys from some
         // rows only
         bool all_seen = true, differ = false;
+        if (!C::E8 || !seen[slot]) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int j0 = j0s[q];
-          all_seen &= j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) &&
-                      !(p.window > 0 && j0 <= p_hi - p.window && j0 + 15 >= p.sinks);
-          differ |= n > 1 && j0 < len &&
-                    ((p.causal && j0 + 15 > p_lo) ||
-                     (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
+          for (int q = 0; q < 4; ++q) {
+            const int j0 = j0s[q];
+            all_seen &= j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) &&
+                        !(p.window > 0 && j0 <= p_hi - p.window && j0 + 15 >= p.sinks);
+            differ |= n > 1 && j0 < len &&
+                      ((p.causal && j0 + 15 > p_lo) ||
+                       (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
+          }
+        }
+        // E8, of each 16 keys: what their scores are to be multiplied by, and the power of two
+        // that takes their weights to `unit` (with LIFT). `lower`: what the sums so far are to
+        // be multiplied by.
+        constexpr int GROUPS = C::E8 ? C::RG : 1;
+        float key_scale[GROUPS], factor[GROUPS], power[GROUPS], lower = 1.f;
+        if constexpr (C::E8) {
+          float most = 0.f, value_scale[GROUPS];
+#pragma unroll
+          for (int q = 0; q < C::RG; ++q) {
+            const float2 sc = kv_scale[slot][copy * C::RG + q];
+            key_scale[q] = sc.x;
+            value_scale[q] = sc.y;
+            factor[q] = own_scale * sc.x;
+            most = fmaxf(most, sc.y);
+          }
+          if (most > unit) {
+            lower = unit * inverse_power(most);
+            unit = most;
+          }
+#pragma unroll
+          for (int q = 0; q < C::RG; ++q)
+            power[q] = static_cast<float>((__float_as_int(value_scale[q]) >> 23) - (__float_as_int(unit) >> 23) + C::LIFT_LOG2);
         }
         tmem_ld_wait();
         auto free_scores = [&] {
@@ -461,35 +507,16 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           if (lane == 0) mbar_arrive(smem_u32(&s_free[b]));
         };
         if (!differ) free_scores();  // (else they may be read again below)
-        float part[C::E8 ? C::RG : 1], lower = 1.f;  // of `unit`, of each 16 keys; what the sums so far are to be multiplied by
         if constexpr (C::E8) {
-          float most = 0.f;
-          float2 sc[C::RG];
 #pragma unroll
-          for (int q = 0; q < C::RG; ++q) {
-            sc[q] = kv_scale[slot][copy * C::RG + q];
-            // (keys that were not loaded have no scale)
-            if (key_pos[slot][copy * C::RG + q] == kNoPosition) sc[q] = make_float2(1.f, 0.f);
-            most = fmaxf(most, sc[q].y);
-          }
-          if (most > unit) {
-            lower = unit * inverse_power(most);
-            unit = most;
-          }
-          const float inverse = unit > 0.f ? inverse_power(unit) : 0.f;
-#pragma unroll
-          for (int q = 0; q < C::RG; ++q) {
-            part[q] = sc[q].y * inverse * C::LIFT;
-            const float f = own_scale * sc[q].x;
-            if (f > 1e-36f && f < 1e36f) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) sv[16 * q + e] = __float_as_uint(__uint_as_float(sv[16 * q + e]) * f);
-            } else {  // the smaller one first, so that it is only the score that can leave the range
-              const float f0 = fminf(own_scale, sc[q].x), f1 = fmaxf(own_scale, sc[q].x);
+          for (int q = 0; q < C::RG; ++q)
+            if (!(factor[q] > 1e-36f && factor[q] < 1e36f)) {
+              // the smaller one first, so that it is only the score that can leave the range
+              const float f0 = fminf(own_scale, key_scale[q]), f1 = fmaxf(own_scale, key_scale[q]);
 #pragma unroll
               for (int e = 0; e < 16; ++e) sv[16 * q + e] = __float_as_uint(__uint_as_float(sv[16 * q + e]) * f0 * f1);
+              factor[q] = 1.f;
             }
-          }
         }
         if (!all_seen) {
 #pragma unroll
@@ -505,8 +532,18 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if constexpr (C::E8) {
 #pragma unroll
-        for (int e = 0; e < C::KEYS; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sv[e]));
+          for (int q = 0; q < C::RG; ++q) {
+            float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m2[e & 1] = fmaxf(m2[e & 1], __uint_as_float(sv[16 * q + e]));
+            m4[q] = fmaxf(m2[0], m2[1]) * factor[q];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < C::KEYS; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sv[e]));
+        }
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), rise = (mx - top) * p.scale_log2;
         const bool rises = rise > kPagedSlack, grow = rises || (C::E8 && lower != 1.f);
         float alpha = 1.f;
@@ -519,16 +556,28 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         const uint64_t top2 = pair_of(-top);
         // weights in two words of the cache's type (see the other kernel)
         uint32_t hi[C::KEYS / 2], lo[C::KEYS / 2];
-        float sum[2] = {0.f, 0.f};
+        float sum[2] = {0.f, 0.f}, own[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < C::KEYS / 2; ++e) {
-          const float2 x = add_mul2(sv[2 * e], sv[2 * e + 1], top2, scale2);
-          float p0 = ex2(x.x), p1 = ex2(x.y);
-          sum[0] += p0;
-          sum[1] += p1;
+          // E8: the power goes into the exponent, and out of the sum of these 16 weights. (Below
+          // 2^-40 a weight, at most 2^8, is 0 in fp16 anyway: the sum is taken by itself.)
+          const int q = C::E8 ? e / 8 : 0;
+          float2 x;
+          if constexpr (C::E8)
+            x = fma2(sv[2 * e], sv[2 * e + 1], pair_of(factor[q]), top2, scale2, pair_of(power[q] < -40.f ? 0.f : power[q]));
+          else
+            x = add_mul2(sv[2 * e], sv[2 * e + 1], top2, scale2);
+          const float p0 = ex2(x.x), p1 = ex2(x.y);
           if constexpr (C::E8) {
-            p0 *= part[e / 8];
-            p1 *= part[e / 8];
+            own[0] = e % 8 ? own[0] + p0 : p0;
+            own[1] = e % 8 ? own[1] + p1 : p1;
+            if (e % 8 == 7) {
+              const float undo = power[q] < -40.f ? 1.f : __int_as_float((127 - static_cast<int>(power[q])) << 23);
+              sum[0] = fmaf(own[0] + own[1], undo, sum[0]);
+            }
+          } else {
+            sum[0] += p0;
+            sum[1] += p1;
           }
           hi[e] = pack2<C::MMA_BF16>(p0, p1);
           if constexpr (C::TWO_WORDS) {
@@ -537,6 +586,17 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           }
         }
         l += sum[0] + sum[1];
+        if constexpr (C::E8) {
+#pragma unroll
+          for (int q = 0; q < C::RG; ++q)
+            if (power[q] < -40.f) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                hi[8 * q + e] = 0;
+                if constexpr (C::TWO_WORDS) lo[8 * q + e] = 0;
+              }
+            }
+        }
         if (!p_idle) wait_products(gi - 2);  // they read this buffer's last P
         if (!ok) break;
         tmem_store(lanes + C::P_COL(b) + copy * (C::KEYS / 2), hi);
