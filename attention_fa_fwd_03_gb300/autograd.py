@@ -1,4 +1,4 @@
-"""Differentiable attention: a ``torch.autograd.Function`` over the C ABI.
+"""Differentiable attention: a node of PyTorch's graph over the C ABI.
 
 Follows page "mlx-bun 0.0.4: package/src/model/flash-attention.ts", section
 "Differentiable op: flash forward + manual backward via CustomVjp": the
@@ -13,6 +13,10 @@ back to another attention op. Only argument marshalling happens here: output
 and workspace tensors are allocated by PyTorch, every step of the computation
 runs in the library's kernels, and there is no CPU path (a CPU tensor raises).
 
+``flash_attention`` is the compiled node (csrc/autograd_binding.h), whose
+backward does not wait for the interpreter's lock; ``FlashAttention`` is the
+same calls as a ``torch.autograd.Function``, for code that builds on one.
+
     from attention_fa_fwd_03_gb300.autograd import flash_attention
     o = flash_attention(q, k, v, causal=True)          # q [B,Hq,Tq,D], k/v [B,Hkv,Tkv,D]
     o.backward(do)                                      # fills q.grad, k.grad, v.grad
@@ -23,7 +27,7 @@ import math
 
 import torch
 
-from . import fa_bwd, fa_bwd_sinks_workspace_size, fa_bwd_workspace_size, fa_fwd
+from . import _paged_calls, fa_bwd, fa_bwd_sinks_workspace_size, fa_bwd_workspace_size, fa_fwd
 
 __all__ = ["FlashAttention", "flash_attention"]
 
@@ -72,6 +76,6 @@ def flash_attention(q, k, v, scale: float | None = None, causal: bool = False, w
     """
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
-    q, k, v = (t.contiguous() for t in (q, k, v))
-    o, lse = FlashAttention.apply(q, k, v, float(scale), bool(causal), int(window), int(sinks))
+    o, lse = _paged_calls().attention(q.contiguous(), k.contiguous(), v.contiguous(), float(scale), bool(causal),
+                                      int(window), int(sinks))
     return (o, lse) if return_lse else o

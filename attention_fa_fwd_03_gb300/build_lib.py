@@ -6,8 +6,9 @@ runtime is linked statically, so loading the library needs no CUDA driver
 until the first call that touches the GPU.
 
 Beside it ``_paged.so`` is built, the Python binding of the paged-cache calls
-(csrc/paged_binding.cpp), by the host compiler against the headers of the
-PyTorch that is installed, and again when that is another one.
+and of differentiable attention (csrc/paged_binding.cpp), by the host compiler
+against the headers of the PyTorch that is installed, and again when that is
+another one.
 """
 from __future__ import annotations
 
@@ -22,6 +23,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa_gb300.so")
 BINDING_SRC = os.path.join(CSRC, "paged_binding.cpp")
+BINDING_DEPS = [BINDING_SRC, os.path.join(CSRC, "autograd_binding.h")]
 BINDING = os.path.join(HERE, "_paged.so")
 BINDING_FOR = os.path.join(BUILD, "paged_binding.pytorch")  # what it was built against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -64,7 +66,8 @@ def _pytorch() -> str | None:
 
 
 def _binding_current(pytorch: str) -> bool:
-    if not _newer(BINDING, [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+    if not _newer(BINDING, BINDING_DEPS + [os.path.abspath(__file__)]
+                  + glob.glob(os.path.join(INCLUDE, "*.h"))):
         return False
     try:
         with open(BINDING_FOR) as fh:

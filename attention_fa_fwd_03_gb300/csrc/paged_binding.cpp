@@ -1,7 +1,7 @@
 // Python binding of the paged-cache calls (fa_kv_append, fa_paged_fwd,
-// fa_page_select, fa_page_assign): checks the tensors, makes the device current and calls the C
-// ABI on the stream. It holds no arithmetic. The other calls go through ctypes;
-// these are made once per layer and token, where a kernel takes a few
+// fa_page_select, fa_page_assign) and of differentiable attention: checks the tensors, makes the
+// device current and calls the C ABI on the stream. It holds no arithmetic. The other calls go
+// through ctypes; these are made once per layer and token, where a kernel takes a few
 // microseconds, and ctypes with checks in Python took 8 to 10 of them per call.
 #include <climits>
 #include <cstdint>
@@ -16,6 +16,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "fa.h"
+
+#include "autograd_binding.h"
 
 namespace {
 
@@ -328,15 +330,60 @@ PyObject* page_assign(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   });
 }
 
+// attention(q, k, v, scale, causal, window, sinks) -> (o, lse), differentiable
+PyObject* dense_attention(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  if (nargs != 7) {
+    PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
+    return nullptr;
+  }
+  try {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    for (const at::Tensor* t : {&q, &k, &v}) {
+      if (!t->is_cuda()) fail(PyExc_ValueError, "%s must live on a CUDA device", "tensors");
+      if (!t->is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous (row-major [B, H, T, D])", "tensors");
+      if (t->dim() != 4) fail(PyExc_ValueError, "%s are [B, H, T, D]", "q, k and v");
+    }
+    if (q.scalar_type() != at::kHalf && q.scalar_type() != at::kBFloat16) {
+      attention::set_status_error(FA_ERR_UNSUPPORTED_DTYPE, "fa_fwd");
+      return nullptr;
+    }
+    if (k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type() || k.get_device() != q.get_device() ||
+        v.get_device() != q.get_device() || k.size(0) != q.size(0) || k.size(3) != q.size(3) || v.sizes() != k.sizes())
+      fail(PyExc_ValueError, "%s [B, Hkv, Tkv, D] of one shape, of q's type, device, B and D", "k and v are");
+    const double scale = PyFloat_AsDouble(a[3]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Failed{};
+    const bool causal = truth(a[4]);
+    const int window = integer(a[5], "window"), sinks = integer(a[6], "sinks");
+    attention::Node::List out;
+    {
+      const Unlocked unlocked;
+      out = attention::Node::apply(q, k, v, scale, causal, static_cast<int64_t>(window), static_cast<int64_t>(sinks));
+    }
+    PyObject* o = THPVariable_Wrap(out[0]);
+    PyObject* lse = o ? THPVariable_Wrap(out[1]) : nullptr;
+    PyObject* both = lse ? PyTuple_Pack(2, o, lse) : nullptr;
+    Py_XDECREF(o);
+    Py_XDECREF(lse);
+    return both;
+  } catch (const Failed&) {
+  } catch (const std::exception&) {  // PyTorch's own and FaError
+    torch::translate_exception_to_python(std::current_exception());
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+  }
+  return nullptr;
+}
+
 PyMethodDef kMethods[] = {
     {"handle", make_handle, METH_VARARGS, nullptr},
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL, nullptr},
     {"paged_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_fwd)), METH_FASTCALL, nullptr},
     {"page_select", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(page_select)), METH_FASTCALL, nullptr},
     {"page_assign", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(page_assign)), METH_FASTCALL, nullptr},
+    {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(dense_attention)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_paged", "Binding of the paged-cache calls.", -1, kMethods,
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_paged", "Binding of the paged-cache calls and of differentiable attention.", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -110,3 +110,53 @@ def test_autograd_has_no_cpu_path():
     k = torch.zeros(1, 1, 8, 64, dtype=torch.float16)
     with pytest.raises((ValueError, RuntimeError)):
         flash_attention(q, k, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 0), (70, 9)])
+def test_function_and_node_give_the_same_bits(window, sinks):
+    """flash_attention's compiled node and the Function over the same calls, with gradients of some inputs only."""
+    from attention_fa_fwd_03_gb300.autograd import FlashAttention, flash_attention
+    w = fa_inputs.Workload("ag_node", 2, 4, 2, 300, 260, 96, "bf16", False, seed=46)
+    x = {n: t.cuda() for n, t in fa_inputs.make_inputs(w).items()}
+    for wanted in (("q", "k", "v"), ("q",), ("v",)):
+        ins = {n: x[n].clone().requires_grad_(n in wanted) for n in ("q", "k", "v")}
+        o, lse = flash_attention(*ins.values(), 0.1, True, window, return_lse=True, sinks=sinks)
+        of, lf = FlashAttention.apply(*ins.values(), 0.1, True, window, *([sinks] if sinks else []))
+        assert torch.equal(o, of) and torch.equal(lse, lf) and not lse.requires_grad and o.requires_grad
+        a, b = (torch.autograd.grad(y, [ins[n] for n in wanted], x["do"]) for y in (o, of))
+        assert all(torch.equal(i, j) for i, j in zip(a, b))
+    with torch.no_grad():
+        assert flash_attention(*ins.values(), 0.1, True, window, sinks=sinks).grad_fn is None
+
+
+@pytest.mark.gpu
+def test_node_errors():
+    """What the library refuses is an FaError with its status, from the forward and from the graph's thread; saved inputs
+    that were written since are found; shapes, types and devices that do not fit are refused."""
+    import attention_fa_fwd_03_gb300 as fa
+    flash_attention = _wrapper()
+    q = torch.randn(1, 4, 40, 64, device="cuda").half().requires_grad_()
+    k = torch.randn(1, 2, 50, 64, device="cuda").half().requires_grad_()
+    with pytest.raises(fa.FaError) as e:
+        flash_attention(q, k, k, window=-1)
+    assert e.value.status == 1
+    with pytest.raises(fa.FaError):
+        flash_attention(q.float(), k.float(), k.float())
+    with pytest.raises(fa.FaError):
+        flash_attention(q[..., :40], k[..., :40], k[..., :40])
+    for a in ((q, k.bfloat16(), k), (q, k, k[:, :, :30]), (q, k[..., :32], k[..., :32]), (q, k.cpu(), k), (q[0], k, k),
+              (q, k.expand(2, -1, -1, -1), k.expand(2, -1, -1, -1))):
+        with pytest.raises(ValueError):
+            flash_attention(*a)
+    o = flash_attention(q, k, k)
+    odd = torch.empty(o.numel() + 1, dtype=o.dtype, device="cuda")[1:].view(o.shape)  # two bytes off
+    with pytest.raises(fa.FaError) as e:
+        o.backward(odd)
+    assert e.value.status == 4
+    o = flash_attention(q, k, k)
+    with torch.no_grad():
+        k.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        o.backward(torch.ones_like(o))
+    torch.cuda.synchronize()
