@@ -10,7 +10,7 @@
 // The work is a few words per sequence and per page that changes hands, microseconds
 // of launch and dependent loads (lengths and states, then tables and stack). So one
 // cluster does it: every CTA sums over all sequences for itself, 1024 at a time, then
-// its warps take sequences in turn. Pages given back have to be on the stack before
+// its warps take sequences in turn, several of them one where there are few. Pages given back have to be on the stack before
 // any is taken from it, and states are written when nobody reads them any more: a
 // barrier each. Slots of a few tokens are written by the same cluster, of many by a
 // second launch that fills the GPU.
@@ -25,6 +25,13 @@ namespace fa {
 namespace {
 
 constexpr int kAssignThreads = 1024;
+// Up to so many sequences and tokens one CTA does all, without a cluster's barriers. (Pages of 16, one
+// CTA and eight, us: 8 sequences and a token each 5.1, 6.3; 64: 6.3, 6.5; 128: 8.3, 6.6. One
+// sequence, 1024 tokens 5.0, 5.6; 8192: 6.6, 6.4.)
+constexpr int kLoneB = 64, kLoneTokens = 4096;
+// Up to so many tokens the cluster writes their slots. (Here and apart, us: 4 x 2048 6.4, 7.7;
+// 16 x 1024 6.7, 7.4; 64 x 1024 8.7, 7.6; 256 x 8192 60, 15.6, of which the slots' bytes are 2.5.)
+constexpr int kSlotsHere = 16384;
 
 struct AssignArgs {
   int *table, *held, *free_pages, *free_count;
@@ -177,22 +184,26 @@ __global__ void __launch_bounds__(kAssignThreads, 1) fa_page_assign_kernel(const
       __syncthreads();
     }
   };
-  // f(b, plan, before) by a warp for each sequence; the sums are those of all sequences
+  // f(b, plan, before, i0, step): sequence b's work i0, i0 + step, ... by one warp, or by several
+  // where there are more warps than sequences; the sums are those of all sequences
   auto sweep = [&](bool planned, bool replaces, const auto& f) {
     Sums carry = {0, 0};
     for (int base = 0; base < p.B; base += kAssignThreads) {
       if (!planned) carry = plan_window(p, sm, base, carry);
       if (!planned && replaces) meet();  // every CTA has read this window's states
       const int n = min(kAssignThreads, p.B - base);
-      for (int i = rank + ranks * warp; i < n; i += ranks * (kAssignThreads / 32)) f(base + i, sm.plan[i], sm.before[i]);
+      const int warps = ranks * (kAssignThreads / 32), w = rank + ranks * warp;
+      const int per = max(walk_log2(warps) - walk_log2(2 * n - 1), 0);  // warps of a sequence: 2^per
+      for (int i = w >> per; i < n; i += warps >> per)
+        f(base + i, sm.plan[i], sm.before[i], 32 * (w & ((1 << per) - 1)) + lane, 32 << per);
     }
     if (!planned) all = carry;
   };
   // pages given back, to the stack
-  sweep(false, false, [&](int b, const Plan& x, const Sums& before) {
+  sweep(false, false, [&](int b, const Plan& x, const Sums& before, int i0, int step) {
     int* row = p.table + static_cast<int64_t>(b) * p.max_pages;
     const int n = x.back();
-    for (int i = lane; i < n; i += 32) {
+    for (int i = i0; i < n; i += step) {
       const int pg = x.back_page(i), id = row[pg];
       const int64_t at = static_cast<int64_t>(count) + before.back + i;
       const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages);
@@ -204,27 +215,27 @@ __global__ void __launch_bounds__(kAssignThreads, 1) fa_page_assign_kernel(const
   const int total = static_cast<int>(min(static_cast<int64_t>(count) + all.back, static_cast<int64_t>(p.num_pages)));
   meet();
   // pages wanted, from its top
-  sweep(one, false, [&](int b, const Plan& x, const Sums& before) {
+  sweep(one, false, [&](int b, const Plan& x, const Sums& before, int i0, int step) {
     int* row = p.table + static_cast<int64_t>(b) * p.max_pages;
     const int n = x.more();
-    for (int i = lane; i < n; i += 32) {
+    for (int i = i0; i < n; i += step) {
       const int at = total - 1 - (before.more + i);
       row[x.more_page(i)] = at >= 0 ? p.free_pages[at] : -1;
     }
   });
   meet();
   // what each sequence holds now, and the slots
-  sweep(one, true, [&](int b, const Plan& x, const Sums& before) {
+  sweep(one, true, [&](int b, const Plan& x, const Sums& before, int i0, int step) {
     const int more = x.more(), want = x.h + x.e - x.f;
     const int got = want - more + min(more, max(0, total - before.more));
     if (p.slots_here) {
       const Lens l = lens_of(p, b);
-      for (int t = lane; t < p.T; t += 32) p.slots[static_cast<int64_t>(b) * p.T + t] = slot_of(p, b, t, l);
+      for (int t = i0; t < p.T; t += step) p.slots[static_cast<int64_t>(b) * p.T + t] = slot_of(p, b, t, l);
     }
-    if (lane < 3) {
+    if (i0 < 3) {
       const int h = min(x.h, got), end = got > h ? x.f + got - h : h;
       const int f = got < want ? min(x.f, end) : x.f, e = got < want ? end : x.e;
-      p.held[3 * b + lane] = lane == 0 ? h : lane == 1 ? f : e;
+      p.held[3 * b + i0] = i0 == 0 ? h : i0 == 1 ? f : e;
     }
   });
   if (rank == 0 && threadIdx.x == 0) {
@@ -233,18 +244,20 @@ __global__ void __launch_bounds__(kAssignThreads, 1) fa_page_assign_kernel(const
   }
 }
 
-// Slots of many tokens: a thread each, four in a row.
-constexpr int kSlotThreads = 256, kSlotsEach = 4;
+// Slots of many tokens: a block writes adjacent ones, each thread every 256th.
+constexpr int kSlotThreads = 256, kSlotsEach = 8;
 __global__ void __launch_bounds__(kSlotThreads) fa_page_slots_kernel(const AssignArgs p, int per_seq) {
   grid_wait_prior();
   grid_release_next();
   const int b = blockIdx.x / per_seq;
   const Lens l = lens_of(p, b);
-  const int t0 = ((blockIdx.x - b * per_seq) * kSlotThreads + threadIdx.x) * kSlotsEach;
-  int64_t* out = p.slots + static_cast<int64_t>(b) * p.T;
+  const int t0 = (blockIdx.x - b * per_seq) * kSlotThreads * kSlotsEach + threadIdx.x;
+  int64_t slot[kSlotsEach];
+#pragma unroll
+  for (int i = 0; i < kSlotsEach; ++i) slot[i] = slot_of(p, b, t0 + i * kSlotThreads, l);  // (-1 behind the last token)
 #pragma unroll
   for (int i = 0; i < kSlotsEach; ++i)
-    if (t0 + i < p.T) out[t0 + i] = slot_of(p, b, t0 + i, l);
+    if (t0 + i * kSlotThreads < p.T) p.slots[static_cast<int64_t>(b) * p.T + t0 + i * kSlotThreads] = slot[i];
 }
 
 }  // namespace
@@ -287,8 +300,9 @@ extern "C" fa_status fa_page_assign(int* page_table, const int* kv_lens, int* he
   p.window = std::min(window, 1 << 30);
   p.sinks = std::min(sinks, 1 << 30);
   p.status = wc.status;
-  p.slots_here = slots && static_cast<int64_t>(B) * T <= 8192;
-  const int ranks = B > 16 || T > 16 * ps ? 8 : 1;
+  const int64_t tokens = static_cast<int64_t>(B) * T;
+  p.slots_here = slots && tokens <= kSlotsHere;
+  const int ranks = B <= kLoneB && tokens <= kLoneTokens ? 1 : 8;
   cudaError_t e = launch_kernel(fa_page_assign_kernel, ranks, kAssignThreads, 0, stream, static_cast<unsigned>(ranks), p, ranks);
   if (e == cudaSuccess && slots && !p.slots_here) {
     const int per_seq = (T + kSlotThreads * kSlotsEach - 1) / (kSlotThreads * kSlotsEach);
