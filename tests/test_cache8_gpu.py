@@ -45,6 +45,8 @@ def attend(kv, q, scale, causal=True, window=0, sinks=0, new_lens=None, sel=None
     o, lse = torch.full_like(q, NAN), torch.full(q.shape[:3], NAN, device="cuda")
     ws = torch.full((fa.fa_paged_workspace_size(q.shape[1], kv.Hkv, q.shape[2], kv.D),), 255, dtype=torch.uint8, device="cuda")
     d = [None if t is None else t.cuda() for t in (new_lens, sel, sel_lens)]
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
     fa.fa_paged_fwd(kv, q, o, lse, scale, causal=causal, window=window, sinks=sinks, new_lens=d[0], sel=d[1], sel_lens=d[2],
                     workspace=ws, stream=stream)
     return o, lse
@@ -52,9 +54,10 @@ def attend(kv, q, scale, causal=True, window=0, sinks=0, new_lens=None, sel=None
 
 def check(o, lse, want, what=""):
     ro, rl, bo, bl = want
+    most = torch.finfo(o.dtype).max * (1 + torch.finfo(o.dtype).eps / 4)  # from here on a number is rounded to infinity
     o, lse = o.double().cpu(), lse.double().cpu()
     assert torch.equal(lse == -math.inf, rl == -math.inf), f"{what}: rows without keys"
-    bad = ~((o - ro).abs() <= bo)
+    bad = ~((o - ro).abs() <= bo) & ~((o.abs() == math.inf) & (o.sign() == ro.sign()) & (ro.abs() + bo >= most))
     assert not bad.any(), f"{what}: O off by {((o - ro).abs() / bo.clamp(min=1e-300))[bad].max():.3g} bounds at {bad.nonzero()[0].tolist()}"
     fin = rl > -math.inf
     bad = ~((lse - rl).abs()[fin] <= bl[fin])
@@ -312,6 +315,72 @@ def test_attend_matches_the_definition(case):
     check(o, lse, want)
     again = attend(kv, q, 0.5 / math.sqrt(D), causal, window, sinks, None if new is None else i32(new))
     assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("rep,T", [(8, 1), (4, 4), (16, 2), (9, 5), (8, 8), (16, 8)])
+def test_attend_over_long_lists_of_all_sizes(rep, T, D, dt):
+    """Every kernel of a long list: rows up to 8, 16, 32, 64 and 128, pages whose scales are far apart."""
+    g = gen(rep * T + D)
+    Hkv, page, L = 2, 32, 20011
+    table, P = make_table(g, 1, -(-L // page))
+    (k_pool, ks), (v_pool, vs) = held_pool(g, P, Hkv, page, D, 1.0), held_pool(g, P, Hkv, page, D, 10.0)
+    kd, vd = ref.held_value(k_pool, ks), ref.held_value(v_pool, vs)
+    kv = handle(k_pool, v_pool, ks, vs, table, i32([L]))
+    q = randn(g, 1, rep * Hkv, T, D, dtype=DT[dt])
+    got = attend(kv, q, 0.5 / math.sqrt(D))
+    assert clear()
+    check(*got, ref.attend(q, kd, vd, table, [L], 0.5 / math.sqrt(D), True, 0, 0, held=True))
+
+
+@pytest.mark.parametrize("rep,T,D", [(1, 1, 64), (4, 3, 64), (8, 5, 64), (3, 1, 256)])
+def test_attend_over_more_sequences_than_a_window_holds(rep, T, D):
+    """Lists of more items than a CTA keeps lengths of, empty sequences and padding among them."""
+    g = gen(rep + T)
+    B, Hkv, page, L = 300, 1, 16, 1200
+    lens = [0 if b % 7 == 3 else 1 + (b * 401) % L for b in range(B)]
+    new = [min(n, b % (T + 1)) for b, n in enumerate(lens)]
+    table, P = make_table(g, B, -(-L // page))
+    k, ks = held_pool(g, 100, Hkv, page, D, 1.0)
+    v, vs = held_pool(g, 100, Hkv, page, D)
+    at = torch.arange(P) % 100  # (the pool's pages repeat a hundred)
+    k_pool, v_pool = (bits(t)[at].view(ref.E4M3) for t in (k, v))
+    kv = handle(k_pool, v_pool, ks[at], vs[at], table, i32(lens))
+    q = randn(g, B, rep, T, D, dtype=torch.bfloat16)
+    got = attend(kv, q, 0.1, new_lens=i32(new))
+    assert clear()
+    kd, vd = ref.held_value(k_pool, ks[at]), ref.held_value(v_pool, vs[at])
+    check(*got, ref.attend(q, kd, vd, table, lens, 0.1, True, 0, 0, new, held=True))
+
+
+def test_pool_beyond_32_bits():
+    """Appending to and attending over pages that lie behind 2^32 bytes of the pools: the bytes and bits of a small pool."""
+    g = gen(33)
+    B, Hq, Hkv, D, page, T = 2, 8, 2, 128, 64, 70
+    lens = [150, 3 * page]
+    small, P = make_table(g, B, 3, spare=2)
+    far = 2 ** 32 // (Hkv * page * D)
+    runs = []
+    for base in (0, far):
+        k, v = (torch.zeros(base + P, Hkv, page, D, dtype=torch.uint8, device="cuda").view(ref.E4M3) for _ in range(2))
+        ks, vs = (torch.full((base + P, Hkv), 2.0 ** -126, device="cuda") for _ in range(2))
+        g.manual_seed(5)
+        kv = fa.PagedKV(k, v, (small + base).cuda(), i32([n - T for n in lens]).cuda(), k_scales=ks, v_scales=vs)
+        for new in ([n - T for n in lens], [T, T], [1, 1]):  # many tokens, many on top of a begun page, one
+            if new[0] == T:
+                kv.kv_lens += T
+            t = max(new)
+            x = [randn(g, B, h, t, D, dtype=torch.bfloat16).cuda() for h in (Hkv, Hkv, Hq)]
+            out = torch.empty_like(x[2])
+            fa.fa_kv_append(kv, x[0], x[1], q=x[2], q_out=out, new_lens=i32(new).cuda())
+        o = [attend(kv, out, 0.1)]
+        assert clear()
+        runs.append([t[base:].clone() for t in (bits(k), bits(v), ks, vs)] + [t for pair in o for t in pair])
+        del k, v, kv
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+    assert runs[0][4].isfinite().all()
 
 
 @pytest.mark.parametrize("D,page,window", [(64, 16, 0), (128, 64, 90), (256, 32, 0), (96, 128, 0)])
