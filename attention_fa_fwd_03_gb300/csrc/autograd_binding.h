@@ -2,14 +2,17 @@
 // fa_fwd_sinks and fa_bwd_sinks on the current stream. It holds no arithmetic.
 //
 // A step over short sequences is host time: B2 Hq6 Hkv2 T1500 D64 with a window is 47 us of kernels,
-// and took 344 us with forward and backward written in Python. The backward runs in a thread of
+// and took 334 us with forward and backward written in Python. The backward runs in a thread of
 // PyTorch's own, which in Python has to wait for the interpreter's lock besides. Here 188 us, of which
 // PyTorch takes 105 for a graph of one node.
 #pragma once
 
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
+#include <torch/csrc/autograd/graph_task.h>
 
 namespace attention {
 
@@ -36,6 +39,29 @@ inline void check_status(fa_status status, const char* what) {
 
 inline cudaStream_t current_stream(const at::Tensor& t) {
   return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
+}
+
+// A leaf's gradient is added, or handed out, on the stream on which the leaf was first used, as long
+// as a graph of that time lives. Within a capture that must not be the legacy default stream: CUDA
+// refuses it, and PyTorch may end the process over that. So such a backward is refused here.
+inline void refuse_leaves_of_default_stream(const c10::cuda::CUDAStream& current) {
+  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
+  const std::shared_ptr<torch::autograd::Node> node = torch::autograd::get_current_node();
+  if (!node) return;
+  const auto* info = torch::autograd::get_current_graph_task_exec_info();
+  for (const torch::autograd::Edge& edge : node->next_edges()) {
+    auto* leaf = dynamic_cast<torch::autograd::AccumulateGrad*>(edge.function.get());
+    if (!leaf) continue;
+    if (info && !info->empty()) {  // gradients of named tensors only
+      const auto it = info->find(leaf);
+      if (it == info->end() || !it->second.should_execute()) continue;
+    }
+    const auto stream = leaf->stream();
+    if (stream && *stream != current.unwrap() && c10::cuda::CUDAStream(*stream).stream() == nullptr)
+      throw std::runtime_error(
+          "flash_attention: this backward pass is being captured into a CUDA graph while an eager graph of the same leaves "
+          "from the default stream lives; delete its outputs first");
+  }
 }
 
 struct Sizes {
@@ -73,6 +99,7 @@ class Node : public torch::autograd::Function<Node> {
 
   static List backward(Context* ctx, List grads) {
     const List saved = ctx->get_saved_variables();
+    refuse_leaves_of_default_stream(c10::cuda::getCurrentCUDAStream(saved[0].get_device()));
     const at::Tensor &q = saved[0], &k = saved[1], &v = saved[2], &o = saved[3], &lse = saved[4];
     const c10::cuda::CUDAGuard on(q.device());
     const Sizes s(q, k);

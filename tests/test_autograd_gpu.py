@@ -160,3 +160,50 @@ def test_node_errors():
     with pytest.raises(RuntimeError, match="modified by an inplace"):
         o.backward(torch.ones_like(o))
     torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_captured_backward_beside_an_eager_graph():
+    """A backward captured while an eager graph of the same leaves lives cannot be where the leaves were used on the default
+    stream: refused, with the process as it was, and captured once the eager graph is gone."""
+    code = """
+import torch
+from attention_fa_fwd_03_gb300.autograd import flash_attention
+q, k, v = (torch.randn(1, 2, 100, 64, device="cuda").half().requires_grad_() for _ in range(3))
+do = torch.randn(1, 2, 100, 64, device="cuda").half()
+eager = flash_attention(q, k, v, causal=True)
+side = torch.cuda.Stream()
+torch.cuda.synchronize()
+def grads():
+    return torch.autograd.grad(flash_attention(q, k, v, causal=True), (q, k, v), do)
+for f in (lambda: flash_attention(q, k, v, causal=True).backward(do), grads):
+    g = torch.cuda.CUDAGraph()
+    try:
+        with torch.cuda.graph(g, stream=side):
+            f()
+        print("captured")
+    except RuntimeError as e:
+        print("refused" if "eager graph" in str(e) else e)
+want = torch.autograd.grad(eager, (q, k, v), do)
+del eager
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=side):
+    got = grads()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+q.grad = k.grad = v.grad = None
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=side):
+    flash_attention(q, k, v, causal=True).backward(do)
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a.grad, b) for a, b in zip((q, k, v), want))
+print("done")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["refused", "refused", "done"], (r.stdout, r.stderr[-2000:])
