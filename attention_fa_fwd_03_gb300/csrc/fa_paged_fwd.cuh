@@ -1344,6 +1344,19 @@ cudaError_t run_split_tc(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t tiles
   return run_split<C>(a, p, tiles, 1, [&](int64_t parts) { return launch_paged_tc<C>(a, p, parts); });
 }
 
+// A cache held in 8 bits, more than 16 rows, all clusters at once: a cluster's CTA takes
+// tiles / ranks tiles one after the other behind a short start, the split list every tile
+// over the SMs at nearly the same rate, but starts 10 us later, and the later the more rows
+// its blocks have. Measured (tiles a CTA of a cluster has and of the list, us of both): D 64, 35 rows
+// 16, 6.7: 17.2, 22.5; 17, 8.7: 20.0, 25.3; 64 rows 16, 6.7: 22.4, 24.2; 16, 15: 23.2, 29.1; 128
+// rows 16, 6.7: 23.0, 34.3; 32, 15: 38.5, 41.6; D 128, 35 rows 16, 6.7: 23.1, 27.1; 64 rows 8, 3.4:
+// 20.2, 23.6; 16, 6.7: 30.6, 27.3; 16, 15: 31.2, 35.3; 128 rows 16, 6.7: 31.0, 37.9; 32, 15: 52.9, 47.3.
+inline bool cluster8_pays(const PagedFwdLaunch& a, int rows, int64_t tiles, int ranks) {
+  const int block = paged_split_rows(rows), later = rows <= 48 ? 13 : rows <= 64 ? 8 : 16;  // tiles' time
+  const int64_t list = static_cast<int64_t>(a.c.B) * a.c.Hkv * ((rows + block - 1) / block) * tiles / device_sm_count();
+  return (tiles + ranks - 1) / ranks <= later + list * 3 / 4;
+}
+
 template <int D, int NT, int RW, bool BF16, bool E8>
 cudaError_t run_paged(const PagedFwdLaunch& a) {
   using C = PagedCfg<D, NT, RW, BF16, true, E8>;
@@ -1372,7 +1385,10 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   int ranks = 1;
   while (tiles > 2 && ranks < kPagedMaxRanks && ranks < tiles) ranks *= 2;  // 2 tiles: 5.7 us in one CTA, 6.6 in two
   while (ranks > 1 && units > resident_clusters<C>(ranks)) ranks /= 2;
-  if (tiles <= C::CLUSTER_TILES * ranks) return launch_paged<C>(a, p, units * ranks, ranks);
+  bool clusters = tiles <= C::CLUSTER_TILES * ranks;
+  if constexpr (E8 && RW > 1 && D < 256)
+    if (ranks > 1 || units <= device_sm_count()) clusters = cluster8_pays(a, p.rows, tiles, ranks);
+  if (clusters) return launch_paged<C>(a, p, units * ranks, ranks);
   if constexpr (RW > 1 && !(E8 && D == 256)) {  // more than 16 rows
     switch (paged_split_rows(p.rows)) {
       case 32: return run_split_tc<D, 1, BF16, E8>(a, p, tiles);
