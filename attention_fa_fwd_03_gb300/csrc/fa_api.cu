@@ -132,7 +132,9 @@ void drop_idle_window(int Tq, int Tkv, int* window, int* sinks) {
 // it where the other blocks see a window's, and would be the last item to end: it is cut into
 // items of a window's query tiles, but not into smaller ones than half of what a CTA has to
 // do in all. (B1 Hq16 Hkv2 T16384 D128, window 4096: 1024 tiles in one item against 264, in all
-// 444 per SM.)
+// 444 per SM. Backward in parts and not: 1092 and 1625 us, where the window alone takes 1064; B1
+// Hq8 Hkv2 T8192 D256, window 1024: 254, 614, 232; B2 Hq6 Hkv2 T1500 D64, window 300: 37, 72, 25;
+// B2 Hq8 Hkv8 T8192 D64, window 1024, 300 first keys, where items are many: 214, 207, 163.)
 SinkParts sink_parts(int B, int Hq, int Hkv, int Tq, int Tkv, int D, int window, int sinks) {
   SinkParts p;
   if (sinks == 0) return p;
