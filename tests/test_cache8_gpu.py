@@ -354,6 +354,28 @@ def test_attend_over_more_sequences_than_a_window_holds(rep, T, D):
     check(*got, ref.attend(q, kd, vd, table, lens, 0.1, True, 0, 0, new, held=True))
 
 
+@pytest.mark.parametrize("B,rep,T,L", [(75, 7, 5, 3000), (36, 8, 8, 2990), (18, 16, 8, 3000), (70, 10, 2, 4000)])
+@pytest.mark.parametrize("D,dt", [(64, "fp16"), (128, "bf16"), (96, "bf16")])
+def test_attend_in_clusters_of_many_tiles(B, rep, T, L, D, dt):
+    """So many units that all SMs have one, of more tiles than the other kernels' clusters take."""
+    g = gen(B + D)
+    Hkv, page = 2, 64
+    lens = [L - 13 * b for b in range(B)]
+    table, P = make_table(g, B, -(-L // page))
+    k, ks = held_pool(g, 64, Hkv, page, D, 1.0)
+    v, vs = held_pool(g, 64, Hkv, page, D)
+    at = torch.arange(P) % 64
+    k_pool, v_pool = (bits(t)[at].view(ref.E4M3) for t in (k, v))
+    q = randn(g, B, rep * Hkv, T, D, dtype=DT[dt])
+    got = attend(handle(k_pool, v_pool, ks[at], vs[at], table, i32(lens)), q, 0.5 / math.sqrt(D))
+    assert clear()
+    some = list(range(0, B, 9))  # sequences that are compared
+    kd, vd = ref.held_value(k, ks), ref.held_value(v, vs)
+    want = ref.attend(q[some], kd, vd, table[some] % 64, [lens[b] for b in some], 0.5 / math.sqrt(D), True, 0, 0, held=True)
+    check(got[0][some], got[1][some], want)
+    assert got[0].isfinite().all() and got[1].isfinite().all()
+
+
 def test_pool_beyond_32_bits():
     """Appending to and attending over pages that lie behind 2^32 bytes of the pools: the bytes and bits of a small pool."""
     g = gen(33)
