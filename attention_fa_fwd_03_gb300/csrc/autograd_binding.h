@@ -3,7 +3,7 @@
 //
 // A step over short sequences is host time: B2 Hq6 Hkv2 T1500 D64 with a window is 47 us of kernels,
 // and took 334 us with forward and backward written in Python. The backward runs in a thread of
-// PyTorch's own, which in Python has to wait for the interpreter's lock besides. Here 188 us, of which
+// PyTorch's own, which in Python has to wait for the interpreter's lock besides. Here 188 to 210 us, of which
 // PyTorch takes 105 for a graph of one node.
 #pragma once
 
