@@ -370,7 +370,7 @@ struct Paged8Cfg {
   static constexpr int OP = D + 4;
   // A unit's beginning and end take as long as two of a group's tiles (64 ragged sequences 104
   // us when they count for nothing, 98 for one, 95 for two; 128 of half the length 113, 102, 96).
-  static constexpr int OVER = 2;
+  static constexpr int OVER = kOver8;
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + STAGES * 2 * TILE;
   static constexpr int OFF_O = OFF_Q + QREGS * QREGION;  // the warps' rows side by side

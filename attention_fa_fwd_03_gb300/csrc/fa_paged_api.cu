@@ -211,11 +211,10 @@ fa_status paged_fwd(const Cache* kv, const void* q, void* o, float* lse, int Hq,
   if (!q || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
   if ((sel == nullptr) != (sel_lens == nullptr)) return FA_ERR_INVALID_ARG;
   if (sel && (n_sel < 1 || n_sel > kMaxSelected)) return FA_ERR_INVALID_ARG;
-  // tiles are counted in 32 bits
-  const int block = paged_block_rows(Hq / kv->Hkv * Tq, kv->D);
-  const int64_t all_units = static_cast<int64_t>(kv->B) * kv->Hkv * ((Hq / kv->Hkv * Tq + block - 1) / block);
-  if (paged_tiles(all_units, static_cast<int64_t>(sel ? n_sel : kv->max_pages) * kv->page_size) +
-          (kv->e4m3 ? all_units : 0) > INT32_MAX)  // (a unit counts for a tile more there)
+  const int unit_rows = Hq / kv->Hkv * Tq, block = paged_block_rows(unit_rows, kv->D);
+  const int64_t all_units = static_cast<int64_t>(kv->B) * kv->Hkv * ((unit_rows + block - 1) / block);
+  if (!list_fits(all_units, static_cast<int64_t>(sel ? n_sel : kv->max_pages) * kv->page_size,
+                 list_over(kv->e4m3, unit_rows)))
     return FA_ERR_INVALID_ARG;
   const size_t need = fwd_workspace(Hq, kv->Hkv, Tq, kv->D);
   if (workspace_bytes < need) return FA_ERR_INVALID_ARG;

@@ -78,9 +78,6 @@ inline int paged_split_rows(int rows) {
 // CTAs of a split list at most: they leave parts of units to be joined.
 __host__ __device__ constexpr int paged_max_parts(int block_rows) { return block_rows <= 16 ? 608 : 192; }
 
-// Tiles of a call's list (32-bit counts on the device).
-inline int64_t paged_tiles(int64_t units, int64_t keys) { return units * ((keys + kPagedTile - 1) / kPagedTile); }
-
 // Device workspace of launch_paged_fwd_d* in bytes: per CTA two parts of a
 // block (fp32 rows, maximum and sum) and a record of what is to be joined.
 inline size_t paged_fwd_workspace(int rows, int D) {

@@ -21,6 +21,16 @@ namespace fa {
 
 // Keys of a tile.
 constexpr int kPagedTile = 64;
+// Tiles of `units` units of `keys` keys.
+inline int64_t paged_tiles(int64_t units, int64_t keys) { return units * ((keys + kPagedTile - 1) / kPagedTile); }
+// Places that a unit counts for beside its tiles where the list of up to 16 rows over a cache
+// held in 8 bits is cut (fa_paged8.cuh says why), as the host counts it too.
+constexpr int kOver8 = 2;
+inline int list_over(bool e4m3, int rows) { return e4m3 && rows <= 16 ? kOver8 : 0; }
+// Places are counted in 32 bits on the device: whether those of the longest list can be.
+inline bool list_fits(int64_t units, int64_t keys, int over) {
+  return paged_tiles(units, keys) + units * over <= INT32_MAX;
+}
 // Items whose lengths a CTA holds at a time.
 constexpr int kItemWindow = 128;
 
@@ -83,7 +93,7 @@ FA_WALK_FN int unit_places(const ListShape& s, const Item& it) { return it.tiles
 
 // One CTA's share of the list: `total` places (tiles, where over is 0) in equal runs, the first total % parts
 // of them one longer. (The host has checked that the longest possible list stays
-// below 2^31 tiles.)
+// below 2^31 places.)
 struct Share {
   int parts;      // CTAs with a share: every one of them has a tile
   int base, more; // tiles of a share, and how many have one more

@@ -283,7 +283,8 @@ size_t fa_paged_workspace_size(int Hq, int Hkv, int Tq, int D);
  *     order). An entry outside the sequence's pages, or sel_lens outside
  *     [0, n_sel], is a bad index.
  * Limit: B * Hkv * ceil(rows / 64) * ceil(keys / 64) < 2^31, rows = (Hq / Hkv) * Tq
- * (D = 256: / 32), keys = max_pages * page_size, with sel n_sel * page_size.
+ * (D = 256: / 32), keys = max_pages * page_size, with sel n_sel * page_size; over a cache
+ * of 8 bits with rows <= 16: B * Hkv * (ceil(keys / 64) + 2) < 2^31.
  * A row that sees no key (or whose every score is -inf), and every padding row,
  * gets O = 0 and LSE = -inf.
  * Scores are held in fp32 in units of ln 2: |scale q.k| above 2.3e38 counts as
