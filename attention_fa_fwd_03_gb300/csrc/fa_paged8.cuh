@@ -103,6 +103,12 @@ __device__ __forceinline__ void QueryRows<C>::store(uint8_t* dst, float* scales,
 }
 
 
+// Weights go to their product as fp16 numbers times this: they are up to 2^8 (kPagedSlack) and
+// parts of scales at most 1, so the products stay within fp16, and small ones keep their digits:
+// as they are, a weight would lose digits from 2^-14 of the running maximum's on and be nothing
+// below 2^-25, where one key dominates and many others share the rest the larger part of the row.
+constexpr float kWeightLift = 128.f;
+
 // One tile's 16 keys of a warp: their scores with the warp's query rows, weights, and the
 // product with the values, added to the running maxima, sums and rows. `ks`, `vs`: shared
 // addresses of the keys' and values' first rows, regions of 128 columns REGION bytes apart;
@@ -142,9 +148,9 @@ __device__ __forceinline__ void step8(const PagedFwdArgs& p, uint32_t ks, uint32
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[0][e] += s2[e];
   }
-  // The values' scale goes to the weights, as a part of the largest one so far, `unit`, in
-  // which rows are summed; where that would cost the weights digits (their words are
-  // fp16), to the products instead.
+  // The values' scale goes to the weights, as a part of the largest one so far, `unit` (rows
+  // are sums in units of unit / kWeightLift); where that would cost the weights digits (below
+  // 1/16), to the products instead.
   if (scale.y > unit) {
     const float f = unit * inverse_power(scale.y);
     unit = scale.y;
@@ -241,7 +247,7 @@ __device__ __forceinline__ void step8(const PagedFwdArgs& p, uint32_t ks, uint32
   // Weights in fp16, for fp16 outputs in two words (p = hi + lo to 2^-22 of p): a bf16
   // output's rounding makes eight times what the one word leaves out (2^-9, 2^-12).
   constexpr bool TWO_WORDS = !C::BF16;
-  const float factor = fold ? part : 1.f, rest = fold ? 1.f : part;
+  const float factor = fold ? part * kWeightLift : kWeightLift, rest = fold ? 1.f : part;
   uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -577,6 +583,7 @@ fa_paged8_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_c
       }
     }
     // the warps' maxima and sums, and their rows side by side
+    const float out = unit * (1.f / kWeightLift);
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
@@ -599,7 +606,7 @@ fa_paged8_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_c
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          om[(kw * C::ROWS + col0 + 8 * nt + (e & 1)) * C::OP + acc_column<C>(i, lane, e)] = acc[nt][i][e] * unit;
+          om[(kw * C::ROWS + col0 + 8 * nt + (e & 1)) * C::OP + acc_column<C>(i, lane, e)] = acc[nt][i][e] * out;
     const Walk done = w;
     more = w.next(list, window);
     if (more) load_ahead();

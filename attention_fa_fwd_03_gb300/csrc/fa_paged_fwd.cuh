@@ -969,12 +969,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 
     // merge the key warps
     if constexpr (C::E8) {
+      const float out = unit * (1.f / kWeightLift);
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][i][e] *= unit;
+          for (int e = 0; e < 4; ++e) acc[nt][i][e] *= out;
     }
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt)
