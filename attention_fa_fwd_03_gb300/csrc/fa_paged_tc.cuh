@@ -54,7 +54,7 @@ struct PagedTcCfg {
   static constexpr int D = D_, RG = RG_;
   static constexpr bool BF16 = BF16_, E8 = E8_;
   static constexpr bool MMA_BF16 = BF16 && !E8;   // type of the products' operands
-  static constexpr bool TWO_WORDS = !(E8 && BF16);  // of weights: fp16 for a bf16 output needs one (fa_paged8.cuh)
+  static constexpr bool TWO_WORDS = !(E8 && BF16);  // of weights: one fp16 word for a bf16 output (fa_paged8.cuh)
   static constexpr int ROWS = 32 * RG;           // rows of a block
   static constexpr int COPIES = 4 / RG;          // of each row
   static constexpr int KEYS = kPagedTile / COPIES;  // of a tile that a copy takes

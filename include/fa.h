@@ -345,7 +345,10 @@ fa_status fa_kv_append8(const fa_paged_kv8* kv, const void* k_new, const int64_t
                         int interleaved, fa_dtype dt, cudaStream_t stream);
 
 /* fa_paged_fwd_sinks over a cache of 8 bits: q and o of type dt; keys and values are the
- * numbers that the cache stands for. Workspace and rules of fa_paged_fwd; a scale that
+ * numbers that the cache stands for. Weights p of the values are rounded to fp16 numbers for
+ * bf16 outputs, so that O is off by up to 2^-11 sum p |v| / sum p beside its own rounding, and
+ * held to 2^-22 of themselves for fp16 outputs; and each key's p v is off by up to 2^-32 of the
+ * row's largest p times 448 times its sequence's largest scale of values. Workspace and rules of fa_paged_fwd; a scale that
  * fa_kv_append8 would not write (0, negative, no power of two, infinite or NaN) gives
  * undefined rows. */
 fa_status fa_paged_fwd8(const fa_paged_kv8* kv, const void* q, void* o, float* lse, int Hq, int Tq,

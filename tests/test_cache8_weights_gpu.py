@@ -113,3 +113,45 @@ def test_first_token_dominates(heads, D, n, dt):
         bound = (1 + h) * (rel[:, None] * (p @ vv.abs()) + lost[:, None]) + h * want.abs() + 2.0 ** -25
         assert ((o[0, :, 0] - want).abs() <= bound).all(), float(((o[0, :, 0] - want).abs() / bound).max())
         assert ((lse[0, :, 0] - lz).abs() <= ds + 2.0 ** -21 + sums + 8 * U * (lz.abs() + s.abs().amax(-1))).all()
+
+
+WORDS = {"fp16": 2.0 ** -22, "bf16": 2.0 ** -11}  # of a weight, what the words it goes to its product in leave out
+
+
+def weights_that_round_alike(dtype):
+    """A score x whose weight exp(x) beside weights of 1 is as far from fp16's numbers as can be; x a number of the type."""
+    xs = torch.linspace(-0.45 * 2.0 ** -10, -0.05 * 2.0 ** -10, 4000).to(dtype).unique()
+    w = xs.double().exp()
+    i = (w.half().double() - w).abs().argmax()
+    return float(xs[i]), float(w[i]), float(w[i].half())
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("heads,D,n", SIZES)
+def test_values_that_cancel(heads, D, n, dt):
+    """Every other key has the weight w < 1 and V = -1, the others 1 and V = 1: O = (1 - w) / (1 + w), next to nothing, and
+    all weights w round alike. For fp16 outputs the second word is what O is made of; for bf16 outputs there is one word, and O
+    is off by its half step of the weights' sum of |V| and no more.
+
+    Bound. The exponential is off by 2^-21 w and the score's by (2 D + 8) u |x| w. Partial sums of O are at most 64 of one sign
+    beyond what cancels, n (1 - w) / 2 in all (with one word n 2^-12 / 2 more), so n additions of 2 u each leave 2 u (64 + that)
+    n over a sum of weights of n (1 + w) / 2; joins a few u."""
+    x, w, rounded = weights_that_round_alike(DT[dt])
+    pages = -(-n // PAGE)
+    k = torch.zeros(pages, 1, PAGE, D)
+    v = torch.ones(pages, 1, PAGE, D)
+    k[:, :, 1::2, 0] = 1
+    v[:, :, 1::2] = -1
+    q = torch.zeros(1, heads, 1, D, dtype=DT[dt])
+    q[..., 0] = x
+    ones, ws = (n + 1) // 2, n // 2
+    want = (ones - ws * w) / (ones + ws * w)
+    h = torch.finfo(DT[dt]).eps / 2
+    o, lse = run(k.to(ref.E4M3), torch.ones(pages, 1), v.to(ref.E4M3), torch.ones(pages, 1), q, 1.0, n)
+    bound = (h * abs(want) + WORDS[dt] + 2.0 ** -32 + 2.0 ** -20 + (2 * D + 8) * U * abs(x) + 4 * U * (64 + n * (1 - w + 2.0 ** -11) / 2)
+             + 16 * U + 2.0 ** -25)
+    if dt == "fp16":
+        one_word = (ones - ws * rounded) / (ones + ws * w)
+        assert abs(one_word - want) > 5 * bound  # the oracle with one word does not pass
+    assert (o - want).abs().max() <= bound, (float((o - want).abs().max()), bound)
+    assert (lse - math.log(ones + ws * w)).abs().max() <= 2.0 ** -20 + 2 * (n + 16) * U
