@@ -14,8 +14,8 @@ and workspace tensors are allocated by PyTorch, every step of the computation
 runs in the library's kernels, and there is no CPU path (a CPU tensor raises).
 
 ``flash_attention`` is the compiled node (csrc/autograd_binding.h), whose
-backward does not wait for the interpreter's lock; ``FlashAttention`` is the
-same calls as a ``torch.autograd.Function``, for code that builds on one.
+backward does not wait for the interpreter's lock. ``FlashAttention.apply`` is
+the same node under the name and arguments of a ``torch.autograd.Function``.
 
     from attention_fa_fwd_03_gb300.autograd import flash_attention
     o = flash_attention(q, k, v, causal=True)          # q [B,Hq,Tq,D], k/v [B,Hkv,Tkv,D]
@@ -27,38 +27,17 @@ import math
 
 import torch
 
-from . import _paged_calls, fa_bwd, fa_bwd_sinks_workspace_size, fa_bwd_workspace_size, fa_fwd
+from . import _paged_calls
 
 __all__ = ["FlashAttention", "flash_attention"]
 
 
 class FlashAttention(torch.autograd.Function):
-    """(q, k, v, scale, causal, window[, sinks]) -> (O, LSE); gradients for q, k, v only."""
+    """``apply(q, k, v, scale, causal, window[, sinks])`` -> (O, LSE); gradients for q, k, v only."""
 
     @staticmethod
-    def forward(ctx, q, k, v, scale: float, causal: bool, window: int, sinks: int = 0):
-        with torch.cuda.device(q.device):
-            o = torch.empty_like(q)
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-            fa_fwd(q, k, v, o, lse, scale, causal, window, sinks=sinks)
-        ctx.save_for_backward(q, k, v, o, lse)
-        ctx.attn = (scale, causal, window, sinks)
-        ctx.mark_non_differentiable(lse)
-        return o, lse
-
-    @staticmethod
-    def backward(ctx, do, _dlse):
-        q, k, v, o, lse = ctx.saved_tensors
-        scale, causal, window, sinks = ctx.attn
-        with torch.cuda.device(q.device):
-            do = do.contiguous()
-            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-            B, Hq, Tq, D = q.shape
-            size = (fa_bwd_sinks_workspace_size(B, Hq, k.shape[1], Tq, k.shape[2], D, window, sinks) if sinks
-                    else fa_bwd_workspace_size(B, Hq, Tq))
-            ws = torch.empty(size, dtype=torch.uint8, device=q.device)
-            fa_bwd(q, k, v, o, do, lse, dq, dk, dv, scale, causal, window, workspace=ws, sinks=sinks)
-        return dq, dk, dv, None, None, None, None
+    def apply(q, k, v, scale: float, causal: bool, window: int, sinks: int = 0):
+        return _paged_calls().attention(q, k, v, scale, causal, window, sinks)
 
 
 def flash_attention(q, k, v, scale: float | None = None, causal: bool = False, window: int = 0,
