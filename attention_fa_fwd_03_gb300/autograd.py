@@ -16,6 +16,7 @@ runs in the library's kernels, and there is no CPU path (a CPU tensor raises).
 ``flash_attention`` is the compiled node (csrc/autograd_binding.h), whose
 backward does not wait for the interpreter's lock. ``FlashAttention.apply`` is
 the same node under the name and arguments of a ``torch.autograd.Function``.
+There is no second derivative: differentiating the gradients raises.
 
     from attention_fa_fwd_03_gb300.autograd import flash_attention
     o = flash_attention(q, k, v, causal=True)          # q [B,Hq,Tq,D], k/v [B,Hkv,Tkv,D]
@@ -51,7 +52,8 @@ def flash_attention(q, k, v, scale: float | None = None, causal: bool = False, w
     the first ``sinks`` keys, which stay visible.
     Non-contiguous inputs are copied to contiguous ones first. With
     ``return_lse`` the natural-log LSE [B,Hq,Tq] (fp32, no gradient) is
-    returned beside O.
+    returned beside O. Gradients made with ``create_graph`` raise where they
+    are differentiated again.
     """
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])

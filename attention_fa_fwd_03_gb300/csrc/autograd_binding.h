@@ -12,6 +12,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/accumulate_grad.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/graph_task.h>
 
 namespace attention {
@@ -62,6 +63,17 @@ inline void refuse_leaves_of_default_stream(const c10::cuda::CUDAStream& current
           "flash_attention: this backward pass is being captured into a CUDA graph while an eager graph of the same leaves "
           "from the default stream lives; delete its outputs first");
   }
+}
+
+// The gradients are kernels' outputs without a graph. Where one is being made of them
+// (create_graph) they get a node that raises if it is differentiated: without it a second
+// derivative would leave attention's part out without a word.
+inline torch::autograd::variable_list not_differentiable_again(torch::autograd::variable_list grads) {
+  if (!at::GradMode::is_enabled()) return grads;
+  for (at::Tensor& g : grads) g.requires_grad_();
+  const auto raise = std::make_shared<torch::autograd::DelayedError>(
+      "flash_attention has no second derivative: its gradients cannot be differentiated", static_cast<int64_t>(grads.size()));
+  return (*raise)(std::move(grads));
 }
 
 struct Sizes {
@@ -115,7 +127,9 @@ class Node : public torch::autograd::Function<Node> {
                               static_cast<float>(ctx->saved_data["scale"].toDouble()), ctx->saved_data["causal"].toBool(),
                               window, sinks, s.dt, workspace.data_ptr(), bytes, current_stream(q)),
                  "fa_bwd");
-    return {dq, dk, dv, at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor()};
+    List out = not_differentiable_again({dq, dk, dv});
+    out.resize(7);  // (none of scale, causal, window and sinks)
+    return out;
   }
 };
 
