@@ -66,6 +66,7 @@ struct PagedTcCfg {
   static constexpr int WGS = D == 256 ? 1 : 2;
   // (E8: whole warpgroups, which share the registers unevenly: producers and issuers, converters)
   static constexpr int SOFT = 128 * WGS, SCORE_WARP = 4 * WGS + PRODUCERS, CONVERT_WARP = 4 * WGS + 4;
+  static_assert(!E8 || SCORE_WARP + 2 == CONVERT_WARP, "every warp has a role: the window moves on with all of them");
   static constexpr int THREADS = E8 ? SOFT + 256 : SOFT + 32 * PRODUCERS + 64;
   static constexpr int REG_SOFT = 168, REG_REST = 88;
   static constexpr int REG_NEEDED = E8 ? SOFT * REG_SOFT + 256 * REG_REST : 0;
@@ -287,10 +288,6 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       produce_share<C>(p, list, share, window, ring);
       ring.drain();
     }
-  } else if (C::E8 && warp >= C::SCORE_WARP + 2) {
-    // (a warp that fills the warpgroup: it goes with the window)
-    Walk w;
-    for (bool more = w.start(list, share, window); more;) more = w.next(list, window);
   } else if (warp >= C::SCORE_WARP) {
     // -------------------------------------------------------------- MMA issuers
     // (all lanes compute the descriptors and one issues)
