@@ -79,6 +79,10 @@ struct PagedCfg {
   static constexpr int D = D_, NT = NT_, RW = RW_;
   static constexpr bool BF16 = BF16_, E8 = E8_;
   static constexpr bool CLUSTER = CLUSTER_;          // a cluster per unit instead of equal shares
+  // fp16 weights: running maxima are held this much lower (in the exp2 domain), so that weights
+  // are up to 2^15 and small ones beside a dominating key keep their digits, down to 2^-17 of
+  // the maximum's (without: 2^-10; a weight below 2^-25 was nothing). Sums follow by themselves.
+  static constexpr float LIFT = BF16_ || E8_ ? 0.f : 7.f;
   // Tiles per CTA up to which clusters are used. 64 rows, D 128, 16 units of 64 tiles (16
   // per CTA): 28.7 us, split 21.7; of 32 tiles: 18.0 and 18.4; 24 rows, 64 tiles 17.6 and 19.4.
   static constexpr int CLUSTER_TILES = NT == 4 ? 8 : 16;
@@ -121,7 +125,8 @@ struct PagedCfg {
 };
 
 // Running maxima may be behind by this much (in the exp2 domain) before the sums
-// are rescaled: weights then reach 2^8 instead of 1, which costs no precision.
+// are rescaled: weights then reach 2^8 instead of 1, which costs no precision. (fp16: 2^15
+// instead of 2^7, see PagedCfg::LIFT.)
 constexpr float kPagedSlack = 8.f;
 // Running maximum of a row that has seen no key: finite, so that a hidden score of
 // -inf less it is -inf, and the lowest number, so that any score raises it.
@@ -836,7 +841,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             x[nt][e] = fmaf(s[nt][e], p.scale_log2, -m[nt][e & 1]);
-            above |= x[nt][e] > kPagedSlack;
+            above |= x[nt][e] > kPagedSlack + C::LIFT;
           }
         }
         if (__any_sync(0xffffffffu, above)) {
@@ -850,7 +855,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-              const float mn = fmaxf(m[nt][h], y * p.scale_log2);
+              const float mn = fmaxf(m[nt][h], __fmul_rn(y, p.scale_log2) - C::LIFT);
               alpha[h] = ex2(m[nt][h] - mn);
               m[nt][h] = mn;
               any_large |= large_max(mn);
@@ -875,7 +880,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           }
         }
         // Weights in two words of the cache's type, p = hi + lo to 2^-17 (bf16) or
-        // 2^-22 (fp16) of p, and transposed into B fragments: with hi alone O would be
+        // 2^-22 (fp16; 2^-25 at least, see LIFT) of p, and transposed into B fragments: with hi alone O would be
         // off by 1.4 times as much as its own rounding makes it. The products with lo
         // cost no time where the tiles' bytes bound the kernel.
         uint32_t pb[C::NT][2], pl[C::NT][2];

@@ -88,10 +88,11 @@ struct PagedTcCfg {
   static constexpr int OFF_ML = E8 ? OFF_Q + (Q_BYTES > O_BYTES ? Q_BYTES : O_BYTES) : OFF_O + O_BYTES;  // [warpgroup][copies][rows]
   static constexpr int OFF_RAW = (OFF_ML + SOFT * 8 + 1023) / 1024 * 1024;
   static constexpr int SMEM_BYTES = (E8 ? OFF_RAW + Raw::STAGES * 2 * Raw::TILE : OFF_ML + SOFT * 8) + 1024;
-  // E8: weights are up to 2^8 and parts of scales at most 1; times this they stay within
-  // fp16, and what a small part leaves of its digits is 2^-31 of the largest scale
-  static constexpr int LIFT_LOG2 = 7;
-  static constexpr float LIFT = 128.f;
+  // fp16 weights are up to 2^8 (E8: times parts of scales, at most 1); times this they stay
+  // within fp16, and small ones beside a dominating key keep their digits (E8: what a small
+  // part leaves of them is 2^-31 of the largest scale)
+  static constexpr int LIFT_LOG2 = MMA_BF16 ? 0 : 7;
+  static constexpr float LIFT = MMA_BF16 ? 1.f : 128.f;
   static_assert(SMEM_BYTES <= 229000, "shared memory");
   // TMEM columns
   __host__ __device__ static constexpr int S_COL(int b) { return kPagedTile * b; }
@@ -138,6 +139,14 @@ __device__ __forceinline__ float2 fma2(uint32_t a, uint32_t b, uint64_t f, uint6
       " mov.b64 x, {%2, %3};\n fma.rn.f32x2 x, x, %4, %5;\n fma.rn.f32x2 x, x, %6, %7;\n mov.b64 {%0, %1}, x;\n}"
       : "=f"(r.x), "=f"(r.y)
       : "r"(a), "r"(b), "l"(f), "l"(c), "l"(g), "l"(d));
+  return r;
+}
+__device__ __forceinline__ float2 add_fma2(uint32_t a, uint32_t b, uint64_t c, uint64_t f, uint64_t d) {  // ((a, b) + c) f + d
+  float2 r;
+  asm("{\n .reg .b64 x;\n"
+      " mov.b64 x, {%2, %3};\n add.rn.f32x2 x, x, %4;\n fma.rn.f32x2 x, x, %5, %6;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(a), "r"(b), "l"(c), "l"(f), "l"(d));
   return r;
 }
 __device__ __forceinline__ float2 add_mul2(uint32_t a, uint32_t b, uint64_t c, uint64_t f) {
@@ -568,6 +577,8 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           float2 x;
           if constexpr (C::E8)
             x = fma2(sv[2 * e], sv[2 * e + 1], pair_of(factor[q]), top2, scale2, pair_of(power[q] < -40.f ? 0.f : power[q]));
+          else if constexpr (C::LIFT_LOG2 > 0)
+            x = add_fma2(sv[2 * e], sv[2 * e + 1], top2, scale2, pair_of(C::LIFT_LOG2));
           else
             x = add_mul2(sv[2 * e], sv[2 * e + 1], top2, scale2);
           const float p0 = ex2(x.x), p1 = ex2(x.y);
@@ -658,7 +669,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 if (!partial(j)) continue;
                 float s = __uint_as_float(tmem_ld1(lanes + C::S_COL(b) + key));
                 tmem_ld_wait();
-                float share = 1.f;
+                float share = C::LIFT;
                 if constexpr (C::E8) {
                   const float2 sc = kv_scale[slot][key >> 4];
                   s = s * fminf(own_scale, sc.x) * fmaxf(own_scale, sc.x);
@@ -720,14 +731,15 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
       }
       const bool begins = w.t0 == 0, ends = w.t1 == w.it.tiles;
       const int part_slot = 2 * part + (begins ? 1 : 0);
-      mls[tid] = make_float2(m, l);  // [warpgroup][copy][row]
+      constexpr float DROP = C::E8 ? 1.f : 1.f / C::LIFT;  // (E8: the units have it, and l is without)
+      mls[tid] = make_float2(m, l * DROP);  // [warpgroup][copy][row]
       if constexpr (C::E8) units[tid] = unit / C::LIFT;
       sync_rows();
       const float2 ml0 = mls[tid & 127], ml1 = mls[128 * (C::WGS - 1) + (tid & 127)];
       float mt = -INFINITY;
 #pragma unroll
       for (int k = 0; k < C::WGS * C::COPIES; ++k) mt = fmaxf(mt, mls[k * C::ROWS + row].x);
-      float f0 = exp2_rel(ml0.x, mt), f1 = exp2_rel(ml1.x, mt);
+      float f0 = exp2_rel(ml0.x, mt) * DROP, f1 = exp2_rel(ml1.x, mt) * DROP;
       if constexpr (C::E8) {
         f0 *= units[tid & 127];
         f1 *= units[128 * (C::WGS - 1) + (tid & 127)];
