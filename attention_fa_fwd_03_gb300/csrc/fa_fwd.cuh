@@ -41,9 +41,20 @@ namespace fa {
 
 // Lazy-rescale threshold in the log2 domain: the running max used for the
 // exponentials is only raised when the true max exceeds it by more than this,
-// so unnormalised P stays below 2^8. The final O = o / l and LSE = m + log2 l
+// so unnormalised P stays below 2^8 (fp16: 2^15, see held_max). The final O = o / l and LSE = m + log2 l
 // use the same max, so the result is exact.
 constexpr float kRescaleThreshold = 8.0f;
+
+// fp16 weights: the running maximum is held this much lower (in the exp2 domain), so that
+// weights are up to 2^15 and small ones beside a dominating key (as a first token is to many
+// heads) keep their digits, down to 2^-21 of the maximum's. Without it a weight loses digits
+// below 2^-14 and is nothing below 2^-25, while the row's sum counts it. Sum, LSE and O follow
+// by themselves. (A maximum beyond 2^22, whose steps are 1/2 and more, is left as it is: its
+// rounding takes the headroom.)
+template <bool BF16>
+__device__ __forceinline__ float held_max(float mx) {
+  return BF16 || fabsf(mx) > 4194304.f ? mx : mx - 7.f;
+}
 
 // One forward work item: a (batch, head) and a block of NQ * 128 query rows;
 // its tiles are the key tiles the block sees.
@@ -391,6 +402,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                          fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
         mx *= c;
         float alpha = 1.f;
+        mx = held_max<C::BF16>(mx);
         const bool grow = mx > m_used + kRescaleThreshold || (m_used == -INFINITY && mx > -INFINITY);
         if (grow) {
           alpha = ex2(m_used - mx);  // 0 when m_used = -inf
