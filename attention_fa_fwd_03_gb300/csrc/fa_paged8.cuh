@@ -364,7 +364,7 @@ __device__ __forceinline__ void step8(const PagedFwdArgs& p, uint32_t ks, uint32
 template <int D_, int NT_, bool BF16_>
 struct Paged8Cfg {
   static constexpr int D = D_, NT = NT_, RW = 1;
-  static constexpr bool BF16 = BF16_, E8 = true, CLUSTER = false;
+  static constexpr bool BF16 = BF16_, E8 = true, CLUSTER = false, WINDOW = true, SINKS = true;
   static constexpr int KW = kPagedKeyWarps, ROWS = 8 * NT;
   static constexpr int GROUPS = D == 256 ? (NT == 1 ? 2 : 1) : NT == 1 ? 3 : 2;
   static constexpr int WARPS = KW, GROUP_THREADS = 32 * (KW + 1);  // of a group: consumers, and with the producer
@@ -473,7 +473,7 @@ fa_paged8_split_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_c
   const int group = consumer ? warp / C::KW : min(warp - C::GROUPS * C::KW, C::GROUPS - 1), kw = warp % C::KW;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u) + group * C::GROUP_BYTES;
   const uint32_t sbase = smem_u32(smem);
-  ListShape list = list_shape(p);
+  ListShape list = list_shape<C>(p);
   list.over = C::OVER;
   const int part = C::GROUPS * blockIdx.x + group;
   if (threadIdx.x == 0) {

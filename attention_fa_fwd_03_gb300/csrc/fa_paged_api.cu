@@ -252,13 +252,15 @@ fa_status paged_fwd(const Cache* kv, const void* q, void* o, float* lse, int Hq,
   a.ws = static_cast<float*>(workspace);
   a.bf16 = kv->dt == FA_BF16;
   a.stream = stream;
-  cudaError_t e;
-  switch (kv->D) {
-    case 64: e = kv->e4m3 ? launch_paged_fwd8_d64(a) : launch_paged_fwd_d64(a); break;
-    case 96: e = kv->e4m3 ? launch_paged_fwd8_d96(a) : launch_paged_fwd_d96(a); break;
-    case 128: e = kv->e4m3 ? launch_paged_fwd8_d128(a) : launch_paged_fwd_d128(a); break;
-    default: e = kv->e4m3 ? launch_paged_fwd8_d256(a) : launch_paged_fwd_d256(a); break;
-  }
+  using Launch = cudaError_t (*)(const PagedFwdLaunch&);
+  static constexpr Launch kLaunch[4][4] = {  // by cache and window, by head dim
+      {launch_paged_fwd_d64, launch_paged_fwd_d96, launch_paged_fwd_d128, launch_paged_fwd_d256},
+      {launch_paged_fwd_window_d64, launch_paged_fwd_window_d96, launch_paged_fwd_window_d128, launch_paged_fwd_window_d256},
+      {launch_paged_fwd_sinks_d64, launch_paged_fwd_sinks_d96, launch_paged_fwd_sinks_d128, launch_paged_fwd_sinks_d256},
+      {launch_paged_fwd8_d64, launch_paged_fwd8_d96, launch_paged_fwd8_d128, launch_paged_fwd8_d256}};
+  const int kind = kv->e4m3 ? 3 : window == 0 ? 0 : sinks == 0 ? 1 : 2;
+  const int dim = kv->D == 64 ? 0 : kv->D == 96 ? 1 : kv->D == 128 ? 2 : 3;
+  const cudaError_t e = kLaunch[kind][dim](a);
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 

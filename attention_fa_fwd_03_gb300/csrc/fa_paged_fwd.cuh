@@ -72,12 +72,17 @@ struct PagedFwdArgs {
   WaitCfg wc;
 };
 
+enum : int { kNoWindow, kWindow, kWindowSinks };
+
 // NT: groups of 8 query rows that a warp holds; RW: warps of other rows beside it.
-// E8: the cache is held in e4m3 with scales (fa_paged8.cuh).
-template <int D_, int NT_, int RW_, bool BF16_, bool CLUSTER_, bool E8_ = false>
+// E8: the cache is held in e4m3 with scales (fa_paged8.cuh). MASK: without a window, with one,
+// or with one that leaves the first p.sinks keys visible. (Kernels of their own over 16 bits:
+// one for all three takes 173.5 us for 64 ragged sequences without a window instead of 167.2,
+// 5.5 instead of 5.3 for two of 1024 keys. Over 8 bits the last one does for all.)
+template <int D_, int NT_, int RW_, bool BF16_, bool CLUSTER_, bool E8_, int MASK_>
 struct PagedCfg {
   static constexpr int D = D_, NT = NT_, RW = RW_;
-  static constexpr bool BF16 = BF16_, E8 = E8_;
+  static constexpr bool BF16 = BF16_, E8 = E8_, WINDOW = MASK_ >= kWindow, SINKS = MASK_ == kWindowSinks;
   static constexpr bool CLUSTER = CLUSTER_;          // a cluster per unit instead of equal shares
   // fp16 weights: running maxima are held this much lower (in the exp2 domain), so that weights
   // are up to 2^15 and small ones beside a dominating key keep their digits, down to 2^-17 of
@@ -139,9 +144,19 @@ constexpr float kLargeMax = 4194304.f;  // 2^22: steps of 1/2
 __device__ __forceinline__ bool large_max(float m) { return fabsf(m) > kLargeMax && m != kNoMax; }
 
 // ----------------------------------------------------------------- the list
+template <class C>
 __device__ __forceinline__ ListShape list_shape(const PagedFwdArgs& p) {
-  return {p.sel ? p.c.B * p.c.Hkv : p.c.B, (p.sel ? 1 : p.c.Hkv) * p.row_blocks, p.sel != nullptr, p.window,
-          p.c.page_shift, p.sinks, 0};
+  return {p.sel ? p.c.B * p.c.Hkv : p.c.B, (p.sel ? 1 : p.c.Hkv) * p.row_blocks, p.sel != nullptr, C::WINDOW ? p.window : 0,
+          p.c.page_shift, C::SINKS ? p.sinks : 0, 0};
+}
+template <class C>
+__device__ __forceinline__ bool windowed(const PagedFwdArgs& p) {
+  return C::WINDOW && p.window > 0;
+}
+// Key j is none of the first keys that a window leaves visible.
+template <class C>
+__device__ __forceinline__ bool past_sinks(const PagedFwdArgs& p, int j) {
+  return !C::SINKS || j >= p.sinks;
 }
 __device__ __forceinline__ int item_seq(const PagedFwdArgs& p, int item) { return p.sel ? item / p.c.Hkv : item; }
 __device__ __forceinline__ ItemLens load_lens(const PagedFwdArgs& p, int item) {
@@ -382,9 +397,10 @@ __device__ __forceinline__ void mbar_arrive_async_loads(uint32_t bar) {
 constexpr int kNoPosition = 1 << 30;
 
 // Whether every new token (positions p_lo to len - 1) sees all of keys j0 to j0 + 15.
+template <class C>
 __device__ __forceinline__ bool sees_all(const PagedFwdArgs& p, int len, int p_lo, int j0) {
   return j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) &&
-         !(p.window > 0 && j0 <= len - 1 - p.window && j0 + 15 >= p.sinks);
+         !(windowed<C>(p) && j0 <= len - 1 - p.window && past_sinks<C>(p, j0 + 15));
 }
 // Beside the position of 16 keys of a stage (E8): that is so.
 constexpr int kSeenByAll = static_cast<int>(0x80000000u);
@@ -431,7 +447,7 @@ struct TileRing {
       const int j0 = kid >= 0 ? (kpage << c.page_shift) + koff + lane * 16 - pl * piece : kNoPosition;
       key_pos[slot][lane] = j0;
       if constexpr (C::E8) {
-        if (sees_all(p, it.len, it.len - it.n, j0)) key_pos[slot][lane] = j0 | kSeenByAll;
+        if (sees_all<C>(p, it.len, it.len - it.n, j0)) key_pos[slot][lane] = j0 | kSeenByAll;
       }
       // the scales come as the tile does, into this stage and to its barrier
       if constexpr (C::E8) {
@@ -471,13 +487,15 @@ struct TileRing {
 
 // First key that the window shows to a new token of the item, apart from the first keys;
 // 0 where no window moves it. (Selected pages are loaded whatever it shows.)
+template <class C>
 __device__ __forceinline__ int first_shown(const PagedFwdArgs& p, const Item& it) {
-  return p.window > 0 && !p.sel ? it.len - it.n - p.window + 1 : 0;
+  return windowed<C>(p) && !p.sel ? it.len - it.n - p.window + 1 : 0;
 }
 // Pool page of keys [key, key + piece), for which the table has `id`, or -1: also where
 // none of them is shown. Their page may have been given back, and the table then has -1.
+template <class C>
 __device__ __forceinline__ int piece_page(const PagedFwdArgs& p, int shown, int key, int piece, int id) {
-  const bool seen = key + piece > shown || key < p.sinks;
+  const bool seen = key + piece > shown || !past_sinks<C>(p, key);
   if (!seen && id == -1) return -1;
   id = checked_page(p.c, id);
   return seen ? id : -1;
@@ -499,7 +517,7 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
     const int count = p.sel ? w.it.listed : pages;
     // pages of list entries [e0, e0 + 32) and the next 32, one per lane (under a window
     // whether the table has a pool page matters only where a tile's keys are shown)
-    const int shown = first_shown(p, w.it);
+    const int shown = first_shown<C>(p, w.it);
     auto look_up = [&](int e, int* page, int* id) {
       *page = -1;
       *id = -1;
@@ -514,7 +532,7 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
       }
       *page = pg;
       *id = c.table[static_cast<int64_t>(b) * c.max_pages + pg];
-      if (shown <= 0) *id = checked_page(c, *id);
+      if (!C::WINDOW || shown <= 0) *id = checked_page(c, *id);
     };
     int e0 = (w.it.tile(w.t0) * kPagedTile) >> c.page_shift;
     int page0, id0, page1, id1;
@@ -523,7 +541,7 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
     for (int t = w.t0; t < w.t1 && ring.ok; ++t) {
       const int x = w.it.tile(t) * kPagedTile;  // first key of the tile in the list
       int e = (x >> c.page_shift) - e0;
-      if (e >= 64) {  // the tiles behind the first keys of a window are further on
+      if (C::SINKS && e >= 64) {  // the tiles behind the first keys of a window are further on
         e0 += e;
         e = 0;
         look_up(e0 + lane, &page0, &id0);
@@ -539,7 +557,7 @@ __device__ __forceinline__ void produce_share(const PagedFwdArgs& p, const ListS
       const int my = e + ((lane * ring.piece) >> c.page_shift);  // below 32: pages of 16 start tiles at multiples of 4
       const int pg = __shfl_sync(0xffffffffu, page0, my & 31);
       int id = __shfl_sync(0xffffffffu, id0, my & 31);
-      if (shown > 0 && lane < ring.pieces && pg >= 0) id = piece_page(p, shown, x + lane * ring.piece, ring.piece, id);
+      if (C::WINDOW && shown > 0 && lane < ring.pieces && pg >= 0) id = piece_page<C>(p, shown, x + lane * ring.piece, ring.piece, id);
       ring.load(x, pg, id, g, w.it);
     }
   }
@@ -568,7 +586,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedView& c = p.c;
-  const ListShape list = list_shape(p);
+  const ListShape list = list_shape<C>(p);
   const int part = blockIdx.x, parts = gridDim.x;
   const uint64_t tmo = p.wc.timeout_cycles;
   if (threadIdx.x == 0) {
@@ -631,17 +649,17 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         if (p.sel) pg = e < p.n_sel ? p.sel[u * p.n_sel + e] : -1;
         if (static_cast<unsigned>(pg) < static_cast<unsigned>(c.max_pages)) id = c.table[row + pg];
       };
-      const bool early = p.sel != nullptr || p.window == 0;
+      const bool early = p.sel != nullptr || !windowed<C>(p);
       if (early) read(0);
       w.start_unit(list, rank, ranks, load_lens_warp(p, w.item));
-      const int shown = first_shown(p, w.it);
+      const int shown = first_shown<C>(p, w.it);
       const int pages = (w.it.len + (1 << c.page_shift) - 1) >> c.page_shift;
       const int count = p.sel ? w.it.listed : pages;
       for (int t0 = 0; t0 < w.t1 && ring.ok; t0 += batch) {
         if (t0 > 0 || !early) read(t0);
         const bool counts = t0 + mine < w.t1 && e < count;
         if (counts && static_cast<unsigned>(pg) < static_cast<unsigned>(pages)) {
-          id = piece_page(p, shown, x, piece, id);
+          id = C::WINDOW ? piece_page<C>(p, shown, x, piece, id) : checked_page(c, id);
         } else {
           if (counts) flag_bad_index(c);  // a selected page that the sequence does not have
           id = -1;
@@ -763,7 +781,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       const uint32_t ks = sbase + C::OFF_KV + slot * 2 * C::TILE, vs = ks + C::TILE;
       // does any row see any of the 16 keys; do all rows see all of them
       const bool known = C::E8 && at_keys < 0;
-      const bool some = has_rows && (known || (j0 < len && !(p.window > 0 && j0 + 15 <= p_lo - p.window && j0 >= p.sinks)));
+      const bool some = has_rows && (known || (j0 < len && !(windowed<C>(p) && j0 + 15 <= p_lo - p.window && past_sinks<C>(p, j0))));
       if constexpr (C::E8) {
         if (some) {
           auto query = [&](uint32_t (&b)[4], int nt, int k2) {
@@ -778,11 +796,15 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                               query, rs, m, l, acc, unit, large);
         }
       } else if (some) {
-        const bool all = sees_all(p, len, p_lo, j0);
+        const bool all = sees_all<C>(p, len, p_lo, j0);
         // S^T = K Q^T: element e of group nt is key j0 + lane / 4 + 8 (e / 2), row
         // col0 + 8 nt + e % 2. One group: two accumulators, half as long a chain.
         float s[C::NT][4], s2[4];
-        const int kr = kw * 16 + (lane & 15), kc = lane >> 4;
+        // (D 128, 16 rows: the lane's places are worked out anew for every tile; held in registers
+        // they spill others: 16 rows of 8 sequences of 8192 keys 55.7 us, 58.7 with them)
+        int ln = lane;
+        if constexpr (C::NT == 2 && D == 128 && !C::CLUSTER) asm volatile("" : "+r"(ln));
+        const int kr = kw * 16 + (ln & 15), kc = ln >> 4;
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) {
           uint32_t a0[4], a1[4];
@@ -821,14 +843,14 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int pos = p_lo + token(nt, h);
-              const int lo = p.window > 0 ? pos - p.window + 1 - j0 : -j0;
+              const int lo = windowed<C>(p) ? pos - p.window + 1 - j0 : -j0;
               const int hi = (p.causal ? min(len, pos + 1) : len) - j0;
               const unsigned span = static_cast<unsigned>(max(hi - lo, 0)), j = (lane >> 2) - lo;
-              const int keep = min(p.sinks - j0, hi);
-              if (j >= span && (lane >> 2) >= keep) s[nt][h] = -INFINITY;
-              if (j + 8 >= span && (lane >> 2) + 8 >= keep) s[nt][2 + h] = -INFINITY;
+              const int keep = C::SINKS ? min(p.sinks - j0, hi) : 0;
+              if (j >= span && (!C::SINKS || (lane >> 2) >= keep)) s[nt][h] = -INFINITY;
+              if (j + 8 >= span && (!C::SINKS || (lane >> 2) + 8 >= keep)) s[nt][2 + h] = -INFINITY;
             }
-          auto seen = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window && j >= p.sinks); };
+          auto seen = [&](int j) { return j < len && !(windowed<C>(p) && j <= p_lo - p.window && past_sinks<C>(p, j)); };
           keep0 = (seen(jv) ? 0xffffu : 0u) | (seen(jv + 1) ? 0xffff0000u : 0u);
           keep1 = (seen(jv + 8) ? 0xffffu : 0u) | (seen(jv + 9) ? 0xffff0000u : 0u);
         }
@@ -904,10 +926,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         // anything; 0 * NaN would not be 0). Where rows differ in what they see and
         // some of these values are no finite numbers, each token's product is
         // taken with the keys it sees and only its rows are kept.
-        const int vr = kw * 16 + ((lane >> 4) << 3) + (lane & 7), vc = (lane >> 3) & 1;
+        if constexpr (C::NT == 2 && D == 128 && !C::CLUSTER) asm volatile("" : "+r"(ln));
+        const int vr = kw * 16 + ((ln >> 4) << 3) + (ln & 7), vc = (ln >> 3) & 1;
         const bool differ = !all && n > 1 &&
                             ((p.causal && j0 + 15 > p_lo && j0 <= p_hi) ||
-                             (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
+                             (windowed<C>(p) && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
         bool apart = false;
         if (differ) {
           uint32_t odd = 0;
@@ -940,7 +963,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           for (int tok = 0; tok < n; ++tok) {
             const int pos = p_lo + tok;
             auto seen = [&](int j) {
-              return j < len && !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window && j >= p.sinks);
+              return j < len && !(p.causal && j > pos) && !(windowed<C>(p) && j <= pos - p.window && past_sinks<C>(p, j));
             };
             const uint32_t k0 = (seen(jv) ? 0xffffu : 0u) | (seen(jv + 1) ? 0xffff0000u : 0u);
             const uint32_t k1 = (seen(jv + 8) ? 0xffffu : 0u) | (seen(jv + 9) ? 0xffff0000u : 0u);
@@ -1140,8 +1163,8 @@ fa_paged_join_kernel(const PagedFwdArgs p) {
   if (threadIdx.x == 0) record = p.joins[blockIdx.x];
   __syncthreads();
   const int2 join = record;
-  const ListShape list = list_shape(p);
-  if (join.x < 0 || join.x >= static_cast<int64_t>(list.items) * list.mult) return;
+  const int64_t units = static_cast<int64_t>(p.c.B) * p.c.Hkv * p.row_blocks;
+  if (join.x < 0 || join.x >= units) return;
   const int unit = p.by_unit ? blockIdx.x : join.x;
   const int rb = unit % p.row_blocks, rows = min(ROWS, p.rows - rb * ROWS);
   const int64_t row0 = static_cast<int64_t>(unit / p.row_blocks) * p.rows + rb * ROWS;
@@ -1344,9 +1367,9 @@ cudaError_t run_split(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t tiles, i
   return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<C::D, C::ROWS, C::BF16>, p);
 }
 
-template <int D, int RG, bool BF16, bool E8 = false>
+template <int D, int RG, bool BF16, bool E8, int MASK>
 cudaError_t run_split_tc(const PagedFwdLaunch& a, PagedFwdArgs& p, int64_t tiles) {
-  using C = PagedTcCfg<D, RG, BF16, E8>;
+  using C = PagedTcCfg<D, RG, BF16, E8, MASK>;
   return run_split<C>(a, p, tiles, 1, [&](int64_t parts) { return launch_paged_tc<C>(a, p, parts); });
 }
 
@@ -1363,9 +1386,9 @@ inline bool cluster8_pays(const PagedFwdLaunch& a, int rows, int64_t tiles, int 
   return (tiles + ranks - 1) / ranks <= later + list * 3 / 4;
 }
 
-template <int D, int NT, int RW, bool BF16, bool E8>
+template <int D, int NT, int RW, bool BF16, bool E8, int MASK>
 cudaError_t run_paged(const PagedFwdLaunch& a) {
-  using C = PagedCfg<D, NT, RW, BF16, true, E8>;
+  using C = PagedCfg<D, NT, RW, BF16, true, E8, MASK>;
   PagedFwdArgs p = {};
   p.c = a.c;
   p.q = a.q; p.o = a.o; p.lse = a.lse;
@@ -1397,45 +1420,43 @@ cudaError_t run_paged(const PagedFwdLaunch& a) {
   if (clusters) return launch_paged<C>(a, p, units * ranks, ranks);
   if constexpr (RW > 1 && !(E8 && D == 256)) {  // more than 16 rows
     switch (paged_split_rows(p.rows)) {
-      case 32: return run_split_tc<D, 1, BF16, E8>(a, p, tiles);
-      case 64: return run_split_tc<D, 2, BF16, E8>(a, p, tiles);
-      default: return run_split_tc<D, 4, BF16, E8>(a, p, tiles);
+      case 32: return run_split_tc<D, 1, BF16, E8, MASK>(a, p, tiles);
+      case 64: return run_split_tc<D, 2, BF16, E8, MASK>(a, p, tiles);
+      default: return run_split_tc<D, 4, BF16, E8, MASK>(a, p, tiles);
     }
   } else if constexpr (E8 && RW == 1) {
     using S = Paged8Cfg<D, NT, BF16>;
     return run_split<S>(a, p, tiles, S::CTAS, [&](int64_t parts) { return launch_paged8<S>(a, p, parts); });
   } else {
-    using S = PagedCfg<D, NT, RW, BF16, false, E8>;
+    using S = PagedCfg<D, NT, RW, BF16, false, E8, MASK>;
     return run_split<S>(a, p, tiles, S::CTAS, [&](int64_t parts) { return launch_paged<S>(a, p, parts, 1); });
   }
 }
 
-template <int D, bool BF16, bool E8 = false>
+template <int D, bool BF16, bool E8, int MASK>
 cudaError_t run_paged_rows(const PagedFwdLaunch& a) {
   switch (paged_block_rows(a.Hq / a.c.Hkv * a.Tq, D)) {
-    case 8: return run_paged<D, 1, 1, BF16, E8>(a);
-    case 16: return run_paged<D, 2, 1, BF16, E8>(a);
-    case 32: return run_paged<D, 2, 2, BF16, E8>(a);
+    case 8: return run_paged<D, 1, 1, BF16, E8, MASK>(a);
+    case 16: return run_paged<D, 2, 1, BF16, E8, MASK>(a);
+    case 32: return run_paged<D, 2, 2, BF16, E8, MASK>(a);
     case 48:
-      if constexpr (D < 256) return run_paged<D, 3, 2, BF16, E8>(a);
+      if constexpr (D < 256) return run_paged<D, 3, 2, BF16, E8, MASK>(a);
       break;
     default:
-      if constexpr (D < 256) return run_paged<D, 4, 2, BF16, E8>(a);
+      if constexpr (D < 256) return run_paged<D, 4, 2, BF16, E8, MASK>(a);
   }
   return cudaErrorInvalidValue;
 }
 
 }  // namespace fa
 
-#define FA_DEFINE_PAGED_HEAD_DIM(DIM)                                      \
-  namespace fa {                                                           \
-  cudaError_t launch_paged_fwd_d##DIM(const PagedFwdLaunch& a) {           \
-    return a.bf16 ? run_paged_rows<DIM, true>(a) : run_paged_rows<DIM, false>(a); \
-  }                                                                        \
+#define FA_DEFINE_PAGED(NAME, DIM, E8, MASK)                                                   \
+  namespace fa {                                                                              \
+  cudaError_t NAME##DIM(const PagedFwdLaunch& a) {                                            \
+    return a.bf16 ? run_paged_rows<DIM, true, E8, MASK>(a) : run_paged_rows<DIM, false, E8, MASK>(a); \
+  }                                                                                           \
   }
-#define FA_DEFINE_PAGED8_HEAD_DIM(DIM)                                     \
-  namespace fa {                                                           \
-  cudaError_t launch_paged_fwd8_d##DIM(const PagedFwdLaunch& a) {          \
-    return a.bf16 ? run_paged_rows<DIM, true, true>(a) : run_paged_rows<DIM, false, true>(a); \
-  }                                                                        \
-  }
+#define FA_DEFINE_PAGED_HEAD_DIM(DIM) FA_DEFINE_PAGED(launch_paged_fwd_d, DIM, false, kNoWindow)
+#define FA_DEFINE_PAGED_WINDOW_HEAD_DIM(DIM) FA_DEFINE_PAGED(launch_paged_fwd_window_d, DIM, false, kWindow)
+#define FA_DEFINE_PAGED_SINKS_HEAD_DIM(DIM) FA_DEFINE_PAGED(launch_paged_fwd_sinks_d, DIM, false, kWindowSinks)
+#define FA_DEFINE_PAGED8_HEAD_DIM(DIM) FA_DEFINE_PAGED(launch_paged_fwd8_d, DIM, true, kWindowSinks)

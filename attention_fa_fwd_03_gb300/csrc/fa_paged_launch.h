@@ -59,6 +59,14 @@ cudaError_t launch_paged_fwd_d64(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd_d96(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd_d128(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd_d256(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_window_d64(const PagedFwdLaunch& a);  // with a window
+cudaError_t launch_paged_fwd_window_d96(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_window_d128(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_window_d256(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_sinks_d64(const PagedFwdLaunch& a);  // and first keys beside it
+cudaError_t launch_paged_fwd_sinks_d96(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_sinks_d128(const PagedFwdLaunch& a);
+cudaError_t launch_paged_fwd_sinks_d256(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd8_d64(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd8_d96(const PagedFwdLaunch& a);
 cudaError_t launch_paged_fwd8_d128(const PagedFwdLaunch& a);

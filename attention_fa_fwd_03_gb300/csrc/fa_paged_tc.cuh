@@ -49,10 +49,10 @@ namespace fa {
 // scales and mask 400, exponentials 550, waits for scores and products 800). Warp-level products,
 // with the same tiles and shares: 64 rows 102, 128 rows 180. D 256 keeps those (64 rows of 16384
 // keys 93 us): fp16 tiles of 64 KB beside their raw ones leave one stage.
-template <int D_, int RG_, bool BF16_, bool E8_ = false>
+template <int D_, int RG_, bool BF16_, bool E8_, int MASK_>
 struct PagedTcCfg {
   static constexpr int D = D_, RG = RG_;
-  static constexpr bool BF16 = BF16_, E8 = E8_;
+  static constexpr bool BF16 = BF16_, E8 = E8_, WINDOW = MASK_ >= kWindow, SINKS = MASK_ == kWindowSinks;
   static constexpr bool MMA_BF16 = BF16 && !E8;   // type of the products' operands
   static constexpr bool TWO_WORDS = !(E8 && BF16);  // of weights: one fp16 word for a bf16 output (fa_paged8.cuh)
   static constexpr int ROWS = 32 * RG;           // rows of a block
@@ -74,7 +74,7 @@ struct PagedTcCfg {
   static constexpr int QREGION = 128 * 128;
   static constexpr int STAGES = E8 ? (D == 64 ? 6 : 4) : D == 256 ? 2 : D == 64 ? 8 : 5;
   struct Raw {  // tiles as they are held
-    static constexpr bool E8 = true;
+    static constexpr bool E8 = true, WINDOW = true, SINKS = true;
     static constexpr int COLS = 128, KREG = (D_ + 127) / 128, REGION = kPagedTile * 128, TILE = KREG * REGION;
     static constexpr int STAGES = D_ == 64 ? 5 : 3, PRODUCERS = PagedTcCfg::PRODUCERS;
   };
@@ -219,7 +219,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
   grid_release_next();
   prefetch_inputs<C>(p, part);
   tc_fence_before();
-  const ListShape list = list_shape(p);
+  const ListShape list = list_shape<C>(p);
   ItemWindow<C::THREADS> window{p, item_lens, list.items, 0};
   const Share share = find_share<C::THREADS>(p, list, part, parts, window);  // barriers inside
   tc_fence_after();
@@ -483,10 +483,10 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           for (int q = 0; q < 4; ++q) {
             const int j0 = j0s[q];
             all_seen &= j0 + 15 < len && !(p.causal && j0 + 15 > p_lo) &&
-                        !(p.window > 0 && j0 <= p_hi - p.window && j0 + 15 >= p.sinks);
+                        !(windowed<C>(p) && j0 <= p_hi - p.window && past_sinks<C>(p, j0 + 15));
             differ |= n > 1 && j0 < len &&
                       ((p.causal && j0 + 15 > p_lo) ||
-                       (p.window > 0 && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
+                       (windowed<C>(p) && j0 <= p_hi - p.window && j0 + 15 > p_lo - p.window));
           }
         }
         // E8, of each 16 keys: what their scores are to be multiplied by, and the power of two
@@ -534,13 +534,13 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
 #pragma unroll
           for (int q = 0; q < C::RG; ++q) {
             const int j0 = key_pos[slot][copy * C::RG + q];
-            const int lo = p.window > 0 ? pos - p.window + 1 - j0 : -j0;
+            const int lo = windowed<C>(p) ? pos - p.window + 1 - j0 : -j0;
             const int hi = (p.causal ? min(len, pos + 1) : len) - j0;
             const unsigned span = static_cast<unsigned>(max(hi - lo, 0));
-            const int keep = min(p.sinks - j0, hi);  // first keys that the window leaves
+            const int keep = C::SINKS ? min(p.sinks - j0, hi) : 0;  // first keys that the window leaves
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (static_cast<unsigned>(e - lo) >= span && e >= keep) sv[16 * q + e] = __float_as_uint(-INFINITY);
+              if (static_cast<unsigned>(e - lo) >= span && (!C::SINKS || e >= keep)) sv[16 * q + e] = __float_as_uint(-INFINITY);
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -635,9 +635,9 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
           // row and get V = 0 as well.
           const uint32_t vs = sbase + C::OFF_KV + slot * 2 * C::TILE + C::TILE;
           uint8_t* v_rows = smem + (vs - sbase);
-          auto kept = [&](int j) { return j < len && !(p.window > 0 && j <= p_lo - p.window && j >= p.sinks); };
+          auto kept = [&](int j) { return j < len && !(windowed<C>(p) && j <= p_lo - p.window && past_sinks<C>(p, j)); };
           auto partial = [&](int j) {
-            return kept(j) && ((p.causal && j > p_lo) || (p.window > 0 && j <= p_hi - p.window && j >= p.sinks));
+            return kept(j) && ((p.causal && j > p_lo) || (windowed<C>(p) && j <= p_hi - p.window && past_sinks<C>(p, j)));
           };
           const int own = key_pos[slot][quarter];
           constexpr int ROW = D / 8;
@@ -675,7 +675,7 @@ fa_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                   s = s * fminf(own_scale, sc.x) * fmaxf(own_scale, sc.x);
                   share = sc.y * inverse_power(unit) * C::LIFT;
                 }
-                const bool seen = !(p.causal && j > pos) && !(p.window > 0 && j <= pos - p.window && j >= p.sinks);
+                const bool seen = !(p.causal && j > pos) && !(windowed<C>(p) && j <= pos - p.window && past_sinks<C>(p, j));
                 const float x = ex2((s - top) * p.scale_log2) * share;
 #pragma unroll 1
                 for (int col = 0; col < D; col += 32) {

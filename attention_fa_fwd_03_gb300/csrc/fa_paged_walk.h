@@ -68,7 +68,7 @@ struct Item {
   int skip;    // and tiles behind them that hold no visible key
   int tiles;   // tiles of each unit
   // place in the list of the unit's tile t
-  FA_WALK_FN int tile(int t) const { return t < head ? t : t + skip; }
+  FA_WALK_FN int tile(int t) const { return head > 0 && t < head ? t : t + skip; }
 };
 FA_WALK_FN Item make_item(const ListShape& s, const ItemLens& x) {
   Item it;
@@ -81,7 +81,7 @@ FA_WALK_FN Item make_item(const ListShape& s, const ItemLens& x) {
     keys = it.listed << s.page_shift;  // at most 2^20 entries of 2^8 keys
   } else if (s.window > 0) {
     const int first = walk_max(0, it.len - it.n - s.window + 1) / kPagedTile;
-    it.head = walk_min(first, (s.sinks + kPagedTile - 1) / kPagedTile);
+    if (s.sinks > 0) it.head = walk_min(first, (s.sinks + kPagedTile - 1) / kPagedTile);
     it.skip = first - it.head;
   }
   it.tiles = it.n > 0 ? (keys + kPagedTile - 1) / kPagedTile - it.skip : 0;
@@ -123,11 +123,17 @@ struct Walk {
   int used;  // places of the share that the segment takes
   // The segment from place `r` of the unit on: false where the share ends before its first tile.
   FA_WALK_FN bool cut(const ListShape& list, int r) {
+    if (list.over == 0) {  // (known where a kernel is compiled)
+      t0 = r;
+      t1 = walk_min(it.tiles, r + left);
+      used = t1 - t0;
+      return true;
+    }
     const int tiles = walk_max(it.tiles, 1);
     t0 = walk_min(walk_max(r - list.over, 0), tiles - 1);
     t1 = walk_min(it.tiles, walk_max(r + left - list.over, t0));
     used = t1 - t0 + walk_max(walk_min(list.over, r + left) - r, 0);
-    return list.over == 0 || t1 > t0;
+    return t1 > t0;
   }
   template <class Lens>
   FA_WALK_FN bool start(const ListShape& list, const Share& s, Lens& lens) {

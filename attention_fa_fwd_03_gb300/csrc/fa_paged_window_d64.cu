@@ -1,0 +1,4 @@
+// Paged-cache attention kernels for head dim 64 of windows.
+#include "fa_paged_fwd.cuh"
+
+FA_DEFINE_PAGED_WINDOW_HEAD_DIM(64)
