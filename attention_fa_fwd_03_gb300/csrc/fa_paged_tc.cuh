@@ -27,11 +27,11 @@
 // by more than 2^8. At the end of a segment both warpgroups read both accumulators,
 // half of the columns each.
 //
-// Measured (269 MB of bf16 keys and values, 16 units, start and join of some 10 us
-// included; warp-level products in brackets): D 128, 32 rows 56 us (64), 64 rows 58
-// (111), 128 rows 66 (190); D 96, 52 and 62 us for 64 and 128 rows of 201 MB; D 64, 32
-// rows 59 (80), 64 rows 68 (128), 128 rows 92 (233); D 256, 32 rows 65 (65), 64 rows 71
-// (106), 128 rows 82 (190). At D 128 the loads bound it up to 64 rows (537 MB 93 to 96
+// Measured (269 MB of bf16 keys and values, 16 units, no window, start and join of some 10 us
+// included; warp-level products in brackets): D 128, 32 rows 57 us (64), 64 rows 59
+// (111), 128 rows 67 (190); D 96, 52 and 65 us for 64 and 128 rows of 201 MB; D 64, 32
+// rows 58 (80), 64 rows 65 (128), 128 rows 88 (233); D 256, 32 rows 66 (65), 64 rows 72
+// (106), 128 rows 83 (190). At D 128 the loads bound it up to 64 rows (537 MB 93 to 96
 // us, 83 to 85% of the copy rate), at D 64, with half the bytes per tile, the softmax's
 // chain, at D 256 the two stages that fit.
 // Rings of their own for K and V (D 256 62 us with 32 rows, but D 64 67 and five drafts
